@@ -30,9 +30,13 @@ KVP_ERR_RANGE = -7
 KVP_ERR_BITS = -8
 KVP_ERR_HEADER = -9
 KVP_ERR_TIMEOUT = -10
+KVP_ERR_PAGE = -11
 KVP_MAX_LAYERS = 512
 KVP_K_PER_TENSOR = 0
 KVP_K_Q8_0 = 1
+KVP_PAGES_BF16 = 0
+KVP_PAGES_K8V8 = 1
+KVP_PAGES_K8V4 = 2
 KVP_NOALLOC_SCRATCH_BYTES = 262144
 KVP_PROBE_STORE = 0
 KVP_PROBE_BULK_STORE = 1
@@ -59,6 +63,23 @@ class CardHeader(C.Structure):
 
 
 assert C.sizeof(CardHeader) == 128
+
+
+
+class PagesConfig(C.Structure):
+    """kvp_pages_config: a container of n_pages pages of page_tokens tokens per layer."""
+    _fields_ = [("n_layers", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_tokens", C.c_int32), ("n_pages", C.c_int32), ("format", C.c_int32)]
+
+    def __repr__(self):
+        return "PagesConfig(L=%d, H=%d, d=%d, P=%d, pages=%d, format=%d)" % (
+            self.n_layers, self.n_kv_heads, self.head_dim, self.page_tokens, self.n_pages, self.format)
+
+
+class Rows(C.Structure):
+    """kvp_rows: a bf16 [tokens][heads][head_dim] tensor with element strides."""
+    _fields_ = [("ptr", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
 
 _vp = C.c_void_p
 _SIGS = {
@@ -87,6 +108,15 @@ _SIGS = {
     "cachecard_unpack_at": (C.c_int, [_vp, C.POINTER(CardHeader), C.c_int64, C.POINTER(C.c_float), C.POINTER(_vp),
                                       C.POINTER(_vp), _vp]),
     "cachecard_status": (C.c_int, [_vp, _vp]),
+    "kvpages_bytes": (C.c_size_t, [_vp]),
+    "kvpages_init": (C.c_int, [_vp, _vp, C.c_size_t, _vp]),
+    "kvpages_append": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_float,
+                                 C.c_int, _vp, _vp, _vp, _vp, _vp]),
+    "kvpages_read": (C.c_int, [_vp, _vp, C.c_int, C.c_int, _vp, C.c_int, _vp, C.c_int, _vp, _vp, _vp]),
+    "kvpages_attend_workspace_bytes": (C.c_size_t, [_vp, C.c_int, C.c_int, C.c_int]),
+    "kvpages_attend": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, _vp, C.c_float, _vp, C.c_int, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "kvpages_status": (C.c_int, [_vp, _vp]),
     "kvp_strerror": (C.c_char_p, [C.c_int]),
     "kvp_launch_count": (C.c_uint64, []),
     "kvp_bandwidth_probe": (C.c_int, [C.c_int, _vp, _vp, C.c_size_t, _vp]),
@@ -257,6 +287,78 @@ def cachecard_unpack_at(card, hdr, pos_dst, inv_freq, k_dst, v_dst, stream=None)
 
 def cachecard_status(card, stream=None):
     return load().cachecard_status(_addr(card), _stream(stream))
+
+
+def _pages(c):
+    return c if isinstance(c, PagesConfig) else PagesConfig(*c)
+
+
+def rows(x, token_stride=None, head_stride=None):
+    """kvp_rows of a [tokens][heads][head_dim] bf16 tensor (a strided view will
+    do; its last dimension contiguous), or of an address with its strides."""
+    if x is None or isinstance(x, Rows):
+        return x
+    if token_stride is not None:
+        return Rows(_addr(x), token_stride, head_stride)
+    t, h, e = x.stride()
+    if e != 1:
+        raise ValueError("the last dimension of a rows tensor is contiguous, got strides %r" % ((t, h, e),))
+    return Rows(x.data_ptr(), t, h)
+
+
+def _ref(x):
+    return None if x is None else C.addressof(x)
+
+
+def _floats(x):
+    """A host float array as a ctypes array: one made earlier passes as it is."""
+    if x is None or isinstance(x, C.Array):
+        return x
+    vals = [float(v) for v in x]
+    return (C.c_float * max(1, len(vals)))(*vals)
+
+
+def kvpages_bytes(cfg):
+    cfg = _pages(cfg)
+    return int(load().kvpages_bytes(_ref(cfg)))
+
+
+def kvpages_init(cfg, pages, pages_bytes, stream=None):
+    cfg = _pages(cfg)
+    return load().kvpages_init(_ref(cfg), _addr(pages), int(pages_bytes), _stream(stream))
+
+
+def kvpages_append(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, positions, q_norm, k_norm, eps, rot_dim,
+                   inv_freq, q_out, k_out, v_out, stream=None):
+    """q, k, v: [tokens][heads][head_dim] tensors or Rows; inv_freq: rot_dim/2
+    host floats (any sequence; a ctypes float array is passed as it is)."""
+    cfg, q, k, v, w = _pages(cfg), rows(q), rows(k), rows(v), _floats(inv_freq)
+    return load().kvpages_append(_addr(pages), _ref(cfg), layer, n_tokens, n_q_heads, _ref(q), _ref(k), _ref(v),
+                                 _addr(slots), _addr(positions), _addr(q_norm), _addr(k_norm), eps, rot_dim, _ref(w),
+                                 _addr(q_out), _addr(k_out), _addr(v_out), _stream(stream))
+
+
+def kvpages_read(pages, cfg, layer, n_seqs, table, max_pages, lens, max_tokens, k_dst, v_dst, stream=None):
+    cfg = _pages(cfg)
+    return load().kvpages_read(_addr(pages), _ref(cfg), layer, n_seqs, _addr(table), max_pages, _addr(lens), max_tokens,
+                               _addr(k_dst), _addr(v_dst), _stream(stream))
+
+
+def kvpages_attend_workspace_bytes(cfg, n_seqs, n_q_tokens, n_q_heads):
+    cfg = _pages(cfg)
+    return int(load().kvpages_attend_workspace_bytes(_ref(cfg), n_seqs, n_q_tokens, n_q_heads))
+
+
+def kvpages_attend(pages, cfg, layer, n_seqs, n_q_tokens, n_q_heads, q, scale, table, max_pages, lens, base_out,
+                   base_lse, out, lse, ws, ws_bytes, stream=None):
+    cfg = _pages(cfg)
+    return load().kvpages_attend(_addr(pages), _ref(cfg), layer, n_seqs, n_q_tokens, n_q_heads, _addr(q), scale,
+                                 _addr(table), max_pages, _addr(lens), _addr(base_out), _addr(base_lse), _addr(out),
+                                 _addr(lse), _addr(ws), ws_bytes, _stream(stream))
+
+
+def kvpages_status(pages, stream=None):
+    return load().kvpages_status(_addr(pages), _stream(stream))
 
 
 def kvp_strerror(status):

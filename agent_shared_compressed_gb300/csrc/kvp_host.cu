@@ -2,7 +2,7 @@
 // status read-back, error text, launch accounting.
 #include <atomic>
 
-#include "kvp_internal.cuh"
+#include "kvp_pages.cuh"
 
 namespace kvp {
 
@@ -34,6 +34,20 @@ int shape_ok(const kvp_shape *s) {
     return KVP_OK;
 }
 
+int pages_ok(const kvp_pages_config *c) {
+    if (!c) return KVP_ERR_ARG;
+    if (c->n_layers <= 0 || c->n_kv_heads <= 0 || c->n_pages <= 0) return KVP_ERR_ARG;
+    if (c->page_tokens < 16 || c->page_tokens > 1024 || (c->page_tokens & (c->page_tokens - 1))) return KVP_ERR_ARG;
+    if (c->format != KVP_PAGES_BF16 && c->format != KVP_PAGES_K8V8 && c->format != KVP_PAGES_K8V4) return KVP_ERR_ARG;
+    if (c->n_layers > KVP_MAX_LAYERS || c->n_kv_heads > 4096) return KVP_ERR_SIZE;
+    if (c->head_dim != 64 && c->head_dim != 128) return KVP_ERR_UNSUPPORTED_D;
+    // a container of at most 2^48 bytes: every offset fits 64 bits
+    const unsigned __int128 tile = (unsigned __int128)pages_block_bytes(c->head_dim, c->format) * (c->page_tokens / 16);
+    if (tile * uint32_t(c->n_kv_heads) * uint32_t(c->n_pages) * uint32_t(c->n_layers) > (uint64_t(1) << 48))
+        return KVP_ERR_SIZE;
+    return KVP_OK;
+}
+
 }  // namespace kvp
 
 using namespace kvp;
@@ -58,6 +72,7 @@ const char *kvp_strerror(int st) {
         case KVP_ERR_BITS: return "CacheCard bitwidth not in {2,4,8,16}";
         case KVP_ERR_HEADER: return "not a pool / card, or its shape does not match";
         case KVP_ERR_TIMEOUT: return "a bounded device-side wait ran out";
+        case KVP_ERR_PAGE: return "a slot, page id or length outside the page container";
         default: return "unknown status";
     }
 }
@@ -67,6 +82,7 @@ uint64_t kvp_launch_count(void) { return g_launches.load(std::memory_order_relax
 static int flags_to_status(uint32_t f) {
     if (f & FLAG_HEADER) return KVP_ERR_HEADER;
     if (f & FLAG_TIMEOUT) return KVP_ERR_TIMEOUT;
+    if (f & FLAG_PAGE) return KVP_ERR_PAGE;
     if (f & FLAG_BITS) return KVP_ERR_BITS;
     if (f & FLAG_SIZE) return KVP_ERR_SIZE;
     if (f & FLAG_NONFINITE) return KVP_ERR_NONFINITE;
@@ -82,6 +98,21 @@ int kvpool_status(const void *pool, void *stream) {
     if (cudaStreamSynchronize(st) != cudaSuccess) return KVP_ERR_CUDA;
     if (h[0] != POOL_MAGIC || h[1] != POOL_VERSION) return KVP_ERR_HEADER;
     return flags_to_status(h[POOL_ERR_WORD]);
+}
+
+size_t kvpages_bytes(const kvp_pages_config *c) {
+    if (pages_ok(c) != KVP_OK) return 0;
+    return size_t(pages_geom(*c).total);
+}
+
+int kvpages_status(const void *pages, void *stream) {
+    if (!pages) return KVP_ERR_ARG;
+    uint32_t h[8];
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cudaMemcpyAsync(h, pages, sizeof h, cudaMemcpyDeviceToHost, st) != cudaSuccess) return KVP_ERR_CUDA;
+    if (cudaStreamSynchronize(st) != cudaSuccess) return KVP_ERR_CUDA;
+    if (h[0] != PAGES_MAGIC || h[1] != PAGES_VERSION) return KVP_ERR_HEADER;
+    return flags_to_status(h[PAGES_ERR_WORD]);
 }
 
 int cachecard_read_header(const void *card, kvp_card_header *out, void *stream) {

@@ -21,6 +21,7 @@ constexpr uint32_t FLAG_BITS = 4u;       // a CacheCard bitwidth not in {2,4,8,1
 constexpr uint32_t FLAG_SIZE = 8u;       // card buffer smaller than the bits need
 constexpr uint32_t FLAG_HEADER = 16u;    // decode asked for a shape the pool lacks
 constexpr uint32_t FLAG_TIMEOUT = 32u;   // a bounded wait on another block ran out
+constexpr uint32_t FLAG_PAGE = 64u;      // a slot, page id or length outside the page container
 
 // ---------------------------------------------------------------------------
 // SharedKVPool geometry ("PolyKV" 2.A: one object, size independent of the

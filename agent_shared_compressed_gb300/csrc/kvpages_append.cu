@@ -1,0 +1,572 @@
+// kvpages_append.cu -- writing new tokens into the page container, and reading
+// a container's tokens back.
+//
+// kvpages_append, per new token and head, in one pass over the projection's
+// output:
+//   y = x rsqrt(mean(x^2) + eps) w             (queries and keys, if asked)
+//   (y_i, y_{i + r/2}) turned by position * w_i  (i < r/2)
+//   q_out = bf16(y);  the key's and the value's codes into their page;
+//   k_out, v_out = bf16(the value that the page now holds).
+// A lane quad holds one row of one token (see kvp_pages.cuh): both halves of
+// every rotated pair and all of a scale group are within the quad, so the norm
+// is two shuffles and a group's extremes two more.  A warp holds the same head
+// of eight tokens, so that every branch on the kind of row is uniform and the
+// (cos, sin) of its tokens, formed once per block, serve all heads.
+//
+// Angles.  position * w_i is only needed modulo a turn, and w_i / 2 pi modulo 1
+// is a 64-bit fraction W_i, formed on the host from the fp32 frequency and 128
+// bits of 1 / 2 pi.  position * W_i in 64-bit integers wraps at exactly one
+// turn, so the reduced angle is off by position * 2^-65 turns at any position;
+// sincospif finishes in fp32.  (The same reduction in fp64 costs some hundred
+// fp64 instructions an angle, and this GPU's fp64 rate is low.)
+#include <algorithm>
+#include <cmath>
+
+#include "kvp_pages.cuh"
+
+namespace kvp {
+
+constexpr int APP_THREADS = 256;
+constexpr int APP_WARPS = APP_THREADS / 32;
+constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
+
+struct AppendArgs {
+    PagesView pv;
+    const uint16_t *q, *k, *v;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
+    const int64_t *slots, *positions;
+    const uint16_t *q_norm, *k_norm;
+    uint16_t *q_out, *k_out, *v_out;
+    float eps;
+    int n, nq, rot, rows_per_block;
+    uint64_t turn[64];  // w_i / 2 pi mod 1, in units of 2^-64
+};
+
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// fp16 of a scale or zero point, kept finite; an overflow sets `bad`.
+__device__ __forceinline__ uint32_t half_bits(float x, uint32_t &bad) {
+    uint32_t h = __half_as_ushort(__float2half_rn(x));
+    if ((h & 0x7C00u) == 0x7C00u) {
+        bad |= FLAG_RANGE;
+        h = (h & 0x8000u) | 0x7BFFu;
+    }
+    return h;
+}
+__device__ __forceinline__ float half_value(uint32_t h) { return __half2float(__ushort_as_half(uint16_t(h))); }
+
+// Codes of a row at 8 bits: s = fp16(max|x| fl(1/127)), code = fl(x / s) rounded
+// to nearest (ties to even).  x * fl(1/s) is within 2^-16 of the quotient, so
+// only a product that near a half-integer is divided out.  x becomes the values
+// held.
+template <int D>
+__device__ __forceinline__ void encode8(float (&x)[D / 32][8], Lane8<D> &c, uint32_t (&sb)[D / 32], uint32_t &bad) {
+    constexpr float MAGIC = 12582912.0f + 128.0f;  // 1.5 * 2^23 + the codes' bias
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        float m = 0.0f;
+        bool fin = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            fin &= finite(x[b][j]);
+            m = fmaxf(m, fabsf(x[b][j]));
+        }
+        if (!fin) {  // Inf and NaN count as zeros, and are reported
+            bad |= FLAG_NONFINITE;
+            m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[b][j] = finite(x[b][j]) ? x[b][j] : 0.0f;
+                m = fmaxf(m, fabsf(x[b][j]));
+            }
+        }
+        m = quad_max(m);
+        sb[b] = half_bits(m * (1.0f / 127.0f), bad);
+        const float s = half_value(sb[b]), rs = s > 0.0f ? 1.0f / s : 0.0f;
+        float r[8], near = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = fmaf(x[b][j], rs, MAGIC);
+            near = fmaxf(near, fabsf(fmaf(x[b][j], rs, MAGIC - r[j])));
+        }
+        if (near > 0.5f - 0x1p-15f || s < 0x1p-14f || m > 8320000.0f) {
+            // near a tie; or the scale is an fp16 subnormal or saturated, where codes can pass 127
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = (s > 0.0f ? fminf(fmaxf(rintf(x[b][j] / s), -127.0f), 127.0f) : 0.0f) + MAGIC;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t lo = __byte_perm(__float_as_uint(r[4 * e]), __float_as_uint(r[4 * e + 1]), 0x0040u);
+            const uint32_t hi = __byte_perm(__float_as_uint(r[4 * e + 2]), __float_as_uint(r[4 * e + 3]), 0x0040u);
+            c.w[b][e] = __byte_perm(lo, hi, 0x5410u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[b][j] = (r[j] - MAGIC) * s;
+    }
+}
+
+// Codes of a value row at 4 bits: s = fp16(fl(max - min) fl(1/15)), z =
+// fp16(min), code = (x - z) / s rounded to nearest even, in [0, 15].  Decided
+// in fp32 unless within 2^-16 of a half-integer (fp32 errs by under 2^-18),
+// then in fp64, where x - z of two 16-bit values is exact.  x becomes the values
+// held.
+template <int D>
+__device__ __forceinline__ void encode4(float (&x)[D / 32][8], Lane4<D> &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
+    constexpr float MAGIC = 12582912.0f;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        bool fin = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) fin &= finite(x[b][j]);
+        if (!fin) {
+            bad |= FLAG_NONFINITE;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[b][j] = finite(x[b][j]) ? x[b][j] : 0.0f;
+        }
+        float hi = x[b][0], nlo = -x[b][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) hi = fmaxf(hi, x[b][j]), nlo = fmaxf(nlo, -x[b][j]);
+        hi = quad_max(hi);
+        const float lo = -quad_max(nlo);
+        const uint32_t sh = half_bits((hi - lo) * (1.0f / 15.0f), bad), zh = half_bits(lo, bad);
+        szb[b] = sh | zh << 16;
+        const float s = half_value(sh), z = half_value(zh), rs = s > 0.0f ? 1.0f / s : 0.0f;
+        float r[8], near = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float y = fminf(fmaxf((x[b][j] - z) * rs, 0.0f), 15.0f);
+            r[j] = y + MAGIC;
+            near = fmaxf(near, fabsf(y - (r[j] - MAGIC)));
+        }
+        if (near > 0.5f - 0x1p-16f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = s > 0.0f ? float(fmin(fmax(rint((double(x[b][j]) - double(z)) / double(s)), 0.0), 15.0)) + MAGIC
+                                : MAGIC;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t h = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h |= (__float_as_uint(r[4 * e + j]) & 15u) << (4 * j);
+            c.h[b][e] = h;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[b][j] = fmaf(r[j] - MAGIC, s, z);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+}
+
+// Eight pairs turned by their (cos, sin).
+__device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const float2 *cs) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 t = cs[j];
+        const float l = lo[j], h = hi[j];
+        lo[j] = l * t.x - h * t.y;
+        hi[j] = h * t.x + l * t.y;
+    }
+}
+
+// The lane's share of a contiguous bf16 row.
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t *row, int tig, const float (&x)[D / 32][8]) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) *reinterpret_cast<uint4 *>(row + 32 * b + 8 * tig) = pack8(x[b]);
+}
+
+// One block: APP_TOKENS tokens, rows [blockIdx.y * rows_per_block, ...) of the
+// nq query, H key and H value rows of each, a warp at a time.
+template <int D, int FMT>
+__global__ void __launch_bounds__(APP_THREADS) pages_append(const __grid_constant__ AppendArgs a) {
+    using B = Block<D, FMT>;
+    constexpr int NB = D / 32;
+    __shared__ float2 cs[APP_TOKENS][D / 2 + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
+    const int64_t t0 = int64_t(blockIdx.x) * APP_TOKENS;
+    const int64_t tok = t0 + tq;
+    const bool real = tok < a.n;
+    if (!pages_match(a.pv)) {
+        if (threadIdx.x == 0) pages_flag(a.pv, FLAG_HEADER);
+        return;
+    }
+    if (a.rot > 0) {
+        for (int i = threadIdx.x; i < APP_TOKENS * (a.rot / 2); i += APP_THREADS) {
+            const int t = i / (a.rot / 2), p = i % (a.rot / 2);
+            if (t0 + t < a.n) {
+                const int64_t turns = int64_t(uint64_t(a.positions[t0 + t]) * a.turn[p]);  // mod one turn
+                float s, c;
+                sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
+                cs[t][p] = make_float2(c, s);
+            } else {
+                cs[t][p] = make_float2(1.0f, 0.0f);
+            }
+        }
+    }
+    __syncthreads();
+    uint8_t *blk = nullptr;  // the token's block of head 0
+    uint32_t row16 = 0, bad = 0;
+    if (real) {
+        const int64_t slot = a.slots[tok];
+        if (slot >= (int64_t(a.pv.n_pages) << a.pv.logP)) {
+            bad |= FLAG_PAGE;
+        } else if (slot >= 0) {
+            const int64_t page = slot >> a.pv.logP;
+            const uint32_t in = uint32_t(slot) & uint32_t(a.pv.P - 1);
+            blk = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(in / PAGES_BLOCK) * B::BYTES;
+            row16 = in % PAGES_BLOCK;
+        }
+    }
+    const int H = a.pv.H, rows = a.nq + 2 * H;
+    const int r1 = min(rows, int(blockIdx.y + 1) * a.rows_per_block);
+    for (int r = int(blockIdx.y) * a.rows_per_block + warp; r < r1; r += APP_WARPS) {
+        const bool is_q = r < a.nq, is_v = r >= a.nq + H;
+        const int h = is_q ? r : (is_v ? r - a.nq - H : r - a.nq);
+        const uint16_t *src = is_q ? a.q + tok * a.q_ts + h * a.q_hs
+                                   : (is_v ? a.v + tok * a.v_ts + h * a.v_hs : a.k + tok * a.k_ts + h * a.k_hs);
+        float x[NB][8];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            unpack8(real ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0), x[b]);
+        uint8_t *hb = blk ? blk + uint64_t(h) * a.pv.tile_bytes : nullptr;
+        if (!is_v) {
+            const uint16_t *w = is_q ? a.q_norm : a.k_norm;
+            if (w) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = fmaf(x[b][j], x[b][j], ss);
+                const float inv = 1.0f / sqrtf(quad_sum(ss) * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float wf[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4 *>(w + 32 * b + 8 * tig)), wf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[b][j] = x[b][j] * inv * wf[j];
+                }
+            }
+            if (a.rot > 0) {
+                const float2 *t = cs[tq] + 8 * tig;
+                if (NB == 4 && a.rot == 128) {
+                    turn(x[0], x[NB - 2], t);
+                    turn(x[1], x[NB - 1], t + 32);
+                } else {
+                    turn(x[0], x[1], t);
+                }
+            }
+            if (is_q) {
+                if (real) store_row<D>(a.q_out + (tok * a.nq + h) * D, tig, x);
+                continue;
+            }
+            if constexpr (!B::Q8) {
+                if (hb) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        *reinterpret_cast<uint4 *>(hb + B::key(row16, (4 * b + tig) * 16)) = pack8(x[b]);
+                }
+            } else {
+                Lane8<D> c;
+                uint32_t sb[NB];
+                encode8<D>(x, c, sb, bad);
+                if (hb) {
+                    store_key8<D, FMT>(hb, row16, tig, c);
+                    if (tig == 0) {
+                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
+                    }
+                }
+            }
+            if (a.k_out && real) store_row<D>(a.k_out + (tok * H + h) * D, tig, x);
+        } else {
+            if constexpr (!B::Q8) {
+                if (hb) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        *reinterpret_cast<uint4 *>(hb + B::value(row16, (4 * b + tig) * 16)) = pack8(x[b]);
+                }
+            } else if constexpr (!B::V4) {
+                Lane8<D> c;
+                uint32_t sb[NB];
+                encode8<D>(x, c, sb, bad);
+                if (hb) {
+                    store_value8<D, FMT>(hb, row16, tig, c);
+                    if (tig == 0) {
+                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
+                    }
+                }
+            } else {
+                Lane4<D> c;
+                uint32_t szb[NB];
+                encode4<D>(x, c, szb, bad);
+                if (hb) {
+                    store_value4<D, FMT>(hb, row16, tig, c);
+                    if (tig == 0) {
+                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) s[i] = szb[i];
+                    }
+                }
+            }
+            if (a.v_out && real) store_row<D>(a.v_out + (tok * H + h) * D, tig, x);
+        }
+    }
+    if (bad) pages_flag(a.pv, bad);
+}
+
+// ---------------------------------------------------------------------------
+// Reading back.  A warp takes a 16-token block of one sequence and head; a
+// quad takes a row.  Output rows past the sequence's length are zeros.
+// ---------------------------------------------------------------------------
+struct ReadArgs {
+    PagesView pv;
+    const int32_t *table, *lens;
+    uint16_t *k, *v;  // [B][H][Tmax][d]
+    int nseq, max_pages, tmax, nblk;
+    uint64_t tasks;
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) pages_read(const __grid_constant__ ReadArgs a) {
+    using B = Block<D, FMT>;
+    constexpr int NB = D / 32;
+    const int lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
+    if (!pages_match(a.pv)) {
+        if (threadIdx.x == 0) pages_flag(a.pv, FLAG_HEADER);
+        return;
+    }
+    const uint64_t nwarps = uint64_t(gridDim.x) * (blockDim.x / 32);
+    for (uint64_t w = uint64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5); w < a.tasks; w += nwarps) {
+        const uint32_t blk16 = uint32_t(w % uint32_t(a.nblk));
+        const uint32_t bh = uint32_t(w / uint32_t(a.nblk));
+        const uint32_t h = bh % uint32_t(a.pv.H), b = bh / uint32_t(a.pv.H);
+        const int t0 = int(blk16) * PAGES_BLOCK;
+        int len = min(max(a.lens[b], 0), a.tmax);
+        if (len > 0 && int64_t(len) > int64_t(a.max_pages) << a.pv.logP) {  // the table is shorter than the sequence
+            if (lane == 0) pages_flag(a.pv, FLAG_PAGE);
+            len = int(int64_t(a.max_pages) << a.pv.logP);
+        }
+        const uint8_t *src = nullptr;
+        if (t0 < len) {
+            const int page = a.table[uint64_t(b) * uint32_t(a.max_pages) + uint32_t(t0 >> a.pv.logP)];
+            if (page >= 0 && page < a.pv.n_pages)
+                src = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(h) * a.pv.tile_bytes +
+                      uint64_t((uint32_t(t0) & uint32_t(a.pv.P - 1)) / PAGES_BLOCK) * B::BYTES;
+            else if (lane == 0)
+                pages_flag(a.pv, FLAG_PAGE);
+        }
+        const uint64_t out = (uint64_t(bh) * uint32_t(a.tmax) + uint32_t(t0)) * D;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 8 * i + tq;
+            if (t0 + t >= a.tmax) continue;
+            float x[NB][8];
+            const bool there = src && t0 + t < len;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (there) {
+                    if (kv == 0)
+                        load_key_row<D, FMT>(src, t, tig, x);
+                    else
+                        load_value_row<D, FMT>(src, t, tig, x);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < NB; ++g)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[g][j] = 0.0f;
+                }
+                uint16_t *row = (kv == 0 ? a.k : a.v) + out + uint64_t(t) * D;
+#pragma unroll
+                for (int g = 0; g < NB; ++g) st_stream_v4(row + 32 * g + 8 * tig, pack8(x[g]));
+            }
+        }
+    }
+}
+
+__global__ void pages_init(uint32_t *h, const __grid_constant__ kvp_pages_config c, uint64_t layer_stride,
+                           uint64_t total) {
+    const int i = threadIdx.x;  // 64 words
+    uint32_t w = 0u;
+    switch (i) {
+        case 0: w = PAGES_MAGIC; break;
+        case 1: w = PAGES_VERSION; break;
+        case 2: w = uint32_t(c.n_layers); break;
+        case 3: w = uint32_t(c.n_kv_heads); break;
+        case 4: w = uint32_t(c.head_dim); break;
+        case 5: w = uint32_t(c.page_tokens); break;
+        case 7: w = uint32_t(c.format); break;
+        case 8: w = uint32_t(c.n_pages); break;
+        case 10: w = uint32_t(layer_stride); break;
+        case 11: w = uint32_t(layer_stride >> 32); break;
+        case 12: w = uint32_t(total); break;
+        case 13: w = uint32_t(total >> 32); break;
+        default: break;
+    }
+    h[i] = w;
+}
+
+// w / 2 pi mod 1 in units of 2^-64, for a finite fp32 w: its 24-bit integer
+// times the first 128 bits of 1 / 2 pi's binary fraction, shifted by its exponent.
+static uint64_t turn_fraction(float w) {
+    constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;  // 1 / 2 pi * 2^128
+    if (w == 0.0f) return 0;
+    int e;
+    const double f = std::frexp(std::fabs(double(w)), &e);     // f in [1/2, 1)
+    const uint64_t m = uint64_t(std::ldexp(f, 24));            // w = m 2^(e - 24), exactly
+    // m / 2 pi = p 2^-128 with p of 152 bits, as three 64-bit words
+    const unsigned __int128 p0 = (unsigned __int128)m * LO, p1 = (unsigned __int128)m * HI + (p0 >> 64);
+    const uint64_t word[3] = {uint64_t(p0), uint64_t(p1), uint64_t(p1 >> 64)};
+    // the turn's 64-bit fraction: bits [s, s + 64) of p, s = 64 - (e - 24)
+    const int s = 88 - e;
+    uint64_t r = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int at = 64 * i - s;  // where the word's bit 0 lands
+        if (at >= 0 && at < 64) r |= word[i] << at;
+        if (at < 0 && at > -64) r |= word[i] >> -at;
+    }
+    return w < 0.0f ? 0u - r : r;
+}
+
+template <int D, int FMT>
+static int launch_append(const AppendArgs &a, dim3 grid, cudaStream_t st) {
+    pages_append<D, FMT><<<grid, APP_THREADS, 0, st>>>(a);
+    count_launch();
+    return launch_status();
+}
+template <int D, int FMT>
+static int launch_read(const ReadArgs &a, unsigned grid, cudaStream_t st) {
+    pages_read<D, FMT><<<grid, 256, 0, st>>>(a);
+    count_launch();
+    return launch_status();
+}
+
+static bool rows_aligned(const kvp_rows *r) {
+    return aligned(r->ptr, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" {
+
+int kvpages_init(const kvp_pages_config *cfg, void *pages, size_t pages_bytes, void *stream) {
+    const int rc = pages_ok(cfg);
+    if (rc != KVP_OK) return rc;
+    if (!pages) return KVP_ERR_ARG;
+    if (!aligned(pages, 256)) return KVP_ERR_ALIGN;
+    const PagesGeom g = pages_geom(*cfg);
+    if (pages_bytes < g.total) return KVP_ERR_SIZE;
+    pages_init<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint32_t *>(pages), *cfg, g.layer_stride,
+                                                                g.total);
+    count_launch();
+    return launch_status();
+}
+
+int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_tokens, int n_q_heads, const kvp_rows *q,
+                   const kvp_rows *k, const kvp_rows *v, const int64_t *slots, const int64_t *positions,
+                   const void *q_norm, const void *k_norm, float eps, int rot_dim, const float *inv_freq, void *q_out,
+                   void *k_out, void *v_out, void *stream) {
+    const int rc = pages_ok(cfg);
+    if (rc != KVP_OK) return rc;
+    if (!pages || layer < 0 || layer >= cfg->n_layers || n_tokens < 0 || n_q_heads < 0) return KVP_ERR_ARG;
+    if (n_q_heads > 65536) return KVP_ERR_SIZE;
+    if (!k || !v || !k->ptr || !v->ptr || !slots) return KVP_ERR_ARG;
+    if (n_q_heads > 0 && (!q || !q->ptr || !q_out)) return KVP_ERR_ARG;
+    if (rot_dim != 0 && rot_dim != 64 && !(rot_dim == 128 && cfg->head_dim == 128)) return KVP_ERR_ARG;
+    if (rot_dim > 0 && (!positions || !inv_freq)) return KVP_ERR_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!std::isfinite(inv_freq[i])) return KVP_ERR_ARG;
+    if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.0f)) return KVP_ERR_ARG;
+    if (!aligned(pages, 256) || !rows_aligned(k) || !rows_aligned(v) || (n_q_heads > 0 && !rows_aligned(q)) ||
+        !aligned(slots, 8) || !aligned(positions, 8) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
+        !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return KVP_ERR_ALIGN;
+    if (n_tokens == 0) return KVP_OK;
+    AppendArgs a;
+    a.pv = pages_view(pages, *cfg, layer);
+    a.q = n_q_heads > 0 ? static_cast<const uint16_t *>(q->ptr) : nullptr;
+    a.q_ts = n_q_heads > 0 ? q->token_stride : 0;
+    a.q_hs = n_q_heads > 0 ? q->head_stride : 0;
+    a.k = static_cast<const uint16_t *>(k->ptr), a.k_ts = k->token_stride, a.k_hs = k->head_stride;
+    a.v = static_cast<const uint16_t *>(v->ptr), a.v_ts = v->token_stride, a.v_hs = v->head_stride;
+    a.slots = slots, a.positions = positions;
+    a.q_norm = static_cast<const uint16_t *>(q_norm), a.k_norm = static_cast<const uint16_t *>(k_norm);
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k_out = static_cast<uint16_t *>(k_out), a.v_out = static_cast<uint16_t *>(v_out);
+    a.eps = eps, a.n = n_tokens, a.nq = n_q_heads, a.rot = rot_dim;
+    for (int i = 0; i < 64; ++i) a.turn[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
+    // Rows of a block: all of a token group's where the groups alone fill the
+    // GPU (the angles are formed once), else as few as one row per warp.
+    const int rows = n_q_heads + 2 * cfg->n_kv_heads;
+    const int groups = int((int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS);
+    const int steps = (rows + APP_WARPS - 1) / APP_WARPS;
+    const int split = std::max(1, std::min(steps, 4 * sm_count() / std::max(groups, 1)));
+    a.rows_per_block = (steps + split - 1) / split * APP_WARPS;
+    const dim3 grid(unsigned(groups), unsigned((rows + a.rows_per_block - 1) / a.rows_per_block));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool d128 = cfg->head_dim == 128;
+    switch (cfg->format) {
+        case KVP_PAGES_BF16:
+            return d128 ? launch_append<128, KVP_PAGES_BF16>(a, grid, st) : launch_append<64, KVP_PAGES_BF16>(a, grid, st);
+        case KVP_PAGES_K8V8:
+            return d128 ? launch_append<128, KVP_PAGES_K8V8>(a, grid, st) : launch_append<64, KVP_PAGES_K8V8>(a, grid, st);
+        default:
+            return d128 ? launch_append<128, KVP_PAGES_K8V4>(a, grid, st) : launch_append<64, KVP_PAGES_K8V4>(a, grid, st);
+    }
+}
+
+int kvpages_read(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, const int32_t *table,
+                 int max_pages, const int32_t *lens, int max_tokens, void *k_dst, void *v_dst, void *stream) {
+    const int rc = pages_ok(cfg);
+    if (rc != KVP_OK) return rc;
+    if (!pages || layer < 0 || layer >= cfg->n_layers || n_seqs < 0 || max_pages <= 0 || max_tokens <= 0)
+        return KVP_ERR_ARG;
+    if (!table || !lens || !k_dst || !v_dst) return KVP_ERR_ARG;
+    if (!aligned(pages, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(k_dst, 16) || !aligned(v_dst, 16))
+        return KVP_ERR_ALIGN;
+    if (int64_t(n_seqs) * cfg->n_kv_heads >= (int64_t(1) << 31)) return KVP_ERR_SIZE;
+    if (n_seqs == 0) return KVP_OK;
+    ReadArgs a;
+    a.pv = pages_view(const_cast<void *>(pages), *cfg, layer);
+    a.table = table, a.lens = lens;
+    a.k = static_cast<uint16_t *>(k_dst), a.v = static_cast<uint16_t *>(v_dst);
+    a.nseq = n_seqs, a.max_pages = max_pages, a.tmax = max_tokens;
+    a.nblk = int((int64_t(max_tokens) + PAGES_BLOCK - 1) / PAGES_BLOCK);
+    a.tasks = uint64_t(n_seqs) * uint64_t(cfg->n_kv_heads) * uint64_t(a.nblk);
+    const unsigned grid = unsigned(std::min<uint64_t>((a.tasks + 7) / 8, uint64_t(sm_count()) * 8));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool d128 = cfg->head_dim == 128;
+    switch (cfg->format) {
+        case KVP_PAGES_BF16:
+            return d128 ? launch_read<128, KVP_PAGES_BF16>(a, grid, st) : launch_read<64, KVP_PAGES_BF16>(a, grid, st);
+        case KVP_PAGES_K8V8:
+            return d128 ? launch_read<128, KVP_PAGES_K8V8>(a, grid, st) : launch_read<64, KVP_PAGES_K8V8>(a, grid, st);
+        default:
+            return d128 ? launch_read<128, KVP_PAGES_K8V4>(a, grid, st) : launch_read<64, KVP_PAGES_K8V4>(a, grid, st);
+    }
+}
+
+}  // extern "C"

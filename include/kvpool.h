@@ -2,7 +2,7 @@
  * kvpool.h -- C ABI of the GB300 (sm_103a) KV-cache codec for multi-agent
  * KV sharing.
  *
- * Two containers, both position-independent byte blobs in device memory:
+ * Three containers, all position-independent byte blobs in device memory:
  *
  *  SharedKVPool -- "PolyKV: A Shared Asymmetrically-Compressed KV Cache Pool
  *    for Multi-Agent LLM Inference", 2.A (write once, read many; one object
@@ -16,6 +16,11 @@
  *    quantized KV groups plus metadata seq_len / model_id / position offset;
  *    the receiver rebuilds 16-bit past_key_values from it).
  *
+ *  Pages -- an agent's own growing cache beside the pool it shares: pages of
+ *    tokens, written a token or a prompt at a time, attended over and joined
+ *    with attention over the pool ("PolyKV" 2.A gives each agent a cache of
+ *    its own on top of the shared one; the papers leave its form open).
+ *
  * Conventions shared by every entry point
  * ----------------------------------------
  *  - KV tensors are bf16, one tensor per layer, layout [H][T][d] contiguous
@@ -28,10 +33,10 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Every compute call only enqueues work on that stream and
  *    returns; it never allocates, frees or synchronises device memory.  The
- *    only synchronising calls are kvpool_status, cachecard_status and
- *    cachecard_read_header, which say so.
+ *    only synchronising calls are kvpool_status, cachecard_status,
+ *    cachecard_read_header and kvpages_status, which say so.
  *  - The caller owns every buffer.  Device pointers to KV tensors must be
- *    16-byte aligned; pool and card buffers 256-byte aligned; workspaces
+ *    16-byte aligned; pool, card and page buffers 256-byte aligned; workspaces
  *    16-byte aligned.
  *  - Errors: 0 is success, negative values are KVP_ERR_*.  Everything the
  *    host can check (null pointers, shapes, alignment, buffer sizes) is
@@ -69,6 +74,7 @@ extern "C" {
 #define KVP_ERR_BITS (-8)           /* CacheCard bitwidth not in {2,4,8,16}  */
 #define KVP_ERR_HEADER (-9)         /* not a pool / card, or shape mismatch  */
 #define KVP_ERR_TIMEOUT (-10)       /* a bounded device-side wait ran out    */
+#define KVP_ERR_PAGE (-11)          /* slot, page id or length out of range  */
 
 /* Largest layer count one call accepts. */
 #define KVP_MAX_LAYERS 512
@@ -77,6 +83,12 @@ extern "C" {
 #define KVP_K_PER_TENSOR 0  /* one fp32 scale per layer's key tensor ("PolyKV" 2.B.1 text) */
 #define KVP_K_Q8_0 1        /* q8_0 blocks: 32 keys along d share an fp16 scale (the label
                                "q8_0" that "PolyKV" 2.B.1 gives the same step)            */
+
+/* Formats of a page container's keys and values. */
+#define KVP_PAGES_BF16 0  /* both bf16                                               */
+#define KVP_PAGES_K8V8 1  /* both q8_0: 32 along d share an fp16 scale, 8-bit codes  */
+#define KVP_PAGES_K8V4 2  /* keys q8_0; values 4-bit, asymmetric groups of 32 along d
+                             with an fp16 scale and zero point                      */
 
 /* Shape of one KV cache: n_layers tensors of [n_kv_heads][n_tokens][head_dim]. */
 typedef struct kvp_shape {
@@ -352,6 +364,116 @@ int cachecard_unpack_at(const void *card, const kvp_card_header *hdr, int64_t po
 /* Synchronises `stream`, then returns KVP_OK or the first device-detected
  * error recorded in the card's header. */
 int cachecard_status(const void *card, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Pages: an agent's own cache                                             */
+/* ---------------------------------------------------------------------- */
+
+/* A page container: n_pages pages in each of n_layers layers; a page holds
+ * page_tokens tokens (a power of two, 16 to 1024) of all KV heads.  Which
+ * pages hold which sequence is the caller's: a table row of page ids per
+ * sequence; sequences may share pages. */
+typedef struct kvp_pages_config {
+    int32_t n_layers;
+    int32_t n_kv_heads; /* at most 4096 */
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t n_pages;
+    int32_t format;     /* KVP_PAGES_* */
+} kvp_pages_config;
+
+/* A bf16 tensor [tokens][heads][head_dim] with strides in elements (multiples
+ * of 8; the innermost dimension contiguous): the slices of a fused projection's
+ * output, or of a [heads][tokens][head_dim] tensor, as they lie. */
+typedef struct kvp_rows {
+    const void *ptr;
+    int64_t token_stride;
+    int64_t head_stride;
+} kvp_rows;
+
+/* Exact byte size of a container, or 0 for an invalid configuration.
+ * Layout: 256-byte header (magic "KVPG", version 1, L, H, d, page_tokens,
+ * error word, format, n_pages, layer stride, total bytes), then per layer
+ * (256-byte aligned) n_pages x H tiles of page_tokens / 16 blocks; a block is
+ * 16 tokens of one head: keys, values, key scales, value scales. */
+size_t kvpages_bytes(const kvp_pages_config *cfg);
+
+/* Writes the header (and clears the error word).  The pages need no
+ * initialisation: what was never written is never read. */
+int kvpages_init(const kvp_pages_config *cfg, void *pages, size_t pages_bytes, void *stream);
+
+/* Write new tokens of one layer: the norm of every query and key head, the
+ * position rotation, and the quantised write, in one pass.
+ *  q, k, v: [n_tokens][n_q_heads or n_kv_heads][head_dim] rows.  q and q_out
+ *    may be NULL when n_q_heads is 0.
+ *  slots: device int64[n_tokens], the place of each token: page id *
+ *    page_tokens + index in the page.  Negative: the token is not cached (its
+ *    outputs are still written).  Two tokens of a call may not share a slot.
+ *  q_norm, k_norm: device bf16[head_dim] or NULL: y = x / sqrt(mean(x^2) +
+ *    eps) * w per head, in fp32; NULL leaves the heads as they are.
+ *  rot_dim: 0, 64, or 128 at head_dim 128: dims i and i + rot_dim/2
+ *    (i < rot_dim/2) turned by positions[t] * inv_freq[i]; the rest pass.
+ *    positions: device int64[n_tokens]; inv_freq: HOST array of rot_dim/2
+ *    fp32 frequencies, read during the call only.  The angle is reduced
+ *    exactly to a turn at any position, its sine and cosine taken in fp32.
+ *  q_out: device bf16 [n_tokens][n_q_heads][head_dim] contiguous.
+ *  k_out, v_out: device bf16 [n_tokens][n_kv_heads][head_dim] contiguous, or
+ *    NULL: the keys and values as the cache now holds them, for a prompt's own
+ *    attention.  No output may overlap an input, except that q_out may be q's
+ *    own contiguous tensor.
+ * Codes: 8-bit s = fp16(max|x| * fl(1/127)), code = RNE(x / s) in [-127, 127],
+ * of the rotated key in fp32 (never rounded to bf16 first); 4-bit
+ * s = fp16(fl(max - min) * fl(1/15)), z = fp16(min), code = RNE((x - z) / s) in
+ * [0, 15]; s = 0 gives codes 0.  Non-finite elements are kept in BF16 pages;
+ * elsewhere they count and code as zeros and kvpages_status reports
+ * KVP_ERR_NONFINITE; a scale or zero point beyond fp16 is held at its largest
+ * value and reported as KVP_ERR_RANGE; a slot past the container is not
+ * written and reported as KVP_ERR_PAGE. */
+int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_tokens, int n_q_heads,
+                   const kvp_rows *q, const kvp_rows *k, const kvp_rows *v, const int64_t *slots,
+                   const int64_t *positions, const void *q_norm, const void *k_norm, float eps, int rot_dim,
+                   const float *inv_freq, void *q_out, void *k_out, void *v_out, void *stream);
+
+/* Read sequences back as bf16 past_key_values of one layer.
+ *  table: device int32 [n_seqs][max_pages] page ids; lens: device
+ *    int32[n_seqs] tokens of each sequence (table entries past a sequence's
+ *    length are not read).
+ *  k_dst, v_dst: device bf16 [n_seqs][n_kv_heads][max_tokens][head_dim];
+ *    sequence b's first min(lens[b], max_tokens) tokens, zeros after them.
+ * A page id outside the container, or a length beyond its table row, reads as
+ * zeros and is reported by kvpages_status as KVP_ERR_PAGE. */
+int kvpages_read(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, const int32_t *table,
+                 int max_pages, const int32_t *lens, int max_tokens, void *k_dst, void *v_dst, void *stream);
+
+/* Bytes of device workspace kvpages_attend needs (0 for invalid counts).  No
+ * initialisation. */
+size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads);
+
+/* Attention of each sequence's newest n_q_tokens tokens (1 to 64; already
+ * written to the pages) over the sequence's pages, causal among themselves:
+ * query token i of sequence b sees the first lens[b] - (n_q_tokens - 1 - i)
+ * tokens.
+ *  q: device bf16 [n_seqs][n_q_tokens][n_q_heads][head_dim]; query head j reads
+ *    KV head j / (n_q_heads / n_kv_heads).
+ *  table, max_pages, lens: as kvpages_read; n_seqs at most 8192.
+ *  base_out, base_lse: device fp32 [n_seqs][n_q_tokens][n_q_heads]([head_dim]),
+ *    both or neither (NULL): attention of the same queries over other tokens,
+ *    as kvpool_attend leaves it.  The result is then attention over both.
+ *  out: device bf16 [n_seqs][n_q_tokens][n_q_heads][head_dim].  lse: device
+ *    fp32 [n_seqs][n_q_tokens][n_q_heads] or NULL (natural log).
+ * A query that sees no token gets the base's output and lse, or zeros and -inf
+ * without one.  Scores are products of the stored codes accumulated in fp32,
+ * softmax statistics fp32.  A page id outside the container or a length beyond
+ * its table row is skipped and reported by kvpages_status as KVP_ERR_PAGE. */
+int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
+                   int n_q_heads, const void *q, float scale, const int32_t *table, int max_pages,
+                   const int32_t *lens, const float *base_out, const float *base_lse, void *out, float *lse, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Synchronises `stream`, then returns KVP_OK or the first device-detected
+ * error recorded in the container's header (KVP_ERR_HEADER if `pages` does not
+ * hold a version-1 container, or a call described another one). */
+int kvpages_status(const void *pages, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */
