@@ -37,6 +37,7 @@ KVP_K_Q8_0 = 1
 KVP_PAGES_BF16 = 0
 KVP_PAGES_K8V8 = 1
 KVP_PAGES_K8V4 = 2
+KVP_PAGES_MAX_SEQS = 8192
 KVP_NOALLOC_SCRATCH_BYTES = 262144
 KVP_PROBE_STORE = 0
 KVP_PROBE_BULK_STORE = 1
@@ -123,6 +124,7 @@ _SIGS = {
     "kvp_test_fail_next_encode": (C.c_int, [C.c_int, C.c_uint32]),
     "kvp_test_limit_next_attend": (C.c_int, [C.c_uint32]),
     "kvp_test_limit_next_unpack": (C.c_int, [C.c_uint32]),
+    "kvp_test_limit_next_pages_attend": (C.c_int, [C.c_uint32]),
 }
 
 _lib = None
@@ -383,6 +385,10 @@ def kvp_test_limit_next_attend(polls):
 
 def kvp_test_limit_next_unpack(polls):
     return load().kvp_test_limit_next_unpack(int(polls))
+
+
+def kvp_test_limit_next_pages_attend(polls):
+    return load().kvp_test_limit_next_pages_attend(int(polls))
 
 
 class KVPError(RuntimeError):

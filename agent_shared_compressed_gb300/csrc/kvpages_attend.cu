@@ -5,17 +5,56 @@
 //   s_t = scale q . k_t,  t < len_b - (m - 1 - i)
 //   out = sum_t softmax(s)_t v_t,  lse = log sum_t exp(s_t)
 // joined: L = log(e^lse + e^base_lse), out = e^(lse-L) out + e^(base_lse-L) base.
+// Exponentials are base 2 throughout.
 //
-// One block per (sequence, query token, query head): a lane quad takes every
-// 32nd token with its own running maximum and sum, and the block's quads are
-// merged at the end.
+// Bound: every cached byte is read once (4 query rows per KV head, say, do 16
+// multiply-adds per byte of 8-bit cache: far below what the tensor cores can
+// take), so the work is keeping enough bytes in flight on every SM and spending
+// few instructions on each.
+//
+// Work split.  The unit is a 16-token block of one (sequence, KV head, tile of
+// query rows).  All units of all sequences, in that order, are one list, cut
+// into equal runs, one per warp: no warp has more to do than another, however
+// ragged the lengths, and the cut follows from the lengths on the device, so a
+// captured graph stays right as sequences grow.  A warp that holds all blocks
+// of a row tile writes its result; otherwise it leaves a partial result (running
+// maximum, sum and weighted values) and pages_join merges them in list order, so
+// results do not depend on timing.
+//
+// A warp's blocks arrive by bulk copies, one per block (a block is one run of
+// bytes), in the warp's own ring in shared memory, on the warp's own barriers:
+// warps never wait for each other after the start.  The codes are in fragment
+// order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or of a
+// value token, expands them to fp16 in registers (exact: |code| <= 128), and
+// multiplies.  Key scales apply to the fp32 sums of their 32 dims.  Value
+// scales go into the weights, one product operand per 32 dims; a weight times
+// its scale is a sum of two bf16 (2^-17, and fp32's range: a token of large
+// weight and tiny values, an attention sink, takes nothing from the others),
+// and the codes are expanded to bf16, exact too.  Rows 8..15 of the product
+// carry the second bf16 where a tile has at most 8 rows.  16-bit pages are
+// multiplied as they are.
+//
+// 4-bit values q s + z enter as (q - c) s + (z + c s) with c the integer of
+// [0, 15] nearest to -z / s, formed once per token and group: then |z + c s| is
+// at most s / 2 (or of the code term's sign, where zero is outside the group's
+// range), and the two sums, of the code terms in the product and of the rest in
+// fp32 once per 32 dims, do not cancel.
+#include <algorithm>
 #include <cmath>
 
+#include "kvp_async.cuh"
 #include "kvp_pages.cuh"
 
 namespace kvp {
 
-constexpr int PAT_THREADS = 128;
+constexpr int PAT_WARPS = 8;
+constexpr int PAT_THREADS = PAT_WARPS * 32;
+constexpr int PAT_MIN_BLOCKS = 2;             // blocks of a warp's run, at least
+constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
+constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
+// The weights' reference is raised only when a score passes it by this much
+// (base 2), so that the accumulators are rarely rescaled.
+constexpr float PAT_SLACK = 8.0f;
 
 struct PagesAttendArgs {
     PagesView pv;
@@ -24,118 +63,913 @@ struct PagesAttendArgs {
     const float *base_out, *base_lse;
     uint16_t *out;
     float *lse;
-    float scale2;  // scale * log2(e)
-    int m, nq, max_pages;
+    float *part;     // [warps][2][rows][D] partial sums
+    float2 *stats;   // [warps][2][rows] (reference, sum), base 2
+    uint32_t *plan;  // [nseq + 1] blocks before each sequence
+    float scale2;    // scale * log2(e)
+    int nseq, m, nq, G, R, RT, max_pages;
+    uint32_t nwarps, polls;
 };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(PAT_THREADS) pages_attend(const __grid_constant__ PagesAttendArgs a) {
-    using B = Block<D, FMT>;
-    constexpr int NB = D / 32, NQD = PAT_THREADS / 4;
-    __shared__ float st[NQD][2];
-    __shared__ float acc_s[NQD][D + 1];
-    const int quad = threadIdx.x >> 2, tig = threadIdx.x & 3;
-    const uint64_t row = blockIdx.x;  // (b, i, j)
-    const int j = int(row % uint32_t(a.nq)), i = int(row / uint32_t(a.nq) % uint32_t(a.m));
-    const uint32_t b = uint32_t(row / (uint64_t(a.nq) * uint32_t(a.m)));
-    const int h = j / (a.nq / a.pv.H);
-    if (!pages_match(a.pv)) {
-        if (threadIdx.x == 0) pages_flag(a.pv, FLAG_HEADER);
-        return;
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void lds_floats(uint32_t at, float (&f)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = lds128(at);
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    } else {
+        const uint2 v = lds64(at);
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
     }
-    int len = max(a.lens[b], 0);
-    if (int64_t(len) > int64_t(a.max_pages) << a.pv.logP) {
-        if (threadIdx.x == 0) pages_flag(a.pv, FLAG_PAGE);
-        len = int(int64_t(a.max_pages) << a.pv.logP);
-    }
-    len = max(0, len - (a.m - 1 - i));
-    float q[NB][8], acc[NB][8];
-#pragma unroll
-    for (int g = 0; g < NB; ++g) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(a.q + row * D + 32 * g + 8 * tig);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q[g][2 * k] = bf16_lo(w[k]), q[g][2 * k + 1] = bf16_hi(w[k]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[g][k] = 0.0f;
-    }
-    float mx = -INFINITY, l = 0.0f;
-    for (int t = quad; t < (len + NQD - 1) / NQD * NQD; t += NQD) {
-        const uint8_t *src = nullptr;
-        if (t < len) {
-            const int page = a.table[uint64_t(b) * uint32_t(a.max_pages) + uint32_t(t >> a.pv.logP)];
-            if (page >= 0 && page < a.pv.n_pages)
-                src = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(h) * a.pv.tile_bytes +
-                      uint64_t((uint32_t(t) & uint32_t(a.pv.P - 1)) / PAGES_BLOCK) * B::BYTES;
-            else if (tig == 0)
-                pages_flag(a.pv, FLAG_PAGE);
-        }
-        float x[NB][8], s = 0.0f;
-        if (src) {
-            load_key_row<D, FMT>(src, uint32_t(t) % PAGES_BLOCK, tig, x);
-#pragma unroll
-            for (int g = 0; g < NB; ++g)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) s = fmaf(q[g][k], x[g][k], s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (!src) continue;
-        s *= a.scale2;
-        const float m2 = fmaxf(mx, s), ref = m2 == -INFINITY ? 0.0f : m2;
-        const float f = exp2f(mx - ref), p = exp2f(s - ref);
-        mx = m2;
-        l = l * f + p;
-        load_value_row<D, FMT>(src, uint32_t(t) % PAGES_BLOCK, tig, x);
-#pragma unroll
-        for (int g = 0; g < NB; ++g)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[g][k] = acc[g][k] * f + p * x[g][k];
-    }
-    if (tig == 0) st[quad][0] = mx, st[quad][1] = l;
-#pragma unroll
-    for (int g = 0; g < NB; ++g)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc_s[quad][32 * g + 8 * tig + k] = acc[g][k];
-    __syncthreads();
-    float M = -INFINITY, L = 0.0f, o = 0.0f;
-    for (int k = 0; k < NQD; ++k) M = fmaxf(M, st[k][0]);
-    const float ref = M == -INFINITY ? 0.0f : M;
-    if (threadIdx.x < D) {
-        for (int k = 0; k < NQD; ++k) {
-            const float f = exp2f(st[k][0] - ref);
-            L += f * st[k][1];
-            o += f * acc_s[k][threadIdx.x];
-        }
-        o = L > 0.0f ? o / L : 0.0f;
-        float lse = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-        if (a.base_out) {
-            const float bl = a.base_lse[row], top = fmaxf(lse, bl);
-            if (top > -INFINITY) {
-                const float wa = expf(lse - top), wb = expf(bl - top);
-                o = (wa * o + wb * a.base_out[row * D + threadIdx.x]) / (wa + wb);
-                lse = top + logf(wa + wb);
-            }
-        }
-        reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
-        if (threadIdx.x == 0 && a.lse) a.lse[row] = lse;
-    }
+}
+__device__ __forceinline__ void sts32(uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+}
+__device__ __forceinline__ void sts128_zero(uint32_t at) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
+}
+__device__ __forceinline__ float2 half2_f32(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two bytes u as fp16 u - 128: 1024 + u by byte placement, less 1152 (exact).
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
+    const uint32_t x = __byte_perm(w, 0x64646464u, sel), bias = 0x64806480u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// The bytes u of each 16-bit half (whatever their upper bytes hold) as bf16
+// u - 128: 128 + (u mod 128), less 256 or, with u's top bit, 128 (exact).
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+    const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, y = (w & 0x00800080u) ^ 0xC380C380u;
+    const __nv_bfloat162 r =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// The low nibble q of each 16-bit half as bf16 q - c: 128 + q, plus the halves of
+// y, -(128 + c) (exact).
+__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t y) {
+    const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 r =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// a = hi + lo in two bf16: the pair's high parts, and the remainders.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
+}
+__device__ __forceinline__ float quad_add(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float quad_top(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// The length that a sequence's table row can hold.
+__device__ __forceinline__ int seq_len(const PagesAttendArgs &a, int b, bool flag) {
+    const int len = max(__ldg(a.lens + b), 0);
+    const int64_t cap = int64_t(a.max_pages) << a.pv.logP;
+    if (int64_t(len) <= cap) return len;
+    if (flag) pages_flag(a.pv, FLAG_PAGE);
+    return int(cap);
+}
+
+// Blocks of a warp's run (both kernels).
+__device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) {
+    const uint64_t per = (units + nwarps - 1) / nwarps;
+    return per < PAT_MIN_BLOCKS ? PAT_MIN_BLOCKS : per;
 }
 
 template <int D, int FMT>
-static int launch_attend(const PagesAttendArgs &a, unsigned grid, cudaStream_t st) {
-    pages_attend<D, FMT><<<grid, PAT_THREADS, 0, st>>>(a);
-    count_launch();
+struct PatSmem {
+    static constexpr uint32_t SLOT = (Block<D, FMT>::BYTES + 127u) / 128u * 128u;
+    static constexpr uint32_t STAGES = SLOT > 8191u ? 3u : (22528u / SLOT > 8u ? 8u : 22528u / SLOT);
+    // 4-bit values: a warp's scales, remainders (fp32 [16][NG]) and -(128 + c) (bf16 pairs)
+    static constexpr uint32_t NE = 16u * Block<D, FMT>::NG;
+    static constexpr uint32_t PREP = Block<D, FMT>::V4 ? NE * 10u : 0u;
+    static constexpr uint32_t OFF_PREP = PAT_BAR_BYTES + PAT_WARPS * STAGES * SLOT;
+    static constexpr uint32_t OFF_PLAN = OFF_PREP + PAT_WARPS * PREP;
+    static_assert(PAT_WARPS * STAGES * 8 <= PAT_BAR_BYTES - 64, "a barrier per slot");
+    // with the static part, within the 227 KB of a block
+    static_assert(OFF_PLAN + 4u * (KVP_PAGES_MAX_SEQS + 1u) + 1024u <= 232448u, "shared memory of a block");
+    static uint32_t bytes(int nseq) { return OFF_PLAN + 4u * uint32_t(nseq + 1); }
+};
+
+// What one row of a tile ends with: the base joined in, bf16 output and lse.
+__device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t row, float lse, bool first) {
+    // weights of (this, base); an empty row without a base has none
+    float wa = 1.0f, wb = 0.0f;
+    if (a.base_lse) {
+        const float bl = a.base_lse[row], top = fmaxf(lse, bl);
+        if (top > -INFINITY) {
+            const float ea = expf(lse - top), eb = expf(bl - top), tot = ea + eb;
+            wa = ea / tot, wb = eb / tot;
+            lse = top + logf(tot);
+        }
+    }
+    if (first && a.lse) a.lse[row] = lse;
+    return make_float2(wa, wb);
+}
+
+// R8: halves of 8 query rows in a tile (1 or 2).
+template <int D, int FMT, int R8>
+__global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_constant__ PagesAttendArgs a) {
+    using B = Block<D, FMT>;
+    using SM = PatSmem<D, FMT>;
+    constexpr int NG = B::NG, NT = D / 8, RTILE = 8 * R8;
+    constexpr uint32_t STAGES = SM::STAGES;
+    constexpr bool Q8 = B::Q8, V4 = B::V4;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint32_t *pre = reinterpret_cast<uint32_t *>(sm + SM::OFF_PLAN);
+    __shared__ uint32_t wsum[PAT_WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+    const uint32_t bar = smem_addr(sm) + uint32_t(warp) * STAGES * 8u;
+    const uint32_t ring = smem_addr(sm) + PAT_BAR_BYTES + uint32_t(warp) * STAGES * SM::SLOT;
+    if (lane == 0) {
+        for (uint32_t s = 0; s < STAGES; ++s) mbar_init1(bar + 8u * s);
+        mbar_init_fence();
+    }
+    // the kernel before this one has completed past this point
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool match = pages_match(a.pv);
+    // blocks before each sequence
+    uint32_t carry = 0;
+    for (int b0 = 0; b0 < a.nseq; b0 += PAT_THREADS) {
+        const int b = b0 + tid;
+        uint32_t n = b < a.nseq ? uint32_t((seq_len(a, b, blockIdx.x == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += y;
+        }
+        if (lane == 31) wsum[warp] = n;
+        __syncthreads();
+        uint32_t before = carry;
+#pragma unroll
+        for (int w = 0; w < PAT_WARPS; ++w) {
+            const uint32_t s = wsum[w];
+            before += w < warp ? s : 0u;
+            carry += s;
+        }
+        if (b < a.nseq) {
+            pre[b + 1] = before + n;
+            if (blockIdx.x == 0) a.plan[b + 1] = before + n;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        pre[0] = 0u;
+        if (blockIdx.x == 0) a.plan[0] = 0u;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!match) {
+        if (tid == 0) pages_flag(a.pv, FLAG_HEADER);
+        return;
+    }
+    const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
+    const uint64_t units = uint64_t(carry) * HRT, per = run_length(units, a.nwarps);
+    const uint32_t gw = blockIdx.x * PAT_WARPS + uint32_t(warp);
+    const uint64_t f0 = gw * per;
+    if (f0 >= units) return;
+    const uint32_t cnt = uint32_t(f0 + per < units ? per : units - f0);
+
+    // unit f: its sequence, row tile and block
+    auto locate = [&](uint64_t f, int &b, uint32_t &tile, uint32_t &blk) {
+        const uint32_t p = (f >> 32) == 0 ? uint32_t(f) / HRT : uint32_t(f / HRT);
+        int lo = 0, hi = a.nseq - 1;  // the last b with pre[b] <= p
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] <= p)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const uint32_t n = pre[lo + 1] - pre[lo];
+        const uint64_t r = f - uint64_t(pre[lo]) * HRT;
+        b = lo;
+        if ((r >> 32) == 0) {
+            tile = uint32_t(r) / n;
+            blk = uint32_t(r) - tile * n;
+        } else {
+            tile = uint32_t(r / n);
+            blk = uint32_t(r - uint64_t(tile) * n);
+        }
+    };
+    // the lane's block of the 32 that start at unit `at` of the run: its address, or
+    // 0 past the run and for a bad page id
+    auto address = [&](uint32_t at) -> uint64_t {
+        const uint32_t u = at + uint32_t(lane);
+        if (u >= cnt) return 0;
+        int b;
+        uint32_t tile, blk;
+        locate(f0 + u, b, tile, blk);
+        const uint32_t t0 = blk * PAGES_BLOCK;
+        const int page = __ldg(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP));
+        if (page < 0 || page >= a.pv.n_pages) {
+            pages_flag(a.pv, FLAG_PAGE);
+            return 0;
+        }
+        return reinterpret_cast<uint64_t>(a.pv.layer) + uint64_t(page) * a.pv.page_bytes +
+               uint64_t(tile / uint32_t(a.RT)) * a.pv.tile_bytes +
+               uint64_t((t0 & uint32_t(a.pv.P - 1)) / PAGES_BLOCK) * B::BYTES;
+    };
+    // this lane's copy into slot s (nothing to copy: the phase still completes)
+    auto issue = [&](uint64_t src, uint32_t s) {
+        mbar_expect_tx(bar + 8u * s, src ? B::BYTES : 0u);
+        fence_proxy_async();  // the warp's reads of the slot come first
+        if (src) bulk_g2s(ring + s * SM::SLOT, reinterpret_cast<const void *>(src), B::BYTES, bar + 8u * s);
+    };
+
+    uint64_t cur = address(0), nxt = address(32);
+    uint32_t good = __ballot_sync(0xffffffffu, cur != 0);
+    if (uint32_t(lane) < STAGES && uint32_t(lane) < cnt) issue(cur, uint32_t(lane));
+
+    int b, len = 0;
+    uint32_t tile, blk, nblk = 0, seg0 = 0;
+    locate(f0, b, tile, blk);
+    bool fresh = true;           // the next block starts a segment
+    uint32_t slot = 0, phase = 0;  // ring position of the next block
+
+    // The segment's state.
+    uint32_t qf[NT / 2][2 * R8];      // query fragments: [k-step][row half, k half]
+    float qs[R8];                     // row factor of the scores (base 2)
+    int lim[R8];                      // tokens that the row sees
+    float ref[R8], sum[R8];
+    float acc[NT][4];
+    float zsum[V4 ? NG : 1][R8];
+
+    for (uint32_t n = 0; n < cnt; ++n) {
+        if (fresh) {
+            fresh = false;
+            seg0 = blk;
+            nblk = pre[b + 1] - pre[b];
+            len = seq_len(a, b, false);
+            const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
+#pragma unroll
+            for (int rr = 0; rr < R8; ++rr) {
+                const int r = r0 + 8 * rr + g;
+                const bool real = r < a.R;
+                const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
+                lim[rr] = real ? len - (a.m - 1 - i) : 0;
+                const uint16_t *qrow = a.q + ((uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
+                if constexpr (Q8) {
+                    // rows enter as fp16 times a power of two that brings their
+                    // largest element to [2^14, 2^15): exact but for elements
+                    // under 2^-28 of it
+                    uint4 v[NG];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) {
+                        v[k] = real ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * k + 8 * tig)) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+                    }
+                    top = quad_top(top);
+                    const int ex = int(__float_as_uint(top) >> 23);  // biased exponent
+                    const int up = ex == 255 ? 0 : min(141 - ex, 126);
+                    const float f = __uint_as_float(uint32_t(127 + up) << 23);
+                    qs[rr] = a.scale2 * __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) {
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            qf[2 * k + (e >> 1)][2 * rr + (e & 1)] = pack_f16x2(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
+                    }
+                } else {
+                    qs[rr] = a.scale2;
+#pragma unroll
+                    for (int k = 0; k < NT / 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            qf[k][2 * rr + e] =
+                                real ? __ldg(reinterpret_cast<const uint32_t *>(qrow + 16 * k + 8 * e + 2 * tig)) : 0u;
+                }
+                ref[rr] = -INFINITY;
+                sum[rr] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+            if constexpr (V4) {
+#pragma unroll
+                for (int k = 0; k < NG; ++k)
+#pragma unroll
+                    for (int rr = 0; rr < R8; ++rr) zsum[k][rr] = 0.0f;
+            }
+        }
+        if (!mbar_wait(bar + 8u * slot, phase, a.polls)) {
+            // a copy did not arrive in time: report it, let the copies in flight
+            // land (with the normal limit), and give the run up
+            if (lane == 0) {
+                pages_flag(a.pv, FLAG_TIMEOUT);
+                uint32_t s = slot, p = phase;
+                for (uint32_t k = n; k < cnt && k < n + STAGES; ++k) {
+                    mbar_wait(bar + 8u * s, p, PAT_WAIT_LIMIT);
+                    if (++s == STAGES) s = 0, p ^= 1u;
+                }
+            }
+            return;
+        }
+        if ((good >> (n & 31u)) & 1u) {
+            const uint32_t at = ring + slot * SM::SLOT;
+            const int t0 = int(blk) * PAGES_BLOCK;
+            const bool tail = t0 + PAGES_BLOCK > len - (a.m - 1);  // some row does not see all 16 tokens
+            const uint32_t prep = smem_addr(sm) + SM::OFF_PREP + uint32_t(warp) * SM::PREP;
+            if constexpr (V4) {
+#pragma unroll
+                for (int u = 0; u < NG / 2; ++u) {
+                    const int e = 32 * u + lane, t = e / NG, gr = e % NG;  // token, group
+                    const float2 sz = half2_f32(lds32(at + B::OFF_VS + 4u * uint32_t(e)));
+                    float s = sz.x, z = sz.y, c;
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(s));
+                    // any integer will do; NaN (0 / 0) becomes 0
+                    c = fminf(fmaxf(rintf(-z * c), 0.0f), 15.0f);
+                    const bool none = t0 + t >= len;  // never written
+                    sts32(prep + 4u * uint32_t(e), none ? 0.0f : s);
+                    sts32(prep + 4u * (SM::NE + uint32_t(e)), none ? 0.0f : fmaf(c, s, z));
+                    sts16(prep + 8u * SM::NE + 2u * uint32_t((t >> 1) * 2 * NG + gr * 2 + (t & 1)),
+                          __bfloat16_as_ushort(__float2bfloat16_rn(-128.0f - c)));
+                }
+                __syncwarp();
+            }
+            float x[2][2][R8];  // scores of tokens 8 nt + 2 tig + k
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                if constexpr (Q8) {
+                    uint32_t w[NG][2];
+                    float ks[2][NG];
+                    {
+                        const uint32_t ka = at + uint32_t(nt) * 8u * B::KROW +
+                                            (D == 128 ? uint32_t(g) * 128u + ((uint32_t(tig) * 32u) ^ ((uint32_t(g) & 1u) << 4))
+                                                      : uint32_t(g) * 64u + uint32_t(tig) * 16u);
+                        const uint4 v = lds128(ka);
+                        w[0][0] = v.x, w[0][1] = v.y, w[1][0] = v.z, w[1][1] = v.w;
+                        if constexpr (D == 128) {
+                            const uint4 u = lds128(ka ^ 16u);
+                            w[2][0] = u.x, w[2][1] = u.y, w[3][0] = u.z, w[3][1] = u.w;
+                        }
+                        const uint32_t sa = at + B::OFF_KS + uint32_t(8 * nt + 2 * tig) * B::SROW;
+                        uint32_t sw[2][NG / 2];
+                        if constexpr (D == 128) {
+                            const uint4 s = lds128(sa);
+                            sw[0][0] = s.x, sw[0][1] = s.y, sw[1][0] = s.z, sw[1][1] = s.w;
+                        } else {
+                            const uint2 s = lds64(sa);
+                            sw[0][0] = s.x, sw[1][0] = s.y;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < NG / 2; ++e) {
+                                const float2 f = half2_f32(sw[k][e]);
+                                ks[k][2 * e] = f.x, ks[k][2 * e + 1] = f.y;
+                            }
+                    }
+#pragma unroll
+                    for (int rr = 0; rr < R8; ++rr) x[nt][0][rr] = x[nt][1][rr] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) {
+                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            mma_f16(c, qf[2 * k + e][0], R8 == 2 ? qf[2 * k + e][2 * R8 - 2] : 0u, qf[2 * k + e][1],
+                                    R8 == 2 ? qf[2 * k + e][2 * R8 - 1] : 0u, codes_f16(w[k][e], 0x4140u),
+                                    codes_f16(w[k][e], 0x4342u));
+#pragma unroll
+                        for (int rr = 0; rr < R8; ++rr) {
+                            x[nt][0][rr] = fmaf(c[2 * rr], ks[0][k], x[nt][0][rr]);
+                            x[nt][1][rr] = fmaf(c[2 * rr + 1], ks[1][k], x[nt][1][rr]);
+                        }
+                    }
+                } else {
+                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint32_t t = uint32_t(lane & 7), c4 = uint32_t(lane >> 3);
+                    const uint32_t ka = at + (uint32_t(8 * nt) + t) * B::KROW + ((c4 * 16u) ^ (t << 4));
+#pragma unroll
+                    for (int k = 0; k < NT / 4; ++k) {
+                        uint32_t w[4];
+                        ldsm4(w, ka ^ (64u * uint32_t(k)));
+                        mma_bf16(c, qf[2 * k][0], R8 == 2 ? qf[2 * k][2 * R8 - 2] : 0u, qf[2 * k][1],
+                                 R8 == 2 ? qf[2 * k][2 * R8 - 1] : 0u, w[0], w[1]);
+                        mma_bf16(c, qf[2 * k + 1][0], R8 == 2 ? qf[2 * k + 1][2 * R8 - 2] : 0u, qf[2 * k + 1][1],
+                                 R8 == 2 ? qf[2 * k + 1][2 * R8 - 1] : 0u, w[2], w[3]);
+                    }
+#pragma unroll
+                    for (int rr = 0; rr < R8; ++rr) x[nt][0][rr] = c[2 * rr], x[nt][1][rr] = c[2 * rr + 1];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int rr = 0; rr < R8; ++rr) {
+                        x[nt][k][rr] *= qs[rr];
+                        if (tail && t0 + 8 * nt + 2 * tig + k >= lim[rr]) x[nt][k][rr] = -INFINITY;
+                    }
+            }
+            // value scales of the lane's tokens (V4: and z + c s, and -(128 + c))
+            float sv[2][2][Q8 ? NG : 1], zv[2][2][V4 ? NG : 1];
+            uint32_t cv[2][V4 ? NG : 1];
+            if constexpr (V4) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t pa = prep + 4u * NG * uint32_t(8 * nt + 2 * tig + k);
+                        lds_floats<NG>(pa, sv[nt][k]);
+                        lds_floats<NG>(pa + 4u * SM::NE, zv[nt][k]);
+                    }
+                    const uint32_t ca = prep + 8u * SM::NE + 4u * NG * uint32_t(4 * nt + tig);
+                    if constexpr (NG == 4) {
+                        const uint4 v = lds128(ca);
+                        cv[nt][0] = v.x, cv[nt][1] = v.y, cv[nt][NG - 2] = v.z, cv[nt][NG - 1] = v.w;
+                    } else {
+                        const uint2 v = lds64(ca);
+                        cv[nt][0] = v.x, cv[nt][1] = v.y;
+                    }
+                }
+            } else if constexpr (Q8) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint32_t sa = at + B::OFF_VS + uint32_t(8 * nt + 2 * tig) * B::VSROW;
+                    uint32_t sw[2][NG / 2];
+                    if constexpr (D == 128) {
+                        const uint4 s = lds128(sa);
+                        sw[0][0] = s.x, sw[0][1] = s.y, sw[1][0] = s.z, sw[1][1] = s.w;
+                    } else {
+                        const uint2 s = lds64(sa);
+                        sw[0][0] = s.x, sw[1][0] = s.y;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const bool none = tail && t0 + 8 * nt + 2 * tig + k >= len;  // never written
+#pragma unroll
+                        for (int e = 0; e < NG / 2; ++e) {
+                            const float2 f = half2_f32(none ? 0u : sw[k][e]);
+                            sv[nt][k][2 * e] = f.x, sv[nt][k][2 * e + 1] = f.y;
+                        }
+                    }
+                }
+            }
+            bool raise = false;
+            float top[R8];
+#pragma unroll
+            for (int rr = 0; rr < R8; ++rr) {
+                top[rr] = quad_top(fmaxf(fmaxf(x[0][0][rr], x[0][1][rr]), fmaxf(x[1][0][rr], x[1][1][rr])));
+                raise |= top[rr] > ref[rr] + PAT_SLACK;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int rr = 0; rr < R8; ++rr) {
+                    const float nr = fmaxf(ref[rr], top[rr]);
+                    const float f = nr == -INFINITY ? 1.0f : exp2f(ref[rr] - nr);
+                    ref[rr] = nr;
+                    sum[rr] *= f;
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) {
+                        acc[k][2 * rr] *= f, acc[k][2 * rr + 1] *= f;
+                        if (R8 == 1) acc[k][2] *= f, acc[k][3] *= f;
+                    }
+                    if constexpr (V4) {
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) zsum[k][rr] *= f;
+                    }
+                }
+            }
+            float p[2][2][R8];
+#pragma unroll
+            for (int rr = 0; rr < R8; ++rr) {
+                const float r = ref[rr] == -INFINITY ? 0.0f : ref[rr];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) p[nt][k][rr] = exp2f(x[nt][k][rr] - r);
+                sum[rr] += (p[0][0][rr] + p[0][1][rr]) + (p[1][0][rr] + p[1][1][rr]);
+            }
+            if constexpr (Q8) {
+                uint32_t vw[2][2][V4 ? NG / 2 : NG];  // the lane's granule of its four tokens
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t va = at + B::value(uint32_t(2 * tig + k), uint32_t(g) * (B::VROW / 8)) +
+                                            uint32_t(nt) * 8u * B::VROW;
+                        if constexpr (B::VROW == 128) {
+                            const uint4 v = lds128(va);
+                            vw[nt][k][0] = v.x, vw[nt][k][1] = v.y, vw[nt][k][NG - 2] = v.z, vw[nt][k][NG - 1] = v.w;
+                        } else if constexpr (B::VROW == 64) {
+                            const uint2 v = lds64(va);
+                            vw[nt][k][0] = v.x, vw[nt][k][1] = v.y;
+                        } else {
+                            vw[nt][k][0] = lds32(va);
+                        }
+                    }
+#pragma unroll
+                for (int e = 0; e < NG; ++e) {
+                    uint32_t pa[2 * R8], pl[2 * R8];
+#pragma unroll
+                    for (int rr = 0; rr < R8; ++rr)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            const float w0 = p[nt][0][rr] * sv[nt][0][e], w1 = p[nt][1][rr] * sv[nt][1][e];
+                            split_bf16x2(w0, w1, pa[2 * rr + nt], pl[2 * rr + nt]);
+                        }
+                    uint32_t v[2][4];  // [token half][dim of the granule's word]
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        if constexpr (!V4) {
+                            // byte j of both tokens' words to the halves' low bytes
+                            v[nt][0] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x5410u));
+                            v[nt][1] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x5511u));
+                            v[nt][2] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x6622u));
+                            v[nt][3] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x7733u));
+                        } else {
+                            const uint32_t w = __byte_perm(vw[nt][0][e / 2], vw[nt][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[nt][j] = nibbles_bf16(w >> (4 * j), cv[nt][e]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (R8 == 1) {
+                            mma_bf16(acc[4 * e + j], pa[0], pl[0], pa[1], pl[1], v[0][j], v[1][j]);
+                        } else {
+                            mma_bf16(acc[4 * e + j], pa[0], pa[2 * R8 - 2], pa[1], pa[2 * R8 - 1], v[0][j], v[1][j]);
+                            mma_bf16(acc[4 * e + j], pl[0], pl[2 * R8 - 2], pl[1], pl[2 * R8 - 1], v[0][j], v[1][j]);
+                        }
+                    }
+                    if constexpr (V4) {
+#pragma unroll
+                        for (int rr = 0; rr < R8; ++rr)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) zsum[e][rr] = fmaf(p[nt][k][rr], zv[nt][k][e], zsum[e][rr]);
+                    }
+                }
+            } else {
+                if (tail) {
+                    // rows of the block that some query does not see: zeros where no
+                    // query sees them; one that holds Inf or NaN is added by
+                    // itself to the rows that see it (0 * Inf would reach the others)
+                    const int first = max(len - (a.m - 1) - t0, 0), nv = len - t0;
+                    for (int t = max(first, 0); t < PAGES_BLOCK; ++t) {
+                        const uint32_t va = at + B::OFF_V + uint32_t(t) * B::VROW;
+                        bool odd = t >= nv;
+                        if (!odd) {
+                            bool inf = false;
+                            for (int c = lane; c < D / 2; c += 32) {
+                                const uint32_t w = lds32(va + 4u * uint32_t(c));
+                                inf |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+                            }
+                            odd = __any_sync(0xffffffffu, inf);
+                            if (odd) {
+#pragma unroll
+                                for (int rr = 0; rr < R8; ++rr) {
+                                    const int tt = t & 7;  // the token's weight is with lane tt / 2 of the quad
+                                    const float mine = t < 8 ? (tt & 1 ? p[0][1][rr] : p[0][0][rr])
+                                                             : (tt & 1 ? p[1][1][rr] : p[1][0][rr]);
+                                    const float w = __shfl_sync(0xffffffffu, mine, (lane & ~3) | (tt >> 1));
+                                    if (t0 + t < lim[rr]) {
+#pragma unroll
+                                        for (int k = 0; k < NT; ++k) {
+                                            const uint32_t u = lds32(
+                                                at + B::value(uint32_t(t), uint32_t(k) * 16u + uint32_t(tig) * 4u));
+                                            acc[k][2 * rr] = fmaf(w, bf16_lo(u), acc[k][2 * rr]);
+                                            acc[k][2 * rr + 1] = fmaf(w, bf16_hi(u), acc[k][2 * rr + 1]);
+                                        }
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                        }
+                        if (odd && lane < D / 8) sts128_zero(va + 16u * uint32_t(lane));
+                    }
+                    fence_proxy_async();  // before a later copy into the slot
+                    __syncwarp();
+                }
+                uint32_t hi[R8][2], lo[R8][2];
+#pragma unroll
+                for (int rr = 0; rr < R8; ++rr)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) split_bf16x2(p[nt][0][rr], p[nt][1][rr], hi[rr][nt], lo[rr][nt]);
+                const uint32_t t = uint32_t(lane & 15), c2 = uint32_t(lane >> 4);
+                const uint32_t va = at + B::OFF_V + t * B::VROW + ((c2 * 16u) ^ ((t & 7u) << 4));
+#pragma unroll
+                for (int k = 0; k < NT / 2; ++k) {
+                    uint32_t w[4];
+                    ldsm4_t(w, va ^ (32u * uint32_t(k)));
+                    if constexpr (R8 == 1) {
+                        mma_bf16(acc[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], w[0], w[1]);
+                        mma_bf16(acc[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], w[2], w[3]);
+                    } else {
+                        mma_bf16(acc[2 * k], hi[0][0], hi[R8 - 1][0], hi[0][1], hi[R8 - 1][1], w[0], w[1]);
+                        mma_bf16(acc[2 * k + 1], hi[0][0], hi[R8 - 1][0], hi[0][1], hi[R8 - 1][1], w[2], w[3]);
+                        mma_bf16(acc[2 * k], lo[0][0], lo[R8 - 1][0], lo[0][1], lo[R8 - 1][1], w[0], w[1]);
+                        mma_bf16(acc[2 * k + 1], lo[0][0], lo[R8 - 1][0], lo[0][1], lo[R8 - 1][1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();  // every lane is done with the slot
+        {
+            const uint32_t nx = n + STAGES;
+            if (nx < cnt && (nx & 31u) == uint32_t(lane)) issue((nx ^ n) < 32u ? cur : nxt, slot);
+        }
+        if (++slot == STAGES) slot = 0, phase ^= 1u;
+        if ((n & 31u) == 31u) {
+            cur = nxt;
+            good = __ballot_sync(0xffffffffu, cur != 0);
+            nxt = address(n + 33u);
+        }
+        ++blk;
+        if (blk < nblk && n + 1 < cnt) continue;
+        // the segment's end
+        const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
+        const bool whole = seg0 == 0 && blk == nblk;
+        if constexpr (R8 == 1) {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) acc[k][0] += acc[k][2], acc[k][1] += acc[k][3];
+        }
+        if constexpr (V4) {
+#pragma unroll
+            for (int e = 0; e < NG; ++e)
+#pragma unroll
+                for (int rr = 0; rr < R8; ++rr) {
+                    const float z = quad_add(zsum[e][rr]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[4 * e + j][2 * rr] += z, acc[4 * e + j][2 * rr + 1] += z;
+                }
+        }
+#pragma unroll
+        for (int rr = 0; rr < R8; ++rr) {
+            const int r = r0 + 8 * rr + g;
+            const float l = quad_add(sum[rr]);
+            if (r >= a.R) continue;
+            if (whole) {
+                const int i = r / a.G, j = h * a.G + r - i * a.G;
+                const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+                const float lse = l > 0.0f ? (ref[rr] + log2f(l)) * 0.69314718055994531f
+                                           : (l == 0.0f ? -INFINITY : l);
+                const float2 w = join_base(a, row, lse, tig == 0);
+                const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+                uint16_t *o = a.out + row * D;
+                const float *bo = a.base_out ? a.base_out + row * D : nullptr;
+                if constexpr (Q8) {
+#pragma unroll
+                    for (int e = 0; e < NG; ++e) {
+                        float y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = acc[4 * e + (k & 3)][2 * rr + (k >> 2)] * inv;
+                        if (bo) {
+                            const float4 b0 = *reinterpret_cast<const float4 *>(bo + 32 * e + 8 * tig);
+                            const float4 b1 = *reinterpret_cast<const float4 *>(bo + 32 * e + 8 * tig + 4);
+                            const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[k] = w.y != 0.0f ? fmaf(w.y, bb[k], y[k]) : y[k];
+                        }
+                        *reinterpret_cast<uint4 *>(o + 32 * e + 8 * tig) =
+                            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7]));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) {
+                        float y0 = acc[k][2 * rr] * inv, y1 = acc[k][2 * rr + 1] * inv;
+                        if (bo && w.y != 0.0f) {
+                            const float2 b0 = *reinterpret_cast<const float2 *>(bo + 8 * k + 2 * tig);
+                            y0 = fmaf(w.y, b0.x, y0), y1 = fmaf(w.y, b0.y, y1);
+                        }
+                        *reinterpret_cast<uint32_t *>(o + 8 * k + 2 * tig) = pack_bf16x2(y0, y1);
+                    }
+                }
+            } else {
+                // slot 0: the segment that the run starts with; 1: its last
+                const uint64_t ps = (uint64_t(gw) * 2u + (n + 1 == blk - seg0 ? 0u : 1u)) * RTILE + uint32_t(8 * rr + g);
+                float *o = a.part + ps * D;
+                if constexpr (Q8) {
+#pragma unroll
+                    for (int e = 0; e < NG; ++e)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<float4 *>(o + 32 * e + 8 * tig + 4 * k) =
+                                make_float4(acc[4 * e][2 * rr + k], acc[4 * e + 1][2 * rr + k], acc[4 * e + 2][2 * rr + k],
+                                            acc[4 * e + 3][2 * rr + k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NT; ++k)
+                        *reinterpret_cast<float2 *>(o + 8 * k + 2 * tig) = make_float2(acc[k][2 * rr], acc[k][2 * rr + 1]);
+                }
+                if (tig == 0) a.stats[ps] = make_float2(ref[rr], l);
+            }
+        }
+        fresh = true;
+        if (blk == nblk) {
+            blk = 0;
+            if (++tile == HRT) {
+                tile = 0;
+                do ++b;
+                while (b < a.nseq && pre[b + 1] == pre[b]);
+            }
+        }
+    }
+}
+
+// Merges the partial results of the rows whose blocks several warps had, and
+// writes the rows of empty sequences.  One block per query row; its four warps
+// take every fourth partial.
+template <int D, int RTILE>
+__global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesAttendArgs a) {
+    constexpr int VPL = D / 32;  // values of a lane
+    __shared__ float macc[4][D], mst[4][2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!pages_match(a.pv)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t row = blockIdx.x;
+    const int j = int(row % uint32_t(a.nq)), i = int(row / uint32_t(a.nq) % uint32_t(a.m));
+    const uint32_t b = uint32_t(row / (uint64_t(a.nq) * uint32_t(a.m)));
+    const int h = j / a.G, r = i * a.G + j % a.G, rt = r / RTILE;
+    const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
+    const uint32_t before = a.plan[b], n = a.plan[b + 1] - before;
+    const uint64_t per = run_length(uint64_t(a.plan[a.nseq]) * HRT, a.nwarps);
+    const uint64_t first = uint64_t(before) * HRT + uint64_t(h * a.RT + rt) * n;
+    const uint64_t w0 = first / per, w1 = n ? (first + n - 1) / per : w0;
+    if (n && w0 == w1) return;  // one warp had it all
+    float acc[VPL], M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
+    const uint32_t parts = n ? uint32_t(w1 - w0 + 1) : 0u;
+    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += 128u) {  // 32 partials of this warp at a time
+        const uint32_t c = c0 + 4u * uint32_t(lane);
+        float2 st = make_float2(-INFINITY, 0.0f);
+        uint64_t ps = 0;
+        if (c < parts) {
+            const uint64_t w = w0 + c;
+            ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
+            st = a.stats[ps];
+        }
+        float top = st.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float nm = fmaxf(M, top), f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
+        const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - nm);
+        float l = f * st.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        L = L * f0 + l;
+        M = nm;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) acc[k] *= f0;
+        const int here = int(min(32u, (parts - c0 + 3u) / 4u));
+#pragma unroll 4
+        for (int k = 0; k < here; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const uint64_t pk = __shfl_sync(0xffffffffu, ps, k);
+            const float *src = a.part + pk * D + lane * VPL;
+            if constexpr (VPL == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                acc[0] = fmaf(fk, v.x, acc[0]), acc[1] = fmaf(fk, v.y, acc[1]);
+                acc[2] = fmaf(fk, v.z, acc[2]), acc[3] = fmaf(fk, v.w, acc[3]);
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                acc[0] = fmaf(fk, v.x, acc[0]), acc[1] = fmaf(fk, v.y, acc[1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) macc[warp][lane * VPL + k] = acc[k];
+    if (lane == 0) mst[warp][0] = M, mst[warp][1] = L;
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    float top = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, mst[k][0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
+        l = fmaf(f, mst[k][1], l);
+        o = fmaf(f, macc[k][threadIdx.x], o);
+    }
+    const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
+    const float2 w = join_base(a, row, lse, threadIdx.x == 0);
+    o *= l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+    if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
+    reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
+}
+
+static thread_local uint32_t g_next_polls = 0;
+static thread_local bool g_limit_next = false;
+
+static unsigned attend_grid() { return unsigned(sm_count()); }
+static int tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
+
+template <int D, int FMT, int R8>
+static int launch_attend(const PagesAttendArgs &a, cudaStream_t st) {
+    using SM = PatSmem<D, FMT>;
+    const uint32_t bytes = SM::bytes(a.nseq);
+    // the opt-in to more than 48 KB, once per device (to the most that any call needs)
+    static bool ready[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        if (cudaFuncSetAttribute(pages_attend<D, FMT, R8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(SM::bytes(KVP_PAGES_MAX_SEQS))) != cudaSuccess)
+            return KVP_ERR_CUDA;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(attend_grid());
+    cfg.blockDim = dim3(PAT_THREADS);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, R8>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, pages_join<D, 8 * R8>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    count_launch(2);
     return launch_status();
+}
+
+template <int D, int FMT>
+static int launch_attend(const PagesAttendArgs &a, int rows, cudaStream_t st) {
+    return rows == 8 ? launch_attend<D, FMT, 1>(a, st) : launch_attend<D, FMT, 2>(a, st);
 }
 
 static int attend_counts_ok(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {
     const int rc = pages_ok(cfg);
     if (rc != KVP_OK) return rc;
     if (n_seqs < 0 || n_q_tokens <= 0 || n_q_heads <= 0 || n_q_heads % cfg->n_kv_heads != 0) return KVP_ERR_ARG;
-    if (n_seqs > 8192 || n_q_tokens > 64 || n_q_heads > 65536) return KVP_ERR_SIZE;
+    if (n_seqs > KVP_PAGES_MAX_SEQS || n_q_tokens > 64 || n_q_heads > 65536) return KVP_ERR_SIZE;
     if (int64_t(n_seqs) * n_q_tokens * n_q_heads >= (int64_t(1) << 31)) return KVP_ERR_SIZE;
     return KVP_OK;
+}
+
+// Workspace: the plan, the partial rows' statistics, the partial rows.
+struct AttendWs {
+    uint64_t stats, part, total;
+};
+static AttendWs attend_ws(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {
+    const uint64_t rows =
+        uint64_t(attend_grid()) * PAT_WARPS * 2u * uint64_t(tile_rows(n_q_tokens * (n_q_heads / cfg->n_kv_heads)));
+    AttendWs w;
+    w.stats = align256(4ull * uint64_t(n_seqs + 1));
+    w.part = w.stats + align256(rows * 8ull);
+    w.total = w.part + rows * uint64_t(cfg->head_dim) * 4ull;
+    return w;
 }
 
 }  // namespace kvp
@@ -146,7 +980,13 @@ extern "C" {
 
 size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {
     if (attend_counts_ok(cfg, n_seqs, n_q_tokens, n_q_heads) != KVP_OK) return 0;
-    return 256;
+    return size_t(attend_ws(cfg, n_seqs, n_q_tokens, n_q_heads).total);
+}
+
+int kvp_test_limit_next_pages_attend(uint32_t polls) {
+    g_next_polls = polls;
+    g_limit_next = true;
+    return KVP_OK;
 }
 
 int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
@@ -161,25 +1001,38 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
     if (!aligned(pages, 256) || !aligned(q, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(base_out, 16) ||
         !aligned(base_lse, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 16))
         return KVP_ERR_ALIGN;
-    if (ws_bytes < kvpages_attend_workspace_bytes(cfg, n_seqs, n_q_tokens, n_q_heads)) return KVP_ERR_SIZE;
+    const AttendWs w = attend_ws(cfg, n_seqs, n_q_tokens, n_q_heads);
+    if (ws_bytes < w.total) return KVP_ERR_SIZE;
+    // block counts are 32-bit
+    const unsigned __int128 blocks = (unsigned __int128)uint32_t(max_pages) * uint32_t(cfg->page_tokens / 16) * uint32_t(n_seqs);
+    if (blocks >> 32) return KVP_ERR_SIZE;
     if (n_seqs == 0) return KVP_OK;
     PagesAttendArgs a;
     a.pv = pages_view(const_cast<void *>(pages), *cfg, layer);
     a.q = static_cast<const uint16_t *>(q);
     a.table = table, a.lens = lens, a.base_out = base_out, a.base_lse = base_lse;
     a.out = static_cast<uint16_t *>(out), a.lse = lse;
+    a.plan = static_cast<uint32_t *>(ws);
+    a.stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + w.stats);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.part);
     a.scale2 = scale * 1.4426950408889634f;
-    a.m = n_q_tokens, a.nq = n_q_heads, a.max_pages = max_pages;
-    const unsigned grid = unsigned(n_seqs) * unsigned(n_q_tokens) * unsigned(n_q_heads);
+    a.nseq = n_seqs, a.m = n_q_tokens, a.nq = n_q_heads, a.G = n_q_heads / cfg->n_kv_heads;
+    a.R = n_q_tokens * a.G;
+    const int rows = tile_rows(a.R);
+    a.RT = (a.R + rows - 1) / rows;
+    a.max_pages = max_pages;
+    a.nwarps = attend_grid() * PAT_WARPS;
+    a.polls = g_limit_next ? g_next_polls : PAT_WAIT_LIMIT;
+    g_limit_next = false;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool d128 = cfg->head_dim == 128;
     switch (cfg->format) {
         case KVP_PAGES_BF16:
-            return d128 ? launch_attend<128, KVP_PAGES_BF16>(a, grid, st) : launch_attend<64, KVP_PAGES_BF16>(a, grid, st);
+            return d128 ? launch_attend<128, KVP_PAGES_BF16>(a, rows, st) : launch_attend<64, KVP_PAGES_BF16>(a, rows, st);
         case KVP_PAGES_K8V8:
-            return d128 ? launch_attend<128, KVP_PAGES_K8V8>(a, grid, st) : launch_attend<64, KVP_PAGES_K8V8>(a, grid, st);
+            return d128 ? launch_attend<128, KVP_PAGES_K8V8>(a, rows, st) : launch_attend<64, KVP_PAGES_K8V8>(a, rows, st);
         default:
-            return d128 ? launch_attend<128, KVP_PAGES_K8V4>(a, grid, st) : launch_attend<64, KVP_PAGES_K8V4>(a, grid, st);
+            return d128 ? launch_attend<128, KVP_PAGES_K8V4>(a, rows, st) : launch_attend<64, KVP_PAGES_K8V4>(a, rows, st);
     }
 }
 

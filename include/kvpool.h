@@ -47,10 +47,11 @@
  *    by the *_status calls.  No kernel traps or asserts.  Two kinds of
  *    device-side wait exist, both bounded: the pool encoder's key-quantize
  *    work waits for its layer's scale, released by another block of the same
- *    kernel; pool attention and CacheCard unpack wait on mbarriers for their
- *    own bulk copies into shared memory.  A wait that runs out is recorded in
- *    the pool's or the card's error word and reported as KVP_ERR_TIMEOUT by
- *    kvpool_status / cachecard_status; the CUDA context stays usable.
+ *    kernel; pool attention, CacheCard unpack and attention over pages wait
+ *    on mbarriers for their own bulk copies into shared memory.  A wait that
+ *    runs out is recorded in the container's error word and reported as
+ *    KVP_ERR_TIMEOUT by kvpool_status / cachecard_status / kvpages_status; the
+ *    CUDA context stays usable.
  */
 #ifndef KVPOOL_H
 #define KVPOOL_H
@@ -369,6 +370,9 @@ int cachecard_status(const void *card, void *stream);
 /* Pages: an agent's own cache                                             */
 /* ---------------------------------------------------------------------- */
 
+/* Most sequences of one kvpages_attend call. */
+#define KVP_PAGES_MAX_SEQS 8192
+
 /* A page container: n_pages pages in each of n_layers layers; a page holds
  * page_tokens tokens (a power of two, 16 to 1024) of all KV heads.  Which
  * pages hold which sequence is the caller's: a table row of page ids per
@@ -455,7 +459,8 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  * tokens.
  *  q: device bf16 [n_seqs][n_q_tokens][n_q_heads][head_dim]; query head j reads
  *    KV head j / (n_q_heads / n_kv_heads).
- *  table, max_pages, lens: as kvpages_read; n_seqs at most 8192.
+ *  table, max_pages, lens: as kvpages_read; n_seqs at most KVP_PAGES_MAX_SEQS,
+ *    and n_seqs * max_pages * page_tokens below 2^36.
  *  base_out, base_lse: device fp32 [n_seqs][n_q_tokens][n_q_heads]([head_dim]),
  *    both or neither (NULL): attention of the same queries over other tokens,
  *    as kvpool_attend leaves it.  The result is then attention over both.
@@ -463,7 +468,10 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  *    fp32 [n_seqs][n_q_tokens][n_q_heads] or NULL (natural log).
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  Scores are products of the stored codes accumulated in fp32,
- * softmax statistics fp32.  A page id outside the container or a length beyond
+ * softmax statistics fp32; the weights (times the values' scales) enter the
+ * value product as a sum of two bf16 (2^-17).  The kernel waits for its bulk copies of the
+ * pages at most about half a second; should a wait run out, the outputs are
+ * unspecified and kvpages_status reports KVP_ERR_TIMEOUT.  A page id outside the container or a length beyond
  * its table row is skipped and reported by kvpages_status as KVP_ERR_PAGE. */
 int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
                    int n_q_heads, const void *q, float scale, const int32_t *table, int max_pages,
@@ -535,6 +543,13 @@ int kvp_test_limit_next_attend(uint32_t polls);
  * each record's copies at most `polls` times (0: not at all, so every warp
  * gives up on its first record); other shapes ignore it.  Returns KVP_OK. */
 int kvp_test_limit_next_unpack(uint32_t polls);
+
+/* Failure-path testing of attention over pages: makes the NEXT kvpages_attend
+ * on this thread poll each block's copy at most `polls` times (0: not at all,
+ * so every warp gives up on its first block, lets its copies in flight land
+ * with the normal limit, and leaves its rows unwritten); kvpages_status then
+ * reports KVP_ERR_TIMEOUT and the CUDA context stays usable.  Returns KVP_OK. */
+int kvp_test_limit_next_pages_attend(uint32_t polls);
 
 #ifdef __cplusplus
 }

@@ -568,3 +568,48 @@ def test_joined_with_the_pool(fmt):
     # the decoded pool's bf16 keys and values stand for the pool's own: 2^-8 each
     assert np.all(np.abs(lse - ref_lse) <= 2.0 ** -8 * reach)
     assert np.all(np.abs(out - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -6 + 2.0 ** -7 * reach[..., None]) * mass)
+
+
+def test_attend_wait_timeout_is_reported_and_context_survives():
+    """With the next call limited to zero polls every warp gives up on its first
+    block, lets its copies land and returns; the call after it is right."""
+    H, d, lens = 4, 128, [900, 20]
+    k, v = _kv(sum(lens), H, d, 18)
+    pg = Pages("k8v8", H, d, 64, lens)
+    pg.append(k, v)
+    q = torch.randn(2, 1, 8, d).to(torch.bfloat16).cuda()
+    assert kv.kvp_test_limit_next_pages_attend(0) == kv.KVP_OK
+    pg.attend(q, 0.1)
+    assert pg.status() == kv.KVP_ERR_TIMEOUT
+    assert kv.kvpages_init(pg.cfg, pg.buf.t, pg.buf.nbytes) == kv.KVP_OK  # clears the error word; the pages stay
+    out, lse = pg.attend(q, 0.1)
+    assert pg.status() == kv.KVP_OK
+    _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), "k8v8", False), lens),
+                  _split(P.held(_f64(v), "k8v8", True), lens), lens, 0.1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_masked_draft_tokens_with_infinities(d):
+    """16-bit pages: a drafted token whose value is Inf or NaN reaches the
+    queries that see it and no others."""
+    H, n, m = 2, 45, 4
+    k, v = _kv(n, H, d, 19)
+    v[n - 2, 0, 5], v[n - 1, 1, 9] = float("inf"), float("nan")
+    pg = Pages("bf16", H, d, 16, [n])
+    pg.append(k, v)
+    q = torch.randn(1, m, 4, d).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.1)
+    assert np.all(np.isfinite(out[0, :2])) and np.all(np.isfinite(lse))
+    clean = v.clone()
+    clean[n - 2:] = 0
+    ref, _, mass, _ = P.attend(_f64(q), [_f64(k)], [_f64(clean)], [n], 0.1)
+    assert np.all(np.abs(out[0, :2] - ref[0, :2]) <= 2.0 ** -8 * np.abs(ref[0, :2]) + 2.0 ** -10 * mass[0, :2])
+    assert np.all(out[0, 2:, :2, 5] == np.inf) and np.all(np.isnan(out[0, 3, 2:, 9]))
+    assert np.all(np.isfinite(out[0, 2, 2:]))
+    # rows that see the Inf are right in their other dims
+    keep = [i for i in range(d) if i != 5]
+    full = v.clone()
+    full[n - 2, 0, 5] = 0
+    ref, _, mass, _ = P.attend(_f64(q), [_f64(k)], [_f64(full)], [n], 0.1)
+    assert np.all(np.abs(out[0, 2:, :2][..., keep] - ref[0, 2:, :2][..., keep])
+                  <= 2.0 ** -8 * np.abs(ref[0, 2:, :2][..., keep]) + 2.0 ** -10 * mass[0, 2:, :2][..., keep])
