@@ -37,7 +37,7 @@ KVP_K_Q8_0 = 1
 KVP_PAGES_BF16 = 0
 KVP_PAGES_K8V8 = 1
 KVP_PAGES_K8V4 = 2
-KVP_PAGES_MAX_SEQS = 8192
+KVP_PAGES_MAX_SEQS = 4096
 KVP_NOALLOC_SCRATCH_BYTES = 262144
 KVP_PROBE_STORE = 0
 KVP_PROBE_BULK_STORE = 1

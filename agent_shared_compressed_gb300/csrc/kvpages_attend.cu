@@ -16,29 +16,36 @@
 // query rows).  All units of all sequences, in that order, are one list, cut
 // into equal runs, one per warp: no warp has more to do than another, however
 // ragged the lengths, and the cut follows from the lengths on the device, so a
-// captured graph stays right as sequences grow.  A warp that holds all blocks
+// captured graph stays right as sequences grow.  A row tile counts PAT_ITEM
+// units more than it has blocks, for its start and end.  A warp that holds all
 // of a row tile writes its result; otherwise it leaves a partial result (running
 // maximum, sum and weighted values) and pages_join merges them in list order, so
 // results do not depend on timing.
 //
 // A warp's blocks arrive by bulk copies, one per block (a block is one run of
 // bytes), in the warp's own ring in shared memory, on the warp's own barriers:
-// warps never wait for each other after the start.  The codes are in fragment
-// order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or of a
-// value token, expands them to fp16 in registers (exact: |code| <= 128), and
-// multiplies.  Key scales apply to the fp32 sums of their 32 dims.  Value
-// scales go into the weights, one product operand per 32 dims; a weight times
-// its scale is a sum of two bf16 (2^-17, and fp32's range: a token of large
-// weight and tiny values, an attention sink, takes nothing from the others),
-// and the codes are expanded to bf16, exact too.  Rows 8..15 of the product
-// carry the second bf16 where a tile has at most 8 rows.  16-bit pages are
-// multiplied as they are.
+// warps never wait for each other after the start.
 //
-// 4-bit values q s + z enter as (q - c) s + (z + c s) with c the integer of
-// [0, 15] nearest to -z / s, formed once per token and group: then |z + c s| is
-// at most s / 2 (or of the code term's sign, where zero is outside the group's
-// range), and the two sums, of the code terms in the product and of the rest in
-// fp32 once per 32 dims, do not cancel.
+// Products, with tokens or dims as the 16 rows and the query rows as the 8
+// columns, so that a tile of up to 8 query rows wastes nothing:
+//   S^T = K Q^T    C: tokens g, g + 8 x queries 2 tig, 2 tig + 1
+//   O^T = V^T P^T  C: dims x queries 2 tig, 2 tig + 1
+// P^T comes from S^T's fragment by two 8 x 8 transposes.  The codes are in
+// fragment order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or
+// of a value token and expands them in registers, keys to fp16 and values to
+// bf16 (exact: |code| <= 128).  What bounds 8- and 4-bit pages beside memory is
+// that expansion, most of it on the integer pipe, which takes a warp's
+// instruction every other cycle: two to four instructions per pair of codes.
+//
+// Key scales apply to the fp32 sums of their 32 dims.  Value scales go into the
+// weights, one product operand per 32 dims; a weight times its scale enters as a
+// sum of two bf16 (2^-17, and fp32's range: a token of large weight and tiny
+// values, an attention sink, takes nothing from the others).  4-bit values
+// q s + z enter as (q - c) s + (z + c s) with c the integer of [0, 15] nearest to
+// -z / s, formed once per token and group: then |z + c s| is at most s / 2 (or of
+// the code term's sign, where zero is outside the group's range), and the two
+// sums, of the code terms in the product and of the rest in fp32 once per 32
+// dims, do not cancel.  16-bit pages are multiplied as they are.
 #include <algorithm>
 #include <cmath>
 
@@ -47,9 +54,9 @@
 
 namespace kvp {
 
-constexpr int PAT_WARPS = 8;
-constexpr int PAT_THREADS = PAT_WARPS * 32;
-constexpr int PAT_MIN_BLOCKS = 2;             // blocks of a warp's run, at least
+constexpr int PAT_MOST_WARPS = 16;             // of a block
+constexpr uint32_t PAT_ITEM = 2;               // units that a row tile counts beside its blocks
+constexpr uint32_t PAT_MIN_RUN = 3;            // units of a warp's run, at least
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
@@ -65,7 +72,7 @@ struct PagesAttendArgs {
     float *lse;
     float *part;     // [warps][2][rows][D] partial sums
     float2 *stats;   // [warps][2][rows] (reference, sum), base 2
-    uint32_t *plan;  // [nseq + 1] blocks before each sequence
+    uint32_t *plan;  // [nseq + 1] units before each sequence, per row tile
     float scale2;    // scale * log2(e)
     int nseq, m, nq, G, R, RT, max_pages;
     uint32_t nwarps, polls;
@@ -119,6 +126,25 @@ __device__ __forceinline__ void lds_floats(uint32_t at, float (&f)[N]) {
         f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
     }
 }
+__device__ __forceinline__ float2 half2_f32(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+// N fp16 values as fp32.
+template <int N>
+__device__ __forceinline__ void lds_halfs(uint32_t at, float (&f)[N]) {
+    uint32_t w[2] = {0u, 0u};
+    if constexpr (N == 4) {
+        const uint2 v = lds64(at);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = lds32(at);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 v = half2_f32(w[i]);
+        f[2 * i] = v.x, f[2 * i + 1] = v.y;
+    }
+}
 __device__ __forceinline__ void sts32(uint32_t at, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
@@ -127,9 +153,6 @@ __device__ __forceinline__ void sts16(uint32_t at, uint16_t v) {
 }
 __device__ __forceinline__ void sts128_zero(uint32_t at) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
-}
-__device__ __forceinline__ float2 half2_f32(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -157,18 +180,32 @@ __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t y) {
         __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// The transpose of an 8 x 8 matrix of 16-bit values, in fragment layout.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {  // results under 2^-126 are 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // a = hi + lo in two bf16: the pair's high parts, and the remainders.
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16x2(a, b);
     lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
 }
-__device__ __forceinline__ float quad_add(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// Over the eight lanes of a quad position (the rows of a C fragment).
+__device__ __forceinline__ float rows_add(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
-__device__ __forceinline__ float quad_top(float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+__device__ __forceinline__ float rows_top(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 
 // The length that a sequence's table row can hold.
@@ -180,22 +217,25 @@ __device__ __forceinline__ int seq_len(const PagesAttendArgs &a, int b, bool fla
     return int(cap);
 }
 
-// Blocks of a warp's run (both kernels).
+// Units of a warp's run (both kernels).
 __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) {
     const uint64_t per = (units + nwarps - 1) / nwarps;
-    return per < PAT_MIN_BLOCKS ? PAT_MIN_BLOCKS : per;
+    return per < PAT_MIN_RUN ? PAT_MIN_RUN : per;
 }
 
-template <int D, int FMT>
-struct PatSmem {
+// Warps of a block: as many as the registers of a tile's state allow.
+template <int D, int FMT, int R8>
+struct PatShape {
+    static constexpr int WARPS = FMT == KVP_PAGES_BF16 && D == 128 ? 8 : (R8 == 2 && D == 128 ? 8 : 16);
     static constexpr uint32_t SLOT = (Block<D, FMT>::BYTES + 127u) / 128u * 128u;
-    static constexpr uint32_t STAGES = SLOT > 8191u ? 3u : (22528u / SLOT > 8u ? 8u : 22528u / SLOT);
+    static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
+    static constexpr uint32_t STAGES = RING < 3u ? 3u : (RING > 8u ? 8u : RING);
     // 4-bit values: a warp's scales, remainders (fp32 [16][NG]) and -(128 + c) (bf16 pairs)
     static constexpr uint32_t NE = 16u * Block<D, FMT>::NG;
     static constexpr uint32_t PREP = Block<D, FMT>::V4 ? NE * 10u : 0u;
-    static constexpr uint32_t OFF_PREP = PAT_BAR_BYTES + PAT_WARPS * STAGES * SLOT;
-    static constexpr uint32_t OFF_PLAN = OFF_PREP + PAT_WARPS * PREP;
-    static_assert(PAT_WARPS * STAGES * 8 <= PAT_BAR_BYTES - 64, "a barrier per slot");
+    static constexpr uint32_t OFF_PREP = PAT_BAR_BYTES + WARPS * STAGES * SLOT;
+    static constexpr uint32_t OFF_PLAN = OFF_PREP + WARPS * PREP;
+    static_assert(WARPS * STAGES * 8 <= PAT_BAR_BYTES, "a barrier per slot");
     // with the static part, within the 227 KB of a block
     static_assert(OFF_PLAN + 4u * (KVP_PAGES_MAX_SEQS + 1u) + 1024u <= 232448u, "shared memory of a block");
     static uint32_t bytes(int nseq) { return OFF_PLAN + 4u * uint32_t(nseq + 1); }
@@ -217,17 +257,18 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
     return make_float2(wa, wb);
 }
 
-// R8: halves of 8 query rows in a tile (1 or 2).
+// R8: groups of 8 query rows in a tile (1 or 2).
 template <int D, int FMT, int R8>
-__global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_constant__ PagesAttendArgs a) {
+__global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
+    pages_attend(const __grid_constant__ PagesAttendArgs a) {
     using B = Block<D, FMT>;
-    using SM = PatSmem<D, FMT>;
-    constexpr int NG = B::NG, NT = D / 8, RTILE = 8 * R8;
+    using SM = PatShape<D, FMT, R8>;
+    constexpr int NG = B::NG, MT = D / 16, RTILE = 8 * R8, WARPS = SM::WARPS, THREADS = WARPS * 32;
     constexpr uint32_t STAGES = SM::STAGES;
     constexpr bool Q8 = B::Q8, V4 = B::V4;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint32_t *pre = reinterpret_cast<uint32_t *>(sm + SM::OFF_PLAN);
-    __shared__ uint32_t wsum[PAT_WARPS];
+    __shared__ uint32_t wsum[WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
     const uint32_t bar = smem_addr(sm) + uint32_t(warp) * STAGES * 8u;
     const uint32_t ring = smem_addr(sm) + PAT_BAR_BYTES + uint32_t(warp) * STAGES * SM::SLOT;
@@ -238,11 +279,12 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
     // the kernel before this one has completed past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool match = pages_match(a.pv);
-    // blocks before each sequence
+    // units before each sequence (of one row tile)
     uint32_t carry = 0;
-    for (int b0 = 0; b0 < a.nseq; b0 += PAT_THREADS) {
+    for (int b0 = 0; b0 < a.nseq; b0 += THREADS) {
         const int b = b0 + tid;
         uint32_t n = b < a.nseq ? uint32_t((seq_len(a, b, blockIdx.x == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
+        n += n ? PAT_ITEM : 0u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
@@ -252,7 +294,7 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
         __syncthreads();
         uint32_t before = carry;
 #pragma unroll
-        for (int w = 0; w < PAT_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const uint32_t s = wsum[w];
             before += w < warp ? s : 0u;
             carry += s;
@@ -275,13 +317,13 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
     }
     const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
     const uint64_t units = uint64_t(carry) * HRT, per = run_length(units, a.nwarps);
-    const uint32_t gw = blockIdx.x * PAT_WARPS + uint32_t(warp);
+    const uint32_t gw = blockIdx.x * WARPS + uint32_t(warp);
     const uint64_t f0 = gw * per;
     if (f0 >= units) return;
     const uint32_t cnt = uint32_t(f0 + per < units ? per : units - f0);
 
-    // unit f: its sequence, row tile and block
-    auto locate = [&](uint64_t f, int &b, uint32_t &tile, uint32_t &blk) {
+    // unit f: its sequence, row tile and place in the tile (PAT_ITEM empty places, then the blocks)
+    auto locate = [&](uint64_t f, int &b, uint32_t &tile, uint32_t &at) {
         const uint32_t p = (f >> 32) == 0 ? uint32_t(f) / HRT : uint32_t(f / HRT);
         int lo = 0, hi = a.nseq - 1;  // the last b with pre[b] <= p
         while (lo < hi) {
@@ -296,21 +338,22 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
         b = lo;
         if ((r >> 32) == 0) {
             tile = uint32_t(r) / n;
-            blk = uint32_t(r) - tile * n;
+            at = uint32_t(r) - tile * n;
         } else {
             tile = uint32_t(r / n);
-            blk = uint32_t(r - uint64_t(tile) * n);
+            at = uint32_t(r - uint64_t(tile) * n);
         }
     };
-    // the lane's block of the 32 that start at unit `at` of the run: its address, or
-    // 0 past the run and for a bad page id
-    auto address = [&](uint32_t at) -> uint64_t {
-        const uint32_t u = at + uint32_t(lane);
+    // the lane's block of the 32 units that start at `first` of the run: its address, or
+    // 0 past the run, in a tile's empty places and for a bad page id
+    auto address = [&](uint32_t first) -> uint64_t {
+        const uint32_t u = first + uint32_t(lane);
         if (u >= cnt) return 0;
         int b;
-        uint32_t tile, blk;
-        locate(f0 + u, b, tile, blk);
-        const uint32_t t0 = blk * PAGES_BLOCK;
+        uint32_t tile, at;
+        locate(f0 + u, b, tile, at);
+        if (at < PAT_ITEM) return 0;
+        const uint32_t t0 = (at - PAT_ITEM) * PAGES_BLOCK;
         const int page = __ldg(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP));
         if (page < 0 || page >= a.pv.n_pages) {
             pages_flag(a.pv, FLAG_PAGE);
@@ -332,33 +375,42 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
     if (uint32_t(lane) < STAGES && uint32_t(lane) < cnt) issue(cur, uint32_t(lane));
 
     int b, len = 0;
-    uint32_t tile, blk, nblk = 0, seg0 = 0;
-    locate(f0, b, tile, blk);
-    bool fresh = true;           // the next block starts a segment
-    uint32_t slot = 0, phase = 0;  // ring position of the next block
+    uint32_t tile, place, nplace = 0, seg0 = 0;
+    locate(f0, b, tile, place);
+    bool fresh = true;             // the next unit starts a segment
+    uint32_t slot = 0, phase = 0;  // ring position of the next unit
 
-    // The segment's state.
-    uint32_t qf[NT / 2][2 * R8];      // query fragments: [k-step][row half, k half]
-    float qs[R8];                     // row factor of the scores (base 2)
-    int lim[R8];                      // tokens that the row sees
-    float ref[R8], sum[R8];
-    float acc[NT][4];
-    float zsum[V4 ? NG : 1][R8];
+    // where the lane's bytes are in a slot
+    const uint32_t k_off = Q8 ? B::key(uint32_t(g), uint32_t(tig) * (D / 4))
+                              : B::key(uint32_t(lane & 15), uint32_t(lane >> 4) * 16u);
+    const uint32_t v_off = Q8 ? B::value(uint32_t(2 * tig), uint32_t(g) * (B::VROW / 8))
+                              : B::value(uint32_t((lane & 7) + ((lane >> 4) << 3)), uint32_t((lane >> 3) & 1) * 16u);
+    const uint32_t v_odd = Q8 ? B::value(uint32_t(2 * tig + 1), uint32_t(g) * (B::VROW / 8)) : 0u;
+    const uint32_t prep = smem_addr(sm) + SM::OFF_PREP + uint32_t(warp) * SM::PREP;
+
+    // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c).
+    uint32_t qf[D / 16][R8][2];  // query fragments by k-step
+    float qs[R8][2];             // factor of the scores (base 2)
+    int lim[R8][2];              // tokens that the query sees
+    float ref[R8][2];            // running maximum score, raised lazily
+    float sum[R8][2];            // the lane's part of the sum of weights
+    float acc[MT][R8][4];
+    float zsum[V4 ? NG : 1][R8][2];
 
     for (uint32_t n = 0; n < cnt; ++n) {
         if (fresh) {
             fresh = false;
-            seg0 = blk;
-            nblk = pre[b + 1] - pre[b];
+            seg0 = place;
+            nplace = pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
             const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
 #pragma unroll
-            for (int rr = 0; rr < R8; ++rr) {
-                const int r = r0 + 8 * rr + g;
+            for (int t = 0; t < R8; ++t) {
+                const int r = r0 + 8 * t + g;
                 const bool real = r < a.R;
                 const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
-                lim[rr] = real ? len - (a.m - 1 - i) : 0;
                 const uint16_t *qrow = a.q + ((uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
+                int up = 0;
                 if constexpr (Q8) {
                     // rows enter as fp16 times a power of two that brings their
                     // largest element to [2^14, 2^15): exact but for elements
@@ -372,39 +424,47 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
 #pragma unroll
                         for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
                     }
-                    top = quad_top(top);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const int ex = int(__float_as_uint(top) >> 23);  // biased exponent
-                    const int up = ex == 255 ? 0 : min(141 - ex, 126);
+                    up = ex == 255 ? 0 : min(141 - ex, 126);
                     const float f = __uint_as_float(uint32_t(127 + up) << 23);
-                    qs[rr] = a.scale2 * __uint_as_float(uint32_t(127 - up) << 23);
 #pragma unroll
                     for (int k = 0; k < NG; ++k) {
                         const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            qf[2 * k + (e >> 1)][2 * rr + (e & 1)] = pack_f16x2(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
+                            qf[2 * k + (e >> 1)][t][e & 1] = pack_f16x2(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
                     }
                 } else {
-                    qs[rr] = a.scale2;
 #pragma unroll
-                    for (int k = 0; k < NT / 2; ++k)
+                    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            qf[k][2 * rr + e] =
+                            qf[k][t][e] =
                                 real ? __ldg(reinterpret_cast<const uint32_t *>(qrow + 16 * k + 8 * e + 2 * tig)) : 0u;
                 }
-                ref[rr] = -INFINITY;
-                sum[rr] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int rc = r0 + 8 * t + 2 * tig + c;
+                    lim[t][c] = rc < a.R ? len - (a.m - 1 - rc / a.G) : 0;
+                    const int u = __shfl_sync(0xffffffffu, up, (2 * tig + c) * 4);
+                    qs[t][c] = Q8 ? a.scale2 * __uint_as_float(uint32_t(127 - u) << 23) : a.scale2;
+                    ref[t][c] = -INFINITY;
+                    sum[t][c] = 0.0f;
+                }
             }
 #pragma unroll
-            for (int k = 0; k < NT; ++k)
+            for (int k = 0; k < MT; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+                for (int t = 0; t < R8; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[k][t][e] = 0.0f;
             if constexpr (V4) {
 #pragma unroll
                 for (int k = 0; k < NG; ++k)
 #pragma unroll
-                    for (int rr = 0; rr < R8; ++rr) zsum[k][rr] = 0.0f;
+                    for (int t = 0; t < R8; ++t) zsum[k][t][0] = zsum[k][t][1] = 0.0f;
             }
         }
         if (!mbar_wait(bar + 8u * slot, phase, a.polls)) {
@@ -422,246 +482,222 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
         }
         if ((good >> (n & 31u)) & 1u) {
             const uint32_t at = ring + slot * SM::SLOT;
-            const int t0 = int(blk) * PAGES_BLOCK;
-            const bool tail = t0 + PAGES_BLOCK > len - (a.m - 1);  // some row does not see all 16 tokens
-            const uint32_t prep = smem_addr(sm) + SM::OFF_PREP + uint32_t(warp) * SM::PREP;
+            const int t0 = int(place - PAT_ITEM) * PAGES_BLOCK;
+            const bool tail = t0 + PAGES_BLOCK > len - (a.m - 1);  // some query does not see all 16 tokens
+            if (Q8 && tail) {
+                // tokens never written: their value scales (and zero points) may be anything
+                const int nv = len - t0;
+                if (lane >= nv && lane < PAGES_BLOCK) {
+                    const uint32_t sa = at + B::OFF_VS + uint32_t(lane) * B::VSROW;
+#pragma unroll
+                    for (uint32_t k = 0; k < B::VSROW; k += 4) sts32(sa + k, 0.0f);
+                }
+                fence_proxy_async();  // before a later copy into the slot
+                __syncwarp();
+            }
             if constexpr (V4) {
 #pragma unroll
                 for (int u = 0; u < NG / 2; ++u) {
                     const int e = 32 * u + lane, t = e / NG, gr = e % NG;  // token, group
                     const float2 sz = half2_f32(lds32(at + B::OFF_VS + 4u * uint32_t(e)));
-                    float s = sz.x, z = sz.y, c;
-                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(s));
+                    float c;
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(sz.x));
                     // any integer will do; NaN (0 / 0) becomes 0
-                    c = fminf(fmaxf(rintf(-z * c), 0.0f), 15.0f);
-                    const bool none = t0 + t >= len;  // never written
-                    sts32(prep + 4u * uint32_t(e), none ? 0.0f : s);
-                    sts32(prep + 4u * (SM::NE + uint32_t(e)), none ? 0.0f : fmaf(c, s, z));
-                    sts16(prep + 8u * SM::NE + 2u * uint32_t((t >> 1) * 2 * NG + gr * 2 + (t & 1)),
-                          __bfloat16_as_ushort(__float2bfloat16_rn(-128.0f - c)));
+                    c = fminf(fmaxf(rintf(-sz.y * c), 0.0f), 15.0f);
+                    sts32(prep + 4u * uint32_t(e), sz.x);
+                    sts32(prep + 4u * (SM::NE + uint32_t(e)), fmaf(c, sz.x, sz.y));
+                    const uint32_t ca = prep + 8u * SM::NE + 2u * uint32_t((t >> 1) * 2 * NG + gr * 2 + (t & 1));
+                    sts16(ca, __bfloat16_as_ushort(__float2bfloat16_rn(-128.0f - c)));
                 }
                 __syncwarp();
             }
-            float x[2][2][R8];  // scores of tokens 8 nt + 2 tig + k
+            // scores: x[t][0..1] token g, [2..3] token g + 8, of the two queries
+            float x[R8][4];
+            if constexpr (Q8) {
+                uint32_t w[2][NG][2];
+                float ks[2][NG];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                if constexpr (Q8) {
-                    uint32_t w[NG][2];
-                    float ks[2][NG];
-                    {
-                        const uint32_t ka = at + uint32_t(nt) * 8u * B::KROW +
-                                            (D == 128 ? uint32_t(g) * 128u + ((uint32_t(tig) * 32u) ^ ((uint32_t(g) & 1u) << 4))
-                                                      : uint32_t(g) * 64u + uint32_t(tig) * 16u);
-                        const uint4 v = lds128(ka);
-                        w[0][0] = v.x, w[0][1] = v.y, w[1][0] = v.z, w[1][1] = v.w;
-                        if constexpr (D == 128) {
-                            const uint4 u = lds128(ka ^ 16u);
-                            w[2][0] = u.x, w[2][1] = u.y, w[3][0] = u.z, w[3][1] = u.w;
-                        }
-                        const uint32_t sa = at + B::OFF_KS + uint32_t(8 * nt + 2 * tig) * B::SROW;
-                        uint32_t sw[2][NG / 2];
-                        if constexpr (D == 128) {
-                            const uint4 s = lds128(sa);
-                            sw[0][0] = s.x, sw[0][1] = s.y, sw[1][0] = s.z, sw[1][1] = s.w;
-                        } else {
-                            const uint2 s = lds64(sa);
-                            sw[0][0] = s.x, sw[1][0] = s.y;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int e = 0; e < NG / 2; ++e) {
-                                const float2 f = half2_f32(sw[k][e]);
-                                ks[k][2 * e] = f.x, ks[k][2 * e + 1] = f.y;
-                            }
-                    }
-#pragma unroll
-                    for (int rr = 0; rr < R8; ++rr) x[nt][0][rr] = x[nt][1][rr] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < NG; ++k) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            mma_f16(c, qf[2 * k + e][0], R8 == 2 ? qf[2 * k + e][2 * R8 - 2] : 0u, qf[2 * k + e][1],
-                                    R8 == 2 ? qf[2 * k + e][2 * R8 - 1] : 0u, codes_f16(w[k][e], 0x4140u),
-                                    codes_f16(w[k][e], 0x4342u));
-#pragma unroll
-                        for (int rr = 0; rr < R8; ++rr) {
-                            x[nt][0][rr] = fmaf(c[2 * rr], ks[0][k], x[nt][0][rr]);
-                            x[nt][1][rr] = fmaf(c[2 * rr + 1], ks[1][k], x[nt][1][rr]);
-                        }
-                    }
-                } else {
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const uint32_t t = uint32_t(lane & 7), c4 = uint32_t(lane >> 3);
-                    const uint32_t ka = at + (uint32_t(8 * nt) + t) * B::KROW + ((c4 * 16u) ^ (t << 4));
-#pragma unroll
-                    for (int k = 0; k < NT / 4; ++k) {
-                        uint32_t w[4];
-                        ldsm4(w, ka ^ (64u * uint32_t(k)));
-                        mma_bf16(c, qf[2 * k][0], R8 == 2 ? qf[2 * k][2 * R8 - 2] : 0u, qf[2 * k][1],
-                                 R8 == 2 ? qf[2 * k][2 * R8 - 1] : 0u, w[0], w[1]);
-                        mma_bf16(c, qf[2 * k + 1][0], R8 == 2 ? qf[2 * k + 1][2 * R8 - 2] : 0u, qf[2 * k + 1][1],
-                                 R8 == 2 ? qf[2 * k + 1][2 * R8 - 1] : 0u, w[2], w[3]);
-                    }
-#pragma unroll
-                    for (int rr = 0; rr < R8; ++rr) x[nt][0][rr] = c[2 * rr], x[nt][1][rr] = c[2 * rr + 1];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int rr = 0; rr < R8; ++rr) {
-                        x[nt][k][rr] *= qs[rr];
-                        if (tail && t0 + 8 * nt + 2 * tig + k >= lim[rr]) x[nt][k][rr] = -INFINITY;
-                    }
-            }
-            // value scales of the lane's tokens (V4: and z + c s, and -(128 + c))
-            float sv[2][2][Q8 ? NG : 1], zv[2][2][V4 ? NG : 1];
-            uint32_t cv[2][V4 ? NG : 1];
-            if constexpr (V4) {
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t pa = prep + 4u * NG * uint32_t(8 * nt + 2 * tig + k);
-                        lds_floats<NG>(pa, sv[nt][k]);
-                        lds_floats<NG>(pa + 4u * SM::NE, zv[nt][k]);
-                    }
-                    const uint32_t ca = prep + 8u * SM::NE + 4u * NG * uint32_t(4 * nt + tig);
-                    if constexpr (NG == 4) {
-                        const uint4 v = lds128(ca);
-                        cv[nt][0] = v.x, cv[nt][1] = v.y, cv[nt][NG - 2] = v.z, cv[nt][NG - 1] = v.w;
-                    } else {
-                        const uint2 v = lds64(ca);
-                        cv[nt][0] = v.x, cv[nt][1] = v.y;
-                    }
-                }
-            } else if constexpr (Q8) {
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint32_t sa = at + B::OFF_VS + uint32_t(8 * nt + 2 * tig) * B::VSROW;
-                    uint32_t sw[2][NG / 2];
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t ka = at + k_off + uint32_t(hf) * 8u * B::KROW;
+                    const uint4 v = lds128(ka);
+                    w[hf][0][0] = v.x, w[hf][0][1] = v.y, w[hf][1][0] = v.z, w[hf][1][1] = v.w;
                     if constexpr (D == 128) {
-                        const uint4 s = lds128(sa);
-                        sw[0][0] = s.x, sw[0][1] = s.y, sw[1][0] = s.z, sw[1][1] = s.w;
-                    } else {
-                        const uint2 s = lds64(sa);
-                        sw[0][0] = s.x, sw[1][0] = s.y;
+                        const uint4 u = lds128(ka ^ 16u);
+                        w[hf][2][0] = u.x, w[hf][2][1] = u.y, w[hf][3][0] = u.z, w[hf][3][1] = u.w;
+                    }
+                    lds_halfs<NG>(at + B::OFF_KS + uint32_t(8 * hf + g) * B::SROW, ks[hf]);
+                }
+#pragma unroll
+                for (int t = 0; t < R8; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) {
+                    float c[R8][4];
+#pragma unroll
+                    for (int t = 0; t < R8; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a0 = codes_f16(w[0][k][e], 0x4140u), a1 = codes_f16(w[1][k][e], 0x4140u);
+                        const uint32_t a2 = codes_f16(w[0][k][e], 0x4342u), a3 = codes_f16(w[1][k][e], 0x4342u);
+#pragma unroll
+                        for (int t = 0; t < R8; ++t) mma_f16(c[t], a0, a1, a2, a3, qf[2 * k + e][t][0], qf[2 * k + e][t][1]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const bool none = tail && t0 + 8 * nt + 2 * tig + k >= len;  // never written
+                    for (int t = 0; t < R8; ++t)
 #pragma unroll
-                        for (int e = 0; e < NG / 2; ++e) {
-                            const float2 f = half2_f32(none ? 0u : sw[k][e]);
-                            sv[nt][k][2 * e] = f.x, sv[nt][k][2 * e + 1] = f.y;
-                        }
+                        for (int e = 0; e < 4; ++e) x[t][e] = fmaf(c[t][e], ks[e >> 1][k], x[t][e]);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < R8; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t w[4];
+                    ldsm4(w, (at + k_off) ^ (32u * uint32_t(k)));
+#pragma unroll
+                    for (int t = 0; t < R8; ++t) mma_bf16(x[t], w[0], w[1], w[2], w[3], qf[k][t][0], qf[k][t][1]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < R8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][e] *= qs[t][e & 1];
+            if (tail) {
+#pragma unroll
+                for (int t = 0; t < R8; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t0 + g + 8 * (e >> 1) >= lim[t][e & 1]) x[t][e] = -INFINITY;
+            }
+            // value scales of tokens g and g + 8
+            float sv[2][Q8 ? NG : 1], zv[2][V4 ? NG : 1];
+            if constexpr (Q8) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    if constexpr (V4) {
+                        const uint32_t pa = prep + 4u * NG * uint32_t(8 * hf + g);
+                        lds_floats<NG>(pa, sv[hf]);
+                        lds_floats<NG>(pa + 4u * SM::NE, zv[hf]);
+                    } else {
+                        lds_halfs<NG>(at + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[hf]);
                     }
                 }
             }
             bool raise = false;
-            float top[R8];
+            float top[R8][2];
 #pragma unroll
-            for (int rr = 0; rr < R8; ++rr) {
-                top[rr] = quad_top(fmaxf(fmaxf(x[0][0][rr], x[0][1][rr]), fmaxf(x[1][0][rr], x[1][1][rr])));
-                raise |= top[rr] > ref[rr] + PAT_SLACK;
-            }
+            for (int t = 0; t < R8; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    top[t][c] = fmaxf(x[t][c], x[t][2 + c]);
+                    raise |= top[t][c] > ref[t][c] + PAT_SLACK;
+                }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int rr = 0; rr < R8; ++rr) {
-                    const float nr = fmaxf(ref[rr], top[rr]);
-                    const float f = nr == -INFINITY ? 1.0f : exp2f(ref[rr] - nr);
-                    ref[rr] = nr;
-                    sum[rr] *= f;
+                for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int k = 0; k < NT; ++k) {
-                        acc[k][2 * rr] *= f, acc[k][2 * rr + 1] *= f;
-                        if (R8 == 1) acc[k][2] *= f, acc[k][3] *= f;
-                    }
-                    if constexpr (V4) {
+                    for (int c = 0; c < 2; ++c) {
+                        const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
+                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
+                        ref[t][c] = nr;
+                        sum[t][c] *= f;
 #pragma unroll
-                        for (int k = 0; k < NG; ++k) zsum[k][rr] *= f;
-                    }
-                }
-            }
-            float p[2][2][R8];
+                        for (int k = 0; k < MT; ++k) acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
+                        if constexpr (V4) {
 #pragma unroll
-            for (int rr = 0; rr < R8; ++rr) {
-                const float r = ref[rr] == -INFINITY ? 0.0f : ref[rr];
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) p[nt][k][rr] = exp2f(x[nt][k][rr] - r);
-                sum[rr] += (p[0][0][rr] + p[0][1][rr]) + (p[1][0][rr] + p[1][1][rr]);
-            }
-            if constexpr (Q8) {
-                uint32_t vw[2][2][V4 ? NG / 2 : NG];  // the lane's granule of its four tokens
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t va = at + B::value(uint32_t(2 * tig + k), uint32_t(g) * (B::VROW / 8)) +
-                                            uint32_t(nt) * 8u * B::VROW;
-                        if constexpr (B::VROW == 128) {
-                            const uint4 v = lds128(va);
-                            vw[nt][k][0] = v.x, vw[nt][k][1] = v.y, vw[nt][k][NG - 2] = v.z, vw[nt][k][NG - 1] = v.w;
-                        } else if constexpr (B::VROW == 64) {
-                            const uint2 v = lds64(va);
-                            vw[nt][k][0] = v.x, vw[nt][k][1] = v.y;
-                        } else {
-                            vw[nt][k][0] = lds32(va);
+                            for (int k = 0; k < NG; ++k) zsum[k][t][c] *= f;
                         }
                     }
+            }
+            float p[R8][4];
+#pragma unroll
+            for (int t = 0; t < R8; ++t) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float r = ref[t][c] == -INFINITY ? 0.0f : ref[t][c];
+                    p[t][c] = exp2_fast(x[t][c] - r);
+                    p[t][2 + c] = exp2_fast(x[t][2 + c] - r);
+                    sum[t][c] += p[t][c] + p[t][2 + c];
+                }
+            }
+            if constexpr (Q8) {
+                uint32_t vw[2][2][V4 ? NG / 2 : NG];  // [token half][odd token]: the lane's granule
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t va = at + (k ? v_odd : v_off) + uint32_t(hf) * 8u * B::VROW;
+                        if constexpr (B::VROW == 128) {
+                            const uint4 v = lds128(va);
+                            vw[hf][k][0] = v.x, vw[hf][k][1] = v.y, vw[hf][k][NG - 2] = v.z, vw[hf][k][NG - 1] = v.w;
+                        } else if constexpr (B::VROW == 64) {
+                            const uint2 v = lds64(va);
+                            vw[hf][k][0] = v.x, vw[hf][k][1] = v.y;
+                        } else {
+                            vw[hf][k][0] = lds32(va);
+                        }
+                    }
+                uint32_t cv[2][V4 ? NG : 1];  // [token half]
+                if constexpr (V4) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t ca = prep + 8u * SM::NE + 4u * NG * uint32_t(4 * hf + tig);
+                        if constexpr (NG == 4) {
+                            const uint4 v = lds128(ca);
+                            cv[hf][0] = v.x, cv[hf][1] = v.y, cv[hf][NG - 2] = v.z, cv[hf][NG - 1] = v.w;
+                        } else {
+                            const uint2 v = lds64(ca);
+                            cv[hf][0] = v.x, cv[hf][1] = v.y;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < NG; ++e) {
-                    uint32_t pa[2 * R8], pl[2 * R8];
+                    uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
-                    for (int rr = 0; rr < R8; ++rr)
+                    for (int t = 0; t < R8; ++t)
 #pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            const float w0 = p[nt][0][rr] * sv[nt][0][e], w1 = p[nt][1][rr] * sv[nt][1][e];
-                            split_bf16x2(w0, w1, pa[2 * rr + nt], pl[2 * rr + nt]);
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t h2, l2;
+                            split_bf16x2(p[t][2 * hf] * sv[hf][e], p[t][2 * hf + 1] * sv[hf][e], h2, l2);
+                            hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
                         }
                     uint32_t v[2][4];  // [token half][dim of the granule's word]
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
+                    for (int hf = 0; hf < 2; ++hf) {
                         if constexpr (!V4) {
                             // byte j of both tokens' words to the halves' low bytes
-                            v[nt][0] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x5410u));
-                            v[nt][1] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x5511u));
-                            v[nt][2] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x6622u));
-                            v[nt][3] = codes_bf16(__byte_perm(vw[nt][0][e], vw[nt][1][e], 0x7733u));
+                            v[hf][0] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5410u));
+                            v[hf][1] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5511u));
+                            v[hf][2] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x6622u));
+                            v[hf][3] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x7733u));
                         } else {
-                            const uint32_t w = __byte_perm(vw[nt][0][e / 2], vw[nt][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
+                            const uint32_t w = __byte_perm(vw[hf][0][e / 2], vw[hf][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[nt][j] = nibbles_bf16(w >> (4 * j), cv[nt][e]);
+                            for (int j = 0; j < 4; ++j) v[hf][j] = nibbles_bf16(w >> (4 * j), cv[hf][e]);
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (R8 == 1) {
-                            mma_bf16(acc[4 * e + j], pa[0], pl[0], pa[1], pl[1], v[0][j], v[1][j]);
-                        } else {
-                            mma_bf16(acc[4 * e + j], pa[0], pa[2 * R8 - 2], pa[1], pa[2 * R8 - 1], v[0][j], v[1][j]);
-                            mma_bf16(acc[4 * e + j], pl[0], pl[2 * R8 - 2], pl[1], pl[2 * R8 - 1], v[0][j], v[1][j]);
+                    for (int t = 0; t < R8; ++t)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            mma_bf16(acc[2 * e + u][t], v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1], hi[t][0], hi[t][1]);
+                            mma_bf16(acc[2 * e + u][t], v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1], lo[t][0], lo[t][1]);
                         }
-                    }
                     if constexpr (V4) {
 #pragma unroll
-                        for (int rr = 0; rr < R8; ++rr)
+                        for (int t = 0; t < R8; ++t)
 #pragma unroll
-                            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) zsum[e][rr] = fmaf(p[nt][k][rr], zv[nt][k][e], zsum[e][rr]);
+                            for (int c = 0; c < 4; ++c)
+                                zsum[e][t][c & 1] = fmaf(p[t][c], zv[c >> 1][e], zsum[e][t][c & 1]);
                     }
                 }
             } else {
                 if (tail) {
-                    // rows of the block that some query does not see: zeros where no
-                    // query sees them; one that holds Inf or NaN is added by
-                    // itself to the rows that see it (0 * Inf would reach the others)
-                    const int first = max(len - (a.m - 1) - t0, 0), nv = len - t0;
-                    for (int t = max(first, 0); t < PAGES_BLOCK; ++t) {
+                    // tokens of the block that some query does not see: zeros where
+                    // none sees them; one that holds Inf or NaN is added by itself
+                    // to the queries that see it (0 * Inf would reach the others)
+                    const int nv = len - t0;
+                    for (int t = max(nv - (a.m - 1), 0); t < PAGES_BLOCK; ++t) {
                         const uint32_t va = at + B::OFF_V + uint32_t(t) * B::VROW;
                         bool odd = t >= nv;
                         if (!odd) {
@@ -673,21 +709,24 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
                             odd = __any_sync(0xffffffffu, inf);
                             if (odd) {
 #pragma unroll
-                                for (int rr = 0; rr < R8; ++rr) {
-                                    const int tt = t & 7;  // the token's weight is with lane tt / 2 of the quad
-                                    const float mine = t < 8 ? (tt & 1 ? p[0][1][rr] : p[0][0][rr])
-                                                             : (tt & 1 ? p[1][1][rr] : p[1][0][rr]);
-                                    const float w = __shfl_sync(0xffffffffu, mine, (lane & ~3) | (tt >> 1));
-                                    if (t0 + t < lim[rr]) {
+                                for (int r = 0; r < R8; ++r)
 #pragma unroll
-                                        for (int k = 0; k < NT; ++k) {
-                                            const uint32_t u = lds32(
-                                                at + B::value(uint32_t(t), uint32_t(k) * 16u + uint32_t(tig) * 4u));
-                                            acc[k][2 * rr] = fmaf(w, bf16_lo(u), acc[k][2 * rr]);
-                                            acc[k][2 * rr + 1] = fmaf(w, bf16_hi(u), acc[k][2 * rr + 1]);
+                                    for (int c = 0; c < 2; ++c) {
+                                        // the token's weight is with lane row t % 8
+                                        const float w = __shfl_sync(0xffffffffu, t < 8 ? p[r][c] : p[r][2 + c],
+                                                                    ((t & 7) << 2) | tig);
+                                        if (t0 + t < lim[r][c]) {
+#pragma unroll
+                                            for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                                for (int u = 0; u < 2; ++u) {  // dims 16 k + 8 u + g
+                                                    const uint32_t x2 = lds32(at + B::value(uint32_t(t), uint32_t(k) * 32u + uint32_t(u) * 16u +
+                                                                                                             uint32_t(g >> 1) * 4u));
+                                                    acc[k][r][2 * u + c] =
+                                                        fmaf(w, g & 1 ? bf16_hi(x2) : bf16_lo(x2), acc[k][r][2 * u + c]);
+                                                }
                                         }
                                     }
-                                }
                                 __syncwarp();
                             }
                         }
@@ -698,23 +737,21 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
                 }
                 uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
-                for (int rr = 0; rr < R8; ++rr)
+                for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) split_bf16x2(p[nt][0][rr], p[nt][1][rr], hi[rr][nt], lo[rr][nt]);
-                const uint32_t t = uint32_t(lane & 15), c2 = uint32_t(lane >> 4);
-                const uint32_t va = at + B::OFF_V + t * B::VROW + ((c2 * 16u) ^ ((t & 7u) << 4));
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t h2, l2;
+                        split_bf16x2(p[t][2 * hf], p[t][2 * hf + 1], h2, l2);
+                        hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
+                    }
 #pragma unroll
-                for (int k = 0; k < NT / 2; ++k) {
+                for (int k = 0; k < MT; ++k) {
                     uint32_t w[4];
-                    ldsm4_t(w, va ^ (32u * uint32_t(k)));
-                    if constexpr (R8 == 1) {
-                        mma_bf16(acc[2 * k], hi[0][0], lo[0][0], hi[0][1], lo[0][1], w[0], w[1]);
-                        mma_bf16(acc[2 * k + 1], hi[0][0], lo[0][0], hi[0][1], lo[0][1], w[2], w[3]);
-                    } else {
-                        mma_bf16(acc[2 * k], hi[0][0], hi[R8 - 1][0], hi[0][1], hi[R8 - 1][1], w[0], w[1]);
-                        mma_bf16(acc[2 * k + 1], hi[0][0], hi[R8 - 1][0], hi[0][1], hi[R8 - 1][1], w[2], w[3]);
-                        mma_bf16(acc[2 * k], lo[0][0], lo[R8 - 1][0], lo[0][1], lo[R8 - 1][1], w[0], w[1]);
-                        mma_bf16(acc[2 * k + 1], lo[0][0], lo[R8 - 1][0], lo[0][1], lo[R8 - 1][1], w[2], w[3]);
+                    ldsm4_t(w, (at + v_off) ^ (32u * uint32_t(k)));
+#pragma unroll
+                    for (int t = 0; t < R8; ++t) {
+                        mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
+                        mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
                     }
                 }
             }
@@ -730,90 +767,80 @@ __global__ void __launch_bounds__(PAT_THREADS, 1) pages_attend(const __grid_cons
             good = __ballot_sync(0xffffffffu, cur != 0);
             nxt = address(n + 33u);
         }
-        ++blk;
-        if (blk < nblk && n + 1 < cnt) continue;
+        ++place;
+        if (place < nplace && n + 1 < cnt) continue;
         // the segment's end
         const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
-        const bool whole = seg0 == 0 && blk == nblk;
-        if constexpr (R8 == 1) {
+        const bool whole = seg0 == 0 && place == nplace;
+        // slot 0: the segment that the run starts with; 1: its last
+        const uint64_t ps = (uint64_t(gw) * 2u + (n + 1 == place - seg0 ? 0u : 1u)) * RTILE;
 #pragma unroll
-            for (int k = 0; k < NT; ++k) acc[k][0] += acc[k][2], acc[k][1] += acc[k][3];
-        }
-        if constexpr (V4) {
+        for (int t = 0; t < R8; ++t)
 #pragma unroll
-            for (int e = 0; e < NG; ++e)
-#pragma unroll
-                for (int rr = 0; rr < R8; ++rr) {
-                    const float z = quad_add(zsum[e][rr]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[4 * e + j][2 * rr] += z, acc[4 * e + j][2 * rr + 1] += z;
-                }
-        }
-#pragma unroll
-        for (int rr = 0; rr < R8; ++rr) {
-            const int r = r0 + 8 * rr + g;
-            const float l = quad_add(sum[rr]);
-            if (r >= a.R) continue;
-            if (whole) {
-                const int i = r / a.G, j = h * a.G + r - i * a.G;
-                const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
-                const float lse = l > 0.0f ? (ref[rr] + log2f(l)) * 0.69314718055994531f
-                                           : (l == 0.0f ? -INFINITY : l);
-                const float2 w = join_base(a, row, lse, tig == 0);
-                const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
-                uint16_t *o = a.out + row * D;
-                const float *bo = a.base_out ? a.base_out + row * D : nullptr;
-                if constexpr (Q8) {
+            for (int c = 0; c < 2; ++c) {
+                const int rr = 8 * t + 2 * tig + c, r = r0 + rr;
+                const float l = rows_add(sum[t][c]);
+                if constexpr (V4) {
 #pragma unroll
                     for (int e = 0; e < NG; ++e) {
-                        float y[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = acc[4 * e + (k & 3)][2 * rr + (k >> 2)] * inv;
-                        if (bo) {
-                            const float4 b0 = *reinterpret_cast<const float4 *>(bo + 32 * e + 8 * tig);
-                            const float4 b1 = *reinterpret_cast<const float4 *>(bo + 32 * e + 8 * tig + 4);
-                            const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) y[k] = w.y != 0.0f ? fmaf(w.y, bb[k], y[k]) : y[k];
-                        }
-                        *reinterpret_cast<uint4 *>(o + 32 * e + 8 * tig) =
-                            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                       pack_bf16x2(y[6], y[7]));
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < NT; ++k) {
-                        float y0 = acc[k][2 * rr] * inv, y1 = acc[k][2 * rr + 1] * inv;
-                        if (bo && w.y != 0.0f) {
-                            const float2 b0 = *reinterpret_cast<const float2 *>(bo + 8 * k + 2 * tig);
-                            y0 = fmaf(w.y, b0.x, y0), y1 = fmaf(w.y, b0.y, y1);
-                        }
-                        *reinterpret_cast<uint32_t *>(o + 8 * k + 2 * tig) = pack_bf16x2(y0, y1);
+                        const float z = rows_add(zsum[e][t][c]);
+                        acc[2 * e][t][c] += z, acc[2 * e][t][2 + c] += z;
+                        acc[2 * e + 1][t][c] += z, acc[2 * e + 1][t][2 + c] += z;
                     }
                 }
-            } else {
-                // slot 0: the segment that the run starts with; 1: its last
-                const uint64_t ps = (uint64_t(gw) * 2u + (n + 1 == blk - seg0 ? 0u : 1u)) * RTILE + uint32_t(8 * rr + g);
-                float *o = a.part + ps * D;
-                if constexpr (Q8) {
+                if (r >= a.R) continue;
+                const float base2 = ref[t][c];
+                if (whole) {
+                    const int i = r / a.G, j = h * a.G + r - i * a.G;
+                    const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+                    const float lse = l > 0.0f ? (base2 + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
+                    const float2 w = join_base(a, row, lse, g == 0);
+                    const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+                    uint16_t *o = a.out + row * D;
+                    const float *bo = a.base_out && w.y != 0.0f ? a.base_out + row * D : nullptr;
+                    if constexpr (Q8) {
 #pragma unroll
-                    for (int e = 0; e < NG; ++e)
+                        for (int e = 0; e < NG; ++e) {
+                            float y[4] = {acc[2 * e][t][c] * inv, acc[2 * e][t][2 + c] * inv, acc[2 * e + 1][t][c] * inv,
+                                          acc[2 * e + 1][t][2 + c] * inv};
+                            if (bo) {
+                                const float4 v = *reinterpret_cast<const float4 *>(bo + 32 * e + 4 * g);
+                                y[0] = fmaf(w.y, v.x, y[0]), y[1] = fmaf(w.y, v.y, y[1]);
+                                y[2] = fmaf(w.y, v.z, y[2]), y[3] = fmaf(w.y, v.w, y[3]);
+                            }
+                            *reinterpret_cast<uint2 *>(o + 32 * e + 4 * g) =
+                                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                        }
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            *reinterpret_cast<float4 *>(o + 32 * e + 8 * tig + 4 * k) =
-                                make_float4(acc[4 * e][2 * rr + k], acc[4 * e + 1][2 * rr + k], acc[4 * e + 2][2 * rr + k],
-                                            acc[4 * e + 3][2 * rr + k]);
+                        for (int k = 0; k < MT; ++k)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int d = 16 * k + 8 * u + g;
+                                float y = acc[k][t][2 * u + c] * inv;
+                                if (bo) y = fmaf(w.y, bo[d], y);
+                                reinterpret_cast<__nv_bfloat16 *>(o)[d] = __float2bfloat16_rn(y);
+                            }
+                    }
                 } else {
+                    float *o = a.part + (ps + uint32_t(rr)) * D;
+                    if constexpr (Q8) {
 #pragma unroll
-                    for (int k = 0; k < NT; ++k)
-                        *reinterpret_cast<float2 *>(o + 8 * k + 2 * tig) = make_float2(acc[k][2 * rr], acc[k][2 * rr + 1]);
+                        for (int e = 0; e < NG; ++e)
+                            *reinterpret_cast<float4 *>(o + 32 * e + 4 * g) =
+                                make_float4(acc[2 * e][t][c], acc[2 * e][t][2 + c], acc[2 * e + 1][t][c], acc[2 * e + 1][t][2 + c]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < MT; ++k)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) o[16 * k + 8 * u + g] = acc[k][t][2 * u + c];
+                    }
+                    if (g == 0) a.stats[ps + uint32_t(rr)] = make_float2(base2, l);
                 }
-                if (tig == 0) a.stats[ps] = make_float2(ref[rr], l);
             }
-        }
         fresh = true;
-        if (blk == nblk) {
-            blk = 0;
+        if (place == nplace) {
+            place = 0;
             if (++tile == HRT) {
                 tile = 0;
                 do ++b;
@@ -912,8 +939,8 @@ static unsigned attend_grid() { return unsigned(sm_count()); }
 static int tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 template <int D, int FMT, int R8>
-static int launch_attend(const PagesAttendArgs &a, cudaStream_t st) {
-    using SM = PatSmem<D, FMT>;
+static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
+    using SM = PatShape<D, FMT, R8>;
     const uint32_t bytes = SM::bytes(a.nseq);
     // the opt-in to more than 48 KB, once per device (to the most that any call needs)
     static bool ready[64] = {false};
@@ -930,7 +957,8 @@ static int launch_attend(const PagesAttendArgs &a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(attend_grid());
-    cfg.blockDim = dim3(PAT_THREADS);
+    cfg.blockDim = dim3(SM::WARPS * 32);
+    a.nwarps = attend_grid() * SM::WARPS;
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -945,7 +973,7 @@ static int launch_attend(const PagesAttendArgs &a, cudaStream_t st) {
 }
 
 template <int D, int FMT>
-static int launch_attend(const PagesAttendArgs &a, int rows, cudaStream_t st) {
+static int launch_attend(PagesAttendArgs &a, int rows, cudaStream_t st) {
     return rows == 8 ? launch_attend<D, FMT, 1>(a, st) : launch_attend<D, FMT, 2>(a, st);
 }
 
@@ -964,7 +992,7 @@ struct AttendWs {
 };
 static AttendWs attend_ws(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {
     const uint64_t rows =
-        uint64_t(attend_grid()) * PAT_WARPS * 2u * uint64_t(tile_rows(n_q_tokens * (n_q_heads / cfg->n_kv_heads)));
+        uint64_t(attend_grid()) * PAT_MOST_WARPS * 2u * uint64_t(tile_rows(n_q_tokens * (n_q_heads / cfg->n_kv_heads)));
     AttendWs w;
     w.stats = align256(4ull * uint64_t(n_seqs + 1));
     w.part = w.stats + align256(rows * 8ull);
@@ -1021,7 +1049,6 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
     const int rows = tile_rows(a.R);
     a.RT = (a.R + rows - 1) / rows;
     a.max_pages = max_pages;
-    a.nwarps = attend_grid() * PAT_WARPS;
     a.polls = g_limit_next ? g_next_polls : PAT_WAIT_LIMIT;
     g_limit_next = false;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -371,7 +371,7 @@ int cachecard_status(const void *card, void *stream);
 /* ---------------------------------------------------------------------- */
 
 /* Most sequences of one kvpages_attend call. */
-#define KVP_PAGES_MAX_SEQS 8192
+#define KVP_PAGES_MAX_SEQS 4096
 
 /* A page container: n_pages pages in each of n_layers layers; a page holds
  * page_tokens tokens (a power of two, 16 to 1024) of all KV heads.  Which
