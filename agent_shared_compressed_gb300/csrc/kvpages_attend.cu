@@ -32,17 +32,20 @@
 //   O^T = V^T P^T  C: dims x queries 2 tig, 2 tig + 1
 // P^T comes from S^T's fragment by two 8 x 8 transposes.  The codes are in
 // fragment order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or
-// of a value token and expands them in registers, keys to fp16 and values to
-// bf16 (exact: |code| <= 128).  What bounds 8- and 4-bit pages beside memory is
-// that expansion, most of it on the integer pipe, which takes a warp's
-// instruction every other cycle: two to four instructions per pair of codes.
+// of a value token and expands them in registers to fp16 (4-bit values: bf16),
+// exactly (|code| <= 128).  What bounds 8- and 4-bit pages beside memory is that
+// expansion, most of it on the integer pipe, which takes a warp's instruction
+// every other cycle: two to three instructions per pair of codes.
 //
 // Key scales apply to the fp32 sums of their 32 dims.  Value scales go into the
-// weights, one product operand per 32 dims; a weight times its scale enters as a
-// sum of two bf16 (2^-17, and fp32's range: a token of large weight and tiny
-// values, an attention sink, takes nothing from the others).  4-bit values
-// q s + z enter as (q - c) s + (z + c s) with c the integer of [0, 15] nearest to
-// -z / s, formed once per token and group: then |z + c s| is at most s / 2 (or of
+// weights, one product operand per 32 dims.  8-bit values: weight times scale in
+// fp16 (2^-12), relative to the running maximum score and to 2^(largest value
+// exponent so far), which leaves 25 binades below the largest before fp16's
+// subnormals round more coarsely: under 2^-36 of the largest value, and nothing
+// when the scales differ less than that.  4-bit and 16-bit values: a sum of two
+// bf16 (2^-17, fp32's range).  4-bit values q s + z enter as
+// (q - c) s + (z + c s) with c the integer of [0, 15] nearest to -z / s, formed
+// once per token and group: then |z + c s| is at most s / 2 (or of
 // the code term's sign, where zero is outside the group's range), and the two
 // sums, of the code terms in the product and of the rest in fp32 once per 32
 // dims, do not cancel.  16-bit pages are multiplied as they are.
@@ -61,7 +64,8 @@ constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
-constexpr float PAT_SLACK = 8.0f;
+constexpr float PAT_SLACK = 4.0f;
+constexpr int PAT_VSHIFT = 11;  // 8-bit values: weights over the reference, in fp16 with the slack
 
 struct PagesAttendArgs {
     PagesView pv;
@@ -164,14 +168,6 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-// The bytes u of each 16-bit half (whatever their upper bytes hold) as bf16
-// u - 128: 128 + (u mod 128), less 256 or, with u's top bit, 128 (exact).
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-    const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, y = (w & 0x00800080u) ^ 0xC380C380u;
-    const __nv_bfloat162 r =
-        __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
 // The low nibble q of each 16-bit half as bf16 q - c: 128 + q, plus the halves of
 // y, -(128 + c) (exact).
 __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t y) {
@@ -265,7 +261,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     using SM = PatShape<D, FMT, R8>;
     constexpr int NG = B::NG, MT = D / 16, RTILE = 8 * R8, WARPS = SM::WARPS, THREADS = WARPS * 32;
     constexpr uint32_t STAGES = SM::STAGES;
-    constexpr bool Q8 = B::Q8, V4 = B::V4;
+    constexpr bool Q8 = B::Q8, V4 = B::V4, V8 = Q8 && !V4;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint32_t *pre = reinterpret_cast<uint32_t *>(sm + SM::OFF_PLAN);
     __shared__ uint32_t wsum[WARPS];
@@ -346,11 +342,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     };
     // the lane's block of the 32 units that start at `first` of the run: its address, or
     // 0 past the run, in a tile's empty places and for a bad page id
-    auto address = [&](uint32_t first) -> uint64_t {
+    auto address = [&](uint32_t first, int &b, uint32_t &tile, uint32_t &at) -> uint64_t {
         const uint32_t u = first + uint32_t(lane);
         if (u >= cnt) return 0;
-        int b;
-        uint32_t tile, at;
         locate(f0 + u, b, tile, at);
         if (at < PAT_ITEM) return 0;
         const uint32_t t0 = (at - PAT_ITEM) * PAGES_BLOCK;
@@ -370,13 +364,17 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
         if (src) bulk_g2s(ring + s * SM::SLOT, reinterpret_cast<const void *>(src), B::BYTES, bar + 8u * s);
     };
 
-    uint64_t cur = address(0), nxt = address(32);
+    int b = 0, len = 0;
+    uint32_t tile = 0, place = 0, nplace = 0, seg0 = 0;
+    uint64_t cur = address(0, b, tile, place), nxt = 0;
     uint32_t good = __ballot_sync(0xffffffffu, cur != 0);
     if (uint32_t(lane) < STAGES && uint32_t(lane) < cnt) issue(cur, uint32_t(lane));
-
-    int b, len = 0;
-    uint32_t tile, place, nplace = 0, seg0 = 0;
-    locate(f0, b, tile, place);
+    b = __shfl_sync(0xffffffffu, b, 0), tile = __shfl_sync(0xffffffffu, tile, 0), place = __shfl_sync(0xffffffffu, place, 0);
+    if (cnt > 32u) {
+        int lb;
+        uint32_t lt, lp;
+        nxt = address(32, lb, lt, lp);
+    }
     bool fresh = true;             // the next unit starts a segment
     uint32_t slot = 0, phase = 0;  // ring position of the next unit
 
@@ -391,6 +389,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c).
     uint32_t qf[D / 16][R8][2];  // query fragments by k-step
     float qs[R8][2];             // factor of the scores (base 2)
+    int vexp = 0;                // V8: biased fp16 exponent of the largest value scale so far
+    float lift = 0.0f;           // weights are 2^(score - ref + lift)
     int lim[R8][2];              // tokens that the query sees
     float ref[R8][2];            // running maximum score, raised lazily
     float sum[R8][2];            // the lane's part of the sum of weights
@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     sum[t][c] = 0.0f;
                 }
             }
+            vexp = 0;
+            lift = V8 ? float(PAT_VSHIFT + 14) : 0.0f;
 #pragma unroll
             for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -583,6 +585,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                 }
             }
             bool raise = false;
+            int ve = 0;
+            if constexpr (V8) {
+                float big = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) big = fmaxf(big, fmaxf(sv[0][k], sv[1][k]));
+                // scales < 2^(ve - 14)
+                ve = max(vexp, int(__reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23) - 112);
+                raise = ve > vexp;
+            }
             float top[R8][2];
 #pragma unroll
             for (int t = 0; t < R8; ++t)
@@ -592,12 +603,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     raise |= top[t][c] > ref[t][c] + PAT_SLACK;
                 }
             if (__any_sync(0xffffffffu, raise)) {
+                const float up = V8 ? float(vexp - ve) : 0.0f;
+                vexp = ve;
+                lift += up;
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
-                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
+                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr + up);
                         ref[t][c] = nr;
                         sum[t][c] *= f;
 #pragma unroll
@@ -613,7 +627,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             for (int t = 0; t < R8; ++t) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float r = ref[t][c] == -INFINITY ? 0.0f : ref[t][c];
+                    const float r = ref[t][c] == -INFINITY ? 0.0f : ref[t][c] - lift;
                     p[t][c] = exp2_fast(x[t][c] - r);
                     p[t][2 + c] = exp2_fast(x[t][2 + c] - r);
                     sum[t][c] += p[t][c] + p[t][2 + c];
@@ -657,19 +671,25 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     for (int t = 0; t < R8; ++t)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t h2, l2;
-                            split_bf16x2(p[t][2 * hf] * sv[hf][e], p[t][2 * hf + 1] * sv[hf][e], h2, l2);
-                            hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
+                            const float w0 = p[t][2 * hf] * sv[hf][e], w1 = p[t][2 * hf + 1] * sv[hf][e];
+                            if constexpr (V4) {
+                                uint32_t h2, l2;
+                                split_bf16x2(w0, w1, h2, l2);
+                                hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
+                            } else {
+                                hi[t][hf] = transpose8(pack_f16x2(w0, w1));
+                            }
                         }
                     uint32_t v[2][4];  // [token half][dim of the granule's word]
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         if constexpr (!V4) {
-                            // byte j of both tokens' words to the halves' low bytes
-                            v[hf][0] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5410u));
-                            v[hf][1] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5511u));
-                            v[hf][2] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x6622u));
-                            v[hf][3] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x7733u));
+                            const uint32_t w0 = __byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5140u);
+                            const uint32_t w1 = __byte_perm(vw[hf][0][e], vw[hf][1][e], 0x7362u);
+                            v[hf][0] = codes_f16(w0, 0x4140u);
+                            v[hf][1] = codes_f16(w0, 0x4342u);
+                            v[hf][2] = codes_f16(w1, 0x4140u);
+                            v[hf][3] = codes_f16(w1, 0x4342u);
                         } else {
                             const uint32_t w = __byte_perm(vw[hf][0][e / 2], vw[hf][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
 #pragma unroll
@@ -680,8 +700,13 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     for (int t = 0; t < R8; ++t)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            mma_bf16(acc[2 * e + u][t], v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1], hi[t][0], hi[t][1]);
-                            mma_bf16(acc[2 * e + u][t], v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1], lo[t][0], lo[t][1]);
+                            const uint32_t a0 = v[0][2 * u], a1 = v[0][2 * u + 1], a2 = v[1][2 * u], a3 = v[1][2 * u + 1];
+                            if constexpr (V4) {
+                                mma_bf16(acc[2 * e + u][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
+                                mma_bf16(acc[2 * e + u][t], a0, a1, a2, a3, lo[t][0], lo[t][1]);
+                            } else {
+                                mma_f16(acc[2 * e + u][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
+                            }
                         }
                     if constexpr (V4) {
 #pragma unroll
@@ -765,7 +790,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
         if ((n & 31u) == 31u) {
             cur = nxt;
             good = __ballot_sync(0xffffffffu, cur != 0);
-            nxt = address(n + 33u);
+            int lb;
+            uint32_t lt, lp;
+            nxt = address(n + 33u, lb, lt, lp);
         }
         ++place;
         if (place < nplace && n + 1 < cnt) continue;
@@ -789,7 +816,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     }
                 }
                 if (r >= a.R) continue;
-                const float base2 = ref[t][c];
+                const float base2 = ref[t][c] - lift;
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
                     const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
@@ -857,16 +884,17 @@ template <int D, int RTILE>
 __global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesAttendArgs a) {
     constexpr int VPL = D / 32;  // values of a lane
     __shared__ float macc[4][D], mst[4][2];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!pages_match(a.pv)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t row = blockIdx.x;
     const int j = int(row % uint32_t(a.nq)), i = int(row / uint32_t(a.nq) % uint32_t(a.m));
     const uint32_t b = uint32_t(row / (uint64_t(a.nq) * uint32_t(a.m)));
     const int h = j / a.G, r = i * a.G + j % a.G, rt = r / RTILE;
     const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
-    const uint32_t before = a.plan[b], n = a.plan[b + 1] - before;
-    const uint64_t per = run_length(uint64_t(a.plan[a.nseq]) * HRT, a.nwarps);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool match = pages_match(a.pv);
+    const uint32_t before = __ldcg(a.plan + b), n = __ldcg(a.plan + b + 1) - before, all = __ldcg(a.plan + a.nseq);
+    if (!match) return;
+    const uint64_t per = run_length(uint64_t(all) * HRT, a.nwarps);
     const uint64_t first = uint64_t(before) * HRT + uint64_t(h * a.RT + rt) * n;
     const uint64_t w0 = first / per, w1 = n ? (first + n - 1) / per : w0;
     if (n && w0 == w1) return;  // one warp had it all
