@@ -28,6 +28,15 @@ namespace kvp {
 
 constexpr int APP_THREADS = 256;
 constexpr int APP_WARPS = APP_THREADS / 32;
+#ifndef APP_OCC
+#define APP_OCC 2
+#endif
+#ifndef APP_OCC64
+#define APP_OCC64 4
+#endif
+#ifndef APP_SPLIT
+#define APP_SPLIT 8
+#endif
 constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
 
 struct AppendArgs {
@@ -38,7 +47,7 @@ struct AppendArgs {
     const uint16_t *q_norm, *k_norm;
     uint16_t *q_out, *k_out, *v_out;
     float eps;
-    int n, nq, rot, rows_per_block;
+    int n, nq, rot;
     uint64_t turn[64];  // w_i / 2 pi mod 1, in units of 2^-64
 };
 
@@ -64,214 +73,280 @@ __device__ __forceinline__ uint32_t half_bits(float x, uint32_t &bad) {
 }
 __device__ __forceinline__ float half_value(uint32_t h) { return __half2float(__ushort_as_half(uint16_t(h))); }
 
-// Codes of a row at 8 bits: s = fp16(max|x| fl(1/127)), code = fl(x / s) rounded
-// to nearest (ties to even).  x * fl(1/s) is within 2^-16 of the quotient, so
-// only a product that near a half-integer is divided out.  x becomes the values
+// 1 / s for an fp16 scale s (0 for 0), within 2^-22.
+__device__ __forceinline__ float rcp_scale(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s > 0.0f ? r : 0.0f;
+}
+
+// (t + e) / s rounded to nearest even, for a quotient within 2^-10 of the
+// half-integer next to y: the sign of (t + e) - (k + 1/2) s decides, and
+// (k + 1/2) s has at most 19 bits, t is within a factor of two of it, so both
+// differences are exact.
+__device__ __forceinline__ float at_border(float t, float e, float s, float y) {
+    const float k = floorf(y), d = (t - (k + 0.5f) * s) + e;
+    return d > 0.0f ? k + 1.0f : (d < 0.0f ? k : rintf(k + 0.5f));
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float most2(float m, float2 a) { return fmaxf(m, fmaxf(fabsf(a.x), fabsf(a.y))); }
+
+// A row's elements that are Inf or NaN set to zero; whether there were any.
+template <int NB>
+__device__ __forceinline__ bool drop_nonfinite(float2 (&x)[NB][4]) {
+    float2 odd = both(0.0f);  // NaN once an element is Inf or NaN
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd = fma2(x[b][j], both(0.0f), odd);
+    if (odd.x + odd.y == 0.0f) return false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[b][j] = make_float2(finite(x[b][j].x) ? x[b][j].x : 0.0f, finite(x[b][j].y) ? x[b][j].y : 0.0f);
+    return true;
+}
+
+// The 8-bit code of x where x / s is near a border or the codes can pass 127.
+__device__ __forceinline__ float code8_exact(float x, float s, float rs) {
+    const float y = x * rs;
+    const float q = fabsf(y - rintf(y)) > 0.5f - 0x1p-14f ? at_border(x, 0.0f, s, y) : rintf(y);
+    return fminf(fmaxf(q, -127.0f), 127.0f);
+}
+// The 4-bit code of x near a border: x - z = t + e exactly (two-sum).
+__device__ __forceinline__ float code4_exact(float x, float z, float s, float rs) {
+    const float t = x - z, xx = t + z, e = (x - xx) + ((xx - t) - z);
+    const float y = fminf(fmaxf(t * rs, 0.0f), 15.0f);
+    return fabsf(y - rintf(y)) > 0.5f - 0x1p-14f ? at_border(t, e, s, y) : rintf(y);
+}
+
+// Codes of a row at 8 bits: s = fp16(max|x| fl(1/127)), code = x / s rounded to
+// nearest (ties to even).  x * rcp(s) is within 2^-14 of the quotient, so only
+// a product that near a half-integer is decided exactly.  x becomes the values
 // held.
 template <int D>
-__device__ __forceinline__ void encode8(float (&x)[D / 32][8], Lane8<D> &c, uint32_t (&sb)[D / 32], uint32_t &bad) {
+__device__ __forceinline__ void encode8(float2 (&x)[D / 32][4], Lane8<D> &c, uint32_t (&sb)[D / 32], uint32_t &bad) {
+    constexpr int NB = D / 32;
     constexpr float MAGIC = 12582912.0f + 128.0f;  // 1.5 * 2^23 + the codes' bias
+    if (drop_nonfinite<NB>(x)) bad |= FLAG_NONFINITE;
+    float m[NB];
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-        float m = 0.0f;
-        bool fin = true;
+    for (int b = 0; b < NB; ++b) {
+        m[b] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            fin &= finite(x[b][j]);
-            m = fmaxf(m, fabsf(x[b][j]));
+        for (int j = 0; j < 4; ++j) m[b] = most2(m[b], x[b][j]);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) m[b] = quad_max(m[b]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        sb[b] = half_bits(m[b] * (1.0f / 127.0f), bad);
+        const float s = half_value(sb[b]), rs = rcp_scale(s);
+        float2 r[4];
+        float near = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = fma2(x[b][j], both(rs), both(MAGIC));
+            const float2 whole = add2(r[j], both(-MAGIC));
+            near = most2(near, fma2(x[b][j], both(rs), make_float2(-whole.x, -whole.y)));
         }
-        if (!fin) {  // Inf and NaN count as zeros, and are reported
-            bad |= FLAG_NONFINITE;
-            m = 0.0f;
+        if (near > 0.5f - 0x1p-14f || s < 0x1p-14f || m[b] > 8320000.0f) {
+            // near a border; or the scale is an fp16 subnormal or saturated, where codes can pass 127
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[b][j] = finite(x[b][j]) ? x[b][j] : 0.0f;
-                m = fmaxf(m, fabsf(x[b][j]));
-            }
-        }
-        m = quad_max(m);
-        sb[b] = half_bits(m * (1.0f / 127.0f), bad);
-        const float s = half_value(sb[b]), rs = s > 0.0f ? 1.0f / s : 0.0f;
-        float r[8], near = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r[j] = fmaf(x[b][j], rs, MAGIC);
-            near = fmaxf(near, fabsf(fmaf(x[b][j], rs, MAGIC - r[j])));
-        }
-        if (near > 0.5f - 0x1p-15f || s < 0x1p-14f || m > 8320000.0f) {
-            // near a tie; or the scale is an fp16 subnormal or saturated, where codes can pass 127
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[j] = (s > 0.0f ? fminf(fmaxf(rintf(x[b][j] / s), -127.0f), 127.0f) : 0.0f) + MAGIC;
+            for (int j = 0; j < 4; ++j)
+                r[j] = make_float2(code8_exact(x[b][j].x, s, rs) + MAGIC, code8_exact(x[b][j].y, s, rs) + MAGIC);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const uint32_t lo = __byte_perm(__float_as_uint(r[4 * e]), __float_as_uint(r[4 * e + 1]), 0x0040u);
-            const uint32_t hi = __byte_perm(__float_as_uint(r[4 * e + 2]), __float_as_uint(r[4 * e + 3]), 0x0040u);
+            const uint32_t lo = __byte_perm(__float_as_uint(r[2 * e].x), __float_as_uint(r[2 * e].y), 0x0040u);
+            const uint32_t hi = __byte_perm(__float_as_uint(r[2 * e + 1].x), __float_as_uint(r[2 * e + 1].y), 0x0040u);
             c.w[b][e] = __byte_perm(lo, hi, 0x5410u);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[b][j] = (r[j] - MAGIC) * s;
+        for (int j = 0; j < 4; ++j) x[b][j] = mul2(add2(r[j], both(-MAGIC)), both(s));
     }
 }
 
 // Codes of a value row at 4 bits: s = fp16(fl(max - min) fl(1/15)), z =
-// fp16(min), code = (x - z) / s rounded to nearest even, in [0, 15].  Decided
-// in fp32 unless within 2^-16 of a half-integer (fp32 errs by under 2^-18),
-// then in fp64, where x - z of two 16-bit values is exact.  x becomes the values
-// held.
+// fp16(min), code = (x - z) / s rounded to nearest even, in [0, 15], decided as
+// above with x - z carried exactly.  x becomes the values held.
 template <int D>
-__device__ __forceinline__ void encode4(float (&x)[D / 32][8], Lane4<D> &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
+__device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane4<D> &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
+    constexpr int NB = D / 32;
     constexpr float MAGIC = 12582912.0f;
+    if (drop_nonfinite<NB>(x)) bad |= FLAG_NONFINITE;
+    float hi[NB], lo[NB];
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-        bool fin = true;
+    for (int b = 0; b < NB; ++b) {
+        hi[b] = fmaxf(x[b][0].x, x[b][0].y), lo[b] = fminf(x[b][0].x, x[b][0].y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fin &= finite(x[b][j]);
-        if (!fin) {
-            bad |= FLAG_NONFINITE;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[b][j] = finite(x[b][j]) ? x[b][j] : 0.0f;
+        for (int j = 1; j < 4; ++j) {
+            hi[b] = fmaxf(hi[b], fmaxf(x[b][j].x, x[b][j].y));
+            lo[b] = fminf(lo[b], fminf(x[b][j].x, x[b][j].y));
         }
-        float hi = x[b][0], nlo = -x[b][0];
+    }
 #pragma unroll
-        for (int j = 1; j < 8; ++j) hi = fmaxf(hi, x[b][j]), nlo = fmaxf(nlo, -x[b][j]);
-        hi = quad_max(hi);
-        const float lo = -quad_max(nlo);
-        const uint32_t sh = half_bits((hi - lo) * (1.0f / 15.0f), bad), zh = half_bits(lo, bad);
+    for (int b = 0; b < NB; ++b) hi[b] = quad_max(hi[b]), lo[b] = -quad_max(-lo[b]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t sh = half_bits((hi[b] - lo[b]) * (1.0f / 15.0f), bad), zh = half_bits(lo[b], bad);
         szb[b] = sh | zh << 16;
-        const float s = half_value(sh), z = half_value(zh), rs = s > 0.0f ? 1.0f / s : 0.0f;
-        float r[8], near = 0.0f;
+        const float s = half_value(sh), z = half_value(zh), rs = rcp_scale(s);
+        float2 r[4];
+        float near = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float y = fminf(fmaxf((x[b][j] - z) * rs, 0.0f), 15.0f);
-            r[j] = y + MAGIC;
-            near = fmaxf(near, fabsf(y - (r[j] - MAGIC)));
+        for (int j = 0; j < 4; ++j) {
+            float2 y = mul2(add2(x[b][j], both(-z)), both(rs));
+            y = make_float2(fminf(fmaxf(y.x, 0.0f), 15.0f), fminf(fmaxf(y.y, 0.0f), 15.0f));
+            r[j] = add2(y, both(MAGIC));
+            const float2 whole = add2(r[j], both(-MAGIC));
+            near = most2(near, add2(y, make_float2(-whole.x, -whole.y)));
         }
-        if (near > 0.5f - 0x1p-16f) {
+        if (near > 0.5f - 0x1p-14f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[j] = s > 0.0f ? float(fmin(fmax(rint((double(x[b][j]) - double(z)) / double(s)), 0.0), 15.0)) + MAGIC
-                                : MAGIC;
+            for (int j = 0; j < 4; ++j)
+                r[j] = make_float2(code4_exact(x[b][j].x, z, s, rs) + MAGIC, code4_exact(x[b][j].y, z, s, rs) + MAGIC);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            uint32_t h = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h |= (__float_as_uint(r[4 * e + j]) & 15u) << (4 * j);
-            c.h[b][e] = h;
+            // the low bits of 2^23 1.5 + code are the code: place four nibbles by sums of shifts
+            const uint32_t lo2 = (__float_as_uint(r[2 * e].x) & 15u) | (__float_as_uint(r[2 * e].y) & 15u) << 4;
+            const uint32_t hi2 = (__float_as_uint(r[2 * e + 1].x) & 15u) | (__float_as_uint(r[2 * e + 1].y) & 15u) << 4;
+            c.h[b][e] = lo2 | hi2 << 8;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[b][j] = fmaf(r[j] - MAGIC, s, z);
+        for (int j = 0; j < 4; ++j) x[b][j] = fma2(add2(r[j], both(-MAGIC)), both(s), both(z));
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                      pack_bf16x2(x[3].x, x[3].y));
 }
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
+    x[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x)), x[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    x[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z)), x[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
 }
 
-// Eight pairs turned by their (cos, sin).
-__device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const float2 *cs) {
+// Eight pairs turned by their cosines and sines.
+__device__ __forceinline__ void turn(float2 (&lo)[4], float2 (&hi)[4], const float *cosines, const float *sines) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 t = cs[j];
-        const float l = lo[j], h = hi[j];
-        lo[j] = l * t.x - h * t.y;
-        hi[j] = h * t.x + l * t.y;
+    for (int j = 0; j < 4; j += 2) {
+        const float4 c = *reinterpret_cast<const float4 *>(cosines + 2 * j);
+        const float4 s = *reinterpret_cast<const float4 *>(sines + 2 * j);
+        const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+        const float2 ss[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 l = lo[j + k], h = hi[j + k];
+            lo[j + k] = fma2(l, cc[k], mul2(h, make_float2(-ss[k].x, -ss[k].y)));
+            hi[j + k] = fma2(h, cc[k], mul2(l, ss[k]));
+        }
     }
 }
 
 // The lane's share of a contiguous bf16 row.
 template <int D>
-__device__ __forceinline__ void store_row(uint16_t *row, int tig, const float (&x)[D / 32][8]) {
+__device__ __forceinline__ void store_row(uint16_t *row, int tig, const float2 (&x)[D / 32][4]) {
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) *reinterpret_cast<uint4 *>(row + 32 * b + 8 * tig) = pack8(x[b]);
 }
 
-// One block: APP_TOKENS tokens, rows [blockIdx.y * rows_per_block, ...) of the
-// nq query, H key and H value rows of each, a warp at a time.
+// One block: APP_TOKENS tokens and a share of the nq query, H key and H value
+// rows of each, a warp at a time.  A row's loads are
+// issued while the row before it is worked on: the kernel is bound by memory
+// latency, then by memory.
 template <int D, int FMT>
-__global__ void __launch_bounds__(APP_THREADS) pages_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(APP_THREADS, D == 128 ? APP_OCC : APP_OCC64) pages_append(const __grid_constant__ AppendArgs a) {
     using B = Block<D, FMT>;
     constexpr int NB = D / 32;
-    __shared__ float2 cs[APP_TOKENS][D / 2 + 2];
+    // rows padded to start on other banks; read as float4
+    __shared__ __align__(16) float cosines[APP_TOKENS][D / 2 + 4], sines[APP_TOKENS][D / 2 + 4], norm[2][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
     const int64_t t0 = int64_t(blockIdx.x) * APP_TOKENS;
     const int64_t tok = t0 + tq;
     const bool real = tok < a.n;
-    if (!pages_match(a.pv)) {
-        if (threadIdx.x == 0) pages_flag(a.pv, FLAG_HEADER);
-        return;
-    }
+    const int H = a.pv.H, r1 = a.nq + 2 * H;
+    // the blocks of a token group take every gridDim.y-th row: an equal mix of kinds
+    const int step = int(gridDim.y) * APP_WARPS;
+    int r = int(blockIdx.y) + int(gridDim.y) * warp;
+    auto load = [&](int row, uint4 (&v)[NB]) {
+        const bool is_q = row < a.nq, is_v = row >= a.nq + H;
+        const uint16_t *src = is_q ? a.q + tok * a.q_ts + row * a.q_hs
+                                   : (is_v ? a.v + tok * a.v_ts + (row - a.nq - H) * a.v_hs
+                                           : a.k + tok * a.k_ts + (row - a.nq) * a.k_hs);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            v[b] = real && row < r1 ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 in[NB];
+    load(r, in);
+    const int64_t slot = real ? a.slots[tok] : -1;
+    const bool match = pages_match(a.pv);
     if (a.rot > 0) {
         for (int i = threadIdx.x; i < APP_TOKENS * (a.rot / 2); i += APP_THREADS) {
             const int t = i / (a.rot / 2), p = i % (a.rot / 2);
+            float s = 0.0f, c = 1.0f;
             if (t0 + t < a.n) {
                 const int64_t turns = int64_t(uint64_t(a.positions[t0 + t]) * a.turn[p]);  // mod one turn
-                float s, c;
                 sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
-                cs[t][p] = make_float2(c, s);
-            } else {
-                cs[t][p] = make_float2(1.0f, 0.0f);
             }
+            cosines[t][p] = c, sines[t][p] = s;
         }
+    }
+    for (int i = threadIdx.x; i < 2 * D; i += APP_THREADS) {
+        const uint16_t *w = i < D ? a.q_norm : a.k_norm;
+        norm[i / D][i % D] = w ? __uint_as_float(uint32_t(w[i % D]) << 16) : 1.0f;
     }
     __syncthreads();
     uint8_t *blk = nullptr;  // the token's block of head 0
-    uint32_t row16 = 0, bad = 0;
-    if (real) {
-        const int64_t slot = a.slots[tok];
-        if (slot >= (int64_t(a.pv.n_pages) << a.pv.logP)) {
-            bad |= FLAG_PAGE;
-        } else if (slot >= 0) {
-            const int64_t page = slot >> a.pv.logP;
-            const uint32_t in = uint32_t(slot) & uint32_t(a.pv.P - 1);
-            blk = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(in / PAGES_BLOCK) * B::BYTES;
-            row16 = in % PAGES_BLOCK;
-        }
+    uint32_t row16 = 0, bad = match ? 0u : FLAG_HEADER;
+    if (slot >= (int64_t(a.pv.n_pages) << a.pv.logP)) {
+        bad |= FLAG_PAGE;
+    } else if (match && slot >= 0) {
+        const int64_t page = slot >> a.pv.logP;
+        const uint32_t at = uint32_t(slot) & uint32_t(a.pv.P - 1);
+        blk = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(at / PAGES_BLOCK) * B::BYTES;
+        row16 = at % PAGES_BLOCK;
     }
-    const int H = a.pv.H, rows = a.nq + 2 * H;
-    const int r1 = min(rows, int(blockIdx.y + 1) * a.rows_per_block);
-    for (int r = int(blockIdx.y) * a.rows_per_block + warp; r < r1; r += APP_WARPS) {
+    for (; r < r1; r += step) {
         const bool is_q = r < a.nq, is_v = r >= a.nq + H;
         const int h = is_q ? r : (is_v ? r - a.nq - H : r - a.nq);
-        const uint16_t *src = is_q ? a.q + tok * a.q_ts + h * a.q_hs
-                                   : (is_v ? a.v + tok * a.v_ts + h * a.v_hs : a.k + tok * a.k_ts + h * a.k_hs);
-        float x[NB][8];
+        float2 x[NB][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-            unpack8(real ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0), x[b]);
+        for (int b = 0; b < NB; ++b) unpack8(in[b], x[b]);
+        load(r + step, in);
         uint8_t *hb = blk ? blk + uint64_t(h) * a.pv.tile_bytes : nullptr;
         if (!is_v) {
-            const uint16_t *w = is_q ? a.q_norm : a.k_norm;
-            if (w) {
-                float ss = 0.0f;
+            if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
+                float2 ss = both(0.0f);
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(x[b][j], x[b][j], ss);
-                const float inv = 1.0f / sqrtf(quad_sum(ss) * (1.0f / D) + a.eps);
+                    for (int j = 0; j < 4; ++j) ss = fma2(x[b][j], x[b][j], ss);
+                const float inv = rsqrtf(quad_sum(ss.x + ss.y) * (1.0f / D) + a.eps);
+                const float *w = norm[is_q ? 0 : 1] + 8 * tig;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float wf[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(w + 32 * b + 8 * tig)), wf);
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[b][j] = x[b][j] * inv * wf[j];
-                }
+                    for (int j = 0; j < 4; j += 2) {
+                        const float4 v = *reinterpret_cast<const float4 *>(w + 32 * b + 2 * j);
+                        x[b][j] = mul2(mul2(x[b][j], both(inv)), make_float2(v.x, v.y));
+                        x[b][j + 1] = mul2(mul2(x[b][j + 1], both(inv)), make_float2(v.z, v.w));
+                    }
             }
             if (a.rot > 0) {
-                const float2 *t = cs[tq] + 8 * tig;
+                const float *c = cosines[tq] + 8 * tig, *s = sines[tq] + 8 * tig;
                 if (NB == 4 && a.rot == 128) {
-                    turn(x[0], x[NB - 2], t);
-                    turn(x[1], x[NB - 1], t + 32);
+                    turn(x[0], x[NB - 2], c, s);
+                    turn(x[1], x[NB - 1], c + 32, s + 32);
                 } else {
-                    turn(x[0], x[1], t);
+                    turn(x[0], x[1], c, s);
                 }
             }
             if (is_q) {
@@ -399,7 +474,9 @@ __global__ void __launch_bounds__(256) pages_read(const __grid_constant__ ReadAr
                 }
                 uint16_t *row = (kv == 0 ? a.k : a.v) + out + uint64_t(t) * D;
 #pragma unroll
-                for (int g = 0; g < NB; ++g) st_stream_v4(row + 32 * g + 8 * tig, pack8(x[g]));
+                for (int g = 0; g < NB; ++g)
+                    st_stream_v4(row + 32 * g + 8 * tig, make_uint4(pack_bf16x2(x[g][0], x[g][1]), pack_bf16x2(x[g][2], x[g][3]),
+                                                                    pack_bf16x2(x[g][4], x[g][5]), pack_bf16x2(x[g][6], x[g][7])));
             }
         }
     }
@@ -518,14 +595,13 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
     a.k_out = static_cast<uint16_t *>(k_out), a.v_out = static_cast<uint16_t *>(v_out);
     a.eps = eps, a.n = n_tokens, a.nq = n_q_heads, a.rot = rot_dim;
     for (int i = 0; i < 64; ++i) a.turn[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
-    // Rows of a block: all of a token group's where the groups alone fill the
-    // GPU (the angles are formed once), else as few as one row per warp.
+    // Blocks of a token group: one where the groups alone fill the GPU (the
+    // angles are formed once a block), else up to one row per warp.
     const int rows = n_q_heads + 2 * cfg->n_kv_heads;
     const int groups = int((int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS);
     const int steps = (rows + APP_WARPS - 1) / APP_WARPS;
-    const int split = std::max(1, std::min(steps, 4 * sm_count() / std::max(groups, 1)));
-    a.rows_per_block = (steps + split - 1) / split * APP_WARPS;
-    const dim3 grid(unsigned(groups), unsigned((rows + a.rows_per_block - 1) / a.rows_per_block));
+    const int split = std::max(1, std::min(steps, APP_SPLIT * sm_count() / std::max(groups, 1)));
+    const dim3 grid{unsigned(groups), unsigned(split)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool d128 = cfg->head_dim == 128;
     switch (cfg->format) {
