@@ -58,12 +58,30 @@
 namespace kvp {
 
 constexpr int PAT_MOST_WARPS = 16;             // of a block
-constexpr uint32_t PAT_ITEM = 2;               // units that a row tile counts beside its blocks
-constexpr uint32_t PAT_MIN_RUN = 3;            // units of a warp's run, at least
+#ifndef PAT_ITEM_N
+#define PAT_ITEM_N 4
+#endif
+#ifndef PAT_RUN_N
+#define PAT_RUN_N 3
+#endif
+constexpr uint32_t PAT_ITEM = PAT_ITEM_N;               // units that a row tile counts beside its blocks
+constexpr uint32_t PAT_MIN_RUN = PAT_RUN_N;            // units of a warp's run, at least
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
+#ifndef PAT_W1
+#define PAT_W1 16
+#endif
+#ifndef PAT_W2
+#define PAT_W2 8
+#endif
+#ifndef PAT_W64
+#define PAT_W64 16
+#endif
+#ifndef PAT_MANY
+#define PAT_MANY 64
+#endif
 constexpr float PAT_SLACK = 4.0f;
 constexpr int PAT_VSHIFT = 11;  // 8-bit values: weights over the reference, in fp16 with the slack
 
@@ -222,7 +240,7 @@ __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) 
 // Warps of a block: as many as the registers of a tile's state allow.
 template <int D, int FMT, int R8>
 struct PatShape {
-    static constexpr int WARPS = FMT == KVP_PAGES_BF16 && D == 128 ? 8 : (R8 == 2 && D == 128 ? 8 : 16);
+    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (R8 == 2 ? PAT_W2 : PAT_W1)) : (R8 == 2 ? PAT_W64 : 16);
     static constexpr uint32_t SLOT = (Block<D, FMT>::BYTES + 127u) / 128u * 128u;
     static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
     static constexpr uint32_t STAGES = RING < 3u ? 3u : (RING > 8u ? 8u : RING);
@@ -397,30 +415,49 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     float acc[MT][R8][4];
     float zsum[V4 ? NG : 1][R8][2];
 
+    // The queries of (b, tile): raw bf16 (Q8), or fragments as they are.
+    uint4 qraw[Q8 ? NG : 1][R8];
+    auto load_queries = [&](int sb, uint32_t st) {
+        const int h = int(st) / a.RT, r0 = int(st) % a.RT * RTILE;
+#pragma unroll
+        for (int t = 0; t < R8; ++t) {
+            const int r = r0 + 8 * t + g;
+            const bool real = r < a.R;
+            const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
+            const uint16_t *qrow = a.q + ((uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
+            if constexpr (Q8) {
+#pragma unroll
+                for (int k = 0; k < NG; ++k)
+                    qraw[k][t] = real ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * k + 8 * tig)) : make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        qf[k][t][e] = real ? __ldg(reinterpret_cast<const uint32_t *>(qrow + 16 * k + 8 * e + 2 * tig)) : 0u;
+            }
+        }
+    };
+    if (cnt) load_queries(b, tile);
+
     for (uint32_t n = 0; n < cnt; ++n) {
         if (fresh) {
             fresh = false;
             seg0 = place;
             nplace = pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
-            const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
+            const int r0 = int(tile) % a.RT * RTILE;
 #pragma unroll
             for (int t = 0; t < R8; ++t) {
-                const int r = r0 + 8 * t + g;
-                const bool real = r < a.R;
-                const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
-                const uint16_t *qrow = a.q + ((uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
                 int up = 0;
                 if constexpr (Q8) {
                     // rows enter as fp16 times a power of two that brings their
                     // largest element to [2^14, 2^15): exact but for elements
                     // under 2^-28 of it
-                    uint4 v[NG];
                     float top = 0.0f;
 #pragma unroll
                     for (int k = 0; k < NG; ++k) {
-                        v[k] = real ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * k + 8 * tig)) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        const uint32_t w[4] = {qraw[k][t].x, qraw[k][t].y, qraw[k][t].z, qraw[k][t].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
                     }
@@ -431,18 +468,11 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     const float f = __uint_as_float(uint32_t(127 + up) << 23);
 #pragma unroll
                     for (int k = 0; k < NG; ++k) {
-                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        const uint32_t w[4] = {qraw[k][t].x, qraw[k][t].y, qraw[k][t].z, qraw[k][t].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             qf[2 * k + (e >> 1)][t][e & 1] = pack_f16x2(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            qf[k][t][e] =
-                                real ? __ldg(reinterpret_cast<const uint32_t *>(qrow + 16 * k + 8 * e + 2 * tig)) : 0u;
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -796,7 +826,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
         }
         ++place;
         if (place < nplace && n + 1 < cnt) continue;
-        // the segment's end
+        // the segment's end; the next one's queries are requested first
+        int nb = b;
+        uint32_t ntile = tile;
+        if (place == nplace && ++ntile == HRT) {
+            ntile = 0;
+            do ++nb;
+            while (nb < a.nseq && pre[nb + 1] == pre[nb]);
+        }
+        if (n + 1 < cnt) load_queries(nb, ntile);
         const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
         const bool whole = seg0 == 0 && place == nplace;
         // slot 0: the segment that the run starts with; 1: its last
@@ -866,24 +904,18 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                 }
             }
         fresh = true;
-        if (place == nplace) {
-            place = 0;
-            if (++tile == HRT) {
-                tile = 0;
-                do ++b;
-                while (b < a.nseq && pre[b + 1] == pre[b]);
-            }
-        }
+        if (place == nplace) place = 0;
+        b = nb, tile = ntile;
     }
 }
 
 // Merges the partial results of the rows whose blocks several warps had, and
-// writes the rows of empty sequences.  One block per query row; its four warps
-// take every fourth partial.
-template <int D, int RTILE>
-__global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesAttendArgs a) {
+// writes the rows of empty sequences.  One block per query row; its WARPS warps
+// take every WARPS-th partial.
+template <int D, int RTILE, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__ PagesAttendArgs a) {
     constexpr int VPL = D / 32;  // values of a lane
-    __shared__ float macc[4][D], mst[4][2];
+    __shared__ float macc[WARPS][D], mst[WARPS][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t row = blockIdx.x;
     const int j = int(row % uint32_t(a.nq)), i = int(row / uint32_t(a.nq) % uint32_t(a.m));
@@ -902,8 +934,8 @@ __global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesA
 #pragma unroll
     for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
     const uint32_t parts = n ? uint32_t(w1 - w0 + 1) : 0u;
-    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += 128u) {  // 32 partials of this warp at a time
-        const uint32_t c = c0 + 4u * uint32_t(lane);
+    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += 32u * WARPS) {  // 32 partials of this warp at a time
+        const uint32_t c = c0 + WARPS * uint32_t(lane);
         float2 st = make_float2(-INFINITY, 0.0f);
         uint64_t ps = 0;
         if (c < parts) {
@@ -923,7 +955,7 @@ __global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesA
         M = nm;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) acc[k] *= f0;
-        const int here = int(min(32u, (parts - c0 + 3u) / 4u));
+        const int here = int(min(32u, (parts - c0 + WARPS - 1u) / WARPS));
 #pragma unroll 4
         for (int k = 0; k < here; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, k);
@@ -946,9 +978,9 @@ __global__ void __launch_bounds__(128) pages_join(const __grid_constant__ PagesA
     if (threadIdx.x >= D) return;
     float top = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, mst[k][0]);
+    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, mst[k][0]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < WARPS; ++k) {
         const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
         l = fmaf(f, mst[k][1], l);
         o = fmaf(f, macc[k][threadIdx.x], o);
@@ -993,9 +1025,12 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, R8>, a) != cudaSuccess) return KVP_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
-    cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, pages_join<D, 8 * R8>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    // warps for a row's partials: a row has about nwarps / (row tiles) of them
+    const bool many = a.nwarps / (unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT)) >= PAT_MANY;
+    cfg.blockDim = dim3(many ? 512 : 128);
+    if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, 8 * R8, 16> : pages_join<D, 8 * R8, 4>, a) != cudaSuccess)
+        return KVP_ERR_CUDA;
     count_launch(2);
     return launch_status();
 }
