@@ -66,12 +66,13 @@ constexpr int PAT_MOST_WARPS = 16;             // of a block
 #endif
 constexpr uint32_t PAT_ITEM = PAT_ITEM_N;               // units that a row tile counts beside its blocks
 constexpr uint32_t PAT_MIN_RUN = PAT_RUN_N;            // units of a warp's run, at least
+constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
 #ifndef PAT_W1
-#define PAT_W1 16
+#define PAT_W1 8
 #endif
 #ifndef PAT_W2
 #define PAT_W2 8
@@ -293,9 +294,29 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     // the kernel before this one has completed past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool match = pages_match(a.pv);
-    // units before each sequence (of one row tile)
+    // units before each sequence (of one row tile); up to 32 sequences, every warp
+    // finds them by itself (all write the same values)
     uint32_t carry = 0;
-    for (int b0 = 0; b0 < a.nseq; b0 += THREADS) {
+    if (a.nseq <= 32) {
+        uint32_t n = lane < a.nseq ? uint32_t((seq_len(a, lane, blockIdx.x == 0 && warp == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
+        n += n ? PAT_ITEM : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += y;
+        }
+        carry = __shfl_sync(0xffffffffu, n, 31);
+        if (lane < a.nseq) {
+            pre[lane + 1] = n;
+            if (blockIdx.x == 0 && warp == 0) a.plan[lane + 1] = n;
+        }
+        if (lane == 0) {
+            pre[0] = 0u;
+            if (blockIdx.x == 0 && warp == 0) a.plan[0] = 0u;
+        }
+        __syncwarp();
+    }
+    for (int b0 = 0; a.nseq > 32 && b0 < a.nseq; b0 += THREADS) {
         const int b = b0 + tid;
         uint32_t n = b < a.nseq ? uint32_t((seq_len(a, b, blockIdx.x == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
         n += n ? PAT_ITEM : 0u;
@@ -319,11 +340,13 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        pre[0] = 0u;
-        if (blockIdx.x == 0) a.plan[0] = 0u;
+    if (a.nseq > 32) {
+        if (tid == 0) {
+            pre[0] = 0u;
+            if (blockIdx.x == 0) a.plan[0] = 0u;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!match) {
         if (tid == 0) pages_flag(a.pv, FLAG_HEADER);
@@ -911,10 +934,14 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
 
 // Merges the partial results of the rows whose blocks several warps had, and
 // writes the rows of empty sequences.  One block per query row; its WARPS warps
-// take every WARPS-th partial.
+// take every WARPS-th partial, eight of them in flight at a time.  A block finds
+// out what it has to merge before pages_attend has ended (up to PAT_OWN_PLAN
+// sequences; beyond, from the plan that pages_attend leaves), and all but block 0
+// leave at once if that is nothing: block 0 stays for pages_attend's end, so that
+// this grid's end means the other's.
 template <int D, int RTILE, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__ PagesAttendArgs a) {
-    constexpr int VPL = D / 32;  // values of a lane
+    constexpr int VPL = D / 32, DEEP = 8;  // values of a lane
     __shared__ float macc[WARPS][D], mst[WARPS][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t row = blockIdx.x;
@@ -922,53 +949,73 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     const uint32_t b = uint32_t(row / (uint64_t(a.nq) * uint32_t(a.m)));
     const int h = j / a.G, r = i * a.G + j % a.G, rt = r / RTILE;
     const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const bool match = pages_match(a.pv);
-    const uint32_t before = __ldcg(a.plan + b), n = __ldcg(a.plan + b + 1) - before, all = __ldcg(a.plan + a.nseq);
-    if (!match) return;
+    // the next attention's blocks may be placed; they wait for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    uint32_t before = 0, n = 0, all = 0;
+    if (a.nseq <= PAT_OWN_PLAN) {
+        // pages_attend has passed its own wait, so the lengths are final
+        for (int k = lane; k < a.nseq; k += 32) {
+            uint32_t u = uint32_t((seq_len(a, k, false) + PAGES_BLOCK - 1) / PAGES_BLOCK);
+            u += u ? PAT_ITEM : 0u;
+            all += u;
+            before += k < int(b) ? u : 0u;
+            n += k == int(b) ? u : 0u;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        before = __reduce_add_sync(0xffffffffu, before);
+        n = __reduce_add_sync(0xffffffffu, n);
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        before = __ldcg(a.plan + b), n = __ldcg(a.plan + b + 1) - before, all = __ldcg(a.plan + a.nseq);
+    }
     const uint64_t per = run_length(uint64_t(all) * HRT, a.nwarps);
     const uint64_t first = uint64_t(before) * HRT + uint64_t(h * a.RT + rt) * n;
     const uint64_t w0 = first / per, w1 = n ? (first + n - 1) / per : w0;
-    if (n && w0 == w1) return;  // one warp had it all
+    const bool whole = n && w0 == w1;  // one warp had it all
+    if (whole && row) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (whole || !pages_match(a.pv)) return;
+    const uint32_t parts = n ? uint32_t(w1 - w0 + 1) : 0u;
     float acc[VPL], M = -INFINITY, L = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
-    const uint32_t parts = n ? uint32_t(w1 - w0 + 1) : 0u;
-    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += 32u * WARPS) {  // 32 partials of this warp at a time
-        const uint32_t c = c0 + WARPS * uint32_t(lane);
-        float2 st = make_float2(-INFINITY, 0.0f);
-        uint64_t ps = 0;
-        if (c < parts) {
-            const uint64_t w = w0 + c;
-            ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
-            st = a.stats[ps];
-        }
-        float top = st.x;
+    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += DEEP * WARPS) {
+        float2 st[DEEP];
+        float v[DEEP][VPL];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float nm = fmaxf(M, top), f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
-        const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - nm);
-        float l = f * st.y;
+        for (int k = 0; k < DEEP; ++k) {
+            const uint32_t c = c0 + uint32_t(k * WARPS);
+            st[k] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        L = L * f0 + l;
-        M = nm;
-#pragma unroll
-        for (int k = 0; k < VPL; ++k) acc[k] *= f0;
-        const int here = int(min(32u, (parts - c0 + WARPS - 1u) / WARPS));
-#pragma unroll 4
-        for (int k = 0; k < here; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const uint64_t pk = __shfl_sync(0xffffffffu, ps, k);
-            const float *src = a.part + pk * D + lane * VPL;
-            if constexpr (VPL == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                acc[0] = fmaf(fk, v.x, acc[0]), acc[1] = fmaf(fk, v.y, acc[1]);
-                acc[2] = fmaf(fk, v.z, acc[2]), acc[3] = fmaf(fk, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                acc[0] = fmaf(fk, v.x, acc[0]), acc[1] = fmaf(fk, v.y, acc[1]);
+            for (int u = 0; u < VPL; ++u) v[k][u] = 0.0f;
+            if (c < parts) {
+                const uint64_t w = w0 + c;
+                const uint64_t ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
+                st[k] = __ldcg(a.stats + ps);
+                const float *src = a.part + ps * D + lane * VPL;
+                if constexpr (VPL == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                    v[k][0] = x.x, v[k][1] = x.y, v[k][VPL - 2] = x.z, v[k][VPL - 1] = x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                    v[k][0] = x.x, v[k][1] = x.y;
+                }
             }
+        }
+        float nm = M;
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) nm = fmaxf(nm, st[k].x);
+        const float f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
+        M = nm, L *= f0;
+#pragma unroll
+        for (int u = 0; u < VPL; ++u) acc[u] *= f0;
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            if (st[k].x == -INFINITY) continue;  // an empty part
+            const float f = exp2f(st[k].x - nm);
+            L = fmaf(f, st[k].y, L);
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) acc[u] = fmaf(f, v[k][u], acc[u]);
         }
     }
 #pragma unroll
@@ -996,7 +1043,10 @@ static thread_local uint32_t g_next_polls = 0;
 static thread_local bool g_limit_next = false;
 
 static unsigned attend_grid() { return unsigned(sm_count()); }
-static int tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
+#ifndef PAT_T8
+#define PAT_T8 8
+#endif
+static int tile_rows(int rows) { return rows <= PAT_T8 ? 8 : 16; }
 
 template <int D, int FMT, int R8>
 static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
