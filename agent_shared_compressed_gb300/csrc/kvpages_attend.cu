@@ -72,7 +72,7 @@ constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
 #ifndef PAT_W1
-#define PAT_W1 8
+#define PAT_W1 12
 #endif
 #ifndef PAT_W2
 #define PAT_W2 8
@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     float lift = 0.0f;           // weights are 2^(score - ref + lift)
     int lim[R8][2];              // tokens that the query sees
     float ref[R8][2];            // running maximum score, raised lazily
+    float bar2[R8][2], off[R8][2];  // where it is raised; what weights are relative to
     float sum[R8][2];            // the lane's part of the sum of weights
     float acc[MT][R8][4];
     float zsum[V4 ? NG : 1][R8][2];
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     lim[t][c] = rc < a.R ? len - (a.m - 1 - rc / a.G) : 0;
                     const int u = __shfl_sync(0xffffffffu, up, (2 * tig + c) * 4);
                     qs[t][c] = Q8 ? a.scale2 * __uint_as_float(uint32_t(127 - u) << 23) : a.scale2;
-                    ref[t][c] = -INFINITY;
+                    ref[t][c] = -INFINITY, bar2[t][c] = -INFINITY, off[t][c] = 0.0f;
                     sum[t][c] = 0.0f;
                 }
             }
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     top[t][c] = fmaxf(x[t][c], x[t][2 + c]);
-                    raise |= top[t][c] > ref[t][c] + PAT_SLACK;
+                    raise |= top[t][c] > bar2[t][c];
                 }
             if (__any_sync(0xffffffffu, raise)) {
                 const float up = V8 ? float(vexp - ve) : 0.0f;
@@ -665,7 +666,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     for (int c = 0; c < 2; ++c) {
                         const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
                         const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr + up);
-                        ref[t][c] = nr;
+                        ref[t][c] = nr, bar2[t][c] = nr + PAT_SLACK;
+                        off[t][c] = nr == -INFINITY ? 0.0f : nr - lift;
                         sum[t][c] *= f;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
@@ -680,9 +682,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             for (int t = 0; t < R8; ++t) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float r = ref[t][c] == -INFINITY ? 0.0f : ref[t][c] - lift;
-                    p[t][c] = exp2_fast(x[t][c] - r);
-                    p[t][2 + c] = exp2_fast(x[t][2 + c] - r);
+                    p[t][c] = exp2_fast(x[t][c] - off[t][c]);
+                    p[t][2 + c] = exp2_fast(x[t][2 + c] - off[t][c]);
                     sum[t][c] += p[t][c] + p[t][2 + c];
                 }
             }
