@@ -12,8 +12,8 @@
 // take), so the work is keeping enough bytes in flight on every SM and spending
 // few instructions on each.
 //
-// Work split.  The unit is a 16-token block of one (sequence, KV head, tile of
-// query rows).  All units of all sequences, in that order, are one list, cut
+// Work split.  The unit is one or two 16-token blocks (8- and 4-bit pages: two)
+// of one (sequence, KV head, tile of query rows).  All units of all sequences, in that order, are one list, cut
 // into equal runs, one per warp: no warp has more to do than another, however
 // ragged the lengths, and the cut follows from the lengths on the device, so a
 // captured graph stays right as sequences grow.  A row tile counts PAT_ITEM
@@ -22,8 +22,8 @@
 // maximum, sum and weighted values) and pages_join merges them in list order, so
 // results do not depend on timing.
 //
-// A warp's blocks arrive by bulk copies, one per block (a block is one run of
-// bytes), in the warp's own ring in shared memory, on the warp's own barriers:
+// A warp's blocks arrive by bulk copies, one per unit (the blocks of a head's
+// tokens in a page are one run of bytes), in the warp's own ring in shared memory, on the warp's own barriers:
 // warps never wait for each other after the start.
 //
 // Products, with tokens or dims as the 16 rows and the query rows as the 8
@@ -32,20 +32,19 @@
 //   O^T = V^T P^T  C: dims x queries 2 tig, 2 tig + 1
 // P^T comes from S^T's fragment by two 8 x 8 transposes.  The codes are in
 // fragment order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or
-// of a value token and expands them in registers to fp16 (4-bit values: bf16),
-// exactly (|code| <= 128).  What bounds 8- and 4-bit pages beside memory is that
-// expansion, most of it on the integer pipe, which takes a warp's instruction
-// every other cycle: two to three instructions per pair of codes.
+// of a value token and expands them in registers, keys to fp16 and values to
+// bf16, exactly (|code| <= 128).  What bounds 8- and 4-bit pages beside memory is
+// that expansion, most of it on the integer pipe, which takes a warp's
+// instruction every other cycle: two to four instructions per pair of codes.
 //
 // Key scales apply to the fp32 sums of their 32 dims.  Value scales go into the
-// weights, one product operand per 32 dims.  8-bit values: weight times scale in
-// fp16 (2^-12), relative to the running maximum score and to 2^(largest value
-// exponent so far), which leaves 25 binades below the largest before fp16's
-// subnormals round more coarsely: under 2^-36 of the largest value, and nothing
-// when the scales differ less than that.  4-bit and 16-bit values: a sum of two
-// bf16 (2^-17, fp32's range).  4-bit values q s + z enter as
-// (q - c) s + (z + c s) with c the integer of [0, 15] nearest to -z / s, formed
-// once per token and group: then |z + c s| is at most s / 2 (or of
+// weights, one product operand per 32 dims, as a sum of two bf16: 2^-17 of the
+// weight, and fp32's range, so that a token of large weight and tiny values (an
+// attention sink) takes nothing from the others.  (One fp16 per weight is 10%
+// fewer instructions, but loses weights 2^-25 below the largest where that one's
+// value is zero.)  4-bit values q s + z enter as (q - c) s + (z + c s) with c the
+// integer of [0, 15] nearest to -z / s, formed once per token and group: then
+// |z + c s| is at most s / 2 (or of
 // the code term's sign, where zero is outside the group's range), and the two
 // sums, of the code terms in the product and of the rest in fp32 once per 32
 // dims, do not cancel.  16-bit pages are multiplied as they are.
@@ -59,10 +58,10 @@ namespace kvp {
 
 constexpr int PAT_MOST_WARPS = 16;             // of a block
 #ifndef PAT_ITEM_N
-#define PAT_ITEM_N 4
+#define PAT_ITEM_N 2
 #endif
 #ifndef PAT_RUN_N
-#define PAT_RUN_N 3
+#define PAT_RUN_N 1
 #endif
 constexpr uint32_t PAT_ITEM = PAT_ITEM_N;               // units that a row tile counts beside its blocks
 constexpr uint32_t PAT_MIN_RUN = PAT_RUN_N;            // units of a warp's run, at least
@@ -71,6 +70,12 @@ constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
+#ifndef PAT_UB8
+#define PAT_UB8 2
+#endif
+#ifndef PAT_W1V8
+#define PAT_W1V8 12
+#endif
 #ifndef PAT_W1
 #define PAT_W1 12
 #endif
@@ -83,8 +88,7 @@ constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 #ifndef PAT_MANY
 #define PAT_MANY 64
 #endif
-constexpr float PAT_SLACK = 4.0f;
-constexpr int PAT_VSHIFT = 11;  // 8-bit values: weights over the reference, in fp16 with the slack
+constexpr float PAT_SLACK = 8.0f;
 
 struct PagesAttendArgs {
     PagesView pv;
@@ -98,6 +102,7 @@ struct PagesAttendArgs {
     uint32_t *plan;  // [nseq + 1] units before each sequence, per row tile
     float scale2;    // scale * log2(e)
     int nseq, m, nq, G, R, RT, max_pages;
+    int unit;  // tokens of a unit
     uint32_t nwarps, polls;
 };
 
@@ -187,6 +192,14 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// The bytes u of each 16-bit half (whatever their upper bytes hold) as bf16
+// u - 128: 128 + (u mod 128), less 256 or, with u's top bit, 128 (exact).
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+    const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, y = (w & 0x00800080u) ^ 0xC380C380u;
+    const __nv_bfloat162 r =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
 // The low nibble q of each 16-bit half as bf16 q - c: 128 + q, plus the halves of
 // y, -(128 + c) (exact).
 __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t y) {
@@ -232,6 +245,10 @@ __device__ __forceinline__ int seq_len(const PagesAttendArgs &a, int b, bool fla
     return int(cap);
 }
 
+// Units of a sequence's row tile (both kernels).
+__device__ __forceinline__ uint32_t tile_units(int len, int unit) {
+    return len ? uint32_t((int64_t(len) + unit - 1) / unit) + PAT_ITEM : 0u;
+}
 // Units of a warp's run (both kernels).
 __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) {
     const uint64_t per = (units + nwarps - 1) / nwarps;
@@ -241,13 +258,15 @@ __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) 
 // Warps of a block: as many as the registers of a tile's state allow.
 template <int D, int FMT, int R8>
 struct PatShape {
-    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (R8 == 2 ? PAT_W2 : PAT_W1)) : (R8 == 2 ? PAT_W64 : 16);
-    static constexpr uint32_t SLOT = (Block<D, FMT>::BYTES + 127u) / 128u * 128u;
+    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (R8 == 2 ? PAT_W2 : (FMT == KVP_PAGES_K8V8 ? PAT_W1V8 : PAT_W1))) : (R8 == 2 ? PAT_W64 : 16);
+    static constexpr int UB = FMT != KVP_PAGES_BF16 && R8 == 1 ? (FMT == KVP_PAGES_K8V8 && D == 128 ? PAT_UB8 : 2) : 1;  // blocks of a unit
+    static constexpr uint32_t SLOT = (UB * Block<D, FMT>::BYTES + 127u) / 128u * 128u;
     static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
-    static constexpr uint32_t STAGES = RING < 3u ? 3u : (RING > 8u ? 8u : RING);
+    static constexpr uint32_t LEAST = UB == 2 ? 2u : 3u;
+    static constexpr uint32_t STAGES = RING < LEAST ? LEAST : (RING > 8u ? 8u : RING);
     // 4-bit values: a warp's scales, remainders (fp32 [16][NG]) and -(128 + c) (bf16 pairs)
     static constexpr uint32_t NE = 16u * Block<D, FMT>::NG;
-    static constexpr uint32_t PREP = Block<D, FMT>::V4 ? NE * 10u : 0u;
+    static constexpr uint32_t PREP = Block<D, FMT>::V4 ? NE * 10u * UB : 0u;
     static constexpr uint32_t OFF_PREP = PAT_BAR_BYTES + WARPS * STAGES * SLOT;
     static constexpr uint32_t OFF_PLAN = OFF_PREP + WARPS * PREP;
     static_assert(WARPS * STAGES * 8 <= PAT_BAR_BYTES, "a barrier per slot");
@@ -279,8 +298,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     using B = Block<D, FMT>;
     using SM = PatShape<D, FMT, R8>;
     constexpr int NG = B::NG, MT = D / 16, RTILE = 8 * R8, WARPS = SM::WARPS, THREADS = WARPS * 32;
+    constexpr int UB = SM::UB, GU = 32 / UB;  // units whose addresses the lanes hold
     constexpr uint32_t STAGES = SM::STAGES;
-    constexpr bool Q8 = B::Q8, V4 = B::V4, V8 = Q8 && !V4;
+    constexpr bool Q8 = B::Q8, V4 = B::V4;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint32_t *pre = reinterpret_cast<uint32_t *>(sm + SM::OFF_PLAN);
     __shared__ uint32_t wsum[WARPS];
@@ -298,8 +318,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     // finds them by itself (all write the same values)
     uint32_t carry = 0;
     if (a.nseq <= 32) {
-        uint32_t n = lane < a.nseq ? uint32_t((seq_len(a, lane, blockIdx.x == 0 && warp == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
-        n += n ? PAT_ITEM : 0u;
+        uint32_t n = lane < a.nseq ? tile_units(seq_len(a, lane, blockIdx.x == 0 && warp == 0), 16 * UB) : 0u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
@@ -318,8 +337,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     }
     for (int b0 = 0; a.nseq > 32 && b0 < a.nseq; b0 += THREADS) {
         const int b = b0 + tid;
-        uint32_t n = b < a.nseq ? uint32_t((seq_len(a, b, blockIdx.x == 0) + PAGES_BLOCK - 1) / PAGES_BLOCK) : 0u;
-        n += n ? PAT_ITEM : 0u;
+        uint32_t n = b < a.nseq ? tile_units(seq_len(a, b, blockIdx.x == 0), 16 * UB) : 0u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
@@ -381,14 +399,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             at = uint32_t(r - uint64_t(tile) * n);
         }
     };
-    // the lane's block of the 32 units that start at `first` of the run: its address, or
-    // 0 past the run, in a tile's empty places and for a bad page id
+    // the lane's block of the GU units that start at `first` of the run: its address, or
+    // 0 past the run or the sequence, in a tile's empty places and for a bad page id
     auto address = [&](uint32_t first, int &b, uint32_t &tile, uint32_t &at) -> uint64_t {
-        const uint32_t u = first + uint32_t(lane);
+        const uint32_t u = first + uint32_t(lane / UB);
         if (u >= cnt) return 0;
         locate(f0 + u, b, tile, at);
         if (at < PAT_ITEM) return 0;
-        const uint32_t t0 = (at - PAT_ITEM) * PAGES_BLOCK;
+        const uint32_t t0 = ((at - PAT_ITEM) * UB + uint32_t(lane % UB)) * PAGES_BLOCK;
+        if (UB > 1 && t0 >= uint32_t(seq_len(a, b, false))) return 0;
         const int page = __ldg(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP));
         if (page < 0 || page >= a.pv.n_pages) {
             pages_flag(a.pv, FLAG_PAGE);
@@ -398,23 +417,35 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                uint64_t(tile / uint32_t(a.RT)) * a.pv.tile_bytes +
                uint64_t((t0 & uint32_t(a.pv.P - 1)) / PAGES_BLOCK) * B::BYTES;
     };
-    // this lane's copy into slot s (nothing to copy: the phase still completes)
-    auto issue = [&](uint64_t src, uint32_t s) {
-        mbar_expect_tx(bar + 8u * s, src ? B::BYTES : 0u);
+    // the copies of unit n into slot s, by the lanes that hold its blocks (nothing to
+    // copy: the phase still completes); two blocks of one page are one run of bytes
+    auto issue = [&](uint32_t n, uint64_t src, uint32_t good, uint32_t s) {
+        if (lane / UB != int(n % GU)) return;
+        const uint32_t to = ring + s * SM::SLOT, at = bar + 8u * s;
+        const uint32_t mine = (good >> (lane / UB * UB)) & (UB == 2 ? 3u : 1u);
+        const bool lead = lane % UB == 0;
+        if (lead) mbar_expect_tx(at, (UB == 2 ? uint32_t(__popc(mine)) : mine) * B::BYTES);
         fence_proxy_async();  // the warp's reads of the slot come first
-        if (src) bulk_g2s(ring + s * SM::SLOT, reinterpret_cast<const void *>(src), B::BYTES, bar + 8u * s);
+        if (UB == 2 && mine == 3u && a.pv.P > PAGES_BLOCK) {
+            if (lead) bulk_g2s(to, reinterpret_cast<const void *>(src), 2u * B::BYTES, at);
+        } else if (src) {
+            bulk_g2s(to + uint32_t(lane % UB) * B::BYTES, reinterpret_cast<const void *>(src), B::BYTES, at);
+        }
     };
 
     int b = 0, len = 0;
     uint32_t tile = 0, place = 0, nplace = 0, seg0 = 0;
     uint64_t cur = address(0, b, tile, place), nxt = 0;
-    uint32_t good = __ballot_sync(0xffffffffu, cur != 0);
-    if (uint32_t(lane) < STAGES && uint32_t(lane) < cnt) issue(cur, uint32_t(lane));
+    uint32_t good = __ballot_sync(0xffffffffu, cur != 0), good_nxt = 0;
+#pragma unroll
+    for (uint32_t s = 0; s < STAGES; ++s)
+        if (s < cnt) issue(s, cur, good, s);
     b = __shfl_sync(0xffffffffu, b, 0), tile = __shfl_sync(0xffffffffu, tile, 0), place = __shfl_sync(0xffffffffu, place, 0);
-    if (cnt > 32u) {
+    if (cnt > uint32_t(GU)) {
         int lb;
         uint32_t lt, lp;
-        nxt = address(32, lb, lt, lp);
+        nxt = address(GU, lb, lt, lp);
+        good_nxt = __ballot_sync(0xffffffffu, nxt != 0);
     }
     bool fresh = true;             // the next unit starts a segment
     uint32_t slot = 0, phase = 0;  // ring position of the next unit
@@ -430,8 +461,6 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
     // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c).
     uint32_t qf[D / 16][R8][2];  // query fragments by k-step
     float qs[R8][2];             // factor of the scores (base 2)
-    int vexp = 0;                // V8: biased fp16 exponent of the largest value scale so far
-    float lift = 0.0f;           // weights are 2^(score - ref + lift)
     int lim[R8][2];              // tokens that the query sees
     float ref[R8][2];            // running maximum score, raised lazily
     float bar2[R8][2], off[R8][2];  // where it is raised; what weights are relative to
@@ -508,8 +537,6 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     sum[t][c] = 0.0f;
                 }
             }
-            vexp = 0;
-            lift = V8 ? float(PAT_VSHIFT + 14) : 0.0f;
 #pragma unroll
             for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -536,15 +563,18 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             }
             return;
         }
-        if ((good >> (n & 31u)) & 1u) {
-            const uint32_t at = ring + slot * SM::SLOT;
-            const int t0 = int(place - PAT_ITEM) * PAGES_BLOCK;
-            const bool tail = t0 + PAGES_BLOCK > len - (a.m - 1);  // some query does not see all 16 tokens
+        const uint32_t here = (good >> (n % GU * UB)) & (UB == 2 ? 3u : 1u);
+        if (here) {
+            const uint32_t at0 = ring + slot * SM::SLOT;
+            const int t0 = int(place - PAT_ITEM) * (PAGES_BLOCK * UB);
+            // some query does not see all of the unit's tokens
+            const bool tail = t0 + PAGES_BLOCK * UB > len - (a.m - 1) || (UB == 2 && here != 3u);
             if (Q8 && tail) {
                 // tokens never written: their value scales (and zero points) may be anything
                 const int nv = len - t0;
-                if (lane >= nv && lane < PAGES_BLOCK) {
-                    const uint32_t sa = at + B::OFF_VS + uint32_t(lane) * B::VSROW;
+                if (lane < PAGES_BLOCK * UB && (lane >= nv || !((here >> (lane / PAGES_BLOCK)) & 1u))) {
+                    const uint32_t sa = at0 + uint32_t(lane / PAGES_BLOCK) * B::BYTES + B::OFF_VS +
+                                        uint32_t(lane % PAGES_BLOCK) * B::VSROW;
 #pragma unroll
                     for (uint32_t k = 0; k < B::VSROW; k += 4) sts32(sa + k, 0.0f);
                 }
@@ -553,121 +583,117 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             }
             if constexpr (V4) {
 #pragma unroll
-                for (int u = 0; u < NG / 2; ++u) {
-                    const int e = 32 * u + lane, t = e / NG, gr = e % NG;  // token, group
-                    const float2 sz = half2_f32(lds32(at + B::OFF_VS + 4u * uint32_t(e)));
+                for (int u = 0; u < NG / 2 * UB; ++u) {
+                    const int e = 32 * u + lane, t = e / NG, gr = e % NG;  // token of the unit, group
+                    const float2 sz = half2_f32(lds32(at0 + uint32_t(u / (NG / 2)) * (B::BYTES - 64u * NG) + B::OFF_VS + 4u * uint32_t(e)));
                     float c;
                     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(sz.x));
                     // any integer will do; NaN (0 / 0) becomes 0
                     c = fminf(fmaxf(rintf(-sz.y * c), 0.0f), 15.0f);
                     sts32(prep + 4u * uint32_t(e), sz.x);
-                    sts32(prep + 4u * (SM::NE + uint32_t(e)), fmaf(c, sz.x, sz.y));
-                    const uint32_t ca = prep + 8u * SM::NE + 2u * uint32_t((t >> 1) * 2 * NG + gr * 2 + (t & 1));
+                    sts32(prep + 4u * (UB * SM::NE + uint32_t(e)), fmaf(c, sz.x, sz.y));
+                    const uint32_t ca = prep + 8u * UB * SM::NE + 2u * uint32_t((t >> 1) * 2 * NG + gr * 2 + (t & 1));
                     sts16(ca, __bfloat16_as_ushort(__float2bfloat16_rn(-128.0f - c)));
                 }
                 __syncwarp();
             }
-            // scores: x[t][0..1] token g, [2..3] token g + 8, of the two queries
-            float x[R8][4];
-            if constexpr (Q8) {
-                uint32_t w[2][NG][2];
-                float ks[2][NG];
+            // scores: x[u][t][0..1] token 16 u + g, [2..3] token 16 u + g + 8, of the two queries
+            float x[UB][R8][4];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t ka = at + k_off + uint32_t(hf) * 8u * B::KROW;
-                    const uint4 v = lds128(ka);
-                    w[hf][0][0] = v.x, w[hf][0][1] = v.y, w[hf][1][0] = v.z, w[hf][1][1] = v.w;
-                    if constexpr (D == 128) {
-                        const uint4 u = lds128(ka ^ 16u);
-                        w[hf][2][0] = u.x, w[hf][2][1] = u.y, w[hf][3][0] = u.z, w[hf][3][1] = u.w;
-                    }
-                    lds_halfs<NG>(at + B::OFF_KS + uint32_t(8 * hf + g) * B::SROW, ks[hf]);
-                }
+            for (int u = 0; u < UB; ++u) {
+                const uint32_t at = at0 + uint32_t(u) * B::BYTES;
 #pragma unroll
-                for (int t = 0; t < R8; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
+                for (int t = 0; t < R8; ++t) x[u][t][0] = x[u][t][1] = x[u][t][2] = x[u][t][3] = 0.0f;
+                if constexpr (Q8) {
+                    uint32_t w[2][NG][2];
+                    float ks[2][NG];
 #pragma unroll
-                for (int k = 0; k < NG; ++k) {
-                    float c[R8][4];
-#pragma unroll
-                    for (int t = 0; t < R8; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t a0 = codes_f16(w[0][k][e], 0x4140u), a1 = codes_f16(w[1][k][e], 0x4140u);
-                        const uint32_t a2 = codes_f16(w[0][k][e], 0x4342u), a3 = codes_f16(w[1][k][e], 0x4342u);
-#pragma unroll
-                        for (int t = 0; t < R8; ++t) mma_f16(c[t], a0, a1, a2, a3, qf[2 * k + e][t][0], qf[2 * k + e][t][1]);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t ka = at + k_off + uint32_t(hf) * 8u * B::KROW;
+                        const uint4 v = lds128(ka);
+                        w[hf][0][0] = v.x, w[hf][0][1] = v.y, w[hf][1][0] = v.z, w[hf][1][1] = v.w;
+                        if constexpr (D == 128) {
+                            const uint4 v2 = lds128(ka ^ 16u);
+                            w[hf][2][0] = v2.x, w[hf][2][1] = v2.y, w[hf][3][0] = v2.z, w[hf][3][1] = v2.w;
+                        }
+                        lds_halfs<NG>(at + B::OFF_KS + uint32_t(8 * hf + g) * B::SROW, ks[hf]);
                     }
 #pragma unroll
-                    for (int t = 0; t < R8; ++t)
+                    for (int k = 0; k < NG; ++k) {
+                        float c[R8][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[t][e] = fmaf(c[t][e], ks[e >> 1][k], x[t][e]);
+                        for (int t = 0; t < R8; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t a0 = codes_f16(w[0][k][e], 0x4140u), a1 = codes_f16(w[1][k][e], 0x4140u);
+                            const uint32_t a2 = codes_f16(w[0][k][e], 0x4342u), a3 = codes_f16(w[1][k][e], 0x4342u);
+#pragma unroll
+                            for (int t = 0; t < R8; ++t)
+                                mma_f16(c[t], a0, a1, a2, a3, qf[2 * k + e][t][0], qf[2 * k + e][t][1]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < R8; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[u][t][e] = fmaf(c[t][e], ks[e >> 1][k], x[u][t][e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t w[4];
+                        ldsm4(w, (at + k_off) ^ (32u * uint32_t(k)));
+#pragma unroll
+                        for (int t = 0; t < R8; ++t) mma_bf16(x[u][t], w[0], w[1], w[2], w[3], qf[k][t][0], qf[k][t][1]);
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int t = 0; t < R8; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t w[4];
-                    ldsm4(w, (at + k_off) ^ (32u * uint32_t(k)));
-#pragma unroll
-                    for (int t = 0; t < R8; ++t) mma_bf16(x[t], w[0], w[1], w[2], w[3], qf[k][t][0], qf[k][t][1]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < R8; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][e] *= qs[t][e & 1];
-            if (tail) {
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (t0 + g + 8 * (e >> 1) >= lim[t][e & 1]) x[t][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) x[u][t][e] *= qs[t][e & 1];
             }
-            // value scales of tokens g and g + 8
-            float sv[2][Q8 ? NG : 1], zv[2][V4 ? NG : 1];
+            if (tail) {
+#pragma unroll
+                for (int u = 0; u < UB; ++u)
+#pragma unroll
+                    for (int t = 0; t < R8; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t0 + 16 * u + g + 8 * (e >> 1) >= lim[t][e & 1] || !((here >> u) & 1u)) x[u][t][e] = -INFINITY;
+            }
+            // value scales of tokens g and g + 8 of each block
+            float sv[UB][2][Q8 ? NG : 1], zv[UB][2][V4 ? NG : 1];
+            bool raise = false;
             if constexpr (Q8) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if constexpr (V4) {
-                        const uint32_t pa = prep + 4u * NG * uint32_t(8 * hf + g);
-                        lds_floats<NG>(pa, sv[hf]);
-                        lds_floats<NG>(pa + 4u * SM::NE, zv[hf]);
-                    } else {
-                        lds_halfs<NG>(at + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[hf]);
-                    }
-                }
-            }
-            bool raise = false;
-            int ve = 0;
-            if constexpr (V8) {
-                float big = 0.0f;
+                for (int u = 0; u < UB; ++u)
 #pragma unroll
-                for (int k = 0; k < NG; ++k) big = fmaxf(big, fmaxf(sv[0][k], sv[1][k]));
-                // scales < 2^(ve - 14)
-                ve = max(vexp, int(__reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23) - 112);
-                raise = ve > vexp;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if constexpr (V4) {
+                            const uint32_t pa = prep + 4u * NG * uint32_t(16 * u + 8 * hf + g);
+                            lds_floats<NG>(pa, sv[u][hf]);
+                            lds_floats<NG>(pa + 4u * UB * SM::NE, zv[u][hf]);
+                        } else {
+                            lds_halfs<NG>(at0 + uint32_t(u) * B::BYTES + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[u][hf]);
+                        }
+                    }
             }
             float top[R8][2];
 #pragma unroll
             for (int t = 0; t < R8; ++t)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    top[t][c] = fmaxf(x[t][c], x[t][2 + c]);
+                    top[t][c] = fmaxf(x[0][t][c], x[0][t][2 + c]);
+                    if constexpr (UB == 2) top[t][c] = fmaxf(top[t][c], fmaxf(x[UB - 1][t][c], x[UB - 1][t][2 + c]));
                     raise |= top[t][c] > bar2[t][c];
                 }
             if (__any_sync(0xffffffffu, raise)) {
-                const float up = V8 ? float(vexp - ve) : 0.0f;
-                vexp = ve;
-                lift += up;
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
-                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr + up);
+                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
                         ref[t][c] = nr, bar2[t][c] = nr + PAT_SLACK;
-                        off[t][c] = nr == -INFINITY ? 0.0f : nr - lift;
+                        off[t][c] = nr == -INFINITY ? 0.0f : nr;
                         sum[t][c] *= f;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
@@ -677,176 +703,171 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                         }
                     }
             }
-            float p[R8][4];
+            float p[UB][R8][4];
 #pragma unroll
-            for (int t = 0; t < R8; ++t) {
+            for (int u = 0; u < UB; ++u)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    p[t][c] = exp2_fast(x[t][c] - off[t][c]);
-                    p[t][2 + c] = exp2_fast(x[t][2 + c] - off[t][c]);
-                    sum[t][c] += p[t][c] + p[t][2 + c];
-                }
-            }
-            if constexpr (Q8) {
-                uint32_t vw[2][2][V4 ? NG / 2 : NG];  // [token half][odd token]: the lane's granule
+                for (int t = 0; t < R8; ++t)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
+                    for (int c = 0; c < 2; ++c) {
+                        p[u][t][c] = exp2_fast(x[u][t][c] - off[t][c]);
+                        p[u][t][2 + c] = exp2_fast(x[u][t][2 + c] - off[t][c]);
+                        sum[t][c] += p[u][t][c] + p[u][t][2 + c];
+                    }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t va = at + (k ? v_odd : v_off) + uint32_t(hf) * 8u * B::VROW;
-                        if constexpr (B::VROW == 128) {
-                            const uint4 v = lds128(va);
-                            vw[hf][k][0] = v.x, vw[hf][k][1] = v.y, vw[hf][k][NG - 2] = v.z, vw[hf][k][NG - 1] = v.w;
-                        } else if constexpr (B::VROW == 64) {
-                            const uint2 v = lds64(va);
-                            vw[hf][k][0] = v.x, vw[hf][k][1] = v.y;
-                        } else {
-                            vw[hf][k][0] = lds32(va);
+            for (int u = 0; u < UB; ++u) {
+                const uint32_t at = at0 + uint32_t(u) * B::BYTES;
+                if constexpr (Q8) {
+                    uint32_t vw[2][2][V4 ? NG / 2 : NG];  // [token half][odd token]: the lane's granule
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t va = at + (k ? v_odd : v_off) + uint32_t(hf) * 8u * B::VROW;
+                            if constexpr (B::VROW == 128) {
+                                const uint4 v = lds128(va);
+                                vw[hf][k][0] = v.x, vw[hf][k][1] = v.y, vw[hf][k][NG - 2] = v.z, vw[hf][k][NG - 1] = v.w;
+                            } else if constexpr (B::VROW == 64) {
+                                const uint2 v = lds64(va);
+                                vw[hf][k][0] = v.x, vw[hf][k][1] = v.y;
+                            } else {
+                                vw[hf][k][0] = lds32(va);
+                            }
+                        }
+                    uint32_t cv[2][V4 ? NG : 1];  // [token half]
+                    if constexpr (V4) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const uint32_t ca = prep + 8u * UB * SM::NE + 4u * NG * uint32_t(8 * u + 4 * hf + tig);
+                            if constexpr (NG == 4) {
+                                const uint4 v = lds128(ca);
+                                cv[hf][0] = v.x, cv[hf][1] = v.y, cv[hf][NG - 2] = v.z, cv[hf][NG - 1] = v.w;
+                            } else {
+                                const uint2 v = lds64(ca);
+                                cv[hf][0] = v.x, cv[hf][1] = v.y;
+                            }
                         }
                     }
-                uint32_t cv[2][V4 ? NG : 1];  // [token half]
-                if constexpr (V4) {
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const uint32_t ca = prep + 8u * SM::NE + 4u * NG * uint32_t(4 * hf + tig);
-                        if constexpr (NG == 4) {
-                            const uint4 v = lds128(ca);
-                            cv[hf][0] = v.x, cv[hf][1] = v.y, cv[hf][NG - 2] = v.z, cv[hf][NG - 1] = v.w;
-                        } else {
-                            const uint2 v = lds64(ca);
-                            cv[hf][0] = v.x, cv[hf][1] = v.y;
+                    for (int e = 0; e < NG; ++e) {
+                        uint32_t hi[R8][2], lo[R8][2];
+#pragma unroll
+                        for (int t = 0; t < R8; ++t)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const float w0 = p[u][t][2 * hf] * sv[u][hf][e], w1 = p[u][t][2 * hf + 1] * sv[u][hf][e];
+                                uint32_t h2, l2;
+                                split_bf16x2(w0, w1, h2, l2);
+                                hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
+                            }
+                        uint32_t v[2][4];  // [token half][dim of the granule's word]
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if constexpr (!V4) {
+                                // byte j of both tokens' words to the halves' low bytes
+                                v[hf][0] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5410u));
+                                v[hf][1] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5511u));
+                                v[hf][2] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x6622u));
+                                v[hf][3] = codes_bf16(__byte_perm(vw[hf][0][e], vw[hf][1][e], 0x7733u));
+                            } else {
+                                const uint32_t w = __byte_perm(vw[hf][0][e / 2], vw[hf][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) v[hf][j] = nibbles_bf16(w >> (4 * j), cv[hf][e]);
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < R8; ++t)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t a0 = v[0][2 * k], a1 = v[0][2 * k + 1], a2 = v[1][2 * k], a3 = v[1][2 * k + 1];
+                                mma_bf16(acc[2 * e + k][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
+                                mma_bf16(acc[2 * e + k][t], a0, a1, a2, a3, lo[t][0], lo[t][1]);
+                            }
+                        if constexpr (V4) {
+#pragma unroll
+                            for (int t = 0; t < R8; ++t)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    zsum[e][t][c & 1] = fmaf(p[u][t][c], zv[u][c >> 1][e], zsum[e][t][c & 1]);
                         }
                     }
-                }
+                } else {
+                    if (tail) {
+                        // tokens of the block that some query does not see: zeros where
+                        // none sees them; one that holds Inf or NaN is added by itself
+                        // to the queries that see it (0 * Inf would reach the others)
+                        const int nv = len - t0;
+                        for (int t = max(nv - (a.m - 1), 0); t < PAGES_BLOCK; ++t) {
+                            const uint32_t va = at + B::OFF_V + uint32_t(t) * B::VROW;
+                            bool odd = t >= nv;
+                            if (!odd) {
+                                bool inf = false;
+                                for (int c = lane; c < D / 2; c += 32) {
+                                    const uint32_t w = lds32(va + 4u * uint32_t(c));
+                                    inf |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+                                }
+                                odd = __any_sync(0xffffffffu, inf);
+                                if (odd) {
 #pragma unroll
-                for (int e = 0; e < NG; ++e) {
+                                    for (int r = 0; r < R8; ++r)
+#pragma unroll
+                                        for (int c = 0; c < 2; ++c) {
+                                            // the token's weight is with lane row t % 8
+                                            const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][2 + c],
+                                                                        ((t & 7) << 2) | tig);
+                                            if (t0 + t >= lim[r][c]) continue;
+#pragma unroll
+                                            for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                                for (int h = 0; h < 2; ++h) {  // dims 16 k + 8 h + g
+                                                    const uint32_t d2 = uint32_t(k) * 32u + uint32_t(h) * 16u + uint32_t(g >> 1) * 4u;
+                                                    const uint32_t y = lds32(at + B::value(uint32_t(t), d2));
+                                                    acc[k][r][2 * h + c] =
+                                                        fmaf(w, g & 1 ? bf16_hi(y) : bf16_lo(y), acc[k][r][2 * h + c]);
+                                                }
+                                        }
+                                    __syncwarp();
+                                }
+                            }
+                            if (odd && lane < D / 8) sts128_zero(va + 16u * uint32_t(lane));
+                        }
+                        fence_proxy_async();  // before a later copy into the slot
+                        __syncwarp();
+                    }
                     uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
                     for (int t = 0; t < R8; ++t)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const float w0 = p[t][2 * hf] * sv[hf][e], w1 = p[t][2 * hf + 1] * sv[hf][e];
-                            if constexpr (V4) {
-                                uint32_t h2, l2;
-                                split_bf16x2(w0, w1, h2, l2);
-                                hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
-                            } else {
-                                hi[t][hf] = transpose8(pack_f16x2(w0, w1));
-                            }
+                            uint32_t h2, l2;
+                            split_bf16x2(p[u][t][2 * hf], p[u][t][2 * hf + 1], h2, l2);
+                            hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
                         }
-                    uint32_t v[2][4];  // [token half][dim of the granule's word]
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        if constexpr (!V4) {
-                            const uint32_t w0 = __byte_perm(vw[hf][0][e], vw[hf][1][e], 0x5140u);
-                            const uint32_t w1 = __byte_perm(vw[hf][0][e], vw[hf][1][e], 0x7362u);
-                            v[hf][0] = codes_f16(w0, 0x4140u);
-                            v[hf][1] = codes_f16(w0, 0x4342u);
-                            v[hf][2] = codes_f16(w1, 0x4140u);
-                            v[hf][3] = codes_f16(w1, 0x4342u);
-                        } else {
-                            const uint32_t w = __byte_perm(vw[hf][0][e / 2], vw[hf][1][e / 2], e & 1 ? 0x7632u : 0x5410u);
+                    for (int k = 0; k < MT; ++k) {
+                        uint32_t w[4];
+                        ldsm4_t(w, (at + v_off) ^ (32u * uint32_t(k)));
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[hf][j] = nibbles_bf16(w >> (4 * j), cv[hf][e]);
+                        for (int t = 0; t < R8; ++t) {
+                            mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
+                            mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
                         }
-                    }
-#pragma unroll
-                    for (int t = 0; t < R8; ++t)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t a0 = v[0][2 * u], a1 = v[0][2 * u + 1], a2 = v[1][2 * u], a3 = v[1][2 * u + 1];
-                            if constexpr (V4) {
-                                mma_bf16(acc[2 * e + u][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
-                                mma_bf16(acc[2 * e + u][t], a0, a1, a2, a3, lo[t][0], lo[t][1]);
-                            } else {
-                                mma_f16(acc[2 * e + u][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
-                            }
-                        }
-                    if constexpr (V4) {
-#pragma unroll
-                        for (int t = 0; t < R8; ++t)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                zsum[e][t][c & 1] = fmaf(p[t][c], zv[c >> 1][e], zsum[e][t][c & 1]);
-                    }
-                }
-            } else {
-                if (tail) {
-                    // tokens of the block that some query does not see: zeros where
-                    // none sees them; one that holds Inf or NaN is added by itself
-                    // to the queries that see it (0 * Inf would reach the others)
-                    const int nv = len - t0;
-                    for (int t = max(nv - (a.m - 1), 0); t < PAGES_BLOCK; ++t) {
-                        const uint32_t va = at + B::OFF_V + uint32_t(t) * B::VROW;
-                        bool odd = t >= nv;
-                        if (!odd) {
-                            bool inf = false;
-                            for (int c = lane; c < D / 2; c += 32) {
-                                const uint32_t w = lds32(va + 4u * uint32_t(c));
-                                inf |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-                            }
-                            odd = __any_sync(0xffffffffu, inf);
-                            if (odd) {
-#pragma unroll
-                                for (int r = 0; r < R8; ++r)
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        // the token's weight is with lane row t % 8
-                                        const float w = __shfl_sync(0xffffffffu, t < 8 ? p[r][c] : p[r][2 + c],
-                                                                    ((t & 7) << 2) | tig);
-                                        if (t0 + t < lim[r][c]) {
-#pragma unroll
-                                            for (int k = 0; k < MT; ++k)
-#pragma unroll
-                                                for (int u = 0; u < 2; ++u) {  // dims 16 k + 8 u + g
-                                                    const uint32_t x2 = lds32(at + B::value(uint32_t(t), uint32_t(k) * 32u + uint32_t(u) * 16u +
-                                                                                                             uint32_t(g >> 1) * 4u));
-                                                    acc[k][r][2 * u + c] =
-                                                        fmaf(w, g & 1 ? bf16_hi(x2) : bf16_lo(x2), acc[k][r][2 * u + c]);
-                                                }
-                                        }
-                                    }
-                                __syncwarp();
-                            }
-                        }
-                        if (odd && lane < D / 8) sts128_zero(va + 16u * uint32_t(lane));
-                    }
-                    fence_proxy_async();  // before a later copy into the slot
-                    __syncwarp();
-                }
-                uint32_t hi[R8][2], lo[R8][2];
-#pragma unroll
-                for (int t = 0; t < R8; ++t)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t h2, l2;
-                        split_bf16x2(p[t][2 * hf], p[t][2 * hf + 1], h2, l2);
-                        hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
-                    }
-#pragma unroll
-                for (int k = 0; k < MT; ++k) {
-                    uint32_t w[4];
-                    ldsm4_t(w, (at + v_off) ^ (32u * uint32_t(k)));
-#pragma unroll
-                    for (int t = 0; t < R8; ++t) {
-                        mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
-                        mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
                     }
                 }
             }
         }
         __syncwarp();  // every lane is done with the slot
-        {
-            const uint32_t nx = n + STAGES;
-            if (nx < cnt && (nx & 31u) == uint32_t(lane)) issue((nx ^ n) < 32u ? cur : nxt, slot);
+        if (n + STAGES < cnt) {
+            const bool far = n % GU + STAGES >= uint32_t(GU);
+            issue(n + STAGES, far ? nxt : cur, far ? good_nxt : good, slot);
         }
         if (++slot == STAGES) slot = 0, phase ^= 1u;
-        if ((n & 31u) == 31u) {
-            cur = nxt;
-            good = __ballot_sync(0xffffffffu, cur != 0);
+        if (n % GU == uint32_t(GU) - 1u) {
+            cur = nxt, good = good_nxt;
             int lb;
             uint32_t lt, lp;
-            nxt = address(n + 33u, lb, lt, lp);
+            nxt = address(n + 1u + uint32_t(GU), lb, lt, lp);
+            good_nxt = __ballot_sync(0xffffffffu, nxt != 0);
         }
         ++place;
         if (place < nplace && n + 1 < cnt) continue;
@@ -878,7 +899,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                     }
                 }
                 if (r >= a.R) continue;
-                const float base2 = ref[t][c] - lift;
+                const float base2 = ref[t][c];
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
                     const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
@@ -956,8 +977,7 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     if (a.nseq <= PAT_OWN_PLAN) {
         // pages_attend has passed its own wait, so the lengths are final
         for (int k = lane; k < a.nseq; k += 32) {
-            uint32_t u = uint32_t((seq_len(a, k, false) + PAGES_BLOCK - 1) / PAGES_BLOCK);
-            u += u ? PAT_ITEM : 0u;
+            const uint32_t u = tile_units(seq_len(a, k, false), a.unit);
             all += u;
             before += k < int(b) ? u : 0u;
             n += k == int(b) ? u : 0u;
@@ -1070,6 +1090,7 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     cfg.gridDim = dim3(attend_grid());
     cfg.blockDim = dim3(SM::WARPS * 32);
     a.nwarps = attend_grid() * SM::WARPS;
+    a.unit = PAGES_BLOCK * SM::UB;
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cfg.attrs = attr;
