@@ -219,10 +219,24 @@ __device__ __forceinline__ float exp2_fast(float x) {  // results under 2^-126 a
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// a = hi + lo in two bf16: the pair's high parts, and the remainders.
-__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
+// The weights (w0, w1) of a token and two queries as value-product operands: a
+// sum of two bf16.  TWICE: lanes of columns 0..3 (tig < 2) give the first, the
+// others the second, in one operand; else one operand each.
+template <bool TWICE>
+__device__ __forceinline__ void split_weights(float w0, float w1, int tig, uint32_t &hi, uint32_t &lo) {
+    const uint32_t h = pack_bf16x2(w0, w1);
+    if constexpr (TWICE) {
+        // the first lanes take nothing off, so that they pack the same again
+        const float h0 = __uint_as_float(__byte_perm(h, 0u, tig < 2 ? 0x4444u : 0x1044u));
+        const float h1 = __uint_as_float(h & (tig < 2 ? 0u : 0xFFFF0000u));
+        const float2 d = __ffma2_rn(make_float2(h0, h1), make_float2(-1.0f, -1.0f), make_float2(w0, w1));
+        hi = transpose8(pack_bf16x2(d.x, d.y));
+        lo = 0u;
+    } else {
+        const float2 d =
+            __ffma2_rn(make_float2(bf16_lo(h), bf16_hi(h)), make_float2(-1.0f, -1.0f), make_float2(w0, w1));
+        hi = transpose8(h), lo = transpose8(pack_bf16x2(d.x, d.y));
+    }
 }
 // Over the eight lanes of a quad position (the rows of a C fragment).
 __device__ __forceinline__ float rows_add(float x) {
@@ -256,10 +270,10 @@ __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) 
 }
 
 // Warps of a block: as many as the registers of a tile's state allow.
-template <int D, int FMT, int R8>
+template <int D, int FMT, int RC>
 struct PatShape {
-    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (R8 == 2 ? PAT_W2 : (FMT == KVP_PAGES_K8V8 ? PAT_W1V8 : PAT_W1))) : (R8 == 2 ? PAT_W64 : 16);
-    static constexpr int UB = FMT != KVP_PAGES_BF16 && R8 == 1 ? (FMT == KVP_PAGES_K8V8 && D == 128 ? PAT_UB8 : 2) : 1;  // blocks of a unit
+    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (RC == 16 ? PAT_W2 : (FMT == KVP_PAGES_K8V8 ? PAT_W1V8 : PAT_W1))) : (RC == 16 ? PAT_W64 : 16);
+    static constexpr int UB = FMT != KVP_PAGES_BF16 && RC <= 8 ? (FMT == KVP_PAGES_K8V8 && D == 128 ? PAT_UB8 : 2) : 1;  // blocks of a unit
     static constexpr uint32_t SLOT = (UB * Block<D, FMT>::BYTES + 127u) / 128u * 128u;
     static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
     static constexpr uint32_t LEAST = UB == 2 ? 2u : 3u;
@@ -291,13 +305,17 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
     return make_float2(wa, wb);
 }
 
-// R8: groups of 8 query rows in a tile (1 or 2).
-template <int D, int FMT, int R8>
-__global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
+// RC: query rows of a tile (4, 8 or 16).  A tile of 4 has its rows in columns
+// 0..3 and again in 4..7: the weights' first bf16 in the former, the second in
+// the latter, so that one value product does for both.
+template <int D, int FMT, int RC>
+__global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     pages_attend(const __grid_constant__ PagesAttendArgs a) {
     using B = Block<D, FMT>;
-    using SM = PatShape<D, FMT, R8>;
-    constexpr int NG = B::NG, MT = D / 16, RTILE = 8 * R8, WARPS = SM::WARPS, THREADS = WARPS * 32;
+    using SM = PatShape<D, FMT, RC>;
+    constexpr int R8 = RC == 16 ? 2 : 1;  // groups of 8 columns
+    constexpr bool TWICE = RC == 4;
+    constexpr int NG = B::NG, MT = D / 16, RTILE = RC, WARPS = SM::WARPS, THREADS = WARPS * 32;
     constexpr int UB = SM::UB, GU = 32 / UB;  // units whose addresses the lanes hold
     constexpr uint32_t STAGES = SM::STAGES;
     constexpr bool Q8 = B::Q8, V4 = B::V4;
@@ -474,7 +492,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
         const int h = int(st) / a.RT, r0 = int(st) % a.RT * RTILE;
 #pragma unroll
         for (int t = 0; t < R8; ++t) {
-            const int r = r0 + 8 * t + g;
+            const int r = r0 + 8 * t + (TWICE ? g & 3 : g);
             const bool real = r < a.R;
             const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
             const uint16_t *qrow = a.q + ((uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
@@ -529,7 +547,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int rc = r0 + 8 * t + 2 * tig + c;
+                    const int rc = r0 + 8 * t + (TWICE ? (2 * tig + c) & 3 : 2 * tig + c);
                     lim[t][c] = rc < a.R ? len - (a.m - 1 - rc / a.G) : 0;
                     const int u = __shfl_sync(0xffffffffu, up, (2 * tig + c) * 4);
                     qs[t][c] = Q8 ? a.scale2 * __uint_as_float(uint32_t(127 - u) << 23) : a.scale2;
@@ -756,9 +774,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 const float w0 = p[u][t][2 * hf] * sv[u][hf][e], w1 = p[u][t][2 * hf + 1] * sv[u][hf][e];
-                                uint32_t h2, l2;
-                                split_bf16x2(w0, w1, h2, l2);
-                                hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
+                                split_weights<TWICE>(w0, w1, tig, hi[t][hf], lo[t][hf]);
                             }
                         uint32_t v[2][4];  // [token half][dim of the granule's word]
 #pragma unroll
@@ -781,7 +797,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                             for (int k = 0; k < 2; ++k) {
                                 const uint32_t a0 = v[0][2 * k], a1 = v[0][2 * k + 1], a2 = v[1][2 * k], a3 = v[1][2 * k + 1];
                                 mma_bf16(acc[2 * e + k][t], a0, a1, a2, a3, hi[t][0], hi[t][1]);
-                                mma_bf16(acc[2 * e + k][t], a0, a1, a2, a3, lo[t][0], lo[t][1]);
+                                if constexpr (!TWICE) mma_bf16(acc[2 * e + k][t], a0, a1, a2, a3, lo[t][0], lo[t][1]);
                             }
                         if constexpr (V4) {
 #pragma unroll
@@ -815,7 +831,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                                             // the token's weight is with lane row t % 8
                                             const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][2 + c],
                                                                         ((t & 7) << 2) | tig);
-                                            if (t0 + t >= lim[r][c]) continue;
+                                            if (t0 + t >= lim[r][c] || (TWICE && tig >= 2)) continue;
 #pragma unroll
                                             for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -838,11 +854,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
 #pragma unroll
                     for (int t = 0; t < R8; ++t)
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t h2, l2;
-                            split_bf16x2(p[u][t][2 * hf], p[u][t][2 * hf + 1], h2, l2);
-                            hi[t][hf] = transpose8(h2), lo[t][hf] = transpose8(l2);
-                        }
+                        for (int hf = 0; hf < 2; ++hf)
+                            split_weights<TWICE>(p[u][t][2 * hf], p[u][t][2 * hf + 1], tig, hi[t][hf], lo[t][hf]);
 #pragma unroll
                     for (int k = 0; k < MT; ++k) {
                         uint32_t w[4];
@@ -850,7 +863,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
 #pragma unroll
                         for (int t = 0; t < R8; ++t) {
                             mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
-                            mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
+                            if constexpr (!TWICE) mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
                         }
                     }
                 }
@@ -890,6 +903,13 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
             for (int c = 0; c < 2; ++c) {
                 const int rr = 8 * t + 2 * tig + c, r = r0 + rr;
                 const float l = rows_add(sum[t][c]);
+                if constexpr (TWICE) {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            acc[k][t][2 * u + c] += __shfl_xor_sync(0xffffffffu, acc[k][t][2 * u + c], 2);
+                }
                 if constexpr (V4) {
 #pragma unroll
                     for (int e = 0; e < NG; ++e) {
@@ -898,7 +918,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, R8>::WARPS * 32, 1)
                         acc[2 * e + 1][t][c] += z, acc[2 * e + 1][t][2 + c] += z;
                     }
                 }
-                if (r >= a.R) continue;
+                if (r >= a.R || (TWICE && tig >= 2)) continue;
                 const float base2 = ref[t][c];
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
@@ -1067,18 +1087,18 @@ static unsigned attend_grid() { return unsigned(sm_count()); }
 #ifndef PAT_T8
 #define PAT_T8 8
 #endif
-static int tile_rows(int rows) { return rows <= PAT_T8 ? 8 : 16; }
+static int tile_rows(int rows) { return rows <= 4 ? 4 : (rows <= PAT_T8 ? 8 : 16); }
 
-template <int D, int FMT, int R8>
+template <int D, int FMT, int RC>
 static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
-    using SM = PatShape<D, FMT, R8>;
+    using SM = PatShape<D, FMT, RC>;
     const uint32_t bytes = SM::bytes(a.nseq);
     // the opt-in to more than 48 KB, once per device (to the most that any call needs)
     static bool ready[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
     if (dev < 0 || dev >= 64 || !ready[dev]) {
-        if (cudaFuncSetAttribute(pages_attend<D, FMT, R8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(pages_attend<D, FMT, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(SM::bytes(KVP_PAGES_MAX_SEQS))) != cudaSuccess)
             return KVP_ERR_CUDA;
         if (dev >= 0 && dev < 64) ready[dev] = true;
@@ -1095,13 +1115,13 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, R8>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, RC>, a) != cudaSuccess) return KVP_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
     cfg.dynamicSmemBytes = 0;
     // warps for a row's partials: a row has about nwarps / (row tiles) of them
     const bool many = a.nwarps / (unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT)) >= PAT_MANY;
     cfg.blockDim = dim3(many ? 512 : 128);
-    if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, 8 * R8, 16> : pages_join<D, 8 * R8, 4>, a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, RC, 16> : pages_join<D, RC, 4>, a) != cudaSuccess)
         return KVP_ERR_CUDA;
     count_launch(2);
     return launch_status();
@@ -1109,7 +1129,8 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
 
 template <int D, int FMT>
 static int launch_attend(PagesAttendArgs &a, int rows, cudaStream_t st) {
-    return rows == 8 ? launch_attend<D, FMT, 1>(a, st) : launch_attend<D, FMT, 2>(a, st);
+    return rows == 4 ? launch_attend<D, FMT, 4>(a, st)
+                     : (rows == 8 ? launch_attend<D, FMT, 8>(a, st) : launch_attend<D, FMT, 16>(a, st));
 }
 
 static int attend_counts_ok(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {

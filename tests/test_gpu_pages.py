@@ -331,6 +331,11 @@ ATTEND = [  # H, d, page, lens, m, query heads
     (2, 64, 16, [90, 3], 8, 6),
     (1, 64, 1024, [3000], 1, 12),
     (5, 128, 16, [40] * 21, 1, 5),
+    (2, 128, 32, [333, 0, 20], 2, 8),       # 8 rows per KV head
+    (1, 64, 16, [50, 1000], 1, 7),
+    (2, 128, 64, [600, 3, 64], 1, 10),      # 5
+    (1, 128, 16, [48, 47], 3, 2),           # 6
+    (1, 64, 16, [10] * 40 + [0] * 3, 1, 4),  # more sequences than a warp has lanes
 ]
 
 
