@@ -57,37 +57,12 @@
 namespace kvp {
 
 constexpr int PAT_MOST_WARPS = 16;             // of a block
-#ifndef PAT_ITEM_N
-#define PAT_ITEM_N 2
-#endif
-#ifndef PAT_RUN_N
-#define PAT_RUN_N 1
-#endif
-constexpr uint32_t PAT_ITEM = PAT_ITEM_N;               // units that a row tile counts beside its blocks
-constexpr uint32_t PAT_MIN_RUN = PAT_RUN_N;            // units of a warp's run, at least
-constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
+constexpr uint32_t PAT_ITEM = 2;               // units that a row tile counts beside its own
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
+constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
-#ifndef PAT_UB8
-#define PAT_UB8 2
-#endif
-#ifndef PAT_W1V8
-#define PAT_W1V8 12
-#endif
-#ifndef PAT_W1
-#define PAT_W1 12
-#endif
-#ifndef PAT_W2
-#define PAT_W2 8
-#endif
-#ifndef PAT_W64
-#define PAT_W64 16
-#endif
-#ifndef PAT_MANY
-#define PAT_MANY 64
-#endif
 constexpr float PAT_SLACK = 8.0f;
 
 struct PagesAttendArgs {
@@ -265,15 +240,19 @@ __device__ __forceinline__ uint32_t tile_units(int len, int unit) {
 }
 // Units of a warp's run (both kernels).
 __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) {
-    const uint64_t per = (units + nwarps - 1) / nwarps;
-    return per < PAT_MIN_RUN ? PAT_MIN_RUN : per;
+    return units ? (units + nwarps - 1) / nwarps : 1u;
 }
 
-// Warps of a block: as many as the registers of a tile's state allow.
+// The shape of a block.  8- and 4-bit pages at head_dim 128: 12 warps (167
+// registers) with units of two blocks measured 57.9 us on four 32K caches (8
+// warps 62, 16 warps at 128 registers 71 with units of one); 16-row tiles take
+// 250 registers, hence 8 warps, as do 16-bit pages, whose blocks are 8 KB each.
+// At head_dim 64 16 warps, 12 for 16-row tiles (35.8 against 37.0 us with 16,
+// which spill, on 30 4K caches with 16 rows).
 template <int D, int FMT, int RC>
 struct PatShape {
-    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 ? 8 : (RC == 16 ? PAT_W2 : (FMT == KVP_PAGES_K8V8 ? PAT_W1V8 : PAT_W1))) : (RC == 16 ? PAT_W64 : 16);
-    static constexpr int UB = FMT != KVP_PAGES_BF16 && RC <= 8 ? (FMT == KVP_PAGES_K8V8 && D == 128 ? PAT_UB8 : 2) : 1;  // blocks of a unit
+    static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 || RC == 16 ? 8 : 12) : (RC == 16 ? 12 : 16);
+    static constexpr int UB = FMT != KVP_PAGES_BF16 && RC <= 8 ? 2 : 1;  // blocks of a unit
     static constexpr uint32_t SLOT = (UB * Block<D, FMT>::BYTES + 127u) / 128u * 128u;
     static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
     static constexpr uint32_t LEAST = UB == 2 ? 2u : 3u;
@@ -1084,10 +1063,15 @@ static thread_local uint32_t g_next_polls = 0;
 static thread_local bool g_limit_next = false;
 
 static unsigned attend_grid() { return unsigned(sm_count()); }
-#ifndef PAT_T8
-#define PAT_T8 8
-#endif
-static int tile_rows(int rows) { return rows <= 4 ? 4 : (rows <= PAT_T8 ? 8 : 16); }
+// Rows of a tile.  One of 16 rows costs 1.8 of 8 rows with 8- and 4-bit pages
+// (54 against 2 x 30 us for 16 rows on 15 4K caches): an odd number of groups of
+// 8 rows goes in tiles of 8 (20 rows: 39 against 43 us); with 16-bit pages it
+// costs 1.2, so only up to 8 rows do.
+static int tile_rows(int rows, int format) {
+    if (rows <= 4) return 4;
+    const int eights = (rows + 7) / 8;
+    return eights == 1 || (format != KVP_PAGES_BF16 && eights % 2 == 1) ? 8 : 16;
+}
 
 template <int D, int FMT, int RC>
 static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
@@ -1118,8 +1102,11 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, RC>, a) != cudaSuccess) return KVP_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
     cfg.dynamicSmemBytes = 0;
-    // warps for a row's partials: a row has about nwarps / (row tiles) of them
-    const bool many = a.nwarps / (unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT)) >= PAT_MANY;
+    // Warps for a row's partials, of which it has about nwarps / (row tiles): 16
+    // where there are 64 or more of them, 8 a warp in flight (one 128K sequence, 300
+    // partials a row: 71 against 76 us with 4 warps); 4 warps where there are fewer
+    // (a step of 15 agents, 16 partials: 20.0 against 23.8 us with 16).
+    const bool many = a.nwarps / (unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT)) >= 64u;
     cfg.blockDim = dim3(many ? 512 : 128);
     if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, RC, 16> : pages_join<D, RC, 4>, a) != cudaSuccess)
         return KVP_ERR_CUDA;
@@ -1148,7 +1135,7 @@ struct AttendWs {
 };
 static AttendWs attend_ws(const kvp_pages_config *cfg, int n_seqs, int n_q_tokens, int n_q_heads) {
     const uint64_t rows =
-        uint64_t(attend_grid()) * PAT_MOST_WARPS * 2u * uint64_t(tile_rows(n_q_tokens * (n_q_heads / cfg->n_kv_heads)));
+        uint64_t(attend_grid()) * PAT_MOST_WARPS * 2u * uint64_t(tile_rows(n_q_tokens * (n_q_heads / cfg->n_kv_heads), cfg->format));
     AttendWs w;
     w.stats = align256(4ull * uint64_t(n_seqs + 1));
     w.part = w.stats + align256(rows * 8ull);
@@ -1202,7 +1189,7 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
     a.scale2 = scale * 1.4426950408889634f;
     a.nseq = n_seqs, a.m = n_q_tokens, a.nq = n_q_heads, a.G = n_q_heads / cfg->n_kv_heads;
     a.R = n_q_tokens * a.G;
-    const int rows = tile_rows(a.R);
+    const int rows = tile_rows(a.R, cfg->format);
     a.RT = (a.R + rows - 1) / rows;
     a.max_pages = max_pages;
     a.polls = g_limit_next ? g_next_polls : PAT_WAIT_LIMIT;
