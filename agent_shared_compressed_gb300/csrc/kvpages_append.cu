@@ -28,15 +28,9 @@ namespace kvp {
 
 constexpr int APP_THREADS = 256;
 constexpr int APP_WARPS = APP_THREADS / 32;
-#ifndef APP_OCC
-#define APP_OCC 2
-#endif
-#ifndef APP_OCC64
-#define APP_OCC64 4
-#endif
-#ifndef APP_SPLIT
-#define APP_SPLIT 8
-#endif
+// Blocks of an SM: what 117 (head_dim 128) and 64 registers a thread allow.  With
+// three of head_dim 128, at 80 registers, which spill, 8192 tokens took 62 us.
+constexpr int app_blocks(int d) { return d == 128 ? 2 : 4; }
 constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
 
 struct AppendArgs {
@@ -48,6 +42,8 @@ struct AppendArgs {
     uint16_t *q_out, *k_out, *v_out;
     float eps;
     int n, nq, rot;
+    int group_steps, run;  // steps of a token group, of a block
+    int64_t steps;
     uint64_t turn[64];  // w_i / 2 pi mod 1, in units of 2^-64
 };
 
@@ -257,70 +253,85 @@ __device__ __forceinline__ void store_row(uint16_t *row, int tig, const float2 (
     for (int b = 0; b < D / 32; ++b) *reinterpret_cast<uint4 *>(row + 32 * b + 8 * tig) = pack8(x[b]);
 }
 
-// One block: APP_TOKENS tokens and a share of the nq query, H key and H value
-// rows of each, a warp at a time.  A row's loads are
-// issued while the row before it is worked on: the kernel is bound by memory
-// latency, then by memory.
+// The work is a list of steps: a group of APP_TOKENS tokens has one for every
+// APP_WARPS of its nq query, H key and H value rows (a warp takes a row of all of
+// the group's tokens).  A block takes an equal run of the list, as many blocks as
+// the GPU holds at once: there is no last, half-empty wave (8192 tokens: 47.5
+// against 51.2 us with a block per group).  A row's loads are issued while the row
+// before it is worked on.
 template <int D, int FMT>
-__global__ void __launch_bounds__(APP_THREADS, D == 128 ? APP_OCC : APP_OCC64) pages_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const __grid_constant__ AppendArgs a) {
     using B = Block<D, FMT>;
     constexpr int NB = D / 32;
     // rows padded to start on other banks; read as float4
     __shared__ __align__(16) float cosines[APP_TOKENS][D / 2 + 4], sines[APP_TOKENS][D / 2 + 4], norm[2][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
-    const int64_t t0 = int64_t(blockIdx.x) * APP_TOKENS;
-    const int64_t tok = t0 + tq;
-    const bool real = tok < a.n;
-    const int H = a.pv.H, r1 = a.nq + 2 * H;
-    // the blocks of a token group take every gridDim.y-th row: an equal mix of kinds
-    const int step = int(gridDim.y) * APP_WARPS;
-    int r = int(blockIdx.y) + int(gridDim.y) * warp;
-    auto load = [&](int row, uint4 (&v)[NB]) {
+    const int H = a.pv.H, rows = a.nq + 2 * H;
+    const int64_t first = int64_t(blockIdx.x) * a.run;
+    int left = int(min(int64_t(a.run), a.steps - first));  // steps of this block
+    int64_t grp = first / a.group_steps;
+    int st = int(first % a.group_steps);
+    auto load = [&](int64_t g, int s, uint4 (&v)[NB]) {
+        const int64_t tok = g * APP_TOKENS + tq;
+        const int row = s * APP_WARPS + warp;
         const bool is_q = row < a.nq, is_v = row >= a.nq + H;
         const uint16_t *src = is_q ? a.q + tok * a.q_ts + row * a.q_hs
                                    : (is_v ? a.v + tok * a.v_ts + (row - a.nq - H) * a.v_hs
                                            : a.k + tok * a.k_ts + (row - a.nq) * a.k_hs);
+        const bool real = row < rows && tok < a.n;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-            v[b] = real && row < r1 ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < NB; ++b) v[b] = real ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
     };
     uint4 in[NB];
-    load(r, in);
-    const int64_t slot = real ? a.slots[tok] : -1;
+    load(grp, st, in);
     const bool match = pages_match(a.pv);
-    if (a.rot > 0) {
-        for (int i = threadIdx.x; i < APP_TOKENS * (a.rot / 2); i += APP_THREADS) {
-            const int t = i / (a.rot / 2), p = i % (a.rot / 2);
-            float s = 0.0f, c = 1.0f;
-            if (t0 + t < a.n) {
-                const int64_t turns = int64_t(uint64_t(a.positions[t0 + t]) * a.turn[p]);  // mod one turn
-                sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
-            }
-            cosines[t][p] = c, sines[t][p] = s;
-        }
-    }
     for (int i = threadIdx.x; i < 2 * D; i += APP_THREADS) {
         const uint16_t *w = i < D ? a.q_norm : a.k_norm;
         norm[i / D][i % D] = w ? __uint_as_float(uint32_t(w[i % D]) << 16) : 1.0f;
     }
-    __syncthreads();
+    int64_t tok = 0;
+    bool real = false, fresh = true;
     uint8_t *blk = nullptr;  // the token's block of head 0
     uint32_t row16 = 0, bad = match ? 0u : FLAG_HEADER;
-    if (slot >= (int64_t(a.pv.n_pages) << a.pv.logP)) {
-        bad |= FLAG_PAGE;
-    } else if (match && slot >= 0) {
-        const int64_t page = slot >> a.pv.logP;
-        const uint32_t at = uint32_t(slot) & uint32_t(a.pv.P - 1);
-        blk = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(at / PAGES_BLOCK) * B::BYTES;
-        row16 = at % PAGES_BLOCK;
-    }
-    for (; r < r1; r += step) {
-        const bool is_q = r < a.nq, is_v = r >= a.nq + H;
-        const int h = is_q ? r : (is_v ? r - a.nq - H : r - a.nq);
+    for (; left > 0; --left) {
+        if (fresh) {  // a new group: its angles, and the places of its tokens
+            fresh = false;
+            __syncthreads();
+            tok = grp * APP_TOKENS + tq;
+            real = tok < a.n;
+            const int64_t slot = real ? a.slots[tok] : -1;
+            if (a.rot > 0) {
+                for (int i = threadIdx.x; i < APP_TOKENS * (a.rot / 2); i += APP_THREADS) {
+                    const int t = i / (a.rot / 2), p = i % (a.rot / 2);
+                    const int64_t at = grp * APP_TOKENS + t;
+                    float s = 0.0f, c = 1.0f;
+                    if (at < a.n) {
+                        const int64_t turns = int64_t(uint64_t(a.positions[at]) * a.turn[p]);  // mod one turn
+                        sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
+                    }
+                    cosines[t][p] = c, sines[t][p] = s;
+                }
+            }
+            blk = nullptr;
+            if (slot >= (int64_t(a.pv.n_pages) << a.pv.logP)) {
+                bad |= FLAG_PAGE;
+            } else if (match && slot >= 0) {
+                const int64_t page = slot >> a.pv.logP;
+                const uint32_t at = uint32_t(slot) & uint32_t(a.pv.P - 1);
+                blk = a.pv.layer + uint64_t(page) * a.pv.page_bytes + uint64_t(at / PAGES_BLOCK) * B::BYTES;
+                row16 = at % PAGES_BLOCK;
+            }
+            __syncthreads();
+        }
+        const int r = st * APP_WARPS + warp;
+        if (++st == a.group_steps) st = 0, ++grp, fresh = true;
         float2 x[NB][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) unpack8(in[b], x[b]);
-        load(r + step, in);
+        if (left > 1) load(grp, st, in);
+        if (r >= rows) continue;
+        const bool is_q = r < a.nq, is_v = r >= a.nq + H;
+        const int h = is_q ? r : (is_v ? r - a.nq - H : r - a.nq);
         uint8_t *hb = blk ? blk + uint64_t(h) * a.pv.tile_bytes : nullptr;
         if (!is_v) {
             if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
@@ -527,7 +538,7 @@ static uint64_t turn_fraction(float w) {
 }
 
 template <int D, int FMT>
-static int launch_append(const AppendArgs &a, dim3 grid, cudaStream_t st) {
+static int launch_append(const AppendArgs &a, unsigned grid, cudaStream_t st) {
     pages_append<D, FMT><<<grid, APP_THREADS, 0, st>>>(a);
     count_launch();
     return launch_status();
@@ -595,13 +606,12 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
     a.k_out = static_cast<uint16_t *>(k_out), a.v_out = static_cast<uint16_t *>(v_out);
     a.eps = eps, a.n = n_tokens, a.nq = n_q_heads, a.rot = rot_dim;
     for (int i = 0; i < 64; ++i) a.turn[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
-    // Blocks of a token group: one where the groups alone fill the GPU (the
-    // angles are formed once a block), else up to one row per warp.
     const int rows = n_q_heads + 2 * cfg->n_kv_heads;
-    const int groups = int((int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS);
-    const int steps = (rows + APP_WARPS - 1) / APP_WARPS;
-    const int split = std::max(1, std::min(steps, APP_SPLIT * sm_count() / std::max(groups, 1)));
-    const dim3 grid{unsigned(groups), unsigned(split)};
+    a.group_steps = (rows + APP_WARPS - 1) / APP_WARPS;
+    a.steps = (int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS * a.group_steps;
+    const int64_t blocks = std::min<int64_t>(a.steps, int64_t(sm_count()) * app_blocks(cfg->head_dim));
+    a.run = int((a.steps + blocks - 1) / blocks);
+    const unsigned grid = unsigned((a.steps + a.run - 1) / a.run);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool d128 = cfg->head_dim == 128;
     switch (cfg->format) {
