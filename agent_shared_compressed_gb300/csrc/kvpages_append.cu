@@ -47,6 +47,14 @@ struct AppendArgs {
     uint64_t turn[64];  // w_i / 2 pi mod 1, in units of 2^-64
 };
 
+// The kernels here are placed while the one before them in the stream still runs
+// (a programmatic dependent launch): they read and write nothing before its end.
+// Then the next one may be placed.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float quad_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -282,6 +290,7 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
 #pragma unroll
         for (int b = 0; b < NB; ++b) v[b] = real ? ld_stream_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
     };
+    wait_for_previous();
     uint4 in[NB];
     load(grp, st, in);
     const bool match = pages_match(a.pv);
@@ -439,6 +448,7 @@ __global__ void __launch_bounds__(256) pages_read(const __grid_constant__ ReadAr
     using B = Block<D, FMT>;
     constexpr int NB = D / 32;
     const int lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
+    wait_for_previous();
     if (!pages_match(a.pv)) {
         if (threadIdx.x == 0) pages_flag(a.pv, FLAG_HEADER);
         return;
@@ -537,17 +547,28 @@ static uint64_t turn_fraction(float w) {
     return w < 0.0f ? 0u - r : r;
 }
 
-template <int D, int FMT>
-static int launch_append(const AppendArgs &a, unsigned grid, cudaStream_t st) {
-    pages_append<D, FMT><<<grid, APP_THREADS, 0, st>>>(a);
+template <typename Args>
+static int launch(void (*kernel)(Args), const Args &a, unsigned grid, unsigned threads, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return KVP_ERR_CUDA;
     count_launch();
     return launch_status();
 }
 template <int D, int FMT>
+static int launch_append(const AppendArgs &a, unsigned grid, cudaStream_t st) {
+    return launch(pages_append<D, FMT>, a, grid, APP_THREADS, st);
+}
+template <int D, int FMT>
 static int launch_read(const ReadArgs &a, unsigned grid, cudaStream_t st) {
-    pages_read<D, FMT><<<grid, 256, 0, st>>>(a);
-    count_launch();
-    return launch_status();
+    return launch(pages_read<D, FMT>, a, grid, 256, st);
 }
 
 static bool rows_aligned(const kvp_rows *r) {
