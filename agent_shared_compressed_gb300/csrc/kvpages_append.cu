@@ -663,7 +663,9 @@ int kvpages_read(const void *pages, const kvp_pages_config *cfg, int layer, int 
     a.nseq = n_seqs, a.max_pages = max_pages, a.tmax = max_tokens;
     a.nblk = int((int64_t(max_tokens) + PAGES_BLOCK - 1) / PAGES_BLOCK);
     a.tasks = uint64_t(n_seqs) * uint64_t(cfg->n_kv_heads) * uint64_t(a.nblk);
-    const unsigned grid = unsigned(std::min<uint64_t>((a.tasks + 7) / 8, uint64_t(sm_count()) * 8));
+    // two to three waves of blocks: 15 4K caches 61.3 us, 64.5 with 8 blocks an SM (about
+    // one wave); 7 ragged ones 23.7 us, 24.8 with 32
+    const unsigned grid = unsigned(std::min<uint64_t>((a.tasks + 7) / 8, uint64_t(sm_count()) * 16));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool d128 = cfg->head_dim == 128;
     switch (cfg->format) {
