@@ -158,13 +158,14 @@ def declared_functions(header=HEADER):
 # --- marshalling helpers ---------------------------------------------------
 
 def _addr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    raise TypeError("expected a tensor, an int address or None, got %r" % type(x))
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        raise TypeError("expected a tensor, an int address or None, got %r" % type(x)) from None
 
 
 def _ptrs(seq):
@@ -292,13 +293,13 @@ def cachecard_status(card, stream=None):
 
 
 def _pages(c):
-    return c if isinstance(c, PagesConfig) else PagesConfig(*c)
+    return c if c.__class__ is PagesConfig else PagesConfig(*c)
 
 
 def rows(x, token_stride=None, head_stride=None):
     """kvp_rows of a [tokens][heads][head_dim] bf16 tensor (a strided view will
     do; its last dimension contiguous), or of an address with its strides."""
-    if x is None or isinstance(x, Rows):
+    if x is None or x.__class__ is Rows:
         return x
     if token_stride is not None:
         return Rows(_addr(x), token_stride, head_stride)
@@ -308,8 +309,11 @@ def rows(x, token_stride=None, head_stride=None):
     return Rows(x.data_ptr(), t, h)
 
 
+_addressof = C.addressof
+
+
 def _ref(x):
-    return None if x is None else C.addressof(x)
+    return None if x is None else _addressof(x)
 
 
 def _floats(x):

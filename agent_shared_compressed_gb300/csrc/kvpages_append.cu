@@ -21,6 +21,7 @@
 // fp64 instructions an angle, and this GPU's fp64 rate is low.)
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "kvp_pages.cuh"
 
@@ -529,22 +530,22 @@ __global__ void pages_init(uint32_t *h, const __grid_constant__ kvp_pages_config
 // times the first 128 bits of 1 / 2 pi's binary fraction, shifted by its exponent.
 static uint64_t turn_fraction(float w) {
     constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;  // 1 / 2 pi * 2^128
-    if (w == 0.0f) return 0;
-    int e;
-    const double f = std::frexp(std::fabs(double(w)), &e);     // f in [1/2, 1)
-    const uint64_t m = uint64_t(std::ldexp(f, 24));            // w = m 2^(e - 24), exactly
+    uint32_t bits;
+    std::memcpy(&bits, &w, 4);
+    const int ex = int(bits >> 23 & 255u);
+    const uint64_t m = (bits & 0x7FFFFFu) | (ex ? 0x800000u : 0u);  // |w| = m 2^(max(ex, 1) - 150)
     // m / 2 pi = p 2^-128 with p of 152 bits, as three 64-bit words
     const unsigned __int128 p0 = (unsigned __int128)m * LO, p1 = (unsigned __int128)m * HI + (p0 >> 64);
     const uint64_t word[3] = {uint64_t(p0), uint64_t(p1), uint64_t(p1 >> 64)};
-    // the turn's 64-bit fraction: bits [s, s + 64) of p, s = 64 - (e - 24)
-    const int s = 88 - e;
+    // the turn's 64-bit fraction: bits [s, s + 64) of p, s = 64 - (max(ex, 1) - 150)
+    const int s = 214 - (ex ? ex : 1);
     uint64_t r = 0;
     for (int i = 0; i < 3; ++i) {
         const int at = 64 * i - s;  // where the word's bit 0 lands
         if (at >= 0 && at < 64) r |= word[i] << at;
         if (at < 0 && at > -64) r |= word[i] >> -at;
     }
-    return w < 0.0f ? 0u - r : r;
+    return bits >> 31 ? 0u - r : r;
 }
 
 template <typename Args>
