@@ -656,23 +656,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         for (int e = 0; e < 4; ++e)
                             if (t0 + 16 * u + g + 8 * (e >> 1) >= lim[t][e & 1] || !((here >> u) & 1u)) x[u][t][e] = -INFINITY;
             }
-            // value scales of tokens g and g + 8 of each block
-            float sv[UB][2][Q8 ? NG : 1], zv[UB][2][V4 ? NG : 1];
             bool raise = false;
-            if constexpr (Q8) {
-#pragma unroll
-                for (int u = 0; u < UB; ++u)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        if constexpr (V4) {
-                            const uint32_t pa = prep + 4u * NG * uint32_t(16 * u + 8 * hf + g);
-                            lds_floats<NG>(pa, sv[u][hf]);
-                            lds_floats<NG>(pa + 4u * UB * SM::NE, zv[u][hf]);
-                        } else {
-                            lds_halfs<NG>(at0 + uint32_t(u) * B::BYTES + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[u][hf]);
-                        }
-                    }
-            }
             float top[R8][2];
 #pragma unroll
             for (int t = 0; t < R8; ++t)
@@ -715,6 +699,17 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
             for (int u = 0; u < UB; ++u) {
                 const uint32_t at = at0 + uint32_t(u) * B::BYTES;
                 if constexpr (Q8) {
+                    float sv[2][NG], zv[2][V4 ? NG : 1];  // value scales of tokens g and g + 8
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if constexpr (V4) {
+                            const uint32_t pa = prep + 4u * NG * uint32_t(16 * u + 8 * hf + g);
+                            lds_floats<NG>(pa, sv[hf]);
+                            lds_floats<NG>(pa + 4u * UB * SM::NE, zv[hf]);
+                        } else {
+                            lds_halfs<NG>(at + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[hf]);
+                        }
+                    }
                     uint32_t vw[2][2][V4 ? NG / 2 : NG];  // [token half][odd token]: the lane's granule
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
@@ -752,7 +747,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         for (int t = 0; t < R8; ++t)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
-                                const float w0 = p[u][t][2 * hf] * sv[u][hf][e], w1 = p[u][t][2 * hf + 1] * sv[u][hf][e];
+                                const float w0 = p[u][t][2 * hf] * sv[hf][e], w1 = p[u][t][2 * hf + 1] * sv[hf][e];
                                 split_weights<TWICE>(w0, w1, tig, hi[t][hf], lo[t][hf]);
                             }
                         uint32_t v[2][4];  // [token half][dim of the granule's word]
@@ -783,7 +778,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                             for (int t = 0; t < R8; ++t)
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
-                                    zsum[e][t][c & 1] = fmaf(p[u][t][c], zv[u][c >> 1][e], zsum[e][t][c & 1]);
+                                    zsum[e][t][c & 1] = fmaf(p[u][t][c], zv[c >> 1][e], zsum[e][t][c & 1]);
                         }
                     }
                 } else {
