@@ -1169,9 +1169,9 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
         return KVP_ERR_ALIGN;
     const AttendWs w = attend_ws(cfg, n_seqs, n_q_tokens, n_q_heads);
     if (ws_bytes < w.total) return KVP_ERR_SIZE;
-    // block counts are 32-bit
+    // unit counts are 32-bit
     const unsigned __int128 blocks = (unsigned __int128)uint32_t(max_pages) * uint32_t(cfg->page_tokens / 16) * uint32_t(n_seqs);
-    if (blocks >> 32) return KVP_ERR_SIZE;
+    if (blocks >> 31) return KVP_ERR_SIZE;
     if (n_seqs == 0) return KVP_OK;
     PagesAttendArgs a;
     a.pv = pages_view(const_cast<void *>(pages), *cfg, layer);

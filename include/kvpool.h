@@ -460,7 +460,7 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  *  q: device bf16 [n_seqs][n_q_tokens][n_q_heads][head_dim]; query head j reads
  *    KV head j / (n_q_heads / n_kv_heads).
  *  table, max_pages, lens: as kvpages_read; n_seqs at most KVP_PAGES_MAX_SEQS,
- *    and n_seqs * max_pages * page_tokens below 2^36.
+ *    and n_seqs * max_pages * page_tokens below 2^35.
  *  base_out, base_lse: device fp32 [n_seqs][n_q_tokens][n_q_heads]([head_dim]),
  *    both or neither (NULL): attention of the same queries over other tokens,
  *    as kvpool_attend leaves it.  The result is then attention over both.

@@ -618,3 +618,74 @@ def test_masked_draft_tokens_with_infinities(d):
     ref, _, mass, _ = P.attend(_f64(q), [_f64(k)], [_f64(full)], [n], 0.1)
     assert np.all(np.abs(out[0, 2:, :2][..., keep] - ref[0, 2:, :2][..., keep])
                   <= 2.0 ** -8 * np.abs(ref[0, 2:, :2][..., keep]) + 2.0 ** -10 * mass[0, 2:, :2][..., keep])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_example_agent_decode(fmt):
+    """The example's decode steps (pool, own pages, joined) against dense
+    attention over the decoded caches.  Their bf16 keys move a score by up to
+    2^-8 of sum |q k| (here below 0.4 where weights matter), their values and the
+    output round to 2^-8."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "agent_decode.py")
+    spec = importlib.util.spec_from_file_location("agent_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, us = mod.run(agents=3, layers=2, heads=8, kv_heads=2, dim=128, pool_tokens=200, steps=20, fmt=fmt, check=True)
+    assert worst < 0.02 and us > 0
+
+
+@pytest.mark.parametrize("fmt,n,d", [("k8v8", 200, 128), ("k8v4", 700, 64), ("bf16", 4096, 64)])
+def test_many_sequences(fmt, n, d):
+    """More sequences than a thread block sums at once, up to the most of a call."""
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, 21 if n > 1000 else 60, n)]
+    pg = Pages(fmt, 1, d, 16, lens, seed=1)
+    k, v = _kv(sum(lens), 1, d, 20)
+    pg.append(k, v, outs=False)
+    q = torch.randn(n, 1, 2, d, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.11)
+    _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), fmt, False), lens), _split(P.held(_f64(v), fmt, True), lens),
+                  lens, 0.11)
+    assert pg.status() == kv.KVP_OK
+
+
+def test_norm_of_queries_or_keys_alone():
+    H, nq, d, n = 2, 4, 128, 21
+    g = torch.Generator().manual_seed(22)
+    q, k = (torch.randn(n, h, d, generator=g).to(torch.bfloat16).cuda() for h in (nq, H))
+    w = (0.5 + torch.rand(d, generator=g)).to(torch.bfloat16).cuda()
+    for qn, kn in ((w, None), (None, w)):
+        pg = Pages("bf16", H, d, 16, [n])
+        qo, ko, _ = pg.append(k, k, q=q, q_norm=qn, k_norm=kn, eps=1e-6)
+        for got, x, ww in ((qo, q, qn), (ko, k, kn)):
+            ref = P.heads(_f64(x), None if ww is None else _f64(ww), 1e-6, None, None, 0)
+            assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -10) if ww is not None else got == ref)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two streams attend over one container at the same time, with workspaces
+    and batches of their own; results are those of the calls one by one."""
+    H, nq, d, lens = 4, 16, 128, [3000, 17, 900, 1]
+    k, v = _kv(sum(lens), H, d, 23)
+    pg = Pages("k8v8", H, d, 32, lens)
+    pg.append(k, v, outs=False)
+    g = torch.Generator().manual_seed(4)
+    qs = [torch.randn(4, m, nq, d, generator=g).to(torch.bfloat16).cuda() for m in (1, 3)]
+    alone = [pg.attend(q, 0.1) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    bufs = []
+    for q in qs:
+        wsb = kv.kvpages_attend_workspace_bytes(pg.cfg, 4, q.shape[1], nq)
+        bufs.append([(torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")) for _ in range(20)]
+                    + [torch.empty(wsb, dtype=torch.uint8, device="cuda")])
+    torch.cuda.synchronize()
+    for i in range(20):
+        for q, st, b in zip(qs, streams, bufs):
+            assert kv.kvpages_attend(pg.buf.t, pg.cfg, 0, 4, q.shape[1], nq, q, 0.1, pg.table_d, pg.max_pages, pg.lens_d,
+                                     None, None, b[i][0], b[i][1], b[-1], b[-1].numel(), st) == 0
+    torch.cuda.synchronize()
+    for (out, lse), b in zip(alone, bufs):
+        for o, ls in b[:-1]:
+            assert np.array_equal(_f64(o), out) and np.array_equal(ls.cpu().numpy().astype(np.float64), lse)

@@ -117,7 +117,7 @@ def test_attend_refusals():
     assert call(w=None) == call(bo=OK) == call(bl=OK) == kv.KVP_ERR_ARG
     assert call(scale=float("nan")) == call(scale=float("inf")) == kv.KVP_ERR_ARG
     assert call(m=65) == call(n=kv.KVP_PAGES_MAX_SEQS + 1) == call(wb=ws - 1) == kv.KVP_ERR_SIZE
-    assert call(mp=2 ** 31 - 1) == kv.KVP_ERR_SIZE                     # 2^36 tokens or more
+    assert call(mp=2 ** 31 - 1) == kv.KVP_ERR_SIZE                     # 2^35 tokens or more
     for bad in (dict(pages=OK + 128), dict(q=OK + 8), dict(table=OK + 2), dict(lens=OK + 2), dict(out=OK + 8),
                 dict(lse=OK + 2), dict(w=OK + 8), dict(bo=OK + 8, bl=OK), dict(bo=OK, bl=OK + 2)):
         assert call(**bad) == kv.KVP_ERR_ALIGN, bad
