@@ -64,6 +64,7 @@ constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
 constexpr float PAT_SLACK = 8.0f;
+constexpr int64_t PAT_SOLO_TOKENS = 768;  // most tokens that a table may hold where a block takes a whole row tile
 
 struct PagesAttendArgs {
     PagesView pv;
@@ -268,6 +269,62 @@ struct PatShape {
     static uint32_t bytes(int nseq) { return OFF_PLAN + 4u * uint32_t(nseq + 1); }
 };
 
+// Units before each sequence (of one row tile), in shared memory and, for pages_join,
+// in the plan; returns their sum.  Up to 32 sequences, every warp finds them by itself
+// (all write the same values).
+__device__ __forceinline__ uint32_t make_plan(const PagesAttendArgs &a, uint32_t *pre, uint32_t *wsum, int unit, int threads) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads / 32;
+    uint32_t carry = 0;
+    if (a.nseq <= 32) {
+        uint32_t n = lane < a.nseq ? tile_units(seq_len(a, lane, blockIdx.x == 0 && warp == 0), unit) : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += y;
+        }
+        carry = __shfl_sync(0xffffffffu, n, 31);
+        if (lane < a.nseq) {
+            pre[lane + 1] = n;
+            if (blockIdx.x == 0 && warp == 0) a.plan[lane + 1] = n;
+        }
+        if (lane == 0) {
+            pre[0] = 0u;
+            if (blockIdx.x == 0 && warp == 0) a.plan[0] = 0u;
+        }
+        __syncwarp();
+    }
+    for (int b0 = 0; a.nseq > 32 && b0 < a.nseq; b0 += threads) {
+        const int b = b0 + tid;
+        uint32_t n = b < a.nseq ? tile_units(seq_len(a, b, blockIdx.x == 0), unit) : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += y;
+        }
+        if (lane == 31) wsum[warp] = n;
+        __syncthreads();
+        uint32_t before = carry;
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t s = wsum[w];
+            before += w < warp ? s : 0u;
+            carry += s;
+        }
+        if (b < a.nseq) {
+            pre[b + 1] = before + n;
+            if (blockIdx.x == 0) a.plan[b + 1] = before + n;
+        }
+        __syncthreads();
+    }
+    if (a.nseq > 32) {
+        if (tid == 0) {
+            pre[0] = 0u;
+            if (blockIdx.x == 0) a.plan[0] = 0u;
+        }
+        __syncthreads();
+    }
+    return carry;
+}
+
 // What one row of a tile ends with: the base joined in, bf16 output and lse.
 __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t row, float lse, bool first) {
     // weights of (this, base); an empty row without a base has none
@@ -287,7 +344,10 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
 // RC: query rows of a tile (4, 8 or 16).  A tile of 4 has its rows in columns
 // 0..3 and again in 4..7: the weights' first bf16 in the former, the second in
 // the latter, so that one value product does for both.
-template <int D, int FMT, int RC>
+//
+// SOLO: a thread block takes one row tile, its warps equal parts of the tile's
+// units, merged in shared memory: no list, no partial results, no join.
+template <int D, int FMT, int RC, bool SOLO>
 __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     pages_attend(const __grid_constant__ PagesAttendArgs a) {
     using B = Block<D, FMT>;
@@ -311,71 +371,35 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     // the kernel before this one has completed past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool match = pages_match(a.pv);
-    // units before each sequence (of one row tile); up to 32 sequences, every warp
-    // finds them by itself (all write the same values)
-    uint32_t carry = 0;
-    if (a.nseq <= 32) {
-        uint32_t n = lane < a.nseq ? tile_units(seq_len(a, lane, blockIdx.x == 0 && warp == 0), 16 * UB) : 0u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
-            if (lane >= o) n += y;
-        }
-        carry = __shfl_sync(0xffffffffu, n, 31);
-        if (lane < a.nseq) {
-            pre[lane + 1] = n;
-            if (blockIdx.x == 0 && warp == 0) a.plan[lane + 1] = n;
-        }
-        if (lane == 0) {
-            pre[0] = 0u;
-            if (blockIdx.x == 0 && warp == 0) a.plan[0] = 0u;
-        }
-        __syncwarp();
-    }
-    for (int b0 = 0; a.nseq > 32 && b0 < a.nseq; b0 += THREADS) {
-        const int b = b0 + tid;
-        uint32_t n = b < a.nseq ? tile_units(seq_len(a, b, blockIdx.x == 0), 16 * UB) : 0u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, n, o);
-            if (lane >= o) n += y;
-        }
-        if (lane == 31) wsum[warp] = n;
-        __syncthreads();
-        uint32_t before = carry;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const uint32_t s = wsum[w];
-            before += w < warp ? s : 0u;
-            carry += s;
-        }
-        if (b < a.nseq) {
-            pre[b + 1] = before + n;
-            if (blockIdx.x == 0) a.plan[b + 1] = before + n;
-        }
-        __syncthreads();
-    }
-    if (a.nseq > 32) {
-        if (tid == 0) {
-            pre[0] = 0u;
-            if (blockIdx.x == 0) a.plan[0] = 0u;
-        }
-        __syncthreads();
+    const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
+    // SOLO: the block's sequence and row tile, and the tile's units
+    const int sb = SOLO ? int(blockIdx.x / HRT) : 0;
+    const uint32_t stile = SOLO ? blockIdx.x % HRT : 0u;
+    uint32_t solo_units = 0, carry = 0;
+    if constexpr (SOLO) {
+        const uint32_t n = tile_units(seq_len(a, sb, stile == 0), 16 * UB);
+        solo_units = n ? n - PAT_ITEM : 0u;
+    } else {
+        carry = make_plan(a, pre, wsum, 16 * UB, THREADS);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!match) {
         if (tid == 0) pages_flag(a.pv, FLAG_HEADER);
         return;
     }
-    const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
-    const uint64_t units = uint64_t(carry) * HRT, per = run_length(units, a.nwarps);
+    const uint64_t units = SOLO ? solo_units : uint64_t(carry) * HRT;
+    const uint64_t per = run_length(units, SOLO ? uint32_t(WARPS) : a.nwarps);
     const uint32_t gw = blockIdx.x * WARPS + uint32_t(warp);
-    const uint64_t f0 = gw * per;
-    if (f0 >= units) return;
-    const uint32_t cnt = uint32_t(f0 + per < units ? per : units - f0);
+    const uint64_t f0 = (SOLO ? uint32_t(warp) : gw) * per;
+    const uint32_t cnt = f0 >= units ? 0u : uint32_t(f0 + per < units ? per : units - f0);
+    if (cnt == 0u && !SOLO) return;
 
     // unit f: its sequence, row tile and place in the tile (PAT_ITEM empty places, then the blocks)
     auto locate = [&](uint64_t f, int &b, uint32_t &tile, uint32_t &at) {
+        if constexpr (SOLO) {
+            b = sb, tile = stile, at = uint32_t(f) + PAT_ITEM;
+            return;
+        }
         const uint32_t p = (f >> 32) == 0 ? uint32_t(f) / HRT : uint32_t(f / HRT);
         int lo = 0, hi = a.nseq - 1;  // the last b with pre[b] <= p
         while (lo < hi) {
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (fresh) {
             fresh = false;
             seg0 = place;
-            nplace = pre[b + 1] - pre[b];
+            nplace = SOLO ? solo_units + PAT_ITEM : pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
             const int r0 = int(tile) % a.RT * RTILE;
 #pragma unroll
@@ -558,7 +582,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     if (++s == STAGES) s = 0, p ^= 1u;
                 }
             }
-            return;
+            break;
         }
         const uint32_t here = (good >> (n % GU * UB)) & (UB == 2 ? 3u : 1u);
         if (here) {
@@ -861,14 +885,14 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         // the segment's end; the next one's queries are requested first
         int nb = b;
         uint32_t ntile = tile;
-        if (place == nplace && ++ntile == HRT) {
+        if (!SOLO && place == nplace && ++ntile == HRT) {
             ntile = 0;
             do ++nb;
             while (nb < a.nseq && pre[nb + 1] == pre[nb]);
         }
         if (n + 1 < cnt) load_queries(nb, ntile);
         const int h = int(tile) / a.RT, r0 = int(tile) % a.RT * RTILE;
-        const bool whole = seg0 == 0 && place == nplace;
+        const bool whole = SOLO ? cnt == solo_units : seg0 == 0 && place == nplace;
         // slot 0: the segment that the run starts with; 1: its last
         const uint64_t ps = (uint64_t(gw) * 2u + (n + 1 == place - seg0 ? 0u : 1u)) * RTILE;
 #pragma unroll
@@ -927,7 +951,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                             }
                     }
                 } else {
-                    float *o = a.part + (ps + uint32_t(rr)) * D;
+                    // SOLO: in the warp's own ring, whose copies have all been used
+                    float *mine = reinterpret_cast<float *>(sm + PAT_BAR_BYTES + uint32_t(warp) * STAGES * SM::SLOT);
+                    float *o = SOLO ? mine + rr * D : a.part + (ps + uint32_t(rr)) * D;
                     if constexpr (Q8) {
 #pragma unroll
                         for (int e = 0; e < NG; ++e)
@@ -939,12 +965,53 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) o[16 * k + 8 * u + g] = acc[k][t][2 * u + c];
                     }
-                    if (g == 0) a.stats[ps + uint32_t(rr)] = make_float2(base2, l);
+                    if (g == 0) {
+                        float2 *st = SOLO ? reinterpret_cast<float2 *>(mine + RTILE * D) + rr : a.stats + ps + uint32_t(rr);
+                        *st = make_float2(base2, l);
+                    }
                 }
             }
         fresh = true;
         if (place == nplace) place = 0;
         b = nb, tile = ntile;
+    }
+    if constexpr (!SOLO) return;
+
+    // The tile's rows, a warp at a time: its warps' parts, in order
+    static_assert(RTILE * (D * 4 + 8) <= STAGES * SM::SLOT, "a warp's part fits its ring");
+    __syncthreads();
+    const uint32_t parts = uint32_t((units + per - 1) / per);
+    if (parts == 1u) return;  // written by the warp that had it all
+    const int h = int(stile) / a.RT, r0 = int(stile) % a.RT * RTILE;
+    for (int rr = warp; rr < min(RTILE, a.R - r0); rr += WARPS) {
+        constexpr int VPL = D / 32;
+        float y[VPL], M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) y[k] = 0.0f;
+        const uint8_t *part = sm + PAT_BAR_BYTES;
+        for (uint32_t w = 0; w < parts; ++w)
+            M = fmaxf(M, reinterpret_cast<const float2 *>(part + w * STAGES * SM::SLOT + RTILE * D * 4)[rr].x);
+        for (uint32_t w = 0; w < parts; ++w) {
+            const float *src = reinterpret_cast<const float *>(part + w * STAGES * SM::SLOT);
+            const float2 st = reinterpret_cast<const float2 *>(src + RTILE * D)[rr];
+            const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - M);
+            L = fmaf(f, st.y, L);
+#pragma unroll
+            for (int k = 0; k < VPL; ++k) y[k] = fmaf(f, src[rr * D + lane * VPL + k], y[k]);
+        }
+        const int r = r0 + rr, i = r / a.G, j = h * a.G + r - i * a.G;
+        const uint64_t row = (uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+        const float lse = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.0f ? -INFINITY : L);
+        const float2 w = join_base(a, row, lse, lane == 0);
+        const float inv = L > 0.0f ? w.x / L : (L == 0.0f ? 0.0f : L);
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            y[k] *= inv;
+            if (a.base_out && w.y != 0.0f) y[k] = fmaf(w.y, a.base_out[row * D + lane * VPL + k], y[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < VPL; k += 2)
+            *reinterpret_cast<uint32_t *>(a.out + row * D + lane * VPL + k) = pack_bf16x2(y[k], y[k + 1]);
     }
 }
 
@@ -1068,44 +1135,61 @@ static int tile_rows(int rows, int format) {
     return eights == 1 || (format != KVP_PAGES_BF16 && eights % 2 == 1) ? 8 : 16;
 }
 
-template <int D, int FMT, int RC>
-static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
+template <int D, int FMT, int RC, bool SOLO>
+static int launch_tiles(cudaLaunchConfig_t &cfg, const PagesAttendArgs &a, unsigned grid) {
     using SM = PatShape<D, FMT, RC>;
-    const uint32_t bytes = SM::bytes(a.nseq);
     // the opt-in to more than 48 KB, once per device (to the most that any call needs)
     static bool ready[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
     if (dev < 0 || dev >= 64 || !ready[dev]) {
-        if (cudaFuncSetAttribute(pages_attend<D, FMT, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(pages_attend<D, FMT, RC, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(SM::bytes(KVP_PAGES_MAX_SEQS))) != cudaSuccess)
             return KVP_ERR_CUDA;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(SM::WARPS * 32);
+    cfg.dynamicSmemBytes = SM::bytes(SOLO ? 0 : a.nseq);
+    if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, RC, SOLO>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    count_launch();
+    return KVP_OK;
+}
+
+template <int D, int FMT, int RC>
+static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
+    using SM = PatShape<D, FMT, RC>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(attend_grid());
-    cfg.blockDim = dim3(SM::WARPS * 32);
-    a.nwarps = attend_grid() * SM::WARPS;
-    a.unit = PAGES_BLOCK * SM::UB;
-    cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pages_attend<D, FMT, RC>, a) != cudaSuccess) return KVP_ERR_CUDA;
+    a.nwarps = attend_grid() * SM::WARPS;
+    a.unit = PAGES_BLOCK * SM::UB;
+    const unsigned tiles = unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT);
+    // A block per row tile where one wave holds them and the tables are short (8
+    // heads of 128, k8v8; 15 sequences of 200 tokens 7.4 us, in runs 11.1; of 700
+    // 11.4 and 13.9; 30 sequences, two waves, of 500 tokens 19.0 and 18.3; one
+    // sequence of 700 tokens 10.2 and 9.6).
+    if (tiles <= attend_grid() && int64_t(a.max_pages) << a.pv.logP <= PAT_SOLO_TOKENS) {
+        const int rc = launch_tiles<D, FMT, RC, true>(cfg, a, tiles);
+        return rc == KVP_OK ? launch_status() : rc;
+    }
+    const int rc = launch_tiles<D, FMT, RC, false>(cfg, a, attend_grid());
+    if (rc != KVP_OK) return rc;
     cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
     cfg.dynamicSmemBytes = 0;
     // Warps for a row's partials, of which it has about nwarps / (row tiles): 16
     // where there are 64 or more of them, 8 a warp in flight (one 128K sequence, 300
     // partials a row: 71 against 76 us with 4 warps); 4 warps where there are fewer
     // (a step of 15 agents, 16 partials: 20.0 against 23.8 us with 16).
-    const bool many = a.nwarps / (unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT)) >= 64u;
+    const bool many = a.nwarps / tiles >= 64u;
     cfg.blockDim = dim3(many ? 512 : 128);
     if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, RC, 16> : pages_join<D, RC, 4>, a) != cudaSuccess)
         return KVP_ERR_CUDA;
-    count_launch(2);
+    count_launch();
     return launch_status();
 }
 

@@ -689,3 +689,42 @@ def test_calls_on_two_streams_at_once():
     for (out, lse), b in zip(alone, bufs):
         for o, ls in b[:-1]:
             assert np.array_equal(_f64(o), out) and np.array_equal(ls.cpu().numpy().astype(np.float64), lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", ATTEND)
+def test_attend_with_a_roomy_table(fmt, case):
+    """The same sequences with a table that could hold far more: the work is
+    split another way, the results are those of the plain form all the same,
+    empty rows and bases among them."""
+    H, d, page, lens, m, nq = case
+    pg = Pages(fmt, H, d, page, lens, seed=len(lens), max_pages=max(200, 65536 // page))
+    k, v = _kv(sum(lens), H, d, 11)
+    pg.append(k, v, outs=False)
+    ks = _split(P.held(_f64(k), fmt, False), lens)
+    vs = _split(P.held(_f64(v), fmt, True), lens)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(len(lens), m, nq, d, generator=g).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.1)
+    _check_attend(out, lse, _f64(q), ks, vs, lens, 0.1)
+    bo, bl = torch.randn(q.shape, generator=g), torch.randn(q.shape[:3], generator=g) * 3
+    out, lse = pg.attend(q.cuda(), 0.1, bo.cuda(), bl.cuda())
+    _check_attend(out, lse, _f64(q), ks, vs, lens, 0.1, (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+    assert pg.status() == kv.KVP_OK
+
+
+@pytest.mark.parametrize("roomy", [False, True])
+def test_attend_wait_timeout_of_either_split(roomy):
+    H, d, lens = 2, 64, [300, 20]
+    k, v = _kv(sum(lens), H, d, 24)
+    pg = Pages("k8v4", H, d, 64, lens, max_pages=4096 if roomy else None)
+    pg.append(k, v)
+    q = torch.randn(2, 1, 8, d).to(torch.bfloat16).cuda()
+    assert kv.kvp_test_limit_next_pages_attend(0) == kv.KVP_OK
+    pg.attend(q, 0.1)
+    assert pg.status() == kv.KVP_ERR_TIMEOUT
+    assert kv.kvpages_init(pg.cfg, pg.buf.t, pg.buf.nbytes) == kv.KVP_OK
+    out, lse = pg.attend(q, 0.1)
+    assert pg.status() == kv.KVP_OK
+    _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), "k8v4", False), lens),
+                  _split(P.held(_f64(v), "k8v4", True), lens), lens, 0.1)
