@@ -13,18 +13,20 @@
 // few instructions on each.
 //
 // Work split.  The unit is one or two 16-token blocks (8- and 4-bit pages: two)
-// of one (sequence, KV head, tile of query rows).  All units of all sequences, in that order, are one list, cut
-// into equal runs, one per warp: no warp has more to do than another, however
-// ragged the lengths, and the cut follows from the lengths on the device, so a
-// captured graph stays right as sequences grow.  A row tile counts PAT_ITEM
-// units more than it has blocks, for its start and end.  A warp that holds all
-// of a row tile writes its result; otherwise it leaves a partial result (running
-// maximum, sum and weighted values) and pages_join merges them in list order, so
-// results do not depend on timing.
+// of one (sequence, KV head, tile of query rows).  All units of all sequences, in
+// that order, are one list, cut into equal runs, one per warp: no warp has more to
+// do than another, however ragged the lengths, and the cut follows from the
+// lengths on the device, so a captured graph stays right as sequences grow.  A row
+// tile counts PAT_ITEM units more than it has, for its start and end.  A warp that
+// holds all of a row tile writes its result; otherwise it leaves a partial result
+// (running maximum, sum and weighted values) and pages_join merges them in list
+// order, so results do not depend on timing.  Where the tables are short, a team of
+// a thread block's warps takes each row tile instead and merges it in shared
+// memory, in one launch (team_units says when).
 //
-// A warp's blocks arrive by bulk copies, one per unit (the blocks of a head's
-// tokens in a page are one run of bytes), in the warp's own ring in shared memory, on the warp's own barriers:
-// warps never wait for each other after the start.
+// A warp's units arrive by bulk copies, one per unit (the blocks of a head's tokens
+// in a page are one run of bytes), in the warp's own ring in shared memory, on the
+// warp's own barriers: warps do not wait for each other between start and merge.
 //
 // Products, with tokens or dims as the 16 rows and the query rows as the 8
 // columns, so that a tile of up to 8 query rows wastes nothing:
@@ -64,7 +66,6 @@ constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums
 // The weights' reference is raised only when a score passes it by this much
 // (base 2), so that the accumulators are rarely rescaled.
 constexpr float PAT_SLACK = 8.0f;
-constexpr int64_t PAT_SOLO_TOKENS = 768;  // most tokens that a table may hold where a block takes a whole row tile
 
 struct PagesAttendArgs {
     PagesView pv;
@@ -80,6 +81,7 @@ struct PagesAttendArgs {
     int nseq, m, nq, G, R, RT, max_pages;
     int unit;  // tokens of a unit
     uint32_t nwarps, polls;
+    int team;  // warps of a row tile where it is not cut from the list
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -345,8 +347,8 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
 // 0..3 and again in 4..7: the weights' first bf16 in the former, the second in
 // the latter, so that one value product does for both.
 //
-// SOLO: a thread block takes one row tile, its warps equal parts of the tile's
-// units, merged in shared memory: no list, no partial results, no join.
+// SOLO: a group of a.team warps takes one row tile, each an equal part of the
+// tile's units, merged in shared memory: no list, no partial results, no join.
 template <int D, int FMT, int RC, bool SOLO>
 __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     pages_attend(const __grid_constant__ PagesAttendArgs a) {
@@ -372,12 +374,16 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool match = pages_match(a.pv);
     const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
-    // SOLO: the block's sequence and row tile, and the tile's units
-    const int sb = SOLO ? int(blockIdx.x / HRT) : 0;
-    const uint32_t stile = SOLO ? blockIdx.x % HRT : 0u;
+    // SOLO: the warp's place in its team, the team's sequence and row tile (the
+    // tiles go round the blocks, so that all have as many), and the tile's units
+    const int team = SOLO ? a.team : 1, place_in = warp % team;
+    const uint32_t stask = SOLO ? uint32_t(warp / team) * gridDim.x + blockIdx.x : 0u;
+    const bool sreal = stask < uint32_t(a.nseq) * HRT;
+    const int sb = SOLO && sreal ? int(stask / HRT) : 0;
+    const uint32_t stile = SOLO && sreal ? stask % HRT : 0u;
     uint32_t solo_units = 0, carry = 0;
     if constexpr (SOLO) {
-        const uint32_t n = tile_units(seq_len(a, sb, stile == 0), 16 * UB);
+        const uint32_t n = sreal ? tile_units(seq_len(a, sb, stile == 0), 16 * UB) : 0u;
         solo_units = n ? n - PAT_ITEM : 0u;
     } else {
         carry = make_plan(a, pre, wsum, 16 * UB, THREADS);
@@ -388,9 +394,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         return;
     }
     const uint64_t units = SOLO ? solo_units : uint64_t(carry) * HRT;
-    const uint64_t per = run_length(units, SOLO ? uint32_t(WARPS) : a.nwarps);
+    const uint64_t per = run_length(units, SOLO ? uint32_t(team) : a.nwarps);
     const uint32_t gw = blockIdx.x * WARPS + uint32_t(warp);
-    const uint64_t f0 = (SOLO ? uint32_t(warp) : gw) * per;
+    const uint64_t f0 = (SOLO ? uint32_t(place_in) : gw) * per;
     const uint32_t cnt = f0 >= units ? 0u : uint32_t(f0 + per < units ? per : units - f0);
     if (cnt == 0u && !SOLO) return;
 
@@ -977,18 +983,18 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     }
     if constexpr (!SOLO) return;
 
-    // The tile's rows, a warp at a time: its warps' parts, in order
+    // The tile's rows, a warp of the team at a time: its warps' parts, in order
     static_assert(RTILE * (D * 4 + 8) <= STAGES * SM::SLOT, "a warp's part fits its ring");
     __syncthreads();
     const uint32_t parts = uint32_t((units + per - 1) / per);
-    if (parts == 1u) return;  // written by the warp that had it all
+    if (!sreal || parts == 1u) return;  // written by the warp that had it all
     const int h = int(stile) / a.RT, r0 = int(stile) % a.RT * RTILE;
-    for (int rr = warp; rr < min(RTILE, a.R - r0); rr += WARPS) {
+    const uint8_t *part = sm + PAT_BAR_BYTES + uint32_t(warp - place_in) * STAGES * SM::SLOT;
+    for (int rr = place_in; rr < min(RTILE, a.R - r0); rr += team) {
         constexpr int VPL = D / 32;
         float y[VPL], M = -INFINITY, L = 0.0f;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) y[k] = 0.0f;
-        const uint8_t *part = sm + PAT_BAR_BYTES;
         for (uint32_t w = 0; w < parts; ++w)
             M = fmaxf(M, reinterpret_cast<const float2 *>(part + w * STAGES * SM::SLOT + RTILE * D * 4)[rr].x);
         for (uint32_t w = 0; w < parts; ++w) {
@@ -1135,6 +1141,21 @@ static int tile_rows(int rows, int format) {
     return eights == 1 || (format != KVP_PAGES_BF16 && eights % 2 == 1) ? 8 : 16;
 }
 
+// Units of a team's warp up to which a team per row tile beats equal runs of the
+// list.  It has one launch and nothing cut, but waits for the longest sequence.
+// Where teams employ half of the GPU's warps or more (us, teams against runs, of
+// 8 KV heads): k8v8 at 128, 64 x 700 tokens (7.3 units) 27 and 32, lengths of 1 to
+// 700 24 and 25, 64 x 1500 (16) 46 and 49, but lengths of 1 to 1500 41 and 34; bf16 at 128, 120 x 200 (12)
+// 22 and 38, 64 x 700 (22) 34 and 41, lengths of 1 to 700 23 and 29; k8v4 at 64,
+// 64 x 1500 (12) 28 and 34, lengths of 1 to 1500 24 and 26.  Where they employ
+// fewer: one sequence of 700 tokens (k8v8, 2 units) 9.9 and 9.6, of 1500 14.7
+// and 9.8; bf16 700 (6) 8.0 and 7.6, 200 (2) 5.7 and 7.4.
+template <int D, int FMT>
+static int team_units(bool half) {
+    if (FMT == KVP_PAGES_BF16) return half ? 24 : 4;
+    return half ? (D == 128 ? 8 : 12) : 2;
+}
+
 template <int D, int FMT, int RC, bool SOLO>
 static int launch_tiles(cudaLaunchConfig_t &cfg, const PagesAttendArgs &a, unsigned grid) {
     using SM = PatShape<D, FMT, RC>;
@@ -1169,12 +1190,13 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     a.nwarps = attend_grid() * SM::WARPS;
     a.unit = PAGES_BLOCK * SM::UB;
     const unsigned tiles = unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT);
-    // A block per row tile where one wave holds them and the tables are short (8
-    // heads of 128, k8v8; 15 sequences of 200 tokens 7.4 us, in runs 11.1; of 700
-    // 11.4 and 13.9; 30 sequences, two waves, of 500 tokens 19.0 and 18.3; one
-    // sequence of 700 tokens 10.2 and 9.6).
-    if (tiles <= attend_grid() && int64_t(a.max_pages) << a.pv.logP <= PAT_SOLO_TOKENS) {
-        const int rc = launch_tiles<D, FMT, RC, true>(cfg, a, tiles);
+    // the largest team of warps for which one wave of blocks holds all tiles
+    a.team = SM::WARPS;
+    while (a.team > 0 && (SM::WARPS % a.team || uint64_t(attend_grid()) * unsigned(SM::WARPS / a.team) < tiles)) --a.team;
+    const int64_t most = ((int64_t(a.max_pages) << a.pv.logP) + a.unit - 1) / a.unit;  // units that a table may hold
+    if (a.team > 0 && most <= int64_t(team_units<D, FMT>(2 * uint64_t(tiles) * a.team >= a.nwarps)) * a.team) {
+        const unsigned per_block = unsigned(SM::WARPS / a.team);
+        const int rc = launch_tiles<D, FMT, RC, true>(cfg, a, (tiles + per_block - 1) / per_block);
         return rc == KVP_OK ? launch_status() : rc;
     }
     const int rc = launch_tiles<D, FMT, RC, false>(cfg, a, attend_grid());
