@@ -198,23 +198,19 @@ __device__ __forceinline__ float exp2_fast(float x) {  // results under 2^-126 a
     return r;
 }
 // The weights (w0, w1) of a token and two queries as value-product operands: a
-// sum of two bf16.  TWICE: lanes of columns 0..3 (tig < 2) give the first, the
-// others the second, in one operand; else one operand each.
-template <bool TWICE>
-__device__ __forceinline__ void split_weights(float w0, float w1, int tig, uint32_t &hi, uint32_t &lo) {
+// sum of two bf16, one operand each.
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo) {
     const uint32_t h = pack_bf16x2(w0, w1);
-    if constexpr (TWICE) {
-        // the first lanes take nothing off, so that they pack the same again
-        const float h0 = __uint_as_float(__byte_perm(h, 0u, tig < 2 ? 0x4444u : 0x1044u));
-        const float h1 = __uint_as_float(h & (tig < 2 ? 0u : 0xFFFF0000u));
-        const float2 d = __ffma2_rn(make_float2(h0, h1), make_float2(-1.0f, -1.0f), make_float2(w0, w1));
-        hi = transpose8(pack_bf16x2(d.x, d.y));
-        lo = 0u;
-    } else {
-        const float2 d =
-            __ffma2_rn(make_float2(bf16_lo(h), bf16_hi(h)), make_float2(-1.0f, -1.0f), make_float2(w0, w1));
-        hi = transpose8(h), lo = transpose8(pack_bf16x2(d.x, d.y));
-    }
+    const float2 d =
+        __ffma2_rn(make_float2(bf16_lo(h), bf16_hi(h)), make_float2(-1.0f, -1.0f), make_float2(w0, w1));
+    hi = transpose8(h), lo = transpose8(pack_bf16x2(d.x, d.y));
+}
+// The weights of two tokens and one query: the two bf16 of each in one operand's
+// neighbouring columns.
+__device__ __forceinline__ void twin_weights(float w0, float w1, uint32_t &b0, uint32_t &b1) {
+    const uint32_t h = pack_bf16x2(w0, w1);
+    b0 = transpose8(pack_bf16x2(w0, w0 - bf16_lo(h)));
+    b1 = transpose8(pack_bf16x2(w1, w1 - bf16_hi(h)));
 }
 // Over the eight lanes of a quad position (the rows of a C fragment).
 __device__ __forceinline__ float rows_add(float x) {
@@ -343,9 +339,9 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
     return make_float2(wa, wb);
 }
 
-// RC: query rows of a tile (4, 8 or 16).  A tile of 4 has its rows in columns
-// 0..3 and again in 4..7: the weights' first bf16 in the former, the second in
-// the latter, so that one value product does for both.
+// RC: query rows of a tile (4, 8 or 16).  A tile of 4 has row i in the columns 2 i
+// and 2 i + 1: the weights' first bf16 in the former, the second in the latter, so
+// that one value product does for both, and a lane has the scores of one row.
 //
 // SOLO: a group of a.team warps takes one row tile, each an equal part of the
 // tile's units, merged in shared memory: no list, no partial results, no join.
@@ -356,6 +352,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     using SM = PatShape<D, FMT, RC>;
     constexpr int R8 = RC == 16 ? 2 : 1;  // groups of 8 columns
     constexpr bool TWICE = RC == 4;
+    constexpr int CQ = TWICE ? 1 : 2;  // queries of a lane and group
     constexpr int NG = B::NG, MT = D / 16, RTILE = RC, WARPS = SM::WARPS, THREADS = WARPS * 32;
     constexpr int UB = SM::UB, GU = 32 / UB;  // units whose addresses the lanes hold
     constexpr uint32_t STAGES = SM::STAGES;
@@ -485,15 +482,16 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     const uint32_t v_odd = Q8 ? B::value(uint32_t(2 * tig + 1), uint32_t(g) * (B::VROW / 8)) : 0u;
     const uint32_t prep = smem_addr(sm) + SM::OFF_PREP + uint32_t(warp) * SM::PREP;
 
-    // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c).
+    // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c); of a
+    // tile of 4, query tig.
     uint32_t qf[D / 16][R8][2];  // query fragments by k-step
-    float qs[R8][2];             // factor of the scores (base 2)
-    int lim[R8][2];              // tokens that the query sees
-    float ref[R8][2];            // running maximum score, raised lazily
-    float bar2[R8][2], off[R8][2];  // where it is raised; what weights are relative to
-    float sum[R8][2];            // the lane's part of the sum of weights
+    float qs[R8][CQ];            // factor of the scores (base 2)
+    int lim[R8][CQ];             // tokens that the query sees
+    float ref[R8][CQ];           // running maximum score, raised lazily
+    float bar2[R8][CQ], off[R8][CQ];  // where it is raised; what weights are relative to
+    float sum[R8][CQ];           // the lane's part of the sum of weights
     float acc[MT][R8][4];
-    float zsum[V4 ? NG : 1][R8][2];
+    float zsum[V4 ? NG : 1][R8][CQ];
 
     // The queries of (b, tile): raw bf16 (Q8), or fragments as they are.
     uint4 qraw[Q8 ? NG : 1][R8];
@@ -501,7 +499,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         const int h = int(st) / a.RT, r0 = int(st) % a.RT * RTILE;
 #pragma unroll
         for (int t = 0; t < R8; ++t) {
-            const int r = r0 + 8 * t + (TWICE ? g & 3 : g);
+            const int r = r0 + 8 * t + (TWICE ? g >> 1 : g);
             const bool real = r < a.R;
             const int i = real ? r / a.G : 0, j = h * a.G + (real ? r - i * a.G : 0);
             const uint16_t *qrow = a.q + ((uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j)) * D;
@@ -555,8 +553,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int rc = r0 + 8 * t + (TWICE ? (2 * tig + c) & 3 : 2 * tig + c);
+                for (int c = 0; c < CQ; ++c) {
+                    const int rc = r0 + 8 * t + (TWICE ? tig : 2 * tig + c);
                     lim[t][c] = rc < a.R ? len - (a.m - 1 - rc / a.G) : 0;
                     const int u = __shfl_sync(0xffffffffu, up, (2 * tig + c) * 4);
                     qs[t][c] = Q8 ? a.scale2 * __uint_as_float(uint32_t(127 - u) << 23) : a.scale2;
@@ -574,7 +572,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                 for (int k = 0; k < NG; ++k)
 #pragma unroll
-                    for (int t = 0; t < R8; ++t) zsum[k][t][0] = zsum[k][t][1] = 0.0f;
+                    for (int t = 0; t < R8; ++t)
+#pragma unroll
+                        for (int c = 0; c < CQ; ++c) zsum[k][t][c] = 0.0f;
             }
         }
         if (!mbar_wait(bar + 8u * slot, phase, a.polls)) {
@@ -624,13 +624,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 }
                 __syncwarp();
             }
-            // scores: x[u][t][0..1] token 16 u + g, [2..3] token 16 u + g + 8, of the two queries
-            float x[UB][R8][4];
+            // scores: x[u][t][c] token 16 u + g, [CQ + c] token 16 u + g + 8
+            float x[UB][R8][2 * CQ];
 #pragma unroll
             for (int u = 0; u < UB; ++u) {
                 const uint32_t at = at0 + uint32_t(u) * B::BYTES;
 #pragma unroll
-                for (int t = 0; t < R8; ++t) x[u][t][0] = x[u][t][1] = x[u][t][2] = x[u][t][3] = 0.0f;
+                for (int t = 0; t < R8; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] = 0.0f;
                 if constexpr (Q8) {
                     uint32_t w[2][NG][2];
                     float ks[2][NG];
@@ -661,21 +663,29 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                         for (int t = 0; t < R8; ++t)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[u][t][e] = fmaf(c[t][e], ks[e >> 1][k], x[u][t][e]);
+                            for (int e = 0; e < 2 * CQ; ++e)
+                                x[u][t][e] = fmaf(c[t][e / CQ * 2 + e % CQ], ks[e / CQ][k], x[u][t][e]);
                     }
                 } else {
+                    float c[R8][4];
+#pragma unroll
+                    for (int t = 0; t < R8; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.0f;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         uint32_t w[4];
                         ldsm4(w, (at + k_off) ^ (32u * uint32_t(k)));
 #pragma unroll
-                        for (int t = 0; t < R8; ++t) mma_bf16(x[u][t], w[0], w[1], w[2], w[3], qf[k][t][0], qf[k][t][1]);
+                        for (int t = 0; t < R8; ++t) mma_bf16(c[t], w[0], w[1], w[2], w[3], qf[k][t][0], qf[k][t][1]);
                     }
+#pragma unroll
+                    for (int t = 0; t < R8; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] = c[t][e / CQ * 2 + e % CQ];
                 }
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[u][t][e] *= qs[t][e & 1];
+                    for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] *= qs[t][e % CQ];
             }
             if (tail) {
 #pragma unroll
@@ -683,47 +693,50 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                     for (int t = 0; t < R8; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (t0 + 16 * u + g + 8 * (e >> 1) >= lim[t][e & 1] || !((here >> u) & 1u)) x[u][t][e] = -INFINITY;
+                        for (int e = 0; e < 2 * CQ; ++e)
+                            if (t0 + 16 * u + g + 8 * (e / CQ) >= lim[t][e % CQ] || !((here >> u) & 1u)) x[u][t][e] = -INFINITY;
             }
             bool raise = false;
-            float top[R8][2];
+            float top[R8][CQ];
 #pragma unroll
             for (int t = 0; t < R8; ++t)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    top[t][c] = fmaxf(x[0][t][c], x[0][t][2 + c]);
-                    if constexpr (UB == 2) top[t][c] = fmaxf(top[t][c], fmaxf(x[UB - 1][t][c], x[UB - 1][t][2 + c]));
+                for (int c = 0; c < CQ; ++c) {
+                    top[t][c] = fmaxf(x[0][t][c], x[0][t][CQ + c]);
+                    if constexpr (UB == 2) top[t][c] = fmaxf(top[t][c], fmaxf(x[UB - 1][t][c], x[UB - 1][t][CQ + c]));
                     raise |= top[t][c] > bar2[t][c];
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < CQ; ++c) {
                         const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
                         const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
                         ref[t][c] = nr, bar2[t][c] = nr + PAT_SLACK;
                         off[t][c] = nr == -INFINITY ? 0.0f : nr;
                         sum[t][c] *= f;
 #pragma unroll
-                        for (int k = 0; k < MT; ++k) acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
+                        for (int k = 0; k < MT; ++k) {
+                            acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
+                            if constexpr (TWICE) acc[k][t][1] *= f, acc[k][t][3] *= f;
+                        }
                         if constexpr (V4) {
 #pragma unroll
                             for (int k = 0; k < NG; ++k) zsum[k][t][c] *= f;
                         }
                     }
             }
-            float p[UB][R8][4];
+            float p[UB][R8][2 * CQ];
 #pragma unroll
             for (int u = 0; u < UB; ++u)
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < CQ; ++c) {
                         p[u][t][c] = exp2_fast(x[u][t][c] - off[t][c]);
-                        p[u][t][2 + c] = exp2_fast(x[u][t][2 + c] - off[t][c]);
-                        sum[t][c] += p[u][t][c] + p[u][t][2 + c];
+                        p[u][t][CQ + c] = exp2_fast(x[u][t][CQ + c] - off[t][c]);
+                        sum[t][c] += p[u][t][c] + p[u][t][CQ + c];
                     }
 #pragma unroll
             for (int u = 0; u < UB; ++u) {
@@ -774,12 +787,16 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     for (int e = 0; e < NG; ++e) {
                         uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
-                        for (int t = 0; t < R8; ++t)
+                        for (int t = 0; t < R8; ++t) {
+                            if constexpr (TWICE) {
+                                twin_weights(p[u][t][0] * sv[0][e], p[u][t][1] * sv[1][e], hi[t][0], hi[t][1]);
+                            } else {
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const float w0 = p[u][t][2 * hf] * sv[hf][e], w1 = p[u][t][2 * hf + 1] * sv[hf][e];
-                                split_weights<TWICE>(w0, w1, tig, hi[t][hf], lo[t][hf]);
+                                for (int hf = 0; hf < 2; ++hf)
+                                    split_weights(p[u][t][2 * hf] * sv[hf][e], p[u][t][2 * hf + 1] * sv[hf][e], hi[t][hf],
+                                                  lo[t][hf]);
                             }
+                        }
                         uint32_t v[2][4];  // [token half][dim of the granule's word]
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
@@ -807,8 +824,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                             for (int t = 0; t < R8; ++t)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    zsum[e][t][c & 1] = fmaf(p[u][t][c], zv[c >> 1][e], zsum[e][t][c & 1]);
+                                for (int c = 0; c < 2 * CQ; ++c)
+                                    zsum[e][t][c % CQ] = fmaf(p[u][t][c], zv[c / CQ][e], zsum[e][t][c % CQ]);
                         }
                     }
                 } else {
@@ -831,11 +848,11 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                                     for (int r = 0; r < R8; ++r)
 #pragma unroll
-                                        for (int c = 0; c < 2; ++c) {
+                                        for (int c = 0; c < CQ; ++c) {
                                             // the token's weight is with lane row t % 8
-                                            const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][2 + c],
+                                            const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][CQ + c],
                                                                         ((t & 7) << 2) | tig);
-                                            if (t0 + t >= lim[r][c] || (TWICE && tig >= 2)) continue;
+                                            if (t0 + t >= lim[r][c]) continue;
 #pragma unroll
                                             for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -856,10 +873,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     }
                     uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
-                    for (int t = 0; t < R8; ++t)
+                    for (int t = 0; t < R8; ++t) {
+                        if constexpr (TWICE) {
+                            twin_weights(p[u][t][0], p[u][t][1], hi[t][0], hi[t][1]);
+                        } else {
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-                            split_weights<TWICE>(p[u][t][2 * hf], p[u][t][2 * hf + 1], tig, hi[t][hf], lo[t][hf]);
+                            for (int hf = 0; hf < 2; ++hf)
+                                split_weights(p[u][t][2 * hf], p[u][t][2 * hf + 1], hi[t][hf], lo[t][hf]);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < MT; ++k) {
                         uint32_t w[4];
@@ -904,15 +926,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
         for (int t = 0; t < R8; ++t)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int rr = 8 * t + 2 * tig + c, r = r0 + rr;
+            for (int c = 0; c < CQ; ++c) {
+                const int rr = TWICE ? tig : 8 * t + 2 * tig + c, r = r0 + rr;
                 const float l = rows_add(sum[t][c]);
                 if constexpr (TWICE) {
 #pragma unroll
-                    for (int k = 0; k < MT; ++k)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            acc[k][t][2 * u + c] += __shfl_xor_sync(0xffffffffu, acc[k][t][2 * u + c], 2);
+                    for (int k = 0; k < MT; ++k) acc[k][t][0] += acc[k][t][1], acc[k][t][2] += acc[k][t][3];
                 }
                 if constexpr (V4) {
 #pragma unroll
@@ -922,7 +941,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         acc[2 * e + 1][t][c] += z, acc[2 * e + 1][t][2 + c] += z;
                     }
                 }
-                if (r >= a.R || (TWICE && tig >= 2)) continue;
+                if (r >= a.R) continue;
                 const float base2 = ref[t][c];
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
