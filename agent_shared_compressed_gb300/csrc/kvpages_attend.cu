@@ -42,14 +42,17 @@
 // Key scales apply to the fp32 sums of their 32 dims.  Value scales go into the
 // weights, one product operand per 32 dims, as a sum of two bf16: 2^-17 of the
 // weight, and fp32's range, so that a token of large weight and tiny values (an
-// attention sink) takes nothing from the others.  (One fp16 per weight is 10%
-// fewer instructions, but loses weights 2^-25 below the largest where that one's
-// value is zero.)  4-bit values q s + z enter as (q - c) s + (z + c s) with c the
-// integer of [0, 15] nearest to -z / s, formed once per token and group: then
-// |z + c s| is at most s / 2 (or of
-// the code term's sign, where zero is outside the group's range), and the two
-// sums, of the code terms in the product and of the rest in fp32 once per 32
-// dims, do not cancel.  16-bit pages are multiplied as they are.
+// attention sink) takes nothing from the others.  (One fp16 per weight is fewer
+// instructions, but loses weights 2^-25 below the largest where that one's value is
+// zero.)  4-bit values q s + z enter as (q - c) s + (z + c s) with c the integer of
+// [0, 15] nearest to -z / s, formed once per token and group: then |z + c s| is at
+// most s / 2 (or of the code term's sign, where zero is outside the group's range),
+// and the two sums, of the code terms in the product and of the rest in fp32 once
+// per 32 dims, do not cancel.  16-bit pages are multiplied as they are.
+//
+// Measured (of the 6789 GB/s that a copy reaches): four 32K caches of 8 bits, 4
+// query rows a KV head, 56 us, 5.1 TB/s; 15 4K caches of 16 bits 45 us, 5.6 TB/s; one
+// 128K with 4-bit values 50.4 us, 4.5 TB/s.
 #include <algorithm>
 #include <cmath>
 
@@ -59,7 +62,9 @@
 namespace kvp {
 
 constexpr int PAT_MOST_WARPS = 16;             // of a block
-constexpr uint32_t PAT_ITEM = 2;               // units that a row tile counts beside its own
+// Units that a row tile counts beside its own (64 ragged sequences 54.3 us, with 1
+// 56.8 and with 3 55.7; 8 sequences of 20 rows 38.7, 37.8 and 39.7).
+constexpr uint32_t PAT_ITEM = 2;
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
@@ -242,12 +247,14 @@ __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) 
     return units ? (units + nwarps - 1) / nwarps : 1u;
 }
 
-// The shape of a block.  8- and 4-bit pages at head_dim 128: 12 warps (167
-// registers) with units of two blocks measured 57.9 us on four 32K caches (8
-// warps 62, 16 warps at 128 registers 71 with units of one); 16-row tiles take
-// 250 registers, hence 8 warps, as do 16-bit pages, whose blocks are 8 KB each.
-// At head_dim 64 16 warps, 12 for 16-row tiles (35.8 against 37.0 us with 16,
-// which spill, on 30 4K caches with 16 rows).
+// The shape of a block.  8- and 4-bit pages at head_dim 128: 12 warps (168
+// registers) with units of two blocks measured 55.7 us on four 32K caches of 8 bits
+// and 50.4 on one of 128K with 4-bit values; 16 warps, at 128 registers and with
+// units of one block, 56.5 and 55.5; 14 warps, which spill, 63.9 on the latter.
+// 16-row tiles take 250 registers, hence 8 warps, as do 16-bit pages, whose blocks
+// are 8 KB each.  At head_dim 64 16 warps (20: 53.9 against 54.4 us on 64 ragged
+// sequences, for a quarter more partial results), 12 for 16-row tiles (35.8 against
+// 37.0 us with 16, which spill, on 30 4K caches with 16 rows).
 template <int D, int FMT, int RC>
 struct PatShape {
     static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 || RC == 16 ? 8 : 12) : (RC == 16 ? 12 : 16);
@@ -1161,14 +1168,16 @@ static int tile_rows(int rows, int format) {
 }
 
 // Units of a team's warp up to which a team per row tile beats equal runs of the
-// list.  It has one launch and nothing cut, but waits for the longest sequence.
-// Where teams employ half of the GPU's warps or more (us, teams against runs, of
-// 8 KV heads): k8v8 at 128, 64 x 700 tokens (7.3 units) 27 and 32, lengths of 1 to
-// 700 24 and 25, 64 x 1500 (16) 46 and 49, but lengths of 1 to 1500 41 and 34; bf16 at 128, 120 x 200 (12)
-// 22 and 38, 64 x 700 (22) 34 and 41, lengths of 1 to 700 23 and 29; k8v4 at 64,
-// 64 x 1500 (12) 28 and 34, lengths of 1 to 1500 24 and 26.  Where they employ
-// fewer: one sequence of 700 tokens (k8v8, 2 units) 9.9 and 9.6, of 1500 14.7
-// and 9.8; bf16 700 (6) 8.0 and 7.6, 200 (2) 5.7 and 7.4.
+// list.  It has one launch and nothing cut, but waits for the longest sequence, so
+// that the limits are below where equal lengths lose.  Where teams employ half of
+// the GPU's warps or more (us, teams against runs, of 8 KV heads): k8v8 at 128, 64
+// x 700 tokens (7.3 units) 25 and 30, lengths of 1 to 700 22 and 23, 64 x 1500 (16)
+// 43 and 46, but lengths of 1 to 1500 38 and 32; bf16 at 128, 120 x 200 (13) 21 and
+// 37, 64 x 700 (22) 33 and 40, lengths of 1 to 700 22 and 27; k8v4 at 64, 64 x 1500
+// (12) 26 and 31, lengths of 1 to 1500 22 and 24, 120 x 1500 (24) 45 and 52, lengths
+// of 1 to 1500 38 and 38.  Where they employ fewer: one sequence of 700 tokens (k8v8,
+// 2 units) 8.8 and 8.9, of 1500 13.3 and 9.1; bf16 700 (6) 7.5 and 7.2, 200 (2) 5.2
+// and 7.0.
 template <int D, int FMT>
 static int team_units(bool half) {
     if (FMT == KVP_PAGES_BF16) return half ? 24 : 4;
