@@ -728,3 +728,27 @@ def test_attend_wait_timeout_of_either_split(roomy):
     assert pg.status() == kv.KVP_OK
     _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), "k8v4", False), lens),
                   _split(P.held(_f64(v), "k8v4", True), lens), lens, 0.1)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("k8v8", 64), ("k8v8", 128), ("k8v4", 64), ("k8v4", 128)])
+@pytest.mark.parametrize("n,m,nq", [(70, 1, 16), (140, 1, 4), (140, 3, 16), (220, 2, 8), (300, 1, 16), (600, 1, 8), (610, 1, 4)])
+def test_attend_by_number_of_row_tiles(fmt, d, n, m, nq):
+    """From few row tiles, which many warps share, to about one a warp, and more
+    than the GPU has warps; ragged, with empty sequences and bases."""
+    H = 4
+    rng = np.random.default_rng(n + m)
+    lens = [int(x) for x in rng.integers(0, 150, n)]
+    lens[0], lens[1], lens[-1] = 150, 0, 1
+    pg = Pages(fmt, H, d, 16, lens, seed=2)
+    k, v = _kv(sum(lens), H, d, 25)
+    pg.append(k, v, outs=False)
+    ks = _split(P.held(_f64(k), fmt, False), lens)
+    vs = _split(P.held(_f64(v), fmt, True), lens)
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(n, m, nq, d, generator=g).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.1)
+    _check_attend(out, lse, _f64(q), ks, vs, lens, 0.1)
+    bo, bl = torch.randn(q.shape, generator=g), torch.randn(q.shape[:3], generator=g) * 3
+    out, lse = pg.attend(q.cuda(), 0.1, bo.cuda(), bl.cuda())
+    _check_attend(out, lse, _f64(q), ks, vs, lens, 0.1, (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+    assert pg.status() == kv.KVP_OK
