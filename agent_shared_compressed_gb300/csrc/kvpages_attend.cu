@@ -17,7 +17,7 @@
 // that order, are one list, cut into equal runs, one per warp: no warp has more to
 // do than another, however ragged the lengths, and the cut follows from the
 // lengths on the device, so a captured graph stays right as sequences grow.  A row
-// tile counts PAT_ITEM units more than it has, for its start and end.  A warp that
+// tile counts PAT_ITEM blocks more than it has, for its start and end.  A warp that
 // holds all of a row tile writes its result; otherwise it leaves a partial result
 // (running maximum, sum and weighted values) and pages_join merges them in list
 // order, so results do not depend on timing.  Where the tables are short, a team of
@@ -62,9 +62,10 @@
 namespace kvp {
 
 constexpr int PAT_MOST_WARPS = 16;             // of a block
-// Units that a row tile counts beside its own (64 ragged sequences 54.3 us, with 1
-// 56.8 and with 3 55.7; 8 sequences of 20 rows 38.7, 37.8 and 39.7).
-constexpr uint32_t PAT_ITEM = 2;
+// Blocks that a row tile counts beside its own (us with 2, 4, 8 of them: 64 ragged
+// sequences of one row a head 56.8, 54.4, 57.8; 40 ragged ones of 64 rows, 8 bits,
+// 166, 157, 161; four 32K caches 56.5, 55.5, 56.4).
+constexpr uint32_t PAT_ITEM = 4;
 constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
@@ -240,7 +241,7 @@ __device__ __forceinline__ int seq_len(const PagesAttendArgs &a, int b, bool fla
 
 // Units of a sequence's row tile (both kernels).
 __device__ __forceinline__ uint32_t tile_units(int len, int unit) {
-    return len ? uint32_t((int64_t(len) + unit - 1) / unit) + PAT_ITEM : 0u;
+    return len ? uint32_t((int64_t(len) + unit - 1 + int64_t(PAT_ITEM) * PAGES_BLOCK) / unit) : 0u;
 }
 // Units of a warp's run (both kernels).
 __device__ __forceinline__ uint64_t run_length(uint64_t units, uint32_t nwarps) {
@@ -259,6 +260,7 @@ template <int D, int FMT, int RC>
 struct PatShape {
     static constexpr int WARPS = D == 128 ? (FMT == KVP_PAGES_BF16 || RC == 16 ? 8 : 12) : (RC == 16 ? 12 : 16);
     static constexpr int UB = FMT != KVP_PAGES_BF16 && RC <= 8 ? 2 : 1;  // blocks of a unit
+    static constexpr uint32_t ITEM = PAT_ITEM / UB;  // units that a row tile counts beside its own
     static constexpr uint32_t SLOT = (UB * Block<D, FMT>::BYTES + 127u) / 128u * 128u;
     static constexpr uint32_t RING = 180224u / WARPS / SLOT;  // of about 176 KB
     static constexpr uint32_t LEAST = UB == 2 ? 2u : 3u;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     uint32_t solo_units = 0, carry = 0;
     if constexpr (SOLO) {
         const uint32_t n = sreal ? tile_units(seq_len(a, sb, stile == 0), 16 * UB) : 0u;
-        solo_units = n ? n - PAT_ITEM : 0u;
+        solo_units = n ? n - SM::ITEM : 0u;
     } else {
         carry = make_plan(a, pre, wsum, 16 * UB, THREADS);
     }
@@ -404,10 +406,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     const uint32_t cnt = f0 >= units ? 0u : uint32_t(f0 + per < units ? per : units - f0);
     if (cnt == 0u && !SOLO) return;
 
-    // unit f: its sequence, row tile and place in the tile (PAT_ITEM empty places, then the blocks)
+    // unit f: its sequence, row tile and place in the tile (ITEM empty places, then the blocks)
     auto locate = [&](uint64_t f, int &b, uint32_t &tile, uint32_t &at) {
         if constexpr (SOLO) {
-            b = sb, tile = stile, at = uint32_t(f) + PAT_ITEM;
+            b = sb, tile = stile, at = uint32_t(f) + SM::ITEM;
             return;
         }
         const uint32_t p = (f >> 32) == 0 ? uint32_t(f) / HRT : uint32_t(f / HRT);
@@ -436,8 +438,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         const uint32_t u = first + uint32_t(lane / UB);
         if (u >= cnt) return 0;
         locate(f0 + u, b, tile, at);
-        if (at < PAT_ITEM) return 0;
-        const uint32_t t0 = ((at - PAT_ITEM) * UB + uint32_t(lane % UB)) * PAGES_BLOCK;
+        if (at < SM::ITEM) return 0;
+        const uint32_t t0 = ((at - SM::ITEM) * UB + uint32_t(lane % UB)) * PAGES_BLOCK;
         if (UB > 1 && t0 >= uint32_t(seq_len(a, b, false))) return 0;
         const int page = __ldg(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP));
         if (page < 0 || page >= a.pv.n_pages) {
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (fresh) {
             fresh = false;
             seg0 = place;
-            nplace = SOLO ? solo_units + PAT_ITEM : pre[b + 1] - pre[b];
+            nplace = SOLO ? solo_units + SM::ITEM : pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
             const int r0 = int(tile) % a.RT * RTILE;
 #pragma unroll
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         const uint32_t here = (good >> (n % GU * UB)) & (UB == 2 ? 3u : 1u);
         if (here) {
             const uint32_t at0 = ring + slot * SM::SLOT;
-            const int t0 = int(place - PAT_ITEM) * (PAGES_BLOCK * UB);
+            const int t0 = int(place - SM::ITEM) * (PAGES_BLOCK * UB);
             // some query does not see all of the unit's tokens
             const bool tail = t0 + PAGES_BLOCK * UB > len - (a.m - 1) || (UB == 2 && here != 3u);
             if (Q8 && tail) {
@@ -839,41 +841,49 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     if (tail) {
                         // tokens of the block that some query does not see: zeros where
                         // none sees them; one that holds Inf or NaN is added by itself
-                        // to the queries that see it (0 * Inf would reach the others)
-                        const int nv = len - t0;
-                        for (int t = max(nv - (a.m - 1), 0); t < PAGES_BLOCK; ++t) {
-                            const uint32_t va = at + B::OFF_V + uint32_t(t) * B::VROW;
-                            bool odd = t >= nv;
-                            if (!odd) {
-                                bool inf = false;
-                                for (int c = lane; c < D / 2; c += 32) {
-                                    const uint32_t w = lds32(va + 4u * uint32_t(c));
-                                    inf |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-                                }
-                                odd = __any_sync(0xffffffffu, inf);
-                                if (odd) {
+                        // to the queries that see it (0 * Inf would reach the others).
+                        // Two lanes look at a token, each at half of its row, every lane
+                        // from another 16 bytes on, for the banks.
+                        constexpr uint32_t CHUNKS = B::VROW / 32;
+                        const int nv = len - t0, tl = lane >> 1;
+                        const uint32_t half = at + B::OFF_V + uint32_t(tl) * B::VROW + uint32_t(lane & 1) * (B::VROW / 2);
+                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);  // NaN once a value is Inf or NaN
+                        if (tl >= nv - (a.m - 1) && tl < nv) {
 #pragma unroll
-                                    for (int r = 0; r < R8; ++r)
+                            for (uint32_t k = 0; k < CHUNKS; ++k) {
+                                const uint4 v = lds128(half + 16u * ((k + uint32_t(lane)) % CHUNKS));
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                        for (int c = 0; c < CQ; ++c) {
-                                            // the token's weight is with lane row t % 8
-                                            const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][CQ + c],
-                                                                        ((t & 7) << 2) | tig);
-                                            if (t0 + t >= lim[r][c]) continue;
-#pragma unroll
-                                            for (int k = 0; k < MT; ++k)
-#pragma unroll
-                                                for (int h = 0; h < 2; ++h) {  // dims 16 k + 8 h + g
-                                                    const uint32_t d2 = uint32_t(k) * 32u + uint32_t(h) * 16u + uint32_t(g >> 1) * 4u;
-                                                    const uint32_t y = lds32(at + B::value(uint32_t(t), d2));
-                                                    acc[k][r][2 * h + c] =
-                                                        fmaf(w, g & 1 ? bf16_hi(y) : bf16_lo(y), acc[k][r][2 * h + c]);
-                                                }
-                                        }
-                                    __syncwarp();
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
                             }
-                            if (odd && lane < D / 8) sts128_zero(va + 16u * uint32_t(lane));
+                        }
+                        uint32_t bits = __ballot_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u);
+                        bits = (bits | bits >> 1) & 0x55555555u;  // bit 2 t: token t
+                        for (uint32_t left = bits; left; left &= left - 1u) {
+                            const int t = (__ffs(int(left)) - 1) >> 1;
+#pragma unroll
+                            for (int r = 0; r < R8; ++r)
+#pragma unroll
+                                for (int c = 0; c < CQ; ++c) {
+                                    // the token's weight is with lane row t % 8
+                                    const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][CQ + c],
+                                                                ((t & 7) << 2) | tig);
+                                    if (t0 + t >= lim[r][c]) continue;
+#pragma unroll
+                                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) {  // dims 16 k + 8 h + g
+                                            const uint32_t d2 = uint32_t(k) * 32u + uint32_t(h) * 16u + uint32_t(g >> 1) * 4u;
+                                            const uint32_t y = lds32(at + B::value(uint32_t(t), d2));
+                                            acc[k][r][2 * h + c] = fmaf(w, g & 1 ? bf16_hi(y) : bf16_lo(y), acc[k][r][2 * h + c]);
+                                        }
+                                }
+                        }
+                        __syncwarp();
+                        if (tl >= nv || ((bits >> (lane & 30)) & 1u)) {
+#pragma unroll
+                            for (uint32_t k = 0; k < CHUNKS; ++k) sts128_zero(half + 16u * ((k + uint32_t(lane)) % CHUNKS));
                         }
                         fence_proxy_async();  // before a later copy into the slot
                         __syncwarp();
