@@ -22,7 +22,7 @@
 // (running maximum, sum and weighted values) and pages_join merges them in list
 // order, so results do not depend on timing.  Where the tables are short, a team of
 // a thread block's warps takes each row tile instead and merges it in shared
-// memory, in one launch (team_units says when).
+// memory, in one launch (team_blocks says when).
 //
 // A warp's units arrive by bulk copies, one per unit (the blocks of a head's tokens
 // in a page are one run of bytes), in the warp's own ring in shared memory, on the
@@ -87,7 +87,8 @@ struct PagesAttendArgs {
     int nseq, m, nq, G, R, RT, max_pages;
     int unit;  // tokens of a unit
     uint32_t nwarps, polls;
-    int team;  // warps of a row tile where it is not cut from the list
+    int team;       // warps of a row tile where it is not cut from the list
+    int join_rows;  // rows of a block of pages_join
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -1058,8 +1059,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 }
 
 // Merges the partial results of the rows whose blocks several warps had, and
-// writes the rows of empty sequences.  One block per query row; its WARPS warps
-// take every WARPS-th partial, eight of them in flight at a time.  A block finds
+// writes the rows of empty sequences.  A block takes a.join_rows rows of a row
+// tile, one after the other; its WARPS warps take every WARPS-th partial, eight of
+// them in flight at a time.  A block finds
 // out what it has to merge before pages_attend has ended (up to PAT_OWN_PLAN
 // sequences; beyond, from the plan that pages_attend leaves), and all but block 0
 // leave at once if that is nothing: block 0 stays for pages_attend's end, so that
@@ -1069,11 +1071,11 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     constexpr int VPL = D / 32, DEEP = 8;  // values of a lane
     __shared__ float macc[WARPS][D], mst[WARPS][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t row = blockIdx.x;
-    const int j = int(row % uint32_t(a.nq)), i = int(row / uint32_t(a.nq) % uint32_t(a.m));
-    const uint32_t b = uint32_t(row / (uint64_t(a.nq) * uint32_t(a.m)));
-    const int h = j / a.G, r = i * a.G + j % a.G, rt = r / RTILE;
     const uint32_t HRT = uint32_t(a.pv.H) * uint32_t(a.RT);
+    const uint32_t splits = uint32_t(min(RTILE, a.R) + a.join_rows - 1) / uint32_t(a.join_rows);  // blocks of a row tile
+    const uint32_t task = blockIdx.x / splits, b = task / HRT;
+    const int h = int(task % HRT) / a.RT, rt = int(task % HRT) % a.RT;
+    const int r0 = rt * RTILE + int(blockIdx.x % splits) * a.join_rows;
     // the next attention's blocks may be placed; they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint32_t before = 0, n = 0, all = 0;
@@ -1096,71 +1098,77 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     const uint64_t first = uint64_t(before) * HRT + uint64_t(h * a.RT + rt) * n;
     const uint64_t w0 = first / per, w1 = n ? (first + n - 1) / per : w0;
     const bool whole = n && w0 == w1;  // one warp had it all
-    if (whole && row) return;
+    if (whole && blockIdx.x) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (whole || !pages_match(a.pv)) return;
     const uint32_t parts = n ? uint32_t(w1 - w0 + 1) : 0u;
-    float acc[VPL], M = -INFINITY, L = 0.0f;
+    for (int r = r0; r < min(min(r0 + a.join_rows, rt * RTILE + RTILE), a.R); ++r) {
+        float acc[VPL], M = -INFINITY, L = 0.0f;
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
-    for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += DEEP * WARPS) {
-        float2 st[DEEP];
-        float v[DEEP][VPL];
+        for (int k = 0; k < VPL; ++k) acc[k] = 0.0f;
+        for (uint32_t c0 = uint32_t(warp); c0 < parts; c0 += DEEP * WARPS) {
+            float2 st[DEEP];
+            float v[DEEP][VPL];
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k) {
-            const uint32_t c = c0 + uint32_t(k * WARPS);
-            st[k] = make_float2(-INFINITY, 0.0f);
+            for (int k = 0; k < DEEP; ++k) {
+                const uint32_t c = c0 + uint32_t(k * WARPS);
+                st[k] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) v[k][u] = 0.0f;
-            if (c < parts) {
-                const uint64_t w = w0 + c;
-                const uint64_t ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
-                st[k] = __ldcg(a.stats + ps);
-                const float *src = a.part + ps * D + lane * VPL;
-                if constexpr (VPL == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                    v[k][0] = x.x, v[k][1] = x.y, v[k][VPL - 2] = x.z, v[k][VPL - 1] = x.w;
-                } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                    v[k][0] = x.x, v[k][1] = x.y;
+                for (int u = 0; u < VPL; ++u) v[k][u] = 0.0f;
+                if (c < parts) {
+                    const uint64_t w = w0 + c;
+                    const uint64_t ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
+                    st[k] = __ldcg(a.stats + ps);
+                    const float *src = a.part + ps * D + lane * VPL;
+                    if constexpr (VPL == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                        v[k][0] = x.x, v[k][1] = x.y, v[k][VPL - 2] = x.z, v[k][VPL - 1] = x.w;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                        v[k][0] = x.x, v[k][1] = x.y;
+                    }
                 }
             }
+            float nm = M;
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) nm = fmaxf(nm, st[k].x);
+            const float f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
+            M = nm, L *= f0;
+#pragma unroll
+            for (int u = 0; u < VPL; ++u) acc[u] *= f0;
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+                if (st[k].x == -INFINITY) continue;  // an empty part
+                const float f = exp2f(st[k].x - nm);
+                L = fmaf(f, st[k].y, L);
+#pragma unroll
+                for (int u = 0; u < VPL; ++u) acc[u] = fmaf(f, v[k][u], acc[u]);
+            }
         }
-        float nm = M;
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k) nm = fmaxf(nm, st[k].x);
-        const float f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
-        M = nm, L *= f0;
+        for (int k = 0; k < VPL; ++k) macc[warp][lane * VPL + k] = acc[k];
+        if (lane == 0) mst[warp][0] = M, mst[warp][1] = L;
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float top = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int u = 0; u < VPL; ++u) acc[u] *= f0;
+            for (int k = 0; k < WARPS; ++k) top = fmaxf(top, mst[k][0]);
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k) {
-            if (st[k].x == -INFINITY) continue;  // an empty part
-            const float f = exp2f(st[k].x - nm);
-            L = fmaf(f, st[k].y, L);
-#pragma unroll
-            for (int u = 0; u < VPL; ++u) acc[u] = fmaf(f, v[k][u], acc[u]);
+            for (int k = 0; k < WARPS; ++k) {
+                const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
+                l = fmaf(f, mst[k][1], l);
+                o = fmaf(f, macc[k][threadIdx.x], o);
+            }
+            const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
+            const int i = r / a.G, j = h * a.G + r - i * a.G;
+            const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+            const float2 w = join_base(a, row, lse, threadIdx.x == 0);
+            o *= l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+            if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
+            reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
         }
+        __syncthreads();  // the next row writes macc again
     }
-#pragma unroll
-    for (int k = 0; k < VPL; ++k) macc[warp][lane * VPL + k] = acc[k];
-    if (lane == 0) mst[warp][0] = M, mst[warp][1] = L;
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float top = -INFINITY, l = 0.0f, o = 0.0f;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, mst[k][0]);
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-        const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
-        l = fmaf(f, mst[k][1], l);
-        o = fmaf(f, macc[k][threadIdx.x], o);
-    }
-    const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
-    const float2 w = join_base(a, row, lse, threadIdx.x == 0);
-    o *= l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
-    if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
-    reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
 }
 
 static thread_local uint32_t g_next_polls = 0;
@@ -1177,21 +1185,21 @@ static int tile_rows(int rows, int format) {
     return eights == 1 || (format != KVP_PAGES_BF16 && eights % 2 == 1) ? 8 : 16;
 }
 
-// Units of a team's warp up to which a team per row tile beats equal runs of the
+// Blocks of a team's warp up to which a team per row tile beats equal runs of the
 // list.  It has one launch and nothing cut, but waits for the longest sequence, so
 // that the limits are below where equal lengths lose.  Where teams employ half of
 // the GPU's warps or more (us, teams against runs, of 8 KV heads): k8v8 at 128, 64
-// x 700 tokens (7.3 units) 25 and 30, lengths of 1 to 700 22 and 23, 64 x 1500 (16)
+// x 700 tokens (15 blocks) 25 and 30, lengths of 1 to 700 22 and 23, 64 x 1500 (31)
 // 43 and 46, but lengths of 1 to 1500 38 and 32; bf16 at 128, 120 x 200 (13) 21 and
 // 37, 64 x 700 (22) 33 and 40, lengths of 1 to 700 22 and 27; k8v4 at 64, 64 x 1500
-// (12) 26 and 31, lengths of 1 to 1500 22 and 24, 120 x 1500 (24) 45 and 52, lengths
-// of 1 to 1500 38 and 38.  Where they employ fewer: one sequence of 700 tokens (k8v8,
-// 2 units) 8.8 and 8.9, of 1500 13.3 and 9.1; bf16 700 (6) 7.5 and 7.2, 200 (2) 5.2
-// and 7.0.
+// (24) 26 and 31, lengths of 1 to 1500 22 and 24.  With more row tiles than the GPU
+// has warps, in several waves: 64 x 200 of 64 rows (13, k8v8 at 128) 50 and 90, 512 x
+// 200 of 4 rows 62 and 66, 2000 x 30 61 and 77.  Where they employ fewer: one
+// sequence of 700 tokens (k8v8, 4 blocks) 8.8 and 8.9, of 1500 (8) 13.3 and 9.1;
+// bf16 700 (6) 7.5 and 7.2, 200 (2) 5.2 and 7.0.
 template <int D, int FMT>
-static int team_units(bool half) {
-    if (FMT == KVP_PAGES_BF16) return half ? 24 : 4;
-    return half ? (D == 128 ? 8 : 12) : 2;
+static int team_blocks(bool half) {
+    return half ? (FMT != KVP_PAGES_BF16 && D == 128 ? 16 : 24) : 4;
 }
 
 template <int D, int FMT, int RC, bool SOLO>
@@ -1228,18 +1236,27 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     a.nwarps = attend_grid() * SM::WARPS;
     a.unit = PAGES_BLOCK * SM::UB;
     const unsigned tiles = unsigned(a.nseq) * unsigned(a.pv.H) * unsigned(a.RT);
-    // the largest team of warps for which one wave of blocks holds all tiles
+    // the largest team of warps for which one wave of blocks holds all tiles, or one
+    // warp and several waves
     a.team = SM::WARPS;
-    while (a.team > 0 && (SM::WARPS % a.team || uint64_t(attend_grid()) * unsigned(SM::WARPS / a.team) < tiles)) --a.team;
-    const int64_t most = ((int64_t(a.max_pages) << a.pv.logP) + a.unit - 1) / a.unit;  // units that a table may hold
-    if (a.team > 0 && most <= int64_t(team_units<D, FMT>(2 * uint64_t(tiles) * a.team >= a.nwarps)) * a.team) {
+    while (a.team > 1 && (SM::WARPS % a.team || uint64_t(attend_grid()) * unsigned(SM::WARPS / a.team) < tiles)) --a.team;
+    const int64_t most = (int64_t(a.max_pages) << a.pv.logP) / PAGES_BLOCK;  // blocks that a table may hold
+    if (most <= int64_t(team_blocks<D, FMT>(2 * uint64_t(tiles) * a.team >= a.nwarps)) * a.team) {
         const unsigned per_block = unsigned(SM::WARPS / a.team);
         const int rc = launch_tiles<D, FMT, RC, true>(cfg, a, (tiles + per_block - 1) / per_block);
         return rc == KVP_OK ? launch_status() : rc;
     }
     const int rc = launch_tiles<D, FMT, RC, false>(cfg, a, attend_grid());
     if (rc != KVP_OK) return rc;
-    cfg.gridDim = dim3(unsigned(a.nseq) * unsigned(a.m) * unsigned(a.nq));
+    // Rows of a row tile to a block, so that about a wave of blocks does (one row a
+    // block: 64 x 200 tokens of 64 rows 131 us, 90 so, 15 x 4096 177 and 171; of 4
+    // rows 19.9 and 19.0; with 16 instead of 12 blocks an SM 19.9, with 8 as with 12).
+    const unsigned rows = unsigned(std::min(RC, a.R));
+    const uint64_t wave = uint64_t(attend_grid()) * 12u;
+    const unsigned most_rows = unsigned(std::min<uint64_t>(rows, (uint64_t(tiles) * rows + wave - 1) / wave));
+    const unsigned splits = (rows + most_rows - 1) / most_rows;
+    a.join_rows = int((rows + splits - 1) / splits);
+    cfg.gridDim = dim3(tiles * splits);
     cfg.dynamicSmemBytes = 0;
     // Warps for a row's partials, of which it has about nwarps / (row tiles): 16
     // where there are 64 or more of them, 8 a warp in flight (one 128K sequence, 300

@@ -752,3 +752,24 @@ def test_attend_by_number_of_row_tiles(fmt, d, n, m, nq):
     out, lse = pg.attend(q.cuda(), 0.1, bo.cuda(), bl.cuda())
     _check_attend(out, lse, _f64(q), ks, vs, lens, 0.1, (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
     assert pg.status() == kv.KVP_OK
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("roomy", [False, True])
+def test_attend_many_rows_of_many_sequences(fmt, roomy):
+    """Several waves of row tiles (a short table), and several rows to a block of
+    the merge (a roomy one)."""
+    H, d, n, m, nq = 4, 64, 90, 16, 16
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 90, n)]
+    lens[3] = 0
+    pg = Pages(fmt, H, d, 16, lens, seed=3, max_pages=4096 if roomy else None)
+    k, v = _kv(sum(lens), H, d, 26)
+    pg.append(k, v, outs=False)
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn(n, m, nq, d, generator=g).to(torch.bfloat16)
+    bo, bl = torch.randn(q.shape, generator=g), torch.randn(q.shape[:3], generator=g) * 3
+    out, lse = pg.attend(q.cuda(), 0.1, bo.cuda(), bl.cuda())
+    _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), fmt, False), lens), _split(P.held(_f64(v), fmt, True), lens),
+                  lens, 0.1, (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+    assert pg.status() == kv.KVP_OK
