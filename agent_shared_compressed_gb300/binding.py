@@ -125,6 +125,7 @@ _SIGS = {
     "kvp_test_limit_next_attend": (C.c_int, [C.c_uint32]),
     "kvp_test_limit_next_unpack": (C.c_int, [C.c_uint32]),
     "kvp_test_limit_next_pages_attend": (C.c_int, [C.c_uint32]),
+    "kvp_test_limit_next_pages_attend_lanes": (C.c_int, [C.c_uint32, C.c_uint32]),
 }
 
 _lib = None
@@ -393,6 +394,10 @@ def kvp_test_limit_next_unpack(polls):
 
 def kvp_test_limit_next_pages_attend(polls):
     return load().kvp_test_limit_next_pages_attend(int(polls))
+
+
+def kvp_test_limit_next_pages_attend_lanes(polls, lanes):
+    return load().kvp_test_limit_next_pages_attend_lanes(int(polls), int(lanes))
 
 
 class KVPError(RuntimeError):

@@ -86,7 +86,8 @@ struct PagesAttendArgs {
     float scale2;    // scale * log2(e)
     int nseq, m, nq, G, R, RT, max_pages;
     int unit;  // tokens of a unit
-    uint32_t nwarps, polls;
+    uint32_t nwarps;
+    uint32_t polls, poll_lanes;  // polls of a copy by these lanes of a warp (the others': PAT_WAIT_LIMIT)
     int team;       // warps of a row tile where it is not cut from the list
     int join_rows;  // rows of a block of pages_join
 };
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                               : B::value(uint32_t((lane & 7) + ((lane >> 4) << 3)), uint32_t((lane >> 3) & 1) * 16u);
     const uint32_t v_odd = Q8 ? B::value(uint32_t(2 * tig + 1), uint32_t(g) * (B::VROW / 8)) : 0u;
     const uint32_t prep = smem_addr(sm) + SM::OFF_PREP + uint32_t(warp) * SM::PREP;
+    const uint32_t polls = (a.poll_lanes >> lane) & 1u ? a.polls : PAT_WAIT_LIMIT;
 
     // The segment's state.  Query 8 t + 2 tig + c of the tile is column (t, c); of a
     // tile of 4, query tig.
@@ -587,7 +589,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         for (int c = 0; c < CQ; ++c) zsum[k][t][c] = 0.0f;
             }
         }
-        if (!mbar_wait(bar + 8u * slot, phase, a.polls)) {
+        // Every lane polls (and so sees the copied bytes), but whether the copy came
+        // in time is the warp's decision: a lane that gave up by itself would be
+        // missing from the votes, shuffles and products that the others go on to.
+        if (!__all_sync(0xffffffffu, mbar_wait(bar + 8u * slot, phase, polls))) {
             // a copy did not arrive in time: report it, let the copies in flight
             // land (with the normal limit), and give the run up
             if (lane == 0) {
@@ -1171,7 +1176,7 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     }
 }
 
-static thread_local uint32_t g_next_polls = 0;
+static thread_local uint32_t g_next_polls = 0, g_next_lanes = 0;
 static thread_local bool g_limit_next = false;
 
 static unsigned attend_grid() { return unsigned(sm_count()); }
@@ -1310,10 +1315,14 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
     return size_t(attend_ws(cfg, n_seqs, n_q_tokens, n_q_heads).total);
 }
 
-int kvp_test_limit_next_pages_attend(uint32_t polls) {
-    g_next_polls = polls;
+int kvp_test_limit_next_pages_attend_lanes(uint32_t polls, uint32_t lanes) {
+    g_next_polls = polls, g_next_lanes = lanes;
     g_limit_next = true;
     return KVP_OK;
+}
+
+int kvp_test_limit_next_pages_attend(uint32_t polls) {
+    return kvp_test_limit_next_pages_attend_lanes(polls, 0xFFFFFFFFu);
 }
 
 int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
@@ -1349,6 +1358,7 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
     a.RT = (a.R + rows - 1) / rows;
     a.max_pages = max_pages;
     a.polls = g_limit_next ? g_next_polls : PAT_WAIT_LIMIT;
+    a.poll_lanes = g_limit_next ? g_next_lanes : 0xFFFFFFFFu;
     g_limit_next = false;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool d128 = cfg->head_dim == 128;

@@ -551,6 +551,11 @@ int kvp_test_limit_next_unpack(uint32_t polls);
  * reports KVP_ERR_TIMEOUT and the CUDA context stays usable.  Returns KVP_OK. */
 int kvp_test_limit_next_pages_attend(uint32_t polls);
 
+/* The same for the lanes of every warp whose bits are set in `lanes`; the other
+ * lanes wait with the normal limit.  A warp gives up if any of its lanes does:
+ * with one bit set the outcome is that of kvp_test_limit_next_pages_attend. */
+int kvp_test_limit_next_pages_attend_lanes(uint32_t polls, uint32_t lanes);
+
 #ifdef __cplusplus
 }
 #endif
