@@ -115,6 +115,39 @@ __device__ __forceinline__ uint32_t ld_stream_u32(const void *p) {
     return r;
 }
 
+// Loads of memory that the kernel before a programmatic dependent launch writes, or
+// the kernel itself: coherent, and never moved above the launch's wait.  (The .nc
+// loads above are for memory that nothing writes while the kernel is resident, which
+// it is from before that wait.)  ld_once: data read once; ld_l2: by way of L2 only, as
+// what is read before the kernel's own wait has to be.
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint2 ld_once_v2(const void *p) {
+    uint2 r;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_plain_u32(const void *p) {
+    uint32_t r;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 ld_l2_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_l2_u32(const void *p) {
+    uint32_t r;
+    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+
 // L2 eviction-priority policies for loads: keep (evict_last) data that is read
 // again soon, drop (evict_first) data read for the last time.
 __device__ __forceinline__ uint64_t l2_evict_last_policy() {

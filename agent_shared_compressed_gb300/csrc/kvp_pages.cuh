@@ -155,10 +155,10 @@ __device__ __forceinline__ void store_key8(uint8_t *blk, uint32_t t, int tig, co
 template <int D, int FMT>
 __device__ __forceinline__ void load_key8(const uint8_t *blk, uint32_t t, int tig, Lane8<D> &c) {
     using B = Block<D, FMT>;
-    const uint4 a = ld_stream_v4(blk + B::key(t, tig * (D / 4)));
+    const uint4 a = ld_once_v4(blk + B::key(t, tig * (D / 4)));
     c.w[0][0] = a.x, c.w[0][1] = a.y, c.w[1][0] = a.z, c.w[1][1] = a.w;
     if constexpr (D == 128) {
-        const uint4 b = ld_stream_v4(blk + B::key(t, tig * 32 + 16));
+        const uint4 b = ld_once_v4(blk + B::key(t, tig * 32 + 16));
         c.w[2][0] = b.x, c.w[2][1] = b.y, c.w[3][0] = b.z, c.w[3][1] = b.w;
     }
 }
@@ -177,11 +177,11 @@ template <int D, int FMT>
 __device__ __forceinline__ void load_value8(const uint8_t *blk, uint32_t t, int tig, Lane8<D> &c) {
     using B = Block<D, FMT>;
     if constexpr (D == 128) {
-        const uint4 a = ld_stream_v4(blk + B::value(t, tig * 32)), b = ld_stream_v4(blk + B::value(t, tig * 32 + 16));
+        const uint4 a = ld_once_v4(blk + B::value(t, tig * 32)), b = ld_once_v4(blk + B::value(t, tig * 32 + 16));
         c.w[0][0] = a.x, c.w[1][0] = a.y, c.w[2][0] = a.z, c.w[3][0] = a.w;
         c.w[0][1] = b.x, c.w[1][1] = b.y, c.w[2][1] = b.z, c.w[3][1] = b.w;
     } else {
-        const uint4 a = ld_stream_v4(blk + B::value(t, tig * 16));
+        const uint4 a = ld_once_v4(blk + B::value(t, tig * 16));
         c.w[0][0] = a.x, c.w[1][0] = a.y, c.w[0][1] = a.z, c.w[1][1] = a.w;
     }
 }
@@ -207,10 +207,10 @@ __device__ __forceinline__ void load_value4(const uint8_t *blk, uint32_t t, int 
     using B = Block<D, FMT>;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if constexpr (D == 128) {
-        const uint4 a = ld_stream_v4(blk + B::value(t, tig * 16));
+        const uint4 a = ld_once_v4(blk + B::value(t, tig * 16));
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     } else {
-        const uint2 a = ld_stream_v2(blk + B::value(t, tig * 8));
+        const uint2 a = ld_once_v2(blk + B::value(t, tig * 8));
         w[0] = a.x, w[1] = a.y;
     }
 #pragma unroll
@@ -266,7 +266,7 @@ __device__ __forceinline__ void load_key_row(const uint8_t *blk, uint32_t t, int
     if constexpr (!B::Q8) {
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
-            const uint4 v = ld_stream_v4(blk + B::key(t, (4 * b + tig) * 16));
+            const uint4 v = ld_once_v4(blk + B::key(t, (4 * b + tig) * 16));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[b][2 * i] = bf16_lo(w[i]), x[b][2 * i + 1] = bf16_hi(w[i]);
@@ -293,7 +293,7 @@ __device__ __forceinline__ void load_value_row(const uint8_t *blk, uint32_t t, i
     if constexpr (!B::Q8) {
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
-            const uint4 v = ld_stream_v4(blk + B::value(t, (4 * b + tig) * 16));
+            const uint4 v = ld_once_v4(blk + B::value(t, (4 * b + tig) * 16));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[b][2 * i] = bf16_lo(w[i]), x[b][2 * i + 1] = bf16_hi(w[i]);

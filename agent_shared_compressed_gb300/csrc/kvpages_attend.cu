@@ -232,9 +232,11 @@ __device__ __forceinline__ float rows_top(float x) {
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 
-// The length that a sequence's table row can hold.
+// The length that a sequence's table row can hold.  EARLY: read before the kernel's
+// own wait (the kernel before it has passed its own).
+template <bool EARLY = false>
 __device__ __forceinline__ int seq_len(const PagesAttendArgs &a, int b, bool flag) {
-    const int len = max(__ldg(a.lens + b), 0);
+    const int len = max(int(EARLY ? ld_l2_u32(a.lens + b) : ld_plain_u32(a.lens + b)), 0);
     const int64_t cap = int64_t(a.max_pages) << a.pv.logP;
     if (int64_t(len) <= cap) return len;
     if (flag) pages_flag(a.pv, FLAG_PAGE);
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (at < SM::ITEM) return 0;
         const uint32_t t0 = ((at - SM::ITEM) * UB + uint32_t(lane % UB)) * PAGES_BLOCK;
         if (UB > 1 && t0 >= uint32_t(seq_len(a, b, false))) return 0;
-        const int page = __ldg(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP));
+        const int page = int(ld_plain_u32(a.table + uint64_t(b) * uint32_t(a.max_pages) + (t0 >> a.pv.logP)));
         if (page < 0 || page >= a.pv.n_pages) {
             pages_flag(a.pv, FLAG_PAGE);
             return 0;
@@ -518,13 +520,13 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
             if constexpr (Q8) {
 #pragma unroll
                 for (int k = 0; k < NG; ++k)
-                    qraw[k][t] = real ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * k + 8 * tig)) : make_uint4(0, 0, 0, 0);
+                    qraw[k][t] = real ? ld_once_v4(qrow + 32 * k + 8 * tig) : make_uint4(0, 0, 0, 0);
             } else {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        qf[k][t][e] = real ? __ldg(reinterpret_cast<const uint32_t *>(qrow + 16 * k + 8 * e + 2 * tig)) : 0u;
+                        qf[k][t][e] = real ? ld_plain_u32(qrow + 16 * k + 8 * e + 2 * tig) : 0u;
             }
         }
     };
@@ -1087,7 +1089,7 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
     if (a.nseq <= PAT_OWN_PLAN) {
         // pages_attend has passed its own wait, so the lengths are final
         for (int k = lane; k < a.nseq; k += 32) {
-            const uint32_t u = tile_units(seq_len(a, k, false), a.unit);
+            const uint32_t u = tile_units(seq_len<true>(a, k, false), a.unit);
             all += u;
             before += k < int(b) ? u : 0u;
             n += k == int(b) ? u : 0u;
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
         n = __reduce_add_sync(0xffffffffu, n);
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        before = __ldcg(a.plan + b), n = __ldcg(a.plan + b + 1) - before, all = __ldcg(a.plan + a.nseq);
+        before = ld_l2_u32(a.plan + b), n = ld_l2_u32(a.plan + b + 1) - before, all = ld_l2_u32(a.plan + a.nseq);
     }
     const uint64_t per = run_length(uint64_t(all) * HRT, a.nwarps);
     const uint64_t first = uint64_t(before) * HRT + uint64_t(h * a.RT + rt) * n;
@@ -1123,14 +1125,16 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
                 if (c < parts) {
                     const uint64_t w = w0 + c;
                     const uint64_t ps = (w * 2u + (first > w * per ? 1u : 0u)) * RTILE + uint32_t(r % RTILE);
-                    st[k] = __ldcg(a.stats + ps);
+                    const uint2 s = ld_once_v2(a.stats + ps);
+                    st[k] = make_float2(__uint_as_float(s.x), __uint_as_float(s.y));
                     const float *src = a.part + ps * D + lane * VPL;
                     if constexpr (VPL == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                        v[k][0] = x.x, v[k][1] = x.y, v[k][VPL - 2] = x.z, v[k][VPL - 1] = x.w;
+                        const uint4 x = ld_once_v4(src);
+                        v[k][0] = __uint_as_float(x.x), v[k][1] = __uint_as_float(x.y);
+                        v[k][VPL - 2] = __uint_as_float(x.z), v[k][VPL - 1] = __uint_as_float(x.w);
                     } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                        v[k][0] = x.x, v[k][1] = x.y;
+                        const uint2 x = ld_once_v2(src);
+                        v[k][0] = __uint_as_float(x.x), v[k][1] = __uint_as_float(x.y);
                     }
                 }
             }
