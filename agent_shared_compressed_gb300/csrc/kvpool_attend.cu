@@ -642,16 +642,19 @@ __global__ void __launch_bounds__(ATT_THREADS, 2) attend_split(const __grid_cons
     // Launched as a programmatic dependent of whatever precedes it on the
     // stream, and waits for it (griddepcontrol.wait) before it reads the
     // queries or writes its workspace.  The pool (and a LoRA cache) is read
-    // before that wait: the only kernel that lets this grid start early is the
-    // combine of a previous attention call, which writes neither, and any
-    // other kernel before it (an encode, a caller's kernel) has completed
-    // before this grid starts.
+    // before that wait: the kernels that let this grid start early are the
+    // combine of a previous attention call and the page kernels, which write
+    // neither and (or the kernel before them) have waited for all before them,
+    // and any other kernel before it (an encode, a caller's kernel) has
+    // completed before this grid starts.
     const uint32_t *hdr = reinterpret_cast<const uint32_t *>(a.pool);
     const uint32_t kmode = hdr[POOL_KMODE_WORD];
     if (hdr[0] != POOL_MAGIC || hdr[1] != POOL_VERSION || hdr[2] != uint32_t(a.L) || hdr[3] != uint32_t(a.H) ||
         hdr[4] != uint32_t(D) || hdr[5] != uint32_t(a.T) || (kmode != KVP_K_PER_TENSOR && kmode != KVP_K_Q8_0)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && hdr[0] == POOL_MAGIC)
             atomicOr(const_cast<uint32_t *>(hdr) + POOL_ERR_WORD, FLAG_HEADER);
+        // this grid's end means the end of the one before it, to whatever comes next
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     if (kmode == KVP_K_Q8_0)

@@ -22,3 +22,13 @@ def test_no_read_only_loads_of_what_may_be_written(name):
     wants memory nobody writes while the kernel is resident, or that the compiler
     may move above the kernel's wait."""
     assert not re.findall(r"\b__ldg\b|\b__ldc[agsv]\b|\.nc\b|\bld_stream_\w+|\bld_v4_policy\b|__restrict__", _code(name))
+
+
+def test_refused_pool_attention_waits_for_the_kernel_before_it():
+    """Attention over the pool may start while a page write runs.  If it finds
+    another pool than the caller described it still ends after that write: what
+    comes next in the stream waits for its end only."""
+    code = _code("kvpool_attend.cu")
+    at = code.index("hdr[0] != POOL_MAGIC")
+    refusal = code[at:code.index("return;", at)]
+    assert "griddepcontrol.wait;" in refusal
