@@ -336,12 +336,14 @@ __device__ __forceinline__ uint32_t make_plan(const PagesAttendArgs &a, uint32_t
     return carry;
 }
 
-// What one row of a tile ends with: the base joined in, bf16 output and lse.
-__device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t row, float lse, bool first) {
+// What one row of a tile ends with: the base joined in and lse written (by `first`).
+// `bl` is base_lse[row], which may be lse[row]: whoever calls this has read it before
+// any thread gets here.
+__device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t row, float lse, float bl, bool first) {
     // weights of (this, base); an empty row without a base has none
     float wa = 1.0f, wb = 0.0f;
     if (a.base_lse) {
-        const float bl = a.base_lse[row], top = fmaxf(lse, bl);
+        const float top = fmaxf(lse, bl);
         if (top > -INFINITY) {
             const float ea = expf(lse - top), eb = expf(bl - top), tot = ea + eb;
             wa = ea / tot, wb = eb / tot;
@@ -971,8 +973,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
                     const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+                    const float bl = a.base_lse ? a.base_lse[row] : -INFINITY;
+                    __syncwarp(0x11111111u << tig);  // the row's lanes have it before one writes lse
                     const float lse = l > 0.0f ? (base2 + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
-                    const float2 w = join_base(a, row, lse, g == 0);
+                    const float2 w = join_base(a, row, lse, bl, g == 0);
                     const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
                     uint16_t *o = a.out + row * D;
                     const float *bo = a.base_out && w.y != 0.0f ? a.base_out + row * D : nullptr;
@@ -1052,7 +1056,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         const int r = r0 + rr, i = r / a.G, j = h * a.G + r - i * a.G;
         const uint64_t row = (uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
         const float lse = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.0f ? -INFINITY : L);
-        const float2 w = join_base(a, row, lse, lane == 0);
+        const float bl = a.base_lse ? a.base_lse[row] : -INFINITY;
+        __syncwarp();  // every lane has it before one writes lse
+        const float2 w = join_base(a, row, lse, bl, lane == 0);
         const float inv = L > 0.0f ? w.x / L : (L == 0.0f ? 0.0f : L);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
@@ -1157,6 +1163,9 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
 #pragma unroll
         for (int k = 0; k < VPL; ++k) macc[warp][lane * VPL + k] = acc[k];
         if (lane == 0) mst[warp][0] = M, mst[warp][1] = L;
+        const int i = r / a.G, j = h * a.G + r - i * a.G;
+        const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
+        const float bl = a.base_lse ? a.base_lse[row] : -INFINITY;  // before thread 0 writes lse
         __syncthreads();
         if (threadIdx.x < D) {
             float top = -INFINITY, l = 0.0f, o = 0.0f;
@@ -1169,9 +1178,7 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
                 o = fmaf(f, macc[k][threadIdx.x], o);
             }
             const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
-            const int i = r / a.G, j = h * a.G + r - i * a.G;
-            const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
-            const float2 w = join_base(a, row, lse, threadIdx.x == 0);
+            const float2 w = join_base(a, row, lse, bl, threadIdx.x == 0);
             o *= l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
             if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
             reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);

@@ -1,5 +1,5 @@
 """GPU tests of attention over pages where it can go wrong: bounded waits that
-run out for some lanes only."""
+run out for some lanes only, joins in place."""
 import numpy as np
 import pytest
 import torch
@@ -39,3 +39,37 @@ def test_wait_that_runs_out_for_some_lanes(fmt, lanes, roomy):
     assert pg.status() == kv.KVP_OK
     _check_attend(out, lse, _f64(q), _split(P.held(_f64(k), fmt, False), lens), _split(P.held(_f64(v), fmt, True), lens),
                   lens, 0.1)
+
+
+# --- joins -------------------------------------------------------------------------
+
+JOINS = [  # H, d, page, lens, m, query heads, table width: which part of the code ends a row
+    (4, 128, 16, [40, 0, 7, 64], 1, 16, None),       # teams' merges and whole tiles, tiles of 4
+    (4, 64, 16, [150, 3, 0], 3, 8, None),            # of 8
+    (2, 128, 16, [90, 33], 8, 8, None),              # of 16
+    (4, 128, 16, [4000, 0, 2500], 1, 16, 4096),      # cut from the list, joined
+    (2, 64, 16, [3000, 900], 3, 8, 4096),
+    (8, 128, 16, [20] * 300, 1, 32, 4096),           # many whole tiles of the list
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", JOINS)
+def test_join_with_lse_in_place(fmt, case):
+    """lse written over base_lse gives what another tensor for it gives, bit for bit."""
+    H, d, page, lens, m, nq, width = case
+    pg = Pages(fmt, H, d, page, lens, max_pages=width)
+    k, v = _kv(sum(lens), H, d, 31)
+    pg.append(k, v, outs=False)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(len(lens), m, nq, d, generator=g).to(torch.bfloat16).cuda()
+    bo, bl = torch.randn(q.shape, generator=g).cuda(), (torch.randn(q.shape[:3], generator=g) * 3).cuda()
+    out, lse = pg.attend(q, 0.1, bo, bl)
+    wsb = kv.kvpages_attend_workspace_bytes(pg.cfg, len(lens), m, nq)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        o, both = torch.empty_like(q), bl.clone()
+        assert kv.kvpages_attend(pg.buf.t, pg.cfg, 0, len(lens), m, nq, q, 0.1, pg.table_d, pg.max_pages, pg.lens_d, bo,
+                                 both, o, both, ws, wsb) == kv.KVP_OK
+        torch.cuda.synchronize()
+        assert np.array_equal(_f64(o), out) and np.array_equal(both.cpu().numpy().astype(np.float64), lse)
