@@ -343,8 +343,8 @@ __device__ __forceinline__ float2 join_base(const PagesAttendArgs &a, uint64_t r
     // weights of (this, base); an empty row without a base has none
     float wa = 1.0f, wb = 0.0f;
     if (a.base_lse) {
-        const float top = fmaxf(lse, bl);
-        if (top > -INFINITY) {
+        if (!(lse == -INFINITY && bl == -INFINITY)) {
+            const float top = fmaxf(lse, bl);  // of a NaN and a number: the number
             const float ea = expf(lse - top), eb = expf(bl - top), tot = ea + eb;
             wa = ea / tot, wb = eb / tot;
             lse = top + logf(tot);

@@ -73,3 +73,21 @@ def test_join_with_lse_in_place(fmt, case):
                                  both, o, both, ws, wsb) == kv.KVP_OK
         torch.cuda.synchronize()
         assert np.array_equal(_f64(o), out) and np.array_equal(both.cpu().numpy().astype(np.float64), lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("width", [None, 4096])
+def test_base_that_is_not_a_number(fmt, width):
+    """A base whose lse is NaN gives NaN, also for queries that see no token of
+    their own; one whose lse is -inf gives what there is, whatever it holds."""
+    H, nq, d, lens = 2, 4, 64, [0, 40, 0, 40]
+    pg = Pages(fmt, H, d, 16, lens, max_pages=width)
+    k, v = _kv(sum(lens), H, d, 32)
+    pg.append(k, v, outs=False)
+    q = torch.randn(4, 1, nq, d, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    bo, bl = torch.full(q.shape, float("nan"), device="cuda"), torch.full(q.shape[:3], float("nan"), device="cuda")
+    bl[2:] = -float("inf")
+    out, lse = pg.attend(q, 0.1, bo, bl)
+    alone = pg.attend(q, 0.1)
+    assert np.all(np.isnan(lse[:2])) and np.all(np.isnan(out[:2]))
+    assert np.array_equal(lse[2:], alone[1][2:]) and np.array_equal(out[2:], alone[0][2:])
