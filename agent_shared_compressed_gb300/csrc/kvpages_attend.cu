@@ -220,6 +220,9 @@ __device__ __forceinline__ void twin_weights(float w0, float w1, uint32_t &b0, u
     b0 = transpose8(pack_bf16x2(w0, w0 - bf16_lo(h)));
     b1 = transpose8(pack_bf16x2(w1, w1 - bf16_hi(h)));
 }
+// The factor of a weighted sum x when it is scaled by f > 0: f, but 1 where f has
+// underflowed to 0 and x is Inf or NaN (16-bit values may be), which it has to stay.
+__device__ __forceinline__ float factor(float f, float x) { return f == 0.0f && !(fabsf(x) < INFINITY) ? 1.0f : f; }
 // Over the eight lanes of a quad position (the rows of a C fragment).
 __device__ __forceinline__ float rows_add(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -736,10 +739,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         off[t][c] = nr == -INFINITY ? 0.0f : nr;
                         sum[t][c] *= f;
 #pragma unroll
-                        for (int k = 0; k < MT; ++k) {
-                            acc[k][t][c] *= f, acc[k][t][2 + c] *= f;
-                            if constexpr (TWICE) acc[k][t][1] *= f, acc[k][t][3] *= f;
-                        }
+                        for (int k = 0; k < MT; ++k)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (TWICE || (e & 1) == c) acc[k][t][e] *= Q8 ? f : factor(f, acc[k][t][e]);
                         if constexpr (V4) {
 #pragma unroll
                             for (int k = 0; k < NG; ++k) zsum[k][t][c] *= f;
@@ -848,24 +851,39 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
                 } else {
-                    if (tail) {
-                        // tokens of the block that some query does not see: zeros where
-                        // none sees them; one that holds Inf or NaN is added by itself
-                        // to the queries that see it (0 * Inf would reach the others).
-                        // Two lanes look at a token, each at half of its row, every lane
-                        // from another 16 bytes on, for the banks.
+                    // The block's values as operands, and whether one is Inf or NaN.
+                    uint32_t w[MT][4];
+                    auto load_values = [&]() {
+                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);  // NaN once a value is Inf or NaN
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            ldsm4_t(w[k], (at + v_off) ^ (32u * uint32_t(k)));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k][e]), __float2bfloat162_rn(0.0f), odd);
+                        }
+                        return __any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u);
+                    };
+                    if (load_values()) {
+                        // Tokens that hold Inf or NaN are added one by one, in fp32, to the
+                        // queries that see them, and are zeros to the product, whose operands
+                        // may not meet them: 0 * Inf would reach queries that do not see the
+                        // token, and of a weight's two bf16 the second is often 0 or negative.
+                        // So are tokens that were never written, whatever they hold.  Two
+                        // lanes look at a token, each at half of its row, every lane from
+                        // another 16 bytes on, for the banks.
                         constexpr uint32_t CHUNKS = B::VROW / 32;
                         const int nv = len - t0, tl = lane >> 1;
                         const uint32_t half = at + B::OFF_V + uint32_t(tl) * B::VROW + uint32_t(lane & 1) * (B::VROW / 2);
-                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);  // NaN once a value is Inf or NaN
-                        if (tl >= nv - (a.m - 1) && tl < nv) {
+                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
+                        if (tl < nv) {
 #pragma unroll
                             for (uint32_t k = 0; k < CHUNKS; ++k) {
                                 const uint4 v = lds128(half + 16u * ((k + uint32_t(lane)) % CHUNKS));
-                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
+                                    odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[e]), __float2bfloat162_rn(0.0f), odd);
                             }
                         }
                         uint32_t bits = __ballot_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u);
@@ -876,17 +894,20 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                             for (int r = 0; r < R8; ++r)
 #pragma unroll
                                 for (int c = 0; c < CQ; ++c) {
-                                    // the token's weight is with lane row t % 8
-                                    const float w = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][CQ + c],
-                                                                ((t & 7) << 2) | tig);
+                                    // the token's weight and score are with lane row t % 8
+                                    const int from = ((t & 7) << 2) | tig;
+                                    const float pw = __shfl_sync(0xffffffffu, t < 8 ? p[u][r][c] : p[u][r][CQ + c], from);
+                                    const float ps = __shfl_sync(0xffffffffu, t < 8 ? x[u][r][c] : x[u][r][CQ + c], from);
                                     if (t0 + t >= lim[r][c]) continue;
 #pragma unroll
                                     for (int k = 0; k < MT; ++k)
 #pragma unroll
                                         for (int h = 0; h < 2; ++h) {  // dims 16 k + 8 h + g
                                             const uint32_t d2 = uint32_t(k) * 32u + uint32_t(h) * 16u + uint32_t(g >> 1) * 4u;
-                                            const uint32_t y = lds32(at + B::value(uint32_t(t), d2));
-                                            acc[k][r][2 * h + c] = fmaf(w, g & 1 ? bf16_hi(y) : bf16_lo(y), acc[k][r][2 * h + c]);
+                                            const uint32_t y2 = lds32(at + B::value(uint32_t(t), d2));
+                                            const float y = g & 1 ? bf16_hi(y2) : bf16_lo(y2);
+                                            acc[k][r][2 * h + c] =
+                                                fmaf(ps > -INFINITY ? factor(pw, y) : pw, y, acc[k][r][2 * h + c]);
                                         }
                                 }
                         }
@@ -897,6 +918,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                         fence_proxy_async();  // before a later copy into the slot
                         __syncwarp();
+                        load_values();
                     }
                     uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
@@ -910,15 +932,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < MT; ++k) {
-                        uint32_t w[4];
-                        ldsm4_t(w, (at + v_off) ^ (32u * uint32_t(k)));
+                    for (int k = 0; k < MT; ++k)
 #pragma unroll
                         for (int t = 0; t < R8; ++t) {
-                            mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
-                            if constexpr (!TWICE) mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
+                            mma_bf16(acc[k][t], w[k][0], w[k][1], w[k][2], w[k][3], hi[t][0], hi[t][1]);
+                            if constexpr (!TWICE) mma_bf16(acc[k][t], w[k][0], w[k][1], w[k][2], w[k][3], lo[t][0], lo[t][1]);
                         }
-                    }
                 }
             }
         }
@@ -999,7 +1018,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int d = 16 * k + 8 * u + g;
-                                float y = acc[k][t][2 * u + c] * inv;
+                                float y = acc[k][t][2 * u + c] * factor(inv, acc[k][t][2 * u + c]);
                                 if (bo) y = fmaf(w.y, bo[d], y);
                                 reinterpret_cast<__nv_bfloat16 *>(o)[d] = __float2bfloat16_rn(y);
                             }
@@ -1051,7 +1070,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
             const float f = st.x == -INFINITY ? 0.0f : exp2f(st.x - M);
             L = fmaf(f, st.y, L);
 #pragma unroll
-            for (int k = 0; k < VPL; ++k) y[k] = fmaf(f, src[rr * D + lane * VPL + k], y[k]);
+            for (int k = 0; k < VPL; ++k) {
+                const float v = src[rr * D + lane * VPL + k];
+                y[k] = fmaf(Q8 ? f : factor(f, v), v, y[k]);
+            }
         }
         const int r = r0 + rr, i = r / a.G, j = h * a.G + r - i * a.G;
         const uint64_t row = (uint64_t(sb) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
@@ -1062,7 +1084,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         const float inv = L > 0.0f ? w.x / L : (L == 0.0f ? 0.0f : L);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            y[k] *= inv;
+            y[k] *= Q8 ? inv : factor(inv, y[k]);
             if (a.base_out && w.y != 0.0f) y[k] = fmaf(w.y, a.base_out[row * D + lane * VPL + k], y[k]);
         }
 #pragma unroll
@@ -1150,14 +1172,14 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
             const float f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
             M = nm, L *= f0;
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) acc[u] *= f0;
+            for (int u = 0; u < VPL; ++u) acc[u] *= factor(f0, acc[u]);
 #pragma unroll
             for (int k = 0; k < DEEP; ++k) {
                 if (st[k].x == -INFINITY) continue;  // an empty part
                 const float f = exp2f(st[k].x - nm);
                 L = fmaf(f, st[k].y, L);
 #pragma unroll
-                for (int u = 0; u < VPL; ++u) acc[u] = fmaf(f, v[k][u], acc[u]);
+                for (int u = 0; u < VPL; ++u) acc[u] = fmaf(factor(f, v[k][u]), v[k][u], acc[u]);
             }
         }
 #pragma unroll
@@ -1175,11 +1197,11 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
             for (int k = 0; k < WARPS; ++k) {
                 const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
                 l = fmaf(f, mst[k][1], l);
-                o = fmaf(f, macc[k][threadIdx.x], o);
+                o = fmaf(factor(f, macc[k][threadIdx.x]), macc[k][threadIdx.x], o);
             }
             const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
             const float2 w = join_base(a, row, lse, bl, threadIdx.x == 0);
-            o *= l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+            o *= factor(l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l), o);
             if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
             reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
         }

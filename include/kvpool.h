@@ -467,6 +467,8 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  *  out: device bf16 [n_seqs][n_q_tokens][n_q_heads][head_dim].  lse: device
  *    fp32 [n_seqs][n_q_tokens][n_q_heads] or NULL (natural log).  No output may
  *    overlap an input or another output, except that lse may be base_lse.
+ * An Inf or NaN value of a BF16 page is one in its dim for the queries that see
+ * its token (weights are positive, however small), and touches no others.
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  Scores are products of the stored codes accumulated in fp32,
  * softmax statistics fp32; the weights (times the values' scales) enter the

@@ -1,5 +1,5 @@
 """GPU tests of attention over pages where it can go wrong: bounded waits that
-run out for some lanes only, joins in place."""
+run out for some lanes only, joins in place, values that are Inf or NaN."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 import agent_shared_compressed_gb300 as kv
 from agent_shared_compressed_gb300 import build as kvbuild
 import pageshelp as P
-from test_gpu_pages import FMTS, Pages, _check_attend, _f64, _kv, _split
+from test_gpu_pages import FMTS, Pages, _bf16, _check_attend, _f64, _kv, _split
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,85 @@ def test_base_that_is_not_a_number(fmt, width):
     alone = pg.attend(q, 0.1)
     assert np.all(np.isnan(lse[:2])) and np.all(np.isnan(out[:2]))
     assert np.array_equal(lse[2:], alone[1][2:]) and np.array_equal(out[2:], alone[0][2:])
+
+
+# --- values that are Inf or NaN ------------------------------------------------------
+
+def _check_with_infinities(out, lse, q, k, v, lens, scale, base=(None, None)):
+    """A weight is positive, so an Inf value is an Inf of its dim for every query that
+    sees its token (NaN beside an Inf of the other sign or a NaN); the other dims are
+    those without it."""
+    clean = [np.where(np.isfinite(x), x, 0.0) for x in v]
+    ref, ref_lse, mass, reach = P.attend(q, k, clean, lens, scale, *base)
+    B, m, nq, d = q.shape
+    special = np.zeros((B, m, nq, d))
+    for b in range(B):
+        H = v[b].shape[1]
+        for i in range(m):
+            see = v[b][:max(0, lens[b] - (m - 1 - i))].repeat(nq // H, 1)
+            up, down, nan = (f.any(0) for f in (see == np.inf, see == -np.inf, np.isnan(see)))
+            special[b, i][up], special[b, i][down] = np.inf, -np.inf
+            special[b, i][nan | (up & down)] = np.nan
+    odd = special != 0
+    assert np.array_equal(out[odd], special[odd], equal_nan=True)
+    # bf16's half step, and 2^-17 of each weight, with fp32's 2^-19 of a score
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -17 + 2.0 ** -19 * (1 + reach[..., None])) * mass + 1e-30
+    assert np.all(np.abs(out - ref)[~odd] <= tol[~odd])
+    some = np.isfinite(ref_lse)
+    assert np.all(np.abs(lse[some] - ref_lse[some]) <= 2.0 ** -19 * (1 + np.abs(ref_lse[some]) + reach[some]))
+
+
+INFS = [  # H, d, page, lens, m, query heads, table width, places (sequence, token, head, dim, value)
+    (1, 128, 16, [1], 1, 1, None, [(0, 0, 0, 5, 1)]),                        # its weight is 1: the second bf16 is 0
+    (1, 64, 16, [1], 1, 1, None, [(0, 0, 0, 63, -1)]),
+    (2, 128, 16, [45, 0, 200], 1, 8, None, [(0, 3, 0, 0, 1), (0, 44, 1, 9, -1), (2, 100, 1, 77, 1), (2, 30, 0, 7, 0)]),
+    (2, 128, 16, [45, 0, 200], 1, 8, 4096, [(0, 3, 0, 0, 1), (0, 44, 1, 9, -1), (2, 100, 1, 77, 1), (2, 30, 0, 7, 0)]),
+    (2, 64, 32, [130, 65], 4, 8, None, [(0, 129, 0, 1, 1), (0, 128, 0, 2, 1), (0, 5, 1, 3, -1), (1, 64, 0, 4, 0), (1, 0, 1, 5, 1)]),
+    (2, 64, 32, [130, 65], 4, 8, 4096, [(0, 129, 0, 1, 1), (0, 128, 0, 2, 1), (0, 5, 1, 3, -1), (1, 64, 0, 4, 0), (1, 0, 1, 5, 1)]),
+    (1, 128, 16, [70], 8, 4, None, [(0, 63, 0, 1, 1), (0, 64, 0, 1, -1), (0, 66, 0, 8, 1), (0, 9, 0, 100, 1)]),
+    (1, 128, 64, [5000], 1, 4, None, [(0, 0, 0, 1, 1), (0, 2500, 0, 1, 1), (0, 2501, 0, 2, -1), (0, 4999, 0, 127, 1)]),
+    (1, 128, 64, [5000], 1, 4, None, [(0, 17, 0, 1, 1), (0, 3333, 0, 1, -1)]),   # Inf - Inf, in different parts
+]
+
+
+@pytest.mark.parametrize("case", INFS)
+def test_values_that_are_infinite(case):
+    """16-bit pages keep Inf and NaN values: wherever the token lies, and however the
+    work is split, they reach the queries that see it as they are, and no others."""
+    H, d, page, lens, m, nq, width, places = case
+    k, v = _kv(sum(lens), H, d, 33)
+    start = np.cumsum([0] + lens)
+    for b, t, h, x, sign in places:
+        v[int(start[b]) + t, h, x] = sign * float("inf") if sign else float("nan")
+    pg = Pages("bf16", H, d, page, lens, max_pages=width)
+    pg.append(k, v, outs=False)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(len(lens), m, nq, d, generator=g).to(torch.bfloat16)
+    args = (_f64(q), _split(_f64(k), lens), _split(_f64(v), lens), lens, 0.1)
+    _check_with_infinities(*pg.attend(q.cuda(), 0.1), *args)
+    bo, bl = torch.randn(q.shape, generator=g), torch.randn(q.shape[:3], generator=g) * 3
+    _check_with_infinities(*pg.attend(q.cuda(), 0.1, bo.cuda(), bl.cuda()), *args,
+                           (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+    assert pg.status() == kv.KVP_OK
+
+
+@pytest.mark.parametrize("width", [None, 4096])
+@pytest.mark.parametrize("n,at", [(16, 3), (200, 3), (200, 190), (3000, 3), (3000, 2990)])
+def test_infinite_value_of_a_weight_below_fp32(n, at, width):
+    """The Inf token's weight is e^-300 of the others': positive all the same, before
+    and after them, in their block and in another warp's part; and so is the whole
+    sequence's share of a join with a base e^300 above it."""
+    H, d = 1, 128
+    rng = np.random.default_rng(9)
+    k, v = 0.01 * rng.standard_normal((n, H, d)), rng.standard_normal((n, H, d))
+    k[:, :, 0], k[at, :, 0], v[at, :, 6] = 10.0, -20.0, np.inf
+    k, v = _bf16(k).cuda(), _bf16(v).cuda()
+    q = torch.zeros(1, 1, 4, d, dtype=torch.bfloat16)
+    q[..., 0] = 10.0
+    pg = Pages("bf16", H, d, 16, [n], max_pages=width)
+    pg.append(k, v, outs=False)
+    args = (_f64(q), [_f64(k)], [_f64(v)], [n], 1.0)
+    _check_with_infinities(*pg.attend(q.cuda(), 1.0), *args)
+    bo, bl = torch.randn(q.shape, generator=torch.Generator().manual_seed(5)), torch.full(q.shape[:3], 400.0)
+    _check_with_infinities(*pg.attend(q.cuda(), 1.0, bo.cuda(), bl.cuda()), *args,
+                           (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
