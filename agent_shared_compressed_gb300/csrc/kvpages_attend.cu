@@ -223,6 +223,15 @@ __device__ __forceinline__ void twin_weights(float w0, float w1, uint32_t &b0, u
 // The factor of a weighted sum x when it is scaled by f > 0: f, but 1 where f has
 // underflowed to 0 and x is Inf or NaN (16-bit values may be), which it has to stay.
 __device__ __forceinline__ float factor(float f, float x) { return f == 0.0f && !(fabsf(x) < INFINITY) ? 1.0f : f; }
+// sq + w^2 of a pair of bf16, and whether one of a pair is Inf or NaN.
+__device__ __forceinline__ __nv_bfloat162 square_sum(uint32_t w, __nv_bfloat162 sq) {
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&w);
+    return __hfma2(v, v, sq);
+}
+__device__ __forceinline__ bool not_finite(__nv_bfloat162 v) {
+    const __nv_bfloat162 z = __hmul2(v, __float2bfloat162_rn(0.0f));  // 0 or -0, else NaN
+    return (*reinterpret_cast<const uint32_t *>(&z) & 0x7FFF7FFFu) != 0u;
+}
 // Over the eight lanes of a quad position (the rows of a C fragment).
 __device__ __forceinline__ float rows_add(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -508,6 +517,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     int lim[R8][CQ];             // tokens that the query sees
     float ref[R8][CQ];           // running maximum score, raised lazily
     float bar2[R8][CQ], off[R8][CQ];  // where it is raised; what weights are relative to
+    float up = 0.0f;             // 16-bit pages: the reference is this far above the largest score
     float sum[R8][CQ];           // the lane's part of the sum of weights
     float acc[MT][R8][4];
     float zsum[V4 ? NG : 1][R8][CQ];
@@ -541,6 +551,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (fresh) {
             fresh = false;
             seg0 = place;
+            up = 0.0f;
             nplace = SOLO ? solo_units + SM::ITEM : pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
             const int r0 = int(tile) % a.RT * RTILE;
@@ -733,9 +744,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
                     for (int c = 0; c < CQ; ++c) {
-                        const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
+                        const float nr = fmaxf(ref[t][c], Q8 ? rows_top(top[t][c]) : rows_top(top[t][c]) + up);
                         const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
-                        ref[t][c] = nr, bar2[t][c] = nr + PAT_SLACK;
+                        ref[t][c] = nr, bar2[t][c] = (Q8 ? nr : nr - up) + PAT_SLACK;
                         off[t][c] = nr == -INFINITY ? 0.0f : nr;
                         sum[t][c] *= f;
 #pragma unroll
@@ -851,20 +862,24 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
                 } else {
-                    // The block's values as operands, and whether one is Inf or NaN.
+                    // The block's values as operands, and whether one is Inf, NaN or of 2^64
+                    // or more: the sum of their squares is then beyond bf16.
                     uint32_t w[MT][4];
                     auto load_values = [&]() {
-                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);  // NaN once a value is Inf or NaN
+                        __nv_bfloat162 sq = __float2bfloat162_rn(0.0f);
 #pragma unroll
                         for (int k = 0; k < MT; ++k) {
                             ldsm4_t(w[k], (at + v_off) ^ (32u * uint32_t(k)));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k][e]), __float2bfloat162_rn(0.0f), odd);
+                            for (int e = 0; e < 4; ++e) sq = square_sum(w[k][e], sq);
                         }
-                        return __any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u);
+                        return __any_sync(0xffffffffu, not_finite(sq));
                     };
                     if (load_values()) {
+                        // Weights go up to 2^PAT_SLACK and are divided by their sum at the
+                        // end.  For values of 2^64 or more (below it, 2^31 of them do not
+                        // pass fp32's range) the reference is put so far above the largest
+                        // score that all of the sequence's weights sum to at most 1/2.
                         // Tokens that hold Inf or NaN are added one by one, in fp32, to the
                         // queries that see them, and are zeros to the product, whose operands
                         // may not meet them: 0 * Inf would reach queries that do not see the
@@ -875,18 +890,37 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         constexpr uint32_t CHUNKS = B::VROW / 32;
                         const int nv = len - t0, tl = lane >> 1;
                         const uint32_t half = at + B::OFF_V + uint32_t(tl) * B::VROW + uint32_t(lane & 1) * (B::VROW / 2);
-                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
+                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f), sq = odd;  // odd: NaN once a value is Inf or NaN
                         if (tl < nv) {
 #pragma unroll
                             for (uint32_t k = 0; k < CHUNKS; ++k) {
                                 const uint4 v = lds128(half + 16u * ((k + uint32_t(lane)) % CHUNKS));
                                 const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
+                                for (int e = 0; e < 4; ++e) {
                                     odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[e]), __float2bfloat162_rn(0.0f), odd);
+                                    sq = square_sum(w4[e], sq);
+                                }
                             }
                         }
-                        uint32_t bits = __ballot_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u);
+                        if (__any_sync(0xffffffffu, not_finite(sq)) && up == 0.0f) {
+                            up = PAT_SLACK + 1.0f + float(32 - __clz(len));
+#pragma unroll
+                            for (int r = 0; r < R8; ++r)
+#pragma unroll
+                                for (int c = 0; c < CQ; ++c) {
+                                    const float nr = ref[r][c] + up;
+                                    const float f = nr == -INFINITY ? 1.0f : exp2f(ref[r][c] - nr);
+                                    ref[r][c] = nr, off[r][c] = nr == -INFINITY ? 0.0f : nr;
+                                    sum[r][c] *= f, p[u][r][c] *= f, p[u][r][CQ + c] *= f;
+#pragma unroll
+                                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (TWICE || (e & 1) == c) acc[k][r][e] *= f;
+                                }
+                        }
+                        uint32_t bits = __ballot_sync(0xffffffffu, not_finite(odd));
                         bits = (bits | bits >> 1) & 0x55555555u;  // bit 2 t: token t
                         for (uint32_t left = bits; left; left &= left - 1u) {
                             const int t = (__ffs(int(left)) - 1) >> 1;

@@ -468,7 +468,9 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  *    fp32 [n_seqs][n_q_tokens][n_q_heads] or NULL (natural log).  No output may
  *    overlap an input or another output, except that lse may be base_lse.
  * An Inf or NaN value of a BF16 page is one in its dim for the queries that see
- * its token (weights are positive, however small), and touches no others.
+ * its token (weights are positive, however small), and touches no others.  Finite
+ * values give finite results up to bf16's largest; where a sequence holds values of
+ * 2^64 or more, its weights below some 2^-80 of the largest count as zero.
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  Scores are products of the stored codes accumulated in fp32,
  * softmax statistics fp32; the weights (times the values' scales) enter the

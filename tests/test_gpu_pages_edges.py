@@ -1,5 +1,6 @@
 """GPU tests of attention over pages where it can go wrong: bounded waits that
-run out for some lanes only, joins in place, values that are Inf or NaN."""
+run out for some lanes only, joins in place, values that are Inf or
+NaN, or near the end of bf16's range."""
 import numpy as np
 import pytest
 import torch
@@ -173,3 +174,55 @@ def test_infinite_value_of_a_weight_below_fp32(n, at, width):
     bo, bl = torch.randn(q.shape, generator=torch.Generator().manual_seed(5)), torch.full(q.shape[:3], 400.0)
     _check_with_infinities(*pg.attend(q.cuda(), 1.0, bo.cuda(), bl.cuda()), *args,
                            (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+
+
+# --- values near the end of bf16's range ---------------------------------------------
+
+@pytest.mark.parametrize("n,nq,m,width", [(1, 1, 1, None), (16, 4, 1, None), (300, 4, 1, None), (300, 8, 3, None),
+                                          (300, 4, 1, 4096), (5000, 4, 1, None), (5000, 8, 2, None), (5000, 16, 4, None)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_finite_values(n, nq, m, width, d):
+    """Values up to the largest of bf16, scores that rise along the sequence by less
+    and by more than the slack of the running maximum: a weighted mean of them is
+    finite.  One dim holds them from the start, one only in the middle, the others
+    ordinary values; the last token of the last case is Inf in one dim besides."""
+    H = 1
+    rng = np.random.default_rng(n + nq)
+    k, v = 0.02 * rng.standard_normal((n, H, d)), rng.standard_normal((n, H, d))
+    top = float(torch.finfo(torch.bfloat16).max)
+    v[:, :, 3] = top
+    v[n // 3:n // 2 + 1, :, 40] = -top * rng.random((n // 2 + 1 - n // 3, H))
+    v[:, :, 41] = np.where(np.arange(n) % 2 == 0, top, -0.75 * top)[:, None]
+    v[n // 2:, :, 50] = 2.0 ** 70
+    if n == 5000 and m == 4:
+        v[-1, :, 60], v[-1, :, 61] = np.inf, top
+    for slope in (0.0, 4.0, 40.0):
+        k[:, :, 0] = slope * np.arange(n)[:, None] / n
+        kb, vb = _bf16(k).cuda(), _bf16(v).cuda()
+        q = rng.standard_normal((1, m, nq, d))
+        q[..., 0] = np.abs(q[..., 0]) + 0.5
+        q = _bf16(q)
+        pg = Pages("bf16", H, d, 16, [n], max_pages=width)
+        pg.append(kb, vb, outs=False)
+        out, lse = pg.attend(q.cuda(), 1.0)
+        _check_with_infinities(out, lse, _f64(q), [_f64(kb)], [_f64(vb)], [n], 1.0)
+        assert np.all(np.abs(out[..., 3] / top - 1) <= 2.0 ** -8)
+        bo, bl = torch.randn(q.shape, generator=torch.Generator().manual_seed(n)) * 5e37, torch.full(q.shape[:3], 10.0)
+        out, lse = pg.attend(q.cuda(), 1.0, bo.cuda(), bl.cuda())
+        _check_with_infinities(out, lse, _f64(q), [_f64(kb)], [_f64(vb)], [n], 1.0,
+                               (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
+
+
+def test_small_values_keep_their_bits():
+    """Values of about 2^-100, where no large ones are: nothing is scaled."""
+    H, d, n = 2, 128, 200
+    k, v = _kv(n, H, d, 34)
+    v = (v.float() * 2.0 ** -100).to(torch.bfloat16)
+    pg = Pages("bf16", H, d, 16, [n])
+    pg.append(k, v, outs=False)
+    q = torch.randn(1, 1, 8, d, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.1)
+    ref, _, mass, reach = P.attend(_f64(q), [_f64(k)], [_f64(v)], [n], 0.1)
+    # any of the n products may be zero where it is below fp32's normal range
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -17 + 2.0 ** -19 * (1 + reach[..., None])) * mass + n * 2.0 ** -126
+    assert np.all(np.abs(out - ref) <= tol)
