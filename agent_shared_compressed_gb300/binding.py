@@ -3,7 +3,9 @@
 Every function has the C name and returns the C status (0 = KVP_OK,
 negative = KVP_ERR_*); all computation happens in the CUDA library.
 Arguments that the C API takes as device pointers accept a torch tensor
-(its data_ptr()), a plain int address or None (NULL).  Per-layer pointer
+(its data_ptr()), a plain int address or None (NULL); the page calls, whose
+kernels read as much as the counts and types say, refuse tensors that do not
+hold it.  Per-layer pointer
 lists accept Python sequences of the same.  `stream` accepts a
 torch.cuda.Stream, a raw cudaStream_t int, or None (legacy default stream).
 
@@ -14,6 +16,7 @@ is no fallback.
 import ctypes as C
 import os
 import re
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkvcodec.so")
@@ -66,7 +69,6 @@ class CardHeader(C.Structure):
 assert C.sizeof(CardHeader) == 128
 
 
-
 class PagesConfig(C.Structure):
     """kvp_pages_config: a container of n_pages pages of page_tokens tokens per layer."""
     _fields_ = [("n_layers", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
@@ -78,8 +80,10 @@ class PagesConfig(C.Structure):
 
 
 class Rows(C.Structure):
-    """kvp_rows: a bf16 [tokens][heads][head_dim] tensor with element strides."""
+    """kvp_rows: a bf16 [tokens][heads][head_dim] tensor with element strides.
+    shape: the tensor's, where it was made from one (rows())."""
     _fields_ = [("ptr", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+    shape = None
 
 
 _vp = C.c_void_p
@@ -297,6 +301,22 @@ def _pages(c):
     return c if c.__class__ is PagesConfig else PagesConfig(*c)
 
 
+_addressof = C.addressof
+
+
+class _Types:
+    """torch's types by the names used here (looked up with the first tensor)."""
+
+    def __getattr__(self, name):
+        import torch
+        self.bf16, self.f32, self.i32, self.i64, self.u8 = (
+            torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8)
+        return self.__dict__[name]
+
+
+_T = _Types()
+
+
 def rows(x, token_stride=None, head_stride=None):
     """kvp_rows of a [tokens][heads][head_dim] bf16 tensor (a strided view will
     do; its last dimension contiguous), or of an address with its strides."""
@@ -307,10 +327,65 @@ def rows(x, token_stride=None, head_stride=None):
     t, h, e = x.stride()
     if e != 1:
         raise ValueError("the last dimension of a rows tensor is contiguous, got strides %r" % ((t, h, e),))
-    return Rows(x.data_ptr(), t, h)
+    if x.dtype is not _T.bf16:
+        raise ValueError("a rows tensor is bfloat16, got %s" % x.dtype)
+    r = Rows(x.data_ptr(), t, h)
+    r.shape = tuple(x.shape)
+    return r
 
 
-_addressof = C.addressof
+_pack_rows = struct.Struct("@Pqq").pack  # a kvp_rows as bytes, for one call
+
+
+def _rows(x, tokens, heads, dim, name):
+    """What the call takes for rows(x), of at least `tokens` tokens of `heads` heads of `dim`."""
+    if x.__class__ is Rows:
+        shape = x.shape
+        if shape is not None:
+            _rows_fit(shape, tokens, heads, dim, name)
+        return _addressof(x)
+    if x is None:
+        return None
+    shape, (t, h, e) = x.shape, x.stride()
+    if e != 1 or x.dtype is not _T.bf16:
+        rows(x)  # raises
+    _rows_fit(shape, tokens, heads, dim, name)
+    return _pack_rows(x.data_ptr(), t, h)
+
+
+def _rows_fit(shape, tokens, heads, dim, name):
+    t, h, d = shape
+    if t < tokens or h != heads or d != dim:
+        raise ValueError("%s: a [%d][%d][%d] tensor is needed, got %r" % (name, tokens, heads, dim, (t, h, d)))
+
+
+def _buf(x, dtype, least, name):
+    """The address of a contiguous tensor of the type with at least `least`
+    elements (or of bytes, as many as they take), of an address, or None."""
+    if x is None:
+        return None
+    try:
+        if x.dtype is dtype and x.numel() >= least and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _addr(x)  # an integer, or a TypeError
+    if x.dtype is _T.u8 and x.is_contiguous() and x.numel() >= least * dtype.itemsize:
+        return x.data_ptr()
+    raise ValueError("%s: a contiguous %s tensor of at least %d elements is needed, got %s %r with strides %r" % (
+        name, dtype, least, x.dtype, tuple(x.shape), x.stride()))
+
+
+def _bytes_buf(x, least, name):
+    """The address of a contiguous tensor of at least `least` bytes, of an address, or None."""
+    if x is None:
+        return None
+    try:
+        if x.nbytes >= least and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _addr(x)
+    raise ValueError("%s: a contiguous tensor of at least %d bytes is needed, got %s %r with strides %r" % (
+        name, least, x.dtype, tuple(x.shape), x.stride()))
 
 
 def _ref(x):
@@ -332,23 +407,35 @@ def kvpages_bytes(cfg):
 
 def kvpages_init(cfg, pages, pages_bytes, stream=None):
     cfg = _pages(cfg)
-    return load().kvpages_init(_ref(cfg), _addr(pages), int(pages_bytes), _stream(stream))
+    return load().kvpages_init(_ref(cfg), _bytes_buf(pages, pages_bytes, "pages"), int(pages_bytes), _stream(stream))
 
 
 def kvpages_append(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, positions, q_norm, k_norm, eps, rot_dim,
                    inv_freq, q_out, k_out, v_out, stream=None):
     """q, k, v: [tokens][heads][head_dim] tensors or Rows; inv_freq: rot_dim/2
-    host floats (any sequence; a ctypes float array is passed as it is)."""
-    cfg, q, k, v, w = _pages(cfg), rows(q), rows(k), rows(v), _floats(inv_freq)
-    return load().kvpages_append(_addr(pages), _ref(cfg), layer, n_tokens, n_q_heads, _ref(q), _ref(k), _ref(v),
-                                 _addr(slots), _addr(positions), _addr(q_norm), _addr(k_norm), eps, rot_dim, _ref(w),
-                                 _addr(q_out), _addr(k_out), _addr(v_out), _stream(stream))
+    host floats (any sequence; a ctypes float array is passed as it is).
+
+    ValueError for a tensor of another type, another shape (q, k, v), not
+    contiguous or too small for the call; so with the calls below.  (A uint8
+    tensor passes as memory for any output or input but q, k and v.)"""
+    cfg, w = _pages(cfg), _floats(inv_freq)
+    h, d = cfg.n_kv_heads, cfg.head_dim
+    q = _rows(q, n_tokens, n_q_heads, d, "q") if n_q_heads else None
+    k, v = _rows(k, n_tokens, h, d, "k"), _rows(v, n_tokens, h, d, "v")
+    return load().kvpages_append(_addr(pages), _ref(cfg), layer, n_tokens, n_q_heads, q, k, v,
+                                 _buf(slots, _T.i64, n_tokens, "slots"), _buf(positions, _T.i64, n_tokens, "positions"),
+                                 _buf(q_norm, _T.bf16, d, "q_norm"), _buf(k_norm, _T.bf16, d, "k_norm"), eps, rot_dim,
+                                 _ref(w), _buf(q_out, _T.bf16, n_tokens * n_q_heads * d, "q_out"),
+                                 _buf(k_out, _T.bf16, n_tokens * h * d, "k_out"),
+                                 _buf(v_out, _T.bf16, n_tokens * h * d, "v_out"), _stream(stream))
 
 
 def kvpages_read(pages, cfg, layer, n_seqs, table, max_pages, lens, max_tokens, k_dst, v_dst, stream=None):
     cfg = _pages(cfg)
-    return load().kvpages_read(_addr(pages), _ref(cfg), layer, n_seqs, _addr(table), max_pages, _addr(lens), max_tokens,
-                               _addr(k_dst), _addr(v_dst), _stream(stream))
+    n = n_seqs * cfg.n_kv_heads * max_tokens * cfg.head_dim
+    return load().kvpages_read(_addr(pages), _ref(cfg), layer, n_seqs, _buf(table, _T.i32, n_seqs * max_pages, "table"),
+                               max_pages, _buf(lens, _T.i32, n_seqs, "lens"), max_tokens, _buf(k_dst, _T.bf16, n, "k_dst"),
+                               _buf(v_dst, _T.bf16, n, "v_dst"), _stream(stream))
 
 
 def kvpages_attend_workspace_bytes(cfg, n_seqs, n_q_tokens, n_q_heads):
@@ -359,9 +446,13 @@ def kvpages_attend_workspace_bytes(cfg, n_seqs, n_q_tokens, n_q_heads):
 def kvpages_attend(pages, cfg, layer, n_seqs, n_q_tokens, n_q_heads, q, scale, table, max_pages, lens, base_out,
                    base_lse, out, lse, ws, ws_bytes, stream=None):
     cfg = _pages(cfg)
-    return load().kvpages_attend(_addr(pages), _ref(cfg), layer, n_seqs, n_q_tokens, n_q_heads, _addr(q), scale,
-                                 _addr(table), max_pages, _addr(lens), _addr(base_out), _addr(base_lse), _addr(out),
-                                 _addr(lse), _addr(ws), ws_bytes, _stream(stream))
+    n = n_seqs * n_q_tokens * n_q_heads
+    nd = n * cfg.head_dim
+    return load().kvpages_attend(_addr(pages), _ref(cfg), layer, n_seqs, n_q_tokens, n_q_heads, _buf(q, _T.bf16, nd, "q"),
+                                 scale, _buf(table, _T.i32, n_seqs * max_pages, "table"), max_pages,
+                                 _buf(lens, _T.i32, n_seqs, "lens"), _buf(base_out, _T.f32, nd, "base_out"),
+                                 _buf(base_lse, _T.f32, n, "base_lse"), _buf(out, _T.bf16, nd, "out"),
+                                 _buf(lse, _T.f32, n, "lse"), _bytes_buf(ws, ws_bytes, "ws"), ws_bytes, _stream(stream))
 
 
 def kvpages_status(pages, stream=None):
