@@ -1135,7 +1135,8 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 // sequences; beyond, from the plan that pages_attend leaves), and all but block 0
 // leave at once if that is nothing: block 0 stays for pages_attend's end, so that
 // this grid's end means the other's.
-template <int D, int RTILE, int WARPS>
+// ODD: values may be Inf or NaN (16-bit pages).
+template <int D, int RTILE, int WARPS, bool ODD>
 __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__ PagesAttendArgs a) {
     constexpr int VPL = D / 32, DEEP = 8;  // values of a lane
     __shared__ float macc[WARPS][D], mst[WARPS][2];
@@ -1206,14 +1207,14 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
             const float f0 = nm == -INFINITY ? 1.0f : exp2f(M - nm);
             M = nm, L *= f0;
 #pragma unroll
-            for (int u = 0; u < VPL; ++u) acc[u] *= factor(f0, acc[u]);
+            for (int u = 0; u < VPL; ++u) acc[u] *= ODD ? factor(f0, acc[u]) : f0;
 #pragma unroll
             for (int k = 0; k < DEEP; ++k) {
                 if (st[k].x == -INFINITY) continue;  // an empty part
                 const float f = exp2f(st[k].x - nm);
                 L = fmaf(f, st[k].y, L);
 #pragma unroll
-                for (int u = 0; u < VPL; ++u) acc[u] = fmaf(factor(f, v[k][u]), v[k][u], acc[u]);
+                for (int u = 0; u < VPL; ++u) acc[u] = fmaf(ODD ? factor(f, v[k][u]) : f, v[k][u], acc[u]);
             }
         }
 #pragma unroll
@@ -1231,11 +1232,13 @@ __global__ void __launch_bounds__(32 * WARPS) pages_join(const __grid_constant__
             for (int k = 0; k < WARPS; ++k) {
                 const float f = mst[k][0] == -INFINITY ? 0.0f : exp2f(mst[k][0] - top);
                 l = fmaf(f, mst[k][1], l);
-                o = fmaf(factor(f, macc[k][threadIdx.x]), macc[k][threadIdx.x], o);
+                const float v = macc[k][threadIdx.x];
+                o = fmaf(ODD ? factor(f, v) : f, v, o);
             }
             const float lse = l > 0.0f ? (top + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
             const float2 w = join_base(a, row, lse, bl, threadIdx.x == 0);
-            o *= factor(l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l), o);
+            const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
+            o *= ODD ? factor(inv, o) : inv;
             if (a.base_out && w.y != 0.0f) o = fmaf(w.y, a.base_out[row * D + threadIdx.x], o);
             reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(o);
         }
@@ -1336,7 +1339,8 @@ static int launch_attend(PagesAttendArgs &a, cudaStream_t st) {
     // (a step of 15 agents, 16 partials: 20.0 against 23.8 us with 16).
     const bool many = a.nwarps / tiles >= 64u;
     cfg.blockDim = dim3(many ? 512 : 128);
-    if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, RC, 16> : pages_join<D, RC, 4>, a) != cudaSuccess)
+    constexpr bool ODD = FMT == KVP_PAGES_BF16;
+    if (cudaLaunchKernelEx(&cfg, many ? pages_join<D, RC, 16, ODD> : pages_join<D, RC, 4, ODD>, a) != cudaSuccess)
         return KVP_ERR_CUDA;
     count_launch();
     return launch_status();
