@@ -392,12 +392,20 @@ def _ref(x):
     return None if x is None else _addressof(x)
 
 
-def _floats(x):
-    """A host float array as a ctypes array: one made earlier passes as it is."""
-    if x is None or isinstance(x, C.Array):
-        return x
-    vals = [float(v) for v in x]
-    return (C.c_float * max(1, len(vals)))(*vals)
+def _floats(x, least=0):
+    """A host float array as a ctypes array of at least `least` floats: one made
+    earlier passes as it is."""
+    if x is None:
+        return None
+    if not isinstance(x, C.Array):
+        vals = [float(v) for v in x]
+        x = (C.c_float * max(1, len(vals)))(*vals)
+        n = len(vals)
+    else:
+        n = len(x)
+    if n < least or x._type_ is not C.c_float:
+        raise ValueError("inv_freq: %d floats are needed, got %d of %s" % (least, n, x._type_.__name__))
+    return x
 
 
 def kvpages_bytes(cfg):
@@ -418,7 +426,7 @@ def kvpages_append(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, posit
     ValueError for a tensor of another type, another shape (q, k, v), not
     contiguous or too small for the call; so with the calls below.  (A uint8
     tensor passes as memory for any output or input but q, k and v.)"""
-    cfg, w = _pages(cfg), _floats(inv_freq)
+    cfg, w = _pages(cfg), _floats(inv_freq, rot_dim // 2)
     h, d = cfg.n_kv_heads, cfg.head_dim
     q = _rows(q, n_tokens, n_q_heads, d, "q") if n_q_heads else None
     k, v = _rows(k, n_tokens, h, d, "k"), _rows(v, n_tokens, h, d, "v")

@@ -1,6 +1,8 @@
 """The page calls of the binding refuse tensors that do not hold what the kernels
 would read or write: another type, too few elements, another order.  A stand-in
 for the library shows that nothing reaches it (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -133,3 +135,20 @@ def test_other_refusals(lib):
     with pytest.raises(TypeError):
         attend(lens="lens")
     assert not lib.calls
+
+
+@pytest.mark.parametrize("freq", [[1.0] * 31, [], (ctypes.c_float * 31)(), (ctypes.c_double * 32)(), (ctypes.c_int * 64)()])
+def test_frequencies_that_do_not_fit(lib, freq):
+    """The library reads rot_dim / 2 fp32 values from the host array it is given."""
+    with pytest.raises(ValueError):
+        append(inv_freq=freq)
+    assert not lib.calls
+
+
+def test_frequencies_that_fit(lib):
+    append(inv_freq=(ctypes.c_float * 32)())
+    append(inv_freq=(ctypes.c_float * 40)())
+    append(inv_freq=range(32))
+    append(inv_freq=None, rot_dim=0)
+    append(inv_freq=[], rot_dim=0)
+    assert len(lib.calls) == 5
