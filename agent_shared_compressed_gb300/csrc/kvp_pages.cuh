@@ -14,6 +14,8 @@
 // and for keys and values alike; a quad holds one row.
 #pragma once
 
+#include <cstring>
+
 #include "kvp_internal.cuh"
 
 namespace kvp {
@@ -77,6 +79,28 @@ inline PagesView pages_view(void *pages, const kvp_pages_config &c, int layer) {
     v.n_pages = c.n_pages;
     v.format = c.format;
     return v;
+}
+
+// w / 2 pi mod 1 in units of 2^-64, cut off towards 0, for an fp32 w: its 24-bit integer
+// times the first 128 bits of 1 / 2 pi's binary fraction, shifted by its exponent.
+inline uint64_t turn_fraction(float w) {
+    constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;  // 1 / 2 pi * 2^128
+    uint32_t bits;
+    std::memcpy(&bits, &w, 4);
+    const int ex = int(bits >> 23 & 255u);
+    const uint64_t m = (bits & 0x7FFFFFu) | (ex ? 0x800000u : 0u);  // |w| = m 2^(max(ex, 1) - 150)
+    // m / 2 pi = p 2^-128 with p of 152 bits, as three 64-bit words
+    const unsigned __int128 p0 = (unsigned __int128)m * LO, p1 = (unsigned __int128)m * HI + (p0 >> 64);
+    const uint64_t word[3] = {uint64_t(p0), uint64_t(p1), uint64_t(p1 >> 64)};
+    // the turn's 64-bit fraction: bits [s, s + 64) of p, s = 64 - (max(ex, 1) - 150)
+    const int s = 214 - (ex ? ex : 1);
+    uint64_t r = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int at = 64 * i - s;  // where the word's bit 0 lands
+        if (at >= 0 && at < 64) r |= word[i] << at;
+        if (at < 0 && at > -64) r |= word[i] >> -at;
+    }
+    return bits >> 31 ? 0u - r : r;
 }
 
 // Whether the container's header is the one the caller described.

@@ -16,12 +16,12 @@
 // Angles.  position * w_i is only needed modulo a turn, and w_i / 2 pi modulo 1
 // is a 64-bit fraction W_i, formed on the host from the fp32 frequency and 128
 // bits of 1 / 2 pi.  position * W_i in 64-bit integers wraps at exactly one
-// turn, so the reduced angle is off by position * 2^-65 turns at any position;
-// sincospif finishes in fp32.  (The same reduction in fp64 costs some hundred
+// turn, so the reduced angle is off by less than |position| * 2^-64 turns (W_i is cut
+// off, not rounded) at any position, for frequencies below 2^60; sincospif finishes in
+// fp32.  (The same reduction in fp64 costs some hundred
 // fp64 instructions an angle, and this GPU's fp64 rate is low.)
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 
 #include "kvp_pages.cuh"
 
@@ -528,28 +528,6 @@ __global__ void pages_init(uint32_t *h, const __grid_constant__ kvp_pages_config
         default: break;
     }
     h[i] = w;
-}
-
-// w / 2 pi mod 1 in units of 2^-64, for a finite fp32 w: its 24-bit integer
-// times the first 128 bits of 1 / 2 pi's binary fraction, shifted by its exponent.
-static uint64_t turn_fraction(float w) {
-    constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;  // 1 / 2 pi * 2^128
-    uint32_t bits;
-    std::memcpy(&bits, &w, 4);
-    const int ex = int(bits >> 23 & 255u);
-    const uint64_t m = (bits & 0x7FFFFFu) | (ex ? 0x800000u : 0u);  // |w| = m 2^(max(ex, 1) - 150)
-    // m / 2 pi = p 2^-128 with p of 152 bits, as three 64-bit words
-    const unsigned __int128 p0 = (unsigned __int128)m * LO, p1 = (unsigned __int128)m * HI + (p0 >> 64);
-    const uint64_t word[3] = {uint64_t(p0), uint64_t(p1), uint64_t(p1 >> 64)};
-    // the turn's 64-bit fraction: bits [s, s + 64) of p, s = 64 - (max(ex, 1) - 150)
-    const int s = 214 - (ex ? ex : 1);
-    uint64_t r = 0;
-    for (int i = 0; i < 3; ++i) {
-        const int at = 64 * i - s;  // where the word's bit 0 lands
-        if (at >= 0 && at < 64) r |= word[i] << at;
-        if (at < 0 && at > -64) r |= word[i] >> -at;
-    }
-    return bits >> 31 ? 0u - r : r;
 }
 
 template <typename Args>

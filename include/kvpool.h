@@ -418,8 +418,9 @@ int kvpages_init(const kvp_pages_config *cfg, void *pages, size_t pages_bytes, v
  *  rot_dim: 0, 64, or 128 at head_dim 128: dims i and i + rot_dim/2
  *    (i < rot_dim/2) turned by positions[t] * inv_freq[i]; the rest pass.
  *    positions: device int64[n_tokens]; inv_freq: HOST array of rot_dim/2
- *    fp32 frequencies, read during the call only.  The angle is reduced
- *    exactly to a turn at any position, its sine and cosine taken in fp32.
+ *    fp32 frequencies (below 2^60 in magnitude), read during the call only.  The
+ *    angle is reduced to a turn with an error below |position| * 2^-64 turns, its
+ *    sine and cosine taken in fp32.
  *  q_out: device bf16 [n_tokens][n_q_heads][head_dim] contiguous.
  *  k_out, v_out: device bf16 [n_tokens][n_kv_heads][head_dim] contiguous, or
  *    NULL: the keys and values as the cache now holds them, for a prompt's own
