@@ -226,3 +226,71 @@ def test_small_values_keep_their_bits():
     # any of the n products may be zero where it is below fp32's normal range
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -17 + 2.0 ** -19 * (1 + reach[..., None])) * mass + n * 2.0 ** -126
     assert np.all(np.abs(out - ref) <= tol)
+
+
+# --- long runs -----------------------------------------------------------------------
+
+def _run_units(fmt, d, rows, lens, tiles):
+    """Units of a warp's run and units whose addresses a warp holds at a time, as
+    csrc/kvpages_attend.cu cuts the list (its PatShape and tile_units)."""
+    quant, tile = fmt != "bf16", 4 if rows <= 4 else (8 if rows <= 8 else 16)
+    warps = (8 if not quant or tile == 16 else 12) if d == 128 else (12 if tile == 16 else 16)
+    blocks = 2 if quant and tile <= 8 else 1
+    units = sum((n + 16 * blocks - 1 + 64) // (16 * blocks) for n in lens if n) * tiles
+    n_warps = torch.cuda.get_device_properties(0).multi_processor_count * warps
+    return (units + n_warps - 1) // n_warps, 32 // blocks
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,H,m,nq,lens", [
+    (128, 8, 1, 32, [70000, 62016, 0, 65001, 64000]),    # tiles of 4
+    (64, 8, 1, 16, [100000, 90001, 87, 95000, 99968]),
+    (128, 4, 2, 16, [129000, 131072, 120001, 130000]),   # of 8
+    (128, 4, 4, 16, [131072, 99000, 120001, 130000]),    # of 16
+])
+@pytest.mark.parametrize("bad", [False, True])
+def test_runs_longer_than_the_address_window(fmt, d, H, m, nq, lens, bad):
+    """A warp's lanes hold the addresses of its run's next 16 or 32 units and fetch
+    more as it goes: runs of more than two such windows, in every format, with page
+    ids outside the container beyond the first.  The table rows name the same few
+    pages over and over, so the plain result needs each token once, by its count."""
+    page, held = 16 if d == 64 else 64, 1024  # (pages of 16: a unit may lack either of its blocks)
+    per, window = _run_units(fmt, d, m * nq // H, lens, H)
+    assert per > 2 * window
+    rng = np.random.default_rng(d + m)
+    pg = Pages(fmt, H, d, page, [held])
+    k, v = _kv(held, H, d, 35)
+    pg.append(k, v, outs=False)
+    hk, hv = P.held(_f64(k), fmt, False), P.held(_f64(v), fmt, True)
+    width = max((n + page - 1) // page for n in lens)
+    which = rng.integers(0, held // page, (len(lens), width))   # the held page that each entry names
+    gone = np.zeros(which.shape, bool)
+    if bad:
+        gone = rng.random(which.shape) < 0.1
+        gone[:, :2 * window * 32 // page] = False
+    pg.table_d = torch.from_numpy(np.where(gone, pg.n_pages + rng.integers(0, 9, which.shape), pg.table[0][which]).astype(np.int32)).cuda()
+    pg.max_pages, pg.lens_d = width, torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(len(lens), m, nq, d, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    out, lse = pg.attend(q.cuda(), 0.05)
+    assert pg.status() == (kv.KVP_ERR_PAGE if bad else kv.KVP_OK)
+    steps = 2 * per + 100  # additions to a sum: the run's blocks, the parts
+    for b, n in enumerate(lens):
+        for i in range(m):
+            see = max(0, n - (m - 1 - i))
+            t = np.arange(see)
+            t = t[~gone[b, t // page]]
+            count = np.bincount(which[b, t // page] * page + t % page, minlength=held).astype(np.float64)
+            for j in range(nq):
+                h, x = j // (nq // H), _f64(q[b, i, j])
+                if not see:
+                    assert not out[b, i, j].any() and lse[b, i, j] == -np.inf
+                    continue
+                s = 0.05 * (hk[:, h] @ x)
+                reach = 0.05 * (np.abs(hk[:, h]) @ np.abs(x)).max()
+                top = s[count > 0].max()
+                e = np.where(count > 0, count * np.exp(s - top), 0.0)
+                ref, mass = (e / e.sum()) @ hv[:, h], (e / e.sum()) @ np.abs(hv[:, h])
+                fine = 2.0 ** -19 * (1 + reach) + steps * 2.0 ** -23
+                assert np.all(np.abs(out[b, i, j] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -17 + fine) * mass + 1e-30)
+                ref_lse = top + np.log(e.sum())
+                assert abs(lse[b, i, j] - ref_lse) <= fine + 2.0 ** -23 * abs(ref_lse)
