@@ -8,6 +8,7 @@ import torch
 import agent_shared_compressed_gb300 as kv
 from agent_shared_compressed_gb300 import build as kvbuild
 import pageshelp as P
+import pagesweights as W
 from test_gpu_pages import FMTS, Pages, _bf16, _check_attend, _f64, _kv, _split
 
 pytestmark = pytest.mark.gpu
@@ -294,3 +295,25 @@ def test_runs_longer_than_the_address_window(fmt, d, H, m, nq, lens, bad):
                 assert np.all(np.abs(out[b, i, j] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -17 + fine) * mass + 1e-30)
                 ref_lse = top + np.log(e.sum())
                 assert abs(lse[b, i, j] - ref_lse) <= fine + 2.0 ** -23 * abs(ref_lse)
+
+
+# --- how exactly weights are held ------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("repeat", [1, 20, 400])
+@pytest.mark.parametrize("rows", [1, 4, 7, 16, 20])
+@pytest.mark.parametrize("width", [None, 4096])
+def test_weights_are_held_to_2_17(fmt, d, repeat, rows, width):
+    """Two terms that cancel leave the weights' roundings: 2^-17 of each, as the
+    header says, where one bf16 or 11 bits would be several times the bound."""
+    q, k, v, scale = W.sequence(fmt, d, repeat, rows, seed=rows)
+    n = len(k)
+    pg = Pages(fmt, 1, d, 16, [n], max_pages=width)
+    pg.append(_bf16(k).cuda(), _bf16(v).cuda(), outs=False)
+    q = q[None, None]
+    hk, hv = P.held(k, fmt, False), P.held(v, fmt, True)
+    out, _ = pg.attend(_bf16(q).cuda(), scale)
+    ref, _, mass, reach = P.attend(q, [hk], [hv], [n], scale)
+    tol = W.bound(ref, mass, reach[..., None], n // 16 + 20)
+    assert np.all(np.abs(out - ref) <= tol), (np.abs(out - ref) / tol).max()
