@@ -657,6 +657,23 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 }
                 __syncwarp();
             }
+            // 16-bit pages: whether the lane's 1/32 of the block's values has one that is Inf,
+            // NaN or of 2^64 or more: the sum of their squares is then beyond bf16.  Read
+            // ahead of the scores, in four short chains (15 4K caches of 64 rows a head:
+            // 123 us, 121 without the test, 133 from the product's own operands).
+            bool odd_values = false;
+            if constexpr (!Q8) {
+                __nv_bfloat162 sq[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sq[e] = __float2bfloat162_rn(0.0f);
+#pragma unroll
+                for (uint32_t k = 0; k < B::VROW / 32; ++k) {
+                    const uint4 v = lds128(at0 + B::OFF_V + 512u * k + 16u * uint32_t(lane));
+                    sq[0] = square_sum(v.x, sq[0]), sq[1] = square_sum(v.y, sq[1]);
+                    sq[2] = square_sum(v.z, sq[2]), sq[3] = square_sum(v.w, sq[3]);
+                }
+                odd_values = not_finite(__hadd2(__hadd2(sq[0], sq[1]), __hadd2(sq[2], sq[3])));
+            }
             // scores: x[u][t][c] token 16 u + g, [CQ + c] token 16 u + g + 8
             float x[UB][R8][2 * CQ];
 #pragma unroll
@@ -740,25 +757,38 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     raise |= top[t][c] > bar2[t][c];
                 }
             if (__any_sync(0xffffffffu, raise)) {
+                float f[R8][CQ];
+                bool lost = false;  // a factor has underflowed
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
                     for (int c = 0; c < CQ; ++c) {
                         const float nr = fmaxf(ref[t][c], Q8 ? rows_top(top[t][c]) : rows_top(top[t][c]) + up);
-                        const float f = nr == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
+                        f[t][c] = ref[t][c] == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
+                        lost |= f[t][c] == 0.0f;
                         ref[t][c] = nr, bar2[t][c] = (Q8 ? nr : nr - up) + PAT_SLACK;
                         off[t][c] = nr == -INFINITY ? 0.0f : nr;
-                        sum[t][c] *= f;
-#pragma unroll
-                        for (int k = 0; k < MT; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (TWICE || (e & 1) == c) acc[k][t][e] *= Q8 ? f : factor(f, acc[k][t][e]);
+                        sum[t][c] *= f[t][c];
                         if constexpr (V4) {
 #pragma unroll
-                            for (int k = 0; k < NG; ++k) zsum[k][t][c] *= f;
+                            for (int k = 0; k < NG; ++k) zsum[k][t][c] *= f[t][c];
                         }
                     }
+                if (!Q8 && __any_sync(0xffffffffu, lost)) {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int t = 0; t < R8; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[k][t][e] *= factor(f[t][e % CQ], acc[k][t][e]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int t = 0; t < R8; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[k][t][e] *= f[t][e % CQ];
+                }
             }
             float p[UB][R8][2 * CQ];
 #pragma unroll
@@ -862,20 +892,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
                 } else {
-                    // The block's values as operands, and whether one is Inf, NaN or of 2^64
-                    // or more: the sum of their squares is then beyond bf16.
-                    uint32_t w[MT][4];
-                    auto load_values = [&]() {
-                        __nv_bfloat162 sq = __float2bfloat162_rn(0.0f);
-#pragma unroll
-                        for (int k = 0; k < MT; ++k) {
-                            ldsm4_t(w[k], (at + v_off) ^ (32u * uint32_t(k)));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) sq = square_sum(w[k][e], sq);
-                        }
-                        return __any_sync(0xffffffffu, not_finite(sq));
-                    };
-                    if (load_values()) {
+                    if (__any_sync(0xffffffffu, odd_values)) {
                         // Weights go up to 2^PAT_SLACK and are divided by their sum at the
                         // end.  For values of 2^64 or more (below it, 2^31 of them do not
                         // pass fp32's range) the reference is put so far above the largest
@@ -952,7 +969,6 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                         fence_proxy_async();  // before a later copy into the slot
                         __syncwarp();
-                        load_values();
                     }
                     uint32_t hi[R8][2], lo[R8][2];
 #pragma unroll
@@ -966,12 +982,15 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < MT; ++k)
+                    for (int k = 0; k < MT; ++k) {
+                        uint32_t w[4];
+                        ldsm4_t(w, (at + v_off) ^ (32u * uint32_t(k)));
 #pragma unroll
                         for (int t = 0; t < R8; ++t) {
-                            mma_bf16(acc[k][t], w[k][0], w[k][1], w[k][2], w[k][3], hi[t][0], hi[t][1]);
-                            if constexpr (!TWICE) mma_bf16(acc[k][t], w[k][0], w[k][1], w[k][2], w[k][3], lo[t][0], lo[t][1]);
+                            mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], hi[t][0], hi[t][1]);
+                            if constexpr (!TWICE) mma_bf16(acc[k][t], w[0], w[1], w[2], w[3], lo[t][0], lo[t][1]);
                         }
+                    }
                 }
             }
         }
