@@ -444,7 +444,7 @@ struct ReadArgs {
     PagesView pv;
     const int32_t *table, *lens;
     uint16_t *k, *v;  // [B][H][Tmax][d]
-    int nseq, max_pages, tmax, nblk;
+    int max_pages, tmax, nblk;
     uint64_t tasks;
 };
 
@@ -643,7 +643,7 @@ int kvpages_read(const void *pages, const kvp_pages_config *cfg, int layer, int 
     a.pv = pages_view(const_cast<void *>(pages), *cfg, layer);
     a.table = table, a.lens = lens;
     a.k = static_cast<uint16_t *>(k_dst), a.v = static_cast<uint16_t *>(v_dst);
-    a.nseq = n_seqs, a.max_pages = max_pages, a.tmax = max_tokens;
+    a.max_pages = max_pages, a.tmax = max_tokens;
     a.nblk = int((int64_t(max_tokens) + PAGES_BLOCK - 1) / PAGES_BLOCK);
     a.tasks = uint64_t(n_seqs) * uint64_t(cfg->n_kv_heads) * uint64_t(a.nblk);
     // two to three waves of blocks: 15 4K caches 61.3 us, 64.5 with 8 blocks an SM (about
