@@ -473,12 +473,21 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  * values give finite results up to bf16's largest; where a sequence holds values of
  * 2^64 or more, its weights below some 2^-80 of the largest count as zero.
  * A query that sees no token gets the base's output and lse, or zeros and -inf
- * without one.  Scores are products of the stored codes accumulated in fp32,
- * softmax statistics fp32; the weights (times the values' scales) enter the
- * value product as a sum of two bf16 (2^-17).  The kernel waits for its bulk copies of the
- * pages at most about half a second; should a wait run out, the outputs are
- * unspecified and kvpages_status reports KVP_ERR_TIMEOUT.  A page id outside the container or a length beyond
- * its table row is skipped and reported by kvpages_status as KVP_ERR_PAGE. */
+ * without one.  Scores are products of the stored codes accumulated in fp32 (over
+ * 8-bit keys a query row enters as fp16 times a power of two, exactly but for
+ * elements below 2^-28 of its largest); softmax statistics are fp32, exponentials
+ * the hardware's in base 2 (2^-22); the weights (times the values' scales) enter
+ * the value product as a sum of two bf16 (2^-17).  The kernel waits for its bulk
+ * copies of the pages at most about half a second; should a wait run out, the
+ * outputs are unspecified and kvpages_status reports KVP_ERR_TIMEOUT.  A page id
+ * outside the container or a length beyond its table row is skipped and reported
+ * by kvpages_status as KVP_ERR_PAGE.
+ * Speed: the lengths are known on the device only, so it is max_pages that chooses
+ * how the work is split.  Where no row can hold more than some thousand tokens, a
+ * team of warps takes each row tile, in one launch; otherwise equal runs of all
+ * tokens are joined by a second one.  A table trimmed to the longest sequence is
+ * therefore faster for short ones: 15 of 200 tokens take 6.3 us, 10.1 with rows for
+ * 32768 tokens (64 of them 11.5 and 18.9; from some 2000 tokens on no difference). */
 int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
                    int n_q_heads, const void *q, float scale, const int32_t *table, int max_pages,
                    const int32_t *lens, const float *base_out, const float *base_lse, void *out, float *lse, void *ws,
