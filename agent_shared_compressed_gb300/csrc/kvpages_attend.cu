@@ -51,8 +51,8 @@
 // per 32 dims, do not cancel.  16-bit pages are multiplied as they are.
 //
 // Measured (of the 6789 GB/s that a copy reaches): four 32K caches of 8 bits, 4
-// query rows a KV head, 56 us, 5.1 TB/s; 15 4K caches of 16 bits 45 us, 5.6 TB/s; one
-// 128K with 4-bit values 50.4 us, 4.5 TB/s.
+// query rows a KV head, 56.7 us, 5.0 TB/s; 15 4K caches of 16 bits 45.4 us, 5.5 TB/s;
+// one 128K with 4-bit values 50.7 us, 4.5 TB/s.
 #include <algorithm>
 #include <cmath>
 
@@ -1269,10 +1269,19 @@ static thread_local uint32_t g_next_polls = 0, g_next_lanes = 0;
 static thread_local bool g_limit_next = false;
 
 static unsigned attend_grid() { return unsigned(sm_count()); }
-// Rows of a tile.  One of 16 rows costs 1.8 of 8 rows with 8- and 4-bit pages
-// (54 against 2 x 30 us for 16 rows on 15 4K caches): an odd number of groups of
-// 8 rows goes in tiles of 8 (20 rows: 39 against 43 us); with 16-bit pages it
-// costs 1.2, so only up to 8 rows do.
+// Rows of a tile.  us of tiles of 8 and of 16 rows on 15 4K caches, 8 KV heads:
+//   rows       12      16      20      24      28      32      40      52      64
+//   k8v8, 128  62  51  64  53  82  87  82  89 111  90 111  90 130 130 178 167 207 171
+//   k8v4, 128  58  53  60  55  78  91  78  92 105  93 105  94 124 135 169 173 196 177
+//   k8v8, 64   36  34  36  35  50  56  51  57  62  58  63  59  79  76 102 101 113 102
+//   k8v4, 64   36  37  36  38  52  59  52  59  64  61  65  62  81  81 104 106 116 108
+//   bf16, 128  52  53  54  55 125  62 126  64  99  65 100  66 117 137 269 118 210 123
+//   bf16, 64   32  27  33  28  65  50  66  51  54  53  55  55  66  59  94  91  99  92
+// An odd number of groups of 8 rows goes in tiles of 8 with 8- and 4-bit pages, where
+// it wins at three groups and is about even beyond; with 16-bit pages more than 8 rows
+// go in tiles of 16 (40 rows at head_dim 128 lose by that).  Up to 4 rows a tile of 4
+// forms no exponential or split twice: one 128K sequence with 4-bit values 50.6 us,
+// 55.9 in a tile of 8.
 static int tile_rows(int rows, int format) {
     if (rows <= 4) return 4;
     const int eights = (rows + 7) / 8;
@@ -1281,16 +1290,26 @@ static int tile_rows(int rows, int format) {
 
 // Blocks of a team's warp up to which a team per row tile beats equal runs of the
 // list.  It has one launch and nothing cut, but waits for the longest sequence, so
-// that the limits are below where equal lengths lose.  Where teams employ half of
-// the GPU's warps or more (us, teams against runs, of 8 KV heads): k8v8 at 128, 64
-// x 700 tokens (15 blocks) 25 and 30, lengths of 1 to 700 22 and 23, 64 x 1500 (31)
-// 43 and 46, but lengths of 1 to 1500 38 and 32; bf16 at 128, 120 x 200 (13) 21 and
-// 37, 64 x 700 (22) 33 and 40, lengths of 1 to 700 22 and 27; k8v4 at 64, 64 x 1500
-// (24) 26 and 31, lengths of 1 to 1500 22 and 24.  With more row tiles than the GPU
-// has warps, in several waves: 64 x 200 of 64 rows (13, k8v8 at 128) 50 and 90, 512 x
-// 200 of 4 rows 62 and 66, 2000 x 30 61 and 77.  Where they employ fewer: one
-// sequence of 700 tokens (k8v8, 4 blocks) 8.8 and 8.9, of 1500 (8) 13.3 and 9.1;
-// bf16 700 (6) 7.5 and 7.2, 200 (2) 5.2 and 7.0.
+// that the limits are below where ragged lengths lose.  us, teams against runs, 8 KV
+// heads of 4 rows.  Where teams employ half of the GPU's warps or more, 64 sequences:
+//   tokens      700      1-700    1000     1-1000   1500     1-1500
+//   k8v8, 128   25  32   23  25   33  38   28  29   44  48   39  33
+//   k8v4, 128   24  31   22  24   31  37   27  28   41  45   37  32
+//   bf16, 128   34  42   23  28   46  54   30  35   66  73   41  44
+//   k8v8, 64    17  22   13  16   20  26   17  19   26  31   22  23
+//   k8v4, 64    17  22   13  16   20  26   16  18   26  31   22  23
+//   bf16, 64    19  26   14  20   25  32   17  23   35  41   23  27
+// (at head_dim 128 15, 21 and 31 blocks a warp, 22, 31 and 47 with 16 bits; at 64 11,
+// 16 and 24).  With more row tiles than the GPU has warps, in several waves: 64 x 200
+// of 64 rows (13, k8v8 at 128) 51 and 92, 512 x 200 of 4 rows 62 and 66 (bf16 75 and 93,
+// at 64 40 and 60; k8v4 at 64 33 and 47).  Where they employ fewer, one sequence:
+//   tokens      400          700          1000         1500
+//   k8v8, 128   7.4   8.8    9.0   8.9    11.1  9.1    13.5  9.3    (4 blocks: 768)
+//   k8v4, 128   7.5   8.7    8.8   9.0    10.7  9.1    13.0  9.2
+//   bf16, 128   6.8   7.5    8.1   7.7     9.7  7.9    12.4  8.2    (512)
+//   k8v8, 64    6.0   8.0    6.9   8.2     7.7  8.4     9.3  8.4    (1024)
+//   k8v4, 64    6.1   8.0    6.9   8.2     7.7  8.4     9.1  8.4
+//   bf16, 64    5.7   7.3    6.7   7.6     7.5  7.8     8.8  8.0
 template <int D, int FMT>
 static int team_blocks(bool half) {
     return half ? (FMT != KVP_PAGES_BF16 && D == 128 ? 16 : 24) : 4;
