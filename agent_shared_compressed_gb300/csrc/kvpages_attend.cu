@@ -168,6 +168,9 @@ __device__ __forceinline__ void sts16(uint32_t at, uint16_t v) {
 __device__ __forceinline__ void sts128_zero(uint32_t at) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -223,11 +226,16 @@ __device__ __forceinline__ void twin_weights(float w0, float w1, uint32_t &b0, u
 // The factor of a weighted sum x when it is scaled by f > 0: f, but 1 where f has
 // underflowed to 0 and x is Inf or NaN (16-bit values may be), which it has to stay.
 __device__ __forceinline__ float factor(float f, float x) { return f == 0.0f && !(fabsf(x) < INFINITY) ? 1.0f : f; }
-// sq + w^2 of a pair of bf16, and whether one of a pair is Inf or NaN.
+// sq + w^2 and w f of a pair of bf16, and whether one of a pair is Inf or NaN.
 __device__ __forceinline__ __nv_bfloat162 square_sum(uint32_t w, __nv_bfloat162 sq) {
     const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&w);
     return __hfma2(v, v, sq);
 }
+__device__ __forceinline__ uint32_t times(uint32_t w, __nv_bfloat162 f) {
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), f);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 __device__ __forceinline__ bool not_finite(__nv_bfloat162 v) {
     const __nv_bfloat162 z = __hmul2(v, __float2bfloat162_rn(0.0f));  // 0 or -0, else NaN
     return (*reinterpret_cast<const uint32_t *>(&z) & 0x7FFF7FFFu) != 0u;
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
     int lim[R8][CQ];             // tokens that the query sees
     float ref[R8][CQ];           // running maximum score, raised lazily
     float bar2[R8][CQ], off[R8][CQ];  // where it is raised; what weights are relative to
-    float up = 0.0f;             // 16-bit pages: the reference is this far above the largest score
+    int up = 0;                  // 16-bit pages: values, and acc, are taken times 2^-up
     float sum[R8][CQ];           // the lane's part of the sum of weights
     float acc[MT][R8][4];
     float zsum[V4 ? NG : 1][R8][CQ];
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (fresh) {
             fresh = false;
             seg0 = place;
-            up = 0.0f;
+            up = 0;
             nplace = SOLO ? solo_units + SM::ITEM : pre[b + 1] - pre[b];
             len = seq_len(a, b, false);
             const int r0 = int(tile) % a.RT * RTILE;
@@ -763,10 +771,10 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
                     for (int c = 0; c < CQ; ++c) {
-                        const float nr = fmaxf(ref[t][c], Q8 ? rows_top(top[t][c]) : rows_top(top[t][c]) + up);
+                        const float nr = fmaxf(ref[t][c], rows_top(top[t][c]));
                         f[t][c] = ref[t][c] == -INFINITY ? 1.0f : exp2f(ref[t][c] - nr);
                         lost |= f[t][c] == 0.0f;
-                        ref[t][c] = nr, bar2[t][c] = (Q8 ? nr : nr - up) + PAT_SLACK;
+                        ref[t][c] = nr, bar2[t][c] = nr + PAT_SLACK;
                         off[t][c] = nr == -INFINITY ? 0.0f : nr;
                         sum[t][c] *= f[t][c];
                         if constexpr (V4) {
@@ -892,11 +900,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         }
                     }
                 } else {
-                    if (__any_sync(0xffffffffu, odd_values)) {
+                    if (__any_sync(0xffffffffu, odd_values) || up) {
                         // Weights go up to 2^PAT_SLACK and are divided by their sum at the
-                        // end.  For values of 2^64 or more (below it, 2^31 of them do not
-                        // pass fp32's range) the reference is put so far above the largest
-                        // score that all of the sequence's weights sum to at most 1/2.
+                        // end.  Values of 2^64 or more (below it, 2^31 of them do not pass
+                        // fp32's range), and all after the first of them, are taken times a
+                        // power of two that leaves all of the sequence's weights, times the
+                        // largest bf16, within half of that range.
                         // Tokens that hold Inf or NaN are added one by one, in fp32, to the
                         // queries that see them, and are zeros to the product, whose operands
                         // may not meet them: 0 * Inf would reach queries that do not see the
@@ -920,22 +929,14 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                                 }
                             }
                         }
-                        if (__any_sync(0xffffffffu, not_finite(sq)) && up == 0.0f) {
-                            up = PAT_SLACK + 1.0f + float(32 - __clz(len));
+                        if (up == 0 && __any_sync(0xffffffffu, not_finite(sq))) {
+                            up = int(PAT_SLACK) + 1 + 32 - __clz(len);
 #pragma unroll
-                            for (int r = 0; r < R8; ++r)
+                            for (int k = 0; k < MT; ++k)
 #pragma unroll
-                                for (int c = 0; c < CQ; ++c) {
-                                    const float nr = ref[r][c] + up;
-                                    const float f = nr == -INFINITY ? 1.0f : exp2f(ref[r][c] - nr);
-                                    ref[r][c] = nr, off[r][c] = nr == -INFINITY ? 0.0f : nr;
-                                    sum[r][c] *= f, p[u][r][c] *= f, p[u][r][CQ + c] *= f;
+                                for (int r = 0; r < R8; ++r)
 #pragma unroll
-                                    for (int k = 0; k < MT; ++k)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e)
-                                            if (TWICE || (e & 1) == c) acc[k][r][e] *= f;
-                                }
+                                    for (int e = 0; e < 4; ++e) acc[k][r][e] *= power2(-up);
                         }
                         uint32_t bits = __ballot_sync(0xffffffffu, not_finite(odd));
                         bits = (bits | bits >> 1) & 0x55555555u;  // bit 2 t: token t
@@ -956,7 +957,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                                         for (int h = 0; h < 2; ++h) {  // dims 16 k + 8 h + g
                                             const uint32_t d2 = uint32_t(k) * 32u + uint32_t(h) * 16u + uint32_t(g >> 1) * 4u;
                                             const uint32_t y2 = lds32(at + B::value(uint32_t(t), d2));
-                                            const float y = g & 1 ? bf16_hi(y2) : bf16_lo(y2);
+                                            const float y = (g & 1 ? bf16_hi(y2) : bf16_lo(y2)) * power2(-up);
                                             acc[k][r][2 * h + c] =
                                                 fmaf(ps > -INFINITY ? factor(pw, y) : pw, y, acc[k][r][2 * h + c]);
                                         }
@@ -966,6 +967,14 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         if (tl >= nv || ((bits >> (lane & 30)) & 1u)) {
 #pragma unroll
                             for (uint32_t k = 0; k < CHUNKS; ++k) sts128_zero(half + 16u * ((k + uint32_t(lane)) % CHUNKS));
+                        } else if (up) {
+                            const __nv_bfloat162 f = __float2bfloat162_rn(power2(-up));
+#pragma unroll
+                            for (uint32_t k = 0; k < CHUNKS; ++k) {
+                                const uint32_t to = half + 16u * ((k + uint32_t(lane)) % CHUNKS);
+                                const uint4 v = lds128(to);
+                                sts128(to, make_uint4(times(v.x, f), times(v.y, f), times(v.z, f), times(v.w, f)));
+                            }
                         }
                         fence_proxy_async();  // before a later copy into the slot
                         __syncwarp();
@@ -1027,7 +1036,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
             for (int c = 0; c < CQ; ++c) {
                 const int rr = TWICE ? tig : 8 * t + 2 * tig + c, r = r0 + rr;
-                const float l = rows_add(sum[t][c]);
+                const float l0 = rows_add(sum[t][c]);
+                // acc's unit: a row's result is acc / l, and a part's weight goes by l and base2
+                const float l = Q8 ? l0 : l0 * power2(-up), base2 = Q8 ? ref[t][c] : ref[t][c] + float(up);
                 if constexpr (TWICE) {
 #pragma unroll
                     for (int k = 0; k < MT; ++k) acc[k][t][0] += acc[k][t][1], acc[k][t][2] += acc[k][t][3];
@@ -1041,13 +1052,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     }
                 }
                 if (r >= a.R) continue;
-                const float base2 = ref[t][c];
                 if (whole) {
                     const int i = r / a.G, j = h * a.G + r - i * a.G;
                     const uint64_t row = (uint64_t(b) * uint32_t(a.m) + uint32_t(i)) * uint32_t(a.nq) + uint32_t(j);
                     const float bl = a.base_lse ? a.base_lse[row] : -INFINITY;
                     __syncwarp(0x11111111u << tig);  // the row's lanes have it before one writes lse
-                    const float lse = l > 0.0f ? (base2 + log2f(l)) * 0.69314718055994531f : (l == 0.0f ? -INFINITY : l);
+                    const float lse = l0 > 0.0f ? (ref[t][c] + log2f(l0)) * 0.69314718055994531f : (l0 == 0.0f ? -INFINITY : l0);
                     const float2 w = join_base(a, row, lse, bl, g == 0);
                     const float inv = l > 0.0f ? w.x / l : (l == 0.0f ? 0.0f : l);
                     uint16_t *o = a.out + row * D;

@@ -470,8 +470,9 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  *    overlap an input or another output, except that lse may be base_lse.
  * An Inf or NaN value of a BF16 page is one in its dim for the queries that see
  * its token (weights are positive, however small), and touches no others.  Finite
- * values give finite results up to bf16's largest; where a sequence holds values of
- * 2^64 or more, its weights below some 2^-80 of the largest count as zero.
+ * values give finite results up to bf16's largest.  Weights below 2^-118 of the
+ * largest count as zero; where a sequence holds values of 2^64 or more, so do its
+ * values below 2^-86.
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  Scores are products of the stored codes accumulated in fp32 (over
  * 8-bit keys a query row enters as fp16 times a power of two, exactly but for

@@ -214,6 +214,31 @@ def test_large_finite_values(n, nq, m, width, d):
                                (bo.numpy().astype(np.float64), bl.numpy().astype(np.float64)))
 
 
+@pytest.mark.parametrize("n,nq,width", [(40, 4, None), (40, 8, 4096), (40, 16, None), (3000, 4, None), (3000, 8, None)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+def test_large_values_of_small_weights(n, nq, width, d, first):
+    """Values up to the largest of bf16 whose weights are 2^-80 to 2^-110 of the
+    others': what they contribute is of any size, beside others of ordinary size in
+    their own dims and in the rest."""
+    H = 1
+    rng = np.random.default_rng(n + nq)
+    k, v = 0.01 * rng.standard_normal((n, H, d)), rng.standard_normal((n, H, d))
+    top = float(torch.finfo(torch.bfloat16).max)
+    at = np.arange(4) + (1 if first else n - 7)
+    k[:, :, 0] = 10.0
+    k[at, 0, 0] = 10.0 - np.log(2.0) * np.array([80, 90, 100, 110]) / 8
+    v[at, :, 5], v[at[::2], :, 9], v[at[1], :, 17] = top, -top, 2.0 ** 100
+    v[at, :, 20 + np.arange(4)] = top
+    k, v = _bf16(k).cuda(), _bf16(v).cuda()
+    q = 0.1 * rng.standard_normal((1, 1, nq, d))
+    q[..., 0] = 8.0
+    q = _bf16(q)
+    pg = Pages("bf16", H, d, 16, [n], max_pages=width)
+    pg.append(k, v, outs=False)
+    _check_with_infinities(*pg.attend(q.cuda(), 1.0), _f64(q), [_f64(k)], [_f64(v)], [n], 1.0)
+
+
 def test_small_values_keep_their_bits():
     """Values of about 2^-100, where no large ones are: nothing is scaled."""
     H, d, n = 2, 128, 200
