@@ -16,8 +16,8 @@ from .binding import (  # noqa: F401
     check, declared_functions, kvp_bandwidth_probe, KVP_PROBE_STORE, KVP_PROBE_BULK_STORE, KVP_PROBE_COPY,
     kvp_launch_count, kvp_test_fail_next_encode, kvp_test_limit_next_attend, kvp_test_limit_next_unpack, kvp_strerror, kvpool_attend, kvpool_attend_workspace_bytes, kvpool_attend_lora,
     kvpool_attend_lora_workspace_bytes, kvpool_decode_into, kvpool_encode, kvpool_encode_ex, kvpool_encode_noalloc, KVP_NOALLOC_SCRATCH_BYTES,
-    KVP_ERR_PAGE, KVP_PAGES_BF16, KVP_PAGES_K8V8, KVP_PAGES_K8V4, KVP_PAGES_MAX_SEQS, kvp_test_limit_next_pages_attend,
-    kvp_test_limit_next_pages_attend_lanes, PagesConfig, Rows, rows, kvpages_append,
-    kvpages_attend, kvpages_attend_workspace_bytes, kvpages_bytes, kvpages_init, kvpages_read, kvpages_status,
+    KVP_ERR_PAGE, KVP_PAGES_BF16, KVP_PAGES_K8V8, KVP_PAGES_K8V4, KVP_PAGES_K4V4, KVP_MAX_AXES, KVP_PAGES_MAX_SEQS, kvp_test_limit_next_pages_attend,
+    kvp_test_limit_next_pages_attend_lanes, PagesConfig, Rows, rows, kvpages_append, kvpages_append_axes,
+    kvpages_attend, kvpages_attend_window, kvpages_attend_workspace_bytes, kvpages_bytes, kvpages_init, kvpages_read, kvpages_status,
     kvpool_pool_bytes, kvpool_pool_bytes_ex, kvpool_status, KVP_K_PER_TENSOR, KVP_K_Q8_0, kvpool_workspace_bytes, load,
 )

@@ -40,6 +40,8 @@ KVP_K_Q8_0 = 1
 KVP_PAGES_BF16 = 0
 KVP_PAGES_K8V8 = 1
 KVP_PAGES_K8V4 = 2
+KVP_PAGES_K4V4 = 4
+KVP_MAX_AXES = 4
 KVP_PAGES_MAX_SEQS = 4096
 KVP_NOALLOC_SCRATCH_BYTES = 262144
 KVP_PROBE_STORE = 0
@@ -117,10 +119,14 @@ _SIGS = {
     "kvpages_init": (C.c_int, [_vp, _vp, C.c_size_t, _vp]),
     "kvpages_append": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_float,
                                  C.c_int, _vp, _vp, _vp, _vp, _vp]),
+    "kvpages_append_axes": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp, C.c_int, _vp, _vp, _vp,
+                                      C.c_float, C.c_int, _vp, _vp, _vp, _vp, _vp]),
     "kvpages_read": (C.c_int, [_vp, _vp, C.c_int, C.c_int, _vp, C.c_int, _vp, C.c_int, _vp, _vp, _vp]),
     "kvpages_attend_workspace_bytes": (C.c_size_t, [_vp, C.c_int, C.c_int, C.c_int]),
     "kvpages_attend": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, _vp, C.c_float, _vp, C.c_int, _vp, _vp,
                                  _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "kvpages_attend_window": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, _vp, C.c_float, C.c_int, C.c_int, _vp,
+                                        C.c_int, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
     "kvpages_status": (C.c_int, [_vp, _vp]),
     "kvp_strerror": (C.c_char_p, [C.c_int]),
     "kvp_launch_count": (C.c_uint64, []),
@@ -438,6 +444,41 @@ def kvpages_append(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, posit
                                  _buf(v_out, _T.bf16, n_tokens * h * d, "v_out"), _stream(stream))
 
 
+def _axes(x, least):
+    """A host array of axis numbers as a ctypes uint8 array of at least `least`: one
+    made earlier passes as it is."""
+    if x is None:
+        return None
+    if not isinstance(x, C.Array):
+        vals = [int(v) for v in x]
+        if vals and not 0 <= min(vals) <= max(vals) <= 255:
+            raise ValueError("axes: numbers from 0 to n_axes - 1 are needed, got %r" % (vals,))
+        x = (C.c_uint8 * max(1, len(vals)))(*vals)
+        n = len(vals)
+    else:
+        n = len(x)
+    if n < least or x._type_ is not C.c_uint8:
+        raise ValueError("axes: %d numbers of 8 bits are needed, got %d of %s" % (least, n, x._type_.__name__))
+    return x
+
+
+def kvpages_append_axes(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, positions, n_axes, axes, q_norm, k_norm,
+                        eps, rot_dim, inv_freq, q_out, k_out, v_out, stream=None):
+    """positions: int64 [n_axes][n_tokens]; axes: rot_dim/2 host numbers (any
+    sequence; a ctypes uint8 array is passed as it is); the rest as kvpages_append."""
+    cfg, w, ax = _pages(cfg), _floats(inv_freq, rot_dim // 2), _axes(axes, rot_dim // 2)
+    h, d = cfg.n_kv_heads, cfg.head_dim
+    q = _rows(q, n_tokens, n_q_heads, d, "q") if n_q_heads else None
+    k, v = _rows(k, n_tokens, h, d, "k"), _rows(v, n_tokens, h, d, "v")
+    return load().kvpages_append_axes(_addr(pages), _ref(cfg), layer, n_tokens, n_q_heads,
+                                      q, k, v, _buf(slots, _T.i64, n_tokens, "slots"),
+                                      _buf(positions, _T.i64, n_axes * n_tokens, "positions"), n_axes, _ref(ax),
+                                      _buf(q_norm, _T.bf16, d, "q_norm"), _buf(k_norm, _T.bf16, d, "k_norm"), eps, rot_dim,
+                                      _ref(w), _buf(q_out, _T.bf16, n_tokens * n_q_heads * d, "q_out"),
+                                      _buf(k_out, _T.bf16, n_tokens * h * d, "k_out"),
+                                      _buf(v_out, _T.bf16, n_tokens * h * d, "v_out"), _stream(stream))
+
+
 def kvpages_read(pages, cfg, layer, n_seqs, table, max_pages, lens, max_tokens, k_dst, v_dst, stream=None):
     cfg = _pages(cfg)
     n = n_seqs * cfg.n_kv_heads * max_tokens * cfg.head_dim
@@ -461,6 +502,18 @@ def kvpages_attend(pages, cfg, layer, n_seqs, n_q_tokens, n_q_heads, q, scale, t
                                  _buf(lens, _T.i32, n_seqs, "lens"), _buf(base_out, _T.f32, nd, "base_out"),
                                  _buf(base_lse, _T.f32, n, "base_lse"), _buf(out, _T.bf16, nd, "out"),
                                  _buf(lse, _T.f32, n, "lse"), _bytes_buf(ws, ws_bytes, "ws"), ws_bytes, _stream(stream))
+
+
+def kvpages_attend_window(pages, cfg, layer, n_seqs, n_q_tokens, n_q_heads, q, scale, window, sinks, table, max_pages, lens,
+                          base_out, base_lse, out, lse, ws, ws_bytes, stream=None):
+    cfg = _pages(cfg)
+    n = n_seqs * n_q_tokens * n_q_heads
+    nd = n * cfg.head_dim
+    return load().kvpages_attend_window(
+        _addr(pages), _ref(cfg), layer, n_seqs, n_q_tokens, n_q_heads, _buf(q, _T.bf16, nd, "q"), scale, window, sinks,
+        _buf(table, _T.i32, n_seqs * max_pages, "table"), max_pages, _buf(lens, _T.i32, n_seqs, "lens"),
+        _buf(base_out, _T.f32, nd, "base_out"), _buf(base_lse, _T.f32, n, "base_lse"), _buf(out, _T.bf16, nd, "out"),
+        _buf(lse, _T.f32, n, "lse"), _bytes_buf(ws, ws_bytes, "ws"), ws_bytes, _stream(stream))
 
 
 def kvpages_status(pages, stream=None):

@@ -38,7 +38,9 @@ int pages_ok(const kvp_pages_config *c) {
     if (!c) return KVP_ERR_ARG;
     if (c->n_layers <= 0 || c->n_kv_heads <= 0 || c->n_pages <= 0) return KVP_ERR_ARG;
     if (c->page_tokens < 16 || c->page_tokens > 1024 || (c->page_tokens & (c->page_tokens - 1))) return KVP_ERR_ARG;
-    if (c->format != KVP_PAGES_BF16 && c->format != KVP_PAGES_K8V8 && c->format != KVP_PAGES_K8V4) return KVP_ERR_ARG;
+    if (c->format != KVP_PAGES_BF16 && c->format != KVP_PAGES_K8V8 && c->format != KVP_PAGES_K8V4 &&
+        c->format != KVP_PAGES_K4V4)
+        return KVP_ERR_ARG;
     if (c->n_layers > KVP_MAX_LAYERS || c->n_kv_heads > 4096) return KVP_ERR_SIZE;
     if (c->head_dim != 64 && c->head_dim != 128) return KVP_ERR_UNSUPPORTED_D;
     // a container of at most 2^48 bytes: every offset fits 64 bits

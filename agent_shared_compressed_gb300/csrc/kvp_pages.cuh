@@ -40,6 +40,7 @@ __host__ __device__ inline uint32_t pages_block_bytes(int d, int format) {
     const uint32_t row = uint32_t(d), ng = uint32_t(d / 32);
     if (format == KVP_PAGES_BF16) return 16u * 4u * row;
     if (format == KVP_PAGES_K8V8) return 16u * (2u * row + 4u * ng);
+    if (format == KVP_PAGES_K4V4) return 16u * (row + 8u * ng);
     return 16u * (row + row / 2u + 6u * ng);
 }
 
@@ -125,11 +126,12 @@ __device__ __forceinline__ void pages_flag(const PagesView &v, uint32_t f) {
 template <int D, int FMT>
 struct Block {
     static constexpr bool Q8 = FMT != KVP_PAGES_BF16;
-    static constexpr bool V4 = FMT == KVP_PAGES_K8V4;
+    static constexpr bool K4 = FMT == KVP_PAGES_K4V4;
+    static constexpr bool V4 = FMT == KVP_PAGES_K8V4 || K4;
     static constexpr int NG = D / 32;                               // scale groups of a row
-    static constexpr uint32_t KROW = Q8 ? D : 2 * D;                // bytes of a key row
+    static constexpr uint32_t KROW = K4 ? D / 2 : (Q8 ? D : 2 * D);  // bytes of a key row
     static constexpr uint32_t VROW = V4 ? D / 2 : KROW;             // bytes of a value row
-    static constexpr uint32_t SROW = 2 * NG;                        // key scales of a token (fp16)
+    static constexpr uint32_t SROW = K4 ? 4 * NG : 2 * NG;          // key scales of a token (fp16), K4: then its zero points
     static constexpr uint32_t VSROW = V4 ? 4 * NG : 2 * NG;         // value scales (fp16), V4: (scale, zero) pairs
     static constexpr uint32_t OFF_V = 16 * KROW;
     static constexpr uint32_t OFF_KS = OFF_V + 16 * VROW;
@@ -140,7 +142,7 @@ struct Block {
     static __host__ __device__ __forceinline__ uint32_t key(uint32_t t, uint32_t x) {
         const uint32_t at = t * KROW + x;
         if (!Q8) return at ^ ((t & 7u) << 4);
-        return D == 128 ? at ^ ((t & 1u) << 4) : at;
+        return D == 128 && !K4 ? at ^ ((t & 1u) << 4) : at;
     }
     // byte `x` of value row t
     static __host__ __device__ __forceinline__ uint32_t value(uint32_t t, uint32_t x) {
@@ -156,6 +158,9 @@ struct Block {
 //  8-bit keys: the lane's d/4 bytes are contiguous, 32-bit word 2 b + e holds
 //         dims 32 b + 8 tig + 4 e + 0..3 (code + 128): the key operand of two
 //         k-steps of 16 dims per group
+//  4-bit keys: the lane's d/8 bytes are contiguous, 32-bit word b holds dims
+//         32 b + 8 tig + 2 j in its nibbles j and + 2 j + 1 in its nibbles 4 + j (j < 4):
+//         a pair of dims is one mask and shift away from a key operand
 //  8-bit values: two granules of d/8 bytes, granule e's word b holds dims
 //         32 b + 8 tig + 4 e + 0..3 (code + 128): granule g = 2 tig + e is what
 //         lane g of a value fragment reads
@@ -243,6 +248,31 @@ __device__ __forceinline__ void load_value4(const uint8_t *blk, uint32_t t, int 
         for (int b = 0; b < D / 32; ++b) c.h[b][e] = (w[e * (D / 64) + b / 2] >> (16 * (b & 1))) & 0xFFFFu;
 }
 
+// 4-bit keys: a word a group, as above.
+template <int D>
+struct Lane4K {
+    uint32_t w[D / 32];
+};
+template <int D, int FMT>
+__device__ __forceinline__ void store_key4(uint8_t *blk, uint32_t t, int tig, const Lane4K<D> &c) {
+    uint8_t *at = blk + Block<D, FMT>::key(t, tig * (D / 8));
+    if constexpr (D == 128)
+        *reinterpret_cast<uint4 *>(at) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    else
+        *reinterpret_cast<uint2 *>(at) = make_uint2(c.w[0], c.w[1]);
+}
+template <int D, int FMT>
+__device__ __forceinline__ void load_key4(const uint8_t *blk, uint32_t t, int tig, Lane4K<D> &c) {
+    const uint8_t *at = blk + Block<D, FMT>::key(t, tig * (D / 8));
+    if constexpr (D == 128) {
+        const uint4 a = ld_once_v4(at);
+        c.w[0] = a.x, c.w[1] = a.y, c.w[2] = a.z, c.w[3] = a.w;
+    } else {
+        const uint2 a = ld_once_v2(at);
+        c.w[0] = a.x, c.w[1] = a.y;
+    }
+}
+
 // Four codes + 128 of a word as fp32 codes: 2^23 + u, less 2^23 + 128 (exact).
 __device__ __forceinline__ void codes8(uint32_t w, float (&x)[4]) {
     x[0] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650u)) - 8388736.0f;
@@ -295,6 +325,16 @@ __device__ __forceinline__ void load_key_row(const uint8_t *blk, uint32_t t, int
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[b][2 * i] = bf16_lo(w[i]), x[b][2 * i + 1] = bf16_hi(w[i]);
         }
+    } else if constexpr (B::K4) {
+        Lane4K<D> c;
+        float s[B::NG], z[B::NG];
+        load_key4<D, FMT>(blk, t, tig, c);
+        load_scales<B::NG>(blk + B::OFF_KS + t * B::SROW, s);
+        load_scales<B::NG>(blk + B::OFF_KS + t * B::SROW + 2 * B::NG, z);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[b][j] = fmaf(float((c.w[b] >> (4 * (j >> 1) + 16 * (j & 1))) & 15u), s[b], z[b]);
     } else {
         Lane8<D> c;
         float s[B::NG];

@@ -48,6 +48,7 @@ struct AppendArgs {
     int group_steps, run;  // steps of a token group, of a block
     int64_t steps;
     uint64_t turn[64];  // w_i / 2 pi mod 1, in units of 2^-64
+    uint8_t axis[64];   // which of the positions pair i turns by
 };
 
 // The kernels here are placed while the one before them in the stream still runs
@@ -179,11 +180,28 @@ __device__ __forceinline__ void encode8(float2 (&x)[D / 32][4], Lane8<D> &c, uin
     }
 }
 
-// Codes of a value row at 4 bits: s = fp16(fl(max - min) fl(1/15)), z =
+// Codes of a value or key row at 4 bits: s = fp16(fl(max - min) fl(1/15)), z =
 // fp16(min), code = (x - z) / s rounded to nearest even, in [0, 15], decided as
 // above with x - z carried exactly.  x becomes the values held.
 template <int D>
-__device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane4<D> &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
+__device__ __forceinline__ void place4(int b, const float2 (&r)[4], Lane4<D> &c) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        // the low bits of 2^23 1.5 + code are the code: place four nibbles by sums of shifts
+        const uint32_t lo2 = (__float_as_uint(r[2 * e].x) & 15u) | (__float_as_uint(r[2 * e].y) & 15u) << 4;
+        const uint32_t hi2 = (__float_as_uint(r[2 * e + 1].x) & 15u) | (__float_as_uint(r[2 * e + 1].y) & 15u) << 4;
+        c.h[b][e] = lo2 | hi2 << 8;
+    }
+}
+template <int D>
+__device__ __forceinline__ void place4(int b, const float2 (&r)[4], Lane4K<D> &c) {
+    c.w[b] = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c.w[b] |= ((__float_as_uint(r[j].x) & 15u) | (__float_as_uint(r[j].y) & 15u) << 16) << (4 * j);
+}
+template <int D, typename Lane>
+__device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
     constexpr int NB = D / 32;
     constexpr float MAGIC = 12582912.0f;
     if (drop_nonfinite<NB>(x)) bad |= FLAG_NONFINITE;
@@ -219,13 +237,7 @@ __device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane4<D> &c, uin
             for (int j = 0; j < 4; ++j)
                 r[j] = make_float2(code4_exact(x[b][j].x, z, s, rs) + MAGIC, code4_exact(x[b][j].y, z, s, rs) + MAGIC);
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            // the low bits of 2^23 1.5 + code are the code: place four nibbles by sums of shifts
-            const uint32_t lo2 = (__float_as_uint(r[2 * e].x) & 15u) | (__float_as_uint(r[2 * e].y) & 15u) << 4;
-            const uint32_t hi2 = (__float_as_uint(r[2 * e + 1].x) & 15u) | (__float_as_uint(r[2 * e + 1].y) & 15u) << 4;
-            c.h[b][e] = lo2 | hi2 << 8;
-        }
+        place4<D>(b, r, c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[b][j] = fma2(add2(r[j], both(-MAGIC)), both(s), both(z));
     }
@@ -320,7 +332,8 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
                     const int64_t at = grp * APP_TOKENS + t;
                     float s = 0.0f, c = 1.0f;
                     if (at < a.n) {
-                        const int64_t turns = int64_t(uint64_t(a.positions[at]) * a.turn[p]);  // mod one turn
+                        const int64_t pos = a.positions[int64_t(a.axis[p]) * a.n + at];
+                        const int64_t turns = int64_t(uint64_t(pos) * a.turn[p]);  // mod one turn
                         sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
                     }
                     cosines[t][p] = c, sines[t][p] = s;
@@ -383,6 +396,21 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
                         *reinterpret_cast<uint4 *>(hb + B::key(row16, (4 * b + tig) * 16)) = pack8(x[b]);
+                }
+            } else if constexpr (B::K4) {
+                Lane4K<D> c;
+                uint32_t szb[NB];
+                encode4<D>(x, c, szb, bad);
+                if (hb) {
+                    store_key4<D, FMT>(hb, row16, tig, c);
+                    if (tig == 0) {  // the scales, then the zero points
+                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) {
+                            s[i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x5410u);
+                            s[NB / 2 + i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x7632u);
+                        }
+                    }
                 }
             } else {
                 Lane8<D> c;
@@ -581,6 +609,16 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
                    const kvp_rows *k, const kvp_rows *v, const int64_t *slots, const int64_t *positions,
                    const void *q_norm, const void *k_norm, float eps, int rot_dim, const float *inv_freq, void *q_out,
                    void *k_out, void *v_out, void *stream) {
+    static const uint8_t one_axis[64] = {0};
+    return kvpages_append_axes(pages, cfg, layer, n_tokens, n_q_heads, q, k, v, slots, positions, 1, one_axis, q_norm, k_norm,
+                               eps, rot_dim, inv_freq, q_out, k_out, v_out, stream);
+}
+
+int kvpages_append_axes(void *pages, const kvp_pages_config *cfg, int layer, int n_tokens, int n_q_heads,
+                        const kvp_rows *q, const kvp_rows *k, const kvp_rows *v, const int64_t *slots,
+                        const int64_t *positions, int n_axes, const uint8_t *axes, const void *q_norm,
+                        const void *k_norm, float eps, int rot_dim, const float *inv_freq, void *q_out, void *k_out,
+                        void *v_out, void *stream) {
     const int rc = pages_ok(cfg);
     if (rc != KVP_OK) return rc;
     if (!pages || layer < 0 || layer >= cfg->n_layers || n_tokens < 0 || n_q_heads < 0) return KVP_ERR_ARG;
@@ -588,9 +626,10 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
     if (!k || !v || !k->ptr || !v->ptr || !slots) return KVP_ERR_ARG;
     if (n_q_heads > 0 && (!q || !q->ptr || !q_out)) return KVP_ERR_ARG;
     if (rot_dim != 0 && rot_dim != 64 && !(rot_dim == 128 && cfg->head_dim == 128)) return KVP_ERR_ARG;
-    if (rot_dim > 0 && (!positions || !inv_freq)) return KVP_ERR_ARG;
+    if (n_axes < 1 || n_axes > KVP_MAX_AXES) return KVP_ERR_ARG;
+    if (rot_dim > 0 && (!positions || !inv_freq || !axes)) return KVP_ERR_ARG;
     for (int i = 0; i < rot_dim / 2; ++i)
-        if (!std::isfinite(inv_freq[i])) return KVP_ERR_ARG;
+        if (!std::isfinite(inv_freq[i]) || axes[i] >= n_axes) return KVP_ERR_ARG;
     if ((q_norm || k_norm) && !(std::isfinite(eps) && eps >= 0.0f)) return KVP_ERR_ARG;
     if (!aligned(pages, 256) || !rows_aligned(k) || !rows_aligned(v) || (n_q_heads > 0 && !rows_aligned(q)) ||
         !aligned(slots, 8) || !aligned(positions, 8) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
@@ -609,7 +648,10 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
     a.q_out = static_cast<uint16_t *>(q_out);
     a.k_out = static_cast<uint16_t *>(k_out), a.v_out = static_cast<uint16_t *>(v_out);
     a.eps = eps, a.n = n_tokens, a.nq = n_q_heads, a.rot = rot_dim;
-    for (int i = 0; i < 64; ++i) a.turn[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
+    for (int i = 0; i < 64; ++i) {
+        a.turn[i] = i < rot_dim / 2 ? turn_fraction(inv_freq[i]) : 0;
+        a.axis[i] = i < rot_dim / 2 ? axes[i] : 0;
+    }
     const int rows = n_q_heads + 2 * cfg->n_kv_heads;
     a.group_steps = (rows + APP_WARPS - 1) / APP_WARPS;
     a.steps = (int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS * a.group_steps;
@@ -623,8 +665,10 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
             return d128 ? launch_append<128, KVP_PAGES_BF16>(a, grid, st) : launch_append<64, KVP_PAGES_BF16>(a, grid, st);
         case KVP_PAGES_K8V8:
             return d128 ? launch_append<128, KVP_PAGES_K8V8>(a, grid, st) : launch_append<64, KVP_PAGES_K8V8>(a, grid, st);
-        default:
+        case KVP_PAGES_K8V4:
             return d128 ? launch_append<128, KVP_PAGES_K8V4>(a, grid, st) : launch_append<64, KVP_PAGES_K8V4>(a, grid, st);
+        default:
+            return d128 ? launch_append<128, KVP_PAGES_K4V4>(a, grid, st) : launch_append<64, KVP_PAGES_K4V4>(a, grid, st);
     }
 }
 
@@ -656,8 +700,10 @@ int kvpages_read(const void *pages, const kvp_pages_config *cfg, int layer, int 
             return d128 ? launch_read<128, KVP_PAGES_BF16>(a, grid, st) : launch_read<64, KVP_PAGES_BF16>(a, grid, st);
         case KVP_PAGES_K8V8:
             return d128 ? launch_read<128, KVP_PAGES_K8V8>(a, grid, st) : launch_read<64, KVP_PAGES_K8V8>(a, grid, st);
-        default:
+        case KVP_PAGES_K8V4:
             return d128 ? launch_read<128, KVP_PAGES_K8V4>(a, grid, st) : launch_read<64, KVP_PAGES_K8V4>(a, grid, st);
+        default:
+            return d128 ? launch_read<128, KVP_PAGES_K4V4>(a, grid, st) : launch_read<64, KVP_PAGES_K4V4>(a, grid, st);
     }
 }
 

@@ -90,6 +90,10 @@ extern "C" {
 #define KVP_PAGES_K8V8 1  /* both q8_0: 32 along d share an fp16 scale, 8-bit codes  */
 #define KVP_PAGES_K8V4 2  /* keys q8_0; values 4-bit, asymmetric groups of 32 along d
                              with an fp16 scale and zero point                      */
+#define KVP_PAGES_K4V4 4  /* keys as well as values so, in 4 bits                    */
+
+/* Most axes of a position (kvpages_append_axes). */
+#define KVP_MAX_AXES 4
 
 /* Shape of one KV cache: n_layers tensors of [n_kv_heads][n_tokens][head_dim]. */
 typedef struct kvp_shape {
@@ -427,9 +431,9 @@ int kvpages_init(const kvp_pages_config *cfg, void *pages, size_t pages_bytes, v
  *    attention.  No output may overlap an input, except that q_out may be q's
  *    own contiguous tensor.
  * Codes: 8-bit s = fp16(max|x| * fl(1/127)), code = RNE(x / s) in [-127, 127],
- * of the rotated key in fp32 (never rounded to bf16 first); 4-bit
- * s = fp16(fl(max - min) * fl(1/15)), z = fp16(min), code = RNE((x - z) / s) in
- * [0, 15]; s = 0 gives codes 0.  Non-finite elements are kept in BF16 pages;
+ * of the rotated key in fp32 (never rounded to bf16 first); 4-bit (a K4V4 key's
+ * too, of the same fp32 values) s = fp16(fl(max - min) * fl(1/15)), z = fp16(min),
+ * code = RNE((x - z) / s) in [0, 15]; s = 0 gives codes 0.  Non-finite elements are kept in BF16 pages;
  * elsewhere they count and code as zeros and kvpages_status reports
  * KVP_ERR_NONFINITE; a scale or zero point beyond fp16 is held at its largest
  * value and reported as KVP_ERR_RANGE; a slot past the container is not
@@ -438,6 +442,21 @@ int kvpages_append(void *pages, const kvp_pages_config *cfg, int layer, int n_to
                    const kvp_rows *q, const kvp_rows *k, const kvp_rows *v, const int64_t *slots,
                    const int64_t *positions, const void *q_norm, const void *k_norm, float eps, int rot_dim,
                    const float *inv_freq, void *q_out, void *k_out, void *v_out, void *stream);
+
+/* kvpages_append for positions of several axes (time, height and width of a
+ * picture's or a film's patches): the pair of dims i and i + rot_dim/2 is turned
+ * by positions[axes[i]][t] * inv_freq[i].
+ *  n_axes: 1 to KVP_MAX_AXES.  positions: device int64 [n_axes][n_tokens].
+ *  axes: HOST array of rot_dim/2 axis numbers below n_axes (KVP_ERR_ARG
+ *    otherwise), read during the call only: sections of pairs, axes in turn, or any
+ *    other assignment.
+ * Everything else, results included, as kvpages_append, which is this call with one
+ * axis. */
+int kvpages_append_axes(void *pages, const kvp_pages_config *cfg, int layer, int n_tokens, int n_q_heads,
+                        const kvp_rows *q, const kvp_rows *k, const kvp_rows *v, const int64_t *slots,
+                        const int64_t *positions, int n_axes, const uint8_t *axes, const void *q_norm,
+                        const void *k_norm, float eps, int rot_dim, const float *inv_freq, void *q_out, void *k_out,
+                        void *v_out, void *stream);
 
 /* Read sequences back as bf16 past_key_values of one layer.
  *  table: device int32 [n_seqs][max_pages] page ids; lens: device
@@ -476,7 +495,8 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  Scores are products of the stored codes accumulated in fp32 (over
  * 8-bit keys a query row enters as fp16 times a power of two, exactly but for
- * elements below 2^-28 of its largest); softmax statistics are fp32, exponentials
+ * elements below 2^-28 of its largest, over 4-bit keys 2^-24; a group's zero point
+ * enters times the sum of the query's 32 elements, in fp32); softmax statistics are fp32, exponentials
  * the hardware's in base 2 (2^-22); the weights (times the values' scales) enter
  * the value product as a sum of two bf16 (2^-17).  The kernel waits for its bulk
  * copies of the pages at most about half a second; should a wait run out, the
@@ -493,6 +513,22 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
                    int n_q_heads, const void *q, float scale, const int32_t *table, int max_pages,
                    const int32_t *lens, const float *base_out, const float *base_lse, void *out, float *lse, void *ws,
                    size_t ws_bytes, void *stream);
+
+/* kvpages_attend with a sliding window: query token i of sequence b, at place
+ * p = lens[b] - n_q_tokens + i, sees its newest `window` tokens (its own among
+ * them: those after p - window) and the sequence's first `sinks` ones.
+ *  window: 0 for none (then this is kvpages_attend), else as many tokens as a query
+ *    sees; may be more than there are.  sinks: 0 or more; without a window they say
+ *    nothing.  KVP_ERR_ARG for negative ones.
+ * Bytes and time go by what is seen.  Table entries of pages that hold no token
+ * which one of the sequence's queries sees are not read: their pages may be used
+ * for something else.  Whatever unseen tokens of other pages hold (Inf and NaN
+ * too) has no part in the result.  Everything else as kvpages_attend; the same
+ * workspace. */
+int kvpages_attend_window(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
+                          int n_q_heads, const void *q, float scale, int window, int sinks, const int32_t *table,
+                          int max_pages, const int32_t *lens, const float *base_out, const float *base_lse, void *out,
+                          float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronises `stream`, then returns KVP_OK or the first device-detected
  * error recorded in the container's header (KVP_ERR_HEADER if `pages` does not
