@@ -42,6 +42,7 @@ KVP_PAGES_K8V8 = 1
 KVP_PAGES_K8V4 = 2
 KVP_PAGES_K4V4 = 4
 KVP_MAX_AXES = 4
+KVP_PROMPT_MAX_SEQS = 65536
 KVP_PAGES_MAX_SEQS = 4096
 KVP_NOALLOC_SCRATCH_BYTES = 262144
 KVP_PROBE_STORE = 0
@@ -79,6 +80,16 @@ class PagesConfig(C.Structure):
     def __repr__(self):
         return "PagesConfig(L=%d, H=%d, d=%d, P=%d, pages=%d, format=%d)" % (
             self.n_layers, self.n_kv_heads, self.head_dim, self.page_tokens, self.n_pages, self.format)
+
+
+class PromptShape(C.Structure):
+    """kvp_prompt_shape: sequences, rows of q, rows of k and v, heads, head_dim."""
+    _fields_ = [("n_seqs", C.c_int32), ("n_q_tokens", C.c_int32), ("n_k_tokens", C.c_int32), ("n_q_heads", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+    def __repr__(self):
+        return "PromptShape(B=%d, n=%d, keys=%d, nq=%d, H=%d, d=%d)" % (
+            self.n_seqs, self.n_q_tokens, self.n_k_tokens, self.n_q_heads, self.n_kv_heads, self.head_dim)
 
 
 class Rows(C.Structure):
@@ -128,6 +139,10 @@ _SIGS = {
     "kvpages_attend_window": (C.c_int, [_vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, _vp, C.c_float, C.c_int, C.c_int, _vp,
                                         C.c_int, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
     "kvpages_status": (C.c_int, [_vp, _vp]),
+    "kvprompt_workspace_bytes": (C.c_size_t, [_vp]),
+    "kvprompt_attend": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_float, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  C.c_size_t, _vp]),
+    "kvprompt_status": (C.c_int, [_vp, _vp]),
     "kvp_strerror": (C.c_char_p, [C.c_int]),
     "kvp_launch_count": (C.c_uint64, []),
     "kvp_bandwidth_probe": (C.c_int, [C.c_int, _vp, _vp, C.c_size_t, _vp]),
@@ -518,6 +533,34 @@ def kvpages_attend_window(pages, cfg, layer, n_seqs, n_q_tokens, n_q_heads, q, s
 
 def kvpages_status(pages, stream=None):
     return load().kvpages_status(_addr(pages), _stream(stream))
+
+
+def _prompt(s):
+    return s if s.__class__ is PromptShape else PromptShape(*s)
+
+
+def kvprompt_workspace_bytes(shape):
+    shape = _prompt(shape)
+    return int(load().kvprompt_workspace_bytes(_ref(shape)))
+
+
+def kvprompt_attend(shape, q, k, v, q_first, k_first, k_lens, scale, window, sinks, base_out, base_lse, out, lse, error, ws,
+                    ws_bytes, stream=None):
+    """q, k, v: [tokens][heads][head_dim] tensors (strided views will do) or Rows;
+    error: an int32 tensor of one element, or None.  ValueError for tensors that do not
+    hold what the call reads or writes, as the page calls."""
+    shape = _prompt(shape)
+    b, n, t, nq, h, d = shape.n_seqs, shape.n_q_tokens, shape.n_k_tokens, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
+    q, k, v = _rows(q, n, nq, d, "q"), _rows(k, t, h, d, "k"), _rows(v, t, h, d, "v")
+    return load().kvprompt_attend(_ref(shape), q, k, v, _buf(q_first, _T.i32, b + 1, "q_first"), _buf(k_first, _T.i32, b, "k_first"),
+                                  _buf(k_lens, _T.i32, b, "k_lens"), scale, window, sinks,
+                                  _buf(base_out, _T.f32, n * nq * d, "base_out"), _buf(base_lse, _T.f32, n * nq, "base_lse"),
+                                  _buf(out, _T.bf16, n * nq * d, "out"), _buf(lse, _T.f32, n * nq, "lse"),
+                                  _buf(error, _T.i32, 1, "error"), _bytes_buf(ws, ws_bytes, "ws"), ws_bytes, _stream(stream))
+
+
+def kvprompt_status(error, stream=None):
+    return load().kvprompt_status(_buf(error, _T.i32, 1, "error"), _stream(stream))
 
 
 def kvp_strerror(status):

@@ -19,7 +19,8 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvcodec.so")
 
 SOURCES = ["kvp_host.cu", "kvpool_encode.cu", "kvpool_decode.cu", "cachecard.cu", "kvpool_noalloc.cu", "kvpool_attend.cu",
-           "kvp_probe.cu", "kvpages_append.cu", "kvpages_attend.cu", "kvpages_attend_4bit.cu", "kvpages_attend_window.cu"]
+           "kvp_probe.cu", "kvpages_append.cu", "kvpages_attend.cu", "kvpages_attend_4bit.cu", "kvpages_attend_window.cu",
+           "kvprompt.cu"]
 HEADERS = ["kvp_internal.cuh", "kvp_vec.cuh", "kvp_async.cuh", "kvp_pages.cuh", "kvpages_attend.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

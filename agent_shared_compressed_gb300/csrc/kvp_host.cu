@@ -50,6 +50,17 @@ int pages_ok(const kvp_pages_config *c) {
     return KVP_OK;
 }
 
+int flags_to_status(uint32_t f) {
+    if (f & FLAG_HEADER) return KVP_ERR_HEADER;
+    if (f & FLAG_TIMEOUT) return KVP_ERR_TIMEOUT;
+    if (f & FLAG_PAGE) return KVP_ERR_PAGE;
+    if (f & FLAG_BITS) return KVP_ERR_BITS;
+    if (f & FLAG_SIZE) return KVP_ERR_SIZE;
+    if (f & FLAG_NONFINITE) return KVP_ERR_NONFINITE;
+    if (f & FLAG_RANGE) return KVP_ERR_RANGE;
+    return KVP_OK;
+}
+
 }  // namespace kvp
 
 using namespace kvp;
@@ -80,17 +91,6 @@ const char *kvp_strerror(int st) {
 }
 
 uint64_t kvp_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
-
-static int flags_to_status(uint32_t f) {
-    if (f & FLAG_HEADER) return KVP_ERR_HEADER;
-    if (f & FLAG_TIMEOUT) return KVP_ERR_TIMEOUT;
-    if (f & FLAG_PAGE) return KVP_ERR_PAGE;
-    if (f & FLAG_BITS) return KVP_ERR_BITS;
-    if (f & FLAG_SIZE) return KVP_ERR_SIZE;
-    if (f & FLAG_NONFINITE) return KVP_ERR_NONFINITE;
-    if (f & FLAG_RANGE) return KVP_ERR_RANGE;
-    return KVP_OK;
-}
 
 int kvpool_status(const void *pool, void *stream) {
     if (!pool) return KVP_ERR_ARG;

@@ -89,6 +89,7 @@ int shape_ok(const kvp_shape *s);            // KVP_OK or an error code
 int sm_count();                              // SMs of the current device (cached)
 void count_launch(int n = 1);                // adds to kvp_launch_count()
 int launch_status();                         // KVP_OK or KVP_ERR_CUDA after launches
+int flags_to_status(uint32_t flags);         // the first of an error word's FLAG_* as a status
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // ---------------------------------------------------------------------------

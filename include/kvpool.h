@@ -34,7 +34,7 @@
  *    stream).  Every compute call only enqueues work on that stream and
  *    returns; it never allocates, frees or synchronises device memory.  The
  *    only synchronising calls are kvpool_status, cachecard_status,
- *    cachecard_read_header and kvpages_status, which say so.
+ *    cachecard_read_header, kvpages_status and kvprompt_status, which say so.
  *  - The caller owns every buffer.  Device pointers to KV tensors must be
  *    16-byte aligned; pool, card and page buffers 256-byte aligned; workspaces
  *    16-byte aligned.
@@ -534,6 +534,65 @@ int kvpages_attend_window(const void *pages, const kvp_pages_config *cfg, int la
  * error recorded in the container's header (KVP_ERR_HEADER if `pages` does not
  * hold a version-1 container, or a call described another one). */
 int kvpages_status(const void *pages, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Prompts                                                                 */
+/* ---------------------------------------------------------------------- */
+
+/* Most sequences of one kvprompt_attend call. */
+#define KVP_PROMPT_MAX_SEQS 65536
+
+/* Sizes of a prompt call: sequences, rows of q and of k and v (of all sequences),
+ * heads; n_q_heads a multiple of n_kv_heads, at most 128 times it. */
+typedef struct kvp_prompt_shape {
+    int32_t n_seqs;
+    int32_t n_q_tokens;
+    int32_t n_k_tokens;
+    int32_t n_q_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} kvp_prompt_shape;
+
+/* Bytes of device workspace kvprompt_attend needs (0 for an invalid shape).  No
+ * initialisation; calls that may overlap on the GPU need one each. */
+size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape);
+
+/* Attention of whole prompts over bf16 keys and values: what kvpages_append returns
+ * of a prompt (q_out, k_out, v_out), what kvpages_read, kvpool_decode_into or
+ * cachecard_unpack rebuild, or a model's own projections.
+ *  q: [n_q_tokens][n_q_heads][head_dim] rows, the sequences' new tokens one sequence
+ *    after the other: sequence b's are rows q_first[b] .. q_first[b + 1] - 1.
+ *  k, v: [n_k_tokens][n_kv_heads][head_dim] rows; sequence b's keys and values are
+ *    rows k_first[b] .. k_first[b] + k_lens[b] - 1, its new tokens' the last ones
+ *    (sequences may share rows).  A [heads][tokens][head_dim] tensor is rows too
+ *    (kvp_rows' strides).  Query head j reads KV head j / (n_q_heads / n_kv_heads).
+ *    Strides of more than one token or head are positive and below 2^38.
+ *  q_first: device int32[n_seqs + 1], not decreasing; k_first, k_lens: device
+ *    int32[n_seqs].
+ *  New token i of n is at place p = k_lens[b] - n + i and sees the places t <= p; with
+ *    a window > 0 of those the newest `window` (its own among them: t > p - window)
+ *    and the sequence's first `sinks` (t < sinks).  window 0: no window.
+ *  base_out, base_lse: device fp32 [n_q_tokens][n_q_heads]([head_dim]), both or
+ *    neither (NULL): attention of the same queries over other tokens (kvpool_attend
+ *    with a prompt's tokens as its agents).  The result is then attention over both.
+ *  out: device bf16 [n_q_tokens][n_q_heads][head_dim].  lse: device fp32
+ *    [n_q_tokens][n_q_heads] or NULL (natural log).  Rows of no sequence are left as
+ *    they are.  No output may overlap an input or another output, except that lse may
+ *    be base_lse.
+ *  error: device uint32 or NULL; the call sets bits in it (the caller clears it once;
+ *    kvprompt_status reads it).  A sequence whose rows lie outside q, k or v, or whose
+ *    numbers are negative, is skipped and reported as KVP_ERR_PAGE.
+ * A query that sees no token gets the base's output and lse, or zeros and -inf
+ * without one.  What a query does not see (Inf and NaN too) has no part in its
+ * result. */
+int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_rows *k, const kvp_rows *v,
+                    const int32_t *q_first, const int32_t *k_first, const int32_t *k_lens, float scale, int window,
+                    int sinks, const float *base_out, const float *base_lse, void *out, float *lse, uint32_t *error,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/* Synchronises `stream`, then returns KVP_OK or the first device-detected error
+ * recorded in the word that kvprompt_attend was given. */
+int kvprompt_status(const uint32_t *error, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */

@@ -163,3 +163,30 @@ class Pages:
 def split(x, lens):
     cut = np.cumsum([0] + list(lens))
     return [x[cut[i]: cut[i + 1]] for i in range(len(lens))]
+
+
+def prompt(q, k, v, n_first, window, sinks, scale):
+    """As rows(), of a whole sequence's new tokens q [n][nq][d] at places n_first ...: by
+    matrix products."""
+    n, nq, d = q.shape
+    T, H = k.shape[:2]
+    out, lse, mass, reach = np.zeros((n, nq, d)), np.full((n, nq), -np.inf), np.zeros((n, nq, d)), np.zeros((n, nq))
+    if not T or not n:
+        return out, lse, mass, reach
+    p, t = n_first + np.arange(n)[:, None], np.arange(T)[None, :]
+    see = t <= p
+    if window:
+        see &= (t > p - window) | (t < sinks)
+    some = see.any(1)
+    for j in range(nq):
+        h = j // (nq // H)
+        kh, vh = np.where(np.isfinite(k[:, h]), k[:, h], 0), np.where(np.isfinite(v[:, h]), v[:, h], 0)
+        s = np.where(see, scale * (q[:, j] @ kh.T), -np.inf)
+        reach[:, j] = np.where(see, abs(scale) * (np.abs(q[:, j]) @ np.abs(kh).T), 0).max(1)
+        top = np.where(some, s.max(1), 0)
+        e = np.exp(s - top[:, None])
+        tot = np.where(some, e.sum(1), 1)
+        w = e / tot[:, None]
+        out[:, j], mass[:, j] = w @ vh, w @ np.abs(vh)
+        lse[:, j] = np.where(some, top + np.log(tot), -np.inf)
+    return out, lse, mass, reach

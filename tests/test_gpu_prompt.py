@@ -1,0 +1,328 @@
+"""GPU tests of attention of whole prompts against 64 bits.  Weights enter the value
+product as bf16: 2^-8 of sum p |v| (their sum is taken before that)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import agent_shared_compressed_gb300 as kv
+from agent_shared_compressed_gb300 import build as kvbuild
+import longhelp as Lg
+from kvhelp import Guarded
+
+pytestmark = pytest.mark.gpu
+WEIGHTS = 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kvbuild.build()
+    kv.load()
+
+
+class Call:
+    """Sequences of (new tokens, tokens behind them), their tensors, and one call."""
+
+    def __init__(self, seqs, H, G, d, seed=0, layout="packed", gap=0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        self.seqs, self.H, self.nq, self.d = seqs, H, H * G, d
+        self.q_first, self.k_first, n, t = [0], [], 0, gap
+        for new, past in seqs:
+            n += new
+            self.q_first.append(n)
+            self.k_first.append(t)
+            t += new + past + gap
+        self.n, self.t = n + gap, t
+        q = Lg.bf16(spread * rng.standard_normal((self.n, self.nq, d))).cuda()
+        k, v = (Lg.bf16(rng.standard_normal((self.t, H, d))).cuda() for _ in range(2))
+        if layout == "fused":            # slices of one projection's rows, and a wider row for q
+            x = torch.cat([k, v], 1)
+            q = torch.cat([q, q.flip(0)], 1)[:, :self.nq]
+            k, v = x[:, :H], x[:, H:]
+        elif layout == "heads":
+            q, k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v))
+        self.q, self.k, self.v = q, k, v
+        self.q_first_d, self.k_first_d, self.k_lens_d = (
+            torch.tensor(x, dtype=torch.int32, device="cuda") for x in (self.q_first, self.k_first, [a + b for a, b in seqs]))
+        self.error = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.shape = kv.PromptShape(len(seqs), self.n, self.t, self.nq, H, d)
+        self.wsb = kv.kvprompt_workspace_bytes(self.shape)
+
+    def launch(self, scale, window=0, sinks=0, base=(None, None), out=None, lse=None, ws=None, stream=None):
+        rc = kv.kvprompt_attend(self.shape, self.q, self.k, self.v, self.q_first_d, self.k_first_d, self.k_lens_d, scale, window,
+                                sinks, *base, out, lse, self.error, ws, self.wsb, stream)
+        assert rc == kv.KVP_OK, kv.kvp_strerror(rc)
+
+    def run(self, scale, window=0, sinks=0, base=(None, None)):
+        out, lse = Guarded(max(16, self.n * self.nq * self.d * 2), fill=0x7F), Guarded(max(16, self.n * self.nq * 4), fill=0x7F)
+        ws = Guarded(self.wsb, fill=0xFF)
+        self.launch(scale, window, sinks, base, out.t, lse.t, ws.t)
+        torch.cuda.synchronize()
+        assert out.canary_ok() and lse.canary_ok() and ws.canary_ok()
+        self.raw = out.t[:self.n * self.nq * self.d * 2].clone(), lse.t[:self.n * self.nq * 4].clone()
+        return (Lg.f64(out.bf16((self.n, self.nq, self.d))),
+                self.raw[1].view(torch.float32).view(self.n, self.nq).cpu().numpy().astype(np.float64))
+
+    def check(self, out, lse, scale, window=0, sinks=0, base=(None, None), weights=WEIGHTS):
+        q, k, v = Lg.f64(self.q), Lg.f64(self.k), Lg.f64(self.v)
+        for b, (new, past) in enumerate(self.seqs):
+            i, t = slice(self.q_first[b], self.q_first[b + 1]), slice(self.k_first[b], self.k_first[b] + new + past)
+            ref, ref_lse, mass, reach = Lg.prompt(q[i], k[t], v[t], past, window, sinks, scale)
+            if base[0] is not None:
+                ref, ref_lse, mass = Lg.join(ref, ref_lse, mass, base[0][i].cpu().numpy().astype(np.float64),
+                                             base[1][i].cpu().numpy().astype(np.float64))
+            Lg.check(out[i], lse[i], ref, ref_lse, mass, reach, weights)
+        # rows of no sequence stay as they were
+        used = self.q_first[-1] * self.nq
+        assert bool((self.raw[0][used * self.d * 2:] == 0x7F).all()) and bool((self.raw[1][used * 4:] == 0x7F).all())
+
+    def both(self, scale=None, **more):
+        scale = 1 / math.sqrt(self.d) if scale is None else scale
+        out, lse = self.run(scale, **more)
+        assert kv.kvprompt_status(self.error) == kv.KVP_OK
+        self.check(out, lse, scale, **more)
+        return out, lse
+
+    def base(self, seed=0):
+        rng = np.random.default_rng(seed)
+        bo = torch.from_numpy(0.1 * rng.standard_normal((self.n, self.nq, self.d))).float().cuda()
+        bl = torch.from_numpy(rng.uniform(2, 6, (self.n, self.nq))).float().cuda()
+        bl[::3, 0] = -math.inf
+        return bo, bl
+
+
+SEQS = [[(1, 0)], [(1, 300)], [(17, 0), (1, 0), (0, 5), (0, 0), (33, 100)], [(128, 0)], [(129, 0), (127, 1)], [(256, 0)],
+        [(257, 0), (3, 1000), (64, 64)], [(700, 0)], [(300, 513), (5, 0), (40, 2)]]
+
+
+@pytest.mark.parametrize("seqs", SEQS, ids=str)
+@pytest.mark.parametrize("H,G,d", [(1, 1, 128), (2, 4, 128), (2, 4, 64), (1, 3, 128), (3, 1, 64), (1, 8, 64), (1, 5, 128)])
+def test_causal(seqs, H, G, d):
+    Call(seqs, H, G, d, seed=len(seqs) + G).both()
+
+
+@pytest.mark.parametrize("H,G,d", [(1, 128, 64), (1, 100, 128), (2, 33, 64), (1, 64, 128), (1, 127, 128)])
+def test_many_heads_of_one(H, G, d):
+    Call([(5, 0), (3, 140)], H, G, d).both()
+    Call([(9, 300)], H, G, d).both(window=20, sinks=2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 0), (64, 4), (128, 128), (129, 3), (100, 300), (300, 17), (2000, 5),
+                                          (2 ** 31 - 1, 2 ** 31 - 1), (31, 2 ** 31 - 1)])
+@pytest.mark.parametrize("H,G,d", [(2, 4, 128), (3, 1, 64), (1, 3, 64)])
+def test_windows(window, sinks, H, G, d):
+    Call([(700, 0), (130, 333), (1, 600), (5, 0)], H, G, d, seed=window % 1000).both(window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_layouts(layout, d):
+    Call([(200, 31), (3, 0), (77, 5)], 2, 4, d, layout=layout, gap=3).both(window=90, sinks=4)
+    Call([(1, 0)], 1, 1, d, layout=layout).both()
+
+
+def test_rows_of_no_sequence_and_joins():
+    for d, window, sinks in ((128, 0, 0), (64, 50, 3)):
+        c = Call([(140, 20), (0, 9), (31, 0)], 2, 4, d, gap=5)
+        c.both(window=window, sinks=sinks, base=c.base())
+
+
+def test_more_new_tokens_than_keys():
+    """Places below 0: the first queries see nothing: zeros and -inf, or the base."""
+    c = Call([(50, -20), (300, -299), (3, -3), (260, -130)], 1, 2, 128)
+    c.both()
+    c.both(base=c.base())
+    c.both(window=10, sinks=1)
+
+
+def test_sharp_negative_and_zero_scales():
+    for scale in (3.0, -0.1, 0.0, 1e-30):
+        Call([(150, 60)], 2, 2, 128, spread=2.0).both(scale=scale)
+
+
+def test_scores_that_rise_and_fall():
+    """The running maximum raised in every tile, by hundreds; and falling ones."""
+    for order in (1, -1):
+        c = Call([(300, 700)], 1, 2, 64)
+        size = torch.linspace(0.05, 6.0, c.t, device="cuda")[::1]
+        c.q[:] = c.q.abs()
+        c.k.copy_((c.k.abs().float() * (size if order == 1 else size.flip(0))[:, None, None]).to(torch.bfloat16))
+        c.both(scale=0.5)
+
+
+def test_shared_rows():
+    """Two sequences over the same keys (a shared prefix), one over a part of them."""
+    c = Call([(40, 100), (40, 100), (10, 20)], 2, 2, 128)
+    c.k_first = [0, 0, 37]
+    c.k_first_d.copy_(torch.tensor(c.k_first, dtype=torch.int32))
+    c.both()
+    c.both(window=33, sinks=5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_unseen_nonfinite(d):
+    """Inf and NaN in keys and values that a query does not see have no part: behind the
+    last key, between sequences, in the window's gap, and later tokens of the prompt's own
+    tiles; what is seen makes its dim Inf or NaN, for the queries that see it alone."""
+    for window, sinks in ((0, 0), (70, 3)):
+        c = Call([(300, 40), (129, 0)], 2, 4, d, gap=7)
+        c.both(window=window, sinks=sinks)
+        clean = c.run(0.1, window, sinks)
+        inside = torch.zeros(c.t, dtype=torch.bool, device="cuda")
+        for b, (new, past) in enumerate(c.seqs):
+            inside[c.k_first[b]:c.k_first[b] + new + past] = True
+        for x in (c.k, c.v):
+            x[~inside] = math.nan
+        got = c.run(0.1, window, sinks)
+        assert np.array_equal(got[0], clean[0], equal_nan=True) and np.array_equal(got[1], clean[1], equal_nan=True)
+        at, dim = 150, 5                       # token 150 of the first sequence: query 110
+        c.v[c.k_first[0] + at, 1, dim] = math.inf
+        c.v[c.k_first[0] + at, 0, dim + 1] = math.nan
+        out, lse = c.run(0.1, window, sinks)
+        q = np.arange(300)
+        sees = (40 + q >= at) & ((40 + q - at < window) if window else True)
+        assert np.array_equal(~np.isfinite(out[:300, 4:, dim]), np.repeat(sees[:, None], 4, 1))
+        assert np.array_equal(~np.isfinite(out[:300, :4, dim + 1]), np.repeat(sees[:, None], 4, 1))
+        rest = np.delete(out[:300], [dim, dim + 1], -1)
+        tol = 2.0 ** -6 * np.abs(clean[0][:300]).max()
+        assert np.all(np.abs(rest - np.delete(clean[0][:300], [dim, dim + 1], -1)) <= tol)
+        assert np.all(np.abs(out[:300][~sees] - clean[0][:300][~sees]) <= tol)
+        assert np.all(np.abs(lse[:300] - clean[1][:300]) <= 1e-4) and np.array_equal(out[300:429], clean[0][300:429])
+        # a key that is NaN takes the rows that see it, and no others
+        c.v.nan_to_num_(0.0, 0.0, 0.0)
+        c.k[c.k_first[0] + at] = math.nan
+        out, lse = c.run(0.1, window, sinks)
+        assert np.array_equal(np.isnan(out[:300]).all((1, 2)), sees) and np.array_equal(np.isnan(out[:300]).any((1, 2)), sees)
+        assert np.array_equal(np.isnan(lse[:300]).any(1), sees)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_up_to_the_largest(d):
+    """Finite values give finite results up to bf16's largest, whatever the sums before
+    the division would be."""
+    c = Call([(200, 900)], 1, 2, d)
+    c.v.fill_(3.3895313892515355e38)
+    c.v[::2, :, ::2] *= -1
+    out, lse = c.run(0.01)
+    assert np.all(np.isfinite(out)) and np.all(np.isfinite(lse))
+    assert np.all(np.abs(out[:, :, 1::2]) >= 3.3e38)
+
+
+def test_ranges_outside_the_tensors():
+    """A sequence whose numbers point outside is skipped and reported; the others are
+    as they were."""
+    good = Call([(40, 10), (20, 0), (30, 5)], 2, 2, 64)
+    out, lse = good.run(0.1)
+    for what, at, value in (("k_lens_d", 1, 1000), ("k_lens_d", 1, -1), ("k_first_d", 1, -1), ("k_first_d", 1, good.t - 5),
+                            ("k_first_d", 1, 2 ** 31 - 1), ("k_lens_d", 1, 2 ** 31 - 1)):
+        c = Call([(40, 10), (20, 0), (30, 5)], 2, 2, 64)
+        getattr(c, what)[at] = value
+        o, l = c.run(0.1)
+        assert kv.kvprompt_status(c.error) == kv.KVP_ERR_PAGE
+        for i in (slice(0, 40), slice(60, 90)):
+            assert np.array_equal(o[i], out[i]) and np.array_equal(l[i], lse[i])
+        assert bool((c.raw[1].view(torch.int32).view(-1, 4)[40:60] == 0x7F7F7F7F).all())
+    c = Call([(40, 10), (20, 0), (30, 5)], 2, 2, 64)
+    c.q_first_d[3] = 91                                                 # past q's rows
+    c.run(0.1)
+    assert kv.kvprompt_status(c.error) == kv.KVP_ERR_PAGE
+    c = Call([(40, 10)], 2, 2, 64)
+    c.q_first_d[0] = 50                                                 # decreasing
+    c.run(0.1)
+    assert kv.kvprompt_status(c.error) in (kv.KVP_OK, kv.KVP_ERR_PAGE)
+
+
+def test_many_sequences():
+    """More sequences than tiles, empty ones among them."""
+    rng = np.random.default_rng(0)
+    seqs = [(int(a), int(b)) for a, b in zip(rng.integers(0, 7, 700), rng.integers(0, 40, 700))]
+    Call(seqs, 2, 2, 64).both(window=9, sinks=2)
+
+
+def test_few_rows_over_many_keys():
+    for H, G, d, seqs in ((2, 4, 128, [(5, 20000)]), (1, 1, 64, [(1, 33333), (2, 70)]), (8, 4, 128, [(64, 5000)])):
+        c = Call(seqs, H, G, d)
+        c.both()
+        c.both(base=c.base(), window=9000, sinks=200)
+
+
+def test_same_results_every_time_and_on_two_streams():
+    """Two calls at once, each with a workspace of its own; results do not depend on
+    timing."""
+    c = Call([(300, 3000), (40, 0)], 2, 4, 128)
+    want = c.run(0.1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    torch.cuda.synchronize()
+    for i in range(6):
+        out, lse = torch.empty(c.n, c.nq, c.d, dtype=torch.bfloat16, device="cuda"), torch.empty(c.n, c.nq, device="cuda")
+        got.append((out, lse, torch.empty(c.wsb, dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    for i, (out, lse, ws) in enumerate(got):
+        c.launch(0.1, 0, 0, (None, None), out, lse, ws, streams[i % 2])
+    torch.cuda.synchronize()
+    for out, lse, _ in got:
+        assert np.array_equal(Lg.f64(out), want[0]) and np.array_equal(lse.cpu().numpy().astype(np.float64), want[1])
+
+
+def test_in_graphs_as_lengths_change():
+    """Captured once and replayed with other lengths; two graphs that run one after the
+    other may share a workspace."""
+    c = Call([(200, 100), (60, 0)], 2, 2, 128)
+    graphs = []
+    ws = torch.empty(c.wsb, dtype=torch.uint8, device="cuda")
+    for window, sinks in ((0, 0), (50, 3)):
+        out, lse = Guarded(c.n * c.nq * c.d * 2, fill=0x7F), Guarded(c.n * c.nq * 4, fill=0x7F)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            c.launch(0.1, window, sinks, (None, None), out.t, lse.t, ws, torch.cuda.current_stream())
+        graphs.append((g, window, sinks, out, lse))
+    for seqs in ([(200, 100), (60, 0)], [(1, 3), (2, 0)], [(0, 0), (260, 40)], [(130, 7), (129, 1)]):
+        c.seqs = seqs
+        c.q_first = [0, seqs[0][0], seqs[0][0] + seqs[1][0]]
+        c.k_first = [0, sum(seqs[0])]
+        for x, y in ((c.q_first_d, c.q_first), (c.k_first_d, c.k_first), (c.k_lens_d, [sum(s) for s in seqs])):
+            x.copy_(torch.tensor(y, dtype=torch.int32))
+        for g, window, sinks, out, lse in graphs:
+            out.t.fill_(0x7F)
+            lse.t.fill_(0x7F)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            c.raw = out.t[:c.n * c.nq * c.d * 2].clone(), lse.t[:c.n * c.nq * 4].clone()
+            c.check(Lg.f64(out.bf16((c.n, c.nq, c.d))),
+                    c.raw[1].view(torch.float32).view(c.n, c.nq).cpu().numpy().astype(np.float64), 0.1, window, sinks)
+
+
+def test_lse_in_place_and_without():
+    c = Call([(100, 30)], 2, 2, 128)
+    bo, bl = c.base()
+    want = c.both(base=(bo, bl))
+    out = torch.empty(c.n, c.nq, c.d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(c.wsb, dtype=torch.uint8, device="cuda")
+    scale = 1 / math.sqrt(128)
+    c.launch(scale, 0, 0, (bo, bl), out, None, ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(Lg.f64(out), want[0])
+    c.launch(scale, 0, 0, (bo, bl), out, bl, ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(Lg.f64(out), want[0]) and np.array_equal(bl.cpu().numpy().astype(np.float64), want[1])
+
+
+def test_rows_past_two_gigabytes():
+    """Keys and values whose offsets pass 32 bits: a sequence at the end of 2^25 rows."""
+    H, d, rows = 1, 128, (1 << 25) + 500
+    c = Call([(70, 300)], H, 2, d)
+    k = torch.zeros(rows, H, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    at = rows - c.t
+    k[at:], v[at:] = c.k, c.v
+    want = c.run(0.1)
+    c.k, c.v = k, v
+    c.k_first_d.fill_(at)
+    c.shape = kv.PromptShape(1, c.n, rows, c.nq, H, d)
+    c.wsb = kv.kvprompt_workspace_bytes(c.shape)
+    got = c.run(0.1)
+    assert np.allclose(got[0], want[0], rtol=2.0 ** -7, atol=2.0 ** -10) and np.allclose(got[1], want[1], atol=1e-5)
