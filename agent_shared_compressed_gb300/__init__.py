@@ -19,6 +19,6 @@ from .binding import (  # noqa: F401
     KVP_ERR_PAGE, KVP_PAGES_BF16, KVP_PAGES_K8V8, KVP_PAGES_K8V4, KVP_PAGES_K4V4, KVP_MAX_AXES, KVP_PAGES_MAX_SEQS, kvp_test_limit_next_pages_attend,
     kvp_test_limit_next_pages_attend_lanes, PagesConfig, Rows, rows, kvpages_append, kvpages_append_axes,
     kvpages_attend, kvpages_attend_window, kvpages_attend_workspace_bytes, kvpages_bytes, kvpages_init, kvpages_read, kvpages_status,
-    kvprompt_attend, kvprompt_status, kvprompt_workspace_bytes, PromptShape, KVP_PROMPT_MAX_SEQS,
+    kvprompt_attend, kvp_test_limit_next_prompt, kvprompt_status, kvprompt_workspace_bytes, PromptShape, KVP_PROMPT_MAX_SEQS,
     kvpool_pool_bytes, kvpool_pool_bytes_ex, kvpool_status, KVP_K_PER_TENSOR, KVP_K_Q8_0, kvpool_workspace_bytes, load,
 )

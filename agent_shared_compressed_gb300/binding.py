@@ -151,6 +151,7 @@ _SIGS = {
     "kvp_test_limit_next_unpack": (C.c_int, [C.c_uint32]),
     "kvp_test_limit_next_pages_attend": (C.c_int, [C.c_uint32]),
     "kvp_test_limit_next_pages_attend_lanes": (C.c_int, [C.c_uint32, C.c_uint32]),
+    "kvp_test_limit_next_prompt": (C.c_int, [C.c_uint32]),
 }
 
 _lib = None
@@ -593,6 +594,10 @@ def kvp_test_limit_next_pages_attend(polls):
 
 def kvp_test_limit_next_pages_attend_lanes(polls, lanes):
     return load().kvp_test_limit_next_pages_attend_lanes(int(polls), int(lanes))
+
+
+def kvp_test_limit_next_prompt(polls):
+    return load().kvp_test_limit_next_prompt(int(polls))
 
 
 class KVPError(RuntimeError):

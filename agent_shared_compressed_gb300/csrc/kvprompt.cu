@@ -6,18 +6,51 @@
 // p = T_b - n_b + i and sees t <= p, with a window w only t > p - w or t < z:
 //   s_t = scale q . k_t,  out = sum_t softmax(s)_t v_t,  lse = log sum_t exp(s_t)
 // joined: L = log(e^lse + e^base_lse), out = e^(lse-L) out + e^(base_lse-L) base.
+// Exponentials are base 2 throughout.
+//
+// Bound: the tensor cores, 4 d multiply-adds for a query row and a key that it sees.
+//
+// A block takes 256 query rows of one KV head as two halves of 128: the heads of a
+// group side by side (row = token * G + head), so that grouped heads share every
+// key and value that is brought in, and goes through the keys that any of its rows
+// sees, 128 at a time: first the first tokens, then the window's.  Products on
+// tcgen05, 128 x 128 (x d) tiles, everything but keys and values staying on the SM:
+//   S = Q K^T   operands in shared memory, S in TMEM (128 columns a half)
+//   O += P V    P as bf16 in TMEM over the first half of S's columns, O in TMEM
+// Warps 0-3 and 4-7 do the softmax of a half each, a thread a row (no shuffles);
+// warp 8 issues the products, warp 9 the copies (TMA, 128-byte swizzle, a ring of
+// key and value tiles).  While one half's softmax runs the tensor core has the
+// other's products.
+//
+// A row's reference (its largest score so far) is raised only when a score passes it
+// by 2^8, so that O is hardly ever rescaled; weights are taken relative to 2^40 times
+// the reference, so that sums of up to 2^31 values up to bf16's largest stay finite.
+// Weights are rounded to bf16 for the value product (2^-9 at most, of either sign; the
+// sum takes them before that): a second product for the rest of them would cost
+// a quarter of the tensor time for less than the result's own rounding to bf16.
+//
+// Values that some of the rows do not see must not meet them in the product, not even
+// with weight 0, if they are Inf or NaN.  Rows of a tile that nobody sees are zeroed in
+// shared memory.  Tiles that some rows see in part are looked over; if one holds Inf or
+// NaN among the tokens seen, the block's rows are computed again one by one in fp32.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
+#include <cuda.h>
+
+#include "kvp_async.cuh"
 #include "kvp_internal.cuh"
 
 namespace kvp {
 
-// Weights are relative to 2^PT_BIAS times the largest, so that sums of values up to bf16's
-// largest stay finite.
-constexpr float PT_BIAS = 40.0f;
+constexpr int PT_KEYS = 128;                  // keys of a tile
+constexpr int PT_THREADS = 320;
+constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
+constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f;
 
 struct PromptArgs {
+    CUtensorMap q_map, k_map, v_map;
     const uint16_t *q, *k, *v;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
     const int32_t *q_first, *k_first, *k_lens;
@@ -25,8 +58,14 @@ struct PromptArgs {
     uint16_t *out;
     float *lse;
     uint32_t *error;
-    float scale2;  // scale * log2(e)
+    float *part;    // [splits][n nq][d] sums of weighted values
+    float2 *stats;  // [splits][n nq] (reference, sum)
+    float scale2;   // |scale| * log2(e); 1 for a scale of 0, whose scores are set to 0
     int nseq, n, nk, nq, H, G, window, sinks;
+    int half_tokens;  // tokens of a half: 128 / G
+    int tiles, splits;
+    uint32_t negative, flat;  // the scale's sign; whether it is 0
+    uint32_t polls;           // of a copy, by the warp that issues products
 };
 
 __device__ __forceinline__ void prompt_flag(const PromptArgs &a, uint32_t f) {
@@ -42,7 +81,7 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, bool
     s.first = int(ld_plain_u32(a.q_first + b));
     const int end = int(ld_plain_u32(a.q_first + b + 1));
     s.k_first = int(ld_plain_u32(a.k_first + b)), s.T = int(ld_plain_u32(a.k_lens + b));
-    s.n = end - s.first;
+    s.n = int(uint32_t(end) - uint32_t(s.first));
     if (s.first < 0 || end < s.first || end > a.n || s.k_first < 0 || s.T < 0 || int64_t(s.k_first) + s.T > a.nk) {
         if (flag) prompt_flag(a, FLAG_PAGE);
         s.n = 0;
@@ -50,12 +89,24 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, bool
     return s;
 }
 
+// The log of a row's sum of exponentials, from its sum in units of 2^(ref + PT_BIAS).
+__device__ __forceinline__ float row_lse(float ref, float sum) {
+    return sum > 0.0f ? (ref + log2f(sum * 0x1p40f)) * 0.69314718055994531f : (sum == 0.0f ? -INFINITY : sum);
+}
+
+// A finite mean of bf16 values is not beyond bf16's largest (the rounded weights' sum
+// may be, by 2^-9).
+__device__ __forceinline__ float within_bf16(float y) {
+    constexpr float MOST = 3.3895313892515355e38f;
+    return fabsf(y) < INFINITY ? fminf(fmaxf(y, -MOST), MOST) : y;
+}
+
 // What a row ends with: the weights of its own result (already divided by its sum)
-// and of the base, and its lse.
-__device__ __forceinline__ float2 prompt_join(const PromptArgs &a, uint64_t row, float lse, bool writes) {
+// and of the base, and its lse (written by one of those who call this).  bl: base_lse[row],
+// which may be lse[row] and has been read by all of them.
+__device__ __forceinline__ float2 prompt_join(const PromptArgs &a, uint64_t row, float lse, float bl, bool writes) {
     float wa = 1.0f, wb = 0.0f;
     if (a.base_lse) {
-        const float bl = a.base_lse[row];
         if (!(lse == -INFINITY && bl == -INFINITY)) {
             const float top = fmaxf(lse, bl);
             const float ea = expf(lse - top), eb = expf(bl - top), tot = ea + eb;
@@ -67,8 +118,26 @@ __device__ __forceinline__ float2 prompt_join(const PromptArgs &a, uint64_t row,
     return make_float2(wa, wb);
 }
 
+// A row's end by a warp: lane l has dims l d/32 ...; acc and sum are in units of
+// 2^(ref + PT_BIAS).
+template <int D>
+__device__ __forceinline__ void prompt_write(const PromptArgs &a, uint64_t row, float ref, float sum, const float (&acc)[D / 32], int lane) {
+    constexpr int VPL = D / 32;
+    const float bl = a.base_lse ? a.base_lse[row] : -INFINITY;
+    __syncwarp();  // every lane has it before one writes lse
+    const float2 f = prompt_join(a, row, row_lse(ref, sum), bl, lane == 0);
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        float y = within_bf16(acc[i] * inv) * f.x;
+        if (a.base_out && f.y != 0.0f) y = fmaf(f.y, a.base_out[row * D + lane * VPL + i], y);
+        reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + lane * VPL + i] = __float2bfloat16_rn(y);
+    }
+}
+
 // One row by one warp, a key at a time in fp32: lane l holds dims l d/32 ...  The keys are
-// those of [k0, k1) that the row at place p sees.  acc is relative to 2^ref.
+// those of [k0, k1) that the row at place p sees.  acc and sum are relative to
+// 2^(ref + PT_BIAS).
 template <int D>
 __device__ __forceinline__ void row_keys(const PromptArgs &a, const float (&q)[D / 32], const uint16_t *k, const uint16_t *v,
                                          int p, int64_t k0, int64_t k1, float (&acc)[D / 32], float &ref, float &sum) {
@@ -85,7 +154,7 @@ __device__ __forceinline__ void row_keys(const PromptArgs &a, const float (&q)[D
         for (int i = 0; i < VPL; ++i) s = fmaf(q[i], __uint_as_float(uint32_t(k[t * a.k_ts + lane * VPL + i]) << 16), s);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale2;
+        s = a.flat ? 0.0f : (a.negative ? -s : s) * a.scale2;
         const float top = fmaxf(ref, s), f = ref == -INFINITY ? 0.0f : exp2f(ref - top);
         const float w = exp2f(s - (top == -INFINITY ? 0.0f : top) - PT_BIAS);
         ref = top, sum = fmaf(sum, f, w);
@@ -95,35 +164,511 @@ __device__ __forceinline__ void row_keys(const PromptArgs &a, const float (&q)[D
     }
 }
 
+// ---------------------------------------------------------------------------
+// tcgen05 and TMA.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mbar_init_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_g2s(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+#define KVP_R8(x, i) "=r"((x)[(i)]), "=r"((x)[(i) + 1]), "=r"((x)[(i) + 2]), "=r"((x)[(i) + 3]), "=r"((x)[(i) + 4]), \
+                     "=r"((x)[(i) + 5]), "=r"((x)[(i) + 6]), "=r"((x)[(i) + 7])
+#define KVP_I8(x, i) "r"((x)[(i)]), "r"((x)[(i) + 1]), "r"((x)[(i) + 2]), "r"((x)[(i) + 3]), "r"((x)[(i) + 4]), \
+                     "r"((x)[(i) + 5]), "r"((x)[(i) + 6]), "r"((x)[(i) + 7])
+// 32 columns of the thread's TMEM lane.
+__device__ __forceinline__ void tc_ld32(uint32_t at, uint32_t *x) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : KVP_R8(x, 0), KVP_R8(x, 8), KVP_R8(x, 16), KVP_R8(x, 24) : "r"(at));
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t *x) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        ::KVP_I8(x, 0), KVP_I8(x, 8), KVP_I8(x, 16), KVP_I8(x, 24), "r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// (the registers of a load are its results only once it has been waited for)
+__device__ __forceinline__ void tc_landed(uint32_t *x) {
+    asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                      "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
+                 :: "memory");
+}
+__device__ __forceinline__ float pt_exp2(float x) {  // results under 2^-126 are 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A shared-memory operand in rows of 128 bytes under the 128-byte swizzle: groups of 8
+// rows are 1024 bytes apart (lbo: from one 64-element column of rows to the next, for
+// the operand whose rows run along the sum).
+__device__ __forceinline__ uint64_t tc_operand(uint32_t at, uint32_t lbo) {
+    return uint64_t((at & 0x3FFFFu) >> 4) | uint64_t(lbo >> 4) << 16 | uint64_t(1024u >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(2) << 61;
+}
+// bf16 x bf16 -> fp32, 128 x n.
+__device__ __forceinline__ constexpr uint32_t tc_kind(uint32_t n) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+constexpr uint32_t TC_NEGATE_A = 1u << 13, TC_B_BY_ROWS = 1u << 16;
+
 template <int D>
-__global__ void __launch_bounds__(128) prompt_rows(const __grid_constant__ PromptArgs a) {
+struct PromptTile {
+    static constexpr uint32_t BYTES = 128u * D * 2u;   // of 128 rows of queries, keys or values
+    static constexpr uint32_t CHUNK = 128u * 128u;     // 64 dims of them
+    static constexpr uint32_t SLOTS = D == 128 ? 5 : 8;
+    static constexpr uint32_t OFF_Q = 1024, OFF_RING = OFF_Q + 2 * BYTES;
+    static constexpr uint32_t SMEM = OFF_RING + SLOTS * BYTES + 1024;  // and the base's alignment
+    static_assert(SMEM <= 232448, "shared memory of a block");
+    // barriers, 8 bytes each
+    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 168, DONE = 184, TMEM = 192, DEAD = 196,
+                              ODD = 200;
+};
+
+// The keys that some row of a block sees: [0, a_end) and [b0, b_end), in tiles; tiles
+// j0 .. j1 - 1 are this block's.
+struct PromptKeys {
+    int a_end, b0, b_end, na, j0, j1;
+    __device__ __forceinline__ void tile(int j, int &t0, int &end) const {
+        if (j < na)
+            t0 = j * PT_KEYS, end = min(t0 + PT_KEYS, a_end);
+        else
+            t0 = b0 + (j - na) * PT_KEYS, end = int(min(int64_t(t0) + PT_KEYS, int64_t(b_end)));
+    }
+};
+
+// Waits until the barrier's phase is over; gives up when the limit or another warp's
+// wait has run out.
+__device__ __forceinline__ bool pt_wait(const PromptArgs &a, uint32_t bar, uint32_t parity, uint32_t dead, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if (i >= 64) {
+            uint32_t d;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
+            if (d) return false;
+            __nanosleep(64);
+        }
+    }
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(1u) : "memory");
+    prompt_flag(a, FLAG_TIMEOUT);
+    return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_constant__ PromptArgs a) {
+    using T = PromptTile<D>;
+    extern __shared__ uint8_t sm_raw[];
+    const uint32_t sm = (smem_addr(sm_raw) + 1023u) & ~1023u;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // the block's sequence and tile: sequence b has its tiles from q_first[b] / tokens + b on
+    const int tokens = 2 * a.half_tokens;
+    const int split = int(blockIdx.x % uint32_t(a.splits));
+    const int h = int(blockIdx.x / uint32_t(a.splits) % uint32_t(a.H));
+    const int slot = a.tiles - 1 - int(blockIdx.x / uint32_t(a.splits) / uint32_t(a.H));  // the longest first
+    int b = 0;
+    {
+        int lo = 0, hi = a.nseq - 1;  // the last b with its first tile at or before this one
+        while (lo < hi) {
+            // 32 places at a time
+            const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
+            const bool before = max(int(ld_plain_u32(a.q_first + at)), 0) / tokens + at <= slot;
+            const int n = __popc(__ballot_sync(0xffffffffu, before));  // (a run of ones)
+            const int nlo = n ? min(lo + n * step, hi) : lo, nhi = n < 32 ? min(lo + (n + 1) * step, hi) - 1 : hi;
+            lo = nlo, hi = max(nlo, nhi);
+        }
+        b = lo;
+    }
+    const PromptSeq s = prompt_seq(a, b, tid == 0);
+    const int64_t i0_ = int64_t(slot - b - max(s.first, 0) / tokens) * tokens;
+    if (i0_ < 0 || i0_ >= s.n) return;
+    const int i0 = int(i0_), count = min(tokens, s.n - i0), halves = count > a.half_tokens ? 2 : 1;
+    const int p_first = s.T - s.n + i0, p_last = p_first + count - 1;  // places (below 0: no keys)
+    PromptKeys keys;
+    {
+        auto tiles_of = [](int64_t n) { return int((n + PT_KEYS - 1) / PT_KEYS); };
+        const int64_t old = a.window ? int64_t(p_first) - a.window + 1 : 0;
+        keys.b_end = max(p_last + 1, 0), keys.b0 = int(max(old, int64_t(0)));
+        keys.a_end = min(a.sinks, keys.b0);
+        // no more tiles without the gap: without it
+        if (tiles_of(keys.b_end) <= tiles_of(keys.a_end) + tiles_of(keys.b_end - keys.b0)) keys.a_end = 0, keys.b0 = 0;
+        keys.na = tiles_of(keys.a_end);
+        const int all = keys.na + tiles_of(keys.b_end - keys.b0);
+        keys.j0 = int(int64_t(all) * split / a.splits), keys.j1 = int(int64_t(all) * (split + 1) / a.splits);
+    }
+    const int nt = keys.j1 - keys.j0;
+
+    const uint32_t dead = sm + T::DEAD;
+    if (warp == 8) {
+        if (lane == 0) {
+            for (uint32_t i = 0; i < T::SLOTS; ++i) mbar_init_n(sm + T::FULL + 8 * i, 1), mbar_init_n(sm + T::FREE + 8 * i, 1);
+            mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
+            for (uint32_t i = 0; i < 2; ++i)
+                mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::P + 8 * i, 128), mbar_init_n(sm + T::O + 8 * i, 1);
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(sm + T::ODD), "r"(0u) : "memory");
+            mbar_init_fence();
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm + T::TMEM), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_before();
+    }
+    __syncthreads();
+    tc_after();
+    uint32_t tmem;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(sm + T::TMEM) : "memory");
+
+    if (warp == 9) {
+        // --- copies: Q, then K_0 V_0 K_1 V_1 ... round the ring
+        if (lane == 0 && nt > 0) {
+            const int head0 = h * a.G;
+            mbar_expect_tx(sm + T::Q, uint32_t(halves) * uint32_t(a.half_tokens) * uint32_t(a.G) * D * 2u);
+            for (int half = 0; half < halves; ++half)
+                for (int c = 0; c < D / 64; ++c)
+                    tma_g2s(sm + T::OFF_Q + uint32_t(half) * T::BYTES + uint32_t(c) * T::CHUNK, &a.q_map, 64 * c, head0,
+                            s.first + i0 + half * a.half_tokens, sm + T::Q);
+            uint32_t n = 0;
+            bool ok = true;
+            for (; ok && n < 2u * uint32_t(nt); ++n) {
+                const uint32_t at = n % T::SLOTS, round = n / T::SLOTS;
+                if (round > 0 && !pt_wait(a, sm + T::FREE + 8 * at, (round - 1) & 1, dead, PT_WAIT_LIMIT)) {
+                    ok = false;
+                    break;
+                }
+                int t0, end;
+                keys.tile(keys.j0 + int(n / 2), t0, end);
+                mbar_expect_tx(sm + T::FULL + 8 * at, T::BYTES);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_g2s(sm + T::OFF_RING + at * T::BYTES + uint32_t(c) * T::CHUNK, n & 1 ? &a.v_map : &a.k_map, 64 * c, h,
+                            s.k_first + t0, sm + T::FULL + 8 * at);
+            }
+            // whoever gave up: the copies in flight land before the block ends
+            if (!ok || n >= 2u * uint32_t(nt)) {
+                for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
+                    mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
+                mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
+            }
+        }
+    } else if (warp == 8) {
+        // --- products
+        if (lane == 0 && nt > 0) {
+            const uint32_t kind_s = tc_kind(128) | (a.negative ? TC_NEGATE_A : 0u), kind_o = tc_kind(D) | TC_B_BY_ROWS;
+            auto scores = [&](int half, uint32_t at) {  // S = Q K^T
+                const uint64_t qd = tc_operand(sm + T::OFF_Q + uint32_t(half) * T::BYTES, 16);
+                const uint64_t kd = tc_operand(sm + T::OFF_RING + at * T::BYTES, 16);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = uint64_t((uint32_t(k / 4) * T::CHUNK + uint32_t(k % 4) * 32u) >> 4);
+                    tc_mma_ss(tmem + uint32_t(half) * 128u, qd + off, kd + off, kind_s, k > 0);
+                }
+                tc_commit(sm + T::S + 8 * uint32_t(half));
+            };
+            bool ok = pt_wait(a, sm + T::Q, 0, dead, PT_WAIT_LIMIT) && pt_wait(a, sm + T::FULL, 0, dead, a.polls);
+            if (ok) {
+                tc_after();
+                for (int half = 0; half < halves; ++half) scores(half, 0);
+                tc_commit(sm + T::FREE);
+            }
+            for (int j = 0; ok && j < nt; ++j) {
+                const uint32_t nv = 2u * uint32_t(j) + 1u, nk = nv + 1u, v_at = nv % T::SLOTS, k_at = nk % T::SLOTS;
+                if (!(ok = pt_wait(a, sm + T::FULL + 8 * v_at, (nv / T::SLOTS) & 1, dead, a.polls))) break;
+                const bool more = j + 1 < nt;
+                for (int half = 0; ok && half < halves; ++half) {
+                    if (!(ok = pt_wait(a, sm + T::P + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) break;
+                    tc_after();
+                    const uint64_t vd = tc_operand(sm + T::OFF_RING + v_at * T::BYTES, T::CHUNK);
+#pragma unroll
+                    for (int k = 0; k < PT_KEYS / 16; ++k)  // O += P V
+                        tc_mma_ts(tmem + 256u + uint32_t(half) * D, tmem + uint32_t(half) * 128u + 8u * uint32_t(k),
+                                  vd + uint64_t(k * 2048 >> 4), kind_o, j > 0 || k > 0);
+                    if (half == halves - 1) tc_commit(sm + T::FREE + 8 * v_at);
+                    if (!more) {
+                        tc_commit(sm + T::O + 8 * uint32_t(half));
+                        continue;
+                    }
+                    if (half == 0 && !(ok = pt_wait(a, sm + T::FULL + 8 * k_at, (nk / T::SLOTS) & 1, dead, a.polls))) break;
+                    tc_after();
+                    scores(half, k_at);
+                    if (half == halves - 1) tc_commit(sm + T::FREE + 8 * k_at);
+                }
+            }
+            if (!ok) {  // nothing may be in flight when TMEM is given back
+                tc_commit(sm + T::DONE);
+                mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4 * halves) {
+        // --- softmax: a thread a row
+        const int half = warp >> 2, r = tid & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's 32 lanes of TMEM
+        const uint32_t s_at = tmem + uint32_t(half) * 128u + lanes, o_at = tmem + 256u + uint32_t(half) * D + lanes;
+        const int tl = r / a.G, i = i0 + half * a.half_tokens + tl;
+        const bool real = tl < a.half_tokens && i < s.n;
+        const int p = real ? s.T - s.n + i : p_last;
+        float ref = -INFINITY, sum = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            int t0, end;
+            keys.tile(keys.j0 + j, t0, end);
+            if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) {
+                ok = false;
+                break;
+            }
+            tc_after();
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
+            // values that not all rows see (the same for all threads)
+            const bool rest = end < t0 + PT_KEYS;
+            const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
+            if (rest || part) {
+                const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
+                const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
+                if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead, PT_WAIT_LIMIT))) {
+                    ok = false;
+                    break;
+                }
+                if (part) {
+                    // Inf and NaN times 0 are NaN.  Each half looks at its share of the rows, a
+                    // thread at one 16-byte column of every fourth or eighth (whatever the swizzle)
+                    constexpr int PER = D / 8;  // chunks of a row
+                    __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
+                    for (int row = half * (128 / PER) + r / PER; row < end - t0; row += halves * (128 / PER)) {
+                        const uint32_t c = uint32_t(r % PER);
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(tile + c / 8u * T::CHUNK + uint32_t(row) * 128u + c % 8u * 16u) : "memory");
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
+                    }
+                    if (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu)
+                        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(sm + T::ODD), "r"(1u) : "memory");
+                }
+                if (rest) {
+                    for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
+                        const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
+                                     ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
+                    }
+                    fence_proxy_async();
+                }
+            }
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
+            float *xf = reinterpret_cast<float *>(x);
+            if (a.flat) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) xf[c] = 0.0f;
+            }
+            {   // columns that the row sees: up to `last`, from `from` on or below `first`
+                const int last = min(end - 1, p) - t0;
+                const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
+                const bool all = last >= 127 && (from <= 0 || first >= 128);
+                if (!__all_sync(0xffffffffu, all)) {
+                    const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > last || (c < f0 && c >= f1)) xf[c] = -INFINITY;
+                }
+            }
+            float m[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m[c] = xf[c];
+#pragma unroll
+            for (int c = 4; c < 128; ++c) m[c & 3] = fmaxf(m[c & 3], xf[c]);
+            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale2;
+            const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise ? pt_exp2(ref - top) : 1.0f;
+                if (raise) ref = top;
+                sum *= f;
+                if (j > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32(o_at + uint32_t(c), o);
+                        tc_wait_ld();
+                        tc_landed(o), tc_landed(o + 16);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc_st32(o_at + uint32_t(c), o);
+                    }
+                }
+            }
+            const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+            float2 part_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                const float2 e = __ffma2_rn(make_float2(xf[2 * c], xf[2 * c + 1]), make_float2(a.scale2, a.scale2), make_float2(off, off));
+                const float2 w = make_float2(pt_exp2(e.x), pt_exp2(e.y));
+                part_sum[c & 1] = __fadd2_rn(part_sum[c & 1], w);
+                x[c] = pack_bf16x2(w.x, w.y);
+            }
+            sum += (part_sum[0].x + part_sum[0].y) + (part_sum[1].x + part_sum[1].y);
+            tc_st32(s_at, x);
+            tc_st32(s_at + 32u, x + 32);
+            tc_wait_st();
+            tc_before();
+            mbar_arrive(sm + T::P + 8 * uint32_t(half));
+        }
+        if (ok && nt > 0) {
+            ok = __all_sync(0xffffffffu, pt_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead, PT_WAIT_LIMIT));
+            tc_after();
+        }
+        // every softmax warp is here: whether any has met Inf or NaN
+        asm volatile("bar.sync 1, %0;" ::"r"(128 * halves) : "memory");
+        uint32_t odd;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sm + T::ODD) : "memory");
+        if (ok && !odd) {
+            const uint64_t row = uint64_t(s.first + i) * uint32_t(a.nq) + uint32_t(h * a.G + r - tl * a.G);
+            float2 f = make_float2(1.0f, 0.0f);
+            float inv = 1.0f;
+            if (real && a.splits == 1) {
+                f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
+                inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+            } else if (real) {
+                a.stats[uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+                if (nt > 0) {
+                    tc_ld32(o_at + uint32_t(c), o);
+                    tc_wait_ld();
+                    tc_landed(o), tc_landed(o + 16);
+                }
+                if (!real) continue;
+                if (a.splits > 1) {
+                    float *to = a.part + (uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row) * D + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) y[u] = within_bf16(__uint_as_float(o[e + u]) * inv) * f.x;
+                    if (a.base_out && f.y != 0.0f) {
+                        const float4 *bo = reinterpret_cast<const float4 *>(a.base_out + row * D + c + e);
+                        const float4 b0 = bo[0], b1 = bo[1];
+                        y[0] = fmaf(f.y, b0.x, y[0]), y[1] = fmaf(f.y, b0.y, y[1]), y[2] = fmaf(f.y, b0.z, y[2]);
+                        y[3] = fmaf(f.y, b0.w, y[3]), y[4] = fmaf(f.y, b1.x, y[4]), y[5] = fmaf(f.y, b1.y, y[5]);
+                        y[6] = fmaf(f.y, b1.z, y[6]), y[7] = fmaf(f.y, b1.w, y[7]);
+                    }
+                    *reinterpret_cast<uint4 *>(a.out + row * D + c + e) =
+                        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                }
+            }
+        } else if (ok) {
+            // row by row
+            constexpr int VPL = D / 32;
+            for (int k = 0; k < 32; ++k) {
+                const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = i0 + half * a.half_tokens + t, jj = h * a.G + rr - t * a.G;
+                if (t >= a.half_tokens || ii >= s.n) break;
+                float q[VPL], acc[VPL];
+                ref = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < VPL; ++e) {
+                    q[e] = __uint_as_float(uint32_t(a.q[(s.first + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
+                    acc[e] = 0.0f;
+                }
+                const uint16_t *kr = a.k + s.k_first * a.k_ts + h * a.k_hs, *vr = a.v + s.k_first * a.v_ts + h * a.v_hs;
+                const int place = s.T - s.n + ii, ja = min(keys.j1, keys.na), jb = max(keys.j0, keys.na);
+                if (keys.j0 < ja)
+                    row_keys<D>(a, q, kr, vr, place, int64_t(keys.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(keys.a_end)), acc, ref, sum);
+                if (jb < keys.j1)
+                    row_keys<D>(a, q, kr, vr, place, keys.b0 + int64_t(jb - keys.na) * PT_KEYS,
+                                min(keys.b0 + int64_t(keys.j1 - keys.na) * PT_KEYS, int64_t(keys.b_end)), acc, ref, sum);
+                const uint64_t row = uint64_t(s.first + ii) * uint32_t(a.nq) + uint32_t(jj);
+                    if (a.splits > 1) {
+                    const uint64_t at = uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row;
+                    if (lane == 0) a.stats[at] = make_float2(ref, sum);
+#pragma unroll
+                    for (int e = 0; e < VPL; ++e) a.part[at * D + lane * VPL + e] = acc[e];
+                } else {
+                    prompt_write<D>(a, row, ref, sum, acc, lane);
+                }
+            }
+        }
+        tc_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    }
+}
+
+// The parts of rows whose keys several blocks had, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_parts(const __grid_constant__ PromptArgs a) {
     constexpr int VPL = D / 32;
     const int lane = threadIdx.x & 31;
-    const uint32_t w = blockIdx.x * 4u + (threadIdx.x >> 5);
-    if (w >= uint32_t(a.n) * uint32_t(a.nq)) return;
-    const int tok = int(w / uint32_t(a.nq)), j = int(w % uint32_t(a.nq)), h = j / a.G;
-    for (int b = 0; b < a.nseq; ++b) {
-        const PromptSeq s = prompt_seq(a, b, lane == 0);
-        if (tok < s.first || tok >= s.first + s.n) continue;
-        float q[VPL], acc[VPL], ref = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            q[i] = __uint_as_float(uint32_t(a.q[tok * a.q_ts + j * a.q_hs + lane * VPL + i]) << 16);
-            acc[i] = 0.0f;
-        }
-        row_keys<D>(a, q, a.k + s.k_first * a.k_ts + h * a.k_hs, a.v + s.k_first * a.v_ts + h * a.v_hs, s.T - s.n + tok - s.first,
-                    0, s.T, acc, ref, sum);
-        const uint64_t row = uint64_t(tok) * uint32_t(a.nq) + uint32_t(j);
-        const float2 f = prompt_join(a, row, sum > 0.0f ? (ref + PT_BIAS + log2f(sum)) * 0.69314718055994531f : (sum == 0.0f ? -INFINITY : sum), lane == 0);
-        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            float y = acc[i] * inv * f.x;
-            if (a.base_out && f.y != 0.0f) y = fmaf(f.y, a.base_out[row * D + lane * VPL + i], y);
-            reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + lane * VPL + i] = __float2bfloat16_rn(y);
-        }
-        return;
+    const uint64_t rows = uint64_t(a.n) * uint32_t(a.nq);
+    const uint64_t row = uint64_t(blockIdx.x) * 8u + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int tok = int(row / uint32_t(a.nq));
+    // rows of no sequence, or of one that was skipped, have no parts
+    int lo = 0, hi = a.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (int(ld_plain_u32(a.q_first + mid)) <= tok)
+            lo = mid;
+        else
+            hi = mid - 1;
     }
+    const PromptSeq s = prompt_seq(a, lo, false);
+    if (tok < s.first || tok >= s.first + s.n) return;
+    float M = -INFINITY, L = 0.0f, acc[VPL];
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) acc[e] = 0.0f;
+    for (int c = 0; c < a.splits; ++c) M = fmaxf(M, a.stats[c * rows + row].x);
+    for (int c = 0; c < a.splits; ++c) {
+        const float2 st = a.stats[c * rows + row];
+        if (st.x == -INFINITY && st.y == 0.0f) continue;  // an empty part
+        const float f = exp2f(st.x - M);
+        L = fmaf(f, st.y, L);
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) acc[e] = fmaf(f, a.part[(c * rows + row) * D + lane * VPL + e], acc[e]);
+    }
+    prompt_write<D>(a, row, M, L, acc, lane);
 }
 
 static int prompt_ok(const kvp_prompt_shape *s) {
@@ -135,6 +680,82 @@ static int prompt_ok(const kvp_prompt_shape *s) {
     if (s->n_seqs > KVP_PROMPT_MAX_SEQS || s->n_q_heads > 65536 || s->n_q_heads / s->n_kv_heads > 128) return KVP_ERR_SIZE;
     if (int64_t(s->n_q_tokens) * s->n_q_heads >= (int64_t(1) << 31)) return KVP_ERR_SIZE;
     return KVP_OK;
+}
+
+// Blocks: tiles of 256 rows (tokens times the heads of a group) for every KV head.
+static int prompt_tokens(const kvp_prompt_shape *s) { return 2 * (128 / (s->n_q_heads / s->n_kv_heads)); }
+static int64_t prompt_tiles(const kvp_prompt_shape *s) { return int64_t(s->n_q_tokens / prompt_tokens(s)) + s->n_seqs; }
+
+// Where there are fewer blocks than SMs, the keys of each are cut into `splits` parts of
+// at least four tiles.  Workspace: the parts' statistics and sums.
+struct PromptSplit {
+    int splits;
+    uint64_t part, total;
+};
+static PromptSplit prompt_split(const kvp_prompt_shape *s) {
+    PromptSplit w;
+    const int64_t blocks = prompt_tiles(s) * s->n_kv_heads, sms = sm_count();
+    const int64_t most = std::max<int64_t>(1, s->n_k_tokens / (4 * PT_KEYS));
+    w.splits = int(std::max<int64_t>(1, std::min(most, sms / std::max<int64_t>(blocks, 1))));
+    const uint64_t rows = uint64_t(s->n_q_tokens) * uint64_t(s->n_q_heads) * uint64_t(w.splits > 1 ? w.splits : 0);
+    w.part = align256(rows * 8u);
+    w.total = std::max<uint64_t>(256, w.part + rows * uint64_t(s->head_dim) * 4u);
+    return w;
+}
+
+// cuTensorMapEncodeTiled, from the driver that the runtime has loaded.
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+    static std::atomic<void *> found{nullptr};
+    void *f = found.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult how;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+            how != cudaDriverEntryPointSuccess)
+            return nullptr;
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// A rows tensor as a tensor map: boxes of 64 dims x `heads` x `tokens`.
+static bool rows_map(CUtensorMap *map, const kvp_rows *r, int tokens, int heads, int d, int box_heads, int box_tokens) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t size[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
+    // the stride of a single head or token says nothing
+    const cuuint64_t stride[2] = {heads > 1 ? cuuint64_t(r->head_stride) * 2 : cuuint64_t(d) * 2,
+                                  tokens > 1 ? cuuint64_t(r->token_stride) * 2 : cuuint64_t(d) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r->ptr), size, stride, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static thread_local uint32_t g_next_polls = 0;
+static thread_local bool g_limit_next = false;
+
+template <int D>
+static int launch_prompt(const PromptArgs &a, unsigned grid, cudaStream_t st) {
+    static bool ready[64] = {false};  // the opt-in to more than 48 KB, once per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        if (cudaFuncSetAttribute(prompt_attend<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(PromptTile<D>::SMEM)) !=
+            cudaSuccess)
+            return KVP_ERR_CUDA;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    prompt_attend<D><<<grid, PT_THREADS, PromptTile<D>::SMEM, st>>>(a);
+    count_launch();
+    if (a.splits > 1) {
+        const uint64_t rows = uint64_t(a.n) * uint64_t(a.nq);
+        prompt_join_parts<D><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+        count_launch();
+    }
+    return launch_status();
 }
 
 static int rows_ok(const kvp_rows *r, int tokens, int heads) {
@@ -155,7 +776,7 @@ extern "C" {
 
 size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape) {
     if (prompt_ok(shape) != KVP_OK) return 0;
-    return 256;
+    return size_t(prompt_split(shape).total);
 }
 
 int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_rows *k, const kvp_rows *v,
@@ -181,18 +802,35 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
     a.q_first = q_first, a.k_first = k_first, a.k_lens = k_lens;
     a.base_out = base_out, a.base_lse = base_lse;
     a.out = static_cast<uint16_t *>(out), a.lse = lse, a.error = error;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.negative = scale < 0.0f, a.flat = scale == 0.0f;
+    a.scale2 = a.flat ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
     a.nseq = shape->n_seqs, a.n = shape->n_q_tokens, a.nk = shape->n_k_tokens;
     a.nq = shape->n_q_heads, a.H = shape->n_kv_heads, a.G = a.nq / a.H;
     a.window = window, a.sinks = sinks;
-    const unsigned rows = unsigned(a.n) * unsigned(a.nq);
+    a.half_tokens = 128 / a.G;
+    const PromptSplit w = prompt_split(shape);
+    a.splits = w.splits;
+    a.stats = static_cast<float2 *>(ws);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.part);
+    const int64_t tiles = prompt_tiles(shape), grid = tiles * a.H * a.splits;
+    if (grid >= (int64_t(1) << 31)) return KVP_ERR_SIZE;
+    a.tiles = int(tiles);
+    // (with no keys at all nothing is copied: the maps are those of the queries)
+    const bool some = shape->n_k_tokens > 0;
+    if (!rows_map(&a.q_map, q, a.n, a.nq, shape->head_dim, a.G, a.half_tokens) ||
+        !rows_map(&a.k_map, some ? k : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS) ||
+        !rows_map(&a.v_map, some ? v : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS))
+        return KVP_ERR_CUDA;
+    a.polls = g_limit_next ? g_next_polls : PT_WAIT_LIMIT;
+    g_limit_next = false;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (shape->head_dim == 128)
-        prompt_rows<128><<<(rows + 3) / 4, 128, 0, st>>>(a);
-    else
-        prompt_rows<64><<<(rows + 3) / 4, 128, 0, st>>>(a);
-    count_launch();
-    return launch_status();
+    return shape->head_dim == 128 ? launch_prompt<128>(a, unsigned(grid), st) : launch_prompt<64>(a, unsigned(grid), st);
+}
+
+int kvp_test_limit_next_prompt(uint32_t polls) {
+    g_next_polls = polls;
+    g_limit_next = true;
+    return KVP_OK;
 }
 
 int kvprompt_status(const uint32_t *error, void *stream) {

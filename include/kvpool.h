@@ -47,10 +47,11 @@
  *    by the *_status calls.  No kernel traps or asserts.  Two kinds of
  *    device-side wait exist, both bounded: the pool encoder's key-quantize
  *    work waits for its layer's scale, released by another block of the same
- *    kernel; pool attention, CacheCard unpack and attention over pages wait
- *    on mbarriers for their own bulk copies into shared memory.  A wait that
- *    runs out is recorded in the container's error word and reported as
- *    KVP_ERR_TIMEOUT by kvpool_status / cachecard_status / kvpages_status; the
+ *    kernel; pool attention, CacheCard unpack, attention over pages and of
+ *    prompts wait on mbarriers for their own copies into shared memory (and
+ *    products).  A wait that runs out is recorded in the container's error
+ *    word (a prompt call's own) and reported as KVP_ERR_TIMEOUT by
+ *    kvpool_status / cachecard_status / kvpages_status / kvprompt_status; the
  *    CUDA context stays usable.
  */
 #ifndef KVPOOL_H
@@ -584,7 +585,14 @@ size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape);
  *    numbers are negative, is skipped and reported as KVP_ERR_PAGE.
  * A query that sees no token gets the base's output and lse, or zeros and -inf
  * without one.  What a query does not see (Inf and NaN too) has no part in its
- * result. */
+ * result; an Inf or NaN value that it sees is Inf or NaN in its dim.  Finite values
+ * give finite results up to bf16's largest.
+ * Scores are products of bf16 summed in fp32; softmax statistics are fp32,
+ * exponentials the hardware's in base 2 (2^-22); weights enter the value product as
+ * bf16 (2^-9, their sum before that), relative to 2^40 times the row's largest: those
+ * below 2^-78 of it count as zero, as do their products with values below 2^-86.  The
+ * kernel waits for its copies at most about half a second; should a wait run out, the
+ * outputs are unspecified and kvprompt_status reports KVP_ERR_TIMEOUT. */
 int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_rows *k, const kvp_rows *v,
                     const int32_t *q_first, const int32_t *k_first, const int32_t *k_lens, float scale, int window,
                     int sinks, const float *base_out, const float *base_lse, void *out, float *lse, uint32_t *error,
@@ -666,6 +674,13 @@ int kvp_test_limit_next_pages_attend(uint32_t polls);
  * lanes wait with the normal limit.  A warp gives up if any of its lanes does:
  * with one bit set the outcome is that of kvp_test_limit_next_pages_attend. */
 int kvp_test_limit_next_pages_attend_lanes(uint32_t polls, uint32_t lanes);
+
+/* Failure-path testing of attention of prompts: makes the NEXT kvprompt_attend on
+ * this thread poll each tile's copy at most `polls` times before its products (0: not
+ * at all, so every block gives up on its first tile, lets its copies in flight land
+ * with the normal limit, and leaves its rows unwritten); kvprompt_status then reports
+ * KVP_ERR_TIMEOUT and the CUDA context stays usable.  Returns KVP_OK. */
+int kvp_test_limit_next_prompt(uint32_t polls);
 
 #ifdef __cplusplus
 }

@@ -326,3 +326,18 @@ def test_rows_past_two_gigabytes():
     c.wsb = kv.kvprompt_workspace_bytes(c.shape)
     got = c.run(0.1)
     assert np.allclose(got[0], want[0], rtol=2.0 ** -7, atol=2.0 ** -10) and np.allclose(got[1], want[1], atol=1e-5)
+
+
+def test_wait_that_runs_out_is_reported():
+    """The next call polls for no copy at all: it gives up, reports it, and leaves the
+    context usable."""
+    for splits in (False, True):
+        c = Call([(5, 20000)] if splits else [(300, 40), (3, 0)], 2, 2, 128)
+        want = c.run(0.1)
+        kv.kvp_test_limit_next_prompt(0)
+        c.run(0.1)
+        assert kv.kvprompt_status(c.error) == kv.KVP_ERR_TIMEOUT
+        c.error.zero_()
+        got = c.run(0.1)
+        assert kv.kvprompt_status(c.error) == kv.KVP_OK
+        assert np.array_equal(got[0], want[0], equal_nan=True) and np.array_equal(got[1], want[1], equal_nan=True)
