@@ -248,8 +248,7 @@ struct PromptTile {
     static constexpr uint32_t SMEM = OFF_RING + SLOTS * BYTES + 1024;  // and the base's alignment
     static_assert(SMEM <= 232448, "shared memory of a block");
     // barriers, 8 bytes each
-    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 168, DONE = 184, TMEM = 192, DEAD = 196,
-                              ODD = 200;
+    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 168, DONE = 184, TMEM = 192, DEAD = 196;
 };
 
 // The keys that some row of a block sees: [0, a_end) and [b0, b_end), in tiles; tiles
@@ -287,6 +286,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     extern __shared__ uint8_t sm_raw[];
     const uint32_t sm = (smem_addr(sm_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < 3) {
+        const CUtensorMap *map = tid == 0 ? &a.q_map : (tid == 1 ? &a.k_map : &a.v_map);
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
 
     // the block's sequence and tile: sequence b has its tiles from q_first[b] / tokens + b on
     const int tokens = 2 * a.half_tokens;
@@ -326,17 +329,34 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     const int nt = keys.j1 - keys.j0;
 
     const uint32_t dead = sm + T::DEAD;
-    if (warp == 8) {
-        if (lane == 0) {
-            for (uint32_t i = 0; i < T::SLOTS; ++i) mbar_init_n(sm + T::FULL + 8 * i, 1), mbar_init_n(sm + T::FREE + 8 * i, 1);
-            mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
-            for (uint32_t i = 0; i < 2; ++i)
-                mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::P + 8 * i, 128), mbar_init_n(sm + T::O + 8 * i, 1);
-            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
-            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(sm + T::ODD), "r"(0u) : "memory");
-            mbar_init_fence();
+    // the n-th copy of K_0 V_0 K_1 V_1 ... into the ring
+    auto copy = [&](uint32_t n) {
+        const uint32_t at = n % T::SLOTS;
+        int t0, end;
+        keys.tile(keys.j0 + int(n / 2), t0, end);
+        mbar_expect_tx(sm + T::FULL + 8 * at, T::BYTES);
+        for (int c = 0; c < D / 64; ++c)
+            tma_g2s(sm + T::OFF_RING + at * T::BYTES + uint32_t(c) * T::CHUNK, n & 1 ? &a.v_map : &a.k_map, 64 * c, h,
+                    s.k_first + t0, sm + T::FULL + 8 * at);
+    };
+    if (warp == 9 && lane == 0) {
+        for (uint32_t i = 0; i < T::SLOTS; ++i) mbar_init_n(sm + T::FULL + 8 * i, 1), mbar_init_n(sm + T::FREE + 8 * i, 1);
+        mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
+        for (uint32_t i = 0; i < 2; ++i)
+            mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::P + 8 * i, 128), mbar_init_n(sm + T::O + 8 * i, 1);
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
+        mbar_init_fence();
+        // Q and the first keys and values: on their way before anything else
+        if (nt > 0) {
+            mbar_expect_tx(sm + T::Q, uint32_t(halves) * uint32_t(a.half_tokens) * uint32_t(a.G) * D * 2u);
+            for (int half = 0; half < halves; ++half)
+                for (int c = 0; c < D / 64; ++c)
+                    tma_g2s(sm + T::OFF_Q + uint32_t(half) * T::BYTES + uint32_t(c) * T::CHUNK, &a.q_map, 64 * c, h * a.G,
+                            s.first + i0 + half * a.half_tokens, sm + T::Q);
+            for (uint32_t n = 0; n < min(T::SLOTS, 2u * uint32_t(nt)); ++n) copy(n);
         }
-        __syncwarp();
+    }
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm + T::TMEM), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_before();
@@ -347,36 +367,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(sm + T::TMEM) : "memory");
 
     if (warp == 9) {
-        // --- copies: Q, then K_0 V_0 K_1 V_1 ... round the ring
+        // --- copies
         if (lane == 0 && nt > 0) {
-            const int head0 = h * a.G;
-            mbar_expect_tx(sm + T::Q, uint32_t(halves) * uint32_t(a.half_tokens) * uint32_t(a.G) * D * 2u);
-            for (int half = 0; half < halves; ++half)
-                for (int c = 0; c < D / 64; ++c)
-                    tma_g2s(sm + T::OFF_Q + uint32_t(half) * T::BYTES + uint32_t(c) * T::CHUNK, &a.q_map, 64 * c, head0,
-                            s.first + i0 + half * a.half_tokens, sm + T::Q);
-            uint32_t n = 0;
-            bool ok = true;
-            for (; ok && n < 2u * uint32_t(nt); ++n) {
-                const uint32_t at = n % T::SLOTS, round = n / T::SLOTS;
-                if (round > 0 && !pt_wait(a, sm + T::FREE + 8 * at, (round - 1) & 1, dead, PT_WAIT_LIMIT)) {
-                    ok = false;
-                    break;
-                }
-                int t0, end;
-                keys.tile(keys.j0 + int(n / 2), t0, end);
-                mbar_expect_tx(sm + T::FULL + 8 * at, T::BYTES);
-                for (int c = 0; c < D / 64; ++c)
-                    tma_g2s(sm + T::OFF_RING + at * T::BYTES + uint32_t(c) * T::CHUNK, n & 1 ? &a.v_map : &a.k_map, 64 * c, h,
-                            s.k_first + t0, sm + T::FULL + 8 * at);
+            const uint32_t all = 2u * uint32_t(nt);
+            uint32_t n = min(T::SLOTS, all);
+            for (; n < all; ++n) {
+                if (!pt_wait(a, sm + T::FREE + 8 * (n % T::SLOTS), (n / T::SLOTS - 1) & 1, dead, PT_WAIT_LIMIT)) break;
+                copy(n);
             }
             // whoever gave up: the copies in flight land before the block ends
-            if (!ok || n >= 2u * uint32_t(nt)) {
-                for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
-                    mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
-                mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
-            }
+            for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
+                mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
+            mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
         }
+        __syncwarp();
     } else if (warp == 8) {
         // --- products
         if (lane == 0 && nt > 0) {
@@ -435,19 +439,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
         const bool real = tl < a.half_tokens && i < s.n;
         const int p = real ? s.T - s.n + i : p_last;
         float ref = -INFINITY, sum = 0.0f;
-        bool ok = true;
+        bool ok = true, met = false;  // met: Inf or NaN
         for (int j = 0; j < nt; ++j) {
             int t0, end;
             keys.tile(keys.j0 + j, t0, end);
-            if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) {
-                ok = false;
-                break;
-            }
-            tc_after();
-            uint32_t x[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
-            // values that not all rows see (the same for all threads)
+            // Values that not all rows see (the same for all threads), while the scores are under
+            // way.
             const bool rest = end < t0 + PT_KEYS;
             const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
             if (rest || part) {
@@ -458,22 +455,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     break;
                 }
                 if (part) {
-                    // Inf and NaN times 0 are NaN.  Each half looks at its share of the rows, a
-                    // thread at one 16-byte column of every fourth or eighth (whatever the swizzle)
-                    constexpr int PER = D / 8;  // chunks of a row
+                    // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
+                    // every eighth or sixteenth row (in whatever place of the row)
+                    constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
+                    const int c = r % PER;
+                    const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
                     __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
-                    for (int row = half * (128 / PER) + r / PER; row < end - t0; row += halves * (128 / PER)) {
-                        const uint32_t c = uint32_t(r % PER);
-                        uint32_t w[4];
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                     : "r"(tile + c / 8u * T::CHUNK + uint32_t(row) * 128u + c % 8u * 16u) : "memory");
+#pragma unroll 8
+                    for (int k = r / PER; k < PT_KEYS; k += STEP) {
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        if (k < end - t0)
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
                     }
-                    if (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu)
-                        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(sm + T::ODD), "r"(1u) : "memory");
+                    met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
                 }
                 if (rest) {
                     for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
@@ -484,6 +482,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     fence_proxy_async();
                 }
             }
+            if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) {
+                ok = false;
+                break;
+            }
+            tc_after();
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
             tc_wait_ld();
 #pragma unroll
             for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
@@ -497,10 +503,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
                 const bool all = last >= 127 && (from <= 0 || first >= 128);
                 if (!__all_sync(0xffffffffu, all)) {
+                    // as bits, a word of 32 columns at a time: the words that a warp's rows see
+                    // whole cost nothing
+                    auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
                     const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > last || (c < f0 && c >= f1)) xf[c] = -INFINITY;
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
+                        if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
+                    }
                 }
             }
             float m[4];
@@ -547,10 +560,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             ok = __all_sync(0xffffffffu, pt_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead, PT_WAIT_LIMIT));
             tc_after();
         }
-        // every softmax warp is here: whether any has met Inf or NaN
-        asm volatile("bar.sync 1, %0;" ::"r"(128 * halves) : "memory");
+        // whether a thread of the half has met Inf or NaN
         uint32_t odd;
-        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sm + T::ODD) : "memory");
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+                     : "=r"(odd) : "r"(uint32_t(met)), "r"(1 + half) : "memory");
         if (ok && !odd) {
             const uint64_t row = uint64_t(s.first + i) * uint32_t(a.nq) + uint32_t(h * a.G + r - tl * a.G);
             float2 f = make_float2(1.0f, 0.0f);
@@ -561,39 +574,71 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             } else if (real) {
                 a.stats[uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
             }
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
+            // By way of shared memory (the half's queries, which nothing reads any more), 128 bytes
+            // of a row at a time: eight lanes then store a row's 128 bytes at once.  (Each thread
+            // its own row's 16 bytes at a time: 4.0 us a block of 256 rows of 128, 1.0 so.)
+            const uint32_t stage = sm + T::OFF_Q + uint32_t(warp) * 4096u;
+            const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
+            auto store = [&](const uint32_t (&w)[32], uint8_t *to, uint32_t row_bytes, uint32_t column) {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                 ::"r"(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u), "r"(w[4 * e]), "r"(w[4 * e + 1]),
+                                   "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0u;
+                for (uint32_t k = 0; k < 8; ++k) {
+                    const uint32_t from = 4u * k + (uint32_t(lane) >> 3), e = uint32_t(lane) & 7u;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stage + from * 128u + (e ^ (from & 7u)) * 16u) : "memory");
+                    const uint32_t its = __shfl_sync(0xffffffffu, at, int(from));
+                    if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes + column + e * 16u) = v;
+                }
+                __syncwarp();
+            };
+            auto load = [&](int c, uint32_t *o) {
                 if (nt > 0) {
                     tc_ld32(o_at + uint32_t(c), o);
                     tc_wait_ld();
                     tc_landed(o), tc_landed(o + 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                if (!real) continue;
-                if (a.splits > 1) {
-                    float *to = a.part + (uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row) * D + c;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    continue;
+            };
+            if (a.splits > 1) {
+                uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) * D);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    load(c, o);
+                    store(o, to, D * 4u, uint32_t(c) * 4u);
                 }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    float y[8];
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t o[32];
+                        load(c + 32 * u, o);
+                        const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D + c + 32 * u : nullptr;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) y[u] = within_bf16(__uint_as_float(o[e + u]) * inv) * f.x;
-                    if (a.base_out && f.y != 0.0f) {
-                        const float4 *bo = reinterpret_cast<const float4 *>(a.base_out + row * D + c + e);
-                        const float4 b0 = bo[0], b1 = bo[1];
-                        y[0] = fmaf(f.y, b0.x, y[0]), y[1] = fmaf(f.y, b0.y, y[1]), y[2] = fmaf(f.y, b0.z, y[2]);
-                        y[3] = fmaf(f.y, b0.w, y[3]), y[4] = fmaf(f.y, b1.x, y[4]), y[5] = fmaf(f.y, b1.y, y[5]);
-                        y[6] = fmaf(f.y, b1.z, y[6]), y[7] = fmaf(f.y, b1.w, y[7]);
+                        for (int e = 0; e < 32; e += 4) {
+                            float y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = within_bf16(__uint_as_float(o[e + k]) * inv) * f.x;
+                            if (bo) {
+                                const float4 b4 = *reinterpret_cast<const float4 *>(bo + e);
+                                y[0] = fmaf(f.y, b4.x, y[0]), y[1] = fmaf(f.y, b4.y, y[1]);
+                                y[2] = fmaf(f.y, b4.z, y[2]), y[3] = fmaf(f.y, b4.w, y[3]);
+                            }
+                            w[16 * u + e / 2] = pack_bf16x2(y[0], y[1]), w[16 * u + e / 2 + 1] = pack_bf16x2(y[2], y[3]);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(a.out + row * D + c + e) =
-                        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                    store(w, reinterpret_cast<uint8_t *>(a.out), D * 2u, uint32_t(c) * 2u);
                 }
             }
         } else if (ok) {
