@@ -45,7 +45,9 @@
 namespace kvp {
 
 constexpr int PT_KEYS = 128;                  // keys of a tile
-constexpr int PT_THREADS = 320;
+// Three warpgroups: 384 threads start with 168 registers each (64512 of the SM's), the third
+// gives 80 of its back and each of the others takes 40 more: 2 * 128 * 208 + 128 * 88 = 64512.
+constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
 constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f;
 
@@ -226,6 +228,13 @@ __device__ __forceinline__ float pt_exp2(float x) {  // results under 2^-126 are
     return r;
 }
 
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0u;
+}
+
 // A shared-memory operand in rows of 128 bytes under the 128-byte swizzle: groups of 8
 // rows are 1024 bytes apart (lbo: from one 64-element column of rows to the next, for
 // the operand whose rows run along the sum).
@@ -248,7 +257,7 @@ struct PromptTile {
     static constexpr uint32_t SMEM = OFF_RING + SLOTS * BYTES + 1024;  // and the base's alignment
     static_assert(SMEM <= 232448, "shared memory of a block");
     // barriers, 8 bytes each
-    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 168, DONE = 184, TMEM = 192, DEAD = 196;
+    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 184, DONE = 200, TMEM = 208, DEAD = 212;
 };
 
 // The keys that some row of a block sees: [0, a_end) and [b0, b_end), in tiles; tiles
@@ -268,7 +277,7 @@ struct PromptKeys {
 __device__ __forceinline__ bool pt_wait(const PromptArgs &a, uint32_t bar, uint32_t parity, uint32_t dead, uint32_t limit) {
     for (uint32_t i = 0; i < limit; ++i) {
         if (mbar_try(bar, parity)) return true;
-        if (i >= 64) {
+        if (i >= 4096 && i % 64 == 0) {
             uint32_t d;
             asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
             if (d) return false;
@@ -278,6 +287,11 @@ __device__ __forceinline__ bool pt_wait(const PromptArgs &a, uint32_t bar, uint3
     asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(1u) : "memory");
     prompt_flag(a, FLAG_TIMEOUT);
     return false;
+}
+
+// The same for a whole warp (one decision for all lanes).
+__device__ __forceinline__ bool warp_wait(const PromptArgs &a, uint32_t bar, uint32_t parity, uint32_t dead) {
+    return __all_sync(0xffffffffu, pt_wait(a, bar, parity, dead, PT_WAIT_LIMIT));
 }
 
 template <int D>
@@ -342,8 +356,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     if (warp == 9 && lane == 0) {
         for (uint32_t i = 0; i < T::SLOTS; ++i) mbar_init_n(sm + T::FULL + 8 * i, 1), mbar_init_n(sm + T::FREE + 8 * i, 1);
         mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
-        for (uint32_t i = 0; i < 2; ++i)
-            mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::P + 8 * i, 128), mbar_init_n(sm + T::O + 8 * i, 1);
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::O + 8 * i, 1);
+            mbar_init_n(sm + T::P + 16 * i, 4), mbar_init_n(sm + T::P + 16 * i + 8, 4);  // a warp each
+        }
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
         mbar_init_fence();
         // Q and the first keys and values: on their way before anything else
@@ -363,321 +379,364 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     }
     __syncthreads();
     tc_after();
-    uint32_t tmem;
-    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(sm + T::TMEM) : "memory");
+    // (a block has all 512 columns of TMEM: they start at 0.  S at 128 half, O at 256 + D half.)
 
-    if (warp == 9) {
-        // --- copies
-        if (lane == 0 && nt > 0) {
-            const uint32_t all = 2u * uint32_t(nt);
-            uint32_t n = min(T::SLOTS, all);
-            for (; n < all; ++n) {
-                if (!pt_wait(a, sm + T::FREE + 8 * (n % T::SLOTS), (n / T::SLOTS - 1) & 1, dead, PT_WAIT_LIMIT)) break;
-                copy(n);
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_LESS));
+        if (warp == 9) {
+            // --- copies
+            if (lane == 0 && nt > 0) {
+                const uint32_t all = 2u * uint32_t(nt);
+                uint32_t n = min(T::SLOTS, all);
+                for (; n < all; ++n) {
+                    if (!pt_wait(a, sm + T::FREE + 8 * (n % T::SLOTS), (n / T::SLOTS - 1) & 1, dead, PT_WAIT_LIMIT)) break;
+                    copy(n);
+                }
+                // whoever gave up: the copies in flight land before the block ends
+                for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
+                    mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
+                mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
             }
-            // whoever gave up: the copies in flight land before the block ends
-            for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
-                mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
-            mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // --- products
-        if (lane == 0 && nt > 0) {
+            __syncwarp();
+        } else if (warp == 8) {
+            // --- products.  The whole warp goes through the loop, with numbers that are the same
+            // in all lanes as far as the compiler can see, and one lane issues: the operands' descriptors
+            // are then formed in uniform registers.  (In a branch of one lane each product costs 130
+            // cycles instead of 65.)
+            const int tiles = __shfl_sync(0xffffffffu, nt, 0);
+            const bool two = __shfl_sync(0xffffffffu, halves, 0) == 2;
             const uint32_t kind_s = tc_kind(128) | (a.negative ? TC_NEGATE_A : 0u), kind_o = tc_kind(D) | TC_B_BY_ROWS;
-            auto scores = [&](int half, uint32_t at) {  // S = Q K^T
-                const uint64_t qd = tc_operand(sm + T::OFF_Q + uint32_t(half) * T::BYTES, 16);
+            auto scores = [&](uint32_t half, uint32_t at) {  // S = Q K^T
+                const uint64_t qd = tc_operand(sm + T::OFF_Q + half * T::BYTES, 16);
                 const uint64_t kd = tc_operand(sm + T::OFF_RING + at * T::BYTES, 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = uint64_t((uint32_t(k / 4) * T::CHUNK + uint32_t(k % 4) * 32u) >> 4);
-                    tc_mma_ss(tmem + uint32_t(half) * 128u, qd + off, kd + off, kind_s, k > 0);
+                    tc_mma_ss(half * 128u, qd + off, kd + off, kind_s, k > 0);
                 }
-                tc_commit(sm + T::S + 8 * uint32_t(half));
+                tc_commit(sm + T::S + 8 * half);
             };
-            bool ok = pt_wait(a, sm + T::Q, 0, dead, PT_WAIT_LIMIT) && pt_wait(a, sm + T::FULL, 0, dead, a.polls);
-            if (ok) {
+            auto values = [&](uint32_t half, uint32_t at, int u, bool add) {  // O += P V, 64 keys
+                const uint64_t vd = tc_operand(sm + T::OFF_RING + at * T::BYTES, T::CHUNK);
+#pragma unroll
+                for (int k = 4 * u; k < 4 * u + 4; ++k)
+                    tc_mma_ts(256u + half * D, half * 128u + 8u * uint32_t(k), vd + uint64_t(k * 2048 >> 4), kind_o, add || k > 0);
+            };
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t limit) {
+                const bool ok = __all_sync(0xffffffffu, pt_wait(a, sm + bar, parity, dead, limit));
                 tc_after();
-                for (int half = 0; half < halves; ++half) scores(half, 0);
+                return ok;
+            };
+            bool ok = tiles > 0 && wait(T::Q, 0, PT_WAIT_LIMIT) && wait(T::FULL, 0, a.polls);
+            if (ok && elect()) {
+                scores(0, 0);
+                if (two) scores(1, 0);
                 tc_commit(sm + T::FREE);
             }
-            for (int j = 0; ok && j < nt; ++j) {
-                const uint32_t nv = 2u * uint32_t(j) + 1u, nk = nv + 1u, v_at = nv % T::SLOTS, k_at = nk % T::SLOTS;
-                if (!(ok = pt_wait(a, sm + T::FULL + 8 * v_at, (nv / T::SLOTS) & 1, dead, a.polls))) break;
-                const bool more = j + 1 < nt;
-                for (int half = 0; ok && half < halves; ++half) {
-                    if (!(ok = pt_wait(a, sm + T::P + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) break;
-                    tc_after();
-                    const uint64_t vd = tc_operand(sm + T::OFF_RING + v_at * T::BYTES, T::CHUNK);
-#pragma unroll
-                    for (int k = 0; k < PT_KEYS / 16; ++k)  // O += P V
-                        tc_mma_ts(tmem + 256u + uint32_t(half) * D, tmem + uint32_t(half) * 128u + 8u * uint32_t(k),
-                                  vd + uint64_t(k * 2048 >> 4), kind_o, j > 0 || k > 0);
-                    if (half == halves - 1) tc_commit(sm + T::FREE + 8 * v_at);
-                    if (!more) {
-                        tc_commit(sm + T::O + 8 * uint32_t(half));
-                        continue;
-                    }
-                    if (half == 0 && !(ok = pt_wait(a, sm + T::FULL + 8 * k_at, (nk / T::SLOTS) & 1, dead, a.polls))) break;
-                    tc_after();
-                    scores(half, k_at);
-                    if (half == halves - 1) tc_commit(sm + T::FREE + 8 * k_at);
+            __syncwarp();
+            uint32_t v_at = 1, v_round = 0;  // V_j's place in the ring
+            for (int j = 0; ok && j < tiles; ++j) {
+                const bool more = j + 1 < tiles;
+                const uint32_t k_at = v_at + 1 == T::SLOTS ? 0 : v_at + 1, k_round = v_round ^ uint32_t(k_at == 0);
+                if (!(ok = wait(T::FULL + 8 * v_at, v_round, a.polls))) break;
+                if (!(ok = wait(T::P, j & 1, PT_WAIT_LIMIT))) break;
+                if (elect()) values(0, v_at, 0, j > 0);
+                __syncwarp();
+                if (!(ok = wait(T::P + 8, j & 1, PT_WAIT_LIMIT))) break;
+                if (elect()) {
+                    values(0, v_at, 1, true);
+                    if (!two) tc_commit(sm + T::FREE + 8 * v_at);
+                    if (!more) tc_commit(sm + T::O);
                 }
+                __syncwarp();
+                if (more) {
+                    if (!(ok = wait(T::FULL + 8 * k_at, k_round, a.polls))) break;
+                    if (elect()) {
+                        scores(0, k_at);
+                        if (!two) tc_commit(sm + T::FREE + 8 * k_at);
+                    }
+                    __syncwarp();
+                }
+                if (two) {
+                    if (!(ok = wait(T::P + 16, j & 1, PT_WAIT_LIMIT))) break;
+                    if (elect()) values(1, v_at, 0, j > 0);
+                    __syncwarp();
+                    if (!(ok = wait(T::P + 24, j & 1, PT_WAIT_LIMIT))) break;
+                    if (elect()) {
+                        values(1, v_at, 1, true);
+                        tc_commit(sm + T::FREE + 8 * v_at);
+                        if (more) {
+                            scores(1, k_at);
+                            tc_commit(sm + T::FREE + 8 * k_at);
+                        } else {
+                            tc_commit(sm + T::O + 8);
+                        }
+                    }
+                    __syncwarp();
+                }
+                v_at = k_at + 1 == T::SLOTS ? 0 : k_at + 1, v_round = k_round ^ uint32_t(v_at == 0);
             }
-            if (!ok) {  // nothing may be in flight when TMEM is given back
-                tc_commit(sm + T::DONE);
+            if (!ok && tiles > 0) {  // nothing may be in flight when TMEM is given back
+                if (elect()) tc_commit(sm + T::DONE);
+                __syncwarp();
                 mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
             }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < 4 * halves) {
-        // --- softmax: a thread a row
-        const int half = warp >> 2, r = tid & 127;
-        const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's 32 lanes of TMEM
-        const uint32_t s_at = tmem + uint32_t(half) * 128u + lanes, o_at = tmem + 256u + uint32_t(half) * D + lanes;
-        const int tl = r / a.G, i = i0 + half * a.half_tokens + tl;
-        const bool real = tl < a.half_tokens && i < s.n;
-        const int p = real ? s.T - s.n + i : p_last;
-        float ref = -INFINITY, sum = 0.0f;
-        bool ok = true, met = false;  // met: Inf or NaN
-        for (int j = 0; j < nt; ++j) {
-            int t0, end;
-            keys.tile(keys.j0 + j, t0, end);
-            // Values that not all rows see (the same for all threads), while the scores are under
-            // way.
-            const bool rest = end < t0 + PT_KEYS;
-            const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
-            if (rest || part) {
-                const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
-                const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
-                if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead, PT_WAIT_LIMIT))) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_MORE));
+        if (warp < 4 * halves) {
+            // --- softmax: a thread a row
+            const int half = warp >> 2, r = tid & 127;
+            const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's 32 lanes of TMEM
+            const uint32_t s_at = uint32_t(half) * 128u + lanes, o_at = 256u + uint32_t(half) * D + lanes;
+            const int tl = r / a.G, i = i0 + half * a.half_tokens + tl;
+            const bool real = tl < a.half_tokens && i < s.n;
+            const int p = real ? s.T - s.n + i : p_last;
+            float ref = -INFINITY, sum = 0.0f;
+            bool ok = true, met = false;  // met: Inf or NaN
+            for (int j = 0; j < nt; ++j) {
+                int t0, end;
+                keys.tile(keys.j0 + j, t0, end);
+                // Values that not all rows see (the same for all threads), while the scores are under
+                // way.
+                const bool rest = end < t0 + PT_KEYS;
+                const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
+                if (rest || part) {
+                    const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
+                    const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
+                    if (!warp_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                    if (part) {
+                        // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
+                        // every eighth or sixteenth row (in whatever place of the row)
+                        constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
+                        const int c = r % PER;
+                        const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
+                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
+#pragma unroll 8
+                        for (int k = r / PER; k < PT_KEYS; k += STEP) {
+                            uint32_t w[4] = {0u, 0u, 0u, 0u};
+                            if (k < end - t0)
+                                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
+                        }
+                        met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
+                    }
+                    if (rest) {
+                        for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
+                            const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
+                                         ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
+                        }
+                        fence_proxy_async();
+                    }
+                }
+                if (!warp_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                if (part) {
-                    // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
-                    // every eighth or sixteenth row (in whatever place of the row)
-                    constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
-                    const int c = r % PER;
-                    const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
-                    __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
-#pragma unroll 8
-                    for (int k = r / PER; k < PT_KEYS; k += STEP) {
-                        uint32_t w[4] = {0u, 0u, 0u, 0u};
-                        if (k < end - t0)
-                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
+                tc_after();
+                uint32_t x[128];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
-                    }
-                    met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
+                for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
+                float *xf = reinterpret_cast<float *>(x);
+                if (a.flat) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) xf[c] = 0.0f;
                 }
-                if (rest) {
-                    for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
-                        const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
-                                     ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
-                    }
-                    fence_proxy_async();
-                }
-            }
-            if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead, PT_WAIT_LIMIT))) {
-                ok = false;
-                break;
-            }
-            tc_after();
-            uint32_t x[128];
+                {   // columns that the row sees: up to `last`, from `from` on or below `first`
+                    const int last = min(end - 1, p) - t0;
+                    const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
+                    const bool all = last >= 127 && (from <= 0 || first >= 128);
+                    if (!__all_sync(0xffffffffu, all)) {
+                        // as bits, a word of 32 columns at a time: the words that a warp's rows see
+                        // whole cost nothing
+                        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
+                        const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
-            tc_wait_ld();
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
+                            if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
-            float *xf = reinterpret_cast<float *>(x);
-            if (a.flat) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) xf[c] = 0.0f;
-            }
-            {   // columns that the row sees: up to `last`, from `from` on or below `first`
-                const int last = min(end - 1, p) - t0;
-                const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
-                const bool all = last >= 127 && (from <= 0 || first >= 128);
-                if (!__all_sync(0xffffffffu, all)) {
-                    // as bits, a word of 32 columns at a time: the words that a warp's rows see
-                    // whole cost nothing
-                    auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
-                    const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
-                        if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
+                            for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
+                        }
                     }
                 }
-            }
-            float m[4];
+                float m[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) m[c] = xf[c];
+                for (int c = 0; c < 4; ++c) m[c] = fmaxf(xf[2 * c], xf[2 * c + 1]);
 #pragma unroll
-            for (int c = 4; c < 128; ++c) m[c & 3] = fmaxf(m[c & 3], xf[c]);
-            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale2;
-            const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? pt_exp2(ref - top) : 1.0f;
-                if (raise) ref = top;
-                sum *= f;
-                if (j > 0) {
+                for (int c = 4; c < 64; ++c) m[c & 3] = fmaxf(m[c & 3], fmaxf(xf[2 * c], xf[2 * c + 1]));
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale2;
+                const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? pt_exp2(ref - top) : 1.0f;
+                    if (raise) ref = top;
+                    sum *= f;
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tc_ld32(o_at + uint32_t(c), o);
+                            tc_wait_ld();
+                            tc_landed(o), tc_landed(o + 16);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st32(o_at + uint32_t(c), o);
+                        }
+                    }
+                }
+                const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                float2 part_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int c = 32 * u; c < 32 * u + 32; ++c) {
+                        const float2 e = __ffma2_rn(make_float2(xf[2 * c], xf[2 * c + 1]), make_float2(a.scale2, a.scale2), make_float2(off, off));
+                        const float2 w = make_float2(pt_exp2(e.x), pt_exp2(e.y));
+                        part_sum[c & 1] = __fadd2_rn(part_sum[c & 1], w);
+                        x[c] = pack_bf16x2(w.x, w.y);
+                    }
+                    tc_st32(s_at + 32u * uint32_t(u), x + 32 * u);
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
+                }
+                sum += (part_sum[0].x + part_sum[0].y) + (part_sum[1].x + part_sum[1].y);
+            }
+            if (ok && nt > 0) {
+                ok = warp_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead);
+                tc_after();
+            }
+            // whether a thread of the half has met Inf or NaN
+            uint32_t odd;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+                         : "=r"(odd) : "r"(uint32_t(met)), "r"(1 + half) : "memory");
+            if (ok && !odd) {
+                const uint64_t row = uint64_t(s.first + i) * uint32_t(a.nq) + uint32_t(h * a.G + r - tl * a.G);
+                float2 f = make_float2(1.0f, 0.0f);
+                float inv = 1.0f;
+                if (real && a.splits == 1) {
+                    f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
+                    inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+                } else if (real) {
+                    a.stats[uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
+                }
+                // By way of shared memory (the half's queries, which nothing reads any more), 128 bytes
+                // of a row at a time: eight lanes then store a row's 128 bytes at once.  (Each thread
+                // its own row's 16 bytes at a time: 4.0 us a block of 256 rows of 128, 1.0 so.)
+                const uint32_t stage = sm + T::OFF_Q + uint32_t(warp) * 4096u;
+                const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
+                auto store = [&](const uint32_t (&w)[32], uint8_t *to, uint32_t row_bytes, uint32_t column) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; ++e)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                     ::"r"(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u), "r"(w[4 * e]), "r"(w[4 * e + 1]),
+                                       "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) {
+                        const uint32_t from = 4u * k + (uint32_t(lane) >> 3), e = uint32_t(lane) & 7u;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(stage + from * 128u + (e ^ (from & 7u)) * 16u) : "memory");
+                        const uint32_t its = __shfl_sync(0xffffffffu, at, int(from));
+                        if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes + column + e * 16u) = v;
+                    }
+                    __syncwarp();
+                };
+                auto load = [&](int c, uint32_t *o) {
+                    if (nt > 0) {
                         tc_ld32(o_at + uint32_t(c), o);
                         tc_wait_ld();
                         tc_landed(o), tc_landed(o + 16);
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_st32(o_at + uint32_t(c), o);
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
                     }
-                }
-            }
-            const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
-            float2 part_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float2 e = __ffma2_rn(make_float2(xf[2 * c], xf[2 * c + 1]), make_float2(a.scale2, a.scale2), make_float2(off, off));
-                const float2 w = make_float2(pt_exp2(e.x), pt_exp2(e.y));
-                part_sum[c & 1] = __fadd2_rn(part_sum[c & 1], w);
-                x[c] = pack_bf16x2(w.x, w.y);
-            }
-            sum += (part_sum[0].x + part_sum[0].y) + (part_sum[1].x + part_sum[1].y);
-            tc_st32(s_at, x);
-            tc_st32(s_at + 32u, x + 32);
-            tc_wait_st();
-            tc_before();
-            mbar_arrive(sm + T::P + 8 * uint32_t(half));
-        }
-        if (ok && nt > 0) {
-            ok = __all_sync(0xffffffffu, pt_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead, PT_WAIT_LIMIT));
-            tc_after();
-        }
-        // whether a thread of the half has met Inf or NaN
-        uint32_t odd;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
-                     : "=r"(odd) : "r"(uint32_t(met)), "r"(1 + half) : "memory");
-        if (ok && !odd) {
-            const uint64_t row = uint64_t(s.first + i) * uint32_t(a.nq) + uint32_t(h * a.G + r - tl * a.G);
-            float2 f = make_float2(1.0f, 0.0f);
-            float inv = 1.0f;
-            if (real && a.splits == 1) {
-                f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
-                inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-            } else if (real) {
-                a.stats[uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
-            }
-            // By way of shared memory (the half's queries, which nothing reads any more), 128 bytes
-            // of a row at a time: eight lanes then store a row's 128 bytes at once.  (Each thread
-            // its own row's 16 bytes at a time: 4.0 us a block of 256 rows of 128, 1.0 so.)
-            const uint32_t stage = sm + T::OFF_Q + uint32_t(warp) * 4096u;
-            const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
-            auto store = [&](const uint32_t (&w)[32], uint8_t *to, uint32_t row_bytes, uint32_t column) {
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-                                 ::"r"(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u), "r"(w[4 * e]), "r"(w[4 * e + 1]),
-                                   "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
-                __syncwarp();
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) {
-                    const uint32_t from = 4u * k + (uint32_t(lane) >> 3), e = uint32_t(lane) & 7u;
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "r"(stage + from * 128u + (e ^ (from & 7u)) * 16u) : "memory");
-                    const uint32_t its = __shfl_sync(0xffffffffu, at, int(from));
-                    if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes + column + e * 16u) = v;
-                }
-                __syncwarp();
-            };
-            auto load = [&](int c, uint32_t *o) {
-                if (nt > 0) {
-                    tc_ld32(o_at + uint32_t(c), o);
-                    tc_wait_ld();
-                    tc_landed(o), tc_landed(o + 16);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-            };
-            if (a.splits > 1) {
-                uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) * D);
+                };
+                if (a.splits > 1) {
+                    uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) * D);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    load(c, o);
-                    store(o, to, D * 4u, uint32_t(c) * 4u);
-                }
-            } else {
-#pragma unroll 1
-                for (int c = 0; c < D; c += 64) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
-                        load(c + 32 * u, o);
-                        const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D + c + 32 * u : nullptr;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float y[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) y[k] = within_bf16(__uint_as_float(o[e + k]) * inv) * f.x;
-                            if (bo) {
-                                const float4 b4 = *reinterpret_cast<const float4 *>(bo + e);
-                                y[0] = fmaf(f.y, b4.x, y[0]), y[1] = fmaf(f.y, b4.y, y[1]);
-                                y[2] = fmaf(f.y, b4.z, y[2]), y[3] = fmaf(f.y, b4.w, y[3]);
-                            }
-                            w[16 * u + e / 2] = pack_bf16x2(y[0], y[1]), w[16 * u + e / 2 + 1] = pack_bf16x2(y[2], y[3]);
-                        }
+                        load(c, o);
+                        store(o, to, D * 4u, uint32_t(c) * 4u);
                     }
-                    store(w, reinterpret_cast<uint8_t *>(a.out), D * 2u, uint32_t(c) * 2u);
-                }
-            }
-        } else if (ok) {
-            // row by row
-            constexpr int VPL = D / 32;
-            for (int k = 0; k < 32; ++k) {
-                const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = i0 + half * a.half_tokens + t, jj = h * a.G + rr - t * a.G;
-                if (t >= a.half_tokens || ii >= s.n) break;
-                float q[VPL], acc[VPL];
-                ref = -INFINITY, sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < VPL; ++e) {
-                    q[e] = __uint_as_float(uint32_t(a.q[(s.first + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
-                    acc[e] = 0.0f;
-                }
-                const uint16_t *kr = a.k + s.k_first * a.k_ts + h * a.k_hs, *vr = a.v + s.k_first * a.v_ts + h * a.v_hs;
-                const int place = s.T - s.n + ii, ja = min(keys.j1, keys.na), jb = max(keys.j0, keys.na);
-                if (keys.j0 < ja)
-                    row_keys<D>(a, q, kr, vr, place, int64_t(keys.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(keys.a_end)), acc, ref, sum);
-                if (jb < keys.j1)
-                    row_keys<D>(a, q, kr, vr, place, keys.b0 + int64_t(jb - keys.na) * PT_KEYS,
-                                min(keys.b0 + int64_t(keys.j1 - keys.na) * PT_KEYS, int64_t(keys.b_end)), acc, ref, sum);
-                const uint64_t row = uint64_t(s.first + ii) * uint32_t(a.nq) + uint32_t(jj);
-                    if (a.splits > 1) {
-                    const uint64_t at = uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row;
-                    if (lane == 0) a.stats[at] = make_float2(ref, sum);
-#pragma unroll
-                    for (int e = 0; e < VPL; ++e) a.part[at * D + lane * VPL + e] = acc[e];
                 } else {
-                    prompt_write<D>(a, row, ref, sum, acc, lane);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t o[32];
+                            load(c + 32 * u, o);
+                            const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D + c + 32 * u : nullptr;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                float y[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) y[k] = within_bf16(__uint_as_float(o[e + k]) * inv) * f.x;
+                                if (bo) {
+                                    const float4 b4 = *reinterpret_cast<const float4 *>(bo + e);
+                                    y[0] = fmaf(f.y, b4.x, y[0]), y[1] = fmaf(f.y, b4.y, y[1]);
+                                    y[2] = fmaf(f.y, b4.z, y[2]), y[3] = fmaf(f.y, b4.w, y[3]);
+                                }
+                                w[16 * u + e / 2] = pack_bf16x2(y[0], y[1]), w[16 * u + e / 2 + 1] = pack_bf16x2(y[2], y[3]);
+                            }
+                        }
+                        store(w, reinterpret_cast<uint8_t *>(a.out), D * 2u, uint32_t(c) * 2u);
+                    }
+                }
+            } else if (ok) {
+                // row by row
+                constexpr int VPL = D / 32;
+                for (int k = 0; k < 32; ++k) {
+                    const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = i0 + half * a.half_tokens + t, jj = h * a.G + rr - t * a.G;
+                    if (t >= a.half_tokens || ii >= s.n) break;
+                    float q[VPL], acc[VPL];
+                    ref = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < VPL; ++e) {
+                        q[e] = __uint_as_float(uint32_t(a.q[(s.first + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
+                        acc[e] = 0.0f;
+                    }
+                    const uint16_t *kr = a.k + s.k_first * a.k_ts + h * a.k_hs, *vr = a.v + s.k_first * a.v_ts + h * a.v_hs;
+                    const int place = s.T - s.n + ii, ja = min(keys.j1, keys.na), jb = max(keys.j0, keys.na);
+                    if (keys.j0 < ja)
+                        row_keys<D>(a, q, kr, vr, place, int64_t(keys.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(keys.a_end)), acc, ref, sum);
+                    if (jb < keys.j1)
+                        row_keys<D>(a, q, kr, vr, place, keys.b0 + int64_t(jb - keys.na) * PT_KEYS,
+                                    min(keys.b0 + int64_t(keys.j1 - keys.na) * PT_KEYS, int64_t(keys.b_end)), acc, ref, sum);
+                    const uint64_t row = uint64_t(s.first + ii) * uint32_t(a.nq) + uint32_t(jj);
+                        if (a.splits > 1) {
+                        const uint64_t at = uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row;
+                        if (lane == 0) a.stats[at] = make_float2(ref, sum);
+#pragma unroll
+                        for (int e = 0; e < VPL; ++e) a.part[at * D + lane * VPL + e] = acc[e];
+                    } else {
+                        prompt_write<D>(a, row, ref, sum, acc, lane);
+                    }
                 }
             }
+            tc_before();
         }
-        tc_before();
     }
     __syncthreads();
     if (warp == 8) {
         tc_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(0u), "r"(512u));
     }
 }
 
