@@ -235,6 +235,12 @@ __device__ __forceinline__ bool elect() {
     return r != 0u;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // A shared-memory operand in rows of 128 bytes under the 128-byte swizzle: groups of 8
 // rows are 1024 bytes apart (lbo: from one 64-element column of rows to the next, for
 // the operand whose rows run along the sum).
@@ -434,11 +440,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 tc_commit(sm + T::FREE);
             }
             __syncwarp();
-            uint32_t v_at = 1, v_round = 0;  // V_j's place in the ring
+            uint32_t v_at = 1;  // V_j's place in the ring
             for (int j = 0; ok && j < tiles; ++j) {
                 const bool more = j + 1 < tiles;
-                const uint32_t k_at = v_at + 1 == T::SLOTS ? 0 : v_at + 1, k_round = v_round ^ uint32_t(k_at == 0);
-                if (!(ok = wait(T::FULL + 8 * v_at, v_round, a.polls))) break;
+                const uint32_t k_at = v_at + 1 == T::SLOTS ? 0 : v_at + 1;
+                // (whoever handed P over has seen V_j and K_{j+1}: a wait costs this warp some 170
+                // cycles even if there is nothing to wait for)
                 if (!(ok = wait(T::P, j & 1, PT_WAIT_LIMIT))) break;
                 if (elect()) values(0, v_at, 0, j > 0);
                 __syncwarp();
@@ -446,17 +453,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 if (elect()) {
                     values(0, v_at, 1, true);
                     if (!two) tc_commit(sm + T::FREE + 8 * v_at);
-                    if (!more) tc_commit(sm + T::O);
-                }
-                __syncwarp();
-                if (more) {
-                    if (!(ok = wait(T::FULL + 8 * k_at, k_round, a.polls))) break;
-                    if (elect()) {
+                    if (more) {
                         scores(0, k_at);
                         if (!two) tc_commit(sm + T::FREE + 8 * k_at);
+                    } else {
+                        tc_commit(sm + T::O);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
                 if (two) {
                     if (!(ok = wait(T::P + 16, j & 1, PT_WAIT_LIMIT))) break;
                     if (elect()) values(1, v_at, 0, j > 0);
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                     __syncwarp();
                 }
-                v_at = k_at + 1 == T::SLOTS ? 0 : k_at + 1, v_round = k_round ^ uint32_t(v_at == 0);
+                v_at = k_at + 1 == T::SLOTS ? 0 : k_at + 1;
             }
             if (!ok && tiles > 0) {  // nothing may be in flight when TMEM is given back
                 if (elect()) tc_commit(sm + T::DONE);
@@ -502,13 +506,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 // way.
                 const bool rest = end < t0 + PT_KEYS;
                 const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
-                if (rest || part) {
-                    const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
-                    const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
-                    if (!warp_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead)) {
+                // Copies that the products after this tile's weights need.  (The second half's come
+                // after the first's.)
+                const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
+                auto there = [&](uint32_t n) {
+                    return __all_sync(0xffffffffu, pt_wait(a, sm + T::FULL + 8 * (n % T::SLOTS), (n / T::SLOTS) & 1, dead, a.polls));
+                };
+                if (half == 0 || rest || part) {
+                    if (!there(n) || (half == 0 && j + 1 < nt && !there(n + 1))) {
                         ok = false;
                         break;
                     }
+                }
+                if (rest || part) {
+                    const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
                     if (part) {
                         // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
                         // every eighth or sixteenth row (in whatever place of the row)
@@ -543,40 +554,73 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 }
                 tc_after();
                 uint32_t x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
-                tc_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
                 float *xf = reinterpret_cast<float *>(x);
-                if (a.flat) {
+                tc_ld32(s_at, x), tc_ld32(s_at + 32u, x + 32);
+                // columns that the row sees: up to `last`, from `from` on or below `first`
+                const int last = min(end - 1, p) - t0;
+                const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
+                const bool all = __all_sync(0xffffffffu, last >= 127 && (from <= 0 || first >= 128));
+                const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
+                // what the row does not see, in half u of the columns, as bits, 32 columns at a
+                // time: the words that a warp's rows see whole cost nothing
+                auto hide = [&](int u) {
+                    if (a.flat) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) xf[c] = 0.0f;
-                }
-                {   // columns that the row sees: up to `last`, from `from` on or below `first`
-                    const int last = min(end - 1, p) - t0;
-                    const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
-                    const bool all = last >= 127 && (from <= 0 || first >= 128);
-                    if (!__all_sync(0xffffffffu, all)) {
-                        // as bits, a word of 32 columns at a time: the words that a warp's rows see
-                        // whole cost nothing
-                        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
-                        const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
-                            if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
-                        }
+                        for (int c = 0; c < 64; ++c) xf[64 * u + c] = 0.0f;
                     }
-                }
+                    if (all) return;
+                    auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
+#pragma unroll
+                    for (int w = 2 * u; w < 2 * u + 2; ++w) {
+                        const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
+                        if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
+                    }
+                };
+                auto landed = [&](int u) {
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc_landed(x + 64 * u + 16 * c);
+                };
+                landed(0);
+                tc_ld32(s_at + 64u, x + 64), tc_ld32(s_at + 96u, x + 96);
+                hide(0);
+                // The weights of the first 64 columns are formed with the reference as it is, while
+                // the others are on their way and the largest score is found; again if that raises it.
+                float2 total;
+                auto weights = [&](int u, float off, uint32_t *w) {
+                    float2 t0 = make_float2(0.0f, 0.0f), t1 = t0;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float2 e = __ffma2_rn(make_float2(xf[64 * u + 2 * c], xf[64 * u + 2 * c + 1]),
+                                                    make_float2(a.scale2, a.scale2), make_float2(off, off));
+                        const float2 y = make_float2(pt_exp2(e.x), pt_exp2(e.y));
+                        (c & 1 ? t1 : t0) = __fadd2_rn(c & 1 ? t1 : t0, y);
+                        w[c] = pack_bf16x2(y.x, y.y);
+                    }
+                    return __fadd2_rn(t0, t1);
+                };
+                auto hand_over = [&](int u, const uint32_t *w) {
+                    tc_st32(s_at + 32u * uint32_t(u), w);
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
+                };
+                float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                uint32_t w[32];
+                total = weights(0, off, w);
                 float m[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) m[c] = fmaxf(xf[2 * c], xf[2 * c + 1]);
 #pragma unroll
-                for (int c = 4; c < 64; ++c) m[c & 3] = fmaxf(m[c & 3], fmaxf(xf[2 * c], xf[2 * c + 1]));
-                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale2;
+                for (int c = 4; c < 32; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
+                landed(1);
+                hide(1);
+#pragma unroll
+                for (int c = 32; c < 64; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
+                const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale2;
                 const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? pt_exp2(ref - top) : 1.0f;
@@ -594,25 +638,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                             tc_st32(o_at + uint32_t(c), o);
                         }
                     }
+                    off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                    total = weights(0, off, w);
                 }
-                const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
-                float2 part_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                    for (int c = 32 * u; c < 32 * u + 32; ++c) {
-                        const float2 e = __ffma2_rn(make_float2(xf[2 * c], xf[2 * c + 1]), make_float2(a.scale2, a.scale2), make_float2(off, off));
-                        const float2 w = make_float2(pt_exp2(e.x), pt_exp2(e.y));
-                        part_sum[c & 1] = __fadd2_rn(part_sum[c & 1], w);
-                        x[c] = pack_bf16x2(w.x, w.y);
-                    }
-                    tc_st32(s_at + 32u * uint32_t(u), x + 32 * u);
-                    tc_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
-                }
-                sum += (part_sum[0].x + part_sum[0].y) + (part_sum[1].x + part_sum[1].y);
+                hand_over(0, w);
+                total = __fadd2_rn(total, weights(1, off, w));
+                hand_over(1, w);
+                sum += total.x + total.y;
             }
             if (ok && nt > 0) {
                 ok = warp_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead);
