@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
         mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::O + 8 * i, 1);
-            mbar_init_n(sm + T::P + 16 * i, 4), mbar_init_n(sm + T::P + 16 * i + 8, 4);  // a warp each
+            // an arrival a warp, and in the first half the one of those who see to the copies
+            mbar_init_n(sm + T::P + 16 * i, i ? 4 : 5), mbar_init_n(sm + T::P + 16 * i + 8, i ? 4 : 5);
         }
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
         mbar_init_fence();
@@ -385,7 +386,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     }
     __syncthreads();
     tc_after();
-    // (a block has all 512 columns of TMEM: they start at 0.  S at 128 half, O at 256 + D half.)
+    // (A block has all 512 columns of TMEM: they start at 0.  S, and over it P, at 128 half, O at
+    // 256 + D half.  At head_dim 64 P has room beside S, and the next scores need then not wait for
+    // its product; measured slower, 351 against 306 us on 8192 tokens: the softmax has one more
+    // barrier, and it is what bounds that.)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_LESS));
@@ -444,8 +448,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             for (int j = 0; ok && j < tiles; ++j) {
                 const bool more = j + 1 < tiles;
                 const uint32_t k_at = v_at + 1 == T::SLOTS ? 0 : v_at + 1;
-                // (whoever handed P over has seen V_j and K_{j+1}: a wait costs this warp some 170
-                // cycles even if there is nothing to wait for)
                 if (!(ok = wait(T::P, j & 1, PT_WAIT_LIMIT))) break;
                 if (elect()) values(0, v_at, 0, j > 0);
                 __syncwarp();
@@ -486,6 +488,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
             }
             __syncwarp();
+        } else if (warp == 10) {
+            // --- what the products wait for beside the softmax: the copies of V_j and K_{j+1}, as one
+            // more arrival at the first half's barriers (a wait costs the others some 100 cycles even
+            // if there is nothing to wait for)
+            if (lane == 0) {
+                auto there = [&](uint32_t n) { return pt_wait(a, sm + T::FULL + 8 * (n % T::SLOTS), (n / T::SLOTS) & 1, dead, a.polls); };
+                for (int j = 0; j < nt; ++j) {
+                    const uint32_t n = 2u * uint32_t(j) + 1u;
+                    const bool more = j + 1 < nt;
+                    if (!there(n)) break;
+                    mbar_arrive(sm + T::P);
+                    if (more && !there(n + 1)) break;
+                    mbar_arrive(sm + T::P + 8);
+                    if (!pt_wait(a, sm + T::P + 8, uint32_t(j) & 1, dead, PT_WAIT_LIMIT)) break;
+                }
+            }
+            __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_MORE));
@@ -499,53 +518,64 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             const int p = real ? s.T - s.n + i : p_last;
             float ref = -INFINITY, sum = 0.0f;
             bool ok = true, met = false;  // met: Inf or NaN
+            // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
+            int in0 = 0, in1 = 0;
+            if (!a.flat) {
+                const int64_t old = a.window ? int64_t(p_last) - a.window + 1 - keys.b0 : 0;
+                in0 = keys.na - keys.j0 + int((max(old, int64_t(0)) + PT_KEYS - 1) / PT_KEYS);
+                in1 = keys.na - keys.j0 + max(p_first + 1 - keys.b0, 0) / PT_KEYS;
+            }
             for (int j = 0; j < nt; ++j) {
-                int t0, end;
-                keys.tile(keys.j0 + j, t0, end);
-                // Values that not all rows see (the same for all threads), while the scores are under
-                // way.
-                const bool rest = end < t0 + PT_KEYS;
-                const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
-                // Copies that the products after this tile's weights need.  (The second half's come
-                // after the first's.)
-                const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
-                auto there = [&](uint32_t n) {
-                    return __all_sync(0xffffffffu, pt_wait(a, sm + T::FULL + 8 * (n % T::SLOTS), (n / T::SLOTS) & 1, dead, a.polls));
-                };
-                if (half == 0 || rest || part) {
-                    if (!there(n) || (half == 0 && j + 1 < nt && !there(n + 1))) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (rest || part) {
-                    const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
-                    if (part) {
-                        // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
-                        // every eighth or sixteenth row (in whatever place of the row)
-                        constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
-                        const int c = r % PER;
-                        const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
-                        __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
-#pragma unroll 8
-                        for (int k = r / PER; k < PT_KEYS; k += STEP) {
-                            uint32_t w[4] = {0u, 0u, 0u, 0u};
-                            if (k < end - t0)
-                                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
+                const bool inner = j >= in0 && j < in1;
+                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // the columns that the row sees, as bits
+                if (!inner) {
+                    int t0, end;
+                    keys.tile(keys.j0 + j, t0, end);
+                    {
+                        const int last = min(end - 1, p) - t0;
+                        const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
+                        const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
+                        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
-                        }
-                        met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
+                        for (int w = 0; w < 4; ++w) see[w] = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
                     }
-                    if (rest) {
-                        for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
-                            const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
-                                         ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
+                    // Values that not all rows see, while the scores are under way.
+                    const bool rest = end < t0 + PT_KEYS;
+                    const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
+                    if (rest || part) {
+                        const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
+                        const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
+                        if (!warp_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead)) {
+                            ok = false;
+                            break;
                         }
-                        fence_proxy_async();
+                        if (part) {
+                            // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
+                            // every eighth or sixteenth row (in whatever place of the row)
+                            constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
+                            const int c = r % PER;
+                            const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
+                            __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
+#pragma unroll 8
+                            for (int k = r / PER; k < PT_KEYS; k += STEP) {
+                                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                                if (k < end - t0)
+                                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
+                            }
+                            met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
+                        }
+                        if (rest) {
+                            for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
+                                const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
+                                             ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
+                            }
+                            fence_proxy_async();
+                        }
                     }
                 }
                 if (!warp_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead)) {
@@ -555,76 +585,35 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 tc_after();
                 uint32_t x[128];
                 float *xf = reinterpret_cast<float *>(x);
-                tc_ld32(s_at, x), tc_ld32(s_at + 32u, x + 32);
-                // columns that the row sees: up to `last`, from `from` on or below `first`
-                const int last = min(end - 1, p) - t0;
-                const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
-                const bool all = __all_sync(0xffffffffu, last >= 127 && (from <= 0 || first >= 128));
-                const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
-                // what the row does not see, in half u of the columns, as bits, 32 columns at a
-                // time: the words that a warp's rows see whole cost nothing
-                auto hide = [&](int u) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
+                float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
+                if (!inner) {
                     if (a.flat) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) xf[64 * u + c] = 0.0f;
+                        for (int c = 0; c < 128; ++c) xf[c] = 0.0f;
                     }
-                    if (all) return;
-                    auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
 #pragma unroll
-                    for (int w = 2 * u; w < 2 * u + 2; ++w) {
-                        const uint32_t see = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
-                        if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
+                    for (int w = 0; w < 4; ++w) {
+                        if (__all_sync(0xffffffffu, see[w] == 0xFFFFFFFFu)) continue;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) xf[32 * w + c] = see & (1u << c) ? xf[32 * w + c] : -INFINITY;
+                        for (int c = 32 * w; c < 32 * w + 32; ++c) xf[c] = see[w] & (1u << (c & 31)) ? xf[c] : -INFINITY;
                     }
-                };
-                auto landed = [&](int u) {
-                    tc_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc_landed(x + 64 * u + 16 * c);
-                };
-                landed(0);
-                tc_ld32(s_at + 64u, x + 64), tc_ld32(s_at + 96u, x + 96);
-                hide(0);
-                // The weights of the first 64 columns are formed with the reference as it is, while
-                // the others are on their way and the largest score is found; again if that raises it.
-                float2 total;
-                auto weights = [&](int u, float off, uint32_t *w) {
-                    float2 t0 = make_float2(0.0f, 0.0f), t1 = t0;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float2 e = __ffma2_rn(make_float2(xf[64 * u + 2 * c], xf[64 * u + 2 * c + 1]),
-                                                    make_float2(a.scale2, a.scale2), make_float2(off, off));
-                        const float2 y = make_float2(pt_exp2(e.x), pt_exp2(e.y));
-                        (c & 1 ? t1 : t0) = __fadd2_rn(c & 1 ? t1 : t0, y);
-                        w[c] = pack_bf16x2(y.x, y.y);
-                    }
-                    return __fadd2_rn(t0, t1);
-                };
-                auto hand_over = [&](int u, const uint32_t *w) {
-                    tc_st32(s_at + 32u * uint32_t(u), w);
-                    tc_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
-                };
-                float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
-                uint32_t w[32];
-                total = weights(0, off, w);
+                }
                 float m[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) m[c] = fmaxf(xf[2 * c], xf[2 * c + 1]);
 #pragma unroll
-                for (int c = 4; c < 32; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
-                landed(1);
-                hide(1);
-#pragma unroll
-                for (int c = 32; c < 64; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
+                for (int c = 4; c < 64; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
                 const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale2;
                 const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? pt_exp2(ref - top) : 1.0f;
                     if (raise) ref = top;
+                    off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
                     sum *= f;
                     if (j > 0) {
 #pragma unroll 1
@@ -638,13 +627,25 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                             tc_st32(o_at + uint32_t(c), o);
                         }
                     }
-                    off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
-                    total = weights(0, off, w);
                 }
-                hand_over(0, w);
-                total = __fadd2_rn(total, weights(1, off, w));
-                hand_over(1, w);
-                sum += total.x + total.y;
+                float2 t0 = make_float2(sum, 0.0f), t1 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int c = 32 * u; c < 32 * u + 32; ++c) {
+                        const float2 e = __ffma2_rn(make_float2(xf[2 * c], xf[2 * c + 1]), make_float2(a.scale2, a.scale2),
+                                                    make_float2(off, off));
+                        const float2 y = make_float2(pt_exp2(e.x), pt_exp2(e.y));
+                        (c & 1 ? t1 : t0) = __fadd2_rn(c & 1 ? t1 : t0, y);
+                        x[c] = pack_bf16x2(y.x, y.y);
+                    }
+                    tc_st32(s_at + 32u * uint32_t(u), x + 32 * u);
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
+                }
+                sum = (t0.x + t0.y) + (t1.x + t1.y);
             }
             if (ok && nt > 0) {
                 ok = warp_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead);
