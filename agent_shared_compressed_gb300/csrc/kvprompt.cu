@@ -258,25 +258,70 @@ template <int D>
 struct PromptTile {
     static constexpr uint32_t BYTES = 128u * D * 2u;   // of 128 rows of queries, keys or values
     static constexpr uint32_t CHUNK = 128u * 128u;     // 64 dims of them
-    static constexpr uint32_t SLOTS = D == 128 ? 5 : 8;
+    static constexpr uint32_t SLOTS = D == 128 ? 4 : 6;
     static constexpr uint32_t OFF_Q = 1024, OFF_RING = OFF_Q + 2 * BYTES;
-    static constexpr uint32_t SMEM = OFF_RING + SLOTS * BYTES + 1024;  // and the base's alignment
+    static constexpr uint32_t OFF_STAGE = OFF_RING + SLOTS * BYTES;  // 4096 bytes a softmax warp
+    static constexpr uint32_t SMEM = OFF_STAGE + 8 * 4096 + 1024;    // and the base's alignment
     static_assert(SMEM <= 232448, "shared memory of a block");
-    // barriers, 8 bytes each
-    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, S = 136, P = 152, O = 184, DONE = 200, TMEM = 208, DEAD = 212;
+    // barriers, 8 bytes each, and what else lies before the queries
+    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, QFREE = 136, S = 144, P = 160, O = 192, DONE = 208, WORK = 216,
+                              READ = 232, NEXT = 248, TMEM = 256, DEAD = 260, ANSWER = 272, ITEM = 320;
 };
 
-// The keys that some row of a block sees: [0, a_end) and [b0, b_end), in tiles; tiles
-// j0 .. j1 - 1 are this block's.
-struct PromptKeys {
-    int a_end, b0, b_end, na, j0, j1;
+// A piece of work: 256 rows (or fewer) of one sequence and KV head, and the keys that some
+// of them see: [0, a_end) and [b0, b_end), in tiles, of which tiles j0 .. j0 + nt - 1.
+struct alignas(16) PromptWork {
+    int valid, split, h;
+    int row, count;      // first row of q, tokens
+    int k_first;         // first row of k and v
+    int p_first;         // place of the first token (below 0: before the first key)
+    int a_end, b0, b_end, na, j0, nt;
+    int unused[3];
+
+    __device__ __forceinline__ int p_last() const { return p_first + count - 1; }
     __device__ __forceinline__ void tile(int j, int &t0, int &end) const {
+        j += j0;
         if (j < na)
             t0 = j * PT_KEYS, end = min(t0 + PT_KEYS, a_end);
         else
             t0 = b0 + (j - na) * PT_KEYS, end = int(min(int64_t(t0) + PT_KEYS, int64_t(b_end)));
     }
 };
+static_assert(sizeof(PromptWork) == 64, "four 16-byte loads");
+
+// The work of a block number; false if it has none.  Sequence b has its tiles from number
+// q_first[b] / tokens + b on: more numbers than tiles, but found without a sum.  (By a warp.)
+__device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block, PromptWork &w) {
+    const int lane = threadIdx.x & 31, tokens = 2 * a.half_tokens;
+    w.split = int(block % uint32_t(a.splits));
+    w.h = int(block / uint32_t(a.splits) % uint32_t(a.H));
+    const int slot = a.tiles - 1 - int(block / uint32_t(a.splits) / uint32_t(a.H));  // the longest first
+    int lo = 0, hi = a.nseq - 1;  // the last b with its first tile at or before this one, 32 places at a time
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
+        const bool before = max(int(ld_plain_u32(a.q_first + at)), 0) / tokens + at <= slot;
+        const int n = __popc(__ballot_sync(0xffffffffu, before));  // (a run of ones)
+        const int nlo = n ? min(lo + n * step, hi) : lo, nhi = n < 32 ? min(lo + (n + 1) * step, hi) - 1 : hi;
+        lo = nlo, hi = max(nlo, nhi);
+    }
+    const PromptSeq s = prompt_seq(a, lo, lane == 0);
+    const int64_t i0 = int64_t(slot - lo - max(s.first, 0) / tokens) * tokens;
+    if (i0 < 0 || i0 >= s.n) return false;
+    w.valid = 1;
+    w.row = s.first + int(i0), w.count = min(tokens, s.n - int(i0));
+    w.k_first = s.k_first;
+    w.p_first = s.T - s.n + int(i0);
+    auto tiles_of = [](int64_t n) { return int((n + PT_KEYS - 1) / PT_KEYS); };
+    const int64_t old = a.window ? int64_t(w.p_first) - a.window + 1 : 0;
+    w.b_end = max(w.p_last() + 1, 0), w.b0 = int(max(old, int64_t(0)));
+    w.a_end = min(a.sinks, w.b0);
+    // no more tiles without the gap: without it
+    if (tiles_of(w.b_end) <= tiles_of(w.a_end) + tiles_of(w.b_end - w.b0)) w.a_end = 0, w.b0 = 0;
+    w.na = tiles_of(w.a_end);
+    const int all = w.na + tiles_of(w.b_end - w.b0);
+    w.j0 = int(int64_t(all) * w.split / a.splits), w.nt = int(int64_t(all) * (w.split + 1) / a.splits) - w.j0;
+    return true;
+}
 
 // Waits until the barrier's phase is over; gives up when the limit or another warp's
 // wait has run out.
@@ -300,6 +345,15 @@ __device__ __forceinline__ bool warp_wait(const PromptArgs &a, uint32_t bar, uin
     return __all_sync(0xffffffffu, pt_wait(a, bar, parity, dead, PT_WAIT_LIMIT));
 }
 
+// The place of the n-th of a running number of tiles in a ring, and the parity of its round.
+struct RingPlace {
+    uint32_t at, parity;
+};
+template <uint32_t SLOTS>
+__device__ __forceinline__ RingPlace ring_place(uint32_t n) {
+    return {n % SLOTS, (n / SLOTS) & 1u};
+}
+
 template <int D>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_constant__ PromptArgs a) {
     using T = PromptTile<D>;
@@ -311,73 +365,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
         asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     }
 
-    // the block's sequence and tile: sequence b has its tiles from q_first[b] / tokens + b on
-    const int tokens = 2 * a.half_tokens;
-    const int split = int(blockIdx.x % uint32_t(a.splits));
-    const int h = int(blockIdx.x / uint32_t(a.splits) % uint32_t(a.H));
-    const int slot = a.tiles - 1 - int(blockIdx.x / uint32_t(a.splits) / uint32_t(a.H));  // the longest first
-    int b = 0;
-    {
-        int lo = 0, hi = a.nseq - 1;  // the last b with its first tile at or before this one
-        while (lo < hi) {
-            // 32 places at a time
-            const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
-            const bool before = max(int(ld_plain_u32(a.q_first + at)), 0) / tokens + at <= slot;
-            const int n = __popc(__ballot_sync(0xffffffffu, before));  // (a run of ones)
-            const int nlo = n ? min(lo + n * step, hi) : lo, nhi = n < 32 ? min(lo + (n + 1) * step, hi) - 1 : hi;
-            lo = nlo, hi = max(nlo, nhi);
-        }
-        b = lo;
-    }
-    const PromptSeq s = prompt_seq(a, b, tid == 0);
-    const int64_t i0_ = int64_t(slot - b - max(s.first, 0) / tokens) * tokens;
-    if (i0_ < 0 || i0_ >= s.n) return;
-    const int i0 = int(i0_), count = min(tokens, s.n - i0), halves = count > a.half_tokens ? 2 : 1;
-    const int p_first = s.T - s.n + i0, p_last = p_first + count - 1;  // places (below 0: no keys)
-    PromptKeys keys;
-    {
-        auto tiles_of = [](int64_t n) { return int((n + PT_KEYS - 1) / PT_KEYS); };
-        const int64_t old = a.window ? int64_t(p_first) - a.window + 1 : 0;
-        keys.b_end = max(p_last + 1, 0), keys.b0 = int(max(old, int64_t(0)));
-        keys.a_end = min(a.sinks, keys.b0);
-        // no more tiles without the gap: without it
-        if (tiles_of(keys.b_end) <= tiles_of(keys.a_end) + tiles_of(keys.b_end - keys.b0)) keys.a_end = 0, keys.b0 = 0;
-        keys.na = tiles_of(keys.a_end);
-        const int all = keys.na + tiles_of(keys.b_end - keys.b0);
-        keys.j0 = int(int64_t(all) * split / a.splits), keys.j1 = int(int64_t(all) * (split + 1) / a.splits);
-    }
-    const int nt = keys.j1 - keys.j0;
-
     const uint32_t dead = sm + T::DEAD;
-    // the n-th copy of K_0 V_0 K_1 V_1 ... into the ring
-    auto copy = [&](uint32_t n) {
-        const uint32_t at = n % T::SLOTS;
-        int t0, end;
-        keys.tile(keys.j0 + int(n / 2), t0, end);
-        mbar_expect_tx(sm + T::FULL + 8 * at, T::BYTES);
-        for (int c = 0; c < D / 64; ++c)
-            tma_g2s(sm + T::OFF_RING + at * T::BYTES + uint32_t(c) * T::CHUNK, n & 1 ? &a.v_map : &a.k_map, 64 * c, h,
-                    s.k_first + t0, sm + T::FULL + 8 * at);
-    };
     if (warp == 9 && lane == 0) {
         for (uint32_t i = 0; i < T::SLOTS; ++i) mbar_init_n(sm + T::FULL + 8 * i, 1), mbar_init_n(sm + T::FREE + 8 * i, 1);
-        mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::DONE, 1);
+        mbar_init_n(sm + T::Q, 1), mbar_init_n(sm + T::QFREE, 1), mbar_init_n(sm + T::DONE, 1), mbar_init_n(sm + T::NEXT, 1);
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::O + 8 * i, 1);
             // an arrival a warp, and in the first half the one of those who see to the copies
             mbar_init_n(sm + T::P + 16 * i, i ? 4 : 5), mbar_init_n(sm + T::P + 16 * i + 8, i ? 4 : 5);
+            mbar_init_n(sm + T::WORK + 8 * i, 1), mbar_init_n(sm + T::READ + 8 * i, 10);  // by warps 0-8 and 10
         }
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
         mbar_init_fence();
-        // Q and the first keys and values: on their way before anything else
-        if (nt > 0) {
-            mbar_expect_tx(sm + T::Q, uint32_t(halves) * uint32_t(a.half_tokens) * uint32_t(a.G) * D * 2u);
-            for (int half = 0; half < halves; ++half)
-                for (int c = 0; c < D / 64; ++c)
-                    tma_g2s(sm + T::OFF_Q + uint32_t(half) * T::BYTES + uint32_t(c) * T::CHUNK, &a.q_map, 64 * c, h * a.G,
-                            s.first + i0 + half * a.half_tokens, sm + T::Q);
-            for (uint32_t n = 0; n < min(T::SLOTS, 2u * uint32_t(nt)); ++n) copy(n);
-        }
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm + T::TMEM), "r"(512u) : "memory");
@@ -386,6 +385,24 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     }
     __syncthreads();
     tc_after();
+    // what the kernel before this one writes is there from here on; the next one may be placed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The k-th piece of this block's work, once it is there; false if there is none, or a wait
+    // ran out.  (By a warp.)
+    auto next_work = [&](uint32_t k, PromptWork &w) {
+        const uint32_t at = k & 1u;
+        if (!warp_wait(a, sm + T::WORK + 8 * at, (k >> 1) & 1u, dead)) return false;
+        uint32_t *to = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(to[4 * i]), "=r"(to[4 * i + 1]), "=r"(to[4 * i + 2]), "=r"(to[4 * i + 3])
+                         : "r"(sm + T::ITEM + 64 * at + 16 * i) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm + T::READ + 8 * at);
+        return w.valid != 0;
+    };
     // (A block has all 512 columns of TMEM: they start at 0.  S, and over it P, at 128 half, O at
     // 256 + D half.  At head_dim 64 P has room beside S, and the next scores need then not wait for
     // its product; measured slower, 351 against 306 us on 8192 tokens: the softmax has one more
@@ -394,18 +411,83 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_LESS));
         if (warp == 9) {
-            // --- copies
-            if (lane == 0 && nt > 0) {
-                const uint32_t all = 2u * uint32_t(nt);
-                uint32_t n = min(T::SLOTS, all);
-                for (; n < all; ++n) {
-                    if (!pt_wait(a, sm + T::FREE + 8 * (n % T::SLOTS), (n / T::SLOTS - 1) & 1, dead, PT_WAIT_LIMIT)) break;
-                    copy(n);
+            // --- work and copies.  A block's own number is its first work; then it takes over numbers
+            // of blocks that have not begun (cluster launch control), one at a time, when the copies
+            // of what it has are all under way: that leaves the others their share, and the next
+            // queries, keys and values come while the last tiles and results are worked on.
+            uint32_t block = blockIdx.x, k = 0, n = 0, queries = 0, asked = 0;
+            bool ok = true, more = true;
+            while (ok) {
+                PromptWork w = {};
+                if (more && !prompt_work(a, block, w)) w.valid = 0;
+                if (w.valid || !more) {
+                    const uint32_t at = k & 1u;
+                    if (k >= 2 && !(ok = warp_wait(a, sm + T::READ + 8 * at, ((k >> 1) - 1u) & 1u, dead))) break;
+                    if (lane == 0) {
+                        const uint32_t *from = reinterpret_cast<const uint32_t *>(&w);
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                         ::"r"(sm + T::ITEM + 64 * at + 16 * i), "r"(from[4 * i]), "r"(from[4 * i + 1]),
+                                           "r"(from[4 * i + 2]), "r"(from[4 * i + 3]) : "memory");
+                        mbar_arrive(sm + T::WORK + 8 * at);
+                    }
+                    __syncwarp();
+                    ++k;
+                    if (!more) break;
                 }
-                // whoever gave up: the copies in flight land before the block ends
-                for (uint32_t k = n > T::SLOTS ? n - T::SLOTS : 0; k < n; ++k)
-                    mbar_wait(sm + T::FULL + 8 * (k % T::SLOTS), (k / T::SLOTS) & 1, PT_WAIT_LIMIT);
-                mbar_wait(sm + T::Q, 0, PT_WAIT_LIMIT);
+                if (w.valid && w.nt > 0) {
+                    const int halves = w.count > a.half_tokens ? 2 : 1;
+                    if (queries > 0 && !(ok = warp_wait(a, sm + T::QFREE, (queries - 1u) & 1u, dead))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(sm + T::Q, uint32_t(halves) * uint32_t(a.half_tokens) * uint32_t(a.G) * D * 2u);
+                        for (int half = 0; half < halves; ++half)
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_g2s(sm + T::OFF_Q + uint32_t(half) * T::BYTES + uint32_t(c) * T::CHUNK, &a.q_map, 64 * c,
+                                        w.h * a.G, w.row + half * a.half_tokens, sm + T::Q);
+                    }
+                    ++queries;
+                    for (int c = 0; c < 2 * w.nt; ++c, ++n) {  // K_0 V_0 K_1 V_1 ... round the ring
+                        const RingPlace to = ring_place<T::SLOTS>(n);
+                        if (n >= T::SLOTS && !(ok = warp_wait(a, sm + T::FREE + 8 * to.at, to.parity ^ 1u, dead))) break;
+                        if (lane == 0) {
+                            int t0, end;
+                            w.tile(c / 2, t0, end);
+                            mbar_expect_tx(sm + T::FULL + 8 * to.at, T::BYTES);
+                            for (int e = 0; e < D / 64; ++e)
+                                tma_g2s(sm + T::OFF_RING + to.at * T::BYTES + uint32_t(e) * T::CHUNK, c & 1 ? &a.v_map : &a.k_map,
+                                        64 * e, w.h, w.k_first + t0, sm + T::FULL + 8 * to.at);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                // the next number
+                if (lane == 0) {
+                    mbar_expect_tx(sm + T::NEXT, 16);
+                    fence_proxy_async();  // the former answer has been read
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                                 ::"r"(sm + T::ANSWER), "r"(sm + T::NEXT) : "memory");
+                }
+                __syncwarp();
+                ++asked;
+                if (!(ok = warp_wait(a, sm + T::NEXT, (asked - 1u) & 1u, dead))) break;
+                uint32_t got;
+                asm volatile(
+                    "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%2];\n\t"
+                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+                    : "=r"(got), "=r"(block) : "r"(sm + T::ANSWER) : "memory");
+                __syncwarp();
+                more = got != 0u;
+            }
+            // whoever gave up: what is in flight lands before the block ends
+            if (lane == 0) {
+                for (uint32_t i = n > T::SLOTS ? n - T::SLOTS : 0; i < n; ++i)
+                    mbar_wait(sm + T::FULL + 8 * (i % T::SLOTS), (i / T::SLOTS) & 1u, PT_WAIT_LIMIT);
+                if (queries) mbar_wait(sm + T::Q, (queries - 1u) & 1u, PT_WAIT_LIMIT);
+                if (asked) mbar_wait(sm + T::NEXT, (asked - 1u) & 1u, PT_WAIT_LIMIT);
             }
             __syncwarp();
         } else if (warp == 8) {
@@ -413,8 +495,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             // in all lanes as far as the compiler can see, and one lane issues: the operands' descriptors
             // are then formed in uniform registers.  (In a branch of one lane each product costs 130
             // cycles instead of 65.)
-            const int tiles = __shfl_sync(0xffffffffu, nt, 0);
-            const bool two = __shfl_sync(0xffffffffu, halves, 0) == 2;
             const uint32_t kind_s = tc_kind(128) | (a.negative ? TC_NEGATE_A : 0u), kind_o = tc_kind(D) | TC_B_BY_ROWS;
             auto scores = [&](uint32_t half, uint32_t at) {  // S = Q K^T
                 const uint64_t qd = tc_operand(sm + T::OFF_Q + half * T::BYTES, 16);
@@ -437,100 +517,139 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 tc_after();
                 return ok;
             };
-            bool ok = tiles > 0 && wait(T::Q, 0, PT_WAIT_LIMIT) && wait(T::FULL, 0, a.polls);
-            if (ok && elect()) {
-                scores(0, 0);
-                if (two) scores(1, 0);
-                tc_commit(sm + T::FREE);
-            }
-            __syncwarp();
-            uint32_t v_at = 1;  // V_j's place in the ring
-            for (int j = 0; ok && j < tiles; ++j) {
-                const bool more = j + 1 < tiles;
-                const uint32_t k_at = v_at + 1 == T::SLOTS ? 0 : v_at + 1;
-                if (!(ok = wait(T::P, j & 1, PT_WAIT_LIMIT))) break;
-                if (elect()) values(0, v_at, 0, j > 0);
-                __syncwarp();
-                if (!(ok = wait(T::P + 8, j & 1, PT_WAIT_LIMIT))) break;
+            bool ok = true;
+            uint32_t at = 0, round = 0;                           // the next tile's place in the ring, its round's parity
+            uint32_t queries = 0, done0 = 0, done1 = 0;           // parities of the queries and of the halves' tiles
+            auto forward = [&]() {
+                if (++at == T::SLOTS) at = 0, round ^= 1u;
+            };
+            PromptWork w;
+            for (uint32_t k = 0; next_work(k, w); ++k) {
+                const int tiles = __shfl_sync(0xffffffffu, w.nt, 0);
+                const bool two = __shfl_sync(0xffffffffu, w.count, 0) > a.half_tokens;
+                if (tiles == 0) continue;
+                if (!(ok = wait(T::Q, queries, PT_WAIT_LIMIT) && wait(T::FULL + 8 * at, round, a.polls))) break;
+                queries ^= 1u;
                 if (elect()) {
-                    values(0, v_at, 1, true);
-                    if (!two) tc_commit(sm + T::FREE + 8 * v_at);
-                    if (more) {
-                        scores(0, k_at);
-                        if (!two) tc_commit(sm + T::FREE + 8 * k_at);
-                    } else {
-                        tc_commit(sm + T::O);
-                    }
+                    scores(0, at);
+                    if (two) scores(1, at);
+                    tc_commit(sm + T::FREE + 8 * at);
+                    if (tiles == 1) tc_commit(sm + T::QFREE);
                 }
                 __syncwarp();
-                if (two) {
-                    if (!(ok = wait(T::P + 16, j & 1, PT_WAIT_LIMIT))) break;
-                    if (elect()) values(1, v_at, 0, j > 0);
+                forward();
+                for (int j = 0; j < tiles; ++j) {
+                    const bool more = j + 1 < tiles, last_scores = j + 2 == tiles;
+                    const uint32_t v_at = at;
+                    forward();
+                    const uint32_t k_at = at;  // (of the next tile, if there is one)
+                    if (!(ok = wait(T::P, done0, PT_WAIT_LIMIT))) break;
+                    if (elect()) values(0, v_at, 0, j > 0);
                     __syncwarp();
-                    if (!(ok = wait(T::P + 24, j & 1, PT_WAIT_LIMIT))) break;
+                    if (!(ok = wait(T::P + 8, done0, PT_WAIT_LIMIT))) break;
                     if (elect()) {
-                        values(1, v_at, 1, true);
-                        tc_commit(sm + T::FREE + 8 * v_at);
+                        values(0, v_at, 1, true);
+                        if (!two) tc_commit(sm + T::FREE + 8 * v_at);
                         if (more) {
-                            scores(1, k_at);
-                            tc_commit(sm + T::FREE + 8 * k_at);
+                            scores(0, k_at);
+                            if (!two) {
+                                tc_commit(sm + T::FREE + 8 * k_at);
+                                if (last_scores) tc_commit(sm + T::QFREE);
+                            }
                         } else {
-                            tc_commit(sm + T::O + 8);
+                            tc_commit(sm + T::O);
                         }
                     }
                     __syncwarp();
+                    done0 ^= 1u;
+                    if (two) {
+                        if (!(ok = wait(T::P + 16, done1, PT_WAIT_LIMIT))) break;
+                        if (elect()) values(1, v_at, 0, j > 0);
+                        __syncwarp();
+                        if (!(ok = wait(T::P + 24, done1, PT_WAIT_LIMIT))) break;
+                        if (elect()) {
+                            values(1, v_at, 1, true);
+                            tc_commit(sm + T::FREE + 8 * v_at);
+                            if (more) {
+                                scores(1, k_at);
+                                tc_commit(sm + T::FREE + 8 * k_at);
+                                if (last_scores) tc_commit(sm + T::QFREE);
+                            } else {
+                                tc_commit(sm + T::O + 8);
+                            }
+                        }
+                        __syncwarp();
+                        done1 ^= 1u;
+                    }
+                    if (more) forward();
                 }
-                v_at = k_at + 1 == T::SLOTS ? 0 : k_at + 1;
+                if (!ok) break;
             }
-            if (!ok && tiles > 0) {  // nothing may be in flight when TMEM is given back
-                if (elect()) tc_commit(sm + T::DONE);
-                __syncwarp();
-                mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
-            }
+            // (a block that gave up: nothing may be in flight when TMEM is given back)
+            if (elect()) tc_commit(sm + T::DONE);
+            __syncwarp();
+            mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
             __syncwarp();
         } else if (warp == 10) {
             // --- what the products wait for beside the softmax: the copies of V_j and K_{j+1}, as one
             // more arrival at the first half's barriers (a wait costs the others some 100 cycles even
             // if there is nothing to wait for)
-            if (lane == 0) {
-                auto there = [&](uint32_t n) { return pt_wait(a, sm + T::FULL + 8 * (n % T::SLOTS), (n / T::SLOTS) & 1, dead, a.polls); };
-                for (int j = 0; j < nt; ++j) {
-                    const uint32_t n = 2u * uint32_t(j) + 1u;
-                    const bool more = j + 1 < nt;
-                    if (!there(n)) break;
-                    mbar_arrive(sm + T::P);
-                    if (more && !there(n + 1)) break;
-                    mbar_arrive(sm + T::P + 8);
-                    if (!pt_wait(a, sm + T::P + 8, uint32_t(j) & 1, dead, PT_WAIT_LIMIT)) break;
+            uint32_t n = 0, done = 0;
+            auto there = [&](uint32_t i) {
+                const RingPlace of = ring_place<T::SLOTS>(i);
+                return __all_sync(0xffffffffu, pt_wait(a, sm + T::FULL + 8 * of.at, of.parity, dead, a.polls));
+            };
+            PromptWork w;
+            bool ok = true;
+            for (uint32_t k = 0; ok && next_work(k, w); ++k) {
+                for (int j = 0; j < w.nt; ++j, n += 2) {
+                    const bool more = j + 1 < w.nt;
+                    if (!(ok = there(n + 1))) break;
+                    if (lane == 0) mbar_arrive(sm + T::P);
+                    if (more && !(ok = there(n + 2))) break;
+                    if (lane == 0) mbar_arrive(sm + T::P + 8);
+                    if (!(ok = warp_wait(a, sm + T::P + 8, done, dead))) break;
+                    done ^= 1u;
                 }
             }
-            __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_MORE));
-        if (warp < 4 * halves) {
-            // --- softmax: a thread a row
-            const int half = warp >> 2, r = tid & 127;
-            const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's 32 lanes of TMEM
-            const uint32_t s_at = uint32_t(half) * 128u + lanes, o_at = 256u + uint32_t(half) * D + lanes;
-            const int tl = r / a.G, i = i0 + half * a.half_tokens + tl;
-            const bool real = tl < a.half_tokens && i < s.n;
-            const int p = real ? s.T - s.n + i : p_last;
+        // --- softmax: a thread a row
+        const int half = warp >> 2, r = tid & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's 32 lanes of TMEM
+        const uint32_t s_at = uint32_t(half) * 128u + lanes, o_at = 256u + uint32_t(half) * D + lanes;
+        const int tl = r / a.G, i = half * a.half_tokens + tl;  // the row's token
+        bool ok = true;
+        uint32_t n = 0, done = 0, ended = 0;  // ring places before this work's; parities of the half's tiles and results
+        PromptWork w;
+        // Whether any thread of the half says so.  What ends a half's work is decided by all of its
+        // warps: one that gave up by itself would be missing from the others' barriers.
+        auto any_of_half = [&](bool says) {
+            uint32_t any;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+                         : "=r"(any) : "r"(uint32_t(says)), "r"(1 + half) : "memory");
+            return any != 0u;
+        };
+        for (uint32_t k = 0; !any_of_half(!next_work(k, w)); n += 2u * uint32_t(w.nt), ++k) {
+            if (half == 1 && w.count <= a.half_tokens) continue;
+            const bool real = tl < a.half_tokens && i < w.count;
+            const int p = w.p_first + (real ? i : w.count - 1);
             float ref = -INFINITY, sum = 0.0f;
-            bool ok = true, met = false;  // met: Inf or NaN
+            bool met = false;  // Inf or NaN
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
             int in0 = 0, in1 = 0;
             if (!a.flat) {
-                const int64_t old = a.window ? int64_t(p_last) - a.window + 1 - keys.b0 : 0;
-                in0 = keys.na - keys.j0 + int((max(old, int64_t(0)) + PT_KEYS - 1) / PT_KEYS);
-                in1 = keys.na - keys.j0 + max(p_first + 1 - keys.b0, 0) / PT_KEYS;
+                const int64_t old = a.window ? int64_t(w.p_last()) - a.window + 1 - w.b0 : 0;
+                in0 = w.na - w.j0 + int((max(old, int64_t(0)) + PT_KEYS - 1) / PT_KEYS);
+                in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
             }
-            for (int j = 0; j < nt; ++j) {
+            for (int j = 0; j < w.nt; ++j) {
                 const bool inner = j >= in0 && j < in1;
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // the columns that the row sees, as bits
                 if (!inner) {
                     int t0, end;
-                    keys.tile(keys.j0 + j, t0, end);
+                    w.tile(j, t0, end);
                     {
                         const int last = min(end - 1, p) - t0;
                         const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
@@ -541,11 +660,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                     // Values that not all rows see, while the scores are under way.
                     const bool rest = end < t0 + PT_KEYS;
-                    const bool part = end - 1 > p_first || (a.window && t0 <= int64_t(p_last) - a.window && end > a.sinks);
+                    const bool part = end - 1 > w.p_first || (a.window && t0 <= int64_t(w.p_last()) - a.window && end > a.sinks);
                     if (rest || part) {
-                        const uint32_t n = 2u * uint32_t(j) + 1u, at = n % T::SLOTS;
-                        const uint32_t tile = sm + T::OFF_RING + at * T::BYTES;
-                        if (!warp_wait(a, sm + T::FULL + 8 * at, (n / T::SLOTS) & 1, dead)) {
+                        const RingPlace of = ring_place<T::SLOTS>(n + 2u * uint32_t(j) + 1u);
+                        const uint32_t tile = sm + T::OFF_RING + of.at * T::BYTES;
+                        if (!warp_wait(a, sm + T::FULL + 8 * of.at, of.parity, dead)) {
                             ok = false;
                             break;
                         }
@@ -578,7 +697,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                         }
                     }
                 }
-                if (!warp_wait(a, sm + T::S + 8 * uint32_t(half), uint32_t(j) & 1, dead)) {
+                if (!warp_wait(a, sm + T::S + 8 * uint32_t(half), done, dead)) {
                     ok = false;
                     break;
                 }
@@ -646,29 +765,29 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
                 }
                 sum = (t0.x + t0.y) + (t1.x + t1.y);
+                done ^= 1u;
             }
-            if (ok && nt > 0) {
-                ok = warp_wait(a, sm + T::O + 8 * uint32_t(half), 0, dead);
+            if (ok && w.nt > 0) {
+                ok = warp_wait(a, sm + T::O + 8 * uint32_t(half), ended, dead);
+                ended ^= 1u;
                 tc_after();
             }
-            // whether a thread of the half has met Inf or NaN
-            uint32_t odd;
-            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
-                         : "=r"(odd) : "r"(uint32_t(met)), "r"(1 + half) : "memory");
-            if (ok && !odd) {
-                const uint64_t row = uint64_t(s.first + i) * uint32_t(a.nq) + uint32_t(h * a.G + r - tl * a.G);
+            const bool odd = any_of_half(met || !ok);
+            if (odd && any_of_half(!ok)) break;
+            if (!odd) {
+                const uint64_t row = uint64_t(w.row + i) * uint32_t(a.nq) + uint32_t(w.h * a.G + r - tl * a.G);
                 float2 f = make_float2(1.0f, 0.0f);
                 float inv = 1.0f;
                 if (real && a.splits == 1) {
                     f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
                     inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
                 } else if (real) {
-                    a.stats[uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
+                    a.stats[uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
                 }
-                // By way of shared memory (the half's queries, which nothing reads any more), 128 bytes
+                // By way of shared memory, 128 bytes
                 // of a row at a time: eight lanes then store a row's 128 bytes at once.  (Each thread
                 // its own row's 16 bytes at a time: 4.0 us a block of 256 rows of 128, 1.0 so.)
-                const uint32_t stage = sm + T::OFF_Q + uint32_t(warp) * 4096u;
+                const uint32_t stage = sm + T::OFF_STAGE + uint32_t(warp) * 4096u;
                 const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
                 auto store = [&](const uint32_t (&w)[32], uint8_t *to, uint32_t row_bytes, uint32_t column) {
 #pragma unroll
@@ -690,7 +809,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     __syncwarp();
                 };
                 auto load = [&](int c, uint32_t *o) {
-                    if (nt > 0) {
+                    if (w.nt > 0) {
                         tc_ld32(o_at + uint32_t(c), o);
                         tc_wait_ld();
                         tc_landed(o), tc_landed(o + 16);
@@ -700,7 +819,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                 };
                 if (a.splits > 1) {
-                    uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) * D);
+                    uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) * D);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
@@ -732,29 +851,29 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                         store(w, reinterpret_cast<uint8_t *>(a.out), D * 2u, uint32_t(c) * 2u);
                     }
                 }
-            } else if (ok) {
-                // row by row
+            } else {
+                // Inf or NaN among values that some row does not see: row by row
                 constexpr int VPL = D / 32;
                 for (int k = 0; k < 32; ++k) {
-                    const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = i0 + half * a.half_tokens + t, jj = h * a.G + rr - t * a.G;
-                    if (t >= a.half_tokens || ii >= s.n) break;
+                    const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = half * a.half_tokens + t, jj = w.h * a.G + rr - t * a.G;
+                    if (t >= a.half_tokens || ii >= w.count) break;
                     float q[VPL], acc[VPL];
                     ref = -INFINITY, sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < VPL; ++e) {
-                        q[e] = __uint_as_float(uint32_t(a.q[(s.first + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
+                        q[e] = __uint_as_float(uint32_t(a.q[(w.row + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
                         acc[e] = 0.0f;
                     }
-                    const uint16_t *kr = a.k + s.k_first * a.k_ts + h * a.k_hs, *vr = a.v + s.k_first * a.v_ts + h * a.v_hs;
-                    const int place = s.T - s.n + ii, ja = min(keys.j1, keys.na), jb = max(keys.j0, keys.na);
-                    if (keys.j0 < ja)
-                        row_keys<D>(a, q, kr, vr, place, int64_t(keys.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(keys.a_end)), acc, ref, sum);
-                    if (jb < keys.j1)
-                        row_keys<D>(a, q, kr, vr, place, keys.b0 + int64_t(jb - keys.na) * PT_KEYS,
-                                    min(keys.b0 + int64_t(keys.j1 - keys.na) * PT_KEYS, int64_t(keys.b_end)), acc, ref, sum);
-                    const uint64_t row = uint64_t(s.first + ii) * uint32_t(a.nq) + uint32_t(jj);
+                    const uint16_t *kr = a.k + w.k_first * a.k_ts + w.h * a.k_hs, *vr = a.v + w.k_first * a.v_ts + w.h * a.v_hs;
+                    const int place = w.p_first + ii, j1 = w.j0 + w.nt, ja = min(j1, w.na), jb = max(w.j0, w.na);
+                    if (w.j0 < ja)
+                        row_keys<D>(a, q, kr, vr, place, int64_t(w.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(w.a_end)), acc, ref, sum);
+                    if (jb < j1)
+                        row_keys<D>(a, q, kr, vr, place, w.b0 + int64_t(jb - w.na) * PT_KEYS,
+                                    min(w.b0 + int64_t(j1 - w.na) * PT_KEYS, int64_t(w.b_end)), acc, ref, sum);
+                    const uint64_t row = uint64_t(w.row + ii) * uint32_t(a.nq) + uint32_t(jj);
                         if (a.splits > 1) {
-                        const uint64_t at = uint64_t(split) * uint32_t(a.n) * uint32_t(a.nq) + row;
+                        const uint64_t at = uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) + row;
                         if (lane == 0) a.stats[at] = make_float2(ref, sum);
 #pragma unroll
                         for (int e = 0; e < VPL; ++e) a.part[at * D + lane * VPL + e] = acc[e];
@@ -763,8 +882,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                 }
             }
-            tc_before();
+            __syncwarp();
         }
+        tc_before();
     }
     __syncthreads();
     if (warp == 8) {
@@ -779,6 +899,8 @@ __global__ void __launch_bounds__(256) prompt_join_parts(const __grid_constant__
     constexpr int VPL = D / 32;
     const int lane = threadIdx.x & 31;
     const uint64_t rows = uint64_t(a.n) * uint32_t(a.nq);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint64_t row = uint64_t(blockIdx.x) * 8u + (threadIdx.x >> 5);
     if (row >= rows) return;
     const int tok = int(row / uint32_t(a.nq));
@@ -796,7 +918,7 @@ __global__ void __launch_bounds__(256) prompt_join_parts(const __grid_constant__
     float M = -INFINITY, L = 0.0f, acc[VPL];
 #pragma unroll
     for (int e = 0; e < VPL; ++e) acc[e] = 0.0f;
-    for (int c = 0; c < a.splits; ++c) M = fmaxf(M, a.stats[c * rows + row].x);
+    for (int c = 0; c < a.splits; ++c) M = fmaxf(M, __uint_as_float(ld_plain_u32(&a.stats[c * rows + row].x)));
     for (int c = 0; c < a.splits; ++c) {
         const float2 st = a.stats[c * rows + row];
         if (st.x == -INFINITY && st.y == 0.0f) continue;  // an empty part
@@ -885,11 +1007,23 @@ static int launch_prompt(const PromptArgs &a, unsigned grid, cudaStream_t st) {
             return KVP_ERR_CUDA;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
-    prompt_attend<D><<<grid, PT_THREADS, PromptTile<D>::SMEM, st>>>(a);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(PT_THREADS);
+    cfg.dynamicSmemBytes = PromptTile<D>::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, prompt_attend<D>, a) != cudaSuccess) return KVP_ERR_CUDA;
     count_launch();
     if (a.splits > 1) {
-        const uint64_t rows = uint64_t(a.n) * uint64_t(a.nq);
-        prompt_join_parts<D><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+        cfg.gridDim = dim3(unsigned((uint64_t(a.n) * uint64_t(a.nq) + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, prompt_join_parts<D>, a) != cudaSuccess) return KVP_ERR_CUDA;
         count_launch();
     }
     return launch_status();
