@@ -264,8 +264,8 @@ struct PromptTile {
     static constexpr uint32_t SMEM = OFF_STAGE + 8 * 4096 + 1024;    // and the base's alignment
     static_assert(SMEM <= 232448, "shared memory of a block");
     // barriers, 8 bytes each, and what else lies before the queries
-    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, QFREE = 136, S = 144, P = 160, O = 192, DONE = 208, WORK = 216,
-                              READ = 232, NEXT = 248, TMEM = 256, DEAD = 260, ANSWER = 272, ITEM = 320;
+    static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, QFREE = 136, S = 144, P = 160, O = 176, DONE = 192, WORK = 200,
+                              READ = 216, NEXT = 232, TMEM = 240, DEAD = 244, ANSWER = 256, ITEM = 320;
 };
 
 // A piece of work: 256 rows (or fewer) of one sequence and KV head, and the keys that some
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init_n(sm + T::S + 8 * i, 1), mbar_init_n(sm + T::O + 8 * i, 1);
             // an arrival a warp, and in the first half the one of those who see to the copies
-            mbar_init_n(sm + T::P + 16 * i, i ? 4 : 5), mbar_init_n(sm + T::P + 16 * i + 8, i ? 4 : 5);
+            mbar_init_n(sm + T::P + 8 * i, i ? 4 : 5);
             mbar_init_n(sm + T::WORK + 8 * i, 1), mbar_init_n(sm + T::READ + 8 * i, 10);  // by warps 0-8 and 10
         }
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(dead), "r"(0u) : "memory");
@@ -506,10 +506,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 }
                 tc_commit(sm + T::S + 8 * half);
             };
-            auto values = [&](uint32_t half, uint32_t at, int u, bool add) {  // O += P V, 64 keys
+            auto values = [&](uint32_t half, uint32_t at, bool add) {  // O += P V
                 const uint64_t vd = tc_operand(sm + T::OFF_RING + at * T::BYTES, T::CHUNK);
 #pragma unroll
-                for (int k = 4 * u; k < 4 * u + 4; ++k)
+                for (int k = 0; k < PT_KEYS / 16; ++k)
                     tc_mma_ts(256u + half * D, half * 128u + 8u * uint32_t(k), vd + uint64_t(k * 2048 >> 4), kind_o, add || k > 0);
             };
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t limit) {
@@ -544,11 +544,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     forward();
                     const uint32_t k_at = at;  // (of the next tile, if there is one)
                     if (!(ok = wait(T::P, done0, PT_WAIT_LIMIT))) break;
-                    if (elect()) values(0, v_at, 0, j > 0);
-                    __syncwarp();
-                    if (!(ok = wait(T::P + 8, done0, PT_WAIT_LIMIT))) break;
                     if (elect()) {
-                        values(0, v_at, 1, true);
+                        values(0, v_at, j > 0);
                         if (!two) tc_commit(sm + T::FREE + 8 * v_at);
                         if (more) {
                             scores(0, k_at);
@@ -563,12 +560,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     __syncwarp();
                     done0 ^= 1u;
                     if (two) {
-                        if (!(ok = wait(T::P + 16, done1, PT_WAIT_LIMIT))) break;
-                        if (elect()) values(1, v_at, 0, j > 0);
-                        __syncwarp();
-                        if (!(ok = wait(T::P + 24, done1, PT_WAIT_LIMIT))) break;
+                        if (!(ok = wait(T::P + 8, done1, PT_WAIT_LIMIT))) break;
                         if (elect()) {
-                            values(1, v_at, 1, true);
+                            values(1, v_at, j > 0);
                             tc_commit(sm + T::FREE + 8 * v_at);
                             if (more) {
                                 scores(1, k_at);
@@ -605,10 +599,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 for (int j = 0; j < w.nt; ++j, n += 2) {
                     const bool more = j + 1 < w.nt;
                     if (!(ok = there(n + 1))) break;
-                    if (lane == 0) mbar_arrive(sm + T::P);
                     if (more && !(ok = there(n + 2))) break;
-                    if (lane == 0) mbar_arrive(sm + T::P + 8);
-                    if (!(ok = warp_wait(a, sm + T::P + 8, done, dead))) break;
+                    if (lane == 0) mbar_arrive(sm + T::P);
+                    if (!(ok = warp_wait(a, sm + T::P, done, dead))) break;
                     done ^= 1u;
                 }
             }
@@ -759,11 +752,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                         x[c] = pack_bf16x2(y.x, y.y);
                     }
                     tc_st32(s_at + 32u * uint32_t(u), x + 32 * u);
-                    tc_wait_st();
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sm + T::P + 16 * uint32_t(half) + 8 * uint32_t(u));
                 }
+                tc_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm + T::P + 8 * uint32_t(half));
                 sum = (t0.x + t0.y) + (t1.x + t1.y);
                 done ^= 1u;
             }
