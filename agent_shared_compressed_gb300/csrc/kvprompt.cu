@@ -48,6 +48,7 @@ constexpr int PT_KEYS = 128;                  // keys of a tile
 // Three warpgroups: 384 threads start with 168 registers each (64512 of the SM's), the third
 // gives 80 of its back and each of the others takes 40 more: 2 * 128 * 208 + 128 * 88 = 64512.
 constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
+constexpr int PT_MOST = 1 << 30;              // rows: sums and differences of places fit 32 bits
 constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f;
 
@@ -235,6 +236,12 @@ __device__ __forceinline__ bool elect() {
     return r != 0u;
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    uint32_t r;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+    return r;
+}
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -265,7 +272,8 @@ struct PromptTile {
     static_assert(SMEM <= 232448, "shared memory of a block");
     // barriers, 8 bytes each, and what else lies before the queries
     static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, QFREE = 136, S = 144, P = 160, O = 176, DONE = 192, WORK = 200,
-                              READ = 216, NEXT = 232, TMEM = 240, DEAD = 244, ANSWER = 256, ITEM = 320;
+                              READ = 216, NEXT = 232, TMEM = 240, DEAD = 244, ANSWER = 256, ODD = 272,
+                              ITEM = 320;
 };
 
 // A piece of work: 256 rows (or fewer) of one sequence and KV head, and the keys that some
@@ -284,7 +292,7 @@ struct alignas(16) PromptWork {
         if (j < na)
             t0 = j * PT_KEYS, end = min(t0 + PT_KEYS, a_end);
         else
-            t0 = b0 + (j - na) * PT_KEYS, end = int(min(int64_t(t0) + PT_KEYS, int64_t(b_end)));
+            t0 = b0 + (j - na) * PT_KEYS, end = min(t0 + PT_KEYS, b_end);
     }
 };
 static_assert(sizeof(PromptWork) == 64, "four 16-byte loads");
@@ -311,9 +319,8 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block,
     w.row = s.first + int(i0), w.count = min(tokens, s.n - int(i0));
     w.k_first = s.k_first;
     w.p_first = s.T - s.n + int(i0);
-    auto tiles_of = [](int64_t n) { return int((n + PT_KEYS - 1) / PT_KEYS); };
-    const int64_t old = a.window ? int64_t(w.p_first) - a.window + 1 : 0;
-    w.b_end = max(w.p_last() + 1, 0), w.b0 = int(max(old, int64_t(0)));
+    auto tiles_of = [](int n) { return (n + PT_KEYS - 1) / PT_KEYS; };
+    w.b_end = max(w.p_last() + 1, 0), w.b0 = a.window ? max(w.p_first - a.window + 1, 0) : 0;
     w.a_end = min(a.sinks, w.b0);
     // no more tiles without the gap: without it
     if (tiles_of(w.b_end) <= tiles_of(w.a_end) + tiles_of(w.b_end - w.b0)) w.a_end = 0, w.b0 = 0;
@@ -585,9 +592,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             mbar_wait(sm + T::DONE, 0, PT_WAIT_LIMIT);
             __syncwarp();
         } else if (warp == 10) {
-            // --- what the products wait for beside the softmax: the copies of V_j and K_{j+1}, as one
-            // more arrival at the first half's barriers (a wait costs the others some 100 cycles even
-            // if there is nothing to wait for)
+            // --- what the products wait for beside the softmax, as one more arrival at the first
+            // half's barrier: the copies of V_j and K_{j+1} (a wait costs the others some 100 cycles
+            // even if there is nothing to wait for), and V_j in a state that no row can come to harm
+            // by: rows of a tile that nobody sees are zeroed, and where some rows see a part only it
+            // is looked over for Inf and NaN, whose product with a weight of 0 is NaN.
             uint32_t n = 0, done = 0;
             auto there = [&](uint32_t i) {
                 const RingPlace of = ring_place<T::SLOTS>(i);
@@ -596,10 +605,44 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             PromptWork w;
             bool ok = true;
             for (uint32_t k = 0; ok && next_work(k, w); ++k) {
+                // (the flag of four pieces of work before: the slowest reader is at most two behind)
+                const uint32_t odd_at = sm + T::ODD + 4u * (k & 3u);
+                if (lane == 0) asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(odd_at), "r"(0u) : "memory");
                 for (int j = 0; j < w.nt; ++j, n += 2) {
                     const bool more = j + 1 < w.nt;
                     if (!(ok = there(n + 1))) break;
+                    int t0, end;
+                    w.tile(j, t0, end);
+                    const int rows = end - t0;
+                    const uint32_t tile = sm + T::OFF_RING + ring_place<T::SLOTS>(n + 1).at * T::BYTES;
+                    constexpr int PER = D / 8, STEP = 32 / PER;  // 16-byte pieces of a row, rows of a pass
+                    const int c = lane % PER;
+                    const uint32_t mine = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;  // (in whatever place of the row)
+                    if (end - 1 > w.p_first || (a.window && t0 <= w.p_last() - a.window && end > a.sinks)) {
+                        __nv_bfloat162 odd[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) odd[e] = __float2bfloat162_rn(0.0f);
+#pragma unroll 8
+                        for (int row = lane / PER; row < PT_KEYS; row += STEP) {
+                            uint32_t v[4] = {0u, 0u, 0u, 0u};
+                            if (row < rows)
+                                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(mine + uint32_t(row) * 128u) : "memory");
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                odd[e] = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v[e]), __float2bfloat162_rn(0.0f), odd[e]);
+                        }
+                        odd[0] = __hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3]));
+                        if (*reinterpret_cast<uint32_t *>(&odd[0]) & 0x7FFF7FFFu)
+                            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(odd_at), "r"(1u) : "memory");
+                    }
+                    if (rows < PT_KEYS) {
+                        for (int row = rows + lane / PER; row < PT_KEYS; row += STEP)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(mine + uint32_t(row) * 128u), "r"(0u) : "memory");
+                        fence_proxy_async();
+                    }
                     if (more && !(ok = there(n + 2))) break;
+                    __syncwarp();
                     if (lane == 0) mbar_arrive(sm + T::P);
                     if (!(ok = warp_wait(a, sm + T::P, done, dead))) break;
                     done ^= 1u;
@@ -624,17 +667,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                          : "=r"(any) : "r"(uint32_t(says)), "r"(1 + half) : "memory");
             return any != 0u;
         };
-        for (uint32_t k = 0; !any_of_half(!next_work(k, w)); n += 2u * uint32_t(w.nt), ++k) {
+        for (uint32_t k = 0; !any_of_half(!ok || !next_work(k, w)); n += 2u * uint32_t(w.nt), ++k) {
             if (half == 1 && w.count <= a.half_tokens) continue;
             const bool real = tl < a.half_tokens && i < w.count;
             const int p = w.p_first + (real ? i : w.count - 1);
             float ref = -INFINITY, sum = 0.0f;
-            bool met = false;  // Inf or NaN
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
             int in0 = 0, in1 = 0;
             if (!a.flat) {
-                const int64_t old = a.window ? int64_t(w.p_last()) - a.window + 1 - w.b0 : 0;
-                in0 = w.na - w.j0 + int((max(old, int64_t(0)) + PT_KEYS - 1) / PT_KEYS);
+                in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
                 in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
             }
             for (int j = 0; j < w.nt; ++j) {
@@ -643,52 +684,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 if (!inner) {
                     int t0, end;
                     w.tile(j, t0, end);
-                    {
-                        const int last = min(end - 1, p) - t0;
-                        const int64_t from = a.window ? int64_t(p) - a.window + 1 - t0 : 0, first = int64_t(a.sinks) - t0;
-                        const int f0 = int(min(max(from, int64_t(0)), int64_t(128))), f1 = int(min(max(first, int64_t(0)), int64_t(128)));
-                        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };
+                    const int last = min(end - 1, p) - t0, from = a.window ? p - a.window + 1 - t0 : 0, first = a.sinks - t0;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) see[w] = below(last + 1 - 32 * w) & (~below(f0 - 32 * w) | below(f1 - 32 * w));
-                    }
-                    // Values that not all rows see, while the scores are under way.
-                    const bool rest = end < t0 + PT_KEYS;
-                    const bool part = end - 1 > w.p_first || (a.window && t0 <= int64_t(w.p_last()) - a.window && end > a.sinks);
-                    if (rest || part) {
-                        const RingPlace of = ring_place<T::SLOTS>(n + 2u * uint32_t(j) + 1u);
-                        const uint32_t tile = sm + T::OFF_RING + of.at * T::BYTES;
-                        if (!warp_wait(a, sm + T::FULL + 8 * of.at, of.parity, dead)) {
-                            ok = false;
-                            break;
-                        }
-                        if (part) {
-                            // Inf and NaN times 0 are NaN.  Each half looks for itself, a thread at 16 bytes of
-                            // every eighth or sixteenth row (in whatever place of the row)
-                            constexpr int PER = D / 8, STEP = 128 / PER;  // 16-byte pieces of a row, rows of a pass
-                            const int c = r % PER;
-                            const uint32_t from = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;
-                            __nv_bfloat162 odd = __float2bfloat162_rn(0.0f);
-#pragma unroll 8
-                            for (int k = r / PER; k < PT_KEYS; k += STEP) {
-                                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                                if (k < end - t0)
-                                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + uint32_t(k) * 128u) : "memory");
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&w[e]), __float2bfloat162_rn(0.0f), odd);
-                            }
-                            met |= (*reinterpret_cast<uint32_t *>(&odd) & 0x7FFF7FFFu) != 0u;
-                        }
-                        if (rest) {
-                            for (int k = r; k < (t0 + PT_KEYS - end) * (D / 8); k += 128) {
-                                const uint32_t row = uint32_t(end - t0 + k / (D / 8)), c = uint32_t(k % (D / 8));
-                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};"
-                                             ::"r"(tile + c / 8u * T::CHUNK + row * 128u + c % 8u * 16u), "r"(0u) : "memory");
-                            }
-                            fence_proxy_async();
-                        }
-                    }
+                    for (int c = 0; c < 4; ++c) see[c] = bits_below(last + 1 - 32 * c) & (~bits_below(from - 32 * c) | bits_below(first - 32 * c));
                 }
                 if (!warp_wait(a, sm + T::S + 8 * uint32_t(half), done, dead)) {
                     ok = false;
@@ -765,83 +763,102 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 ended ^= 1u;
                 tc_after();
             }
-            const bool odd = any_of_half(met || !ok);
-            if (odd && any_of_half(!ok)) break;
-            if (!odd) {
+            uint32_t odd;  // whether there are Inf or NaN among values that some row does not see
+            asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sm + T::ODD + 4u * (k & 3u)) : "memory");
+            if (!ok) {
+            } else if (!odd || w.nt == 0) {
                 const uint64_t row = uint64_t(w.row + i) * uint32_t(a.nq) + uint32_t(w.h * a.G + r - tl * a.G);
-                float2 f = make_float2(1.0f, 0.0f);
-                float inv = 1.0f;
-                if (real && a.splits == 1) {
-                    f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
-                    inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-                } else if (real) {
-                    a.stats[uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) + row] = make_float2(ref, sum);
-                }
-                // By way of shared memory, 128 bytes
-                // of a row at a time: eight lanes then store a row's 128 bytes at once.  (Each thread
-                // its own row's 16 bytes at a time: 4.0 us a block of 256 rows of 128, 1.0 so.)
+                // By way of shared memory, 64 bytes of a row (parts: 128) at a time, which four (eight)
+                // lanes then store at once.  (Each thread its own row's 16 bytes at a time: 4.0 us a
+                // block of 256 rows of 128.)  The code is short, as it is met with once a block and has
+                // to be fetched for that.
                 const uint32_t stage = sm + T::OFF_STAGE + uint32_t(warp) * 4096u;
                 const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
-                auto store = [&](const uint32_t (&w)[32], uint8_t *to, uint32_t row_bytes, uint32_t column) {
-#pragma unroll
-                    for (uint32_t e = 0; e < 8; ++e)
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-                                     ::"r"(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u), "r"(w[4 * e]), "r"(w[4 * e + 1]),
-                                       "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
-                    __syncwarp();
-#pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k) {
-                        const uint32_t from = 4u * k + (uint32_t(lane) >> 3), e = uint32_t(lane) & 7u;
-                        uint4 v;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(stage + from * 128u + (e ^ (from & 7u)) * 16u) : "memory");
-                        const uint32_t its = __shfl_sync(0xffffffffu, at, int(from));
-                        if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes + column + e * 16u) = v;
-                    }
-                    __syncwarp();
+                auto put = [&](uint32_t to, const uint32_t *v) {
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
                 };
-                auto load = [&](int c, uint32_t *o) {
-                    if (w.nt > 0) {
-                        tc_ld32(o_at + uint32_t(c), o);
-                        tc_wait_ld();
-                        tc_landed(o), tc_landed(o + 16);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    }
+                auto move = [&](uint32_t from, uint32_t of, uint8_t *to, uint32_t row_bytes) {  // 16 bytes of lane `of`'s row
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+                    const uint32_t its = __shfl_sync(0xffffffffu, at, int(of));
+                    if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes) = v;
                 };
-                if (a.splits > 1) {
-                    uint8_t *to = reinterpret_cast<uint8_t *>(a.part + uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) * D);
+                if (a.splits == 1) {
+                    float2 f = make_float2(1.0f, 0.0f);
+                    if (real) f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
+                    const float inv = sum > 0.0f ? __frcp_rn(sum) : (sum == 0.0f ? 0.0f : sum);
+                    const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D : nullptr;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
-                        load(c, o);
-                        store(o, to, D * 4u, uint32_t(c) * 4u);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 64) {
-                        uint32_t w[32];
+                        float *of = reinterpret_cast<float *>(o);
+                        if (w.nt > 0) {
+                            tc_ld32(o_at + uint32_t(c), o);
+                            tc_wait_ld();
+                            tc_landed(o), tc_landed(o + 16);
+                        } else {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            uint32_t o[32];
-                            load(c + 32 * u, o);
-                            const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D + c + 32 * u : nullptr;
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        }
+                        float most = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            of[e] *= inv, of[e + 1] *= inv;
+                            most = max3(most, fabsf(of[e]), fabsf(of[e + 1]));
+                        }
+                        if (most > 3.3e38f) {  // near the end of bf16's range
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) of[e] = within_bf16(of[e]);
+                        }
+                        if (bo) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                float y[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) y[k] = within_bf16(__uint_as_float(o[e + k]) * inv) * f.x;
-                                if (bo) {
-                                    const float4 b4 = *reinterpret_cast<const float4 *>(bo + e);
-                                    y[0] = fmaf(f.y, b4.x, y[0]), y[1] = fmaf(f.y, b4.y, y[1]);
-                                    y[2] = fmaf(f.y, b4.z, y[2]), y[3] = fmaf(f.y, b4.w, y[3]);
-                                }
-                                w[16 * u + e / 2] = pack_bf16x2(y[0], y[1]), w[16 * u + e / 2 + 1] = pack_bf16x2(y[2], y[3]);
+                                const float4 b4 = *reinterpret_cast<const float4 *>(bo + c + e);
+                                of[e] = fmaf(f.y, b4.x, of[e] * f.x), of[e + 1] = fmaf(f.y, b4.y, of[e + 1] * f.x);
+                                of[e + 2] = fmaf(f.y, b4.z, of[e + 2] * f.x), of[e + 3] = fmaf(f.y, b4.w, of[e + 3] * f.x);
                             }
                         }
-                        store(w, reinterpret_cast<uint8_t *>(a.out), D * 2u, uint32_t(c) * 2u);
+                        const uint32_t turn = (uint32_t(lane) >> 1) & 3u;  // for the banks
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (uint32_t u = 0; u < 4; ++u) v[u] = pack_bf16x2(of[8 * e + 2 * u], of[8 * e + 2 * u + 1]);
+                            put(stage + uint32_t(lane) * 64u + (e ^ turn) * 16u, v);
+                        }
+                        __syncwarp();
+                        uint8_t *to = reinterpret_cast<uint8_t *>(a.out) + c * 2 + (lane & 3) * 16;
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            const uint32_t of_lane = 8u * e + (uint32_t(lane) >> 2);
+                            move(stage + of_lane * 64u + ((uint32_t(lane) & 3u) ^ ((of_lane >> 1) & 3u)) * 16u, of_lane, to, D * 2u);
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    const uint64_t part0 = uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq);
+                    if (real) a.stats[part0 + row] = make_float2(ref, sum);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        if (w.nt > 0) {
+                            tc_ld32(o_at + uint32_t(c), o);
+                            tc_wait_ld();
+                            tc_landed(o), tc_landed(o + 16);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        }
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e) put(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u, o + 4 * e);
+                        __syncwarp();
+                        uint8_t *to = reinterpret_cast<uint8_t *>(a.part + part0 * D + c) + (lane & 7) * 16;
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e) {
+                            const uint32_t of_lane = 4u * e + (uint32_t(lane) >> 3);
+                            move(stage + of_lane * 128u + ((uint32_t(lane) & 7u) ^ (of_lane & 7u)) * 16u, of_lane, to, D * 4u);
+                        }
+                        __syncwarp();
                     }
                 }
             } else {
@@ -931,6 +948,7 @@ static int prompt_ok(const kvp_prompt_shape *s) {
     if (s->head_dim != 64 && s->head_dim != 128) return KVP_ERR_UNSUPPORTED_D;
     if (s->n_seqs > KVP_PROMPT_MAX_SEQS || s->n_q_heads > 65536 || s->n_q_heads / s->n_kv_heads > 128) return KVP_ERR_SIZE;
     if (int64_t(s->n_q_tokens) * s->n_q_heads >= (int64_t(1) << 31)) return KVP_ERR_SIZE;
+    if (s->n_q_tokens > PT_MOST || s->n_k_tokens > PT_MOST) return KVP_ERR_SIZE;
     return KVP_OK;
 }
 
@@ -1070,7 +1088,7 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
     a.scale2 = a.flat ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
     a.nseq = shape->n_seqs, a.n = shape->n_q_tokens, a.nk = shape->n_k_tokens;
     a.nq = shape->n_q_heads, a.H = shape->n_kv_heads, a.G = a.nq / a.H;
-    a.window = window, a.sinks = sinks;
+    a.window = std::min(window, PT_MOST), a.sinks = std::min(sinks, PT_MOST);  // (no more keys than that)
     a.half_tokens = 128 / a.G;
     const PromptSplit w = prompt_split(shape);
     a.splits = w.splits;
