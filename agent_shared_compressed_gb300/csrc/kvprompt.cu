@@ -68,6 +68,7 @@ struct PromptArgs {
     int half_tokens;  // tokens of a half: 128 / G
     int tiles, splits;
     uint32_t negative, flat;  // the scale's sign; whether it is 0
+    uint32_t sectors;         // whether out and the workspace lie on 32-byte boundaries
     uint32_t polls;           // of a copy, by the warp that issues products
 };
 
@@ -95,6 +96,23 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, bool
 // The log of a row's sum of exponentials, from its sum in units of 2^(ref + PT_BIAS).
 __device__ __forceinline__ float row_lse(float ref, float sum) {
     return sum > 0.0f ? (ref + log2f(sum * 0x1p40f)) * 0.69314718055994531f : (sum == 0.0f ? -INFINITY : sum);
+}
+
+// N runs of 32 bytes to one place after the other; `whole`: it lies on a sector's boundary.
+template <int N>
+__device__ __forceinline__ void st_sectors(void *to, const uint32_t *v, uint32_t whole) {
+    uint8_t *p = static_cast<uint8_t *>(to);
+    if (whole) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                         ::"l"(p + 32 * k), "r"(v[8 * k]), "r"(v[8 * k + 1]), "r"(v[8 * k + 2]), "r"(v[8 * k + 3]), "r"(v[8 * k + 4]),
+                           "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7]) : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2 * N; ++k)
+            *reinterpret_cast<uint4 *>(p + 16 * k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
 }
 
 // A finite mean of bf16 values is not beyond bf16's largest (the rounded weights' sum
@@ -267,8 +285,7 @@ struct PromptTile {
     static constexpr uint32_t CHUNK = 128u * 128u;     // 64 dims of them
     static constexpr uint32_t SLOTS = D == 128 ? 4 : 6;
     static constexpr uint32_t OFF_Q = 1024, OFF_RING = OFF_Q + 2 * BYTES;
-    static constexpr uint32_t OFF_STAGE = OFF_RING + SLOTS * BYTES;  // 4096 bytes a softmax warp
-    static constexpr uint32_t SMEM = OFF_STAGE + 8 * 4096 + 1024;    // and the base's alignment
+    static constexpr uint32_t SMEM = OFF_RING + SLOTS * BYTES + 1024;  // and the base's alignment
     static_assert(SMEM <= 232448, "shared memory of a block");
     // barriers, 8 bytes each, and what else lies before the queries
     static constexpr uint32_t FULL = 0, FREE = 64, Q = 128, QFREE = 136, S = 144, P = 160, O = 176, DONE = 192, WORK = 200,
@@ -768,44 +785,36 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             if (!ok) {
             } else if (!odd || w.nt == 0) {
                 const uint64_t row = uint64_t(w.row + i) * uint32_t(a.nq) + uint32_t(w.h * a.G + r - tl * a.G);
-                // By way of shared memory, 64 bytes of a row (parts: 128) at a time, which four (eight)
-                // lanes then store at once.  (Each thread its own row's 16 bytes at a time: 4.0 us a
-                // block of 256 rows of 128.)  The code is short, as it is met with once a block and has
-                // to be fetched for that.
-                const uint32_t stage = sm + T::OFF_STAGE + uint32_t(warp) * 4096u;
-                const uint32_t at = real ? uint32_t(row) : 0xFFFFFFFFu;  // (below 2^31)
-                auto put = [&](uint32_t to, const uint32_t *v) {
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-                };
-                auto move = [&](uint32_t from, uint32_t of, uint8_t *to, uint32_t row_bytes) {  // 16 bytes of lane `of`'s row
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
-                    const uint32_t its = __shfl_sync(0xffffffffu, at, int(of));
-                    if (its != 0xFFFFFFFFu) *reinterpret_cast<uint4 *>(to + uint64_t(its) * row_bytes) = v;
+                // Each thread stores its own row, 32 bytes (a sector) at a time.  The code is short, as it
+                // is met with once a block and has to be fetched for that.
+                auto load = [&](int c, uint32_t *o) {
+                    if (w.nt > 0) {
+                        tc_ld32(o_at + uint32_t(c), o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
                 };
                 if (a.splits == 1) {
                     float2 f = make_float2(1.0f, 0.0f);
+                    uint32_t o[32];
+                    load(0, o);
                     if (real) f = prompt_join(a, row, row_lse(ref, sum), a.base_lse ? a.base_lse[row] : -INFINITY, true);
                     const float inv = sum > 0.0f ? __frcp_rn(sum) : (sum == 0.0f ? 0.0f : sum);
                     const float *bo = real && a.base_out && f.y != 0.0f ? a.base_out + row * D : nullptr;
+                    uint16_t *to = a.out + row * D;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        float *of = reinterpret_cast<float *>(o);
-                        if (w.nt > 0) {
-                            tc_ld32(o_at + uint32_t(c), o);
-                            tc_wait_ld();
-                            tc_landed(o), tc_landed(o + 16);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = 0u;
-                        }
+                        float of[32];
+                        tc_wait_ld();
+                        tc_landed(o), tc_landed(o + 16);
                         float most = 0.0f;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            of[e] *= inv, of[e + 1] *= inv;
+                            of[e] = __uint_as_float(o[e]) * inv, of[e + 1] = __uint_as_float(o[e + 1]) * inv;
                             most = max3(most, fabsf(of[e]), fabsf(of[e + 1]));
                         }
+                        if (c + 32 < D) load(c + 32, o);
                         if (most > 3.3e38f) {  // near the end of bf16's range
 #pragma unroll
                             for (int e = 0; e < 32; ++e) of[e] = within_bf16(of[e]);
@@ -818,46 +827,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                                 of[e + 2] = fmaf(f.y, b4.z, of[e + 2] * f.x), of[e + 3] = fmaf(f.y, b4.w, of[e + 3] * f.x);
                             }
                         }
-                        const uint32_t turn = (uint32_t(lane) >> 1) & 3u;  // for the banks
+                        uint32_t v[16];
 #pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (uint32_t u = 0; u < 4; ++u) v[u] = pack_bf16x2(of[8 * e + 2 * u], of[8 * e + 2 * u + 1]);
-                            put(stage + uint32_t(lane) * 64u + (e ^ turn) * 16u, v);
-                        }
-                        __syncwarp();
-                        uint8_t *to = reinterpret_cast<uint8_t *>(a.out) + c * 2 + (lane & 3) * 16;
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) {
-                            const uint32_t of_lane = 8u * e + (uint32_t(lane) >> 2);
-                            move(stage + of_lane * 64u + ((uint32_t(lane) & 3u) ^ ((of_lane >> 1) & 3u)) * 16u, of_lane, to, D * 2u);
-                        }
+                        for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(of[2 * e], of[2 * e + 1]);
+                        if (real) st_sectors<2>(to + c, v, a.sectors);
                         __syncwarp();
                     }
                 } else {
-                    const uint64_t part0 = uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq);
-                    if (real) a.stats[part0 + row] = make_float2(ref, sum);
+                    const uint64_t at = uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) + row;
+                    if (real) a.stats[at] = make_float2(ref, sum);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
-                        if (w.nt > 0) {
-                            tc_ld32(o_at + uint32_t(c), o);
-                            tc_wait_ld();
-                            tc_landed(o), tc_landed(o + 16);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = 0u;
-                        }
-#pragma unroll
-                        for (uint32_t e = 0; e < 8; ++e) put(stage + uint32_t(lane) * 128u + (e ^ (uint32_t(lane) & 7u)) * 16u, o + 4 * e);
-                        __syncwarp();
-                        uint8_t *to = reinterpret_cast<uint8_t *>(a.part + part0 * D + c) + (lane & 7) * 16;
-#pragma unroll
-                        for (uint32_t e = 0; e < 8; ++e) {
-                            const uint32_t of_lane = 4u * e + (uint32_t(lane) >> 3);
-                            move(stage + of_lane * 128u + ((uint32_t(lane) & 7u) ^ (of_lane & 7u)) * 16u, of_lane, to, D * 4u);
-                        }
+                        load(c, o);
+                        tc_wait_ld();
+                        tc_landed(o), tc_landed(o + 16);
+                        if (real) st_sectors<4>(a.part + at * D + c, o, a.sectors);
                         __syncwarp();
                     }
                 }
@@ -1103,6 +1088,7 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
         !rows_map(&a.k_map, some ? k : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS) ||
         !rows_map(&a.v_map, some ? v : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS))
         return KVP_ERR_CUDA;
+    a.sectors = aligned(out, 32) && aligned(ws, 32);
     a.polls = g_limit_next ? g_next_polls : PT_WAIT_LIMIT;
     g_limit_next = false;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
