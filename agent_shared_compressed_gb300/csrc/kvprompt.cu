@@ -941,18 +941,33 @@ static int prompt_ok(const kvp_prompt_shape *s) {
 static int prompt_tokens(const kvp_prompt_shape *s) { return 2 * (128 / (s->n_q_heads / s->n_kv_heads)); }
 static int64_t prompt_tiles(const kvp_prompt_shape *s) { return int64_t(s->n_q_tokens / prompt_tokens(s)) + s->n_seqs; }
 
-// Where there are fewer blocks than SMs, the keys of each are cut into `splits` parts of
-// at least four tiles.  Workspace: the parts' statistics and sums.
+// Where the blocks would leave SMs idle, the keys of each are cut into `splits` parts, joined by a
+// second kernel.  The number is the one that is expected to take least, in tiles: rounds of the SMs,
+// each a part's tiles and START for its start and end, and the parts' way to memory and back (a
+// block's 256 rows of 128: as many bytes as four tiles' keys and values).  A turn of 509 tokens over
+// 32768 (64 blocks, 2 parts): 195 us; in 7 parts, three full rounds, 200.
+constexpr int PT_START = 5, PT_MOST_SPLITS = 32;
+static int prompt_splits(const kvp_prompt_shape *s, int window, int sinks) {
+    const int64_t blocks = prompt_tiles(s) * s->n_kv_heads, sms = sm_count();
+    int64_t keys = s->n_k_tokens / std::max(1, s->n_seqs);
+    if (window > 0) keys = std::min<int64_t>(keys, int64_t(window) + prompt_tokens(s) + std::min(sinks, PT_KEYS));
+    const int64_t tiles = keys / PT_KEYS + 1;
+    int best = 1;
+    int64_t least = 0;
+    for (int n = 1; n <= PT_MOST_SPLITS && n <= tiles; ++n) {
+        const int64_t rounds = (blocks * n + sms - 1) / sms, a_part = (tiles + n - 1) / n;
+        const int64_t takes = rounds * (a_part + PT_START) + (n > 1 ? 4 + rounds * 2 : 0);
+        if (n == 1 || takes < least) best = n, least = takes;
+    }
+    return best;
+}
+// Workspace: the parts' statistics and sums, for the most parts that any window leads to.
 struct PromptSplit {
-    int splits;
     uint64_t part, total;
 };
-static PromptSplit prompt_split(const kvp_prompt_shape *s) {
+static PromptSplit prompt_split(const kvp_prompt_shape *s, int splits) {
     PromptSplit w;
-    const int64_t blocks = prompt_tiles(s) * s->n_kv_heads, sms = sm_count();
-    const int64_t most = std::max<int64_t>(1, s->n_k_tokens / (4 * PT_KEYS));
-    w.splits = int(std::max<int64_t>(1, std::min(most, sms / std::max<int64_t>(blocks, 1))));
-    const uint64_t rows = uint64_t(s->n_q_tokens) * uint64_t(s->n_q_heads) * uint64_t(w.splits > 1 ? w.splits : 0);
+    const uint64_t rows = uint64_t(s->n_q_tokens) * uint64_t(s->n_q_heads) * uint64_t(splits > 1 ? splits : 0);
     w.part = align256(rows * 8u);
     w.total = std::max<uint64_t>(256, w.part + rows * uint64_t(s->head_dim) * 4u);
     return w;
@@ -1043,7 +1058,7 @@ extern "C" {
 
 size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape) {
     if (prompt_ok(shape) != KVP_OK) return 0;
-    return size_t(prompt_split(shape).total);
+    return size_t(prompt_split(shape, prompt_splits(shape, 0, 0)).total);
 }
 
 int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_rows *k, const kvp_rows *v,
@@ -1075,8 +1090,8 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
     a.nq = shape->n_q_heads, a.H = shape->n_kv_heads, a.G = a.nq / a.H;
     a.window = std::min(window, PT_MOST), a.sinks = std::min(sinks, PT_MOST);  // (no more keys than that)
     a.half_tokens = 128 / a.G;
-    const PromptSplit w = prompt_split(shape);
-    a.splits = w.splits;
+    a.splits = std::min(prompt_splits(shape, a.window, a.sinks), prompt_splits(shape, 0, 0));
+    const PromptSplit w = prompt_split(shape, a.splits);
     a.stats = static_cast<float2 *>(ws);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.part);
     const int64_t tiles = prompt_tiles(shape), grid = tiles * a.H * a.splits;
