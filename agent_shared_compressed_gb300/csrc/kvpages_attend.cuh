@@ -52,7 +52,14 @@
 // [0, 15] nearest to -z / s, formed once per token and group: then |z + c s| is at
 // most s / 2 (or of the code term's sign, where zero is outside the group's range),
 // and the two sums, of the code terms in the product and of the rest in fp32 once
-// per 32 dims, do not cancel.  16-bit pages are multiplied as they are.
+// per 32 dims, do not cancel.  Beside 4-bit keys c is 8, the middle: no rounding then adds
+// more than 2^-13 of a step of the codes (2^-17 of 8 s and of |z + 8 s|), which is far
+// below what the codes themselves leave out, and nothing has to be prepared (four 32K
+// caches 49.1 us with c formed by group, 45.7 so).  16-bit pages are multiplied as they are.
+//
+// 4-bit keys: four of a word's eight codes are fp16 subnormals as they lie (times 2^-24 or
+// 2^-20, exactly), after one shift the other four, so that a pair costs one mask where 8 bits
+// cost two instructions; their zero points enter as one product more per 16 tokens.
 //
 // Measured (of the 6789 GB/s that a copy reaches): four 32K caches of 8 bits, 4
 // query rows a KV head, 56.7 us, 5.0 TB/s; 15 4K caches of 16 bits 45.4 us, 5.5 TB/s;
@@ -164,6 +171,23 @@ __device__ __forceinline__ void lds_halfs(uint32_t at, float (&f)[N]) {
     for (int i = 0; i < N / 2; ++i) {
         const float2 v = half2_f32(w[i]);
         f[2 * i] = v.x, f[2 * i + 1] = v.y;
+    }
+}
+// N fp16 (scale s, zero point z) pairs as fp32 s and z + 8 s.
+template <int N>
+__device__ __forceinline__ void lds_middles(uint32_t at, float (&s)[N], float (&m)[N]) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if constexpr (N == 4) {
+        const uint4 v = lds128(at);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = lds64(at);
+        w[0] = v.x, w[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 v = half2_f32(w[i]);
+        s[i] = v.x, m[i] = fmaf(8.0f, v.x, v.y);
     }
 }
 __device__ __forceinline__ void sts32(uint32_t at, float v) {
@@ -319,7 +343,7 @@ struct PatShape {
     static constexpr uint32_t STAGES = RING < LEAST ? LEAST : (RING > 8u ? 8u : RING);
     // 4-bit values: a warp's scales, remainders (fp32 [16][NG]) and -(128 + c) (bf16 pairs)
     static constexpr uint32_t NE = 16u * Block<D, FMT>::NG;
-    static constexpr uint32_t PREP = Block<D, FMT>::V4 ? NE * 10u * UB : 0u;
+    static constexpr uint32_t PREP = Block<D, FMT>::V4 && !Block<D, FMT>::K4 ? NE * 10u * UB : 0u;
     static constexpr uint32_t OFF_PREP = PAT_BAR_BYTES + WARPS * STAGES * SLOT;
     static constexpr uint32_t OFF_PLAN = OFF_PREP + WARPS * PREP;
     static_assert(WARPS * STAGES * 8 <= PAT_BAR_BYTES, "a barrier per slot");
@@ -738,7 +762,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 fence_proxy_async();  // before a later copy into the slot
                 __syncwarp();
             }
-            if constexpr (V4) {
+            if constexpr (V4 && !K4) {
 #pragma unroll
                 for (int u = 0; u < NG / 2 * UB; ++u) {
                     const int e = 32 * u + lane, t = e / NG, gr = e % NG;  // token of the unit, group
@@ -952,7 +976,9 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     float sv[2][NG], zv[2][V4 ? NG : 1];  // value scales of tokens g and g + 8
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        if constexpr (V4) {
+                        if constexpr (K4) {
+                            lds_middles<NG>(at + B::OFF_VS + uint32_t(8 * hf + g) * B::VSROW, sv[hf], zv[hf]);
+                        } else if constexpr (V4) {
                             const uint32_t pa = prep + 4u * NG * uint32_t(16 * u + 8 * hf + g);
                             lds_floats<NG>(pa, sv[hf]);
                             lds_floats<NG>(pa + 4u * UB * SM::NE, zv[hf]);
@@ -977,7 +1003,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                             }
                         }
                     uint32_t cv[2][V4 ? NG : 1];  // [token half]
-                    if constexpr (V4) {
+                    if constexpr (K4) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int e = 0; e < NG; ++e) cv[hf][e] = 0xC308C308u;  // -(128 + 8)
+                    } else if constexpr (V4) {
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             const uint32_t ca = prep + 8u * UB * SM::NE + 4u * NG * uint32_t(8 * u + 4 * hf + tig);

@@ -1,7 +1,10 @@
 """GPU tests of 4-bit pages, windows with first tokens, and positions of several
 axes, against the plain 64-bit forms in longhelp.py.  Weights enter the value
-product as two bf16 (2^-17), 4-bit values and their remainder about a group's zero
-(a factor of 3 of the value at most): 3 * 2^-17 of sum p |v|."""
+product as two bf16 (2^-17 of each term that they multiply).  A 4-bit value q s + z is the
+terms (q - c) s and z + c s: beside 8-bit keys c is the integer nearest to -z / s, so that
+their magnitudes add up to at most 3 |v|; beside 4-bit keys it is 8, and they add up to at
+most |v - (z + 8 s)| + |z + 8 s| <= 8 s + |z + 8 s| (q <= 15: |q - 8| <= 8).  So the error is
+2^-17 of sum p times 3 |v|, or times that sum."""
 import math
 
 import numpy as np
@@ -55,7 +58,18 @@ def _case(fmt, H, d, page, lens, G, m, window, sinks, seed=0, base=False, forget
                                       2 * Lg.zero_points(kb) if fmt == "k4v4" and lens[b] else None)
         if base:
             ro, rl, mass = Lg.join(ro, rl, mass, bo[b].cpu().numpy().astype(np.float64), bl[b].cpu().numpy().astype(np.float64))
+        if fmt == "k4v4" and lens[b]:
+            mass = _middle_mass(Lg.f64(q[b]), kb, vb, [lens[b] - m + i for i in range(m)], window, sinks, scale, mass)
         Lg.check(out[b], lse[b], ro, rl, mass, reach, WEIGHTS)
+
+
+def _middle_mass(q, k, v, places, window, sinks, scale, mass):
+    """sum p (8 s + |z + 8 s|) / 3 of 4-bit values (as large as WEIGHTS wants it), at least sum p |v|.
+    s, z from the held values: their group's least and (at most) largest."""
+    g = v.reshape(*v.shape[:-1], -1, 32)
+    s, z = (g.max(-1, keepdims=True) - g.min(-1, keepdims=True)) / 15, g.min(-1, keepdims=True)
+    terms = np.repeat(8 * s + np.abs(z + 8 * s), 32, -1).reshape(v.shape) * (1 + 2.0 ** -9)
+    return np.maximum(mass, Lg.rows(q, k, terms, places, window, sinks, scale)[0] / 3)
 
 
 # --- 4-bit pages ---------------------------------------------------------------
@@ -147,6 +161,7 @@ def test_4bit_zero_points_far_from_zero():
     q = Lg.bf16(rng.standard_normal((1, 1, 4, d))).cuda()
     out, lse = pg.attend(q, 0.1)
     ro, rl, mass, reach = Lg.rows(Lg.f64(q[0]), hk, hv, [n - 1], 0, 0, 0.1, 2 * Lg.zero_points(hk))
+    mass = _middle_mass(Lg.f64(q[0]), hk, hv, [n - 1], 0, 0, 0.1, mass)
     Lg.check(out[0], lse[0], ro, rl, mass, reach, WEIGHTS)
 
 
@@ -237,6 +252,8 @@ def test_window_in_a_graph_on_another_stream():
         for _, w, s, out, lse, _ in calls:
             ro, rl, mass, reach = Lg.rows(Lg.f64(q[0]), hk[:length], hv[:length], [length - 1], w, s, 0.1,
                                           2 * Lg.zero_points(hk[:length]) if length else None)
+            if length:
+                mass = _middle_mass(Lg.f64(q[0]), hk[:length], hv[:length], [length - 1], w, s, 0.1, mass)
             Lg.check(Lg.f64(out[0]), lse[0].cpu().numpy().astype(np.float64), ro, rl, mass, reach, WEIGHTS)
 
 
