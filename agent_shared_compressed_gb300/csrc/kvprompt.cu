@@ -17,14 +17,17 @@
 // tcgen05, 128 x 128 (x d) tiles, everything but keys and values staying on the SM:
 //   S = Q K^T   operands in shared memory, S in TMEM (128 columns a half)
 //   O += P V    P as bf16 in TMEM over the first half of S's columns, O in TMEM
-// Warps 0-3 and 4-7 do the softmax of a half each, a thread a row (no shuffles);
-// warp 8 issues the products, warp 9 the copies (TMA, 128-byte swizzle, a ring of
-// key and value tiles).  While one half's softmax runs the tensor core has the
-// other's products.
+// Warps 0-3 and 4-7 do the softmax of a half each, a thread a row (no shuffles), and
+// write its result; warp 8 issues the products; warp 9 finds the work and brings
+// queries, keys and values (TMA, 128-byte swizzle, a ring of tiles); warp 10 looks after
+// the values.  While one half's softmax runs the tensor core has the other's products.
+// A half's tile is a chain: scores, softmax (some 1200 cycles, its exponentials 512 of
+// them), values, next scores (1030 cycles of products, of 2060 for both halves); with
+// the handovers 2630 cycles measured a tile, 78 % of the products' rate.
 //
 // A row's reference (its largest score so far) is raised only when a score passes it
 // by 2^8, so that O is hardly ever rescaled; weights are taken relative to 2^40 times
-// the reference, so that sums of up to 2^31 values up to bf16's largest stay finite.
+// the reference, so that sums of up to 2^30 values up to bf16's largest stay finite.
 // Weights are rounded to bf16 for the value product (2^-9 at most, of either sign; the
 // sum takes them before that): a second product for the rest of them would cost
 // a quarter of the tensor time for less than the result's own rounding to bf16.
@@ -33,6 +36,13 @@
 // with weight 0, if they are Inf or NaN.  Rows of a tile that nobody sees are zeroed in
 // shared memory.  Tiles that some rows see in part are looked over; if one holds Inf or
 // NaN among the tokens seen, the block's rows are computed again one by one in fp32.
+//
+// Measured (32 query over 8 KV heads of 128; cuBLAS reaches 1895 TFLOP/s): 16384 tokens
+// 1.25 ms, 1760 TFLOP/s, in a graph (1.39 ms over minutes, where the power limit lowers the
+// clock); 8192 tokens with a window of 1024 and 4 first tokens 130 us, 990 TFLOP/s of what is
+// seen: a block's 10 tiles are 9.5 tiles' worth of keys that some row does not see besides,
+// and about 4 of start and end; 509 tokens over 32768 in two parts 195 us.  32 heads of 64, window
+// 256, 17 first tokens, 7 ragged prompts of 37 to 1851: 69 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -943,25 +953,27 @@ static int64_t prompt_tiles(const kvp_prompt_shape *s) { return int64_t(s->n_q_t
 
 // Where the blocks would leave SMs idle, the keys of each are cut into `splits` parts, joined by a
 // second kernel.  The number is the one that is expected to take least, in tiles: rounds of the SMs,
-// each a part's tiles and START for its start and end, and the parts' way to memory and back (a
-// block's 256 rows of 128: as many bytes as four tiles' keys and values).  A turn of 509 tokens over
-// 32768 (64 blocks, 2 parts): 195 us; in 7 parts, three full rounds, 200.
-constexpr int PT_START = 5, PT_MOST_SPLITS = 32;
+// each a part's tiles and PT_START for its start and end, PT_MOVE for the way of a block's 256 rows of
+// sums to memory and back; it has to gain a twentieth, and to do with PT_PARTS bytes.  A turn of 509
+// tokens over 32768 (64 blocks): 195 us in 2 parts, 200 in 7 (three full rounds).
+constexpr int PT_START = 5, PT_MOVE = 6, PT_MOST_SPLITS = 32;
+constexpr uint64_t PT_PARTS = 256u << 20;
 static int prompt_splits(const kvp_prompt_shape *s, int window, int sinks) {
     const int64_t blocks = prompt_tiles(s) * s->n_kv_heads, sms = sm_count();
     int64_t keys = s->n_k_tokens / std::max(1, s->n_seqs);
     if (window > 0) keys = std::min<int64_t>(keys, int64_t(window) + prompt_tokens(s) + std::min(sinks, PT_KEYS));
     const int64_t tiles = keys / PT_KEYS + 1;
+    const uint64_t a_part_bytes = uint64_t(s->n_q_tokens) * uint64_t(s->n_q_heads) * uint64_t(s->head_dim * 4 + 8);
     int best = 1;
     int64_t least = 0;
-    for (int n = 1; n <= PT_MOST_SPLITS && n <= tiles; ++n) {
+    for (int n = 1; n <= PT_MOST_SPLITS && n <= tiles && (n == 1 || a_part_bytes * n <= PT_PARTS); ++n) {
         const int64_t rounds = (blocks * n + sms - 1) / sms, a_part = (tiles + n - 1) / n;
-        const int64_t takes = rounds * (a_part + PT_START) + (n > 1 ? 4 + rounds * 2 : 0);
-        if (n == 1 || takes < least) best = n, least = takes;
+        const int64_t takes = rounds * (a_part + PT_START + (n > 1 ? PT_MOVE : 0));
+        if (n == 1 || takes * (best == 1 ? 21 : 20) < least * 20) best = n, least = takes;
     }
     return best;
 }
-// Workspace: the parts' statistics and sums, for the most parts that any window leads to.
+// Workspace: the parts' statistics and sums.
 struct PromptSplit {
     uint64_t part, total;
 };
@@ -991,9 +1003,9 @@ static EncodeTiled encode_tiled() {
 }
 
 // A rows tensor as a tensor map: boxes of 64 dims x `heads` x `tokens`.
-static bool rows_map(CUtensorMap *map, const kvp_rows *r, int tokens, int heads, int d, int box_heads, int box_tokens) {
+static int rows_map(CUtensorMap *map, const kvp_rows *r, int tokens, int heads, int d, int box_heads, int box_tokens) {
     const EncodeTiled encode = encode_tiled();
-    if (!encode) return false;
+    if (!encode) return KVP_ERR_CUDA;
     const cuuint64_t size[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
     // the stride of a single head or token says nothing
     const cuuint64_t stride[2] = {heads > 1 ? cuuint64_t(r->head_stride) * 2 : cuuint64_t(d) * 2,
@@ -1001,7 +1013,9 @@ static bool rows_map(CUtensorMap *map, const kvp_rows *r, int tokens, int heads,
     const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)}, step[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(r->ptr), size, stride, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KVP_OK
+               : KVP_ERR_ARG;
 }
 
 static thread_local uint32_t g_next_polls = 0;
@@ -1099,10 +1113,10 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
     a.tiles = int(tiles);
     // (with no keys at all nothing is copied: the maps are those of the queries)
     const bool some = shape->n_k_tokens > 0;
-    if (!rows_map(&a.q_map, q, a.n, a.nq, shape->head_dim, a.G, a.half_tokens) ||
-        !rows_map(&a.k_map, some ? k : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS) ||
-        !rows_map(&a.v_map, some ? v : q, some ? a.nk : a.n, some ? a.H : a.nq, shape->head_dim, 1, PT_KEYS))
-        return KVP_ERR_CUDA;
+    const int keys = some ? a.nk : a.n, heads = some ? a.H : a.nq;
+    if ((rc = rows_map(&a.q_map, q, a.n, a.nq, shape->head_dim, a.G, a.half_tokens)) != KVP_OK) return rc;
+    if ((rc = rows_map(&a.k_map, some ? k : q, keys, heads, shape->head_dim, 1, PT_KEYS)) != KVP_OK) return rc;
+    if ((rc = rows_map(&a.v_map, some ? v : q, keys, heads, shape->head_dim, 1, PT_KEYS)) != KVP_OK) return rc;
     a.sectors = aligned(out, 32) && aligned(ws, 32);
     a.polls = g_limit_next ? g_next_polls : PT_WAIT_LIMIT;
     g_limit_next = false;
