@@ -74,3 +74,15 @@ def test_attend_window_refusals():
         with pytest.raises(ValueError):
             call(**bad)
     assert cfg.format == kv.KVP_PAGES_K4V4
+
+
+def test_no_read_only_loads_of_what_may_be_written():
+    """The kernels that may be resident while the one before them runs read what it writes: no
+    loads of the kind that wants memory nobody writes meanwhile (as the other page kernels)."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "agent_shared_compressed_gb300", "csrc")
+    for name in ("kvpages_attend.cuh", "kvprompt.cu"):
+        code = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(os.path.join(csrc, name)).read(), flags=re.S)
+        assert not re.findall(r"\b__ldg\b|\b__ldc[agsv]\b|\.nc\b|\bld_stream_\w+|\bld_v4_policy\b|__restrict__", code), name
+        assert "griddepcontrol.wait;" in code
