@@ -699,7 +699,6 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                     lim[t][c] = rc < a.R ? len - (a.m - 1 - rc / a.G) : 0;
                     const int u = __shfl_sync(0xffffffffu, up, (2 * tig + c) * 4);
                     qs[t][c] = Q8 ? a.scale2 * __uint_as_float(uint32_t(127 - u) << 23) : a.scale2;
-                    if constexpr (K4) qs[t][c] *= 0x1p24f;  // the codes enter as fp16 times 2^-24
                     ref[t][c] = -INFINITY, bar2[t][c] = -INFINITY, off[t][c] = 0.0f;
                     sum[t][c] = 0.0f;
                 }
@@ -830,7 +829,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                         float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         mma_f16(c, kz[0], kz[1], kz[0], kz[1], qz[t][0], qz[t][1]);
 #pragma unroll
-                        for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] = c[e / CQ * 2 + e % CQ] * 0x1p-18f;
+                        for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] = c[e / CQ * 2 + e % CQ] * 0x1p-18f;  // as the codes' part: times 2^-24
                     }
 #pragma unroll
                     for (int k = 0; k < NG; ++k) {
@@ -903,7 +902,7 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
 #pragma unroll
                 for (int t = 0; t < R8; ++t)
 #pragma unroll
-                    for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] *= qs[t][e % CQ];
+                    for (int e = 0; e < 2 * CQ; ++e) x[u][t][e] = (K4 ? x[u][t][e] * 0x1p24f : x[u][t][e]) * qs[t][e % CQ];
             }
             if (tail) {
 #pragma unroll

@@ -58,6 +58,9 @@ constexpr int PT_KEYS = 128;                  // keys of a tile
 // Three warpgroups: 384 threads start with 168 registers each (64512 of the SM's), the third
 // gives 80 of its back and each of the others takes 40 more: 2 * 128 * 208 + 128 * 88 = 64512.
 constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
+// First tokens that a narrow tile holds.  Without it, 4 of them cost a window of 1024 a twentieth (8192
+// tokens: 130 us, 137).
+constexpr int PT_FEW = 32;
 constexpr int PT_MOST = 1 << 30;              // rows: sums and differences of places fit 32 bits
 constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
 constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f;
@@ -243,6 +246,10 @@ __device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t *x) {
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
         ::KVP_I8(x, 0), KVP_I8(x, 8), KVP_I8(x, 16), KVP_I8(x, 24), "r"(at) : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t *x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+                 ::KVP_I8(x, 0), KVP_I8(x, 8), "r"(at) : "memory");
+}
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // (the registers of a load are its results only once it has been waited for)
@@ -314,6 +321,9 @@ struct alignas(16) PromptWork {
     int unused[3];
 
     __device__ __forceinline__ int p_last() const { return p_first + count - 1; }
+    // Whether the first tile holds a few first tokens only: PT_FEW columns of it do then.  (They
+    // lie before every row's window, so that all rows see them.)
+    __device__ __forceinline__ bool few() const { return na == 1 && a_end <= PT_FEW && j0 == 0 && nt > 0; }
     __device__ __forceinline__ void tile(int j, int &t0, int &end) const {
         j += j0;
         if (j < na)
@@ -349,8 +359,9 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block,
     auto tiles_of = [](int n) { return (n + PT_KEYS - 1) / PT_KEYS; };
     w.b_end = max(w.p_last() + 1, 0), w.b0 = a.window ? max(w.p_first - a.window + 1, 0) : 0;
     w.a_end = min(a.sinks, w.b0);
-    // no more tiles without the gap: without it
-    if (tiles_of(w.b_end) <= tiles_of(w.a_end) + tiles_of(w.b_end - w.b0)) w.a_end = 0, w.b0 = 0;
+    // no more (whole) tiles without the gap: without it
+    const int apart = tiles_of(w.b_end - w.b0) + (w.a_end > PT_FEW ? tiles_of(w.a_end) : 0);
+    if (tiles_of(w.b_end) <= apart) w.a_end = 0, w.b0 = 0;
     w.na = tiles_of(w.a_end);
     const int all = w.na + tiles_of(w.b_end - w.b0);
     w.j0 = int(int64_t(all) * w.split / a.splits), w.nt = int(int64_t(all) * (w.split + 1) / a.splits) - w.j0;
@@ -530,21 +541,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             // are then formed in uniform registers.  (In a branch of one lane each product costs 130
             // cycles instead of 65.)
             const uint32_t kind_s = tc_kind(128) | (a.negative ? TC_NEGATE_A : 0u), kind_o = tc_kind(D) | TC_B_BY_ROWS;
-            auto scores = [&](uint32_t half, uint32_t at) {  // S = Q K^T
+            const uint32_t kind_few = tc_kind(PT_FEW) | (a.negative ? TC_NEGATE_A : 0u);
+            auto scores = [&](uint32_t half, uint32_t at, uint32_t kind) {  // S = Q K^T
                 const uint64_t qd = tc_operand(sm + T::OFF_Q + half * T::BYTES, 16);
                 const uint64_t kd = tc_operand(sm + T::OFF_RING + at * T::BYTES, 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = uint64_t((uint32_t(k / 4) * T::CHUNK + uint32_t(k % 4) * 32u) >> 4);
-                    tc_mma_ss(half * 128u, qd + off, kd + off, kind_s, k > 0);
+                    tc_mma_ss(half * 128u, qd + off, kd + off, kind, k > 0);
                 }
                 tc_commit(sm + T::S + 8 * half);
             };
-            auto values = [&](uint32_t half, uint32_t at, bool add) {  // O += P V
+            auto values = [&](uint32_t half, uint32_t at, bool add, bool few) {  // O += P V
                 const uint64_t vd = tc_operand(sm + T::OFF_RING + at * T::BYTES, T::CHUNK);
 #pragma unroll
                 for (int k = 0; k < PT_KEYS / 16; ++k)
-                    tc_mma_ts(256u + half * D, half * 128u + 8u * uint32_t(k), vd + uint64_t(k * 2048 >> 4), kind_o, add || k > 0);
+                    if (k < PT_FEW / 16 || !few) tc_mma_ts(256u + half * D, half * 128u + 8u * uint32_t(k), vd + uint64_t(k * 2048 >> 4), kind_o, add || k > 0);
             };
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t limit) {
                 const bool ok = __all_sync(0xffffffffu, pt_wait(a, sm + bar, parity, dead, limit));
@@ -561,12 +573,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             for (uint32_t k = 0; next_work(k, w); ++k) {
                 const int tiles = __shfl_sync(0xffffffffu, w.nt, 0);
                 const bool two = __shfl_sync(0xffffffffu, w.count, 0) > a.half_tokens;
+                const bool few = __shfl_sync(0xffffffffu, int(w.few()), 0) != 0;
                 if (tiles == 0) continue;
                 if (!(ok = wait(T::Q, queries, PT_WAIT_LIMIT) && wait(T::FULL + 8 * at, round, a.polls))) break;
                 queries ^= 1u;
                 if (elect()) {
-                    scores(0, at);
-                    if (two) scores(1, at);
+                    scores(0, at, few ? kind_few : kind_s);
+                    if (two) scores(1, at, few ? kind_few : kind_s);
                     tc_commit(sm + T::FREE + 8 * at);
                     if (tiles == 1) tc_commit(sm + T::QFREE);
                 }
@@ -579,10 +592,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     const uint32_t k_at = at;  // (of the next tile, if there is one)
                     if (!(ok = wait(T::P, done0, PT_WAIT_LIMIT))) break;
                     if (elect()) {
-                        values(0, v_at, j > 0);
+                        values(0, v_at, j > 0, few && j == 0);
                         if (!two) tc_commit(sm + T::FREE + 8 * v_at);
                         if (more) {
-                            scores(0, k_at);
+                            scores(0, k_at, kind_s);
                             if (!two) {
                                 tc_commit(sm + T::FREE + 8 * k_at);
                                 if (last_scores) tc_commit(sm + T::QFREE);
@@ -596,10 +609,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     if (two) {
                         if (!(ok = wait(T::P + 8, done1, PT_WAIT_LIMIT))) break;
                         if (elect()) {
-                            values(1, v_at, j > 0);
+                            values(1, v_at, j > 0, few && j == 0);
                             tc_commit(sm + T::FREE + 8 * v_at);
                             if (more) {
-                                scores(1, k_at);
+                                scores(1, k_at, kind_s);
                                 tc_commit(sm + T::FREE + 8 * k_at);
                                 if (last_scores) tc_commit(sm + T::QFREE);
                             } else {
@@ -663,8 +676,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                         if (*reinterpret_cast<uint32_t *>(&odd[0]) & 0x7FFF7FFFu)
                             asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(odd_at), "r"(1u) : "memory");
                     }
-                    if (rows < PT_KEYS) {
-                        for (int row = rows + lane / PER; row < PT_KEYS; row += STEP)
+                    const int used = w.few() && j == 0 ? PT_FEW : PT_KEYS;  // rows that enter the product
+                    if (rows < used) {
+                        for (int row = rows + lane / PER; row < used; row += STEP)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(mine + uint32_t(row) * 128u), "r"(0u) : "memory");
                         fence_proxy_async();
                     }
@@ -705,7 +719,39 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
                 in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
             }
-            for (int j = 0; j < w.nt; ++j) {
+            int j = 0;
+            if (w.few()) {
+                if ((ok = warp_wait(a, sm + T::S + 8 * uint32_t(half), done, dead))) {
+                    tc_after();
+                    uint32_t x[32];
+                    float *xf = reinterpret_cast<float *>(x);
+                    tc_ld32(s_at, x);
+                    tc_wait_ld();
+                    tc_landed(x), tc_landed(x + 16);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        xf[c] = c < w.a_end ? (a.flat ? 0.0f : xf[c] * a.scale2) : -INFINITY;
+                        top = fmaxf(top, xf[c]);
+                    }
+                    ref = top;
+                    const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float y0 = pt_exp2(xf[2 * c] + off), y1 = pt_exp2(xf[2 * c + 1] + off);
+                        sum += y0 + y1;
+                        x[c] = pack_bf16x2(y0, y1);
+                    }
+                    tc_st16(s_at, x);
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sm + T::P + 8 * uint32_t(half));
+                    done ^= 1u;
+                }
+                j = 1;
+            }
+            for (; ok && j < w.nt; ++j) {
                 const bool inner = j >= in0 && j < in1;
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // the columns that the row sees, as bits
                 if (!inner) {

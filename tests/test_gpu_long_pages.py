@@ -165,6 +165,22 @@ def test_4bit_zero_points_far_from_zero():
     Lg.check(out[0], lse[0], ro, rl, mass, reach, WEIGHTS)
 
 
+def test_4bit_large_queries():
+    """Queries up to bf16's largest over keys so small that scores are finite; and tiny ones."""
+    rng = np.random.default_rng(9)
+    H, d, n = 1, 128, 40
+    for size, keys, scale in ((3e38, 1e-6, 1e-33), (1e-38, 1.0, 1e37)):
+        pg = Lg.Pages("k4v4", H, d, 16, [n])
+        k = Lg.bf16(keys * rng.standard_normal((n, H, d))).cuda()
+        _, v = _kv(n, H, d, 2)
+        pg.write(k, v)
+        hk, hv = P.held4(Lg.f64(k)), P.held4(Lg.f64(v))
+        q = Lg.bf16(size * rng.uniform(-1, 1, (1, 1, 4, d))).cuda()
+        out, lse = pg.attend(q, scale)
+        ro, rl, mass, reach = Lg.rows(Lg.f64(q[0]), hk, hv, [n - 1], 0, 0, scale, 2 * Lg.zero_points(hk))
+        Lg.check(out[0], lse[0], ro, rl, _middle_mass(Lg.f64(q[0]), hk, hv, [n - 1], 0, 0, scale, mass), reach, WEIGHTS)
+
+
 # --- windows ---------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", FMTS)

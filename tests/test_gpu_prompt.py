@@ -115,6 +115,15 @@ def test_windows(window, sinks, H, G, d):
     Call([(700, 0), (130, 333), (1, 600), (5, 0)], H, G, d, seed=window % 1000).both(window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(40, 1), (40, 31), (40, 32), (40, 33), (300, 32), (256, 160)])
+def test_first_tokens_apart_from_the_window(window, sinks):
+    """First tokens that a narrow tile holds, and one more than that, behind a gap; scales of either
+    sign and 0; few rows over many keys, which are split."""
+    for d, scale in ((128, None), (64, -0.2), (128, 0.0)):
+        Call([(140, 900), (1, 1100), (300, 0)], 2, 4, d, seed=sinks).both(scale=scale, window=window, sinks=sinks)
+    Call([(3, 30000)], 1, 2, 64).both(window=9000 + window, sinks=sinks)
+
+
 @pytest.mark.parametrize("layout", ["fused", "heads"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_layouts(layout, d):
@@ -134,6 +143,63 @@ def test_more_new_tokens_than_keys():
     c.both()
     c.both(base=c.base())
     c.both(window=10, sinks=1)
+
+
+def test_no_keys_at_all():
+    """Sequences without keys, and no rows of k and v (null pointers): zeros and -inf, or the base."""
+    c = Call([(5, -5), (200, -200)], 1, 3, 64)
+    assert c.t == 0
+    c.k = c.v = kv.Rows(None, 64, 64)
+    for base in ((None, None), c.base()):
+        out, lse = c.run(0.1, 0, 0, base)
+        assert kv.kvprompt_status(c.error) == kv.KVP_OK
+        if base[0] is None:
+            assert not out[:205].any() and np.all(lse[:205] == -np.inf)
+        else:
+            want = base[0].to(torch.bfloat16)
+            want[base[1] == -math.inf] = 0
+            assert np.array_equal(out, Lg.f64(want)) and np.array_equal(lse, base[1].cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("seqs", [[(150, 10)], [(5, 20000)]])
+def test_outputs_and_rows_anywhere(seqs):
+    """Results on 16-byte boundaries only, the workspace too; sequences that do not begin with q's
+    first row, and not in order in k; rows of none are left as they are."""
+    c = Call(seqs, 2, 2, 128, gap=4)
+    want, want_lse = c.run(0.1)
+    n = c.n * c.nq * c.d
+    for off in (8, 16):
+        out = torch.full((n + 64,), 3.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(c.wsb + 64, dtype=torch.uint8, device="cuda")
+        lse = torch.full((c.n * c.nq + 4,), 3.0, device="cuda")
+        c.launch(0.1, 0, 0, (None, None), out[off:off + n], lse[1:1 + c.n * c.nq], ws[16:16 + c.wsb])
+        torch.cuda.synchronize()
+        used = sum(a for a, _ in seqs) * c.nq
+        assert np.array_equal(Lg.f64(out[off:off + used * c.d]), want.reshape(-1)[:used * c.d])
+        assert np.array_equal(lse[1:1 + used].cpu().numpy().astype(np.float64), want_lse.reshape(-1)[:used])
+        assert bool((out[:off] == 3).all()) and bool((out[off + used * c.d:] == 3).all()) and bool((lse[1 + used:] == 3).all())
+    c = Call([(0, 0), (30, 40), (20, 0)], 1, 2, 64, gap=9)
+    ref = c.run(0.1)
+    q = c.q.clone()
+    c.q[9:] = q[:-9]
+    c.q_first_d += 9
+    got = c.run(0.1)
+    assert np.array_equal(got[0][9:59], ref[0][:50]) and np.array_equal(got[1][9:59], ref[1][:50])
+    assert bool((c.raw[0][:9 * c.nq * c.d * 2] == 0x7F).all()) and bool((c.raw[1][:9 * c.nq * 4] == 0x7F).all())
+
+
+def test_unseen_nonfinite_beside_the_first_tokens():
+    """Inf in tokens that share a tile with the first ones: the queries whose window has left them
+    behind do not meet it."""
+    c = Call([(600, 0)], 1, 4, 128)
+    clean = c.run(0.1, 64, 5)
+    c.v[5:40] = math.inf
+    out, lse = c.run(0.1, 64, 5)
+    p = np.arange(600)
+    sees = (p >= 5) & (p - 39 < 64)
+    assert np.array_equal(~np.isfinite(out).all((1, 2)), sees)
+    tol = 2.0 ** -6 * np.abs(clean[0]).max()
+    assert np.all(np.abs(out[~sees] - clean[0][~sees]) <= tol) and np.all(np.abs(lse - clean[1]) <= 1e-4)
 
 
 def test_sharp_negative_and_zero_scales():
