@@ -5,7 +5,8 @@ a Walsh-Hadamard transform and coded at 3 bits with the Lloyd-Max N(0,1)
 codebook; fan-out decode into N agent caches) and CacheCard ("QKVShare":
 per-token {2,4,8,16}-bit asymmetric group quantization with metadata) and
 pages (an agent's own growing cache, quantised as it is written, attended over
-and joined with the pool's attention), as a C-ABI CUDA library
+and joined with the pool's attention, whole or through a window) and attention of
+whole prompts, as a C-ABI CUDA library
 (include/kvpool.h) with this thin ctypes binding.
 """
 from .binding import (  # noqa: F401

@@ -21,6 +21,9 @@
  *    with attention over the pool ("PolyKV" 2.A gives each agent a cache of
  *    its own on top of the shared one; the papers leave its form open).
  *
+ *  Attention of whole prompts needs no container: it reads bf16 keys and values
+ *    as the calls on the three above return them.
+ *
  * Conventions shared by every entry point
  * ----------------------------------------
  *  - KV tensors are bf16, one tensor per layer, layout [H][T][d] contiguous
