@@ -288,6 +288,10 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
     constexpr int NB = D / 32;
     // rows padded to start on other banks; read as float4
     __shared__ __align__(16) float cosines[APP_TOKENS][D / 2 + 4], sines[APP_TOKENS][D / 2 + 4], norm[2][D];
+    // what pair i turns by, and where its positions begin: a warp's lanes want 32 of them
+    // at once, which the parameters' constant memory gives one by one
+    __shared__ uint64_t turns[D / 2];
+    __shared__ const int64_t *from[D / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tq = lane >> 2, tig = lane & 3;
     const int H = a.pv.H, rows = a.nq + 2 * H;
     const int64_t first = int64_t(blockIdx.x) * a.run;
@@ -307,6 +311,11 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
 #pragma unroll
         for (int b = 0; b < NB; ++b) v[b] = real ? ld_l2_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
     };
+    if (threadIdx.x < D / 2) {
+        turns[threadIdx.x] = a.turn[threadIdx.x];
+        from[threadIdx.x] = a.positions + int64_t(a.axis[threadIdx.x]) * a.n;
+    }
+    const int log_half = a.rot == 128 ? 6 : 5;
     wait_for_previous();
     uint4 in[NB];
     load(grp, st, in);
@@ -327,14 +336,13 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
             real = tok < a.n;
             const int64_t slot = real ? a.slots[tok] : -1;
             if (a.rot > 0) {
-                for (int i = threadIdx.x; i < APP_TOKENS * (a.rot / 2); i += APP_THREADS) {
-                    const int t = i / (a.rot / 2), p = i % (a.rot / 2);
+                for (int i = threadIdx.x; i < APP_TOKENS << log_half; i += APP_THREADS) {
+                    const int t = i >> log_half, p = i & ((1 << log_half) - 1);
                     const int64_t at = grp * APP_TOKENS + t;
                     float s = 0.0f, c = 1.0f;
                     if (at < a.n) {
-                        const int64_t pos = a.positions[int64_t(a.axis[p]) * a.n + at];
-                        const int64_t turns = int64_t(uint64_t(pos) * a.turn[p]);  // mod one turn
-                        sincospif(2.0f * (float(turns) * 0x1p-64f), &s, &c);
+                        const int64_t part = int64_t(uint64_t(from[p][at]) * turns[p]);  // mod one turn
+                        sincospif(2.0f * (float(part) * 0x1p-64f), &s, &c);
                     }
                     cosines[t][p] = c, sines[t][p] = s;
                 }
