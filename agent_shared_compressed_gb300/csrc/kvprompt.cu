@@ -34,8 +34,9 @@
 //
 // Values that some of the rows do not see must not meet them in the product, not even
 // with weight 0, if they are Inf or NaN.  Rows of a tile that nobody sees are zeroed in
-// shared memory.  Tiles that some rows see in part are looked over; if one holds Inf or
-// NaN among the tokens seen, the block's rows are computed again one by one in fp32.
+// shared memory.  Tiles that only some of the rows see whole are looked over (a block has a
+// few of them, however long the sequence): Inf and NaN there are zeros to the product, and
+// are added to the results of the rows that do see them.
 //
 // Measured (32 query over 8 KV heads of 128; cuBLAS reaches 1895 TFLOP/s): 16384 tokens
 // 1.25 ms, 1760 TFLOP/s, in a graph (1.39 ms over minutes, where the power limit lowers the
@@ -169,35 +170,6 @@ __device__ __forceinline__ void prompt_write(const PromptArgs &a, uint64_t row, 
     }
 }
 
-// One row by one warp, a key at a time in fp32: lane l holds dims l d/32 ...  The keys are
-// those of [k0, k1) that the row at place p sees.  acc and sum are relative to
-// 2^(ref + PT_BIAS).
-template <int D>
-__device__ __forceinline__ void row_keys(const PromptArgs &a, const float (&q)[D / 32], const uint16_t *k, const uint16_t *v,
-                                         int p, int64_t k0, int64_t k1, float (&acc)[D / 32], float &ref, float &sum) {
-    constexpr int VPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t old = a.window ? int64_t(p) - a.window + 1 : 0;  // the oldest token of the window
-    for (int64_t t = k0; t < min(k1, int64_t(p) + 1); ++t) {
-        if (t < old && t >= a.sinks) {
-            t = min(old, k1) - 1;
-            continue;
-        }
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) s = fmaf(q[i], __uint_as_float(uint32_t(k[t * a.k_ts + lane * VPL + i]) << 16), s);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s = a.flat ? 0.0f : (a.negative ? -s : s) * a.scale2;
-        const float top = fmaxf(ref, s), f = ref == -INFINITY ? 0.0f : exp2f(ref - top);
-        const float w = exp2f(s - (top == -INFINITY ? 0.0f : top) - PT_BIAS);
-        ref = top, sum = fmaf(sum, f, w);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            acc[i] = fmaf(acc[i], f, w * __uint_as_float(uint32_t(v[t * a.v_ts + lane * VPL + i]) << 16));
-    }
-}
-
 // ---------------------------------------------------------------------------
 // tcgen05 and TMA.
 // ---------------------------------------------------------------------------
@@ -271,6 +243,12 @@ __device__ __forceinline__ bool elect() {
     return r != 0u;
 }
 
+// Two bf16, with zeros for Inf and NaN.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t v) {
+    const uint32_t lo = (v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu, hi = (v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u;
+    return lo | hi;
+}
+
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     uint32_t r;
@@ -330,6 +308,10 @@ struct alignas(16) PromptWork {
             t0 = j * PT_KEYS, end = min(t0 + PT_KEYS, a_end);
         else
             t0 = b0 + (j - na) * PT_KEYS, end = min(t0 + PT_KEYS, b_end);
+    }
+    // Whether some row does not see all of the tile's tokens.
+    __device__ __forceinline__ bool part_seen(const PromptArgs &a, int t0, int end) const {
+        return end - 1 > p_first || (a.window && t0 <= p_last() - a.window && end > a.sinks);
     }
 };
 static_assert(sizeof(PromptWork) == 64, "four 16-byte loads");
@@ -437,7 +419,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
     // ran out.  (By a warp.)
     auto next_work = [&](uint32_t k, PromptWork &w) {
         const uint32_t at = k & 1u;
-        if (!warp_wait(a, sm + T::WORK + 8 * at, (k >> 1) & 1u, dead)) return false;
+        // (a half that has no rows waits while the other works: 64 polls for each of its tiles)
+        const uint32_t limit = PT_WAIT_LIMIT + (k ? 64u * uint32_t(w.nt) : 0u);
+        if (!__all_sync(0xffffffffu, pt_wait(a, sm + T::WORK + 8 * at, (k >> 1) & 1u, dead, limit))) return false;
         uint32_t *to = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
@@ -658,7 +642,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     constexpr int PER = D / 8, STEP = 32 / PER;  // 16-byte pieces of a row, rows of a pass
                     const int c = lane % PER;
                     const uint32_t mine = tile + uint32_t(c / 8) * T::CHUNK + uint32_t(c % 8) * 16u;  // (in whatever place of the row)
-                    if (end - 1 > w.p_first || (a.window && t0 <= w.p_last() - a.window && end > a.sinks)) {
+                    if (w.part_seen(a, t0, end)) {
                         __nv_bfloat162 odd[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) odd[e] = __float2bfloat162_rn(0.0f);
@@ -673,8 +657,21 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                                 odd[e] = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v[e]), __float2bfloat162_rn(0.0f), odd[e]);
                         }
                         odd[0] = __hadd2(__hadd2(odd[0], odd[1]), __hadd2(odd[2], odd[3]));
-                        if (*reinterpret_cast<uint32_t *>(&odd[0]) & 0x7FFF7FFFu)
-                            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(odd_at), "r"(1u) : "memory");
+                        const bool bad = (*reinterpret_cast<uint32_t *>(&odd[0]) & 0x7FFF7FFFu) != 0u;
+                        if (__any_sync(0xffffffffu, bad)) {
+                            if (bad) {
+                                asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(odd_at), "r"(1u) : "memory");
+                                for (int row = lane / PER; row < rows; row += STEP)
+#pragma unroll
+                                    for (uint32_t e = 0; e < 4; ++e) {
+                                        const uint32_t at = mine + uint32_t(row) * 128u + 4u * e;
+                                        uint32_t v;
+                                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+                                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(finite_halves(v)) : "memory");
+                                    }
+                            }
+                            fence_proxy_async();
+                        }
                     }
                     const int used = w.few() && j == 0 ? PT_FEW : PT_KEYS;  // rows that enter the product
                     if (rows < used) {
@@ -714,11 +711,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             const int p = w.p_first + (real ? i : w.count - 1);
             float ref = -INFINITY, sum = 0.0f;
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
-            int in0 = 0, in1 = 0;
-            if (!a.flat) {
-                in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
-                in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
-            }
+            const int in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
+            const int in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
             int j = 0;
             if (w.few()) {
                 if ((ok = warp_wait(a, sm + T::S + 8 * uint32_t(half), done, dead))) {
@@ -752,7 +746,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 j = 1;
             }
             for (; ok && j < w.nt; ++j) {
-                const bool inner = j >= in0 && j < in1;
+                const bool inner = j >= in0 && j < in1 && !a.flat;
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // the columns that the row sees, as bits
                 if (!inner) {
                     int t0, end;
@@ -838,8 +832,50 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             }
             uint32_t odd;  // whether there are Inf or NaN among values that some row does not see
             asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sm + T::ODD + 4u * (k & 3u)) : "memory");
-            if (!ok) {
-            } else if (!odd || w.nt == 0) {
+            if (ok && odd && w.nt > 0) {  // they were zeros to the product: to O of the rows that see them
+                const uint16_t *vr = a.v + w.k_first * a.v_ts + w.h * a.v_hs;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc_ld32(o_at + uint32_t(c), o);
+                    tc_wait_ld();
+                    tc_landed(o), tc_landed(o + 16);
+#pragma unroll 1
+                    for (int j = 0; j < w.nt; ++j) {
+                        if (j >= in0 && j < in1) {
+                            j = in1 - 1;
+                            continue;
+                        }
+                        int t0, end;
+                        w.tile(j, t0, end);
+                        if (!w.part_seen(a, t0, end)) continue;
+#pragma unroll 1
+                        for (int t = t0; t < end; ++t) {
+                            const uint16_t *from = vr + t * a.v_ts + c;  // (the same of all lanes)
+                            uint32_t v[16];
+                            bool any = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint4 four = ld_l2_v4(from + 8 * e);
+                                v[4 * e] = four.x, v[4 * e + 1] = four.y, v[4 * e + 2] = four.z, v[4 * e + 3] = four.w;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) any |= finite_halves(v[e]) != v[e];
+                            if (!any || t > p || (a.window && t <= p - a.window && t >= a.sinks)) continue;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t x = v[e] - finite_halves(v[e]);  // Inf and NaN alone
+                                o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16_lo(x));
+                                o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16_hi(x));
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    tc_st32(o_at + uint32_t(c), o);
+                }
+                tc_wait_st();
+            }
+            if (ok) {
                 const uint64_t row = uint64_t(w.row + i) * uint32_t(a.nq) + uint32_t(w.h * a.G + r - tl * a.G);
                 // Each thread stores its own row, 32 bytes (a sector) at a time.  The code is short, as it
                 // is met with once a block and has to be fetched for that.
@@ -900,36 +936,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                         tc_landed(o), tc_landed(o + 16);
                         if (real) st_sectors<4>(a.part + at * D + c, o, a.sectors);
                         __syncwarp();
-                    }
-                }
-            } else {
-                // Inf or NaN among values that some row does not see: row by row
-                constexpr int VPL = D / 32;
-                for (int k = 0; k < 32; ++k) {
-                    const int rr = (warp & 3) * 32 + k, t = rr / a.G, ii = half * a.half_tokens + t, jj = w.h * a.G + rr - t * a.G;
-                    if (t >= a.half_tokens || ii >= w.count) break;
-                    float q[VPL], acc[VPL];
-                    ref = -INFINITY, sum = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < VPL; ++e) {
-                        q[e] = __uint_as_float(uint32_t(a.q[(w.row + ii) * a.q_ts + jj * a.q_hs + lane * VPL + e]) << 16);
-                        acc[e] = 0.0f;
-                    }
-                    const uint16_t *kr = a.k + w.k_first * a.k_ts + w.h * a.k_hs, *vr = a.v + w.k_first * a.v_ts + w.h * a.v_hs;
-                    const int place = w.p_first + ii, j1 = w.j0 + w.nt, ja = min(j1, w.na), jb = max(w.j0, w.na);
-                    if (w.j0 < ja)
-                        row_keys<D>(a, q, kr, vr, place, int64_t(w.j0) * PT_KEYS, min(int64_t(ja) * PT_KEYS, int64_t(w.a_end)), acc, ref, sum);
-                    if (jb < j1)
-                        row_keys<D>(a, q, kr, vr, place, w.b0 + int64_t(jb - w.na) * PT_KEYS,
-                                    min(w.b0 + int64_t(j1 - w.na) * PT_KEYS, int64_t(w.b_end)), acc, ref, sum);
-                    const uint64_t row = uint64_t(w.row + ii) * uint32_t(a.nq) + uint32_t(jj);
-                        if (a.splits > 1) {
-                        const uint64_t at = uint64_t(w.split) * uint32_t(a.n) * uint32_t(a.nq) + row;
-                        if (lane == 0) a.stats[at] = make_float2(ref, sum);
-#pragma unroll
-                        for (int e = 0; e < VPL; ++e) a.part[at * D + lane * VPL + e] = acc[e];
-                    } else {
-                        prompt_write<D>(a, row, ref, sum, acc, lane);
                     }
                 }
             }

@@ -263,6 +263,36 @@ def test_unseen_nonfinite(d):
         assert np.array_equal(np.isnan(lse[:300]).any(1), sees)
 
 
+@pytest.mark.parametrize("d,times", [(64, 80), (128, 80), (128, 1)])
+def test_unseen_nonfinite_over_many_keys(d, times):
+    """A block that meets Inf or NaN has no more to do for its sequence being long: no other
+    warp's wait runs out (sequences of 40256 keys, as many as fill the GPU, and one, which is
+    split).  What does not see them is what it was, bit for bit."""
+    c = Call([(256, 40000)], 2, 1, d)
+    c.seqs, c.n = c.seqs * times, 256 * times
+    c.q = c.q.repeat(times, 1, 1)
+    c.q_first_d = torch.arange(0, c.n + 1, 256, dtype=torch.int32, device="cuda")
+    c.k_first_d, c.k_lens_d = (torch.full((times,), x, dtype=torch.int32, device="cuda") for x in (0, 40256))
+    c.shape = kv.PromptShape(times, c.n, c.t, c.nq, c.H, d)
+    c.wsb = kv.kvprompt_workspace_bytes(c.shape)
+    at = [(0, 40100, 3, math.inf), (0, 40100, d - 1, -math.inf), (1, 40255, 7, math.nan), (1, 40000, 33, math.inf)]
+    for window, sinks, scale in ((0, 0, 0.1), (30000, 9, 0.1), (0, 0, 0.0)):
+        clean = c.run(scale, window, sinks)
+        was = c.v.clone()
+        for h, t, e, x in at:
+            c.v[t, h, e] = x
+        out, lse = c.run(scale, window, sinks)
+        c.v = was
+        assert kv.kvprompt_status(c.error) == kv.KVP_OK
+        want = clean[0].reshape(times, 256, 2, d)
+        got = out.reshape(want.shape)
+        for h, t, e, x in at:
+            sees = 40000 + np.arange(256) >= t
+            assert np.array_equal(got[:, :, h, e] == x if math.isinf(x) else np.isnan(got[:, :, h, e]), np.broadcast_to(sees, (times, 256)))
+            want[:, sees, h, e] = got[:, sees, h, e]
+        assert np.array_equal(got, want, equal_nan=True) and np.array_equal(lse, clean[1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_values_up_to_the_largest(d):
     """Finite values give finite results up to bf16's largest, whatever the sums before
