@@ -30,11 +30,11 @@ namespace kvp {
 
 constexpr int APP_THREADS = 256;
 constexpr int APP_WARPS = APP_THREADS / 32;
-// Blocks of an SM: what 117 (head_dim 128) and 64 registers a thread allow.  With
-// three of head_dim 128, at 80 registers, which spill, 8192 tokens took 62 us, with
-// blocks of 10 warps 47.4 against 46.8; five of head_dim 64 31.9 against 25.0 us on
-// three ragged prompts of 32 heads.  (Without any arithmetic: 40.6 and 23.6 us.)
-constexpr int app_blocks(int d) { return d == 128 ? 2 : 4; }
+// Blocks of an SM: what 123 (head_dim 128) and 80 registers a thread allow.  With three of
+// head_dim 128, at 80 registers, which spill, 8192 tokens took 62 us where two took 47, with
+// blocks of 10 warps 47.4 against 46.8.  Of head_dim 64 four, at 64 registers, spill too: three
+// ragged prompts of 32 heads in k8v4 25.0 us, 19.7 with three.
+constexpr int app_blocks(int d) { return d == 128 ? 2 : 3; }
 constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
 // Rows of a warp on their way, by asynchronous copies into shared memory (8192 tokens: 41.3 us;
 // one row ahead, in registers, 44.4; 3 rows 41.9, 4 rows 43.1).
@@ -92,15 +92,6 @@ __device__ __forceinline__ float rcp_scale(float s) {
     return s > 0.0f ? r : 0.0f;
 }
 
-// (t + e) / s rounded to nearest even, for a quotient within 2^-10 of the
-// half-integer next to y: the sign of (t + e) - (k + 1/2) s decides, and
-// (k + 1/2) s has at most 19 bits, t is within a factor of two of it, so both
-// differences are exact.
-__device__ __forceinline__ float at_border(float t, float e, float s, float y) {
-    const float k = floorf(y), d = (t - (k + 0.5f) * s) + e;
-    return d > 0.0f ? k + 1.0f : (d < 0.0f ? k : rintf(k + 0.5f));
-}
-
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -124,17 +115,20 @@ __device__ __forceinline__ bool drop_nonfinite(float2 (&x)[NB][4]) {
     return true;
 }
 
-// The 8-bit code of x where x / s is near a border or the codes can pass 127.
-__device__ __forceinline__ float code8_exact(float x, float s, float rs) {
-    const float y = x * rs;
-    const float q = fabsf(y - rintf(y)) > 0.5f - 0x1p-14f ? at_border(x, 0.0f, s, y) : rintf(y);
-    return fminf(fmaxf(q, -127.0f), 127.0f);
-}
-// The 4-bit code of x near a border: x - z = t + e exactly (two-sum).
-__device__ __forceinline__ float code4_exact(float x, float z, float s, float rs) {
-    const float t = x - z, xx = t + z, e = (x - xx) + ((xx - t) - z);
-    const float y = fminf(fmaxf(t * rs, 0.0f), 15.0f);
-    return fabsf(y - rintf(y)) > 0.5f - 0x1p-14f ? at_border(t, e, s, y) : rintf(y);
+// Two quotients (t + e) / s decided exactly, t being the sum's rounding and y within 2^-10 of
+// the quotients: k is the whole number below one (or, next to a whole number, either), held in
+// [least, most - 1], and the sign of (t + e) - (k + 1/2) s says on which side of k + 1/2 it lies.
+// (k + 1/2) s has at most 19 bits; where the quotient is near k + 1/2, t is within a factor of
+// two of it, so that both differences are exact, and elsewhere they are far from 0.  The result
+// rounds to nearest even to the code.  (No choice by element, two at a time: bf16 rows have ties in
+// every 50th group of 4-bit codes, so that half of a warp's rows come here.)
+__device__ __forceinline__ float2 decide2(float2 t, float2 e, float s, float2 y, float least, float most) {
+    constexpr float WHOLE = 12582912.0f;
+    float2 k = add2(add2(add2(y, both(-0.5f)), both(WHOLE)), both(-WHOLE));
+    k = make_float2(fminf(fmaxf(k.x, least), most - 1.0f), fminf(fmaxf(k.y, least), most - 1.0f));
+    const float2 mid = add2(k, both(0.5f)), d = add2(fma2(mid, both(-s), t), e);
+    const bool some = s > 0.0f;  // (a scale of 0: codes 0)
+    return add2(mid, make_float2(some && d.x != 0.0f ? copysignf(0.25f, d.x) : 0.0f, some && d.y != 0.0f ? copysignf(0.25f, d.y) : 0.0f));
 }
 
 // Codes of a row at 8 bits: s = fp16(max|x| fl(1/127)), code = x / s rounded to
@@ -171,7 +165,7 @@ __device__ __forceinline__ void encode8(float2 (&x)[D / 32][4], Lane8<D> &c, uin
             // near a border; or the scale is an fp16 subnormal or saturated, where codes can pass 127
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                r[j] = make_float2(code8_exact(x[b][j].x, s, rs) + MAGIC, code8_exact(x[b][j].y, s, rs) + MAGIC);
+                r[j] = add2(decide2(x[b][j], both(0.0f), s, mul2(x[b][j], both(rs)), -127.0f, 127.0f), both(MAGIC));
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -188,24 +182,7 @@ __device__ __forceinline__ void encode8(float2 (&x)[D / 32][4], Lane8<D> &c, uin
 // fp16(min), code = (x - z) / s rounded to nearest even, in [0, 15], decided as
 // above with x - z carried exactly.  x becomes the values held.
 template <int D>
-__device__ __forceinline__ void place4(int b, const float2 (&r)[4], Lane4<D> &c) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        // the low bits of 2^23 1.5 + code are the code: place four nibbles by sums of shifts
-        const uint32_t lo2 = (__float_as_uint(r[2 * e].x) & 15u) | (__float_as_uint(r[2 * e].y) & 15u) << 4;
-        const uint32_t hi2 = (__float_as_uint(r[2 * e + 1].x) & 15u) | (__float_as_uint(r[2 * e + 1].y) & 15u) << 4;
-        c.h[b][e] = lo2 | hi2 << 8;
-    }
-}
-template <int D>
-__device__ __forceinline__ void place4(int b, const float2 (&r)[4], Lane4K<D> &c) {
-    c.w[b] = 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        c.w[b] |= ((__float_as_uint(r[j].x) & 15u) | (__float_as_uint(r[j].y) & 15u) << 16) << (4 * j);
-}
-template <int D, typename Lane>
-__device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
+__device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane4<D> &c, uint32_t (&szb)[D / 32], uint32_t &bad) {
     constexpr int NB = D / 32;
     constexpr float MAGIC = 12582912.0f;
     if (drop_nonfinite<NB>(x)) bad |= FLAG_NONFINITE;
@@ -238,13 +215,38 @@ __device__ __forceinline__ void encode4(float2 (&x)[D / 32][4], Lane &c, uint32_
         }
         if (near > 0.5f - 0x1p-14f) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                r[j] = make_float2(code4_exact(x[b][j].x, z, s, rs) + MAGIC, code4_exact(x[b][j].y, z, s, rs) + MAGIC);
+            for (int j = 0; j < 4; ++j) {
+                // x - z = t + e exactly
+                const float2 t = add2(x[b][j], both(-z)), xx = add2(t, both(z)), u = add2(xx, make_float2(-t.x, -t.y));
+                const float2 e = add2(add2(x[b][j], make_float2(-xx.x, -xx.y)), add2(u, both(-z)));
+                r[j] = add2(decide2(t, e, s, mul2(t, both(rs)), 0.0f, 15.0f), both(MAGIC));
+            }
         }
-        place4<D>(b, r, c);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // the low bits of 2^23 1.5 + code are the code: place four nibbles by sums of shifts
+            const uint32_t lo2 = (__float_as_uint(r[2 * e].x) & 15u) | (__float_as_uint(r[2 * e].y) & 15u) << 4;
+            const uint32_t hi2 = (__float_as_uint(r[2 * e + 1].x) & 15u) | (__float_as_uint(r[2 * e + 1].y) & 15u) << 4;
+            c.h[b][e] = lo2 | hi2 << 8;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[b][j] = fma2(add2(r[j], both(-MAGIC)), both(s), both(z));
     }
+}
+
+// The codes in the order of 4-bit keys: a word's even nibbles below its odd ones.
+template <int D>
+__device__ __forceinline__ Lane4K<D> key_order(const Lane4<D> &c) {
+    Lane4K<D> k;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        uint32_t w = c.h[b][0] | c.h[b][1] << 16;
+        uint32_t x = (w ^ w >> 4) & 0x00F000F0u;
+        w ^= x ^ x << 4;
+        x = (w ^ w >> 8) & 0x0000FF00u;
+        k.w[b] = w ^ x ^ x << 8;
+    }
+    return k;
 }
 
 __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
@@ -423,75 +425,78 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
                 if (real) store_row<D>(a.q_out + (tok * a.nq + h) * D, tig, x);
                 continue;
             }
-            if constexpr (!B::Q8) {
-                if (hb) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<uint4 *>(hb + B::key(row16, (4 * b + tig) * 16)) = pack8(x[b]);
-                }
-            } else if constexpr (B::K4) {
-                Lane4K<D> c;
-                uint32_t szb[NB];
-                encode4<D>(x, c, szb, bad);
-                if (hb) {
-                    store_key4<D, FMT>(hb, row16, tig, c);
-                    if (tig == 0) {  // the scales, then the zero points
-                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) {
-                            s[i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x5410u);
-                            s[NB / 2 + i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x7632u);
-                        }
-                    }
-                }
-            } else {
-                Lane8<D> c;
-                uint32_t sb[NB];
-                encode8<D>(x, c, sb, bad);
-                if (hb) {
-                    store_key8<D, FMT>(hb, row16, tig, c);
-                    if (tig == 0) {
-                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
-                    }
-                }
-            }
-            if (a.k_out && real) store_row<D>(a.k_out + (tok * H + h) * D, tig, x);
-        } else {
-            if constexpr (!B::Q8) {
-                if (hb) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<uint4 *>(hb + B::value(row16, (4 * b + tig) * 16)) = pack8(x[b]);
-                }
-            } else if constexpr (!B::V4) {
-                Lane8<D> c;
-                uint32_t sb[NB];
-                encode8<D>(x, c, sb, bad);
-                if (hb) {
-                    store_value8<D, FMT>(hb, row16, tig, c);
-                    if (tig == 0) {
-                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
-                    }
-                }
-            } else {
-                Lane4<D> c;
-                uint32_t szb[NB];
-                encode4<D>(x, c, szb, bad);
-                if (hb) {
-                    store_value4<D, FMT>(hb, row16, tig, c);
-                    if (tig == 0) {
-                        uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) s[i] = szb[i];
-                    }
-                }
-            }
-            if (a.v_out && real) store_row<D>(a.v_out + (tok * H + h) * D, tig, x);
         }
+        if constexpr (!B::Q8) {
+            if (hb) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t at = (4 * b + tig) * 16;
+                    *reinterpret_cast<uint4 *>(hb + (is_v ? B::value(row16, at) : B::key(row16, at))) = pack8(x[b]);
+                }
+            }
+        } else if constexpr (B::K4) {
+            // Keys and values share the encoder: fetching instructions is what a step waits for most
+            // (8192 tokens into 4-bit pages: 20.8 us, 24.4 with one each; 8-bit pages gain nothing).
+            Lane4<D> c;
+            uint32_t szb[NB];
+            encode4<D>(x, c, szb, bad);
+            if (hb && is_v) {
+                store_value4<D, FMT>(hb, row16, tig, c);
+                if (tig == 0) {
+                    uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) s[i] = szb[i];
+                }
+            } else if (hb) {
+                store_key4<D, FMT>(hb, row16, tig, key_order<D>(c));
+                if (tig == 0) {  // the scales, then the zero points
+                    uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) {
+                        s[i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x5410u);
+                        s[NB / 2 + i] = __byte_perm(szb[2 * i], szb[2 * i + 1], 0x7632u);
+                    }
+                }
+            }
+        } else if (!is_v) {
+            Lane8<D> c;
+            uint32_t sb[NB];
+            encode8<D>(x, c, sb, bad);
+            if (hb) {
+                store_key8<D, FMT>(hb, row16, tig, c);
+                if (tig == 0) {
+                    uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_KS + row16 * B::SROW);
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
+                }
+            }
+        } else if constexpr (!B::V4) {
+            Lane8<D> c;
+            uint32_t sb[NB];
+            encode8<D>(x, c, sb, bad);
+            if (hb) {
+                store_value8<D, FMT>(hb, row16, tig, c);
+                if (tig == 0) {
+                    uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) s[i] = sb[2 * i] | sb[2 * i + 1] << 16;
+                }
+            }
+        } else {
+            Lane4<D> c;
+            uint32_t szb[NB];
+            encode4<D>(x, c, szb, bad);
+            if (hb) {
+                store_value4<D, FMT>(hb, row16, tig, c);
+                if (tig == 0) {
+                    uint32_t *s = reinterpret_cast<uint32_t *>(hb + B::OFF_VS + row16 * B::VSROW);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) s[i] = szb[i];
+                }
+            }
+        }
+        uint16_t *back = is_v ? a.v_out : a.k_out;
+        if (back && real) store_row<D>(back + (tok * H + h) * D, tig, x);
     }
     if (bad) pages_flag(a.pv, bad);
 }

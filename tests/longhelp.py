@@ -24,6 +24,16 @@ def held(x, fmt, values):
     return P.held4(x) if fmt == "k4v4" else P.held(x, fmt, values)
 
 
+def held8(x):
+    """What 8-bit codes hold for fp32 x, scales beyond fp16 held at its largest too."""
+    g = np.asarray(x, np.float32).reshape(*np.shape(x)[:-1], -1, 32)
+    with np.errstate(over="ignore"):
+        s = (np.abs(g).max(-1, keepdims=True) * np.float32(1.0 / 127.0)).astype(np.float16)
+    s = s.clip(-65504, 65504).astype(np.float64)
+    code = np.rint(g.astype(np.float64) / np.where(s > 0, s, 1)).clip(-127, 127)
+    return (code * s).reshape(np.shape(x))
+
+
 def zero_points(k):
     """|zero point| of every dim's group of 32."""
     g = np.asarray(k, np.float64).reshape(*k.shape[:-1], -1, 32)

@@ -93,6 +93,29 @@ def test_4bit_write_and_read_back_exact(H, d, page, lens):
     assert pg.status() == kv.KVP_OK
 
 
+@pytest.mark.parametrize("fmt", ["k8v8", "k8v4", "k4v4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_at_every_border(fmt, d):
+    """Halves of codes and their neighbours (in 16 bits ties are common), scales that are 0,
+    the smallest, subnormal and held at the largest, zero points far from the range: bit for bit."""
+    rng = np.random.default_rng(d)
+    rows = [np.full(d, 2.0 ** -26), 2.0 ** -26 * rng.choice([-1.0, 1.0], d), 2.0 ** -19 * rng.standard_normal(d),
+            3e38 * rng.uniform(-1, 1, d), np.where(np.arange(d) % 32 == 7, 3e38, rng.standard_normal(d))]
+    for size in (0.0, 1.0, -100.0, 6e4):                  # the middle, beside a range of about 4
+        rows += [size + x for x in rng.standard_normal((300, d))]
+    for scale in 2.0 ** np.arange(-24, 11, 3.0):          # whole codes, halves and what lies next to them
+        for top, off in ((127.0, -64.0), (15.0, 0.0)):
+            x = scale * (rng.integers(0, int(top), (20, d)) + rng.choice([0.0, 0.5, 0.5 - 2.0 ** -7, 0.5 + 2.0 ** -7], (20, d)) + off)
+            x[:, ::32], x[:, 1::32] = scale * top, scale * off
+            rows += list(x)
+    x = Lg.bf16(np.stack(rows)[:, None]).cuda()
+    pg = Lg.Pages(fmt, 1, d, 32, [x.shape[0]])
+    ko, vo = pg.write(x, x.neg())
+    held = {"k8v8": (Lg.held8, Lg.held8), "k8v4": (Lg.held8, P.held4), "k4v4": (P.held4, P.held4)}[fmt]
+    assert np.array_equal(ko, P.to_bf16(held[0](Lg.f64(x))))
+    assert np.array_equal(vo, P.to_bf16(held[1](-Lg.f64(x))))
+
+
 def test_4bit_keys_are_coded_from_the_turned_fp32_key():
     """Half a step of the group's range, (max - min) / 30 (its scale rounded to fp16:
     15 codes' worth of 2^-11 of it; the zero point 2^-11 of itself), fp32 angles and
