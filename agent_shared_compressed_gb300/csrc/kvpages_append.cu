@@ -23,7 +23,6 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kvp_async.cuh"
 #include "kvp_pages.cuh"
 
 namespace kvp {
@@ -36,9 +35,6 @@ constexpr int APP_WARPS = APP_THREADS / 32;
 // ragged prompts of 32 heads in k8v4 25.0 us, 19.7 with three.
 constexpr int app_blocks(int d) { return d == 128 ? 2 : 3; }
 constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
-// Rows of a warp on their way, by asynchronous copies into shared memory (8192 tokens: 41.3 us;
-// one row ahead, in registers, 44.4; 3 rows 41.9, 4 rows 43.1).
-constexpr int APP_AHEAD = 2;
 
 struct AppendArgs {
     PagesView pv;
@@ -286,8 +282,8 @@ __device__ __forceinline__ void store_row(uint16_t *row, int tig, const float2 (
 // APP_WARPS of its nq query, H key and H value rows (a warp takes a row of all of
 // the group's tokens).  A block takes an equal run of the list, as many blocks as
 // the GPU holds at once: there is no last, half-empty wave (8192 tokens: 47.5
-// against 51.2 us with a block per group).  A row's copies are issued while the rows
-// before it are worked on.
+// against 51.2 us with a block per group).  A row's loads are issued while the row
+// before it is worked on.
 template <int D, int FMT>
 __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const __grid_constant__ AppendArgs a) {
     using B = Block<D, FMT>;
@@ -304,31 +300,18 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
     int left = int(min(int64_t(a.run), a.steps - first));  // steps of this block
     int64_t grp = first / a.group_steps;
     int st = int(first % a.group_steps);
-    // A lane's pieces come to a place of its own, so that no lane waits for another's.
-    __shared__ __align__(16) uint8_t ring[APP_AHEAD * APP_WARPS * NB * 512];
-    const uint32_t mine = smem_addr(ring) + uint32_t(warp) * (NB * 512u) + uint32_t(lane) * 16u;
-    constexpr uint32_t STAGE = APP_WARPS * NB * 512u;
-    const int steps = left;
-    int64_t next_grp = grp;
-    int next_st = st, issued = 0, stage = 0;
-    auto copy_next = [&](int to) {  // (a group of copies a step, also where there is none left)
-        if (issued < steps) {
-            const int64_t tok = next_grp * APP_TOKENS + tq;
-            const int row = next_st * APP_WARPS + warp;
-            const bool is_q = row < a.nq, is_v = row >= a.nq + H, real = row < rows && tok < a.n;
-            const uint16_t *src = is_q ? a.q + tok * a.q_ts + row * a.q_hs
-                                       : (is_v ? a.v + tok * a.v_ts + (row - a.nq - H) * a.v_hs
-                                               : a.k + tok * a.k_ts + (row - a.nq) * a.k_hs);
-            if (!real) src = a.k;  // (nothing is read: zeros)
+    auto load = [&](int64_t g, int s, uint4 (&v)[NB]) {
+        const int64_t tok = g * APP_TOKENS + tq;
+        const int row = s * APP_WARPS + warp;
+        const bool is_q = row < a.nq, is_v = row >= a.nq + H;
+        const uint16_t *src = is_q ? a.q + tok * a.q_ts + row * a.q_hs
+                                   : (is_v ? a.v + tok * a.v_ts + (row - a.nq - H) * a.v_hs
+                                           : a.k + tok * a.k_ts + (row - a.nq) * a.k_hs);
+        const bool real = row < rows && tok < a.n;
+        // (by way of L2: 8192 tokens 45.8 us, 47.6 with ld_once_v4; pages_read the other
+        // way round, 62.4 and 61.5)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                             ::"r"(mine + uint32_t(to) * STAGE + uint32_t(b) * 512u), "l"(src + 32 * b + 8 * tig), "r"(real ? 16u : 0u)
-                             : "memory");
-            if (++next_st == a.group_steps) next_st = 0, ++next_grp;
-            ++issued;
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int b = 0; b < NB; ++b) v[b] = real ? ld_l2_v4(src + 32 * b + 8 * tig) : make_uint4(0, 0, 0, 0);
     };
     if (threadIdx.x < D / 2) {
         turns[threadIdx.x] = a.turn[threadIdx.x];
@@ -336,8 +319,8 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
     }
     const int log_half = a.rot == 128 ? 6 : 5;
     wait_for_previous();
-#pragma unroll
-    for (int i = 0; i < APP_AHEAD; ++i) copy_next(i);
+    uint4 in[NB];
+    load(grp, st, in);
     const bool match = pages_match(a.pv);
     for (int i = threadIdx.x; i < 2 * D; i += APP_THREADS) {
         const uint16_t *w = i < D ? a.q_norm : a.k_norm;
@@ -380,16 +363,9 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const
         const int r = st * APP_WARPS + warp;
         if (++st == a.group_steps) st = 0, ++grp, fresh = true;
         float2 x[NB][4];
-        asm volatile("cp.async.wait_group %0;" ::"n"(APP_AHEAD - 1) : "memory");
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint4 v;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(mine + uint32_t(stage) * STAGE + uint32_t(b) * 512u) : "memory");
-            unpack8(v, x[b]);
-        }
-        copy_next(stage);
-        if (++stage == APP_AHEAD) stage = 0;
+        for (int b = 0; b < NB; ++b) unpack8(in[b], x[b]);
+        if (left > 1) load(grp, st, in);
         if (r >= rows) continue;
         const bool is_q = r < a.nq, is_v = r >= a.nq + H;
         const int h = is_q ? r : (is_v ? r - a.nq - H : r - a.nq);
