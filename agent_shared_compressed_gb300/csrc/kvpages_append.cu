@@ -29,11 +29,12 @@ namespace kvp {
 
 constexpr int APP_THREADS = 256;
 constexpr int APP_WARPS = APP_THREADS / 32;
-// Blocks of an SM: what 123 (head_dim 128) and 80 registers a thread allow.  With three of
+// Blocks of an SM: what 128 (head_dim 128), 80 and 64 registers a thread allow.  With three of
 // head_dim 128, at 80 registers, which spill, 8192 tokens took 62 us where two took 47, with
-// blocks of 10 warps 47.4 against 46.8.  Of head_dim 64 four, at 64 registers, spill too: three
-// ragged prompts of 32 heads in k8v4 25.0 us, 19.7 with three.
-constexpr int app_blocks(int d) { return d == 128 ? 2 : 3; }
+// blocks of 10 warps 47.4 against 46.8.  Of head_dim 64 four spill where there are codes to form
+// (8192 tokens of 32 heads in 4 bits 38.0 us, 26.4 with three) and gain where there are none (three
+// ragged prompts of 32 heads in 16 bits 23.6 us, 26.4 with three, 31.9 with five).
+constexpr int app_blocks(int d, int format) { return d == 128 ? 2 : (format == KVP_PAGES_BF16 ? 4 : 3); }
 constexpr int APP_TOKENS = 8;  // tokens of a block: one per lane quad of a warp
 
 struct AppendArgs {
@@ -285,7 +286,7 @@ __device__ __forceinline__ void store_row(uint16_t *row, int tig, const float2 (
 // against 51.2 us with a block per group).  A row's loads are issued while the row
 // before it is worked on.
 template <int D, int FMT>
-__global__ void __launch_bounds__(APP_THREADS, app_blocks(D)) pages_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(APP_THREADS, app_blocks(D, FMT)) pages_append(const __grid_constant__ AppendArgs a) {
     using B = Block<D, FMT>;
     constexpr int NB = D / 32;
     // rows padded to start on other banks; read as float4
@@ -668,7 +669,7 @@ int kvpages_append_axes(void *pages, const kvp_pages_config *cfg, int layer, int
     const int rows = n_q_heads + 2 * cfg->n_kv_heads;
     a.group_steps = (rows + APP_WARPS - 1) / APP_WARPS;
     a.steps = (int64_t(n_tokens) + APP_TOKENS - 1) / APP_TOKENS * a.group_steps;
-    const int64_t blocks = std::min<int64_t>(a.steps, int64_t(sm_count()) * app_blocks(cfg->head_dim));
+    const int64_t blocks = std::min<int64_t>(a.steps, int64_t(sm_count()) * app_blocks(cfg->head_dim, cfg->format));
     a.run = int((a.steps + blocks - 1) / blocks);
     const unsigned grid = unsigned((a.steps + a.run - 1) / a.run);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
