@@ -753,9 +753,11 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
                 return t >= lim || (WIN && a.window && t >= a.sinks && t < max(lim, 0) - a.window);
             };
             if (Q8 && tail) {
-                // tokens never written: their value scales (and zero points) may be anything
+                // tokens that no query sees, which may never have been written: their value scales (and
+                // zero points) may be anything, and 0 times Inf or NaN is NaN
                 const int nv = len - t0;
-                if (lane < PAGES_BLOCK * UB && (lane >= nv || !((here >> (lane / PAGES_BLOCK)) & 1u))) {
+                const bool gap = WIN && t0 + lane >= a.sinks && lane < nv - (a.m - 1) - a.window;
+                if (lane < PAGES_BLOCK * UB && (lane >= nv || gap || !((here >> (lane / PAGES_BLOCK)) & 1u))) {
                     const uint32_t sa = at0 + uint32_t(lane / PAGES_BLOCK) * B::BYTES + B::OFF_VS +
                                         uint32_t(lane % PAGES_BLOCK) * B::VSROW;
 #pragma unroll

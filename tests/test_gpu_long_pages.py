@@ -261,6 +261,32 @@ def test_window_leaves_unseen_values_out():
         assert np.all(np.isinf(out[0, 0, 2:, 3])) and np.isinf(out).sum() == 2 and not np.isnan(out).any()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,G,page,lens,m,window,sinks,roomy", [
+    (2, 4, 16, [200, 3, 90], 1, 37, 5, False), (1, 1, 64, [333, 61], 1, 50, 33, True),         # tiles of 4 rows
+    (1, 8, 32, [150, 40], 1, 21, 0, True), (2, 4, 64, [777, 64, 31], 2, 100, 7, False),        # of 8
+    (1, 8, 16, [300, 129], 2, 19, 3, False), (2, 3, 128, [513, 40, 256], 5, 77, 40, True),     # of 16
+    (1, 1, 16, [2000], 64, 20, 33, False), (1, 4, 64, [9000, 8191], 1, 6001, 9, False)])
+def test_window_over_tokens_never_written(fmt, d, H, G, page, lens, m, window, sinks, roomy):
+    """Tokens that no query sees are not written at all (a negative slot): the NaN patterns that
+    lie in their places, in blocks that hold seen tokens too, have no part.  The result is that of
+    pages which hold every token, bit for bit."""
+    k, v = _kv(sum(lens), H, d, m + d)
+    q = Lg.bf16(np.random.default_rng(G).standard_normal((len(lens), m, H * G, d))).cuda()
+    unseen = torch.tensor([sinks <= t < n - (m - 1) - window for n in lens for t in range(n)], device="cuda")
+    assert bool(unseen.any())
+    got = []
+    for leave_out in (False, True):
+        pg = Lg.Pages(fmt, H, d, page, lens, max_pages=20000 // page if roomy else None)
+        if leave_out:
+            pg.slots[unseen] = -1
+        pg.write(k, v)
+        got.append(pg.attend(q, 1 / math.sqrt(d), window, sinks))
+        assert pg.status() == kv.KVP_OK
+    assert np.array_equal(got[0][0], got[1][0]) and np.array_equal(got[0][1], got[1][1])
+
+
 def test_window_in_a_graph_on_another_stream():
     """Captured once, replayed as the sequence grows past its window; another stream than
     the current one, beside a second graph with a workspace of its own."""
