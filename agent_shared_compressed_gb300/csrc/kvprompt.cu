@@ -28,6 +28,11 @@
 // A row's reference (its largest score so far) is raised only when a score passes it
 // by 2^8, so that O is hardly ever rescaled; weights are taken relative to 2^40 times
 // the reference, so that sums of up to 2^30 values up to bf16's largest stay finite.
+// A weight's exponent is one multiply-add of a product x = q . k, scale x - (reference + 40).
+// The reference is a rounded product there, the multiply-add's own is not, and the sum with
+// 40 is rounded: from scores of some 2^31 on either is off by as much as exponents reach.  So
+// rows keep their largest x, and from references of 2^12 on (whose last bit is 2^-11) it is
+// subtracted first: scale (x - x_largest) - 40.
 // Weights are rounded to bf16 for the value product (2^-9 at most, of either sign; the
 // sum takes them before that): a second product for the rest of them would cost
 // a quarter of the tensor time for less than the result's own rounding to bf16.
@@ -64,7 +69,7 @@ constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
 constexpr int PT_FEW = 32;
 constexpr int PT_MOST = 1 << 30;              // rows: sums and differences of places fit 32 bits
 constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
-constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f;
+constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f, PT_FAR = 4096.0f;
 
 struct PromptArgs {
     CUtensorMap q_map, k_map, v_map;
@@ -709,7 +714,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             if (half == 1 && w.count <= a.half_tokens) continue;
             const bool real = tl < a.half_tokens && i < w.count;
             const int p = w.p_first + (real ? i : w.count - 1);
-            float ref = -INFINITY, sum = 0.0f;
+            float raw = -INFINITY, sum = 0.0f;  // the reference, over the scale
+            // What is added to a score for a weight's exponent; whether a row's reference is far from 0.
+            auto offset = [&]() { return -(raw == -INFINITY ? 0.0f : raw * a.scale2) - PT_BIAS; };
+            auto is_far = [&]() { return real && raw > -INFINITY && fabsf(raw * a.scale2) >= PT_FAR; };
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
             const int in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
             const int in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
@@ -725,14 +733,19 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     float top = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        xf[c] = c < w.a_end ? (a.flat ? 0.0f : xf[c] * a.scale2) : -INFINITY;
+                        xf[c] = c < w.a_end ? (a.flat ? 0.0f : xf[c]) : -INFINITY;
                         top = fmaxf(top, xf[c]);
                     }
-                    ref = top;
-                    const float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                    raw = top;
+                    float off = offset();
+                    if (__any_sync(0xffffffffu, is_far())) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) xf[c] -= raw == -INFINITY ? 0.0f : raw;
+                        off = -PT_BIAS;
+                    }
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float y0 = pt_exp2(xf[2 * c] + off), y1 = pt_exp2(xf[2 * c + 1] + off);
+                        const float y0 = pt_exp2(fmaf(xf[2 * c], a.scale2, off)), y1 = pt_exp2(fmaf(xf[2 * c + 1], a.scale2, off));
                         sum += y0 + y1;
                         x[c] = pack_bf16x2(y0, y1);
                     }
@@ -764,7 +777,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 float *xf = reinterpret_cast<float *>(x);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
-                float off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                float off = offset();
+                // what a score has to pass for a look at the reference (a far one is looked at in every tile)
+                const float bar = is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK;
                 tc_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
@@ -785,14 +800,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 for (int c = 0; c < 4; ++c) m[c] = fmaxf(xf[2 * c], xf[2 * c + 1]);
 #pragma unroll
                 for (int c = 4; c < 64; ++c) m[c & 3] = max3(m[c & 3], xf[2 * c], xf[2 * c + 1]);
-                const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * a.scale2;
-                const bool raise = top > ref + PT_SLACK || (ref == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float f = raise ? pt_exp2(ref - top) : 1.0f;
-                    if (raise) ref = top;
-                    off = -(ref == -INFINITY ? 0.0f : ref) - PT_BIAS;
+                const float most = fmaxf(max3(m[0], m[1], m[2]), m[3]), top = most * a.scale2;
+                if (__any_sync(0xffffffffu, top > bar)) {
+                    const bool raise = top > bar && (most - raw) * a.scale2 > PT_SLACK;
+                    const float f = raise ? pt_exp2((raw - most) * a.scale2) : 1.0f;
+                    if (raise) raw = most;
+                    off = offset();
                     sum *= f;
-                    if (j > 0) {
+                    if (j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
@@ -803,6 +818,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                             tc_st32(o_at + uint32_t(c), o);
                         }
+                    }
+                    if (__any_sync(0xffffffffu, is_far())) {
+                        const float less = raw == -INFINITY ? 0.0f : -raw;
+#pragma unroll
+                        for (int c = 0; c < 128; c += 2) {
+                            const float2 y = __fadd2_rn(make_float2(xf[c], xf[c + 1]), make_float2(less, less));
+                            xf[c] = y.x, xf[c + 1] = y.y;
+                        }
+                        off = -PT_BIAS;
                     }
                 }
                 float2 t0 = make_float2(sum, 0.0f), t1 = make_float2(0.0f, 0.0f);
@@ -876,6 +900,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                 tc_wait_st();
             }
             if (ok) {
+                const float ref = raw * a.scale2;
                 const uint64_t row = uint64_t(w.row + i) * uint32_t(a.nq) + uint32_t(w.h * a.G + r - tl * a.G);
                 // Each thread stores its own row, 32 bytes (a sector) at a time.  The code is short, as it
                 // is met with once a block and has to be fetched for that.

@@ -217,6 +217,56 @@ def test_scores_that_rise_and_fall():
         c.both(scale=0.5)
 
 
+def _exact_scores(c, size, seed=0):
+    """Queries and keys whose products and sums fp32 holds exactly: `size` times small whole numbers."""
+    rng = np.random.default_rng(seed)
+    c.q.copy_(Lg.bf16(size * rng.integers(-1, 2, c.q.shape)))
+    c.k.copy_(Lg.bf16(size * rng.integers(-3, 4, c.k.shape)))
+
+
+@pytest.mark.parametrize("size", [2.0 ** x for x in (4, 8, 9, 10, 13, 15, 17, 30, 59)])
+def test_large_scores(size):
+    """Scores up to 2^123: sums of products are exact, and keys that differ do so by a twelfth of
+    size^2 or more: a row's result is the mean of the values whose keys score most."""
+    for seqs, H, G, d, window, sinks in (([(300, 40), (140, 900)], 2, 4, 128, 0, 0), ([(300, 0), (5, 700)], 3, 1, 64, 70, 3),
+                                         ([(200, 513)], 1, 3, 128, 300, 17), ([(3, 30000)], 1, 2, 64, 0, 0)):
+        c = Call(seqs, H, G, d, seed=d + window)
+        _exact_scores(c, size)
+        for scale, base in ((1 / math.sqrt(d), False), (-1 / math.sqrt(d), True)):
+            bo, bl = c.base() if base else (None, None)
+            out, lse = c.run(scale, window, sinks, (bo, bl))
+            assert kv.kvprompt_status(c.error) == kv.KVP_OK
+            q, k, v = Lg.f64(c.q), Lg.f64(c.k), Lg.f64(c.v)
+            for b, (new, past) in enumerate(seqs):
+                i, t = slice(c.q_first[b], c.q_first[b + 1]), slice(c.k_first[b], c.k_first[b] + new + past)
+                ref, ref_lse, mass, reach = Lg.prompt(q[i], k[t], v[t], past, window, sinks, scale)
+                if base:
+                    ref, ref_lse, mass = Lg.join(ref, ref_lse, mass, bo[i].cpu().numpy().astype(np.float64),
+                                                 bl[i].cpu().numpy().astype(np.float64))
+                # (what the scale's and the product's roundings make is the same for keys of one score;
+                # of the lse they are 2^-22)
+                Lg.check(out[i], lse[i], ref, ref_lse, mass, 0 * reach, WEIGHTS)
+
+
+@pytest.mark.parametrize("size", [1e3, 4e4, 1e5, 1e9])
+def test_large_random_scores(size):
+    """Normal queries and keys of any size: fp32 does not say which of two keys scores more, but
+    weights still make up a mean: of ones it is one (the weights' rounding and the result's, 2^-8
+    each), of bf16's largest finite."""
+    for seqs, H, G, d, window, sinks in (([(300, 40), (140, 900)], 2, 4, 128, 0, 0), ([(300, 0), (5, 700)], 3, 1, 64, 70, 3),
+                                         ([(3, 30000)], 1, 2, 64, 0, 0)):
+        c = Call(seqs, H, G, d, seed=d)
+        c.q.mul_(size)
+        c.k.mul_(size)
+        c.v.fill_(1.0)
+        out, lse = c.run(1 / math.sqrt(d), window, sinks)
+        assert np.all(np.abs(out - 1.0) <= 2.0 ** -7)
+        c.check(out, lse, 1 / math.sqrt(d), window, sinks)                     # the lse
+        c.v.fill_(3.3895313892515355e38)
+        out, _ = c.run(1 / math.sqrt(d), window, sinks)
+        assert np.all(np.isfinite(out)) and np.all(out >= 3.3e38)
+
+
 def test_shared_rows():
     """Two sequences over the same keys (a shared prefix), one over a part of them."""
     c = Call([(40, 100), (40, 100), (10, 20)], 2, 2, 128)
