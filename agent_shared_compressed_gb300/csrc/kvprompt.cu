@@ -336,7 +336,7 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block,
         const int nlo = n ? min(lo + n * step, hi) : lo, nhi = n < 32 ? min(lo + (n + 1) * step, hi) - 1 : hi;
         lo = nlo, hi = max(nlo, nhi);
     }
-    const PromptSeq s = prompt_seq(a, lo, lane == 0);
+    const PromptSeq s = prompt_seq(a, lo, false);  // (prompt_report says what is wrong)
     const int64_t i0 = int64_t(slot - lo - max(s.first, 0) / tokens) * tokens;
     if (i0 < 0 || i0 >= s.n) return false;
     w.valid = 1;
@@ -353,6 +353,15 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block,
     const int all = w.na + tiles_of(w.b_end - w.b0);
     w.j0 = int(int64_t(all) * w.split / a.splits), w.nt = int(int64_t(all) * (w.split + 1) / a.splits) - w.j0;
     return true;
+}
+
+// Reports a sequence with numbers outside the tensors, or that decrease: block numbers are at least
+// as many as sequences, and some of them have one each to look at (the search above need not meet
+// a sequence whose numbers are out of order).
+__device__ __forceinline__ void prompt_report(const PromptArgs &a, uint32_t block) {
+    const uint32_t each = uint32_t(a.splits) * uint32_t(a.H);
+    const int b = a.tiles - 1 - int(block / each);
+    if (block % each == 0u && b < a.nseq) prompt_seq(a, b, true);
 }
 
 // Waits until the barrier's phase is over; gives up when the limit or another warp's
@@ -502,6 +511,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     fence_proxy_async();  // the former answer has been read
                     asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
                                  ::"r"(sm + T::ANSWER), "r"(sm + T::NEXT) : "memory");
+                    prompt_report(a, block);
                 }
                 __syncwarp();
                 ++asked;

@@ -571,7 +571,8 @@ size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape);
  *    (sequences may share rows).  A [heads][tokens][head_dim] tensor is rows too
  *    (kvp_rows' strides).  Query head j reads KV head j / (n_q_heads / n_kv_heads).
  *    Strides of more than one token or head are positive and below 2^38.
- *  q_first: device int32[n_seqs + 1], not decreasing; k_first, k_lens: device
+ *  q_first: device int32[n_seqs + 1], not decreasing (KVP_ERR_PAGE where it does; which
+ *    of the sequences' rows are written is then left open); k_first, k_lens: device
  *    int32[n_seqs].
  *  New token i of n is at place p = k_lens[b] - n + i and sees the places t <= p; with
  *    a window > 0 of those the newest `window` (its own among them: t > p - window)

@@ -379,6 +379,25 @@ def test_ranges_outside_the_tensors():
     assert kv.kvprompt_status(c.error) in (kv.KVP_OK, kv.KVP_ERR_PAGE)
 
 
+def test_numbers_of_new_tokens_that_decrease():
+    """They are reported wherever they are, and nothing outside the calls' rows is written (a
+    sequence alone: nothing at all)."""
+    c = Call([(40, 10)], 2, 2, 64)
+    c.q_first_d[0] = 50
+    c.run(0.1)
+    assert kv.kvprompt_status(c.error) == kv.KVP_ERR_PAGE
+    assert bool((c.raw[0] == 0x7F).all()) and bool((c.raw[1] == 0x7F).all())
+    for seqs, at, value in (([(500, 0), (20, 0), (80, 0)], 2, 100), ([(500, 0), (20, 0), (80, 0)], 1, 590),
+                            ([(3, 20000), (2, 0), (700, 0), (6, 0)], 3, 4), ([(7, 2)] * 700, 350, 3), ([(7, 2)] * 700, 699, 0),
+                            ([(7, 2)] * 700, 0, 4000), ([(7, 2)] * 700, 40, 4899)):
+        c = Call(seqs, 2, 2, 64, gap=3)
+        c.q_first_d[at] = value
+        c.run(0.1)
+        assert kv.kvprompt_status(c.error) == kv.KVP_ERR_PAGE, (at, value)
+        used = sum(a for a, _ in seqs) * c.nq
+        assert bool((c.raw[0][used * c.d * 2:] == 0x7F).all()) and bool((c.raw[1][used * 4:] == 0x7F).all())
+
+
 def test_many_sequences():
     """More sequences than tiles, empty ones among them."""
     rng = np.random.default_rng(0)
