@@ -33,9 +33,9 @@
 // 40 is rounded: from scores of some 2^31 on either is off by as much as exponents reach.  So
 // rows keep their largest x, and from references of 2^12 on (whose last bit is 2^-11) it is
 // subtracted first: scale (x - x_largest) - 40.
-// Weights are rounded to bf16 for the value product (2^-9 at most, of either sign; the
+// Weights are rounded to bf16 for the value product (2^-8 at most, of either sign; the
 // sum takes them before that): a second product for the rest of them would cost
-// a quarter of the tensor time for less than the result's own rounding to bf16.
+// a quarter of the tensor time for no more than the result's own rounding to bf16.
 //
 // Values that some of the rows do not see must not meet them in the product, not even
 // with weight 0, if they are Inf or NaN.  Rows of a tile that nobody sees are zeroed in
@@ -135,7 +135,7 @@ __device__ __forceinline__ void st_sectors(void *to, const uint32_t *v, uint32_t
 }
 
 // A finite mean of bf16 values is not beyond bf16's largest (the rounded weights' sum
-// may be, by 2^-9).
+// may be, by 2^-8).
 __device__ __forceinline__ float within_bf16(float y) {
     constexpr float MOST = 3.3895313892515355e38f;
     return fabsf(y) < INFINITY ? fminf(fmaxf(y, -MOST), MOST) : y;

@@ -593,7 +593,7 @@ size_t kvprompt_workspace_bytes(const kvp_prompt_shape *shape);
  * give finite results up to bf16's largest.
  * Scores are products of bf16 summed in fp32; softmax statistics are fp32,
  * exponentials the hardware's in base 2 (2^-22); weights enter the value product as
- * bf16 (2^-9, their sum before that), relative to 2^40 times the row's largest: those
+ * bf16 (2^-8, their sum before that), relative to 2^40 times the row's largest: those
  * below 2^-86 of it may count as zero, as may products with values below 2^-86.  The
  * kernel waits for its copies at most about half a second; should a wait run out, the
  * outputs are unspecified and kvprompt_status reports KVP_ERR_TIMEOUT. */

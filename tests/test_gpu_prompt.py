@@ -207,6 +207,31 @@ def test_sharp_negative_and_zero_scales():
         Call([(150, 60)], 2, 2, 128, spread=2.0).both(scale=scale)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seqs", [[(200, 300)], [(16, 9000)]], ids=str)
+def test_weights_and_results_are_rounded_once(d, seqs):
+    """The mean square of the error is what one bf16 rounding of every weight and one of the result
+    make: a weight's is even within half a step, 2^-8 / m of it for a significand m, whose 1 / m^2
+    is 3 / (8 log 2) on average (m even by its logarithm); a result's has a twelfth of its step
+    squared.  Both parts are about as large; a second rounding of either would make 1.5 of it."""
+    c = Call(seqs, 2, 4, d, seed=d)
+    scale = 1 / math.sqrt(d)
+    out, _ = c.run(scale)
+    q, k, v = Lg.f64(c.q), Lg.f64(c.k), Lg.f64(c.v)
+    (new, past), = seqs
+    see = np.arange(new + past)[None] <= past + np.arange(new)[:, None]
+    off = expected = 0.0
+    for j in range(c.nq):
+        s = np.where(see, scale * (q[:new, j] @ k[:, j // 4].T), -np.inf)
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        ref = p @ v[:, j // 4]
+        step = 2.0 ** (np.floor(np.log2(np.abs(ref))) - 7)
+        off += ((out[:new, j] - ref) ** 2).sum()
+        expected += (2.0 ** -16 / (8 * math.log(2)) * (p ** 2 @ v[:, j // 4] ** 2) + step ** 2 / 12).sum()
+    assert off <= 1.25 * expected, off / expected
+
+
 def test_scores_that_rise_and_fall():
     """The running maximum raised in every tile, by hundreds; and falling ones."""
     for order in (1, -1):
