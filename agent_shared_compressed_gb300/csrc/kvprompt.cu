@@ -73,8 +73,8 @@ constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f, PT_FAR = 4096.0f;
 
 struct PromptArgs {
     CUtensorMap q_map, k_map, v_map;
-    const uint16_t *q, *k, *v;
-    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
+    const uint16_t *v;
+    int64_t v_ts, v_hs;  // strides in elements
     const int32_t *q_first, *k_first, *k_lens;
     const float *base_out, *base_lse;
     uint16_t *out;
@@ -327,7 +327,7 @@ __device__ __forceinline__ bool prompt_work(const PromptArgs &a, uint32_t block,
     const int lane = threadIdx.x & 31, tokens = 2 * a.half_tokens;
     w.split = int(block % uint32_t(a.splits));
     w.h = int(block / uint32_t(a.splits) % uint32_t(a.H));
-    const int slot = a.tiles - 1 - int(block / uint32_t(a.splits) / uint32_t(a.H));  // the longest first
+    const int slot = a.tiles - 1 - int(block / uint32_t(a.splits) / uint32_t(a.H));  // the last tokens first: of one prompt they see the most
     int lo = 0, hi = a.nseq - 1;  // the last b with its first tile at or before this one, 32 places at a time
     while (lo < hi) {
         const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
         const uint32_t s_at = uint32_t(half) * 128u + lanes, o_at = 256u + uint32_t(half) * D + lanes;
         const int tl = r / a.G, i = half * a.half_tokens + tl;  // the row's token
         bool ok = true;
-        uint32_t n = 0, done = 0, ended = 0;  // ring places before this work's; parities of the half's tiles and results
+        uint32_t done = 0, ended = 0;  // parities of the half's tiles and results
         PromptWork w;
         // Whether any thread of the half says so.  What ends a half's work is decided by all of its
         // warps: one that gave up by itself would be missing from the others' barriers.
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                          : "=r"(any) : "r"(uint32_t(says)), "r"(1 + half) : "memory");
             return any != 0u;
         };
-        for (uint32_t k = 0; !any_of_half(!ok || !next_work(k, w)); n += 2u * uint32_t(w.nt), ++k) {
+        for (uint32_t k = 0; !any_of_half(!ok || !next_work(k, w)); ++k) {
             if (half == 1 && w.count <= a.half_tokens) continue;
             const bool real = tl < a.half_tokens && i < w.count;
             const int p = w.p_first + (real ? i : w.count - 1);
@@ -1179,8 +1179,6 @@ int kvprompt_attend(const kvp_prompt_shape *shape, const kvp_rows *q, const kvp_
     if (ws_bytes < kvprompt_workspace_bytes(shape)) return KVP_ERR_SIZE;
     if (shape->n_seqs == 0 || shape->n_q_tokens == 0) return KVP_OK;
     PromptArgs a;
-    a.q = static_cast<const uint16_t *>(q->ptr), a.q_ts = q->token_stride, a.q_hs = q->head_stride;
-    a.k = static_cast<const uint16_t *>(k->ptr), a.k_ts = k->token_stride, a.k_hs = k->head_stride;
     a.v = static_cast<const uint16_t *>(v->ptr), a.v_ts = v->token_stride, a.v_hs = v->head_stride;
     a.q_first = q_first, a.k_first = k_first, a.k_lens = k_lens;
     a.base_out = base_out, a.base_lse = base_lse;
