@@ -741,12 +741,12 @@ __global__ void __launch_bounds__(PatShape<D, FMT, RC>::WARPS * 32, 1)
         if (here) {
             const uint32_t at0 = ring + slot * SM::SLOT;
             int t0 = int(place - SM::ITEM) * (PAGES_BLOCK * UB);
-            // some query does not see all of the unit's tokens
-            bool tail = t0 + PAGES_BLOCK * UB > len - (a.m - 1) || (UB == 2 && here != 3u);
+            // some query does not see all of the unit's tokens (whose end may be 2^31)
+            bool tail = uint32_t(t0) + PAGES_BLOCK * UB > uint32_t(max(len - (a.m - 1), 0)) || (UB == 2 && here != 3u);
             if constexpr (WIN) {
                 if (place - SM::ITEM >= span.head) t0 += int(span.skip) * (PAGES_BLOCK * UB);
-                tail = t0 + PAGES_BLOCK * UB > len - (a.m - 1) || (UB == 2 && here != 3u) ||
-                       (a.window && t0 < len - a.window && t0 + PAGES_BLOCK * UB > a.sinks);
+                tail = uint32_t(t0) + PAGES_BLOCK * UB > uint32_t(max(len - (a.m - 1), 0)) || (UB == 2 && here != 3u) ||
+                       (a.window && t0 < len - a.window && uint32_t(t0) + PAGES_BLOCK * UB > uint32_t(a.sinks));
             }
             // whether the query of `lim` does not see token t
             auto hidden = [&](int t, int lim) {

@@ -287,6 +287,40 @@ def test_window_over_tokens_never_written(fmt, d, H, G, page, lens, m, window, s
     assert np.array_equal(got[0][0], got[1][0]) and np.array_equal(got[0][1], got[1][1])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "k8v4", "k4v4"])
+@pytest.mark.parametrize("past", [1, 2, 5, 16, 32, 33])
+def test_lengths_up_to_the_largest(fmt, past):
+    """A sequence of 2^31 - past tokens, all of them in one shared page but the last ones, behind
+    which nothing has been written: its newest tokens by a window, and all of it."""
+    H, d, page, window, sinks = 1, 64, 1024, 70, 3
+    pg = Lg.Pages(fmt, H, d, page, [page, page])
+    k, v = _kv(2 * page, H, d, past)
+    shared, last = (int(pg.table[b, 0]) for b in (0, 1))
+    pg.slots[2 * page - past:] = -1
+    pg.write(k, v)
+    pg.max_pages, pg.lens = 1 << 21, [2 ** 31 - past]
+    pg.table_d = torch.full((1, 1 << 21), shared, dtype=torch.int32, device="cuda")
+    pg.table_d[0, -1] = last
+    pg.lens_d = torch.tensor(pg.lens, dtype=torch.int32, device="cuda")
+    hk, hv = Lg.held(Lg.f64(k), fmt, False), Lg.held(Lg.f64(v), fmt, True)
+    q = Lg.bf16(np.random.default_rng(past).standard_normal((1, 2, 4, d))).cuda()
+    out, lse = pg.attend(q, 0.1, window, sinks)
+    n = 2 * page - past                                                        # as two pages: the same tokens are seen
+    ro, rl, mass, reach = Lg.rows(Lg.f64(q[0]), hk[:n], hv[:n], [n - 2, n - 1], window, sinks, 0.1,
+                                  2 * Lg.zero_points(hk[:n]) if fmt == "k4v4" else None)
+    if fmt == "k4v4":
+        mass = _middle_mass(Lg.f64(q[0]), hk[:n], hv[:n], [n - 2, n - 1], window, sinks, 0.1, mass)
+    Lg.check(out[0], lse[0], ro, rl, mass, reach, WEIGHTS)
+    if past == 5:
+        # the shared page's tokens, 2^21 - 1 times: a warp adds some 2^16 weights one after the other
+        # (2^-24 of half of their sum each, on average, if all are cut to one side: 2^-9)
+        out, lse = pg.attend(q, 0.1, 0, 0, plain=True)
+        ro, rl, mass, reach = Lg.rows(Lg.f64(q[0]), hk[:page], hv[:page], [page] * 2, 0, 0, 0.1)
+        assert np.all(np.abs(out[0] - ro) <= 2.0 ** -6 * np.abs(v.float().cpu().numpy()).max())
+        assert np.all(np.abs(lse[0] - rl - 21 * math.log(2)) <= 2.0 ** -8)
+    assert pg.status() == kv.KVP_OK
+
+
 def test_window_in_a_graph_on_another_stream():
     """Captured once, replayed as the sequence grows past its window; another stream than
     the current one, beside a second graph with a workspace of its own."""
