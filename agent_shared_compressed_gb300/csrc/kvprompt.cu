@@ -725,9 +725,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             const bool real = tl < a.half_tokens && i < w.count;
             const int p = w.p_first + (real ? i : w.count - 1);
             float raw = -INFINITY, sum = 0.0f;  // the reference, over the scale
-            // What is added to a score for a weight's exponent; whether a row's reference is far from 0.
+            // What is added to a score for a weight's exponent; whether the reference is far from 0; the score
+            // that has to be passed for a look at the reference (a far one is looked at in every tile).
             auto offset = [&]() { return -(raw == -INFINITY ? 0.0f : raw * a.scale2) - PT_BIAS; };
             auto is_far = [&]() { return real && raw > -INFINITY && fabsf(raw * a.scale2) >= PT_FAR; };
+            auto bar_of = [&]() { return is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK; };
+            float bar = -INFINITY;
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
             const int in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
             const int in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
@@ -748,6 +751,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                     raw = top;
                     float off = offset();
+                    bar = bar_of();
                     if (__any_sync(0xffffffffu, is_far())) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) xf[c] -= raw == -INFINITY ? 0.0f : raw;
@@ -788,8 +792,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32u * uint32_t(c), x + 32 * c);
                 float off = offset();
-                // what a score has to pass for a look at the reference (a far one is looked at in every tile)
-                const float bar = is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK;
                 tc_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) tc_landed(x + 16 * c);
@@ -816,6 +818,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     const float f = raise ? pt_exp2((raw - most) * a.scale2) : 1.0f;
                     if (raise) raw = most;
                     off = offset();
+                    bar = bar_of();
                     sum *= f;
                     if (j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
