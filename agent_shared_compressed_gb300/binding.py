@@ -339,6 +339,15 @@ class _Types:
 _T = _Types()
 
 
+def _strides(x):
+    """A rows tensor's strides; one without elements may have any, and has those of a
+    contiguous one here."""
+    if x.numel():
+        return x.stride()
+    _, h, d = x.shape
+    return h * d, d, 1
+
+
 def rows(x, token_stride=None, head_stride=None):
     """kvp_rows of a [tokens][heads][head_dim] bf16 tensor (a strided view will
     do; its last dimension contiguous), or of an address with its strides."""
@@ -346,7 +355,7 @@ def rows(x, token_stride=None, head_stride=None):
         return x
     if token_stride is not None:
         return Rows(_addr(x), token_stride, head_stride)
-    t, h, e = x.stride()
+    t, h, e = _strides(x)
     if e != 1:
         raise ValueError("the last dimension of a rows tensor is contiguous, got strides %r" % ((t, h, e),))
     if x.dtype is not _T.bf16:
@@ -368,7 +377,7 @@ def _rows(x, tokens, heads, dim, name):
         return _addressof(x)
     if x is None:
         return None
-    shape, (t, h, e) = x.shape, x.stride()
+    shape, (t, h, e) = x.shape, _strides(x)
     if e != 1 or x.dtype is not _T.bf16:
         rows(x)  # raises
     _rows_fit(shape, tokens, heads, dim, name)

@@ -65,3 +65,16 @@ def test_tensors_that_do_not_hold_it():
                 dict(err=torch.zeros(1, dtype=torch.int64)), dict(ws=torch.zeros(16, dtype=torch.uint8), wb=17)):
         with pytest.raises(ValueError):
             call(**bad)
+
+
+def test_tensors_without_elements():
+    """No new tokens, or no keys: such a tensor's strides say nothing (one made from an empty
+    numpy array has strides of 0)."""
+    for empty in (torch.empty(0, 8, 128, dtype=torch.bfloat16),
+                  torch.as_strided(torch.empty(1, dtype=torch.bfloat16), (0, 8, 128), (0, 0, 0))):
+        assert call(shape=(2, 0, 9, 8, 4, 128), q=empty) == kv.KVP_OK
+        assert call(shape=(2, 0, 0, 8, 4, 128), q=empty, k=empty[:, :4], v=empty[:, :4]) == kv.KVP_OK
+        r = kv.rows(empty)
+        assert (r.token_stride, r.head_stride) == (1024, 128)
+        with pytest.raises(ValueError):
+            call(shape=(2, 1, 9, 8, 4, 128), q=empty)
