@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(CARD_THREADS, 4) card_unpack_rope(const __grid
 // warp fit 96 KB per block and every part of a record starts on a 16-byte
 // boundary (d = 128, or H even).
 // ---------------------------------------------------------------------------
-constexpr uint32_t CARD_WAIT_LIMIT = 1u << 22;  // polls, about half a second
+constexpr uint32_t CARD_WAIT_LIMIT = WAIT_POLLS;
 
 // A task's position, bitwidth and record offset; ok: its record may be read.
 struct StagedTask {

@@ -26,6 +26,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0u;
 }
+// What a wait for copies is given up after, in polls: about half a second, as each suspends its
+// thread for some 4 us (by the global timer, a barrier that nothing completes: 3.94 us a poll, and
+// 4.10 with mbar_wait's sleep, for one warp of an SM as for 12).
+constexpr uint32_t WAIT_POLLS = 1u << 17;
 // Waits for the completion of the barrier's phase of the given parity; gives
 // up (false) after `limit` polls.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit) {

@@ -79,7 +79,7 @@ constexpr int PAT_MOST_WARPS = 16;             // of a block
 // sequences of one row a head 56.8, 54.4, 57.8; 40 ragged ones of 64 rows, 8 bits,
 // 166, 157, 161; four 32K caches 56.5, 55.5, 56.4).
 constexpr uint32_t PAT_ITEM = 4;
-constexpr uint32_t PAT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
+constexpr uint32_t PAT_WAIT_LIMIT = WAIT_POLLS;
 constexpr uint32_t PAT_BAR_BYTES = 1024;       // barriers, before the rings
 constexpr int PAT_OWN_PLAN = 128;              // sequences that pages_join sums by itself
 // The weights' reference is raised only when a score passes it by this much

@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 // Waits on the bulk-copy ring give up after ATT_WAIT_LIMIT polls (about half
 // a second) and report KVP_ERR_TIMEOUT.
-constexpr uint32_t ATT_WAIT_LIMIT = 1u << 22;
+constexpr uint32_t ATT_WAIT_LIMIT = WAIT_POLLS;
 
 // Shared memory of the split kernel (bytes).  A ring of NST raw sub-chunks
 // (the pool's bytes as they are, filled by bulk copies), then the staged

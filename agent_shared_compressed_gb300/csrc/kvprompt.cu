@@ -68,7 +68,10 @@ constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
 // tokens: 130 us, 137).
 constexpr int PT_FEW = 32;
 constexpr int PT_MOST = 1 << 30;              // rows: sums and differences of places fit 32 bits
-constexpr uint32_t PT_WAIT_LIMIT = 1u << 22;  // polls, about half a second
+constexpr uint32_t PT_WAIT_LIMIT = WAIT_POLLS;
+// Block numbers without work, one after the other, after which the other warps are given an empty
+// piece of work, so that their waits begin anew (a number takes 1.2 us).
+constexpr uint32_t PT_IDLE = 4096;
 constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f, PT_FAR = 4096.0f;
 
 struct PromptArgs {
@@ -458,11 +461,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             // of blocks that have not begun (cluster launch control), one at a time, when the copies
             // of what it has are all under way: that leaves the others their share, and the next
             // queries, keys and values come while the last tiles and results are worked on.
-            uint32_t block = blockIdx.x, k = 0, n = 0, queries = 0, asked = 0;
+            uint32_t block = blockIdx.x, k = 0, n = 0, queries = 0, asked = 0, idle = 0;
             bool ok = true, more = true;
             while (ok) {
                 PromptWork w = {};
-                if (more && !prompt_work(a, block, w)) w.valid = 0;
+                if (more && !prompt_work(a, block, w)) w.valid = ++idle % PT_IDLE == 0u;
                 if (w.valid || !more) {
                     const uint32_t at = k & 1u;
                     if (k >= 2 && !(ok = warp_wait(a, sm + T::READ + 8 * at, ((k >> 1) - 1u) & 1u, dead))) break;

@@ -430,6 +430,23 @@ def test_many_sequences():
     Call(seqs, 2, 2, 64).both(window=9, sinks=2)
 
 
+def test_hardly_any_work_among_many_numbers():
+    """65536 sequences of 1024 heads, all but the first and the last empty: the blocks look at 67
+    million numbers, longer than a wait may be, before the first one's."""
+    H, d, B = 1024, 64, kv.KVP_PROMPT_MAX_SEQS
+    c = Call([(3, 6), (2, 0)], H, 1, d)
+    want = c.run(0.1)
+    c.q_first_d = torch.full((B + 1,), 3, dtype=torch.int32, device="cuda")
+    c.q_first_d[0], c.q_first_d[B] = 0, 5
+    c.k_first_d, c.k_lens_d = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), 9, dtype=torch.int32, device="cuda")
+    c.k_first_d[B - 1], c.k_lens_d[B - 1] = 9, 2
+    c.shape = kv.PromptShape(B, c.n, c.t, c.nq, H, d)
+    c.wsb = kv.kvprompt_workspace_bytes(c.shape)
+    got = c.run(0.1)
+    assert kv.kvprompt_status(c.error) == kv.KVP_OK
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
 def test_few_rows_over_many_keys():
     for H, G, d, seqs in ((2, 4, 128, [(5, 20000)]), (1, 1, 64, [(1, 33333), (2, 70)]), (8, 4, 128, [(64, 5000)])):
         c = Call(seqs, H, G, d)
