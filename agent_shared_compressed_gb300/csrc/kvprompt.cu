@@ -72,6 +72,7 @@ constexpr uint32_t PT_WAIT_LIMIT = WAIT_POLLS;
 // Block numbers without work, one after the other, after which the other warps are given an empty
 // piece of work, so that their waits begin anew (a number takes 1.2 us).
 constexpr uint32_t PT_IDLE = 4096;
+// (Rows with references beyond PT_FAR take longer: 16384 tokens 1.55 ms, 1.31.)
 constexpr float PT_SLACK = 8.0f, PT_BIAS = 40.0f, PT_FAR = 4096.0f;
 
 struct PromptArgs {
@@ -728,16 +729,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
             const bool real = tl < a.half_tokens && i < w.count;
             const int p = w.p_first + (real ? i : w.count - 1);
             float raw = -INFINITY, sum = 0.0f;  // the reference, over the scale
-            // What is added to a score for a weight's exponent; whether the reference is far from 0; the score
-            // that has to be passed for a look at the reference (a far one is looked at in every tile).
+            // What is added to a score for a weight's exponent; whether the reference is far from 0.
             auto offset = [&]() { return -(raw == -INFINITY ? 0.0f : raw * a.scale2) - PT_BIAS; };
             auto is_far = [&]() { return real && raw > -INFINITY && fabsf(raw * a.scale2) >= PT_FAR; };
-            auto bar_of = [&]() { return is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK; };
-            float bar = -INFINITY;
             // Tiles [in0, in1) are seen whole by all rows: nothing to hide.
             const int in0 = w.na - w.j0 + (a.window ? (max(w.p_last() - a.window + 1 - w.b0, 0) + PT_KEYS - 1) / PT_KEYS : 0);
             const int in1 = w.na - w.j0 + max(w.p_first + 1 - w.b0, 0) / PT_KEYS;
             int j = 0;
+            float bar = -INFINITY;  // passed by a score that needs a look at the reference (by all, of a far one)
             if (w.few()) {
                 if ((ok = warp_wait(a, sm + T::S + 8 * uint32_t(half), done, dead))) {
                     tc_after();
@@ -754,7 +753,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     }
                     raw = top;
                     float off = offset();
-                    bar = bar_of();
+                    bar = is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK;
                     if (__any_sync(0xffffffffu, is_far())) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) xf[c] -= raw == -INFINITY ? 0.0f : raw;
@@ -821,9 +820,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_attend(const __grid_cons
                     const float f = raise ? pt_exp2((raw - most) * a.scale2) : 1.0f;
                     if (raise) raw = most;
                     off = offset();
-                    bar = bar_of();
+                    bar = is_far() ? -INFINITY : raw * a.scale2 + PT_SLACK;
                     sum *= f;
-                    if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                    if (j > 0) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
