@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(APP_THREADS, app_blocks(D, FMT)) pages_append(
                 }
             }
         } else if constexpr (B::K4) {
-            // Keys and values share the encoder: fetching instructions is what a step waits for most
-            // (8192 tokens into 4-bit pages: 20.8 us, 24.4 with one each; 8-bit pages gain nothing).
+            // Keys and values share the encoder: with one each, fetching instructions is what a step waits
+            // for most (8192 tokens into 4-bit pages, nothing returned: 17.5 us; before halves were decided two
+            // at a time 20.8, and 24.4 with one each; 8-bit pages gain nothing).
             Lane4<D> c;
             uint32_t szb[NB];
             encode4<D>(x, c, szb, bad);

@@ -40,8 +40,10 @@
 // fragment order already (kvp_pages.cuh): a lane takes 16 bytes of a key row or
 // of a value token and expands them in registers, keys to fp16 and values to
 // bf16, exactly (|code| <= 128).  What bounds 8- and 4-bit pages beside memory is
-// that expansion, most of it on the integer pipe, which takes a warp's
-// instruction every other cycle: two to four instructions per pair of codes.
+// instructions: about half of them are on the integer pipe, which takes a warp's
+// instruction every other cycle (55 to 58 % of what it can take), many of them the
+// expansion, two to four per pair of codes.  No pipe is full; the longest stall is a
+// warp's wait for its own results.
 //
 // Key scales apply to the fp32 sums of their 32 dims.  Value scales go into the
 // weights, one product operand per 32 dims, as a sum of two bf16: 2^-17 of the

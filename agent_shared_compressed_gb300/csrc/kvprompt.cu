@@ -44,11 +44,11 @@
 // are added to the results of the rows that do see them.
 //
 // Measured (32 query over 8 KV heads of 128; cuBLAS reaches 1895 TFLOP/s): 16384 tokens
-// 1.25 ms, 1760 TFLOP/s, in a graph (1.39 ms over minutes, where the power limit lowers the
-// clock); 8192 tokens with a window of 1024 and 4 first tokens 130 us, 990 TFLOP/s of what is
-// seen: a block's 10 tiles are 9.5 tiles' worth of keys that some row does not see besides,
-// and about 4 of start and end; 509 tokens over 32768 in two parts 195 us.  32 heads of 64, window
-// 256, 17 first tokens, 7 ragged prompts of 37 to 1851: 69 us.
+// 1.25 ms, 1760 TFLOP/s, at first (1.34 ms in a graph that runs for a tenth of a second, where the
+// power limit lowers the clock); 8192 tokens with a window of 1024 and 4 first tokens 120 us, 1080
+// TFLOP/s of what is seen: products of 9.25 tiles where a row sees 8, and a block's start and end, as
+// long as 4; 509 tokens over 32768 in two parts 189 us (209 under the power limit).  32 heads of 64,
+// window 256, 17 first tokens, 7 ragged prompts of 37 to 1851: 68 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -64,8 +64,8 @@ constexpr int PT_KEYS = 128;                  // keys of a tile
 // Three warpgroups: 384 threads start with 168 registers each (64512 of the SM's), the third
 // gives 80 of its back and each of the others takes 40 more: 2 * 128 * 208 + 128 * 88 = 64512.
 constexpr int PT_THREADS = 384, PT_MORE = 208, PT_LESS = 88;
-// First tokens that a narrow tile holds.  Without it, 4 of them cost a window of 1024 a twentieth (8192
-// tokens: 130 us, 137).
+// First tokens that a narrow tile holds.  Without it, 4 of them cost a window of 1024 a fifteenth (8192
+// tokens: 120 us, 128).
 constexpr int PT_FEW = 32;
 constexpr int PT_MOST = 1 << 30;              // rows: sums and differences of places fit 32 bits
 constexpr uint32_t PT_WAIT_LIMIT = WAIT_POLLS;

@@ -502,7 +502,8 @@ size_t kvpages_attend_workspace_bytes(const kvp_pages_config *cfg, int n_seqs, i
  * elements below 2^-28 of its largest, over 4-bit keys 2^-24; a group's zero point
  * enters times the sum of the query's 32 elements, in fp32); softmax statistics are fp32, exponentials
  * the hardware's in base 2 (2^-22); the weights (times the values' scales) enter
- * the value product as a sum of two bf16 (2^-17).  The kernel waits for its bulk
+ * the value product as a sum of two bf16 (2^-17; 4-bit values beside 4-bit keys as
+ * code - 8: 2^-17 of 8 s and of |z + 8 s|).  The kernel waits for its bulk
  * copies of the pages at most about half a second; should a wait run out, the
  * outputs are unspecified and kvpages_status reports KVP_ERR_TIMEOUT.  A page id
  * outside the container or a length beyond its table row is skipped and reported
@@ -527,8 +528,8 @@ int kvpages_attend(const void *pages, const kvp_pages_config *cfg, int layer, in
  * Bytes and time go by what is seen.  Table entries of pages that hold no token
  * which one of the sequence's queries sees are not read: their pages may be used
  * for something else.  Whatever unseen tokens of other pages hold (Inf and NaN
- * too) has no part in the result.  Everything else as kvpages_attend; the same
- * workspace. */
+ * too) has no part in the result; they need not have been written.  Everything else
+ * as kvpages_attend; the same workspace. */
 int kvpages_attend_window(const void *pages, const kvp_pages_config *cfg, int layer, int n_seqs, int n_q_tokens,
                           int n_q_heads, const void *q, float scale, int window, int sinks, const int32_t *table,
                           int max_pages, const int32_t *lens, const float *base_out, const float *base_lse, void *out,
